@@ -462,6 +462,139 @@ QV_API qv_status qv_logit_fidelity(const float* ref_logits, const float* logits,
                                    float* kl, int32_t* top1_ref, int32_t* top1, cudaStream_t stream);
 
 /*
+ * The 4-bit paged KV cache: qv_kv4_write, qv_kv4_read, qv_attention_verify_kv4
+ *
+ *   Lower bit widths are the next step the Quasar summaries name
+ *   (gist.science/it, gist.science/de and gist.science/ja summaries, section
+ *   5). They quantize the weights; at long contexts the bf16 cache is what a
+ *   verify step reads most of after that. The pages give no cache format: the
+ *   one here keeps the a0 rule (symmetric, half to even) with 7 for 127 and one
+ *   scale for 32 elements of a head's row.
+ *
+ * Format. A block holds QV_KV4_BLOCK = 32 positions. cache is a pool of
+ * `pages` blocks, [pages][Hkv][34 D] bytes (uint8): block p of key/value head
+ * h is the record at (p * Hkv + h) * 34 D:
+ *     [0, 16 D)     key codes    [32][D/2]    [32 D, 33 D)  key scales   [32][D/32]
+ *     [16 D, 32 D)  value codes  [32][D/2]    [33 D, 34 D)  value scales [32][D/32]
+ * A code is a 4-bit two's complement number, element 2j in the low nibble of
+ * byte j. A scale byte b stands for s(b) = (1 + (b & 7) / 8) * 2^((b >> 3) - 15),
+ * 2^-15 to 122880. An element's value is its code times its scale, which bf16
+ * holds exactly (7 significant bits). For a group x of 32 elements
+ *     t = fl32(max |x| / 7) (IEEE division)
+ *     b = the scale nearest to t, ties to the even byte, clamped to [0, 255]
+ *     q = clamp(round_half_even(fl32(x / s(b))), -7, 7)
+ * so that |value - x| <= s / 2 for |x| <= 7 * 122880, with s <= (17/16) t or
+ * s = 2^-15. NaN is written as 0; larger magnitudes and infinities saturate.
+ * Every byte is a valid scale and every nibble a finite code: a cache that was
+ * never written may hold anything.
+ *
+ * Blocks of a sequence. block_table [B][NB] int32: positions 32 i .. 32 i + 31
+ * of sequence b are in page block_table[b][i]. An entry outside [0, pages) is
+ * no page: nothing is written there, nothing is read back, and attention takes
+ * its positions as absent. Sequences may share pages they only read. NULL:
+ * sequence b's blocks are pages b * NB + i, and pages must be >= B * NB.
+ * NB is the row length of the table, 32 * NB the most positions of a sequence.
+ *   1 <= B <= 65535, 1 <= Hkv <= QV_KV4_MAX_HEADS, D in {64, 128},
+ *   0 <= NB < 2^26, B * T <= 2^24.
+ *
+ * qv_kv4_write -- quantizes the key and value heads of qkv rows into the cache.
+ *   qkv    [B*T][(Hq + 2 Hkv) * D] fp32 or bf16, 16-byte aligned: the qkv
+ *          projection's rows (row b*T + j; Hq query heads, not read, then the
+ *          key heads, then the value heads; Hq may be 0)
+ *   start  [B] int32: row j of sequence b goes to position start[b] + j
+ *   count  [B] int32 or NULL: rows of sequence b that are written (at most T;
+ *          0 or less: none), e.g. qv_accept's accept_len
+ *   Rows whose position is negative, past the table or on no page are not
+ *   written. No other byte of the cache changes. Two rows of one call must not
+ *   have the same position of the same page.
+ *
+ * qv_kv4_read -- the same positions read back as values.
+ *   k_out, v_out [B*T][Hkv * D] fp32 or bf16 (dtype), 16-byte aligned: row
+ *          b*T + j is position start[b] + j. Rows that qv_kv4_write would not
+ *          write are left as they were.
+ *   With start 0 and T = Lmax the outputs are the k_cache and v_cache of
+ *   qv_attention_verify.
+ */
+#define QV_KV4_BLOCK 32
+#define QV_KV4_MAX_HEADS 1024
+QV_API qv_status qv_kv4_write(const void* qkv, qv_dtype dtype, const int32_t* start, const int32_t* count,
+                              const int32_t* block_table, int B, int T, int Hq, int Hkv, int D, int NB,
+                              int pages, uint8_t* cache, cudaStream_t stream);
+QV_API qv_status qv_kv4_read(const uint8_t* cache, const int32_t* start, const int32_t* count,
+                             const int32_t* block_table, int B, int T, int Hkv, int D, int NB, int pages,
+                             void* k_out, void* v_out, qv_dtype dtype, cudaStream_t stream);
+
+/*
+ * qv_attention_verify_kv4 -- qv_attention_verify over the 4-bit paged cache:
+ * causal grouped-query scaled dot-product attention of the verify tokens over
+ * the cached positions and the step's own keys and values (bf16, as they are
+ * in qkv, not rounded to 4 bits). With one token (T = 1) it is the decode step
+ * of a sequence.
+ *   qkv       [B*T][(Hq + 2 Hkv) * D] bf16, 16-byte aligned, as in
+ *             qv_attention_verify
+ *   cache, block_table, NB, pages, D: the format above (cache may be NULL when
+ *             NB == 0)
+ *   cache_len [B] int32: cached positions of each sequence (clamped to
+ *             [0, 32 NB]). Positions at and past it are not attended to and may
+ *             hold anything, as may whole pages past it.
+ *   out       [B*T][Hq * D] fp32 or bf16 (out_dtype), 16-byte aligned
+ *   T in [1, QV_MAX_M], Hq a multiple of Hkv; any T * Hq / Hkv (groups of 32
+ *   query rows read the cache once each).
+ *   workspace: qv_attention_kv4_workspace_bytes(...) bytes (a host function;
+ *             0 for an invalid shape), 16-byte aligned. Its first 4096 bytes
+ *             must be ZERO-FILLED before its first use and are zero again
+ *             after every call; the rest is scratch. One workspace serves any
+ *             sequence of stream-ordered calls of any shapes it is large
+ *             enough for. It must not be shared with calls that may run at the
+ *             same time (another stream, another captured graph), nor with the
+ *             GEMM calls, whose whole workspace has to stay zero-filled.
+ *   A later row's key or value that is not finite (padding) does not reach the
+ *   rows before it; what a row does see, it sees: its output is then not
+ *   finite either.
+ *   A wait inside the kernel that runs out sets QV_DEVICE_ERR_FULL_WAIT
+ *   (qv_device_error); the call's outputs are then undefined, the workspace
+ *   stays usable.
+ * fp32 outputs are within about 1e-6 (2-norm) of the binary64 definition over
+ * the values the cache holds; for bf16 outputs the probabilities are rounded to
+ * bf16 before the product with the values.
+ */
+QV_API size_t qv_attention_kv4_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int NB);
+QV_API qv_status qv_attention_verify_kv4(const uint16_t* qkv, const uint8_t* cache, const int32_t* block_table,
+                                         const int32_t* cache_len, int B, int T, int Hq, int Hkv, int D, int NB,
+                                         int pages, float scale, void* out, qv_dtype out_dtype, void* workspace,
+                                         size_t workspace_bytes, cudaStream_t stream);
+
+/*
+ * qv_token_logprobs -- log probability of one given token per row of logits,
+ * the row's entropy and its most probable tokens: what a server reports for
+ * the tokens of a verify step (or of a scored text).
+ *   The verifier's logits stay in high precision: gist.science/it summary,
+ *   section 2 item 3.
+ *   logits   [M*V] fp32 or bf16 (dtype), aligned to its elements
+ *   tokens   [M] int32, e.g. the out_tokens of qv_accept or qv_spec_sample
+ *   logprob  [M] fp32 out: ln softmax(logits row)[token]; 0 for a token outside
+ *            [0, V) (the -1 that fills out_tokens up), so that a sequence's
+ *            rows can simply be added
+ *   entropy  [M] fp32 out in nats, or NULL
+ *   top_tokens [M*top_k] int32 out, top_logprobs [M*top_k] fp32 out: the top_k
+ *            largest logits, in descending order, equal logits by the lower
+ *            index (-0 equals +0); both ignored when top_k == 0
+ *   1 <= M <= 65535, 1 <= V <= 2^24, 0 <= top_k <= min(QV_MAX_TOP_K, V).
+ * A logit of -inf (a masked token) has probability 0 and log probability
+ * -inf. In a row with nothing above -inf every log probability is -inf and the
+ * entropy is 0. A NaN or +inf makes the row's logprob (of a token in range),
+ * entropy and top_logprobs NaN; its top_tokens are then unspecified (in [0, V),
+ * or -1 where fewer than top_k logits are numbers).
+ * Sums are binary32 per thread (relative error about 1e-7), combined in a fixed
+ * order. One launch: a CTA per row, or a cluster of up to 16 CTAs (a
+ * non-portable size) when there are few rows; no workspace.
+ */
+#define QV_MAX_TOP_K 32
+QV_API qv_status qv_token_logprobs(const void* logits, qv_dtype dtype, const int32_t* tokens, int M, int V,
+                                   int top_k, float* logprob, float* entropy, int32_t* top_tokens,
+                                   float* top_logprobs, cudaStream_t stream);
+
+/*
  * W4A8 -- the lower-bit verifier: int4 weights against the int8 activation
  * codes of qv_quantize_act.
  *   Lower bit widths (4-bit, 2-bit) for the verifier are the next step the
@@ -607,12 +740,13 @@ QV_API qv_status qv_device_error(unsigned int* code);
  *   qv_debug_set_slot_wait_ns(ns): limit, in ns of %globaltimer, of the
  *     split-K head's wait for partial sums in the streaming kernels of
  *     qv_w8a8_linear / qv_w8a8_swiglu / qv_lm_head_argmax and the W4A8 calls
- *     (up to 32 token rows per launch); 0 restores the default (1 s).
+ *     (up to 32 token rows per launch), and of the attention kernels'
+ *     stage waits; 0 restores the default (1 s).
  *   qv_debug_drop_partials(n): the next n such launches publish no split-K
  *     partial sums, so every split tile's head waits out its limit, sets
  *     QV_DEVICE_ERR_SLOT_WAIT and finishes with incomplete sums.
- *   qv_debug_hold_attention_loads(n): the next n qv_attention_verify calls
- *     request none of their key/value stages, so every stage wait runs out
+ *   qv_debug_hold_attention_loads(n): the next n qv_attention_verify or
+ *     qv_attention_verify_kv4 calls request none of their key/value stages, so every stage wait runs out
  *     (after the qv_debug_set_slot_wait_ns limit, else 1 s), sets
  *     QV_DEVICE_ERR_FULL_WAIT and the outputs are undefined; no copy is left
  *     in flight, and later calls are unaffected.

@@ -30,12 +30,13 @@ NVCC_FLAGS = ARCH + [
     "-I", INCLUDE, "-I", CSRC,
 ]
 # Translation units whose floating point results are checked against a
-# tolerance (attention, the logit-fidelity diagnostic) may contract a*b+c
+# tolerance (attention, the logit-fidelity diagnostic, the token log
+# probabilities) may contract a*b+c
 # into one fused multiply-add; every other unit computes results that must
 # equal the oracle's bit for bit, so no expression there may be contracted
 # (explicit fused operations, where the definition has one, are written as
 # such).
-FMA_CONTRACTION_OK = {"k_attn.cu", "k_fidelity.cu"}
+FMA_CONTRACTION_OK = {"k_attn.cu", "k_attn_kv4.cu", "k_fidelity.cu", "k_logprobs.cu"}
 
 
 def flags_for(src: str) -> list[str]:

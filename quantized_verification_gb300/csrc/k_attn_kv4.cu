@@ -1,0 +1,895 @@
+// k_attn_kv4.cu -- attention of the verify tokens over a 4-bit paged KV cache.
+//
+//   The attention of k_attn.cu (causal grouped-query scaled dot-product
+//   attention; the non-GEMM computation of the layer stays in high precision:
+//   Quasar, gist.science/ja summary, section 2.2 item 3) with the cache of
+//   kv4_common.cuh in place of the bf16 one: 4.25 bits per cached element
+//   instead of 16. The step's own keys and values are the bf16 rows of the
+//   qkv projection, unrounded.
+//
+// Work split. A tile is one (sequence, key/value head, group of at most 32 of
+// its T * Hq/Hkv query rows); a unit is one record of 32 cached positions, or
+// 32 of the step's own rows. The units of all tiles, sequence by sequence,
+// form one line that the CTAs cut into equal ranges, so that ragged lengths
+// leave no SM idle. A tile that lies in one range is written by its CTA; one
+// that is cut leaves partial results (running maximum, running sum, weighted
+// values) in the workspace, and the last of its CTAs to arrive adds them in
+// range order. Nobody waits for anybody, and the order of arrival changes
+// nothing.
+//
+// Inside a CTA each of the 8 warps takes every 8th unit of the range and keeps
+// its own online softmax. A record comes in one bulk copy into the warp's own
+// ring. Both products run on the tensor cores (mma.sync m16n8k16, bf16
+// operands, fp32 accumulation) with the keys, or the value dims, on the M side
+// and the query rows on the N side in tiles of 8: a verify step has 4 to 32
+// rows per head group, far too few to fill a tcgen05 tile's 128.
+//   S^T = K Q^T:  in bf16. Codes become bf16 values exactly (kv4_common.cuh): a nibble
+//     shifted to bits 3..6 under the pattern of 16.0 is the number 24 + q, and
+//     one fused multiply-add gives (24 + q) s - 24 s = q s without rounding.
+//     A thread's 4 * W code words are one 16-byte read (W = D / 32) and all
+//     belong to one scale group; which k index of the product each nibble
+//     takes is free, so the query fragments are permuted to match.
+//   P in base 2, kept unnormalised: p = 2^(7 + s - m). m follows the row's
+//     maximum lazily: it moves only when a score exceeds it by more than 8 (p
+//     is at most 2^15 then), so the usual unit needs no reduction across lanes
+//     and no rescaling. P is split into two f16 parts (an error of 2^-22 P, and
+//     2^-32 of the largest P below f16's normal range) for fp32 outputs; for
+//     bf16 outputs one part is enough (2^-11 P, an eighth of the output's own
+//     rounding).
+//   O^T += V^T P^T:  in f16, whose 11 bits make P's parts. The value scales
+//     are taken times 2^-6, where every product q s is exact in f16 (2^-21 to
+//     7 * 1920, and 24 s below 65504), and the output is multiplied by 2^6.
+//     V's pairs run along keys: the 16-bit halves of two keys' words
+//     interleave (prmt), after which the nibble step, with the pattern of 16.0
+//     in f16, gives the A fragments of the dims a thread owns.
+// Every byte of a record is a finite value, so positions at and past a
+// sequence's length may hold anything: their probability is 0 and 0 * v = 0.
+// The step's own value rows can hold infinities or NaN in rows that some
+// query rows must not see (padding): they are taken as 0 in the product and
+// added afterwards to the rows that do see them.
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "kv4_common.cuh"
+#include "qv_internal.h"
+#include "qv_ptx.cuh"
+
+namespace qv {
+
+__device__ unsigned int g_attn_kv4_error;
+
+namespace {
+
+constexpr int kWarps = 8;
+constexpr int kThreads = kWarps * 32;
+constexpr int kRowTile = 32;                    // query rows of a tile
+constexpr int kMinUnits = 8;                    // units of a CTA's range at least
+constexpr size_t kCounterBytes = 4096;         // at the workspace's start, whatever the shape
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLazy = 8.f;                    // log2 of the growth a running maximum may lag behind
+constexpr float kBias = 7.f;                    // log2 of p at the running maximum: 2^(kBias + kLazy) < 65504
+
+struct Args {
+    const uint16_t* qkv;       // [B*T][(Hq + 2 Hkv) D] bf16
+    const uint8_t* cache;
+    const int32_t* table;      // [B][NB] or null
+    const int32_t* len;        // [B]
+    int B, T, Hq, Hkv, G, NB, pages;
+    int RT, rows;              // row tiles per head group, query rows per row tile
+    float scale;
+    void* out;                 // [B*T][Hq D] fp32 or bf16
+    unsigned* counters;        // [grid] arrivals at the tile that begins in CTA i's range (zero between calls)
+    float* partials;           // [grid][2][slot]
+    int hold;                  // test hook: request no record
+    unsigned long long wait_ns;
+};
+
+template <int D, int NR>
+struct Layout {
+    using Rec = Kv4Rec<D>;
+    static constexpr int W = D / 32;                      // 32-bit code words of a thread per key row
+    static constexpr int KS = D / 16;                     // k steps of Q K^T = dim tiles of P V
+    static constexpr bool TwoCtas = D / 64 * NR <= 2;     // two CTAs per SM (at most 128 registers a thread)
+    static constexpr int Stages = TwoCtas ? 2 : 4;
+    static constexpr int Ring = 0;
+    static constexpr int Area = Ring + kWarps * Stages * Rec::Bytes;      // 4 warps' partial outputs
+    static constexpr int AreaBytes = 4 * NR * 8 * D * 4;
+    static constexpr int Q = Area + AreaBytes;            // query fragments [NR][KS][32] uint2
+    static constexpr int ML = Q + NR * KS * 32 * 8;       // m [8 warps][NR*8], l [8][NR*8]
+    static constexpr int MW = ML + 2 * kWarps * NR * 8 * 4;   // the tile's m, l [2][NR*8]
+    static constexpr int Bar = MW + 2 * NR * 8 * 4;
+    static constexpr int Valid = Bar + kWarps * Stages * 8;
+    static constexpr int Scan = Valid + kWarps * Stages * 4;  // long long [8] + found tile
+    static constexpr int Misc = Scan + 16 * 8;
+    static constexpr int Bytes = Misc + 64;
+    static constexpr int Slot = NR * 8 * D + 2 * NR * 8;  // floats of a partial result
+    static_assert(Area % 16 == 0 && Q % 16 == 0 && Bar % 8 == 0 && Scan % 8 == 0, "alignment");
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t hfma2_bf16(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+__device__ __forceinline__ uint32_t hmul2_bf16(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+// {lo, hi} rounded to bf16.
+__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint32_t hfma2_f16(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
+__device__ __forceinline__ uint32_t hmul2_f16(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+// {lo, hi} rounded to f16.
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t d;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+    return d;
+}
+__device__ __forceinline__ float2 unpack_f16x2(uint32_t x) {
+    float lo, hi;
+    asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.f32.f16 %0, l;\n\tcvt.f32.f16 %1, h;\n\t}"
+        : "=f"(lo), "=f"(hi) : "r"(x));
+    return make_float2(lo, hi);
+}
+
+// A key scale as a bf16 pair, and -24 times it (exact: 2 + 4 bits).
+struct KeyScale {
+    uint32_t s, off;
+    __device__ __forceinline__ KeyScale() {}
+    __device__ __forceinline__ explicit KeyScale(uint32_t b) {
+        s = b * 0x00100010u + 0x38003800u;
+        off = hmul2_bf16(s, 0xC1C0C1C0u);                 // -24.0
+    }
+};
+// Nibbles J of the two 16-bit halves of x as bf16 values q * s: shifted to bits
+// 3..6 with the sign bit flipped, under 16.0 (0x4180), a nibble is 24 + q.
+template <int J>
+__device__ __forceinline__ uint32_t key_pair(uint32_t x, const KeyScale& sc) {
+    const uint32_t y = J == 0 ? x * 8u : x >> (J == 0 ? 0 : 4 * J - 3);
+    return hfma2_bf16((y & 0x00780078u) ^ 0x41C041C0u, sc.s, sc.off);
+}
+// The value scales of two positions times 2^-6 as an f16 pair, and -24 times them.
+struct ValScale {
+    uint32_t s, off;
+    __device__ __forceinline__ ValScale() {}
+    __device__ __forceinline__ ValScale(uint32_t b_lo, uint32_t b_hi) {
+        s = pack_f16x2(__uint_as_float((b_lo << 20) + (106u << 23)), __uint_as_float((b_hi << 20) + (106u << 23)));
+        off = hmul2_f16(s, 0xCE00CE00u);                  // -24.0
+    }
+};
+// The same in f16: bits 6..9 under 16.0 (0x4C00).
+template <int J>
+__device__ __forceinline__ uint32_t val_pair(uint32_t x, const ValScale& sc) {
+    const uint32_t y = J == 0 ? x * 64u : (J == 1 ? x * 4u : x >> (J < 2 ? 0 : 4 * J - 6));
+    return hfma2_f16((y & 0x03C003C0u) ^ 0x4E004E00u, sc.s, sc.off);
+}
+
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, unsigned bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
+                 :: "r"(dst), "l"(src), "r"(bytes), "r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ bool bar_wait(uint64_t* bar, unsigned parity, volatile int* abort,
+                                         unsigned long long limit_ns) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = global_timer_ns();
+    while (true) {
+        if (*abort) return false;
+        if (mbar_try_wait(bar, parity)) return true;
+        if (global_timer_ns() - t0 > limit_ns) {
+            *abort = 1;
+            return false;
+        }
+    }
+}
+
+__device__ __forceinline__ uint32_t lds_u8(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+__device__ __forceinline__ uint32_t lds_u32(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+
+// The units of sequence b: cached records, then groups of 32 own rows.
+__device__ __forceinline__ int seq_len(const Args& a, int b) {
+    const long long cap = (long long)a.NB * kKv4Block;
+    const int n = a.len[b];
+    return n < 0 ? 0 : ((long long)n > cap ? (int)cap : n);
+}
+
+template <int D, int NR, bool OUTBF>
+__global__ void __launch_bounds__(kThreads, Layout<D, NR>::TwoCtas ? 2 : 1) attn_kv4_kernel(const Args a) {
+    using Ly = Layout<D, NR>;
+    using Rec = Kv4Rec<D>;
+    constexpr int W = Ly::W, KS = Ly::KS, S = Ly::Stages, RW = NR * 8;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const uint32_t sbase = smem_u32(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
+    uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Ly::Bar) + warp * S;
+    volatile int* valid = reinterpret_cast<volatile int*>(smem + Ly::Valid) + warp * S;
+    float* s_area = reinterpret_cast<float*>(smem + Ly::Area);
+    float* s_wm = reinterpret_cast<float*>(smem + Ly::ML);
+    float* s_wl = s_wm + kWarps * RW;
+    float* s_m = reinterpret_cast<float*>(smem + Ly::MW);
+    float* s_l = s_m + RW;
+    long long* s_scan = reinterpret_cast<long long*>(smem + Ly::Scan);
+    volatile int* abort = reinterpret_cast<volatile int*>(smem + Ly::Misc);
+    int* s_flag = reinterpret_cast<int*>(smem + Ly::Misc) + 1;       // [1] bad value row, [2] last arrival
+    const float NEG_INF = -__uint_as_float(0x7F800000u);
+    const uint32_t ring = sbase + (uint32_t)(Ly::Ring + warp * S * Rec::Bytes);
+
+    if (lane == 0)
+        for (int s = 0; s < S; ++s) mbar_init(&bars[s], 1);
+    if (tid == 0) {
+        *abort = 0;
+        s_flag[0] = 0;
+    }
+    fence_barrier_init();
+    allow_dependent_launch();
+    grid_dependency_wait();
+
+    // ---- this CTA's range [u0, u1) of the line of units, and the sequence it begins in
+    const int own_units = (a.T + 31) / 32, tps = a.Hkv * a.RT;   // own units of a tile, tiles of a sequence
+    const int seg = (a.B + kThreads - 1) / kThreads;             // sequences per thread
+    long long mine = 0;
+    for (int b = tid * seg; b < min(a.B, (tid + 1) * seg); ++b)
+        mine += (long long)((seq_len(a, b) + kKv4Block - 1) / kKv4Block + own_units) * tps;
+    long long incl = mine;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+        const long long v = __shfl_up_sync(0xffffffffu, incl, off);
+        if (lane >= off) incl += v;
+    }
+    if (lane == 31) s_scan[warp] = incl;
+    __syncthreads();
+    long long before = incl - mine, total = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) before += s_scan[w];
+        total += s_scan[w];
+    }
+    long long per = (total + gridDim.x - 1) / gridDim.x;
+    per = per < kMinUnits ? kMinUnits : per;
+    const long long u0 = per * blockIdx.x, u1 = min(total, u0 + per);
+    if (u0 >= u1) return;                                        // (the whole CTA)
+    if (u0 >= before && u0 < before + mine) {                    // exactly one thread
+        long long at = before;
+        int b = tid * seg;
+        while (true) {
+            const long long n = (long long)((seq_len(a, b) + kKv4Block - 1) / kKv4Block + own_units) * tps;
+            if (u0 < at + n) break;
+            at += n;
+            ++b;
+        }
+        s_scan[8] = at;
+        s_scan[9] = b;
+    }
+    __syncthreads();
+    long long seq_at = s_scan[8];                                // where sequence b's units begin
+    int b = (int)s_scan[9];
+    long long u = u0;
+    unsigned issued = 0, used = 0;                               // this warp's records so far
+    bool dead = false;                                           // a wait of this warp ran out: it takes no more units
+
+    while (u < u1) {
+        // ---- the tile that unit u belongs to, and this CTA's part [ua, ub) of it
+        const int L = seq_len(a, b);
+        const int nc = (L + kKv4Block - 1) / kKv4Block, nu = nc + own_units;
+        const int ti = (int)((u - seq_at) / nu);
+        const long long tile_at = seq_at + (long long)ti * nu;
+        const int kh = ti / a.RT, rt = ti - kh * a.RT;
+        const int ua = (int)(u - tile_at), ub = (int)min((long long)nu, u1 - tile_at);
+        const int r0 = rt * a.rows, R = min(a.rows, a.T * a.G - r0);   // query rows of this tile
+
+        auto issue = [&](int unit) {                             // lane 0: request a cached unit's record
+            const int s = issued % S;
+            const int page = kv4_page(a.table, b, a.NB, a.pages, unit);
+            valid[s] = page >= 0;
+            if (a.hold) return;
+            if (page < 0) {
+                mbar_arrive(&bars[s]);
+                return;
+            }
+            mbar_arrive_expect_tx(&bars[s], Rec::Bytes);
+            bulk_load(ring + (uint32_t)(s * Rec::Bytes), a.cache + ((size_t)page * a.Hkv + kh) * Rec::Bytes, Rec::Bytes,
+                      &bars[s]);
+        };
+        int next = ua + warp;                                    // next unit to request
+        for (int s = 0; s < S; ++s)
+            if (next < min(ub, nc) && !dead) {
+                if (lane == 0) issue(next);
+                ++issued;
+                next += kWarps;
+            }
+
+        // ---- the query fragments: word w of the row's 16-byte piece at dims
+        // t4 * D/4 + 8 w holds the pairs (d, d + 4) of two k steps
+        const size_t rowlen = (size_t)(a.Hq + 2 * a.Hkv) * D;
+        for (int e = tid; e < NR * W * 32; e += kThreads) {
+            const int ln = e & 31, w = (e >> 5) % W, nt = (e >> 5) / W;
+            const int r = 8 * nt + (ln >> 2);
+            uint4 q = make_uint4(0u, 0u, 0u, 0u);
+            if (r < R) {
+                const int j = (r0 + r) / a.G, h = kh * a.G + (r0 + r) - j * a.G;
+                q = *reinterpret_cast<const uint4*>(a.qkv + ((size_t)b * a.T + j) * rowlen + (size_t)h * D + (ln & 3) * (D / 4) + 8 * w);
+            }
+            uint2* dst = reinterpret_cast<uint2*>(smem + Ly::Q) + (nt * KS + 2 * w) * 32 + ln;
+            dst[0] = make_uint2(__byte_perm(q.x, q.z, 0x5410), __byte_perm(q.x, q.z, 0x7632));
+            dst[32] = make_uint2(__byte_perm(q.y, q.w, 0x5410), __byte_perm(q.y, q.w, 0x7632));
+        }
+        __syncthreads();
+
+        const float sl2 = a.scale * kLog2e;
+        float o[KS][NR][4];                                      // O^T: dims x rows
+        float m_run[NR][2], l_run[NR][2];                        // rows 8 nt + 2 t4 + e
+        int tok[NR][2];                                          // their token (own rows 0..tok are visible)
+#pragma unroll
+        for (int nt = 0; nt < NR; ++nt) {
+#pragma unroll
+            for (int i = 0; i < KS; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][nt][e] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = 8 * nt + 2 * t4 + e;
+                m_run[nt][e] = NEG_INF;
+                l_run[nt][e] = 0.f;
+                tok[nt][e] = r < R ? (r0 + r) / a.G : -1;
+            }
+        }
+        const int key_g = g ^ ((g >> 1) & 1);                    // position in its 8 of S^T row g (see below)
+
+        // The scores of 32 positions (two halves of 16) into the running softmax:
+        // scores in, probabilities out.
+        auto softmax = [&](float (&acc)[2][NR][4]) {
+            bool grow = false;
+            float mx[NR][2];
+#pragma unroll
+            for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    mx[nt][e] = fmaxf(fmaxf(acc[0][nt][e], acc[0][nt][2 + e]), fmaxf(acc[1][nt][e], acc[1][nt][2 + e]));
+                    grow = grow || mx[nt][e] > m_run[nt][e] + kLazy;
+                }
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float v = fmaxf(mx[nt][e], m_run[nt][e]);
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+                        v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+                        const float f = v == NEG_INF ? 1.f : ex2(m_run[nt][e] - v);
+                        m_run[nt][e] = v;
+                        l_run[nt][e] *= f;
+#pragma unroll
+                        for (int i = 0; i < KS; ++i) {
+                            o[i][nt][e] *= f;
+                            o[i][nt][2 + e] *= f;
+                        }
+                    }
+            }
+#pragma unroll
+            for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const float m = m_run[nt][e] == NEG_INF ? 0.f : m_run[nt][e] - kBias;   // no visible key yet: 2^-inf = 0
+                    float sum = 0.f;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const float p = ex2(acc[h][nt][2 * k + e] - m);
+                            acc[h][nt][2 * k + e] = p;
+                            sum += p;
+                        }
+                    l_run[nt][e] += sum;
+                }
+        };
+        // P^T of half h as the B operand (rows g; keys 2 t4, 2 t4 + 1 and + 8) in
+        // parts of 16 bits: f16 ones for the cache's values, bf16 ones of p 2^-6
+        // for the step's own
+        constexpr int Parts = OUTBF ? 1 : 2, OwnParts = OUTBF ? 2 : 3;
+        auto p_frag = [&](const float (&p)[NR][4], uint32_t (&f)[Parts][NR][2]) {
+#pragma unroll
+            for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const uint32_t h = pack_f16x2(p[nt][2 * k], p[nt][2 * k + 1]);
+                    f[0][nt][k] = movmatrix_trans(h);
+                    if constexpr (Parts == 2) {
+                        const float2 hv = unpack_f16x2(h);
+                        f[1][nt][k] = movmatrix_trans(pack_f16x2(p[nt][2 * k] - hv.x, p[nt][2 * k + 1] - hv.y));
+                    }
+                }
+        };
+        auto own_p_frag = [&](const float (&p)[NR][4], uint32_t (&f)[OwnParts][NR][2]) {
+#pragma unroll
+            for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    float x = p[nt][2 * k] * 0x1p-6f, y = p[nt][2 * k + 1] * 0x1p-6f;
+#pragma unroll
+                    for (int q = 0; q < OwnParts; ++q) {
+                        const uint32_t h = pack_bf16x2(x, y);
+                        f[q][nt][k] = movmatrix_trans(h);
+                        x -= __uint_as_float(h << 16);
+                        y -= __uint_as_float(h & 0xFFFF0000u);
+                    }
+                }
+        };
+        auto pv = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, const uint32_t (&f)[Parts][NR][2]) {
+#pragma unroll
+            for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                for (int q = 0; q < Parts; ++q) mma_f16_16816(o[i][nt], a0, a1, a2, a3, f[q][nt][0], f[q][nt][1]);
+        };
+        auto own_pv = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                          const uint32_t (&f)[OwnParts][NR][2]) {
+#pragma unroll
+            for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                for (int q = 0; q < OwnParts; ++q) mma_bf16_16816(o[i][nt], a0, a1, a2, a3, f[q][nt][0], f[q][nt][1]);
+        };
+        auto qk = [&](float (&acc)[NR][4], int kk, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
+#pragma unroll
+            for (int nt = 0; nt < NR; ++nt) {
+                uint32_t b0, b1;
+                lds_v2_u32(sbase + (uint32_t)(Ly::Q + ((nt * KS + kk) * 32 + lane) * 8), b0, b1);
+                mma_bf16_16816(acc[nt], a0, a1, a2, a3, b0, b1);
+            }
+        };
+
+        // ---- the units of this warp
+        for (int un = ua + warp; un < ub && !dead; un += kWarps) {
+            float acc[2][NR][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[h][nt][e] = 0.f;
+            if (un < nc) {
+                // a record. Row i of S^T (and k index i of P V) is position
+                // i ^ ((i >> 1) & 1) of its 8: neighbouring rows g of a 16-byte
+                // read, and the four t4 of an 8-byte one, then alternate between
+                // the two halves of the banks
+                const int s = used % S;
+                const unsigned ph = (used / S) & 1u;
+                const bool ok = bar_wait(&bars[s], ph, abort, a.wait_ns);
+                if (!__all_sync(0xffffffffu, ok)) {
+                    atomicOr(&g_attn_kv4_error, kErrFullWait);
+                    dead = true;
+                    break;
+                }
+                if (valid[s]) {
+                    const uint32_t rec = ring + (uint32_t)(s * Rec::Bytes);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t x[2][W];
+                        KeyScale sc[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int key = 16 * h + 8 * k + key_g;
+                            const uint32_t at = rec + (uint32_t)(Rec::KC + key * Rec::RowBytes + t4 * (D / 8));
+                            if constexpr (W == 4) lds_v4_u32(at, x[k][0], x[k][1], x[k][2], x[k][3]);
+                            else lds_v2_u32(at, x[k][0], x[k][1]);
+                            const uint32_t sb = lds_u8(rec + (uint32_t)(Rec::KS + key * Rec::RowScales + (D == 128 ? t4 : t4 >> 1)));
+                            sc[k] = KeyScale(sb);
+                        }
+#pragma unroll
+                        for (int w = 0; w < W; ++w) {
+                            qk(acc[h], 2 * w, key_pair<0>(x[0][w], sc[0]), key_pair<0>(x[1][w], sc[1]),
+                               key_pair<1>(x[0][w], sc[0]), key_pair<1>(x[1][w], sc[1]));
+                            qk(acc[h], 2 * w + 1, key_pair<2>(x[0][w], sc[0]), key_pair<2>(x[1][w], sc[1]),
+                               key_pair<3>(x[0][w], sc[0]), key_pair<3>(x[1][w], sc[1]));
+                        }
+                    }
+                    const int left = L - un * kKv4Block;         // positions of the record that are cached
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                acc[h][nt][e] *= sl2;
+                                if (left < kKv4Block && 16 * h + 8 * (e >> 1) + key_g >= left) acc[h][nt][e] = NEG_INF;
+                            }
+                    softmax(acc);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t f[Parts][NR][2];
+                        p_frag(acc[h], f);
+                        uint32_t y[2][2][W / 2];                 // [k index + 8][even, odd key][word]
+                        ValScale sc[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            uint32_t sb[2];
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int key = 16 * h + 8 * k + 2 * t4 + (e ^ (t4 & 1));
+                                const uint32_t at = rec + (uint32_t)(Rec::VC + key * Rec::RowBytes + g * (D / 16));
+                                if constexpr (W == 4) lds_v2_u32(at, y[k][e][0], y[k][e][1]);
+                                else y[k][e][0] = lds_u32(at);
+                                sb[e] = lds_u8(rec + (uint32_t)(Rec::VS + key * Rec::RowScales + (D == 128 ? g >> 1 : g >> 2)));
+                            }
+                            sc[k] = ValScale(sb[0], sb[1]);
+                        }
+#pragma unroll
+                        for (int w = 0; w < W / 2; ++w) {
+                            const uint32_t a0 = __byte_perm(y[0][0][w], y[0][1][w], 0x5410), a1 = __byte_perm(y[0][0][w], y[0][1][w], 0x7632);
+                            const uint32_t a2 = __byte_perm(y[1][0][w], y[1][1][w], 0x5410), a3 = __byte_perm(y[1][0][w], y[1][1][w], 0x7632);
+                            pv(4 * w, val_pair<0>(a0, sc[0]), val_pair<0>(a1, sc[0]), val_pair<0>(a2, sc[1]), val_pair<0>(a3, sc[1]), f);
+                            pv(4 * w + 1, val_pair<1>(a0, sc[0]), val_pair<1>(a1, sc[0]), val_pair<1>(a2, sc[1]), val_pair<1>(a3, sc[1]), f);
+                            pv(4 * w + 2, val_pair<2>(a0, sc[0]), val_pair<2>(a1, sc[0]), val_pair<2>(a2, sc[1]), val_pair<2>(a3, sc[1]), f);
+                            pv(4 * w + 3, val_pair<3>(a0, sc[0]), val_pair<3>(a1, sc[0]), val_pair<3>(a2, sc[1]), val_pair<3>(a3, sc[1]), f);
+                        }
+                    }
+                }
+                ++used;
+                __syncwarp();                                    // every lane has read the stage
+                if (next < min(ub, nc)) {
+                    if (lane == 0) issue(next);
+                    ++issued;
+                    next += kWarps;
+                }
+            } else {
+                // 32 of the step's own rows, straight from the qkv rows (bf16)
+                const int j0 = (un - nc) * 32;
+                const uint16_t* base = a.qkv + (size_t)b * a.T * rowlen + (size_t)(a.Hq + kh) * D;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int w = 0; w < W; ++w) {
+                        uint4 x[2];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k) {
+                            const int j = j0 + 16 * h + 8 * k + key_g;
+                            x[k] = make_uint4(0u, 0u, 0u, 0u);
+                            if (j < a.T) x[k] = *reinterpret_cast<const uint4*>(base + (size_t)j * rowlen + t4 * (D / 4) + 8 * w);
+                        }
+                        qk(acc[h], 2 * w, __byte_perm(x[0].x, x[0].z, 0x5410), __byte_perm(x[1].x, x[1].z, 0x5410),
+                           __byte_perm(x[0].x, x[0].z, 0x7632), __byte_perm(x[1].x, x[1].z, 0x7632));
+                        qk(acc[h], 2 * w + 1, __byte_perm(x[0].y, x[0].w, 0x5410), __byte_perm(x[1].y, x[1].w, 0x5410),
+                           __byte_perm(x[0].y, x[0].w, 0x7632), __byte_perm(x[1].y, x[1].w, 0x7632));
+                    }
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e)
+                            acc[h][nt][e] = j0 + 16 * h + 8 * (e >> 1) + key_g <= tok[nt][e & 1] ? acc[h][nt][e] * sl2 : NEG_INF;
+                softmax(acc);
+                bool bad = false;
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t f[OwnParts][NR][2];
+                    own_p_frag(acc[h], f);
+#pragma unroll
+                    for (int w = 0; w < W / 2; ++w) {
+                        uint32_t y[2][2][4];
+#pragma unroll
+                        for (int k = 0; k < 2; ++k)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int j = j0 + 16 * h + 8 * k + 2 * t4 + (e ^ (t4 & 1));
+                                uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                                if (j < a.T) v = *reinterpret_cast<const uint4*>(base + (size_t)j * rowlen + (size_t)a.Hkv * D + g * (D / 8) + 8 * w);
+                                y[k][e][0] = v.x; y[k][e][1] = v.y; y[k][e][2] = v.z; y[k][e][3] = v.w;
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {    // infinities and NaN: 0 here, added below
+                                    if ((y[k][e][i] & 0x7F80u) == 0x7F80u) { y[k][e][i] &= 0xFFFF0000u; bad = true; }
+                                    if ((y[k][e][i] & 0x7F800000u) == 0x7F800000u) { y[k][e][i] &= 0xFFFFu; bad = true; }
+                                }
+                            }
+                        // tile 4 w + j: rows g are dims 8 w + j, rows g + 8 dims 8 w + 4 + j
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const int sel = j & 1 ? 0x7632 : 0x5410, i0 = j >> 1;
+                            own_pv(4 * w + j, __byte_perm(y[0][0][i0], y[0][1][i0], sel), __byte_perm(y[0][0][2 + i0], y[0][1][2 + i0], sel),
+                               __byte_perm(y[1][0][i0], y[1][1][i0], sel), __byte_perm(y[1][0][2 + i0], y[1][1][2 + i0], sel), f);
+                        }
+                    }
+                }
+                if (bad) s_flag[0] = 1;
+            }
+        }
+
+        // ---- the 8 warps' results into the CTA's: rows' maxima and sums, then
+        // the outputs scaled to the common maximum, added in two rounds
+#pragma unroll
+        for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float l = l_run[nt][e];
+                l += __shfl_xor_sync(0xffffffffu, l, 4);
+                l += __shfl_xor_sync(0xffffffffu, l, 8);
+                l += __shfl_xor_sync(0xffffffffu, l, 16);
+                if (g == 0) {
+                    s_wm[warp * RW + 8 * nt + 2 * t4 + e] = m_run[nt][e];
+                    s_wl[warp * RW + 8 * nt + 2 * t4 + e] = l;
+                }
+            }
+        __syncthreads();
+#pragma unroll
+        for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int r = 8 * nt + 2 * t4 + e;
+                float M = s_wm[r];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) M = fmaxf(M, s_wm[w * RW + r]);
+                const float f = m_run[nt][e] == NEG_INF ? 0.f : ex2(m_run[nt][e] - M);
+#pragma unroll
+                for (int i = 0; i < KS; ++i) {
+                    o[i][nt][e] *= f;
+                    o[i][nt][2 + e] *= f;
+                }
+            }
+        if (tid < RW) {
+            float M = s_wm[tid], l = 0.f;
+            for (int w = 1; w < kWarps; ++w) M = fmaxf(M, s_wm[w * RW + tid]);
+            for (int w = 0; w < kWarps; ++w)
+                l += s_wm[w * RW + tid] == NEG_INF ? 0.f : s_wl[w * RW + tid] * ex2(s_wm[w * RW + tid] - M);
+            s_m[tid] = M;
+            s_l[tid] = l;
+        }
+        // area[warp & 3][(nt, c, tile)][lane]
+        constexpr int Plane = NR * 4 * KS * 32;
+        if (warp >= 4) {
+#pragma unroll
+            for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int i = 0; i < KS; ++i) s_area[(warp - 4) * Plane + ((nt * 4 + c) * KS + i) * 32 + lane] = o[i][nt][c];
+        }
+        __syncthreads();
+        if (warp < 4) {
+#pragma unroll
+            for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int i = 0; i < KS; ++i) {
+                        float* p = s_area + warp * Plane + ((nt * 4 + c) * KS + i) * 32 + lane;
+                        *p += o[i][nt][c];
+                    }
+        }
+        __syncthreads();
+
+        // ---- items of 8 dims of one row: (nt, e, word, lane); whole tiles go
+        // out, parts to the workspace
+        constexpr int Items = NR * 2 * (W / 2) * 32;
+        auto item_sum = [&](int it, int& r, int& d0, float (&v)[8]) {
+            const int ln = it & 31, w = (it >> 5) % (W / 2), ne = (it >> 5) / (W / 2), nt = ne >> 1, e = ne & 1;
+            r = 8 * nt + 2 * (ln & 3) + e;
+            d0 = (ln >> 2) * (D / 8) + 8 * w;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float x = 0.f;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) x += s_area[q * Plane + ((nt * 4 + 2 * c + e) * KS + 4 * w + j) * 32 + ln];
+                    v[4 * c + j] = x;
+                }
+            if (s_flag[0] && r < R) {                            // rare: own value rows that are not finite
+                const int tk = (r0 + r) / a.G;
+                const int jb = max(0, (ua - nc) * 32), je = min(tk + 1, (ub - nc) * 32);
+                const uint16_t* vb = a.qkv + (size_t)b * a.T * rowlen + (size_t)(a.Hq + a.Hkv + kh) * D + d0;
+                for (int j = jb; j < je; ++j)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint32_t y = vb[(size_t)j * rowlen + i];
+                        if ((y & 0x7F80u) == 0x7F80u) v[i] += __uint_as_float(y << 16);
+                    }
+            }
+        };
+        auto store = [&](int r, int d0, const float (&v)[8], float l) {
+            if (r >= R) return;
+            const int j = (r0 + r) / a.G, h = kh * a.G + (r0 + r) - j * a.G;
+            const size_t at = ((size_t)b * a.T + j) * (size_t)a.Hq * D + (size_t)h * D + d0;
+            const float inv = 64.f / l;                          // (the values were taken times 2^-6)
+            if (OUTBF) {
+                uint4 y;
+                y.x = pack_bf16x2(v[0] * inv, v[1] * inv);
+                y.y = pack_bf16x2(v[2] * inv, v[3] * inv);
+                y.z = pack_bf16x2(v[4] * inv, v[5] * inv);
+                y.w = pack_bf16x2(v[6] * inv, v[7] * inv);
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at) = y;
+            } else {
+                float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);
+                p[0] = make_float4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+                p[1] = make_float4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
+            }
+        };
+        if (ua == 0 && ub == nu) {
+            for (int it = tid; it < Items; it += kThreads) {
+                int r, d0;
+                float v[8];
+                item_sum(it, r, d0, v);
+                store(r, d0, v, s_l[r]);
+            }
+        } else {
+            float* slot = a.partials + ((size_t)blockIdx.x * 2 + (ua == 0 ? 1 : 0)) * Ly::Slot;
+            for (int it = tid; it < Items; it += kThreads) {
+                int r, d0;
+                float v[8];
+                item_sum(it, r, d0, v);
+                float4* p = reinterpret_cast<float4*>(slot + it * 8);
+                p[0] = make_float4(v[0], v[1], v[2], v[3]);
+                p[1] = make_float4(v[4], v[5], v[6], v[7]);
+            }
+            if (tid < RW) {
+                slot[NR * 8 * D + tid] = s_m[tid];
+                slot[NR * 8 * D + RW + tid] = s_l[tid];
+            }
+            const int c0 = (int)(tile_at / per), c1 = (int)((tile_at + nu - 1) / per);   // the tile's CTAs
+            __threadfence();
+            __syncthreads();
+            if (tid == 0) {
+                const unsigned before_me = atomicAdd(a.counters + c0, 1u);
+                s_flag[1] = before_me == (unsigned)(c1 - c0);
+                if (s_flag[1]) a.counters[c0] = 0;
+            }
+            __syncthreads();
+            if (s_flag[1]) {
+                __threadfence();
+                const float* first = a.partials + ((size_t)c0 * 2 + 1) * Ly::Slot;
+                const size_t step = 2 * (size_t)Ly::Slot;        // contributors after the first: their slot 0
+                auto part = [&](int c) { return c == c0 ? first : a.partials + (size_t)c * step; };
+                if (tid < RW) {
+                    float M = NEG_INF, l = 0.f;
+                    for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(part(c) + NR * 8 * D + tid));
+                    for (int c = c0; c <= c1; ++c) {
+                        const float m = __ldcg(part(c) + NR * 8 * D + tid);
+                        l += m == NEG_INF ? 0.f : ex2(m - M) * __ldcg(part(c) + NR * 8 * D + RW + tid);
+                    }
+                    s_m[tid] = M;
+                    s_l[tid] = l;
+                }
+                __syncthreads();
+                for (int it = tid; it < Items; it += kThreads) {
+                    const int ln = it & 31, w = (it >> 5) % (W / 2), ne = (it >> 5) / (W / 2);
+                    const int r = 8 * (ne >> 1) + 2 * (ln & 3) + (ne & 1), d0 = (ln >> 2) * (D / 8) + 8 * w;
+                    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                    for (int c = c0; c <= c1; ++c) {
+                        const float* p = part(c);
+                        const float m = __ldcg(p + NR * 8 * D + r);
+                        const float f = m == NEG_INF ? 0.f : ex2(m - s_m[r]);
+                        const float4 x = __ldcg(reinterpret_cast<const float4*>(p + it * 8));
+                        const float4 y = __ldcg(reinterpret_cast<const float4*>(p + it * 8) + 1);
+                        v[0] += f * x.x; v[1] += f * x.y; v[2] += f * x.z; v[3] += f * x.w;
+                        v[4] += f * y.x; v[5] += f * y.y; v[6] += f * y.z; v[7] += f * y.w;
+                    }
+                    store(r, d0, v, s_l[r]);
+                }
+            }
+        }
+        __syncthreads();                                         // the area, Q and the flags are free again
+        if (tid == 0) s_flag[0] = 0;
+        u = tile_at + ub;
+        if (u == seq_at + (long long)tps * nu) {                 // the next sequence
+            seq_at = u;
+            ++b;
+        }
+    }
+    // after a wait that ran out: no copy may be in flight when the CTA ends
+    if (dead && !a.hold) {
+        volatile int none = 0;
+        for (; used < issued; ++used) bar_wait(&bars[used % S], (used / S) & 1u, &none, kWaitLimitNs);
+    }
+}
+
+template <int D, int NR, bool OUTBF>
+cudaError_t launch(const Args& a, int grid, cudaStream_t s) {
+    using Ly = Layout<D, NR>;
+    static_assert(Ly::Bytes <= (int)(Ly::TwoCtas ? kMaxDynSmem / 2 - 1024 : kMaxDynSmem), "shared memory budget");
+    cudaError_t e = cudaFuncSetAttribute(attn_kv4_kernel<D, NR, OUTBF>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ly::Bytes);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Ly::Bytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_kv4_kernel<D, NR, OUTBF>, a);
+}
+
+// Row tiles of a head group's T * G query rows, and rows per tile: as few
+// tiles of at most 32 rows as there can be, of equal size.
+void row_tiles(int rows, int& RT, int& per) {
+    RT = (rows + kRowTile - 1) / kRowTile;
+    per = (rows + RT - 1) / RT;
+}
+
+struct Plan {
+    int RT, rows, NR, grid;
+    size_t total;                // workspace bytes
+};
+Plan plan(int B, int T, int Hq, int Hkv, int D, int NB, int sms) {
+    Plan p;
+    row_tiles(T * (Hq / Hkv), p.RT, p.rows);
+    p.NR = (p.rows + 7) / 8;
+    const long long most = (long long)B * Hkv * p.RT * ((long long)NB + (T + 31) / 32);   // units at most
+    long long ctas = (long long)sms * (D / 64 * p.NR <= 2 ? 2 : 1);
+    ctas = ctas < (long long)(kCounterBytes / 4) ? ctas : (long long)(kCounterBytes / 4);
+    const long long want = (most + kMinUnits - 1) / kMinUnits;
+    p.grid = (int)(want < ctas ? want : ctas);
+    p.total = kCounterBytes + (size_t)p.grid * 2 * (p.NR * 8 * D + 2 * p.NR * 8) * 4;
+    return p;
+}
+
+}  // namespace
+
+size_t attention_kv4_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int NB, int sms) {
+    return plan(B, T, Hq, Hkv, D, NB, sms).total;
+}
+
+cudaError_t launch_attention_kv4(const uint16_t* qkv, const uint8_t* cache, const int32_t* table, const int32_t* len,
+                                 int B, int T, int Hq, int Hkv, int D, int NB, int pages, float scale, void* out,
+                                 bool out_bf16, void* ws, int sms, int hold, unsigned long long wait_ns,
+                                 cudaStream_t s) {
+    const Plan p = plan(B, T, Hq, Hkv, D, NB, sms);
+    Args a;
+    a.qkv = qkv; a.cache = cache; a.table = table; a.len = len;
+    a.B = B; a.T = T; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv; a.NB = NB; a.pages = pages;
+    a.RT = p.RT; a.rows = p.rows;
+    a.scale = scale; a.out = out;
+    a.counters = static_cast<unsigned*>(ws);
+    a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kCounterBytes);
+    a.hold = hold; a.wait_ns = wait_ns ? wait_ns : kWaitLimitNs;
+#define QV_KV4_CASE(DV, NRV) \
+    if (D == DV && p.NR == NRV) return out_bf16 ? launch<DV, NRV, true>(a, p.grid, s) : launch<DV, NRV, false>(a, p.grid, s);
+    QV_KV4_CASE(128, 1) QV_KV4_CASE(128, 2) QV_KV4_CASE(128, 3) QV_KV4_CASE(128, 4)
+    QV_KV4_CASE(64, 1) QV_KV4_CASE(64, 2) QV_KV4_CASE(64, 3) QV_KV4_CASE(64, 4)
+#undef QV_KV4_CASE
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t read_and_clear_attn_kv4_error(unsigned* code) {
+    cudaError_t e = cudaMemcpyFromSymbol(code, g_attn_kv4_error, sizeof(unsigned));
+    if (e != cudaSuccess) return e;
+    const unsigned zero = 0;
+    return cudaMemcpyToSymbol(g_attn_kv4_error, &zero, sizeof(unsigned));
+}
+
+}  // namespace qv

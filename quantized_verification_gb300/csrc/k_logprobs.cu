@@ -1,0 +1,380 @@
+// k_logprobs.cu -- log probability of one given token per row of logits, the
+// row's entropy, and its K most probable tokens.
+//
+//   The verifier's logits stay in high precision for the acceptance test
+//   (gist.science/it summary, section 2 item 3); a server reports the emitted
+//   tokens' log probabilities from the same logits.
+//
+// With m = max_v x_v, z_v = (x_v - m) log2 e, S = sum 2^z_v, T = sum z_v 2^z_v:
+//   log p_v = (x_v - m) - ln S,   H = ln S - ln 2 * T / S.
+// One pass over the row: each thread keeps its own running m, S and T and
+// rescales them when its m grows by d: S *= 2^-d, T = 2^-d (T - d S). The
+// alternatives cost the pass nothing more: m is also the thread's largest
+// logit, and the K-th largest of the threads' maxima, tau, is a lower bound of
+// the row's K-th largest logit, reached by few more than K threads. Only
+// those threads' entries (1/512 of the slice each) are read again, from L2,
+// by whole warps that keep a sorted list of 32 keys (value, then the lower
+// index) across their lanes.
+//
+// A row is the work of one CTA, or of a cluster of C of them that split it
+// (launch_token_logprobs) and combine through distributed shared memory.
+
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+#include <cstdint>
+
+#include "qv_internal.h"
+#include "qv_ptx.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace qv {
+namespace {
+
+constexpr int kLpThreads = 512;
+constexpr int kLpWarps = kLpThreads / 32;
+constexpr int kLpMaxCluster = 16;
+constexpr int kLpUnroll = 4;                    // vectors in flight per thread
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+static_assert(kLpMaxCluster <= kLpWarps, "one warp per CTA's list in the cluster merge");
+
+struct LpArgs {
+    const uint8_t* x;          // logits [M][V]
+    const int32_t* tok;        // [M]
+    int V, K;
+    float* logprob;            // [M]
+    float* entropy;            // [M] or null
+    int32_t* top_tok;          // [M][K]
+    float* top_lp;             // [M][K]
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// The larger of the two, NaN if either is NaN.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+// Running statistics of some entries: their maximum (-inf for none), and the
+// sums S and T relative to it.
+struct Stat {
+    float m, S, T;
+};
+__device__ __forceinline__ Stat combine(Stat a, Stat b) {
+    const float m = fmaxf(a.m, b.m);
+    // a part with no probability (S == 0: nothing above -inf) adds nothing
+    const float da = a.S == 0.f ? 0.f : (a.m - m) * kLog2e, db = b.S == 0.f ? 0.f : (b.m - m) * kLog2e;
+    const float fa = ex2(max_nan(da, -150.f)), fb = ex2(max_nan(db, -150.f));
+    Stat r;
+    r.m = m;
+    r.S = a.S * fa + b.S * fb;
+    r.T = (fa == 0.f ? 0.f : fa * (a.T + da * a.S)) + (fb == 0.f ? 0.f : fb * (b.T + db * b.S));
+    return r;
+}
+
+template <int N>
+__device__ __forceinline__ void add_entries(Stat& st, const float (&v)[N]) {
+    float mx = v[0];
+#pragma unroll
+    for (int i = 1; i < N; ++i) mx = fmaxf(mx, v[i]);
+    if (mx > st.m) {
+        const float d = (st.m - mx) * kLog2e;                  // -inf on the first entries (S = T = 0)
+        const float f = ex2(d);
+        st.T = f == 0.f ? 0.f : f * (st.T + d * st.S);
+        st.S *= f;
+        st.m = mx;
+    }
+    // nothing above -inf yet: subtract 0, so that -inf entries count 0
+    const float ref = st.m == -__uint_as_float(0x7F800000u) ? 0.f : st.m;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        const float z = max_nan((v[i] - ref) * kLog2e, -150.f);   // 2^-150 is 0 in binary32; keeps 0 * z finite
+        const float e = ex2(z);
+        st.S += e;
+        st.T += z * e;
+    }
+}
+
+// A key that orders entries by value, then by the lower index; 0 is below all.
+// -0 counts as +0. (A NaN's key is 1: below every number's.)
+__device__ __forceinline__ unsigned long long entry_key(float v, int idx) {
+    if (v != v) return 1ull;
+    const uint32_t u = __float_as_uint(v + 0.f);
+    const uint32_t o = u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
+    return ((unsigned long long)o << 32) | (uint32_t)~(uint32_t)idx;
+}
+__device__ __forceinline__ float key_value(unsigned long long k) {
+    const uint32_t o = (uint32_t)(k >> 32);
+    return __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xFFFFFFFFu));
+}
+
+// Sorts one value per lane, the largest in lane 0 (Batcher's bitonic network).
+template <class T>
+__device__ __forceinline__ T warp_sort_desc(T v) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+        for (int j = k >> 1; j > 0; j >>= 1) {
+            const T o = __shfl_xor_sync(0xffffffffu, v, j);
+            const bool up = ((lane & k) == 0) == ((lane & j) == 0);   // this lane keeps the larger
+            v = up ? (o > v ? o : v) : (o < v ? o : v);
+        }
+    return v;
+}
+// The 32 largest of two descending lists, descending; `o` is the other list
+// reversed (lane i holds its entry 31 - i).
+template <class T>
+__device__ __forceinline__ T warp_merge_desc(T v, T o) {
+    const int lane = threadIdx.x & 31;
+    v = o > v ? o : v;                                         // bitonic, and the 32 largest of both
+#pragma unroll
+    for (int j = 16; j > 0; j >>= 1) {
+        const T p = __shfl_xor_sync(0xffffffffu, v, j);
+        v = (lane & j) == 0 ? (p > v ? p : v) : (p < v ? p : v);
+    }
+    return v;
+}
+// Merges the descending lists of warps 0..n-1 (n a power of two) into warp
+// 0's. All threads of the CTA call it.
+template <class T>
+__device__ __forceinline__ T block_merge_desc(T v, T* sm /* [kLpWarps][32] */, int n) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    for (int h = n >> 1; h > 0; h >>= 1) {
+        if (warp >= h && warp < 2 * h) sm[warp * 32 + lane] = v;
+        __syncthreads();
+        if (warp < h) v = warp_merge_desc(v, sm[(warp + h) * 32 + 31 - lane]);
+    }
+    return v;
+}
+
+template <bool BF16>
+struct Row {
+    static constexpr int E = BF16 ? 8 : 4;      // entries of a 16-byte vector
+    const uint8_t* p;
+    int head, nvec, tail;                       // leading single entries, vectors, trailing single entries
+
+    __device__ Row(const uint8_t* x, size_t row, int V) {
+        p = x + row * (size_t)V * (BF16 ? 2 : 4);
+        const int off = (int)(reinterpret_cast<uintptr_t>(p) & 15u);
+        head = min(V, ((16 - off) & 15) / (BF16 ? 2 : 4));
+        nvec = (V - head) / E;
+        tail = V - head - nvec * E;
+    }
+    __device__ __forceinline__ float at(int i) const {
+        if (BF16) return __uint_as_float((uint32_t)reinterpret_cast<const uint16_t*>(p)[i] << 16);
+        return reinterpret_cast<const float*>(p)[i];
+    }
+    __device__ __forceinline__ uint4 vec(int n) const {
+        return reinterpret_cast<const uint4*>(p + (size_t)head * (BF16 ? 2 : 4))[n];
+    }
+    static __device__ __forceinline__ void unpack(const uint4& u, float* v) {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (BF16) {
+                v[2 * i] = __uint_as_float(w[i] << 16);
+                v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+            } else {
+                v[i] = __uint_as_float(w[i]);
+            }
+        }
+    }
+    // The single entry thread t of the row's first CTA owns, or -1.
+    __device__ __forceinline__ int single(int t) const {
+        if (t < head) return t;
+        if (t >= 16 && t < 16 + tail) return head + nvec * E + (t - 16);
+        return -1;
+    }
+};
+
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
+
+// Inserts the keys of the lanes where `want` holds into the warp's descending
+// list (lane i holds the i-th).
+__device__ __forceinline__ void warp_insert(unsigned long long& list, unsigned long long key, bool want) {
+    const int lane = threadIdx.x & 31;
+    unsigned who = __ballot_sync(0xffffffffu, want);
+    while (who) {
+        const unsigned long long k = __shfl_sync(0xffffffffu, key, __ffs(who) - 1);
+        who &= who - 1;
+        const int pos = __popc(__ballot_sync(0xffffffffu, list > k));
+        const unsigned long long up = __shfl_up_sync(0xffffffffu, list, 1);
+        list = lane < pos ? list : (lane == pos ? k : up);
+    }
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const LpArgs a) {
+    constexpr int E = Row<BF16>::E;
+    __shared__ Stat s_stat[kLpWarps];
+    __shared__ Stat c_stat[kLpMaxCluster];                     // written by every CTA of the row (in CTA 0)
+    __shared__ unsigned long long s_keys[kLpWarps * 32];
+    __shared__ unsigned long long c_keys[kLpMaxCluster * 32];
+    __shared__ int s_who[kLpThreads];
+    __shared__ int s_n;
+    __shared__ float s_tau;
+    cg::cluster_group cluster = cg::this_cluster();
+    const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    if (C > 1) cluster_arrive_relaxed();                       // waited for before the first store into another CTA
+    allow_dependent_launch();
+    grid_dependency_wait();
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const size_t row = blockIdx.x / C;
+    const Row<BF16> r(a.x, row, a.V);
+    const int per = (r.nvec + C - 1) / C;
+    const int v0 = min(r.nvec, rank * per), v1 = min(r.nvec, v0 + per);
+    if (tid == 0) s_n = 0;
+
+    // ---- the pass
+    Stat st = {-__uint_as_float(0x7F800000u), 0.f, 0.f};
+    const int own1 = rank == 0 ? r.single(tid) : -1;
+    if (own1 >= 0) {
+        const float v[1] = {r.at(own1)};
+        add_entries(st, v);
+    }
+    int n = v0 + tid;
+    for (; n + (kLpUnroll - 1) * kLpThreads < v1; n += kLpUnroll * kLpThreads) {
+        uint4 u[kLpUnroll];
+#pragma unroll
+        for (int i = 0; i < kLpUnroll; ++i) u[i] = r.vec(n + i * kLpThreads);
+        float v[kLpUnroll * E];
+#pragma unroll
+        for (int i = 0; i < kLpUnroll; ++i) Row<BF16>::unpack(u[i], v + i * E);
+        add_entries(st, v);
+    }
+    for (; n < v1; n += kLpThreads) {
+        float v[E];
+        Row<BF16>::unpack(r.vec(n), v);
+        add_entries(st, v);
+    }
+    const float mine = st.m;
+
+    // ---- the CTA's statistics, then the row's in CTA 0, in rank order
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        Stat o;
+        o.m = __shfl_xor_sync(0xffffffffu, st.m, off);
+        o.S = __shfl_xor_sync(0xffffffffu, st.S, off);
+        o.T = __shfl_xor_sync(0xffffffffu, st.T, off);
+        st = combine(st, o);
+    }
+    if (lane == 0) s_stat[warp] = st;
+
+    // ---- this CTA's K largest entries
+    unsigned long long list = 0;
+    if (a.K > 0) {
+        float* s_f = reinterpret_cast<float*>(s_keys);
+        float t = block_merge_desc(warp_sort_desc(mine), s_f, kLpWarps);
+        if (tid == a.K - 1) s_tau = t;                         // K <= 32: warp 0
+        __syncthreads();
+        const float tau = s_tau;
+        if (mine >= tau) s_who[atomicAdd(&s_n, 1)] = tid;      // (an entry's place in the list does not matter)
+        __syncthreads();
+        for (int i = warp; i < s_n; i += kLpWarps) {
+            const int t1 = s_who[i];
+            const int one = rank == 0 ? r.single(t1) : -1;
+            if (one >= 0) {
+                const float v = r.at(one);
+                warp_insert(list, entry_key(v, one), lane == 0 && v >= tau);
+            }
+            for (int base = v0 + t1; base < v1; base += 32 * kLpThreads) {
+                const int vn = base + lane * kLpThreads;
+                float v[E];
+                if (vn < v1) Row<BF16>::unpack(r.vec(vn), v);
+#pragma unroll
+                for (int e = 0; e < E; ++e) {
+                    const bool in = vn < v1 && v[e] >= tau;
+                    if (!__any_sync(0xffffffffu, in)) continue;
+                    const unsigned long long k = in ? entry_key(v[e], r.head + vn * E + e) : 0ull;
+                    const unsigned long long least = __shfl_sync(0xffffffffu, list, a.K - 1);
+                    warp_insert(list, k, in && k > least);
+                }
+            }
+        }
+        __syncthreads();                                       // s_keys still held the maxima's lists
+        list = block_merge_desc(list, s_keys, kLpWarps);
+    }
+    __syncthreads();
+    if (C > 1) {
+        cluster_wait();                                        // every CTA of the cluster has started
+        if (warp == 0) {
+            Stat c = s_stat[0];
+            for (int w = 1; w < kLpWarps; ++w) c = combine(c, s_stat[w]);
+            if (lane == 0) *cluster.map_shared_rank(c_stat + rank, 0) = c;
+            if (a.K > 0) *cluster.map_shared_rank(c_keys + rank * 32 + lane, 0) = list;
+        }
+        cluster.sync();                                        // every push into CTA 0 has landed
+        if (rank != 0) return;
+        if (a.K > 0) {
+            list = warp < C ? c_keys[warp * 32 + lane] : 0ull;
+            list = block_merge_desc(list, s_keys, C);
+        }
+    }
+    if (warp != 0) return;
+    Stat c = C > 1 ? c_stat[0] : s_stat[0];
+    for (int i = 1; i < (C > 1 ? C : kLpWarps); ++i) c = combine(c, C > 1 ? c_stat[i] : s_stat[i]);
+    const float NEG_INF = -__uint_as_float(0x7F800000u);
+    const bool none = c.m == NEG_INF;                          // every entry is -inf (or NaN, and then S is NaN)
+    const float ls = none ? c.S : logf(c.S);
+    const float m = none ? 0.f : c.m;
+    if (lane == 0) {
+        const int tk = a.tok[row];
+        float lp = 0.f;                                        // tokens outside the vocabulary (padding) count 0
+        if (tk >= 0 && tk < a.V) lp = (r.at(tk) - m) - ls;
+        a.logprob[row] = lp;
+        if (a.entropy) {
+            const float h = none ? ls : ls - kLn2 * (c.T / c.S);
+            a.entropy[row] = h < 0.f ? 0.f : h;                // (rounding below 0)
+        }
+    }
+    if (lane < a.K) {
+        const size_t o = row * (size_t)a.K + lane;
+        a.top_tok[o] = list > 1ull ? (int32_t)~(uint32_t)list : -1;
+        a.top_lp[o] = list > 1ull ? (key_value(list) - m) - ls : __uint_as_float(0x7FC00000u);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_token_logprobs(const void* x, bool bf16, const int32_t* tok, int M, int V, int K, float* logprob,
+                                  float* entropy, int32_t* top_tok, float* top_lp, int sms, cudaStream_t s) {
+    LpArgs a;
+    a.x = static_cast<const uint8_t*>(x);
+    a.tok = tok; a.V = V; a.K = K; a.logprob = logprob; a.entropy = entropy; a.top_tok = top_tok; a.top_lp = top_lp;
+    int C = 1;
+    while (C < kLpMaxCluster && (long long)M * C * 2 <= 2 * sms && V / (C * 2) >= 2 * kLpThreads * (bf16 ? 8 : 4)) C *= 2;
+    auto kernel = bf16 ? token_logprobs_kernel<true> : token_logprobs_kernel<false>;
+    if (C > 8) {
+        cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e != cudaSuccess) return e;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(M * C));
+    cfg.blockDim = dim3(kLpThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = C;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[1].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
+}  // namespace qv

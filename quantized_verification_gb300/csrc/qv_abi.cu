@@ -692,6 +692,161 @@ qv_status qv_logit_fidelity(const float* ref_logits, const float* logits, int M,
     return ok();
 }
 
+namespace {
+bool is_dtype(qv_dtype t) { return t == QV_F32 || t == QV_BF16; }
+
+// The shape of a 4-bit cache call; t_max is T's largest value.
+qv_status check_kv4_shape(int B, int T, int t_max, int Hkv, int D, int NB, int pages, bool table) {
+    if (B < 1 || B > 65535) return fail(QV_ERR_INVALID_ARG, "B=%d outside [1, 65535]", B);
+    if (T < 1 || T > t_max) return fail(QV_ERR_INVALID_ARG, "T=%d outside [1, %d]", T, t_max);
+    if (Hkv < 1 || Hkv > QV_KV4_MAX_HEADS) return fail(QV_ERR_INVALID_ARG, "Hkv=%d outside [1, %d]", Hkv, QV_KV4_MAX_HEADS);
+    if (D != 64 && D != 128) return fail(QV_ERR_INVALID_ARG, "D=%d must be 64 or 128", D);
+    if (NB < 0 || NB >= (1 << 26)) return fail(QV_ERR_INVALID_ARG, "NB=%d outside [0, 2^26)", NB);
+    if (pages < 0) return fail(QV_ERR_INVALID_ARG, "pages=%d must be >= 0", pages);
+    if (!table && (long long)B * NB > pages)
+        return fail(QV_ERR_INVALID_ARG, "without a block table the cache must hold B*NB=%lld pages, it has %d",
+                    (long long)B * NB, pages);
+    return QV_OK;
+}
+
+// Rows one write or read call handles.
+constexpr int kKv4MaxRows = 1 << 24;
+}  // namespace
+
+qv_status qv_kv4_write(const void* qkv, qv_dtype dtype, const int32_t* start, const int32_t* count,
+                       const int32_t* block_table, int B, int T, int Hq, int Hkv, int D, int NB, int pages,
+                       uint8_t* cache, cudaStream_t stream) {
+    qv_status st = check_kv4_shape(B, T, kKv4MaxRows, Hkv, D, NB, pages, block_table != nullptr);
+    if (st != QV_OK) return st;
+    if ((long long)B * T > kKv4MaxRows) return fail(QV_ERR_INVALID_ARG, "B*T must be <= 2^24");
+    if (Hq < 0 || Hq > 65535) return fail(QV_ERR_INVALID_ARG, "Hq=%d outside [0, 65535]", Hq);
+    if (NB < 1 || pages < 1) return fail(QV_ERR_INVALID_ARG, "the cache has no pages (NB=%d, pages=%d)", NB, pages);
+    if (!is_dtype(dtype)) return fail(QV_ERR_INVALID_ARG, "dtype must be QV_F32 or QV_BF16");
+    if (!qkv || !start || !cache) return fail(QV_ERR_INVALID_ARG, "null pointer");
+    if (!aligned(qkv, 16) || !aligned(cache, 16) || !aligned(start, 4) || (count && !aligned(count, 4)) ||
+        (block_table && !aligned(block_table, 4)))
+        return fail(QV_ERR_INVALID_ARG, "qkv and cache must be 16-byte aligned, int32 buffers 4-byte aligned");
+    QV_CHECK_DEV(qkv);
+    QV_CHECK_DEV(start);
+    QV_CHECK_DEV(count);
+    QV_CHECK_DEV(block_table);
+    QV_CHECK_DEV(cache);
+    cudaError_t e = qv::launch_kv4_write(qkv, dtype == QV_BF16, start, count, block_table, B, T, Hq, Hkv, D, NB, pages,
+                                         cache, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "qv_kv4_write launch");
+    return ok();
+}
+
+qv_status qv_kv4_read(const uint8_t* cache, const int32_t* start, const int32_t* count, const int32_t* block_table,
+                      int B, int T, int Hkv, int D, int NB, int pages, void* k_out, void* v_out, qv_dtype dtype,
+                      cudaStream_t stream) {
+    qv_status st = check_kv4_shape(B, T, kKv4MaxRows, Hkv, D, NB, pages, block_table != nullptr);
+    if (st != QV_OK) return st;
+    if ((long long)B * T > kKv4MaxRows) return fail(QV_ERR_INVALID_ARG, "B*T must be <= 2^24");
+    if (NB < 1 || pages < 1) return fail(QV_ERR_INVALID_ARG, "the cache has no pages (NB=%d, pages=%d)", NB, pages);
+    if (!is_dtype(dtype)) return fail(QV_ERR_INVALID_ARG, "dtype must be QV_F32 or QV_BF16");
+    if (!cache || !start || !k_out || !v_out) return fail(QV_ERR_INVALID_ARG, "null pointer");
+    if (!aligned(cache, 16) || !aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(start, 4) ||
+        (count && !aligned(count, 4)) || (block_table && !aligned(block_table, 4)))
+        return fail(QV_ERR_INVALID_ARG, "cache, k_out and v_out must be 16-byte aligned, int32 buffers 4-byte aligned");
+    QV_CHECK_DEV(cache);
+    QV_CHECK_DEV(start);
+    QV_CHECK_DEV(count);
+    QV_CHECK_DEV(block_table);
+    QV_CHECK_DEV(k_out);
+    QV_CHECK_DEV(v_out);
+    cudaError_t e = qv::launch_kv4_read(cache, start, count, block_table, B, T, Hkv, D, NB, pages, k_out, v_out,
+                                        dtype == QV_BF16, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "qv_kv4_read launch");
+    return ok();
+}
+
+namespace {
+qv_status check_attention_kv4_shape(int B, int T, int Hq, int Hkv, int D, int NB) {
+    qv_status st = check_kv4_shape(B, T, QV_MAX_M, Hkv, D, NB, 0, true);
+    if (st != QV_OK) return st;
+    if (Hq < Hkv || Hq > 65535 || Hq % Hkv != 0)
+        return fail(QV_ERR_INVALID_ARG, "Hq=%d must be a positive multiple of Hkv=%d and <= 65535", Hq, Hkv);
+    return QV_OK;
+}
+}  // namespace
+
+size_t qv_attention_kv4_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int NB) {
+    if (check_attention_kv4_shape(B, T, Hq, Hkv, D, NB) != QV_OK) return 0;
+    cudaError_t e;
+    const int sms = sms_of_current_device(&e);
+    if (e != cudaSuccess) {
+        cuda_fail(e, "device query");
+        return 0;
+    }
+    return qv::attention_kv4_workspace_bytes(B, T, Hq, Hkv, D, NB, sms);
+}
+
+qv_status qv_attention_verify_kv4(const uint16_t* qkv, const uint8_t* cache, const int32_t* block_table,
+                                  const int32_t* cache_len, int B, int T, int Hq, int Hkv, int D, int NB, int pages,
+                                  float scale, void* out, qv_dtype out_dtype, void* workspace, size_t workspace_bytes,
+                                  cudaStream_t stream) {
+    qv_status st = check_attention_kv4_shape(B, T, Hq, Hkv, D, NB);
+    if (st != QV_OK) return st;
+    if ((st = check_kv4_shape(B, T, QV_MAX_M, Hkv, D, NB, pages, block_table != nullptr)) != QV_OK) return st;
+    if (!qkv || !cache_len || !out) return fail(QV_ERR_INVALID_ARG, "null pointer");
+    if (NB > 0 && !cache) return fail(QV_ERR_INVALID_ARG, "cache is null with NB > 0");
+    if (!is_dtype(out_dtype)) return fail(QV_ERR_INVALID_ARG, "out_dtype must be QV_F32 or QV_BF16");
+    if (!(scale > 0.0f) || scale > 3.0e38f) return fail(QV_ERR_INVALID_ARG, "scale must be finite and > 0");
+    if (!aligned(qkv, 16) || (cache && !aligned(cache, 16)) || !aligned(out, 16) || !aligned(cache_len, 4) ||
+        (block_table && !aligned(block_table, 4)))
+        return fail(QV_ERR_INVALID_ARG, "qkv, cache and out must be 16-byte aligned, int32 buffers 4-byte aligned");
+    cudaError_t e;
+    const int sms = sms_of_current_device(&e);
+    if (e != cudaSuccess) return cuda_fail(e, "device query");
+    const size_t need = qv::attention_kv4_workspace_bytes(B, T, Hq, Hkv, D, NB, sms);
+    if (!workspace) return fail(QV_ERR_WORKSPACE, "workspace is null (%zu bytes needed)", need);
+    if (!aligned(workspace, 16)) return fail(QV_ERR_WORKSPACE, "workspace must be 16-byte aligned");
+    if (workspace_bytes < need) return fail(QV_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
+    QV_CHECK_DEV(qkv);
+    QV_CHECK_DEV(cache);
+    QV_CHECK_DEV(block_table);
+    QV_CHECK_DEV(cache_len);
+    QV_CHECK_DEV(out);
+    QV_CHECK_DEV(workspace);
+    const int hold = qv::debug_take_hold_attention() ? 1 : 0;
+    e = qv::launch_attention_kv4(qkv, cache, block_table, cache_len, B, T, Hq, Hkv, D, NB, pages, scale, out,
+                                 out_dtype == QV_BF16, workspace, sms, hold, qv::debug_slot_wait_ns(), stream);
+    if (e != cudaSuccess) return cuda_fail(e, "qv_attention_verify_kv4 launch");
+    return ok();
+}
+
+qv_status qv_token_logprobs(const void* logits, qv_dtype dtype, const int32_t* tokens, int M, int V, int top_k,
+                            float* logprob, float* entropy, int32_t* top_tokens, float* top_logprobs,
+                            cudaStream_t stream) {
+    if (!logits || !tokens || !logprob) return fail(QV_ERR_INVALID_ARG, "null pointer");
+    if (!is_dtype(dtype)) return fail(QV_ERR_INVALID_ARG, "dtype must be QV_F32 or QV_BF16");
+    if (M < 1 || M > 65535) return fail(QV_ERR_INVALID_ARG, "M=%d outside [1, 65535]", M);
+    if (V < 1 || V > (1 << 24)) return fail(QV_ERR_INVALID_ARG, "V=%d outside [1, 2^24]", V);
+    if (top_k < 0 || top_k > QV_MAX_TOP_K || top_k > V)
+        return fail(QV_ERR_INVALID_ARG, "top_k=%d outside [0, min(%d, V)]", top_k, QV_MAX_TOP_K);
+    if (top_k > 0 && (!top_tokens || !top_logprobs)) return fail(QV_ERR_INVALID_ARG, "top_tokens / top_logprobs null with top_k > 0");
+    if (!aligned(logits, dtype == QV_F32 ? 4 : 2) || !aligned(tokens, 4) || !aligned(logprob, 4) ||
+        (entropy && !aligned(entropy, 4)) || (top_tokens && !aligned(top_tokens, 4)) ||
+        (top_logprobs && !aligned(top_logprobs, 4)))
+        return fail(QV_ERR_INVALID_ARG, "buffers must be aligned to their elements");
+    QV_CHECK_DEV(logits);
+    QV_CHECK_DEV(tokens);
+    QV_CHECK_DEV(logprob);
+    QV_CHECK_DEV(entropy);
+    if (top_k > 0) {
+        QV_CHECK_DEV(top_tokens);
+        QV_CHECK_DEV(top_logprobs);
+    }
+    cudaError_t e;
+    const int sms = sms_of_current_device(&e);
+    if (e != cudaSuccess) return cuda_fail(e, "device query");
+    e = qv::launch_token_logprobs(logits, dtype == QV_BF16, tokens, M, V, top_k, logprob, entropy, top_tokens,
+                                  top_logprobs, sms, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "qv_token_logprobs launch");
+    return ok();
+}
+
 qv_status qv_accept(const int32_t* verify_tokens, const int32_t* draft, int B, int gamma,
                     int32_t* accept_len, int32_t* out_tokens, cudaStream_t stream) {
     if (!verify_tokens || !accept_len || !out_tokens) return fail(QV_ERR_INVALID_ARG, "null pointer");
@@ -855,12 +1010,13 @@ qv_status qv_device_error(unsigned int* code) {
     if (!code) return fail(QV_ERR_INVALID_ARG, "code is null");
     cudaError_t e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
-    unsigned tc = 0, at = 0;
+    unsigned tc = 0, at = 0, a4 = 0;
     e = qv::read_and_clear_stream_gemm_error(code);
     if (e == cudaSuccess) e = qv::read_and_clear_tc_gemm_error(&tc);
     if (e == cudaSuccess) e = qv::read_and_clear_attn_error(&at);
+    if (e == cudaSuccess) e = qv::read_and_clear_attn_kv4_error(&a4);
     if (e != cudaSuccess) return cuda_fail(e, "reading the device error word");
-    *code |= tc | at;
+    *code |= tc | at | a4;
     return ok();
 }
 

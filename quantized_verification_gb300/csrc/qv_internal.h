@@ -154,6 +154,27 @@ cudaError_t launch_attention_verify(const uint16_t* qkv, const KvMaps* maps, con
                                     unsigned long long wait_ns, cudaStream_t s);
 cudaError_t read_and_clear_attn_error(unsigned* code);
 
+// The 4-bit paged KV cache: rows written (k_kv4.cu), positions read back, and
+// attention over it (k_attn_kv4.cu). table may be null (sequence b's blocks
+// are pages b * NB + i), count may be null (all T rows).
+cudaError_t launch_kv4_write(const void* x, bool bf16, const int32_t* start, const int32_t* count,
+                             const int32_t* table, int B, int T, int Hq, int Hkv, int D, int NB, int pages,
+                             uint8_t* cache, cudaStream_t s);
+cudaError_t launch_kv4_read(const uint8_t* cache, const int32_t* start, const int32_t* count, const int32_t* table,
+                            int B, int T, int Hkv, int D, int NB, int pages, void* k_out, void* v_out, bool bf16,
+                            cudaStream_t s);
+size_t attention_kv4_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int NB, int sms);
+cudaError_t launch_attention_kv4(const uint16_t* qkv, const uint8_t* cache, const int32_t* table, const int32_t* len,
+                                 int B, int T, int Hq, int Hkv, int D, int NB, int pages, float scale, void* out,
+                                 bool out_bf16, void* ws, int sms, int hold, unsigned long long wait_ns,
+                                 cudaStream_t s);
+cudaError_t read_and_clear_attn_kv4_error(unsigned* code);
+
+// Log probabilities of given tokens, entropy and the K most probable tokens
+// of each row of logits (k_logprobs.cu).
+cudaError_t launch_token_logprobs(const void* x, bool bf16, const int32_t* tok, int M, int V, int K, float* logprob,
+                                  float* entropy, int32_t* top_tok, float* top_lp, int sms, cudaStream_t s);
+
 // Logit-fidelity diagnostic (k_fidelity.cu): per row KL(softmax(a) ||
 // softmax(b)) and both top-1 indices.
 cudaError_t launch_logit_fidelity(const float* a, const float* b, int M, int V, float* kl, int32_t* top_a,

@@ -31,9 +31,12 @@ EXPORTS = ("qv_quantize_act", "qv_w8a8_linear", "qv_lm_head_argmax", "qv_accept"
            "qv_rmsnorm_quant", "qv_swiglu_quant", "qv_w8a8_swiglu", "qv_spec_sample",
            "qv_tree_accept", "qv_quantize_weight_w4", "qv_w4a8_linear", "qv_w4a8_swiglu",
            "qv_w4a8_lm_head_argmax", "qv_logit_fidelity", "qv_attention_workspace_bytes",
-           "qv_attention_verify", "qv_debug_set_slot_wait_ns", "qv_debug_drop_partials",
+           "qv_attention_verify", "qv_kv4_write", "qv_kv4_read", "qv_attention_kv4_workspace_bytes",
+           "qv_attention_verify_kv4", "qv_token_logprobs", "qv_debug_set_slot_wait_ns", "qv_debug_drop_partials",
            "qv_debug_hold_attention_loads")
 MAX_STACK_M = 16
+QV_KV4_BLOCK = 32        # positions of a 4-bit cache block
+QV_MAX_TOP_K = 32
 
 
 class LinearDesc(ctypes.Structure):
@@ -87,6 +90,12 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         L.qv_attention_workspace_bytes.argtypes = [I, I, I, I, I, I]
         L.qv_attention_workspace_bytes.restype = S
         L.qv_attention_verify.argtypes = [P, P, P, P, I, I, I, I, I, I, ctypes.c_float, P, P, S, P]
+        L.qv_kv4_write.argtypes = [P, I, P, P, P, I, I, I, I, I, I, I, P, P]
+        L.qv_kv4_read.argtypes = [P, P, P, P, I, I, I, I, I, I, P, P, I, P]
+        L.qv_attention_kv4_workspace_bytes.argtypes = [I, I, I, I, I, I]
+        L.qv_attention_kv4_workspace_bytes.restype = S
+        L.qv_attention_verify_kv4.argtypes = [P, P, P, P, I, I, I, I, I, I, I, ctypes.c_float, P, I, P, S, P]
+        L.qv_token_logprobs.argtypes = [P, I, P, I, I, I, P, P, P, P, P]
         L.qv_w4a8_linear.argtypes = [P, P, I, I, P, P, I, P, I, P, P, S, P]
         L.qv_w4a8_swiglu.argtypes = [P, P, I, I, P, P, I, P, P, S, P]
         L.qv_w4a8_lm_head_argmax.argtypes = [P, P, I, I, P, P, I, P, P, P, S, P]
@@ -336,6 +345,100 @@ def qv_attention_verify(qkv, k_cache, v_cache, cache_len, T, Hq, Hkv, scale, out
                                       ctypes.c_float(scale), _ptr(out), _ptr(workspace),
                                       0 if workspace is None else workspace.numel(),
                                       ctypes.c_void_p(_stream(stream))))
+
+
+# --- the 4-bit paged KV cache: uint8 [pages, Hkv, 34 * D], blocks of 32 positions ---
+def kv4_cache(pages: int, Hkv: int, D: int, device=None) -> torch.Tensor:
+    """An empty 4-bit cache of `pages` blocks (torch allocation). Its bytes need no initial value."""
+    return torch.empty(pages, Hkv, 34 * D, dtype=torch.uint8, device=device or "cuda")
+
+
+def _kv4_shapes(cache, block_table, B):
+    """Hkv, D, NB and pages of a cache and of its block table (None: sequence
+    b's blocks are pages b * NB + i, with the pool divided evenly)."""
+    _need(cache.dtype == torch.uint8 and cache.dim() == 3 and cache.shape[2] % 34 == 0,
+          "cache must be uint8 [pages, Hkv, 34 * D]")
+    pages, Hkv, D = cache.shape[0], cache.shape[1], cache.shape[2] // 34
+    if block_table is None:
+        _need(B > 0 and pages % B == 0, "without a block table the cache must hold the same number of pages per sequence")
+        return Hkv, D, pages // B, pages
+    _need(block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.shape[0] == B,
+          "block_table must be int32 [B, NB]")
+    return Hkv, D, block_table.shape[1], pages
+
+
+def qv_kv4_write(qkv, start, cache, T, Hq, Hkv, block_table=None, count=None, stream=None):
+    """Quantize the key and value heads of qkv [B*T, (Hq+2Hkv)*D] (fp32 or
+    bf16) into the cache: row j of sequence b at position start[b] + j, for
+    j < count[b] (all T rows when count is None)."""
+    B = start.shape[0]
+    hkv, D, NB, pages = _kv4_shapes(cache, block_table, B)
+    _need(hkv == Hkv, "cache must have Hkv heads")
+    _need(qkv.shape == (B * T, (Hq + 2 * Hkv) * D), "qkv must be [B*T, (Hq+2Hkv)*D]")
+    _need(start.shape == (B,) and start.dtype == torch.int32, "start int32 [B]")
+    if count is not None:
+        _need(count.shape == (B,) and count.dtype == torch.int32, "count int32 [B]")
+    _check(load().qv_kv4_write(_ptr(qkv), _dtype(qkv), _ptr(start), _ptr(count), _ptr(block_table), B, T, Hq, Hkv, D,
+                               NB, pages, _ptr(cache), ctypes.c_void_p(_stream(stream))))
+
+
+def qv_kv4_read(cache, start, k_out, v_out, block_table=None, count=None, stream=None):
+    """Cached positions as values: k_out, v_out [B, T, Hkv, D] (fp32 or bf16),
+    row j of sequence b from position start[b] + j, for j < count[b]; other
+    rows are left as they were."""
+    B, T, hkv, d = k_out.shape
+    Hkv, D, NB, pages = _kv4_shapes(cache, block_table, B)
+    _need((hkv, d) == (Hkv, D) and v_out.shape == k_out.shape and v_out.dtype == k_out.dtype,
+          "k_out, v_out must be [B, T, Hkv, D] of one dtype")
+    _need(start.shape == (B,) and start.dtype == torch.int32, "start int32 [B]")
+    if count is not None:
+        _need(count.shape == (B,) and count.dtype == torch.int32, "count int32 [B]")
+    _check(load().qv_kv4_read(_ptr(cache), _ptr(start), _ptr(count), _ptr(block_table), B, T, Hkv, D, NB, pages,
+                              _ptr(k_out), _ptr(v_out), _dtype(k_out), ctypes.c_void_p(_stream(stream))))
+
+
+def qv_attention_kv4_workspace_bytes(B, T, Hq, Hkv, D, NB) -> int:
+    return int(load().qv_attention_kv4_workspace_bytes(B, T, Hq, Hkv, D, NB))
+
+
+def qv_attention_verify_kv4(qkv, cache, cache_len, T, Hq, Hkv, scale, out, workspace, block_table=None, stream=None):
+    """Causal grouped-query attention of the verify tokens over the 4-bit cache
+    and the step's own keys: qkv [B*T, (Hq+2Hkv)*D] bf16, cache_len [B] int32
+    -> out [B*T, Hq*D] fp32 or bf16. The workspace's first 4096 bytes must be
+    zero before its first use (they are left zero)."""
+    B = cache_len.shape[0]
+    hkv, D, NB, pages = _kv4_shapes(cache, block_table, B)
+    _need(hkv == Hkv, "cache must have Hkv heads")
+    _need(qkv.dtype == torch.bfloat16 and qkv.shape == (B * T, (Hq + 2 * Hkv) * D), "qkv bf16 [B*T, (Hq+2Hkv)*D]")
+    _need(cache_len.shape == (B,) and cache_len.dtype == torch.int32, "cache_len int32 [B]")
+    _need(out.shape == (B * T, Hq * D), "out [B*T, Hq*D]")
+    _need(workspace.dtype == torch.uint8, "workspace must be a uint8 tensor")
+    _check(load().qv_attention_verify_kv4(_ptr(qkv), _ptr(cache) if NB > 0 and pages > 0 else None,
+                                          _ptr(block_table) if NB > 0 else None, _ptr(cache_len), B, T, Hq, Hkv, D,
+                                          NB, pages, ctypes.c_float(scale), _ptr(out), _dtype(out), _ptr(workspace),
+                                          workspace.numel(), ctypes.c_void_p(_stream(stream))))
+
+
+def qv_token_logprobs(logits, tokens, logprob, entropy=None, top_tokens=None, top_logprobs=None, stream=None):
+    """Per row of logits [M, V] (fp32 or bf16): logprob [M] of tokens [M]
+    int32, entropy [M] (optional), and the most probable tokens top_tokens
+    [M, K] int32 with top_logprobs [M, K] (optional, together)."""
+    M, V = logits.shape
+    _need(tokens.shape == (M,) and tokens.dtype == torch.int32, "tokens int32 [M]")
+    _need(logprob.shape == (M,) and logprob.dtype == torch.float32, "logprob float32 [M]")
+    if entropy is not None:
+        _need(entropy.shape == (M,) and entropy.dtype == torch.float32, "entropy float32 [M]")
+    _need((top_tokens is None) == (top_logprobs is None), "top_tokens and top_logprobs go together")
+    K = 0
+    if top_tokens is not None:
+        _need(top_tokens.dim() == 2 and top_tokens.shape[0] == M and top_tokens.dtype == torch.int32,
+              "top_tokens int32 [M, K]")
+        _need(top_logprobs.shape == top_tokens.shape and top_logprobs.dtype == torch.float32,
+              "top_logprobs float32 [M, K]")
+        K = top_tokens.shape[1]
+    _check(load().qv_token_logprobs(_ptr(logits), _dtype(logits), _ptr(tokens), M, V, K, _ptr(logprob), _ptr(entropy),
+                                    _ptr(top_tokens) if K else None, _ptr(top_logprobs) if K else None,
+                                    ctypes.c_void_p(_stream(stream))))
 
 
 # --- W4A8: packed int4 weights [N, K/2] uint8 (even k in the low nibble) ---
