@@ -29,10 +29,11 @@
 //     A thread's 4 * W code words are one 16-byte read (W = D / 32) and all
 //     belong to one scale group; which k index of the product each nibble
 //     takes is free, so the query fragments are permuted to match.
-//   P in base 2, kept unnormalised: p = 2^(7 + s - m). m follows the row's
-//     maximum lazily: it moves only when a score exceeds it by more than 8 (p
-//     is at most 2^15 then), so the usual unit needs no reduction across lanes
-//     and no rescaling. P is split into two f16 parts (an error of 2^-22 P, and
+//   P in base 2, kept unnormalised: p = 2^(7 + s - m). m is a whole number (so
+//     that every rescaling factor is an exact power of two) that follows the
+//     row's maximum lazily: it moves only when a score exceeds it by more than
+//     8 (p is below 2^15.6 then), so the usual step needs no reduction across
+//     lanes and no rescaling. P is split into two f16 parts (an error of 2^-22 P, and
 //     2^-32 of the largest P below f16's normal range) for fp32 outputs; for
 //     bf16 outputs one part is enough (2^-11 P, an eighth of the output's own
 //     rounding).
@@ -69,8 +70,9 @@ constexpr int kRowTile = 32;                    // query rows of a tile
 constexpr int kMinUnits = 8;                    // units of a CTA's range at least
 constexpr size_t kCounterBytes = 4096;         // at the workspace's start, whatever the shape
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr int kTileCost = 12;                   // units' worth of a tile's own costs
 constexpr float kLazy = 8.f;                    // log2 of the growth a running maximum may lag behind
-constexpr float kBias = 7.f;                    // log2 of p at the running maximum: 2^(kBias + kLazy) < 65504
+constexpr float kBias = 7.f;                    // log2 of p at the running maximum: 2^(kBias + kLazy + 0.5) < 65504
 
 struct Args {
     const uint16_t* qkv;       // [B*T][(Hq + 2 Hkv) D] bf16
@@ -94,6 +96,7 @@ struct Layout {
     static constexpr int KS = D / 16;                     // k steps of Q K^T = dim tiles of P V
     static constexpr bool TwoCtas = D / 64 * NR <= 2;     // two CTAs per SM (at most 128 registers a thread)
     static constexpr int Stages = TwoCtas ? 2 : 4;
+    static constexpr bool QRegs = D / 64 * NR <= 6;       // the query fragments stay in registers
     static constexpr int Ring = 0;
     static constexpr int Area = Ring + kWarps * Stages * Rec::Bytes;      // 4 warps' partial outputs
     static constexpr int AreaBytes = 4 * NR * 8 * D * 4;
@@ -221,7 +224,7 @@ __device__ __forceinline__ uint32_t lds_u32(uint32_t addr) {
     return v;
 }
 
-// The units of sequence b: cached records, then groups of 32 own rows.
+// The cached positions of sequence b.
 __device__ __forceinline__ int seq_len(const Args& a, int b) {
     const long long cap = (long long)a.NB * kKv4Block;
     const int n = a.len[b];
@@ -264,7 +267,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NR>::TwoCtas ? 2 : 1) attn
     const int seg = (a.B + kThreads - 1) / kThreads;             // sequences per thread
     long long mine = 0;
     for (int b = tid * seg; b < min(a.B, (tid + 1) * seg); ++b)
-        mine += (long long)((seq_len(a, b) + kKv4Block - 1) / kKv4Block + own_units) * tps;
+        mine += (long long)((seq_len(a, b) + kKv4Block - 1) / kKv4Block + own_units + kTileCost) * tps;
     long long incl = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
@@ -287,7 +290,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NR>::TwoCtas ? 2 : 1) attn
         long long at = before;
         int b = tid * seg;
         while (true) {
-            const long long n = (long long)((seq_len(a, b) + kKv4Block - 1) / kKv4Block + own_units) * tps;
+            const long long n = (long long)((seq_len(a, b) + kKv4Block - 1) / kKv4Block + own_units + kTileCost) * tps;
             if (u0 < at + n) break;
             at += n;
             ++b;
@@ -305,33 +308,45 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NR>::TwoCtas ? 2 : 1) attn
     while (u < u1) {
         // ---- the tile that unit u belongs to, and this CTA's part [ua, ub) of it
         const int L = seq_len(a, b);
-        const int nc = (L + kKv4Block - 1) / kKv4Block, nu = nc + own_units;
-        const int ti = (int)((u - seq_at) / nu);
-        const long long tile_at = seq_at + (long long)ti * nu;
+        const int nc = (L + kKv4Block - 1) / kKv4Block, nu = nc + own_units, place = nu + kTileCost;
+        const int ti = (int)((u - seq_at) / place);
+        const long long tile_at = seq_at + (long long)ti * place;
         const int kh = ti / a.RT, rt = ti - kh * a.RT;
         const int ua = (int)(u - tile_at), ub = (int)min((long long)nu, u1 - tile_at);
+        u = tile_at + place;                                     // where this CTA goes on
+        const int b0 = b;
+        if (ti == tps - 1) {
+            seq_at = u;
+            ++b;
+        }
+        if (ua >= nu) continue;                                  // (only empty places of the tile)
         const int r0 = rt * a.rows, R = min(a.rows, a.T * a.G - r0);   // query rows of this tile
 
-        auto issue = [&](int unit) {                             // lane 0: request a cached unit's record
-            const int s = issued % S;
-            const int page = kv4_page(a.table, b, a.NB, a.pages, unit);
-            valid[s] = page >= 0;
-            if (a.hold) return;
-            if (page < 0) {
-                mbar_arrive(&bars[s]);
-                return;
+        int next = ua + warp;                                    // next unit to request, and its page
+        const int last = min(ub, nc);
+        auto page_of = [&](int unit) { return unit < last ? kv4_page(a.table, b0, a.NB, a.pages, unit) : -1; };
+        int page = page_of(next);
+        auto issue = [&]() {                                     // request the next unit's record, if there is one
+            if (next >= last || dead) return;
+            if (lane == 0) {
+                const int s = issued % S;
+                valid[s] = page >= 0;
+                if (!a.hold) {
+                    if (page >= 0) {
+                        mbar_arrive_expect_tx(&bars[s], Rec::Bytes);
+                        bulk_load(ring + (uint32_t)(s * Rec::Bytes), a.cache + ((size_t)page * a.Hkv + kh) * Rec::Bytes,
+                                  Rec::Bytes, &bars[s]);
+                    } else {
+                        mbar_arrive(&bars[s]);
+                    }
+                }
             }
-            mbar_arrive_expect_tx(&bars[s], Rec::Bytes);
-            bulk_load(ring + (uint32_t)(s * Rec::Bytes), a.cache + ((size_t)page * a.Hkv + kh) * Rec::Bytes, Rec::Bytes,
-                      &bars[s]);
+            ++issued;
+            next += kWarps;
+            page = page_of(next);
         };
-        int next = ua + warp;                                    // next unit to request
-        for (int s = 0; s < S; ++s)
-            if (next < min(ub, nc) && !dead) {
-                if (lane == 0) issue(next);
-                ++issued;
-                next += kWarps;
-            }
+#pragma unroll 1
+        for (int s = 0; s < S; ++s) issue();
 
         // ---- the query fragments: word w of the row's 16-byte piece at dims
         // t4 * D/4 + 8 w holds the pairs (d, d + 4) of two k steps
@@ -342,7 +357,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NR>::TwoCtas ? 2 : 1) attn
             uint4 q = make_uint4(0u, 0u, 0u, 0u);
             if (r < R) {
                 const int j = (r0 + r) / a.G, h = kh * a.G + (r0 + r) - j * a.G;
-                q = *reinterpret_cast<const uint4*>(a.qkv + ((size_t)b * a.T + j) * rowlen + (size_t)h * D + (ln & 3) * (D / 4) + 8 * w);
+                q = *reinterpret_cast<const uint4*>(a.qkv + ((size_t)b0 * a.T + j) * rowlen + (size_t)h * D + (ln & 3) * (D / 4) + 8 * w);
             }
             uint2* dst = reinterpret_cast<uint2*>(smem + Ly::Q) + (nt * KS + 2 * w) * 32 + ln;
             dst[0] = make_uint2(__byte_perm(q.x, q.z, 0x5410), __byte_perm(q.x, q.z, 0x7632));
@@ -350,9 +365,19 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NR>::TwoCtas ? 2 : 1) attn
         }
         __syncthreads();
 
+        uint2 qf[Ly::QRegs ? NR : 1][Ly::QRegs ? KS : 1];
+        if constexpr (Ly::QRegs) {
+#pragma unroll
+            for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                for (int kk = 0; kk < KS; ++kk)
+                    lds_v2_u32(sbase + (uint32_t)(Ly::Q + ((nt * KS + kk) * 32 + lane) * 8), qf[nt][kk].x, qf[nt][kk].y);
+        }
         const float sl2 = a.scale * kLog2e;
         float o[KS][NR][4];                                      // O^T: dims x rows
-        float m_run[NR][2], l_run[NR][2];                        // rows 8 nt + 2 t4 + e
+        // rows 8 nt + 2 t4 + e: p = 2^(sl2 x + c) of the product x, c = kBias - m
+        // (+inf before the first key), limit: the product at which m moves
+        float c[NR][2], limit[NR][2], l_run[NR][2];
         int tok[NR][2];                                          // their token (own rows 0..tok are visible)
 #pragma unroll
         for (int nt = 0; nt < NR; ++nt) {
@@ -363,41 +388,42 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NR>::TwoCtas ? 2 : 1) attn
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = 8 * nt + 2 * t4 + e;
-                m_run[nt][e] = NEG_INF;
+                c[nt][e] = -NEG_INF;
+                limit[nt][e] = NEG_INF;
                 l_run[nt][e] = 0.f;
                 tok[nt][e] = r < R ? (r0 + r) / a.G : -1;
             }
         }
         const int key_g = g ^ ((g >> 1) & 1);                    // position in its 8 of S^T row g (see below)
 
-        // The scores of 32 positions (two halves of 16) into the running softmax:
-        // scores in, probabilities out.
-        auto softmax = [&](float (&acc)[2][NR][4]) {
+        // The products of 16 positions into the running softmax: products in,
+        // probabilities out.
+        auto softmax = [&](float (&acc)[NR][4]) {
             bool grow = false;
-            float mx[NR][2];
 #pragma unroll
             for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    mx[nt][e] = fmaxf(fmaxf(acc[0][nt][e], acc[0][nt][2 + e]), fmaxf(acc[1][nt][e], acc[1][nt][2 + e]));
-                    grow = grow || mx[nt][e] > m_run[nt][e] + kLazy;
-                }
+                for (int e = 0; e < 2; ++e) grow = grow || fmaxf(acc[nt][e], acc[nt][2 + e]) > limit[nt][e];
             if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
                 for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        float v = fmaxf(mx[nt][e], m_run[nt][e]);
+                        float v = fmaxf(acc[nt][e], acc[nt][2 + e]);
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-                        const float f = v == NEG_INF ? 1.f : ex2(m_run[nt][e] - v);
-                        m_run[nt][e] = v;
-                        l_run[nt][e] *= f;
+                        if (v > limit[nt][e]) {                  // (the same in the row's 8 lanes)
+                            const float m = rintf(v * sl2), cn = kBias - m;
+                            const float f = ex2(cn - c[nt][e]);  // 2^-inf = 0 on the first keys
+                            c[nt][e] = cn;
+                            limit[nt][e] = (m + kLazy) / sl2;
+                            l_run[nt][e] *= f;
 #pragma unroll
-                        for (int i = 0; i < KS; ++i) {
-                            o[i][nt][e] *= f;
-                            o[i][nt][2 + e] *= f;
+                            for (int i = 0; i < KS; ++i) {
+                                o[i][nt][e] *= f;
+                                o[i][nt][2 + e] *= f;
+                            }
                         }
                     }
             }
@@ -405,17 +431,11 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NR>::TwoCtas ? 2 : 1) attn
             for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float m = m_run[nt][e] == NEG_INF ? 0.f : m_run[nt][e] - kBias;   // no visible key yet: 2^-inf = 0
-                    float sum = 0.f;
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const float p = ex2(acc[h][nt][2 * k + e] - m);
-                            acc[h][nt][2 * k + e] = p;
-                            sum += p;
-                        }
-                    l_run[nt][e] += sum;
+                    const float cc = c[nt][e] == -NEG_INF ? 0.f : c[nt][e];   // no visible key yet: 2^-inf = 0
+                    const float p0 = ex2(acc[nt][e] * sl2 + cc), p1 = ex2(acc[nt][2 + e] * sl2 + cc);
+                    acc[nt][e] = p0;
+                    acc[nt][2 + e] = p1;
+                    l_run[nt][e] += p0 + p1;
                 }
         };
         // P^T of half h as the B operand (rows g; keys 2 t4, 2 t4 + 1 and + 8) in
@@ -466,166 +486,156 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NR>::TwoCtas ? 2 : 1) attn
         auto qk = [&](float (&acc)[NR][4], int kk, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
             for (int nt = 0; nt < NR; ++nt) {
-                uint32_t b0, b1;
-                lds_v2_u32(sbase + (uint32_t)(Ly::Q + ((nt * KS + kk) * 32 + lane) * 8), b0, b1);
-                mma_bf16_16816(acc[nt], a0, a1, a2, a3, b0, b1);
+                uint2 q;
+                if constexpr (Ly::QRegs) q = qf[nt][kk];
+                else lds_v2_u32(sbase + (uint32_t)(Ly::Q + ((nt * KS + kk) * 32 + lane) * 8), q.x, q.y);
+                mma_bf16_16816(acc[nt], a0, a1, a2, a3, q.x, q.y);
             }
         };
+        auto zero = [&](float (&acc)[NR][4]) {
+#pragma unroll
+            for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
+        };
 
-        // ---- the units of this warp
-        for (int un = ua + warp; un < ub && !dead; un += kWarps) {
-            float acc[2][NR][4];
+        // ---- the units of this warp, 16 positions at a time
+#pragma unroll 1
+        for (int un = ua + warp; un < last && !dead; un += kWarps) {
+            // a record. Row i of S^T (and k index i of P V) is position
+            // i ^ ((i >> 1) & 1) of its 8: neighbouring rows g of a 16-byte read,
+            // and the four t4 of an 8-byte one, then alternate between the two
+            // halves of the banks
+            const int s = used % S;
+            const bool ok = bar_wait(&bars[s], (used / S) & 1u, abort, a.wait_ns);
+            if (!__all_sync(0xffffffffu, ok)) {
+                atomicOr(&g_attn_kv4_error, kErrFullWait);
+                dead = true;
+                break;
+            }
+            const uint32_t rec = ring + (uint32_t)(s * Rec::Bytes);
+            const int left = valid[s] ? L - un * kKv4Block : 0;  // positions of the record that are cached
+#pragma unroll 1
+            for (int p0 = 0; p0 < kKv4Block && p0 < left; p0 += 16) {
+                float acc[NR][4];
+                zero(acc);
+                {
+                    uint32_t x[2][W];
+                    KeyScale sc[2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int nt = 0; nt < NR; ++nt)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) acc[h][nt][e] = 0.f;
-            if (un < nc) {
-                // a record. Row i of S^T (and k index i of P V) is position
-                // i ^ ((i >> 1) & 1) of its 8: neighbouring rows g of a 16-byte
-                // read, and the four t4 of an 8-byte one, then alternate between
-                // the two halves of the banks
-                const int s = used % S;
-                const unsigned ph = (used / S) & 1u;
-                const bool ok = bar_wait(&bars[s], ph, abort, a.wait_ns);
-                if (!__all_sync(0xffffffffu, ok)) {
-                    atomicOr(&g_attn_kv4_error, kErrFullWait);
-                    dead = true;
-                    break;
-                }
-                if (valid[s]) {
-                    const uint32_t rec = ring + (uint32_t)(s * Rec::Bytes);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t x[2][W];
-                        KeyScale sc[2];
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int key = 16 * h + 8 * k + key_g;
-                            const uint32_t at = rec + (uint32_t)(Rec::KC + key * Rec::RowBytes + t4 * (D / 8));
-                            if constexpr (W == 4) lds_v4_u32(at, x[k][0], x[k][1], x[k][2], x[k][3]);
-                            else lds_v2_u32(at, x[k][0], x[k][1]);
-                            const uint32_t sb = lds_u8(rec + (uint32_t)(Rec::KS + key * Rec::RowScales + (D == 128 ? t4 : t4 >> 1)));
-                            sc[k] = KeyScale(sb);
-                        }
-#pragma unroll
-                        for (int w = 0; w < W; ++w) {
-                            qk(acc[h], 2 * w, key_pair<0>(x[0][w], sc[0]), key_pair<0>(x[1][w], sc[1]),
-                               key_pair<1>(x[0][w], sc[0]), key_pair<1>(x[1][w], sc[1]));
-                            qk(acc[h], 2 * w + 1, key_pair<2>(x[0][w], sc[0]), key_pair<2>(x[1][w], sc[1]),
-                               key_pair<3>(x[0][w], sc[0]), key_pair<3>(x[1][w], sc[1]));
-                        }
+                    for (int k = 0; k < 2; ++k) {
+                        const int key = p0 + 8 * k + key_g;
+                        const uint32_t at = rec + (uint32_t)(Rec::KC + key * Rec::RowBytes + t4 * (D / 8));
+                        if constexpr (W == 4) lds_v4_u32(at, x[k][0], x[k][1], x[k][2], x[k][3]);
+                        else lds_v2_u32(at, x[k][0], x[k][1]);
+                        sc[k] = KeyScale(lds_u8(rec + (uint32_t)(Rec::KS + key * Rec::RowScales + (D == 128 ? t4 : t4 >> 1))));
                     }
-                    const int left = L - un * kKv4Block;         // positions of the record that are cached
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int nt = 0; nt < NR; ++nt)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                acc[h][nt][e] *= sl2;
-                                if (left < kKv4Block && 16 * h + 8 * (e >> 1) + key_g >= left) acc[h][nt][e] = NEG_INF;
-                            }
-                    softmax(acc);
-#pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        uint32_t f[Parts][NR][2];
-                        p_frag(acc[h], f);
-                        uint32_t y[2][2][W / 2];                 // [k index + 8][even, odd key][word]
-                        ValScale sc[2];
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            uint32_t sb[2];
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int key = 16 * h + 8 * k + 2 * t4 + (e ^ (t4 & 1));
-                                const uint32_t at = rec + (uint32_t)(Rec::VC + key * Rec::RowBytes + g * (D / 16));
-                                if constexpr (W == 4) lds_v2_u32(at, y[k][e][0], y[k][e][1]);
-                                else y[k][e][0] = lds_u32(at);
-                                sb[e] = lds_u8(rec + (uint32_t)(Rec::VS + key * Rec::RowScales + (D == 128 ? g >> 1 : g >> 2)));
-                            }
-                            sc[k] = ValScale(sb[0], sb[1]);
-                        }
-#pragma unroll
-                        for (int w = 0; w < W / 2; ++w) {
-                            const uint32_t a0 = __byte_perm(y[0][0][w], y[0][1][w], 0x5410), a1 = __byte_perm(y[0][0][w], y[0][1][w], 0x7632);
-                            const uint32_t a2 = __byte_perm(y[1][0][w], y[1][1][w], 0x5410), a3 = __byte_perm(y[1][0][w], y[1][1][w], 0x7632);
-                            pv(4 * w, val_pair<0>(a0, sc[0]), val_pair<0>(a1, sc[0]), val_pair<0>(a2, sc[1]), val_pair<0>(a3, sc[1]), f);
-                            pv(4 * w + 1, val_pair<1>(a0, sc[0]), val_pair<1>(a1, sc[0]), val_pair<1>(a2, sc[1]), val_pair<1>(a3, sc[1]), f);
-                            pv(4 * w + 2, val_pair<2>(a0, sc[0]), val_pair<2>(a1, sc[0]), val_pair<2>(a2, sc[1]), val_pair<2>(a3, sc[1]), f);
-                            pv(4 * w + 3, val_pair<3>(a0, sc[0]), val_pair<3>(a1, sc[0]), val_pair<3>(a2, sc[1]), val_pair<3>(a3, sc[1]), f);
-                        }
-                    }
-                }
-                ++used;
-                __syncwarp();                                    // every lane has read the stage
-                if (next < min(ub, nc)) {
-                    if (lane == 0) issue(next);
-                    ++issued;
-                    next += kWarps;
-                }
-            } else {
-                // 32 of the step's own rows, straight from the qkv rows (bf16)
-                const int j0 = (un - nc) * 32;
-                const uint16_t* base = a.qkv + (size_t)b * a.T * rowlen + (size_t)(a.Hq + kh) * D;
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
 #pragma unroll
                     for (int w = 0; w < W; ++w) {
-                        uint4 x[2];
-#pragma unroll
-                        for (int k = 0; k < 2; ++k) {
-                            const int j = j0 + 16 * h + 8 * k + key_g;
-                            x[k] = make_uint4(0u, 0u, 0u, 0u);
-                            if (j < a.T) x[k] = *reinterpret_cast<const uint4*>(base + (size_t)j * rowlen + t4 * (D / 4) + 8 * w);
-                        }
-                        qk(acc[h], 2 * w, __byte_perm(x[0].x, x[0].z, 0x5410), __byte_perm(x[1].x, x[1].z, 0x5410),
-                           __byte_perm(x[0].x, x[0].z, 0x7632), __byte_perm(x[1].x, x[1].z, 0x7632));
-                        qk(acc[h], 2 * w + 1, __byte_perm(x[0].y, x[0].w, 0x5410), __byte_perm(x[1].y, x[1].w, 0x5410),
-                           __byte_perm(x[0].y, x[0].w, 0x7632), __byte_perm(x[1].y, x[1].w, 0x7632));
+                        qk(acc, 2 * w, key_pair<0>(x[0][w], sc[0]), key_pair<0>(x[1][w], sc[1]),
+                           key_pair<1>(x[0][w], sc[0]), key_pair<1>(x[1][w], sc[1]));
+                        qk(acc, 2 * w + 1, key_pair<2>(x[0][w], sc[0]), key_pair<2>(x[1][w], sc[1]),
+                           key_pair<3>(x[0][w], sc[0]), key_pair<3>(x[1][w], sc[1]));
                     }
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
+                }
+                if (p0 + 16 > left) {
 #pragma unroll
                     for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
                         for (int e = 0; e < 4; ++e)
-                            acc[h][nt][e] = j0 + 16 * h + 8 * (e >> 1) + key_g <= tok[nt][e & 1] ? acc[h][nt][e] * sl2 : NEG_INF;
+                            if (p0 + 8 * (e >> 1) + key_g >= left) acc[nt][e] = NEG_INF;
+                }
                 softmax(acc);
-                bool bad = false;
+                uint32_t f[Parts][NR][2];
+                p_frag(acc, f);
+                uint32_t y[2][2][W / 2];                         // [k index + 8][even, odd key][word]
+                ValScale sc[2];
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t f[OwnParts][NR][2];
-                    own_p_frag(acc[h], f);
+                for (int k = 0; k < 2; ++k) {
+                    uint32_t sb[2];
 #pragma unroll
-                    for (int w = 0; w < W / 2; ++w) {
-                        uint32_t y[2][2][4];
+                    for (int e = 0; e < 2; ++e) {
+                        const int key = p0 + 8 * k + 2 * t4 + (e ^ (t4 & 1));
+                        const uint32_t at = rec + (uint32_t)(Rec::VC + key * Rec::RowBytes + g * (D / 16));
+                        if constexpr (W == 4) lds_v2_u32(at, y[k][e][0], y[k][e][1]);
+                        else y[k][e][0] = lds_u32(at);
+                        sb[e] = lds_u8(rec + (uint32_t)(Rec::VS + key * Rec::RowScales + (D == 128 ? g >> 1 : g >> 2)));
+                    }
+                    sc[k] = ValScale(sb[0], sb[1]);
+                }
 #pragma unroll
-                        for (int k = 0; k < 2; ++k)
+                for (int w = 0; w < W / 2; ++w) {
+                    const uint32_t a0 = __byte_perm(y[0][0][w], y[0][1][w], 0x5410), a1 = __byte_perm(y[0][0][w], y[0][1][w], 0x7632);
+                    const uint32_t a2 = __byte_perm(y[1][0][w], y[1][1][w], 0x5410), a3 = __byte_perm(y[1][0][w], y[1][1][w], 0x7632);
+                    pv(4 * w, val_pair<0>(a0, sc[0]), val_pair<0>(a1, sc[0]), val_pair<0>(a2, sc[1]), val_pair<0>(a3, sc[1]), f);
+                    pv(4 * w + 1, val_pair<1>(a0, sc[0]), val_pair<1>(a1, sc[0]), val_pair<1>(a2, sc[1]), val_pair<1>(a3, sc[1]), f);
+                    pv(4 * w + 2, val_pair<2>(a0, sc[0]), val_pair<2>(a1, sc[0]), val_pair<2>(a2, sc[1]), val_pair<2>(a3, sc[1]), f);
+                    pv(4 * w + 3, val_pair<3>(a0, sc[0]), val_pair<3>(a1, sc[0]), val_pair<3>(a2, sc[1]), val_pair<3>(a3, sc[1]), f);
+                }
+            }
+            ++used;
+            __syncwarp();                                        // every lane has read the stage
+            issue();
+        }
+        // the step's own rows, straight from the qkv rows (bf16): unit nc + i
+        // (the warp that comes next in the units' order) holds rows 32 i .. 32 i + 31
+#pragma unroll 1
+        for (int un = max(ua, nc) + ((warp - (max(ua, nc) - ua)) & (kWarps - 1)); un < ub && !dead; un += kWarps) {
+            const uint16_t* base = a.qkv + (size_t)b0 * a.T * rowlen + (size_t)(a.Hq + kh) * D;
+            bool bad = false;
+#pragma unroll 1
+            for (int j0 = (un - nc) * 32; j0 < min(a.T, (un - nc) * 32 + 32); j0 += 16) {
+                float acc[NR][4];
+                zero(acc);
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int j = j0 + 16 * h + 8 * k + 2 * t4 + (e ^ (t4 & 1));
-                                uint4 v = make_uint4(0u, 0u, 0u, 0u);
-                                if (j < a.T) v = *reinterpret_cast<const uint4*>(base + (size_t)j * rowlen + (size_t)a.Hkv * D + g * (D / 8) + 8 * w);
-                                y[k][e][0] = v.x; y[k][e][1] = v.y; y[k][e][2] = v.z; y[k][e][3] = v.w;
+                for (int w = 0; w < W; ++w) {
+                    uint4 x[2];
 #pragma unroll
-                                for (int i = 0; i < 4; ++i) {    // infinities and NaN: 0 here, added below
-                                    if ((y[k][e][i] & 0x7F80u) == 0x7F80u) { y[k][e][i] &= 0xFFFF0000u; bad = true; }
-                                    if ((y[k][e][i] & 0x7F800000u) == 0x7F800000u) { y[k][e][i] &= 0xFFFFu; bad = true; }
-                                }
+                    for (int k = 0; k < 2; ++k) {
+                        const int j = j0 + 8 * k + key_g;
+                        x[k] = make_uint4(0u, 0u, 0u, 0u);
+                        if (j < a.T) x[k] = *reinterpret_cast<const uint4*>(base + (size_t)j * rowlen + t4 * (D / 4) + 8 * w);
+                    }
+                    qk(acc, 2 * w, __byte_perm(x[0].x, x[0].z, 0x5410), __byte_perm(x[1].x, x[1].z, 0x5410),
+                       __byte_perm(x[0].x, x[0].z, 0x7632), __byte_perm(x[1].x, x[1].z, 0x7632));
+                    qk(acc, 2 * w + 1, __byte_perm(x[0].y, x[0].w, 0x5410), __byte_perm(x[1].y, x[1].w, 0x5410),
+                       __byte_perm(x[0].y, x[0].w, 0x7632), __byte_perm(x[1].y, x[1].w, 0x7632));
+                }
+#pragma unroll
+                for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (j0 + 8 * (e >> 1) + key_g > tok[nt][e & 1]) acc[nt][e] = NEG_INF;
+                softmax(acc);
+                uint32_t f[OwnParts][NR][2];
+                own_p_frag(acc, f);
+#pragma unroll
+                for (int w = 0; w < W / 2; ++w) {
+                    uint32_t y[2][2][4];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int j = j0 + 8 * k + 2 * t4 + (e ^ (t4 & 1));
+                            uint4 v = make_uint4(0u, 0u, 0u, 0u);
+                            if (j < a.T) v = *reinterpret_cast<const uint4*>(base + (size_t)j * rowlen + (size_t)a.Hkv * D + g * (D / 8) + 8 * w);
+                            y[k][e][0] = v.x; y[k][e][1] = v.y; y[k][e][2] = v.z; y[k][e][3] = v.w;
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {        // infinities and NaN: 0 here, added below
+                                if ((y[k][e][i] & 0x7F80u) == 0x7F80u) { y[k][e][i] &= 0xFFFF0000u; bad = true; }
+                                if ((y[k][e][i] & 0x7F800000u) == 0x7F800000u) { y[k][e][i] &= 0xFFFFu; bad = true; }
                             }
-                        // tile 4 w + j: rows g are dims 8 w + j, rows g + 8 dims 8 w + 4 + j
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const int sel = j & 1 ? 0x7632 : 0x5410, i0 = j >> 1;
-                            own_pv(4 * w + j, __byte_perm(y[0][0][i0], y[0][1][i0], sel), __byte_perm(y[0][0][2 + i0], y[0][1][2 + i0], sel),
-                               __byte_perm(y[1][0][i0], y[1][1][i0], sel), __byte_perm(y[1][0][2 + i0], y[1][1][2 + i0], sel), f);
                         }
+                    // tile 4 w + j: rows g are dims 8 w + j, rows g + 8 dims 8 w + 4 + j
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int sel = j & 1 ? 0x7632 : 0x5410, i0 = j >> 1;
+                        own_pv(4 * w + j, __byte_perm(y[0][0][i0], y[0][1][i0], sel), __byte_perm(y[0][0][2 + i0], y[0][1][2 + i0], sel),
+                               __byte_perm(y[1][0][i0], y[1][1][i0], sel), __byte_perm(y[1][0][2 + i0], y[1][1][2 + i0], sel), f);
                     }
                 }
-                if (bad) s_flag[0] = 1;
             }
+            if (bad) s_flag[0] = 1;
         }
 
         // ---- the 8 warps' results into the CTA's: rows' maxima and sums, then
@@ -639,7 +649,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NR>::TwoCtas ? 2 : 1) attn
                 l += __shfl_xor_sync(0xffffffffu, l, 8);
                 l += __shfl_xor_sync(0xffffffffu, l, 16);
                 if (g == 0) {
-                    s_wm[warp * RW + 8 * nt + 2 * t4 + e] = m_run[nt][e];
+                    s_wm[warp * RW + 8 * nt + 2 * t4 + e] = kBias - c[nt][e];
                     s_wl[warp * RW + 8 * nt + 2 * t4 + e] = l;
                 }
             }
@@ -652,7 +662,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NR>::TwoCtas ? 2 : 1) attn
                 float M = s_wm[r];
 #pragma unroll
                 for (int w = 1; w < kWarps; ++w) M = fmaxf(M, s_wm[w * RW + r]);
-                const float f = m_run[nt][e] == NEG_INF ? 0.f : ex2(m_run[nt][e] - M);
+                const float f = c[nt][e] == -NEG_INF ? 0.f : ex2(kBias - c[nt][e] - M);
 #pragma unroll
                 for (int i = 0; i < KS; ++i) {
                     o[i][nt][e] *= f;
@@ -710,7 +720,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NR>::TwoCtas ? 2 : 1) attn
             if (s_flag[0] && r < R) {                            // rare: own value rows that are not finite
                 const int tk = (r0 + r) / a.G;
                 const int jb = max(0, (ua - nc) * 32), je = min(tk + 1, (ub - nc) * 32);
-                const uint16_t* vb = a.qkv + (size_t)b * a.T * rowlen + (size_t)(a.Hq + a.Hkv + kh) * D + d0;
+                const uint16_t* vb = a.qkv + (size_t)b0 * a.T * rowlen + (size_t)(a.Hq + a.Hkv + kh) * D + d0;
                 for (int j = jb; j < je; ++j)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
@@ -722,7 +732,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NR>::TwoCtas ? 2 : 1) attn
         auto store = [&](int r, int d0, const float (&v)[8], float l) {
             if (r >= R) return;
             const int j = (r0 + r) / a.G, h = kh * a.G + (r0 + r) - j * a.G;
-            const size_t at = ((size_t)b * a.T + j) * (size_t)a.Hq * D + (size_t)h * D + d0;
+            const size_t at = ((size_t)b0 * a.T + j) * (size_t)a.Hq * D + (size_t)h * D + d0;
             const float inv = 64.f / l;                          // (the values were taken times 2^-6)
             if (OUTBF) {
                 uint4 y;
@@ -802,11 +812,6 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NR>::TwoCtas ? 2 : 1) attn
         }
         __syncthreads();                                         // the area, Q and the flags are free again
         if (tid == 0) s_flag[0] = 0;
-        u = tile_at + ub;
-        if (u == seq_at + (long long)tps * nu) {                 // the next sequence
-            seq_at = u;
-            ++b;
-        }
     }
     // after a wait that ran out: no copy may be in flight when the CTA ends
     if (dead && !a.hold) {
@@ -849,7 +854,7 @@ Plan plan(int B, int T, int Hq, int Hkv, int D, int NB, int sms) {
     Plan p;
     row_tiles(T * (Hq / Hkv), p.RT, p.rows);
     p.NR = (p.rows + 7) / 8;
-    const long long most = (long long)B * Hkv * p.RT * ((long long)NB + (T + 31) / 32);   // units at most
+    const long long most = (long long)B * Hkv * p.RT * ((long long)NB + (T + 31) / 32 + kTileCost);   // places at most
     long long ctas = (long long)sms * (D / 64 * p.NR <= 2 ? 2 : 1);
     ctas = ctas < (long long)(kCounterBytes / 4) ? ctas : (long long)(kCounterBytes / 4);
     const long long want = (most + kMinUnits - 1) / kMinUnits;
