@@ -67,7 +67,7 @@ namespace {
 constexpr int kWarps = 8;
 constexpr int kThreads = kWarps * 32;
 constexpr int kRowTile = 32;                    // query rows of a tile
-constexpr int kMinUnits = 8;                    // units of a CTA's range at least
+constexpr int kMinUnits = 16;                   // places of a CTA's range at least: two units a warp
 constexpr size_t kCounterBytes = 4096;         // at the workspace's start, whatever the shape
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTileCost = 12;                   // units' worth of a tile's own costs
@@ -95,21 +95,26 @@ struct Layout {
     static constexpr int W = D / 32;                      // 32-bit code words of a thread per key row
     static constexpr int KS = D / 16;                     // k steps of Q K^T = dim tiles of P V
     static constexpr bool TwoCtas = D / 64 * NR <= 2;     // two CTAs per SM (at most 128 registers a thread)
-    static constexpr int Stages = TwoCtas ? 2 : 4;
-    static constexpr bool QRegs = D / 64 * NR <= 6;       // the query fragments stay in registers
+    static constexpr int Stages = D == 128 && TwoCtas ? 3 : 4;
+    // With one CTA (two warps a scheduler) the products of the next 16 positions
+    // are formed between those of P and V of the present ones.
+    static constexpr bool Pipe = !TwoCtas;
+    static constexpr bool QRegs = TwoCtas;                // the query fragments stay in registers
+    static constexpr int RW = NR * 8;
     static constexpr int Ring = 0;
-    static constexpr int Area = Ring + kWarps * Stages * Rec::Bytes;      // 4 warps' partial outputs
-    static constexpr int AreaBytes = 4 * NR * 8 * D * 4;
-    static constexpr int Q = Area + AreaBytes;            // query fragments [NR][KS][32] uint2
-    static constexpr int ML = Q + NR * KS * 32 * 8;       // m [8 warps][NR*8], l [8][NR*8]
-    static constexpr int MW = ML + 2 * kWarps * NR * 8 * 4;   // the tile's m, l [2][NR*8]
-    static constexpr int Bar = MW + 2 * NR * 8 * 4;
+    static constexpr int RingBytes = kWarps * Stages * Rec::Bytes;
+    static constexpr int AreaBytes = kWarps * RW * D * 4; // the warps' outputs [8][NR*4*KS][32], in the drained ring
+    static constexpr int Q = Ring + RingBytes;            // query fragments [NR][KS][32] uint2
+    static constexpr int ML = Q + NR * KS * 32 * 8;       // m [8 warps][RW], l [8][RW]
+    static constexpr int Bar = ML + 2 * kWarps * RW * 4;
     static constexpr int Valid = Bar + kWarps * Stages * 8;
-    static constexpr int Scan = Valid + kWarps * Stages * 4;  // long long [8] + found tile
-    static constexpr int Misc = Scan + 16 * 8;
+    static constexpr int Scan = Valid + kWarps * Stages * 4;  // unsigned [8], then the first sequence and its place
+    static constexpr int Misc = Scan + 16 * 4;
     static constexpr int Bytes = Misc + 64;
-    static constexpr int Slot = NR * 8 * D + 2 * NR * 8;  // floats of a partial result
-    static_assert(Area % 16 == 0 && Q % 16 == 0 && Bar % 8 == 0 && Scan % 8 == 0, "alignment");
+    static constexpr int Items = RW * D / 4;              // groups of 4 dims of one row
+    static constexpr int Slot = RW * D + 2 * RW;          // floats of a partial result: items, m, l
+    static_assert(AreaBytes <= RingBytes, "the warps' outputs fit the ring");
+    static_assert(Q % 16 == 0 && Bar % 8 == 0 && Scan % 4 == 0, "alignment");
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -139,6 +144,12 @@ __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t x) {
     return y;
 }
 
+// (a & b) ^ c
+__device__ __forceinline__ uint32_t and_xor(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t d;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6A;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
+    return d;
+}
 __device__ __forceinline__ uint32_t hfma2_f16(uint32_t a, uint32_t b, uint32_t c) {
     uint32_t d;
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(d) : "r"(a), "r"(b), "r"(c));
@@ -173,10 +184,12 @@ struct KeyScale {
 };
 // Nibbles J of the two 16-bit halves of x as bf16 values q * s: shifted to bits
 // 3..6 with the sign bit flipped, under 16.0 (0x4180), a nibble is 24 + q.
+// Left shifts are multiplications by a register (the FMA pipe has room, the
+// ALU, which does the masking and the right shifts, is the busiest pipe).
 template <int J>
-__device__ __forceinline__ uint32_t key_pair(uint32_t x, const KeyScale& sc) {
-    const uint32_t y = J == 0 ? x * 8u : x >> (J == 0 ? 0 : 4 * J - 3);
-    return hfma2_bf16((y & 0x00780078u) ^ 0x41C041C0u, sc.s, sc.off);
+__device__ __forceinline__ uint32_t key_pair(uint32_t x, const KeyScale& sc, uint32_t eight) {
+    const uint32_t y = J == 0 ? x * eight : x >> (J == 0 ? 0 : 4 * J - 3);
+    return hfma2_bf16(and_xor(y, 0x00780078u, 0x41C041C0u), sc.s, sc.off);
 }
 // The value scales of two positions times 2^-6 as an f16 pair, and -24 times them.
 struct ValScale {
@@ -189,10 +202,17 @@ struct ValScale {
 };
 // The same in f16: bits 6..9 under 16.0 (0x4C00).
 template <int J>
-__device__ __forceinline__ uint32_t val_pair(uint32_t x, const ValScale& sc) {
-    const uint32_t y = J == 0 ? x * 64u : (J == 1 ? x * 4u : x >> (J < 2 ? 0 : 4 * J - 6));
-    return hfma2_f16((y & 0x03C003C0u) ^ 0x4E004E00u, sc.s, sc.off);
+__device__ __forceinline__ uint32_t val_pair(uint32_t x, const ValScale& sc, uint32_t four, uint32_t sixty4) {
+    const uint32_t y = J == 0 ? x * sixty4 : (J == 1 ? x * four : x >> (J < 2 ? 0 : 4 * J - 6));
+    return hfma2_f16(and_xor(y, 0x03C003C0u, 0x4E004E00u), sc.s, sc.off);
 }
+
+// A thread's code words and scales of two key rows.
+template <int W>
+struct Keys {
+    uint32_t x[2][W];
+    KeyScale sc[2];
+};
 
 __device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, unsigned bytes, uint64_t* bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];"
@@ -235,20 +255,18 @@ template <int D, int NR, bool OUTBF>
 __global__ void __launch_bounds__(kThreads, Layout<D, NR>::TwoCtas ? 2 : 1) attn_kv4_kernel(const Args a) {
     using Ly = Layout<D, NR>;
     using Rec = Kv4Rec<D>;
-    constexpr int W = Ly::W, KS = Ly::KS, S = Ly::Stages, RW = NR * 8;
+    constexpr int W = Ly::W, KS = Ly::KS, S = Ly::Stages, RW = Ly::RW;
     extern __shared__ __align__(128) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
     uint64_t* bars = reinterpret_cast<uint64_t*>(smem + Ly::Bar) + warp * S;
     volatile int* valid = reinterpret_cast<volatile int*>(smem + Ly::Valid) + warp * S;
-    float* s_area = reinterpret_cast<float*>(smem + Ly::Area);
+    float* s_area = reinterpret_cast<float*>(smem + Ly::Ring);
     float* s_wm = reinterpret_cast<float*>(smem + Ly::ML);
     float* s_wl = s_wm + kWarps * RW;
-    float* s_m = reinterpret_cast<float*>(smem + Ly::MW);
-    float* s_l = s_m + RW;
-    long long* s_scan = reinterpret_cast<long long*>(smem + Ly::Scan);
+    unsigned* s_scan = reinterpret_cast<unsigned*>(smem + Ly::Scan);
     volatile int* abort = reinterpret_cast<volatile int*>(smem + Ly::Misc);
-    int* s_flag = reinterpret_cast<int*>(smem + Ly::Misc) + 1;       // [1] bad value row, [2] last arrival
+    int* s_flag = reinterpret_cast<int*>(smem + Ly::Misc) + 1;       // [0] bad value row, [1] last arrival
     const float NEG_INF = -__uint_as_float(0x7F800000u);
     const uint32_t ring = sbase + (uint32_t)(Ly::Ring + warp * S * Rec::Bytes);
 
@@ -262,77 +280,87 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NR>::TwoCtas ? 2 : 1) attn
     allow_dependent_launch();
     grid_dependency_wait();
 
-    // ---- this CTA's range [u0, u1) of the line of units, and the sequence it begins in
+    // ---- this CTA's range [u0, u1) of the line of units, and the sequence it
+    // begins in (the line has less than 2^31 places)
     const int own_units = (a.T + 31) / 32, tps = a.Hkv * a.RT;   // own units of a tile, tiles of a sequence
     const int seg = (a.B + kThreads - 1) / kThreads;             // sequences per thread
-    long long mine = 0;
+    unsigned mine = 0;
     for (int b = tid * seg; b < min(a.B, (tid + 1) * seg); ++b)
-        mine += (long long)((seq_len(a, b) + kKv4Block - 1) / kKv4Block + own_units + kTileCost) * tps;
-    long long incl = mine;
+        mine += (unsigned)(((seq_len(a, b) + kKv4Block - 1) / kKv4Block + own_units + kTileCost) * tps);
+    unsigned incl = mine;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-        const long long v = __shfl_up_sync(0xffffffffu, incl, off);
+        const unsigned v = __shfl_up_sync(0xffffffffu, incl, off);
         if (lane >= off) incl += v;
     }
     if (lane == 31) s_scan[warp] = incl;
     __syncthreads();
-    long long before = incl - mine, total = 0;
+    unsigned before = incl - mine, total = 0;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
         if (w < warp) before += s_scan[w];
         total += s_scan[w];
     }
-    long long per = (total + gridDim.x - 1) / gridDim.x;
-    per = per < kMinUnits ? kMinUnits : per;
-    const long long u0 = per * blockIdx.x, u1 = min(total, u0 + per);
+    const unsigned per = max((total + gridDim.x - 1) / gridDim.x, (unsigned)kMinUnits);
+    const unsigned u0 = per * blockIdx.x, u1 = min(total, u0 + per);
     if (u0 >= u1) return;                                        // (the whole CTA)
     if (u0 >= before && u0 < before + mine) {                    // exactly one thread
-        long long at = before;
+        unsigned at = before;
         int b = tid * seg;
         while (true) {
-            const long long n = (long long)((seq_len(a, b) + kKv4Block - 1) / kKv4Block + own_units + kTileCost) * tps;
+            const unsigned n = (unsigned)(((seq_len(a, b) + kKv4Block - 1) / kKv4Block + own_units + kTileCost) * tps);
             if (u0 < at + n) break;
             at += n;
             ++b;
         }
         s_scan[8] = at;
-        s_scan[9] = b;
+        s_scan[9] = (unsigned)b;
     }
     __syncthreads();
-    long long seq_at = s_scan[8];                                // where sequence b's units begin
-    int b = (int)s_scan[9];
-    long long u = u0;
+    unsigned seq_at = s_scan[8];                                 // where the sequence's places begin
+    int b_next = (int)s_scan[9];
+    unsigned u = u0;
     unsigned issued = 0, used = 0;                               // this warp's records so far
     bool dead = false;                                           // a wait of this warp ran out: it takes no more units
+    const size_t rowlen = (size_t)(a.Hq + 2 * a.Hkv) * D;
+    const float sl2 = a.scale * kLog2e;
+    const int key_g = g ^ ((g >> 1) & 1);                        // position in its 8 of S^T row g (see below)
+    uint32_t c4 = 4u, c8 = 8u, c64 = 64u;                        // multipliers the compiler may not turn into shifts
+    asm volatile("" : "+r"(c4), "+r"(c8), "+r"(c64));
 
     while (u < u1) {
-        // ---- the tile that unit u belongs to, and this CTA's part [ua, ub) of it
+        // ---- the tile that place u belongs to, and this CTA's part [ua, ub) of it
+        const int b = b_next;
         const int L = seq_len(a, b);
-        const int nc = (L + kKv4Block - 1) / kKv4Block, nu = nc + own_units, place = nu + kTileCost;
-        const int ti = (int)((u - seq_at) / place);
-        const long long tile_at = seq_at + (long long)ti * place;
+        const int nc = (L + kKv4Block - 1) / kKv4Block, nu = nc + own_units;
+        const unsigned places = (unsigned)(nu + kTileCost);
+        const int ti = (int)((u - seq_at) / places);
+        const unsigned tile_at = seq_at + (unsigned)ti * places;
         const int kh = ti / a.RT, rt = ti - kh * a.RT;
-        const int ua = (int)(u - tile_at), ub = (int)min((long long)nu, u1 - tile_at);
-        u = tile_at + place;                                     // where this CTA goes on
-        const int b0 = b;
+        const int ua = (int)(u - tile_at), ub = (int)min((unsigned)nu, u1 - tile_at);
+        u = tile_at + places;                                    // where this CTA goes on
         if (ti == tps - 1) {
             seq_at = u;
-            ++b;
+            ++b_next;
         }
         if (ua >= nu) continue;                                  // (only empty places of the tile)
         const int r0 = rt * a.rows, R = min(a.rows, a.T * a.G - r0);   // query rows of this tile
 
         int next = ua + warp;                                    // next unit to request, and its page
         const int last = min(ub, nc);
-        auto page_of = [&](int unit) { return unit < last ? kv4_page(a.table, b0, a.NB, a.pages, unit) : -1; };
+        // (the table's entry is looked at only when it is used, a unit later)
+        auto page_of = [&](int unit) {
+            return unit >= last ? -1 : (a.table ? a.table[(size_t)b * a.NB + unit] : b * a.NB + unit);
+        };
         int page = page_of(next);
         auto issue = [&]() {                                     // request the next unit's record, if there is one
             if (next >= last || dead) return;
             if (lane == 0) {
                 const int s = issued % S;
-                valid[s] = page >= 0;
+                const bool there = (unsigned)page < (unsigned)a.pages;
+                valid[s] = there;
                 if (!a.hold) {
-                    if (page >= 0) {
+                    if (there) {
                         mbar_arrive_expect_tx(&bars[s], Rec::Bytes);
                         bulk_load(ring + (uint32_t)(s * Rec::Bytes), a.cache + ((size_t)page * a.Hkv + kh) * Rec::Bytes,
                                   Rec::Bytes, &bars[s]);
@@ -350,21 +378,19 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NR>::TwoCtas ? 2 : 1) attn
 
         // ---- the query fragments: word w of the row's 16-byte piece at dims
         // t4 * D/4 + 8 w holds the pairs (d, d + 4) of two k steps
-        const size_t rowlen = (size_t)(a.Hq + 2 * a.Hkv) * D;
         for (int e = tid; e < NR * W * 32; e += kThreads) {
             const int ln = e & 31, w = (e >> 5) % W, nt = (e >> 5) / W;
             const int r = 8 * nt + (ln >> 2);
             uint4 q = make_uint4(0u, 0u, 0u, 0u);
             if (r < R) {
                 const int j = (r0 + r) / a.G, h = kh * a.G + (r0 + r) - j * a.G;
-                q = *reinterpret_cast<const uint4*>(a.qkv + ((size_t)b0 * a.T + j) * rowlen + (size_t)h * D + (ln & 3) * (D / 4) + 8 * w);
+                q = *reinterpret_cast<const uint4*>(a.qkv + ((size_t)b * a.T + j) * rowlen + (size_t)h * D + (ln & 3) * (D / 4) + 8 * w);
             }
             uint2* dst = reinterpret_cast<uint2*>(smem + Ly::Q) + (nt * KS + 2 * w) * 32 + ln;
             dst[0] = make_uint2(__byte_perm(q.x, q.z, 0x5410), __byte_perm(q.x, q.z, 0x7632));
             dst[32] = make_uint2(__byte_perm(q.y, q.w, 0x5410), __byte_perm(q.y, q.w, 0x7632));
         }
         __syncthreads();
-
         uint2 qf[Ly::QRegs ? NR : 1][Ly::QRegs ? KS : 1];
         if constexpr (Ly::QRegs) {
 #pragma unroll
@@ -373,12 +399,10 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NR>::TwoCtas ? 2 : 1) attn
                 for (int kk = 0; kk < KS; ++kk)
                     lds_v2_u32(sbase + (uint32_t)(Ly::Q + ((nt * KS + kk) * 32 + lane) * 8), qf[nt][kk].x, qf[nt][kk].y);
         }
-        const float sl2 = a.scale * kLog2e;
         float o[KS][NR][4];                                      // O^T: dims x rows
-        // rows 8 nt + 2 t4 + e: p = 2^(sl2 x + c) of the product x, c = kBias - m
-        // (+inf before the first key), limit: the product at which m moves
+        // rows 8 nt + 2 t4 + e: p = 2^(sl2 x + c) of the product x, c = kBias - m;
+        // limit: the product at which m moves (-inf before the first key)
         float c[NR][2], limit[NR][2], l_run[NR][2];
-        int tok[NR][2];                                          // their token (own rows 0..tok are visible)
 #pragma unroll
         for (int nt = 0; nt < NR; ++nt) {
 #pragma unroll
@@ -387,14 +411,11 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NR>::TwoCtas ? 2 : 1) attn
                 for (int e = 0; e < 4; ++e) o[i][nt][e] = 0.f;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const int r = 8 * nt + 2 * t4 + e;
-                c[nt][e] = -NEG_INF;
+                c[nt][e] = 0.f;
                 limit[nt][e] = NEG_INF;
                 l_run[nt][e] = 0.f;
-                tok[nt][e] = r < R ? (r0 + r) / a.G : -1;
             }
         }
-        const int key_g = g ^ ((g >> 1) & 1);                    // position in its 8 of S^T row g (see below)
 
         // The products of 16 positions into the running softmax: products in,
         // probabilities out.
@@ -415,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NR>::TwoCtas ? 2 : 1) attn
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
                         if (v > limit[nt][e]) {                  // (the same in the row's 8 lanes)
                             const float m = rintf(v * sl2), cn = kBias - m;
-                            const float f = ex2(cn - c[nt][e]);  // 2^-inf = 0 on the first keys
+                            const float f = limit[nt][e] == NEG_INF ? 0.f : ex2(cn - c[nt][e]);
                             c[nt][e] = cn;
                             limit[nt][e] = (m + kLazy) / sl2;
                             l_run[nt][e] *= f;
@@ -431,16 +452,15 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NR>::TwoCtas ? 2 : 1) attn
             for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    const float cc = c[nt][e] == -NEG_INF ? 0.f : c[nt][e];   // no visible key yet: 2^-inf = 0
-                    const float p0 = ex2(acc[nt][e] * sl2 + cc), p1 = ex2(acc[nt][2 + e] * sl2 + cc);
+                    const float p0 = ex2(acc[nt][e] * sl2 + c[nt][e]), p1 = ex2(acc[nt][2 + e] * sl2 + c[nt][e]);
                     acc[nt][e] = p0;
                     acc[nt][2 + e] = p1;
                     l_run[nt][e] += p0 + p1;
                 }
         };
-        // P^T of half h as the B operand (rows g; keys 2 t4, 2 t4 + 1 and + 8) in
-        // parts of 16 bits: f16 ones for the cache's values, bf16 ones of p 2^-6
-        // for the step's own
+        // P^T of 16 positions as the B operand (rows g; keys 2 t4, 2 t4 + 1 and
+        // + 8) in parts of 16 bits: f16 ones for the cache's values, bf16 ones of
+        // p 2^-6 for the step's own
         constexpr int Parts = OUTBF ? 1 : 2, OwnParts = OUTBF ? 2 : 3;
         auto p_frag = [&](const float (&p)[NR][4], uint32_t (&f)[Parts][NR][2]) {
 #pragma unroll
@@ -472,16 +492,16 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NR>::TwoCtas ? 2 : 1) attn
         };
         auto pv = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, const uint32_t (&f)[Parts][NR][2]) {
 #pragma unroll
-            for (int nt = 0; nt < NR; ++nt)
+            for (int q = 0; q < Parts; ++q)
 #pragma unroll
-                for (int q = 0; q < Parts; ++q) mma_f16_16816(o[i][nt], a0, a1, a2, a3, f[q][nt][0], f[q][nt][1]);
+                for (int nt = 0; nt < NR; ++nt) mma_f16_16816(o[i][nt], a0, a1, a2, a3, f[q][nt][0], f[q][nt][1]);
         };
         auto own_pv = [&](int i, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                           const uint32_t (&f)[OwnParts][NR][2]) {
 #pragma unroll
-            for (int nt = 0; nt < NR; ++nt)
+            for (int q = 0; q < OwnParts; ++q)
 #pragma unroll
-                for (int q = 0; q < OwnParts; ++q) mma_bf16_16816(o[i][nt], a0, a1, a2, a3, f[q][nt][0], f[q][nt][1]);
+                for (int nt = 0; nt < NR; ++nt) mma_bf16_16816(o[i][nt], a0, a1, a2, a3, f[q][nt][0], f[q][nt][1]);
         };
         auto qk = [&](float (&acc)[NR][4], int kk, uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3) {
 #pragma unroll
@@ -499,89 +519,12 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NR>::TwoCtas ? 2 : 1) attn
                 for (int e = 0; e < 4; ++e) acc[nt][e] = 0.f;
         };
 
-        // ---- the units of this warp, 16 positions at a time
+        // ---- the step's own rows, straight from the qkv rows (bf16), while the
+        // first records are on their way: unit nc + i holds rows 32 i .. 32 i + 31
+        // and belongs to the warp that comes next in the units' order
 #pragma unroll 1
-        for (int un = ua + warp; un < last && !dead; un += kWarps) {
-            // a record. Row i of S^T (and k index i of P V) is position
-            // i ^ ((i >> 1) & 1) of its 8: neighbouring rows g of a 16-byte read,
-            // and the four t4 of an 8-byte one, then alternate between the two
-            // halves of the banks
-            const int s = used % S;
-            const bool ok = bar_wait(&bars[s], (used / S) & 1u, abort, a.wait_ns);
-            if (!__all_sync(0xffffffffu, ok)) {
-                atomicOr(&g_attn_kv4_error, kErrFullWait);
-                dead = true;
-                break;
-            }
-            const uint32_t rec = ring + (uint32_t)(s * Rec::Bytes);
-            const int left = valid[s] ? L - un * kKv4Block : 0;  // positions of the record that are cached
-#pragma unroll 1
-            for (int p0 = 0; p0 < kKv4Block && p0 < left; p0 += 16) {
-                float acc[NR][4];
-                zero(acc);
-                {
-                    uint32_t x[2][W];
-                    KeyScale sc[2];
-#pragma unroll
-                    for (int k = 0; k < 2; ++k) {
-                        const int key = p0 + 8 * k + key_g;
-                        const uint32_t at = rec + (uint32_t)(Rec::KC + key * Rec::RowBytes + t4 * (D / 8));
-                        if constexpr (W == 4) lds_v4_u32(at, x[k][0], x[k][1], x[k][2], x[k][3]);
-                        else lds_v2_u32(at, x[k][0], x[k][1]);
-                        sc[k] = KeyScale(lds_u8(rec + (uint32_t)(Rec::KS + key * Rec::RowScales + (D == 128 ? t4 : t4 >> 1))));
-                    }
-#pragma unroll
-                    for (int w = 0; w < W; ++w) {
-                        qk(acc, 2 * w, key_pair<0>(x[0][w], sc[0]), key_pair<0>(x[1][w], sc[1]),
-                           key_pair<1>(x[0][w], sc[0]), key_pair<1>(x[1][w], sc[1]));
-                        qk(acc, 2 * w + 1, key_pair<2>(x[0][w], sc[0]), key_pair<2>(x[1][w], sc[1]),
-                           key_pair<3>(x[0][w], sc[0]), key_pair<3>(x[1][w], sc[1]));
-                    }
-                }
-                if (p0 + 16 > left) {
-#pragma unroll
-                    for (int nt = 0; nt < NR; ++nt)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            if (p0 + 8 * (e >> 1) + key_g >= left) acc[nt][e] = NEG_INF;
-                }
-                softmax(acc);
-                uint32_t f[Parts][NR][2];
-                p_frag(acc, f);
-                uint32_t y[2][2][W / 2];                         // [k index + 8][even, odd key][word]
-                ValScale sc[2];
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    uint32_t sb[2];
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int key = p0 + 8 * k + 2 * t4 + (e ^ (t4 & 1));
-                        const uint32_t at = rec + (uint32_t)(Rec::VC + key * Rec::RowBytes + g * (D / 16));
-                        if constexpr (W == 4) lds_v2_u32(at, y[k][e][0], y[k][e][1]);
-                        else y[k][e][0] = lds_u32(at);
-                        sb[e] = lds_u8(rec + (uint32_t)(Rec::VS + key * Rec::RowScales + (D == 128 ? g >> 1 : g >> 2)));
-                    }
-                    sc[k] = ValScale(sb[0], sb[1]);
-                }
-#pragma unroll
-                for (int w = 0; w < W / 2; ++w) {
-                    const uint32_t a0 = __byte_perm(y[0][0][w], y[0][1][w], 0x5410), a1 = __byte_perm(y[0][0][w], y[0][1][w], 0x7632);
-                    const uint32_t a2 = __byte_perm(y[1][0][w], y[1][1][w], 0x5410), a3 = __byte_perm(y[1][0][w], y[1][1][w], 0x7632);
-                    pv(4 * w, val_pair<0>(a0, sc[0]), val_pair<0>(a1, sc[0]), val_pair<0>(a2, sc[1]), val_pair<0>(a3, sc[1]), f);
-                    pv(4 * w + 1, val_pair<1>(a0, sc[0]), val_pair<1>(a1, sc[0]), val_pair<1>(a2, sc[1]), val_pair<1>(a3, sc[1]), f);
-                    pv(4 * w + 2, val_pair<2>(a0, sc[0]), val_pair<2>(a1, sc[0]), val_pair<2>(a2, sc[1]), val_pair<2>(a3, sc[1]), f);
-                    pv(4 * w + 3, val_pair<3>(a0, sc[0]), val_pair<3>(a1, sc[0]), val_pair<3>(a2, sc[1]), val_pair<3>(a3, sc[1]), f);
-                }
-            }
-            ++used;
-            __syncwarp();                                        // every lane has read the stage
-            issue();
-        }
-        // the step's own rows, straight from the qkv rows (bf16): unit nc + i
-        // (the warp that comes next in the units' order) holds rows 32 i .. 32 i + 31
-#pragma unroll 1
-        for (int un = max(ua, nc) + ((warp - (max(ua, nc) - ua)) & (kWarps - 1)); un < ub && !dead; un += kWarps) {
-            const uint16_t* base = a.qkv + (size_t)b0 * a.T * rowlen + (size_t)(a.Hq + kh) * D;
+        for (int un = max(ua, nc) + ((warp - (max(ua, nc) - ua)) & (kWarps - 1)); un < ub; un += kWarps) {
+            const uint16_t* base = a.qkv + (size_t)b * a.T * rowlen + (size_t)(a.Hq + kh) * D;
             bool bad = false;
 #pragma unroll 1
             for (int j0 = (un - nc) * 32; j0 < min(a.T, (un - nc) * 32 + 32); j0 += 16) {
@@ -604,8 +547,11 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NR>::TwoCtas ? 2 : 1) attn
 #pragma unroll
                 for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        if (j0 + 8 * (e >> 1) + key_g > tok[nt][e & 1]) acc[nt][e] = NEG_INF;
+                    for (int e = 0; e < 2; ++e) {
+                        const int r = 8 * nt + 2 * t4 + e, tok = r < R ? (r0 + r) / a.G : -1;   // rows 0..tok are visible
+                        if (j0 + key_g > tok) acc[nt][e] = NEG_INF;
+                        if (j0 + 8 + key_g > tok) acc[nt][2 + e] = NEG_INF;
+                    }
                 softmax(acc);
                 uint32_t f[OwnParts][NR][2];
                 own_p_frag(acc, f);
@@ -638,8 +584,167 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NR>::TwoCtas ? 2 : 1) attn
             if (bad) s_flag[0] = 1;
         }
 
-        // ---- the 8 warps' results into the CTA's: rows' maxima and sums, then
-        // the outputs scaled to the common maximum, added in two rounds
+        // ---- the cached units of this warp, 16 positions at a time. Row i of S^T
+        // (and k index i of P V) is position i ^ ((i >> 1) & 1) of its 8:
+        // neighbouring rows g of a 16-byte read, and the four t4 of an 8-byte one,
+        // then alternate between the two halves of the banks
+        auto load_keys = [&](Keys<W>& k2, uint32_t rec, int p0) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const int key = p0 + 8 * k + key_g;
+                const uint32_t at = rec + (uint32_t)(Rec::KC + key * Rec::RowBytes + t4 * (D / 8));
+                if constexpr (W == 4) lds_v4_u32(at, k2.x[k][0], k2.x[k][1], k2.x[k][2], k2.x[k][3]);
+                else lds_v2_u32(at, k2.x[k][0], k2.x[k][1]);
+                k2.sc[k] = KeyScale(lds_u8(rec + (uint32_t)(Rec::KS + key * Rec::RowScales + (D == 128 ? t4 : t4 >> 1))));
+            }
+        };
+        auto qk_word = [&](float (&acc)[NR][4], const Keys<W>& k2, int w) {
+            qk(acc, 2 * w, key_pair<0>(k2.x[0][w], k2.sc[0], c8), key_pair<0>(k2.x[1][w], k2.sc[1], c8),
+               key_pair<1>(k2.x[0][w], k2.sc[0], c8), key_pair<1>(k2.x[1][w], k2.sc[1], c8));
+            qk(acc, 2 * w + 1, key_pair<2>(k2.x[0][w], k2.sc[0], c8), key_pair<2>(k2.x[1][w], k2.sc[1], c8),
+               key_pair<3>(k2.x[0][w], k2.sc[0], c8), key_pair<3>(k2.x[1][w], k2.sc[1], c8));
+        };
+        auto mask = [&](float (&acc)[NR][4], int p0, int left) {
+            if (p0 + 16 > left) {
+#pragma unroll
+                for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (p0 + 8 * (e >> 1) + key_g >= left) acc[nt][e] = NEG_INF;
+            }
+        };
+        // P V of 16 positions; with Pipe the following step's products are formed in
+        // between, two k steps after every second dim tile
+        auto values = [&](uint32_t rec, int p0, const uint32_t (&f)[Parts][NR][2], float (&nxt)[NR][4], const Keys<W>& k2) {
+            uint32_t y[2][2][W / 2];                             // [k index + 8][even, odd key][word]
+            ValScale sc[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t sb[2];
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int key = p0 + 8 * k + 2 * t4 + (e ^ (t4 & 1));
+                    const uint32_t at = rec + (uint32_t)(Rec::VC + key * Rec::RowBytes + g * (D / 16));
+                    if constexpr (W == 4) lds_v2_u32(at, y[k][e][0], y[k][e][1]);
+                    else y[k][e][0] = lds_u32(at);
+                    sb[e] = lds_u8(rec + (uint32_t)(Rec::VS + key * Rec::RowScales + (D == 128 ? g >> 1 : g >> 2)));
+                }
+                sc[k] = ValScale(sb[0], sb[1]);
+            }
+#pragma unroll
+            for (int w = 0; w < W / 2; ++w) {
+                const uint32_t a0 = __byte_perm(y[0][0][w], y[0][1][w], 0x5410), a1 = __byte_perm(y[0][0][w], y[0][1][w], 0x7632);
+                const uint32_t a2 = __byte_perm(y[1][0][w], y[1][1][w], 0x5410), a3 = __byte_perm(y[1][0][w], y[1][1][w], 0x7632);
+                pv(4 * w, val_pair<0>(a0, sc[0], c4, c64), val_pair<0>(a1, sc[0], c4, c64), val_pair<0>(a2, sc[1], c4, c64), val_pair<0>(a3, sc[1], c4, c64), f);
+                pv(4 * w + 1, val_pair<1>(a0, sc[0], c4, c64), val_pair<1>(a1, sc[0], c4, c64), val_pair<1>(a2, sc[1], c4, c64), val_pair<1>(a3, sc[1], c4, c64), f);
+                if (Ly::Pipe) qk_word(nxt, k2, 2 * w);
+                pv(4 * w + 2, val_pair<2>(a0, sc[0], c4, c64), val_pair<2>(a1, sc[0], c4, c64), val_pair<2>(a2, sc[1], c4, c64), val_pair<2>(a3, sc[1], c4, c64), f);
+                pv(4 * w + 3, val_pair<3>(a0, sc[0], c4, c64), val_pair<3>(a1, sc[0], c4, c64), val_pair<3>(a2, sc[1], c4, c64), val_pair<3>(a3, sc[1], c4, c64), f);
+                if (Ly::Pipe) qk_word(nxt, k2, 2 * w + 1);
+            }
+        };
+        // Waits for the record of unit `un`, the i-th this warp takes; its cached
+        // positions (0: no page), or -1 when the wait ran out.
+        auto take = [&](int un, unsigned i) {
+            const bool ok = bar_wait(&bars[i % S], (i / S) & 1u, abort, a.wait_ns);
+            if (!__all_sync(0xffffffffu, ok)) {
+                atomicOr(&g_attn_kv4_error, kErrFullWait);
+                dead = true;
+                return -1;
+            }
+            return valid[i % S] ? min(kKv4Block, L - un * kKv4Block) : 0;
+        };
+        auto done = [&]() {                                      // with the oldest record
+            ++used;
+            __syncwarp();                                        // every lane has read the stage
+            issue();
+        };
+        if constexpr (!Ly::Pipe) {
+#pragma unroll 1
+            for (int un = ua + warp; un < last && !dead; un += kWarps) {
+                const int left = take(un, used);
+                if (left < 0) break;
+                const uint32_t rec = ring + (uint32_t)((used % S) * Rec::Bytes);
+#pragma unroll 1
+                for (int p0 = 0; p0 < left; p0 += 16) {
+                    Keys<W> k2;
+                    load_keys(k2, rec, p0);
+                    float acc[NR][4];
+                    zero(acc);
+#pragma unroll
+                    for (int w = 0; w < W; ++w) qk_word(acc, k2, w);
+                    mask(acc, p0, left);
+                    softmax(acc);
+                    uint32_t f[Parts][NR][2];
+                    p_frag(acc, f);
+                    values(rec, p0, f, acc, k2);
+                }
+                done();
+            }
+        } else {
+            // acc: the products of the present step (record, p0); nxt: those of
+            // the following one, formed between the present one's tiles of P V
+            int un = ua + warp;
+            int left = 0;                                        // of the present record
+            while (un < last && !dead) {                         // the first record with a page
+                left = take(un, used);
+                if (left != 0) break;
+                done();
+                un += kWarps;
+            }
+            if (left > 0) {
+                uint32_t rec = ring + (uint32_t)((used % S) * Rec::Bytes);
+                int p0 = 0;
+                float acc[NR][4];
+                {
+                    Keys<W> k2;
+                    load_keys(k2, rec, 0);
+                    zero(acc);
+#pragma unroll
+                    for (int w = 0; w < W; ++w) qk_word(acc, k2, w);
+                }
+#pragma unroll 1
+                while (true) {
+                    // the following step: in this record, or in the next one
+                    const int left_now = left;
+                    const uint32_t rec_now = rec;
+                    const int p_now = p0;
+                    bool fresh = false, more = true;
+                    p0 += 16;
+                    if (p0 >= left) {
+                        fresh = true;
+                        p0 = 0;
+                        un += kWarps;
+                        if (un < last) {
+                            left = take(un, used + 1);
+                            if (left < 0) break;
+                            rec = ring + (uint32_t)(((used + 1) % S) * Rec::Bytes);
+                        } else {
+                            more = false;                        // (the last step's products are formed again, in vain)
+                            rec = rec_now;
+                        }
+                    }
+                    Keys<W> k2;
+                    load_keys(k2, rec, p0);
+                    mask(acc, p_now, left_now);
+                    softmax(acc);
+                    uint32_t f[Parts][NR][2];
+                    p_frag(acc, f);
+                    float nxt[NR][4];
+                    zero(nxt);
+                    values(rec_now, p_now, f, nxt, k2);
+#pragma unroll
+                    for (int nt = 0; nt < NR; ++nt)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) acc[nt][e] = nxt[nt][e];
+                    if (fresh) done();
+                    if (!more) break;
+                }
+            }
+        }
+
+        // ---- the warps' results side by side in shared memory (the ring has been
+        // read: every record requested has been waited for)
 #pragma unroll
         for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
@@ -649,168 +754,162 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NR>::TwoCtas ? 2 : 1) attn
                 l += __shfl_xor_sync(0xffffffffu, l, 8);
                 l += __shfl_xor_sync(0xffffffffu, l, 16);
                 if (g == 0) {
-                    s_wm[warp * RW + 8 * nt + 2 * t4 + e] = kBias - c[nt][e];
+                    s_wm[warp * RW + 8 * nt + 2 * t4 + e] = limit[nt][e] == NEG_INF ? NEG_INF : kBias - c[nt][e];
                     s_wl[warp * RW + 8 * nt + 2 * t4 + e] = l;
                 }
             }
         __syncthreads();
+        constexpr int Plane = NR * 4 * KS * 32;                  // [warp][(nt, c, tile)][lane]
 #pragma unroll
         for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const int r = 8 * nt + 2 * t4 + e;
-                float M = s_wm[r];
+            for (int q = 0; q < 4; ++q)
 #pragma unroll
-                for (int w = 1; w < kWarps; ++w) M = fmaxf(M, s_wm[w * RW + r]);
-                const float f = c[nt][e] == -NEG_INF ? 0.f : ex2(kBias - c[nt][e] - M);
-#pragma unroll
-                for (int i = 0; i < KS; ++i) {
-                    o[i][nt][e] *= f;
-                    o[i][nt][2 + e] *= f;
-                }
-            }
-        if (tid < RW) {
-            float M = s_wm[tid], l = 0.f;
-            for (int w = 1; w < kWarps; ++w) M = fmaxf(M, s_wm[w * RW + tid]);
-            for (int w = 0; w < kWarps; ++w)
-                l += s_wm[w * RW + tid] == NEG_INF ? 0.f : s_wl[w * RW + tid] * ex2(s_wm[w * RW + tid] - M);
-            s_m[tid] = M;
-            s_l[tid] = l;
-        }
-        // area[warp & 3][(nt, c, tile)][lane]
-        constexpr int Plane = NR * 4 * KS * 32;
-        if (warp >= 4) {
-#pragma unroll
-            for (int nt = 0; nt < NR; ++nt)
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int i = 0; i < KS; ++i) s_area[(warp - 4) * Plane + ((nt * 4 + c) * KS + i) * 32 + lane] = o[i][nt][c];
-        }
-        __syncthreads();
-        if (warp < 4) {
-#pragma unroll
-            for (int nt = 0; nt < NR; ++nt)
-#pragma unroll
-                for (int c = 0; c < 4; ++c)
-#pragma unroll
-                    for (int i = 0; i < KS; ++i) {
-                        float* p = s_area + warp * Plane + ((nt * 4 + c) * KS + i) * 32 + lane;
-                        *p += o[i][nt][c];
-                    }
-        }
+                for (int i = 0; i < KS; ++i) s_area[warp * Plane + ((nt * 4 + q) * KS + i) * 32 + lane] = o[i][nt][q];
         __syncthreads();
 
-        // ---- items of 8 dims of one row: (nt, e, word, lane); whole tiles go
-        // out, parts to the workspace
-        constexpr int Items = NR * 2 * (W / 2) * 32;
-        auto item_sum = [&](int it, int& r, int& d0, float (&v)[8]) {
-            const int ln = it & 31, w = (it >> 5) % (W / 2), ne = (it >> 5) / (W / 2), nt = ne >> 1, e = ne & 1;
-            r = 8 * nt + 2 * (ln & 3) + e;
-            d0 = (ln >> 2) * (D / 8) + 8 * w;
+        // ---- items of 4 dims of one row: (nt, e, word, half, lane); the warps'
+        // parts added at the row's common maximum. Whole tiles go out, parts of
+        // tiles to the workspace
+        auto item_at = [&](int it, int& r, int& d0) {
+            const int ln = it & 31, q = it >> 5, hf = q & 1, w = (q >> 1) % (W / 2), ne = (q >> 1) / (W / 2);
+            r = 8 * (ne >> 1) + 2 * (ln & 3) + (ne & 1);
+            d0 = (ln >> 2) * (D / 8) + 8 * w + 4 * hf;
+        };
+        auto item_sum = [&](int it, int r, int d0, float (&v)[4], float& M, float& l) {
+            const int ln = it & 31, q = it >> 5, hf = q & 1, w = (q >> 1) % (W / 2), ne = (q >> 1) / (W / 2);
+            M = s_wm[r];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
+            for (int x = 1; x < kWarps; ++x) M = fmaxf(M, s_wm[x * RW + r]);
+            l = 0.f;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float x = 0.f;
+            for (int j = 0; j < 4; ++j) v[j] = 0.f;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) x += s_area[q * Plane + ((nt * 4 + 2 * c + e) * KS + 4 * w + j) * 32 + ln];
-                    v[4 * c + j] = x;
-                }
+            for (int x = 0; x < kWarps; ++x) {
+                const float m = s_wm[x * RW + r];
+                const float f = m == NEG_INF ? 0.f : ex2(m - M);
+                l += f * s_wl[x * RW + r];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    v[j] += f * s_area[x * Plane + (((ne >> 1) * 4 + 2 * hf + (ne & 1)) * KS + 4 * w + j) * 32 + ln];
+            }
             if (s_flag[0] && r < R) {                            // rare: own value rows that are not finite
                 const int tk = (r0 + r) / a.G;
                 const int jb = max(0, (ua - nc) * 32), je = min(tk + 1, (ub - nc) * 32);
-                const uint16_t* vb = a.qkv + (size_t)b0 * a.T * rowlen + (size_t)(a.Hq + a.Hkv + kh) * D + d0;
+                const uint16_t* vb = a.qkv + (size_t)b * a.T * rowlen + (size_t)(a.Hq + a.Hkv + kh) * D + d0;
                 for (int j = jb; j < je; ++j)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
+                    for (int i = 0; i < 4; ++i) {
                         const uint32_t y = vb[(size_t)j * rowlen + i];
                         if ((y & 0x7F80u) == 0x7F80u) v[i] += __uint_as_float(y << 16);
                     }
             }
         };
-        auto store = [&](int r, int d0, const float (&v)[8], float l) {
+        auto store = [&](int r, int d0, const float (&v)[4], float l) {
             if (r >= R) return;
             const int j = (r0 + r) / a.G, h = kh * a.G + (r0 + r) - j * a.G;
-            const size_t at = ((size_t)b0 * a.T + j) * (size_t)a.Hq * D + (size_t)h * D + d0;
+            const size_t at = ((size_t)b * a.T + j) * (size_t)a.Hq * D + (size_t)h * D + d0;
             const float inv = 64.f / l;                          // (the values were taken times 2^-6)
-            if (OUTBF) {
-                uint4 y;
-                y.x = pack_bf16x2(v[0] * inv, v[1] * inv);
-                y.y = pack_bf16x2(v[2] * inv, v[3] * inv);
-                y.z = pack_bf16x2(v[4] * inv, v[5] * inv);
-                y.w = pack_bf16x2(v[6] * inv, v[7] * inv);
-                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + at) = y;
-            } else {
-                float4* p = reinterpret_cast<float4*>(static_cast<float*>(a.out) + at);
-                p[0] = make_float4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-                p[1] = make_float4(v[4] * inv, v[5] * inv, v[6] * inv, v[7] * inv);
-            }
+            if (OUTBF)
+                *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
+                    make_uint2(pack_bf16x2(v[0] * inv, v[1] * inv), pack_bf16x2(v[2] * inv, v[3] * inv));
+            else
+                *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) =
+                    make_float4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
         };
         if (ua == 0 && ub == nu) {
-            for (int it = tid; it < Items; it += kThreads) {
+            for (int it = tid; it < Ly::Items; it += kThreads) {
                 int r, d0;
-                float v[8];
-                item_sum(it, r, d0, v);
-                store(r, d0, v, s_l[r]);
+                float v[4], M, l;
+                item_at(it, r, d0);
+                item_sum(it, r, d0, v, M, l);
+                store(r, d0, v, l);
             }
         } else {
             float* slot = a.partials + ((size_t)blockIdx.x * 2 + (ua == 0 ? 1 : 0)) * Ly::Slot;
-            for (int it = tid; it < Items; it += kThreads) {
+            for (int it = tid; it < Ly::Items; it += kThreads) {
                 int r, d0;
-                float v[8];
-                item_sum(it, r, d0, v);
-                float4* p = reinterpret_cast<float4*>(slot + it * 8);
-                p[0] = make_float4(v[0], v[1], v[2], v[3]);
-                p[1] = make_float4(v[4], v[5], v[6], v[7]);
+                float v[4], M, l;
+                item_at(it, r, d0);
+                item_sum(it, r, d0, v, M, l);
+                *reinterpret_cast<float4*>(slot + it * 4) = make_float4(v[0], v[1], v[2], v[3]);
+                if (d0 == 0) {
+                    slot[RW * D + r] = M;
+                    slot[RW * D + RW + r] = l;
+                }
             }
-            if (tid < RW) {
-                slot[NR * 8 * D + tid] = s_m[tid];
-                slot[NR * 8 * D + RW + tid] = s_l[tid];
-            }
-            const int c0 = (int)(tile_at / per), c1 = (int)((tile_at + nu - 1) / per);   // the tile's CTAs
-            __threadfence();
-            __syncthreads();
+            const unsigned c0 = tile_at / per, c1 = (tile_at + (unsigned)nu - 1) / per;   // the tile's CTAs
+            __syncthreads();                                     // (the parts are written before thread 0's fence)
             if (tid == 0) {
+                __threadfence();
                 const unsigned before_me = atomicAdd(a.counters + c0, 1u);
-                s_flag[1] = before_me == (unsigned)(c1 - c0);
-                if (s_flag[1]) a.counters[c0] = 0;
+                s_flag[1] = before_me == c1 - c0;
+                if (s_flag[1]) {
+                    a.counters[c0] = 0;
+                    __threadfence();
+                }
             }
             __syncthreads();
             if (s_flag[1]) {
-                __threadfence();
-                const float* first = a.partials + ((size_t)c0 * 2 + 1) * Ly::Slot;
-                const size_t step = 2 * (size_t)Ly::Slot;        // contributors after the first: their slot 0
-                auto part = [&](int c) { return c == c0 ? first : a.partials + (size_t)c * step; };
-                if (tid < RW) {
-                    float M = NEG_INF, l = 0.f;
-                    for (int c = c0; c <= c1; ++c) M = fmaxf(M, __ldcg(part(c) + NR * 8 * D + tid));
-                    for (int c = c0; c <= c1; ++c) {
-                        const float m = __ldcg(part(c) + NR * 8 * D + tid);
-                        l += m == NEG_INF ? 0.f : ex2(m - M) * __ldcg(part(c) + NR * 8 * D + RW + tid);
-                    }
-                    s_m[tid] = M;
-                    s_l[tid] = l;
+                // the tile's parts, added in range order at a running maximum;
+                // kAhead of them are loaded at a time
+                constexpr int Own = (Ly::Items + kThreads - 1) / kThreads;    // items of a thread
+                constexpr int kAhead = Own >= 3 ? 2 : 4;
+                float v[Own][4], M[Own], l[Own];
+#pragma unroll
+                for (int k = 0; k < Own; ++k) {
+                    M[k] = NEG_INF;
+                    l[k] = 0.f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) v[k][j] = 0.f;
                 }
-                __syncthreads();
-                for (int it = tid; it < Items; it += kThreads) {
-                    const int ln = it & 31, w = (it >> 5) % (W / 2), ne = (it >> 5) / (W / 2);
-                    const int r = 8 * (ne >> 1) + 2 * (ln & 3) + (ne & 1), d0 = (ln >> 2) * (D / 8) + 8 * w;
-                    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                    for (int c = c0; c <= c1; ++c) {
-                        const float* p = part(c);
-                        const float m = __ldcg(p + NR * 8 * D + r);
-                        const float f = m == NEG_INF ? 0.f : ex2(m - s_m[r]);
-                        const float4 x = __ldcg(reinterpret_cast<const float4*>(p + it * 8));
-                        const float4 y = __ldcg(reinterpret_cast<const float4*>(p + it * 8) + 1);
-                        v[0] += f * x.x; v[1] += f * x.y; v[2] += f * x.z; v[3] += f * x.w;
-                        v[4] += f * y.x; v[5] += f * y.y; v[6] += f * y.z; v[7] += f * y.w;
+#pragma unroll 1
+                for (unsigned cc = c0; cc <= c1; cc += kAhead) {
+                    float4 x[kAhead][Own];
+                    float pm[kAhead][Own], pl[kAhead][Own];
+#pragma unroll
+                    for (int i = 0; i < kAhead; ++i) {
+                        const unsigned ci = min(cc + i, c1);
+                        const float* part = a.partials + ((size_t)ci * 2 + (ci == c0 ? 1 : 0)) * Ly::Slot;
+#pragma unroll
+                        for (int k = 0; k < Own; ++k) {
+                            const int it = min(tid + k * kThreads, Ly::Items - 1);
+                            int r, d0;
+                            item_at(it, r, d0);
+                            x[i][k] = __ldcg(reinterpret_cast<const float4*>(part + it * 4));
+                            pm[i][k] = cc + i <= c1 ? __ldcg(part + RW * D + r) : NEG_INF;
+                            pl[i][k] = __ldcg(part + RW * D + RW + r);
+                        }
                     }
-                    store(r, d0, v, s_l[r]);
+#pragma unroll
+                    for (int i = 0; i < kAhead; ++i)
+#pragma unroll
+                        for (int k = 0; k < Own; ++k) {
+                            const float Mn = fmaxf(M[k], pm[i][k]);
+                            const float fo = M[k] == NEG_INF ? 0.f : ex2(M[k] - Mn);
+                            const float fn = pm[i][k] == NEG_INF ? 0.f : ex2(pm[i][k] - Mn);
+                            M[k] = Mn;
+                            // (a part without a visible key adds 0, or NaN if its row saw one)
+                            l[k] = l[k] * fo + pl[i][k] * fn;
+                            v[k][0] = v[k][0] * fo + x[i][k].x * fn;
+                            v[k][1] = v[k][1] * fo + x[i][k].y * fn;
+                            v[k][2] = v[k][2] * fo + x[i][k].z * fn;
+                            v[k][3] = v[k][3] * fo + x[i][k].w * fn;
+                        }
+                }
+#pragma unroll
+                for (int k = 0; k < Own; ++k) {
+                    const int it = tid + k * kThreads;
+                    if (it < Ly::Items) {
+                        int r, d0;
+                        item_at(it, r, d0);
+                        store(r, d0, v[k], l[k]);
+                    }
                 }
             }
         }
-        __syncthreads();                                         // the area, Q and the flags are free again
+        fence_proxy_async_smem();                                // before the ring's next copies
+        __syncthreads();                                         // the ring, Q and the flags are free again
         if (tid == 0) s_flag[0] = 0;
     }
     // after a wait that ran out: no copy may be in flight when the CTA ends
@@ -848,7 +947,7 @@ void row_tiles(int rows, int& RT, int& per) {
 
 struct Plan {
     int RT, rows, NR, grid;
-    size_t total;                // workspace bytes
+    size_t total;                // workspace bytes; 0: more units than the kernel's 32-bit places can count
 };
 Plan plan(int B, int T, int Hq, int Hkv, int D, int NB, int sms) {
     Plan p;
@@ -859,7 +958,7 @@ Plan plan(int B, int T, int Hq, int Hkv, int D, int NB, int sms) {
     ctas = ctas < (long long)(kCounterBytes / 4) ? ctas : (long long)(kCounterBytes / 4);
     const long long want = (most + kMinUnits - 1) / kMinUnits;
     p.grid = (int)(want < ctas ? want : ctas);
-    p.total = kCounterBytes + (size_t)p.grid * 2 * (p.NR * 8 * D + 2 * p.NR * 8) * 4;
+    p.total = most < (1ll << 31) ? kCounterBytes + (size_t)p.grid * 2 * (p.NR * 8 * D + 2 * p.NR * 8) * 4 : 0;
     return p;
 }
 

@@ -800,6 +800,7 @@ qv_status qv_attention_verify_kv4(const uint16_t* qkv, const uint8_t* cache, con
     const int sms = sms_of_current_device(&e);
     if (e != cudaSuccess) return cuda_fail(e, "device query");
     const size_t need = qv::attention_kv4_workspace_bytes(B, T, Hq, Hkv, D, NB, sms);
+    if (need == 0) return fail(QV_ERR_UNSUPPORTED, "B * Hkv * NB is too large for one call");
     if (!workspace) return fail(QV_ERR_WORKSPACE, "workspace is null (%zu bytes needed)", need);
     if (!aligned(workspace, 16)) return fail(QV_ERR_WORKSPACE, "workspace must be 16-byte aligned");
     if (workspace_bytes < need) return fail(QV_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
