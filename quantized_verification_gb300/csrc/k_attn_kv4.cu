@@ -17,8 +17,8 @@
 // range order. Nobody waits for anybody, and the order of arrival changes
 // nothing.
 //
-// Inside a CTA each of the 8 warps takes every 8th unit of the range and keeps
-// its own online softmax. A record comes in one bulk copy into the warp's own
+// Inside a CTA each of the W warps (8 or 12) takes every W-th unit of the range
+// and keeps its own online softmax. A record comes in one bulk copy into the warp's own
 // ring. Both products run on the tensor cores (mma.sync m16n8k16, bf16
 // operands, fp32 accumulation) with the keys, or the value dims, on the M side
 // and the query rows on the N side in tiles of 8: a verify step has 4 to 32
@@ -64,8 +64,6 @@ __device__ unsigned int g_attn_kv4_error;
 
 namespace {
 
-constexpr int kWarps = 8;
-constexpr int kThreads = kWarps * 32;
 constexpr int kRowTile = 32;                    // query rows of a tile
 constexpr int kMinUnits = 16;                   // places of a CTA's range at least: two units a warp
 constexpr size_t kCounterBytes = 4096;         // at the workspace's start, whatever the shape
@@ -94,21 +92,28 @@ struct Layout {
     using Rec = Kv4Rec<D>;
     static constexpr int W = D / 32;                      // 32-bit code words of a thread per key row
     static constexpr int KS = D / 16;                     // k steps of Q K^T = dim tiles of P V
-    static constexpr bool TwoCtas = D / 64 * NR <= 2;     // two CTAs per SM (at most 128 registers a thread)
-    static constexpr int Stages = D == 128 && TwoCtas ? 3 : 4;
-    // With one CTA (two warps a scheduler) the products of the next 16 positions
-    // are formed between those of P and V of the present ones.
-    static constexpr bool Pipe = !TwoCtas;
-    static constexpr bool QRegs = TwoCtas;                // the query fragments stay in registers
+    // What a warp's outputs take of its registers decides how many warps an SM
+    // holds: 16 (two CTAs, 128 registers a thread), 12 (168) or 8 (255). The
+    // tensor and ALU work of a step comes in dependent runs, so warps are what
+    // keeps the pipes busy.
+    static constexpr int ORegs = KS * NR * 4;
+    static constexpr int Ctas = ORegs <= 64 ? 2 : 1;
+    static constexpr int Warps = ORegs <= 64 ? 8 : (ORegs <= 96 ? 12 : 8);
+    static constexpr int Threads = Warps * 32;
+    static constexpr int Stages = D == 128 && Warps * Ctas >= 12 ? 3 : 4;
+    // With 8 warps on an SM the products of the next 16 positions are formed
+    // between those of P and V of the present ones.
+    static constexpr bool Pipe = Warps * Ctas == 8;
+    static constexpr bool QRegs = ORegs <= 32;            // the query fragments stay in registers
     static constexpr int RW = NR * 8;
     static constexpr int Ring = 0;
-    static constexpr int RingBytes = kWarps * Stages * Rec::Bytes;
-    static constexpr int AreaBytes = kWarps * RW * D * 4; // the warps' outputs [8][NR*4*KS][32], in the drained ring
+    static constexpr int RingBytes = Warps * Stages * Rec::Bytes;
+    static constexpr int AreaBytes = Warps * RW * D * 4; // the warps' outputs [Warps][NR*4*KS][32], in the drained ring
     static constexpr int Q = Ring + RingBytes;            // query fragments [NR][KS][32] uint2
-    static constexpr int ML = Q + NR * KS * 32 * 8;       // m [8 warps][RW], l [8][RW]
-    static constexpr int Bar = ML + 2 * kWarps * RW * 4;
-    static constexpr int Valid = Bar + kWarps * Stages * 8;
-    static constexpr int Scan = Valid + kWarps * Stages * 4;  // unsigned [8], then the first sequence and its place
+    static constexpr int ML = Q + NR * KS * 32 * 8;       // m [Warps][RW], l [Warps][RW]
+    static constexpr int Bar = ML + 2 * Warps * RW * 4;
+    static constexpr int Valid = Bar + Warps * Stages * 8;
+    static constexpr int Scan = Valid + Warps * Stages * 4;    // unsigned [Warps], then [14], [15]: the first sequence's place and number
     static constexpr int Misc = Scan + 16 * 4;
     static constexpr int Bytes = Misc + 64;
     static constexpr int Items = RW * D / 4;              // groups of 4 dims of one row
@@ -252,10 +257,10 @@ __device__ __forceinline__ int seq_len(const Args& a, int b) {
 }
 
 template <int D, int NR, bool OUTBF>
-__global__ void __launch_bounds__(kThreads, Layout<D, NR>::TwoCtas ? 2 : 1) attn_kv4_kernel(const Args a) {
+__global__ void __launch_bounds__(Layout<D, NR>::Threads, Layout<D, NR>::Ctas) attn_kv4_kernel(const Args a) {
     using Ly = Layout<D, NR>;
     using Rec = Kv4Rec<D>;
-    constexpr int W = Ly::W, KS = Ly::KS, S = Ly::Stages, RW = Ly::RW;
+    constexpr int W = Ly::W, KS = Ly::KS, S = Ly::Stages, RW = Ly::RW, kWarps = Ly::Warps, kThreads = Ly::Threads;
     extern __shared__ __align__(128) uint8_t smem[];
     const uint32_t sbase = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t4 = lane & 3;
@@ -313,12 +318,12 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NR>::TwoCtas ? 2 : 1) attn
             at += n;
             ++b;
         }
-        s_scan[8] = at;
-        s_scan[9] = (unsigned)b;
+        s_scan[14] = at;
+        s_scan[15] = (unsigned)b;
     }
     __syncthreads();
-    unsigned seq_at = s_scan[8];                                 // where the sequence's places begin
-    int b_next = (int)s_scan[9];
+    unsigned seq_at = s_scan[14];                                 // where the sequence's places begin
+    int b_next = (int)s_scan[15];
     unsigned u = u0;
     unsigned issued = 0, used = 0;                               // this warp's records so far
     bool dead = false;                                           // a wait of this warp ran out: it takes no more units
@@ -523,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NR>::TwoCtas ? 2 : 1) attn
         // first records are on their way: unit nc + i holds rows 32 i .. 32 i + 31
         // and belongs to the warp that comes next in the units' order
 #pragma unroll 1
-        for (int un = max(ua, nc) + ((warp - (max(ua, nc) - ua)) & (kWarps - 1)); un < ub; un += kWarps) {
+        for (int un = max(ua, nc) + (warp + kWarps - (max(ua, nc) - ua) % kWarps) % kWarps; un < ub; un += kWarps) {
             const uint16_t* base = a.qkv + (size_t)b * a.T * rowlen + (size_t)(a.Hq + kh) * D;
             bool bad = false;
 #pragma unroll 1
@@ -922,12 +927,12 @@ __global__ void __launch_bounds__(kThreads, Layout<D, NR>::TwoCtas ? 2 : 1) attn
 template <int D, int NR, bool OUTBF>
 cudaError_t launch(const Args& a, int grid, cudaStream_t s) {
     using Ly = Layout<D, NR>;
-    static_assert(Ly::Bytes <= (int)(Ly::TwoCtas ? kMaxDynSmem / 2 - 1024 : kMaxDynSmem), "shared memory budget");
+    static_assert(Ly::Bytes <= (int)(Ly::Ctas == 2 ? kMaxDynSmem / 2 - 1024 : kMaxDynSmem), "shared memory budget");
     cudaError_t e = cudaFuncSetAttribute(attn_kv4_kernel<D, NR, OUTBF>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ly::Bytes);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)grid);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(Ly::Threads);
     cfg.dynamicSmemBytes = Ly::Bytes;
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -954,7 +959,7 @@ Plan plan(int B, int T, int Hq, int Hkv, int D, int NB, int sms) {
     row_tiles(T * (Hq / Hkv), p.RT, p.rows);
     p.NR = (p.rows + 7) / 8;
     const long long most = (long long)B * Hkv * p.RT * ((long long)NB + (T + 31) / 32 + kTileCost);   // places at most
-    long long ctas = (long long)sms * (D / 64 * p.NR <= 2 ? 2 : 1);
+    long long ctas = (long long)sms * (D / 64 * p.NR <= 4 ? 2 : 1);
     ctas = ctas < (long long)(kCounterBytes / 4) ? ctas : (long long)(kCounterBytes / 4);
     const long long want = (most + kMinUnits - 1) / kMinUnits;
     p.grid = (int)(want < ctas ? want : ctas);

@@ -7,11 +7,13 @@
 //   for 127 and one scale for every 32 elements of a head's row, so that an
 //   outlier channel costs its own 32 neighbours precision and no others.
 //
-// Both kernels move 8 elements a thread (16 bytes of bf16), four threads a
-// scale group, consecutive threads on consecutive elements of a row: reads and
-// writes of the wide side are whole lines, those of the code side whole
-// sectors (64 bytes a head's row at D = 128). They are bound by memory at
-// prompt lengths and by launch latency at a step's few rows.
+// A CTA takes the positions of one sequence in one block, for one head or a
+// few, so that the chain start -> block table -> record is walked once for up
+// to 64 KB. A thread moves 8 elements (16 bytes of bf16), four threads a scale
+// group, consecutive threads on consecutive elements: the wide side moves in
+// runs of 256 bytes (a head's row at D = 128), the codes in whole sectors, and
+// the four rows of a thread are requested before the first is worked on. Bound
+// by memory at prompt lengths and by launch latency at a step's few rows.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -35,38 +37,60 @@ struct Kv4Args {
     const int32_t* table;
     const int32_t* start;
     const int32_t* count;
-    int T, rows, Hq, Hkv, NB, pages;
+    int T, Hq, Hkv, NB, pages;
+    int heads;                 // heads of a CTA
 };
 
-// The record position a (sequence, row) maps to, or false: rows past the
-// sequence's count, positions outside the block table and pages outside the
-// pool have none.
-__device__ __forceinline__ bool locate(const Kv4Args& a, int row, int& page, int& slot) {
-    const int b = row / a.T, j = row - b * a.T;
-    if (a.count && j >= a.count[b]) return false;
-    const long long pos = (long long)a.start[b] + j;
-    if (pos < 0 || pos >= (long long)a.NB * kKv4Block) return false;
-    page = kv4_page(a.table, b, a.NB, a.pages, (int)(pos / kKv4Block));
-    slot = (int)(pos % kKv4Block);
-    return page >= 0;
+// What a CTA works on: sequence b's rows in one block. Rows past the count,
+// positions outside the block table and pages outside the pool have none.
+struct Block {
+    int first;                 // the sequence's row (j) at the block's slot 0; may be negative
+    int rows;                  // rows j in [0, rows) exist
+    const uint8_t* page;       // the block's records, or null
+};
+__device__ __forceinline__ Block find_block(const Kv4Args& a, int b, int nth, size_t rec_bytes) {
+    const int start = a.start[b], cnt = a.count ? a.count[b] : a.T;
+    const long long blk = (long long)(start >> 5) + nth;         // (>> rounds down)
+    Block k;
+    k.rows = cnt < a.T ? cnt : a.T;
+    k.page = nullptr;
+    k.first = (int)(blk * kKv4Block - start);
+    if (blk < 0 || blk >= a.NB || k.first >= k.rows) return k;
+    const int page = kv4_page(a.table, b, a.NB, a.pages, (int)blk);
+    if (page >= 0) k.page = a.cache + (size_t)page * a.Hkv * rec_bytes;
+    return k;
+}
+
+// The larger magnitude, NaN if either is NaN.
+__device__ __forceinline__ float max_abs_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(fabsf(b)));
+    return y;
 }
 
 template <bool BF16>
-__device__ __forceinline__ void load8(const uint8_t* p, float (&v)[8]) {
-    if (BF16) {
-        const uint4 u = *reinterpret_cast<const uint4*>(p);
-        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+struct Raw {                   // 8 elements as they are in memory
+    uint4 u[BF16 ? 1 : 2];
+    __device__ __forceinline__ void load(const uint8_t* p) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            v[2 * i] = __uint_as_float(w[i] << 16);
-            v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
-        }
-    } else {
-        const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 16);
-        v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-        v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+        for (int i = 0; i < (BF16 ? 1 : 2); ++i) u[i] = reinterpret_cast<const uint4*>(p)[i];
     }
-}
+    __device__ __forceinline__ void values(float (&v)[8]) const {
+#pragma unroll
+        for (int i = 0; i < (BF16 ? 1 : 2); ++i) {
+            const uint32_t w[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (BF16) {
+                    v[2 * k] = __uint_as_float(w[k] << 16);
+                    v[2 * k + 1] = __uint_as_float(w[k] & 0xFFFF0000u);
+                } else {
+                    v[4 * i + k] = __uint_as_float(w[k]);
+                }
+            }
+        }
+    }
+};
 
 // The scale byte of a group whose largest magnitude is amax: the nearest scale
 // to fl32(amax / 7), ties to the even byte. Rounding adds half of the last
@@ -77,94 +101,146 @@ __device__ __forceinline__ uint32_t scale_byte(float amax) {
     return (uint32_t)(b < 0 ? 0 : (b > 255 ? 255 : b));
 }
 
-template <int D, bool BF16>
-__global__ void __launch_bounds__(kKv4Threads) kv4_write_kernel(const Kv4Args a) {
-    using Rec = Kv4Rec<D>;
-    allow_dependent_launch();
-    grid_dependency_wait();
-    const int ipr = 2 * a.Hkv * D / 8;                         // items of 8 elements per row
-    const int item = blockIdx.y * blockDim.x + threadIdx.x;
-    const int row = blockIdx.x * blockDim.y + threadIdx.y;
-    if (item >= ipr || row >= a.rows) return;                  // whole groups of 4 threads
-    float v[8];
-    const size_t e0 = (size_t)row * (size_t)(a.Hq + 2 * a.Hkv) * D + (size_t)a.Hq * D + (size_t)item * 8;
-    load8<BF16>(a.x + e0 * (BF16 ? 2 : 4), v);
-    int page, slot;
-    if (!locate(a, row, page, slot)) return;
-    const int lane = (threadIdx.y * blockDim.x + threadIdx.x) & 31;
-    const unsigned mask = 0xFu << (lane & ~3);
-    // magnitudes are compared as bit patterns: infinities and NaN sort last
-    uint32_t am = 0;
+// The codes of 8 elements, four neighbouring threads (of `mask`) a group.
+//
+// The code is the integer nearest fl32(x / s). With r = fl32(1 / s) and
+// q0 = fl32(x r), the residual x - q0 s is exact in a fused multiply-add, and
+// q0 + r * residual is the correctly rounded quotient (one correction step of
+// Markstein, IBM J. Res. Dev. 34, 1990; checked against the quotient for every
+// binary32 significand and all 8 significands of s). Adding 1.5 * 2^23 + 8
+// rounds it half to even and leaves q + 8 in the low bits; the eight sums are
+// weighted by 16^i, and one subtraction takes the constant parts off.
+// |x / s| < 7.5 by the choice of s, but for scales cut off at the largest one.
+__device__ __forceinline__ uint32_t encode8(float (&v)[8], unsigned mask, uint32_t& sb) {
+    float am = fabsf(v[0]);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) am = max(am, __float_as_uint(v[i]) & 0x7FFFFFFFu);
-    am = max(am, __shfl_xor_sync(mask, am, 1));
-    am = max(am, __shfl_xor_sync(mask, am, 2));
-    if (am >= 0x7F800000u) {                                   // rare: NaN counts as 0, infinities saturate
-        am = 0;
+    for (int i = 1; i < 8; ++i) am = max_abs_nan(am, v[i]);
+    am = max_abs_nan(am, __shfl_xor_sync(mask, am, 1));
+    am = max_abs_nan(am, __shfl_xor_sync(mask, am, 2));
+    if (!(am <= 7.f * 122880.f)) {                             // rare: NaN counts as 0, large magnitudes saturate
+        am = 0.f;
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            if (isnan(v[i])) v[i] = 0.f;
-            v[i] = fminf(fmaxf(v[i], -3.402823466e38f), 3.402823466e38f);
-            am = max(am, __float_as_uint(v[i]) & 0x7FFFFFFFu);
+            v[i] = v[i] == v[i] ? fminf(fmaxf(v[i], -7.f * 122880.f), 7.f * 122880.f) : 0.f;
+            am = fmaxf(am, fabsf(v[i]));
         }
-        am = max(am, __shfl_xor_sync(mask, am, 1));
-        am = max(am, __shfl_xor_sync(mask, am, 2));
+        am = fmaxf(am, __shfl_xor_sync(mask, am, 1));
+        am = fmaxf(am, __shfl_xor_sync(mask, am, 2));
     }
-    const uint32_t sb = scale_byte(__uint_as_float(am));
-    const float s = kv4_scale(sb);
+    sb = scale_byte(am);
+    const float s = kv4_scale(sb), r = __fdiv_rn(1.0f, s);
     uint32_t w = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float q = fminf(fmaxf(rintf(__fdiv_rn(v[i], s)), -7.f), 7.f);
-        w |= ((uint32_t)(int)q & 15u) << (4 * i);
+        const float q0 = __fmul_rn(v[i], r);
+        const float q = __fmaf_rn(__fmaf_rn(-q0, s, v[i]), r, q0);
+        w += __float_as_uint(__fadd_rn(q, 12582920.0f)) * (1u << (4 * i));
     }
-    const int kv = item >= ipr / 2, rem = item - kv * (ipr / 2);
-    const int h = rem / (D / 8), c = rem - h * (D / 8);
-    uint8_t* rec = a.cache + ((size_t)page * a.Hkv + h) * Rec::Bytes;
-    *reinterpret_cast<uint32_t*>(rec + (kv ? Rec::VC : Rec::KC) + slot * Rec::RowBytes + c * 4) = w;
-    if ((c & 3) == 0) rec[(kv ? Rec::VS : Rec::KS) + slot * Rec::RowScales + (c >> 2)] = (uint8_t)sb;
+    constexpr uint32_t ones = 0x11111111u;
+    return (w - 0x4B400000u * ones) ^ 0x88888888u;             // q + 8, then two's complement
+}
+
+template <int D, bool BF16>
+__global__ void __launch_bounds__(kKv4Threads) kv4_write_kernel(const Kv4Args a) {
+    using Rec = Kv4Rec<D>;
+    constexpr int Chunks = D / 8;                              // threads of a row
+    constexpr int Rows = kKv4Threads / Chunks;                 // rows the CTA takes at once
+    constexpr int Steps = 2 * kKv4Block / Rows;                // keys, then values
+    allow_dependent_launch();
+    grid_dependency_wait();
+    const int b = blockIdx.z, h0 = blockIdx.y * a.heads;
+    const Block k = find_block(a, b, blockIdx.x, Rec::Bytes);
+    if (!k.page) return;
+    const int c = threadIdx.x % Chunks, r = threadIdx.x / Chunks;
+    const unsigned mask = 0xFu << (threadIdx.x & 28);
+    constexpr int E = BF16 ? 2 : 4;
+    const size_t rowlen = (size_t)(a.Hq + 2 * a.Hkv) * D;
+    for (int h = h0; h < min(a.Hkv, h0 + a.heads); ++h) {
+        uint8_t* rec = const_cast<uint8_t*>(k.page) + (size_t)h * Rec::Bytes;
+        const uint8_t* x = a.x + ((size_t)b * a.T * rowlen + (size_t)(a.Hq + h) * D + c * 8) * E;
+        Raw<BF16> raw[Steps];
+#pragma unroll
+        for (int i = 0; i < Steps; ++i) {
+            const int kv = i / (Steps / 2), slot = (i % (Steps / 2)) * Rows + r, j = k.first + slot;
+            if (j >= 0 && j < k.rows) raw[i].load(x + ((size_t)j * rowlen + (size_t)kv * a.Hkv * D) * E);
+        }
+#pragma unroll
+        for (int i = 0; i < Steps; ++i) {
+            const int kv = i / (Steps / 2), slot = (i % (Steps / 2)) * Rows + r, j = k.first + slot;
+            if (j < 0 || j >= k.rows) continue;                // (whole rows: groups of 4 threads stay together)
+            float v[8];
+            raw[i].values(v);
+            uint32_t sb;
+            const uint32_t w = encode8(v, mask, sb);
+            *reinterpret_cast<uint32_t*>(rec + (kv ? Rec::VC : Rec::KC) + slot * Rec::RowBytes + c * 4) = w;
+            if ((c & 3) == 0) rec[(kv ? Rec::VS : Rec::KS) + slot * Rec::RowScales + (c >> 2)] = (uint8_t)sb;
+        }
+    }
+}
+
+// The values of 8 codes as four bf16 pairs: a nibble shifted to bits 3..6 with
+// its sign bit flipped, under the bf16 pattern of 16.0, is 24 + q; one fused
+// multiply-add gives (24 + q) s - 24 s = q s exactly. That yields the pairs
+// (j, j + 4), which byte permutations put in order.
+__device__ __forceinline__ uint4 decode8(uint32_t w, uint32_t sb) {
+    const uint32_t s = sb * 0x00100010u + 0x38003800u;
+    uint32_t off, p[4];
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(off) : "r"(s), "r"(0xC1C0C1C0u));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const uint32_t y = ((j == 0 ? w << 3 : w >> (4 * j - 3)) & 0x00780078u) ^ 0x41C041C0u;
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(p[j]) : "r"(y), "r"(s), "r"(off));
+    }
+    return make_uint4(__byte_perm(p[0], p[1], 0x5410), __byte_perm(p[2], p[3], 0x5410), __byte_perm(p[0], p[1], 0x7632),
+                      __byte_perm(p[2], p[3], 0x7632));
 }
 
 template <int D, bool BF16>
 __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(const Kv4Args a) {
     using Rec = Kv4Rec<D>;
+    constexpr int Chunks = D / 8, Rows = kKv4Threads / Chunks, Steps = 2 * kKv4Block / Rows;
     allow_dependent_launch();
     grid_dependency_wait();
-    const int ipr = 2 * a.Hkv * D / 8;
-    const int item = blockIdx.y * blockDim.x + threadIdx.x;
-    const int row = blockIdx.x * blockDim.y + threadIdx.y;
-    if (item >= ipr || row >= a.rows) return;
-    int page, slot;
-    if (!locate(a, row, page, slot)) return;
-    const int kv = item >= ipr / 2, rem = item - kv * (ipr / 2);
-    const int h = rem / (D / 8), c = rem - h * (D / 8);
-    const uint8_t* rec = a.cache + ((size_t)page * a.Hkv + h) * Rec::Bytes;
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(rec + (kv ? Rec::VC : Rec::KC) + slot * Rec::RowBytes + c * 4);
-    const float s = kv4_scale(rec[(kv ? Rec::VS : Rec::KS) + slot * Rec::RowScales + (c >> 2)]);
-    float v[8];
+    const int b = blockIdx.z, h0 = blockIdx.y * a.heads;
+    const Block k = find_block(a, b, blockIdx.x, Rec::Bytes);
+    if (!k.page) return;
+    const int c = threadIdx.x % Chunks, r = threadIdx.x / Chunks;
+    constexpr int E = BF16 ? 2 : 4;
+    for (int h = h0; h < min(a.Hkv, h0 + a.heads); ++h) {
+        const uint8_t* rec = k.page + (size_t)h * Rec::Bytes;
+        uint32_t w[Steps], sb[Steps];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = (float)((int)(w << (28 - 4 * i)) >> 28) * s;   // exact: 7 significant bits
-    const size_t e = (size_t)row * a.Hkv * D + (size_t)rem * 8;
-    uint8_t* o = (kv ? a.v_out : a.k_out) + e * (BF16 ? 2 : 4);
-    if (BF16) {
-        uint32_t p[4];
+        for (int i = 0; i < Steps; ++i) {                      // (every slot of the record can be read)
+            const int kv = i / (Steps / 2), slot = (i % (Steps / 2)) * Rows + r;
+            w[i] = *reinterpret_cast<const uint32_t*>(rec + (kv ? Rec::VC : Rec::KC) + slot * Rec::RowBytes + c * 4);
+            sb[i] = rec[(kv ? Rec::VS : Rec::KS) + slot * Rec::RowScales + (c >> 2)];
+        }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = __byte_perm(__float_as_uint(v[2 * i]), __float_as_uint(v[2 * i + 1]), 0x7632);
-        *reinterpret_cast<uint4*>(o) = make_uint4(p[0], p[1], p[2], p[3]);
-    } else {
-        *reinterpret_cast<float4*>(o) = make_float4(v[0], v[1], v[2], v[3]);
-        *reinterpret_cast<float4*>(o + 16) = make_float4(v[4], v[5], v[6], v[7]);
+        for (int i = 0; i < Steps; ++i) {
+            const int kv = i / (Steps / 2), slot = (i % (Steps / 2)) * Rows + r, j = k.first + slot;
+            if (j < 0 || j >= k.rows) continue;
+            const uint4 y = decode8(w[i], sb[i]);
+            uint8_t* o = (kv ? a.v_out : a.k_out) + (((size_t)b * a.T + j) * (size_t)a.Hkv * D + (size_t)h * D + c * 8) * E;
+            if (BF16) {
+                *reinterpret_cast<uint4*>(o) = y;
+            } else {
+                *reinterpret_cast<uint4*>(o) = make_uint4(y.x << 16, y.x & 0xFFFF0000u, y.y << 16, y.y & 0xFFFF0000u);
+                *reinterpret_cast<uint4*>(o + 16) = make_uint4(y.z << 16, y.z & 0xFFFF0000u, y.w << 16, y.w & 0xFFFF0000u);
+            }
+        }
     }
 }
 
+// One CTA per sequence, block that its T rows can touch, and group of heads:
+// as many heads as leave 8 CTAs an SM (or one head each).
 template <class Kernel>
-cudaError_t launch_rows(Kernel kernel, const Kv4Args& a, int D, cudaStream_t s) {
-    const int ipr = 2 * a.Hkv * D / 8;                         // a multiple of 16
-    const int bx = ipr < kKv4Threads ? ipr : kKv4Threads;
-    const int by = kKv4Threads / bx;
+cudaError_t launch_rows(Kernel kernel, Kv4Args& a, int B, int sms, cudaStream_t s) {
+    const int blocks = (a.T + kKv4Block - 2) / kKv4Block + 1;
+    a.heads = 1;
+    while (a.heads * 2 <= a.Hkv && (long long)blocks * B * ceil_div(a.Hkv, a.heads * 2) >= 8LL * sms) a.heads *= 2;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)ceil_div(a.rows, by), (unsigned)ceil_div(ipr, bx));
-    cfg.blockDim = dim3((unsigned)bx, (unsigned)by);
+    cfg.gridDim = dim3((unsigned)blocks, (unsigned)ceil_div(a.Hkv, a.heads), (unsigned)B);
+    cfg.blockDim = dim3(kKv4Threads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -178,24 +254,24 @@ cudaError_t launch_rows(Kernel kernel, const Kv4Args& a, int D, cudaStream_t s) 
 
 cudaError_t launch_kv4_write(const void* x, bool bf16, const int32_t* start, const int32_t* count,
                              const int32_t* table, int B, int T, int Hq, int Hkv, int D, int NB, int pages,
-                             uint8_t* cache, cudaStream_t s) {
+                             uint8_t* cache, int sms, cudaStream_t s) {
     Kv4Args a = {};
     a.x = static_cast<const uint8_t*>(x);
     a.cache = cache; a.table = table; a.start = start; a.count = count;
-    a.T = T; a.rows = B * T; a.Hq = Hq; a.Hkv = Hkv; a.NB = NB; a.pages = pages;
-    if (D == 128) return bf16 ? launch_rows(kv4_write_kernel<128, true>, a, D, s) : launch_rows(kv4_write_kernel<128, false>, a, D, s);
-    return bf16 ? launch_rows(kv4_write_kernel<64, true>, a, D, s) : launch_rows(kv4_write_kernel<64, false>, a, D, s);
+    a.T = T; a.Hq = Hq; a.Hkv = Hkv; a.NB = NB; a.pages = pages;
+    if (D == 128) return bf16 ? launch_rows(kv4_write_kernel<128, true>, a, B, sms, s) : launch_rows(kv4_write_kernel<128, false>, a, B, sms, s);
+    return bf16 ? launch_rows(kv4_write_kernel<64, true>, a, B, sms, s) : launch_rows(kv4_write_kernel<64, false>, a, B, sms, s);
 }
 
 cudaError_t launch_kv4_read(const uint8_t* cache, const int32_t* start, const int32_t* count, const int32_t* table,
                             int B, int T, int Hkv, int D, int NB, int pages, void* k_out, void* v_out, bool bf16,
-                            cudaStream_t s) {
+                            int sms, cudaStream_t s) {
     Kv4Args a = {};
     a.k_out = static_cast<uint8_t*>(k_out); a.v_out = static_cast<uint8_t*>(v_out);
     a.cache = const_cast<uint8_t*>(cache); a.table = table; a.start = start; a.count = count;
-    a.T = T; a.rows = B * T; a.Hkv = Hkv; a.NB = NB; a.pages = pages;
-    if (D == 128) return bf16 ? launch_rows(kv4_read_kernel<128, true>, a, D, s) : launch_rows(kv4_read_kernel<128, false>, a, D, s);
-    return bf16 ? launch_rows(kv4_read_kernel<64, true>, a, D, s) : launch_rows(kv4_read_kernel<64, false>, a, D, s);
+    a.T = T; a.Hkv = Hkv; a.NB = NB; a.pages = pages;
+    if (D == 128) return bf16 ? launch_rows(kv4_read_kernel<128, true>, a, B, sms, s) : launch_rows(kv4_read_kernel<128, false>, a, B, sms, s);
+    return bf16 ? launch_rows(kv4_read_kernel<64, true>, a, B, sms, s) : launch_rows(kv4_read_kernel<64, false>, a, B, sms, s);
 }
 
 }  // namespace qv

@@ -10,14 +10,16 @@
 // One pass over the row: each thread keeps its own running m, S and T and
 // rescales them when its m grows by d: S *= 2^-d, T = 2^-d (T - d S). The
 // alternatives cost the pass nothing more: m is also the thread's largest
-// logit, and the K-th largest of the threads' maxima, tau, is a lower bound of
-// the row's K-th largest logit, reached by few more than K threads. Only
-// those threads' entries (1/512 of the slice each) are read again, from L2,
-// by whole warps that keep a sorted list of 32 keys (value, then the lower
-// index) across their lanes.
+// logit. Of the two largest maxima of each of the 16 warps the K-th largest,
+// tau, is a lower bound of the row's K-th largest logit, and few more than K
+// threads reach it. Only those threads' entries (1/512 of the slice each) are
+// read again, from L2, and the entries at or above tau are ordered by counting,
+// for each, those before it (by value, then by the lower index). Where ties or
+// masks leave too many of them, warps keep sorted lists of 32 instead.
 //
 // A row is the work of one CTA, or of a cluster of C of them that split it
-// (launch_token_logprobs) and combine through distributed shared memory.
+// (launch_token_logprobs) and combine through distributed shared memory: the
+// statistics and the largest tau, then the entries.
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -39,7 +41,8 @@ constexpr int kLpMaxCluster = 16;
 constexpr int kLpUnroll = 4;                    // vectors in flight per thread
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-static_assert(kLpMaxCluster <= kLpWarps, "one warp per CTA's list in the cluster merge");
+constexpr int kLpCand = 512;                    // entries of a row ordered by counting, kLpCand / C of a CTA
+static_assert(kLpCand / kLpMaxCluster >= 32 && kLpCand <= kLpThreads, "a CTA's K entries fit, one thread an entry");
 
 struct LpArgs {
     const uint8_t* x;          // logits [M][V]
@@ -116,20 +119,6 @@ __device__ __forceinline__ float key_value(unsigned long long k) {
     return __uint_as_float(o ^ ((o >> 31) ? 0x80000000u : 0xFFFFFFFFu));
 }
 
-// Sorts one value per lane, the largest in lane 0 (Batcher's bitonic network).
-template <class T>
-__device__ __forceinline__ T warp_sort_desc(T v) {
-    const int lane = threadIdx.x & 31;
-#pragma unroll
-    for (int k = 2; k <= 32; k <<= 1)
-#pragma unroll
-        for (int j = k >> 1; j > 0; j >>= 1) {
-            const T o = __shfl_xor_sync(0xffffffffu, v, j);
-            const bool up = ((lane & k) == 0) == ((lane & j) == 0);   // this lane keeps the larger
-            v = up ? (o > v ? o : v) : (o < v ? o : v);
-        }
-    return v;
-}
 // The 32 largest of two descending lists, descending; `o` is the other list
 // reversed (lane i holds its entry 31 - i).
 template <class T>
@@ -215,16 +204,37 @@ __device__ __forceinline__ void warp_insert(unsigned long long& list, unsigned l
     }
 }
 
+// Visits the entries that thread t of the CTA owns, 32 vectors at a time (the
+// whole warp calls it): fn(value, index, there).
+template <bool BF16, class F>
+__device__ __forceinline__ void for_thread(const Row<BF16>& r, int t, bool first_cta, int v0, int v1, F&& fn) {
+    constexpr int E = Row<BF16>::E;
+    const int lane = threadIdx.x & 31;
+    const int one = first_cta ? r.single(t) : -1;
+    if (one >= 0) fn(r.at(one), one, lane == 0);
+    for (int base = v0 + t; base < v1; base += 32 * kLpThreads) {
+        const int vn = base + lane * kLpThreads;
+        float v[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) v[e] = 0.f;
+        if (vn < v1) Row<BF16>::unpack(r.vec(vn), v);
+#pragma unroll
+        for (int e = 0; e < E; ++e) fn(v[e], r.head + vn * E + e, vn < v1);
+    }
+}
+
 template <bool BF16>
 __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const LpArgs a) {
     constexpr int E = Row<BF16>::E;
     __shared__ Stat s_stat[kLpWarps];
-    __shared__ Stat c_stat[kLpMaxCluster];                     // written by every CTA of the row (in CTA 0)
-    __shared__ unsigned long long s_keys[kLpWarps * 32];
-    __shared__ unsigned long long c_keys[kLpMaxCluster * 32];
+    __shared__ Stat c_stat[kLpMaxCluster];                     // one per CTA of the row, in every CTA
+    __shared__ float c_tau[kLpMaxCluster];
+    __shared__ unsigned long long c_keys[kLpCand];             // entries of the row (in CTA 0), `cap` places per CTA
+    __shared__ int c_n[kLpMaxCluster];
+    __shared__ unsigned long long s_keys[kLpCand];             // this CTA's entries, or the warps' lists
+    __shared__ float s_top[32];
     __shared__ int s_who[kLpThreads];
-    __shared__ int s_n;
-    __shared__ float s_tau;
+    __shared__ int s_n, s_m;
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     if (C > 1) cluster_arrive_relaxed();                       // waited for before the first store into another CTA
@@ -232,14 +242,19 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const LpA
     grid_dependency_wait();
 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const float NEG_INF = -__uint_as_float(0x7F800000u);
     const size_t row = blockIdx.x / C;
     const Row<BF16> r(a.x, row, a.V);
     const int per = (r.nvec + C - 1) / C;
     const int v0 = min(r.nvec, rank * per), v1 = min(r.nvec, v0 + per);
-    if (tid == 0) s_n = 0;
+    if (tid == 0) s_n = s_m = 0;
+    // the given token's logit, early: its two loads hide behind the pass
+    const int tok = rank == 0 && tid == 0 ? a.tok[row] : -1;
+    const bool in_range = tok >= 0 && tok < a.V;
+    const float x_tok = in_range ? r.at(tok) : 0.f;
 
     // ---- the pass
-    Stat st = {-__uint_as_float(0x7F800000u), 0.f, 0.f};
+    Stat st = {NEG_INF, 0.f, 0.f};
     const int own1 = rank == 0 ? r.single(tid) : -1;
     if (own1 >= 0) {
         const float v[1] = {r.at(own1)};
@@ -262,7 +277,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const LpA
     }
     const float mine = st.m;
 
-    // ---- the CTA's statistics, then the row's in CTA 0, in rank order
+    // ---- each warp's statistics and two largest maxima, then the CTA's
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) {
         Stat o;
@@ -271,79 +286,133 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const LpA
         o.T = __shfl_xor_sync(0xffffffffu, st.T, off);
         st = combine(st, o);
     }
-    if (lane == 0) s_stat[warp] = st;
-
-    // ---- this CTA's K largest entries
-    unsigned long long list = 0;
     if (a.K > 0) {
-        float* s_f = reinterpret_cast<float*>(s_keys);
-        float t = block_merge_desc(warp_sort_desc(mine), s_f, kLpWarps);
-        if (tid == a.K - 1) s_tau = t;                         // K <= 32: warp 0
-        __syncthreads();
-        const float tau = s_tau;
-        if (mine >= tau) s_who[atomicAdd(&s_n, 1)] = tid;      // (an entry's place in the list does not matter)
-        __syncthreads();
-        for (int i = warp; i < s_n; i += kLpWarps) {
-            const int t1 = s_who[i];
-            const int one = rank == 0 ? r.single(t1) : -1;
-            if (one >= 0) {
-                const float v = r.at(one);
-                warp_insert(list, entry_key(v, one), lane == 0 && v >= tau);
-            }
-            for (int base = v0 + t1; base < v1; base += 32 * kLpThreads) {
-                const int vn = base + lane * kLpThreads;
-                float v[E];
-                if (vn < v1) Row<BF16>::unpack(r.vec(vn), v);
+        const unsigned at = __ballot_sync(0xffffffffu, mine == st.m);
+        float second = lane == __ffs(at) - 1 ? NEG_INF : mine;
 #pragma unroll
-                for (int e = 0; e < E; ++e) {
-                    const bool in = vn < v1 && v[e] >= tau;
-                    if (!__any_sync(0xffffffffu, in)) continue;
-                    const unsigned long long k = in ? entry_key(v[e], r.head + vn * E + e) : 0ull;
-                    const unsigned long long least = __shfl_sync(0xffffffffu, list, a.K - 1);
-                    warp_insert(list, k, in && k > least);
-                }
-            }
+        for (int off = 16; off > 0; off >>= 1) second = fmaxf(second, __shfl_xor_sync(0xffffffffu, second, off));
+        if (lane == 0) {
+            s_top[warp] = st.m;
+            s_top[16 + warp] = second;
         }
-        __syncthreads();                                       // s_keys still held the maxima's lists
-        list = block_merge_desc(list, s_keys, kLpWarps);
     }
+    if (lane == 0) s_stat[warp] = st;
     __syncthreads();
+    auto reduce16 = [&](const Stat* p, int count) {            // in a fixed order; the same in every lane
+        Stat c = lane < count ? p[lane] : Stat{NEG_INF, 0.f, 0.f};
+#pragma unroll
+        for (int off = 8; off > 0; off >>= 1) {
+            Stat o;
+            o.m = __shfl_xor_sync(0xffffffffu, c.m, off);
+            o.S = __shfl_xor_sync(0xffffffffu, c.S, off);
+            o.T = __shfl_xor_sync(0xffffffffu, c.T, off);
+            c = combine(c, o);
+        }
+        return c;
+    };
+    float tau = NEG_INF;
+    if (a.K > 0) {                                             // the K-th largest of the 32 maxima
+        const float v = s_top[lane];
+        int before = 0;
+#pragma unroll
+        for (int j = 0; j < 32; ++j) {
+            const float o = __shfl_sync(0xffffffffu, v, j);
+            before += (o > v || (o == v && j < lane)) ? 1 : 0;
+        }
+        tau = __shfl_sync(0xffffffffu, v, __ffs(__ballot_sync(0xffffffffu, before == a.K - 1)) - 1);
+    }
+    Stat c = {NEG_INF, 0.f, 0.f};
+    if (warp == 0) c = reduce16(s_stat, kLpWarps);
     if (C > 1) {
         cluster_wait();                                        // every CTA of the cluster has started
-        if (warp == 0) {
-            Stat c = s_stat[0];
-            for (int w = 1; w < kLpWarps; ++w) c = combine(c, s_stat[w]);
-            if (lane == 0) *cluster.map_shared_rank(c_stat + rank, 0) = c;
-            if (a.K > 0) *cluster.map_shared_rank(c_keys + rank * 32 + lane, 0) = list;
+        if (warp == 0 && lane < C) {
+            *cluster.map_shared_rank(c_stat + rank, lane) = c;
+            *cluster.map_shared_rank(c_tau + rank, lane) = tau;
         }
-        cluster.sync();                                        // every push into CTA 0 has landed
-        if (rank != 0) return;
-        if (a.K > 0) {
-            list = warp < C ? c_keys[warp * 32 + lane] : 0ull;
-            list = block_merge_desc(list, s_keys, C);
+        cluster.sync();
+        if (a.K > 0)
+            for (int i = 0; i < C; ++i) tau = fmaxf(tau, c_tau[i]);
+        if (warp == 0) c = reduce16(c_stat, C);
+    }
+
+    // ---- the entries at or above tau
+    const int cap = kLpCand / C;
+    if (a.K > 0) {
+        if (mine >= tau) s_who[atomicAdd(&s_m, 1)] = tid;      // (the order of the list does not matter)
+        __syncthreads();
+        const int who = s_m;
+        for (int i = warp; i < who; i += kLpWarps)
+            for_thread(r, s_who[i], rank == 0, v0, v1, [&](float v, int idx, bool there) {
+                if (there && v >= tau) {
+                    const int p = atomicAdd(&s_n, 1);
+                    if (p < cap) s_keys[p] = entry_key(v, idx);
+                }
+            });
+        __syncthreads();
+        int count = s_n;
+        if (count > cap) {                                     // ties or masks: the K first by sorted lists
+            unsigned long long list = 0;
+            for (int i = warp; i < who; i += kLpWarps)
+                for_thread(r, s_who[i], rank == 0, v0, v1, [&](float v, int idx, bool there) {
+                    const bool in = there && v >= tau;
+                    if (!__any_sync(0xffffffffu, in)) return;
+                    const unsigned long long k = in ? entry_key(v, idx) : 0ull;
+                    const unsigned long long least = __shfl_sync(0xffffffffu, list, a.K - 1);
+                    warp_insert(list, k, in && k > least);
+                });
+            list = block_merge_desc(list, s_keys, kLpWarps);
+            __syncthreads();
+            if (warp == 0) s_keys[lane] = list;
+            count = a.K;                                       // (cap >= 32 entries were there)
+            __syncthreads();
+        }
+        int total = count;
+        if (C > 1) {                                           // into CTA 0
+            if (tid < count) *cluster.map_shared_rank(c_keys + rank * cap + tid, 0) = s_keys[tid];
+            if (tid == 0) *cluster.map_shared_rank(c_n + rank, 0) = count;
+            cluster.sync();                                    // every push into CTA 0 has landed
+            if (rank != 0) return;
+            const int from = tid / cap;                        // side by side
+            int at = tid - from * cap;
+            const bool filled = at < c_n[from];
+            total = 0;
+            for (int i = 0; i < C; ++i) {
+                at += i < from ? c_n[i] : 0;
+                total += c_n[i];
+            }
+            if (filled) s_keys[at] = c_keys[tid];
+            __syncthreads();
+        }
+        // an entry's place is the number of entries before it
+        __shared__ float s_ml[2];
+        if (tid == 0) {
+            const bool none = c.m == NEG_INF;
+            s_ml[0] = none ? 0.f : c.m;
+            s_ml[1] = none ? c.S : logf(c.S);
+        }
+        __syncthreads();
+        const unsigned long long key = tid < total ? s_keys[tid] : 0ull;
+        int place = 0;
+#pragma unroll 8
+        for (int i = 0; i < total; ++i) place += s_keys[i] > key ? 1 : 0;
+        const size_t o = row * (size_t)a.K;
+        if (tid < total && place < a.K) {
+            a.top_tok[o + place] = (int32_t)~(uint32_t)key;
+            a.top_lp[o + place] = (key_value(key) - s_ml[0]) - s_ml[1];
+        }
+        if (tid >= total && tid < a.K) {                       // a row with fewer numbers than K
+            a.top_tok[o + tid] = -1;
+            a.top_lp[o + tid] = __uint_as_float(0x7FC00000u);
         }
     }
-    if (warp != 0) return;
-    Stat c = C > 1 ? c_stat[0] : s_stat[0];
-    for (int i = 1; i < (C > 1 ? C : kLpWarps); ++i) c = combine(c, C > 1 ? c_stat[i] : s_stat[i]);
-    const float NEG_INF = -__uint_as_float(0x7F800000u);
-    const bool none = c.m == NEG_INF;                          // every entry is -inf (or NaN, and then S is NaN)
-    const float ls = none ? c.S : logf(c.S);
-    const float m = none ? 0.f : c.m;
-    if (lane == 0) {
-        const int tk = a.tok[row];
-        float lp = 0.f;                                        // tokens outside the vocabulary (padding) count 0
-        if (tk >= 0 && tk < a.V) lp = (r.at(tk) - m) - ls;
-        a.logprob[row] = lp;
+    if (rank == 0 && tid == 0) {
+        const bool none = c.m == NEG_INF;                      // every entry is -inf (or NaN, and then S is NaN)
+        const float m = none ? 0.f : c.m, ls = none ? c.S : logf(c.S);
+        a.logprob[row] = in_range ? (x_tok - m) - ls : 0.f;    // tokens outside the vocabulary (padding) count 0
         if (a.entropy) {
             const float h = none ? ls : ls - kLn2 * (c.T / c.S);
             a.entropy[row] = h < 0.f ? 0.f : h;                // (rounding below 0)
         }
-    }
-    if (lane < a.K) {
-        const size_t o = row * (size_t)a.K + lane;
-        a.top_tok[o] = list > 1ull ? (int32_t)~(uint32_t)list : -1;
-        a.top_lp[o] = list > 1ull ? (key_value(list) - m) - ls : __uint_as_float(0x7FC00000u);
     }
 }
 

@@ -731,8 +731,11 @@ qv_status qv_kv4_write(const void* qkv, qv_dtype dtype, const int32_t* start, co
     QV_CHECK_DEV(count);
     QV_CHECK_DEV(block_table);
     QV_CHECK_DEV(cache);
-    cudaError_t e = qv::launch_kv4_write(qkv, dtype == QV_BF16, start, count, block_table, B, T, Hq, Hkv, D, NB, pages,
-                                         cache, stream);
+    cudaError_t e;
+    const int sms = sms_of_current_device(&e);
+    if (e != cudaSuccess) return cuda_fail(e, "device query");
+    e = qv::launch_kv4_write(qkv, dtype == QV_BF16, start, count, block_table, B, T, Hq, Hkv, D, NB, pages,
+                             cache, sms, stream);
     if (e != cudaSuccess) return cuda_fail(e, "qv_kv4_write launch");
     return ok();
 }
@@ -755,8 +758,11 @@ qv_status qv_kv4_read(const uint8_t* cache, const int32_t* start, const int32_t*
     QV_CHECK_DEV(block_table);
     QV_CHECK_DEV(k_out);
     QV_CHECK_DEV(v_out);
-    cudaError_t e = qv::launch_kv4_read(cache, start, count, block_table, B, T, Hkv, D, NB, pages, k_out, v_out,
-                                        dtype == QV_BF16, stream);
+    cudaError_t e;
+    const int sms = sms_of_current_device(&e);
+    if (e != cudaSuccess) return cuda_fail(e, "device query");
+    e = qv::launch_kv4_read(cache, start, count, block_table, B, T, Hkv, D, NB, pages, k_out, v_out,
+                            dtype == QV_BF16, sms, stream);
     if (e != cudaSuccess) return cuda_fail(e, "qv_kv4_read launch");
     return ok();
 }

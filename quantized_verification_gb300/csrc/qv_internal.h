@@ -159,10 +159,10 @@ cudaError_t read_and_clear_attn_error(unsigned* code);
 // are pages b * NB + i), count may be null (all T rows).
 cudaError_t launch_kv4_write(const void* x, bool bf16, const int32_t* start, const int32_t* count,
                              const int32_t* table, int B, int T, int Hq, int Hkv, int D, int NB, int pages,
-                             uint8_t* cache, cudaStream_t s);
+                             uint8_t* cache, int sms, cudaStream_t s);
 cudaError_t launch_kv4_read(const uint8_t* cache, const int32_t* start, const int32_t* count, const int32_t* table,
                             int B, int T, int Hkv, int D, int NB, int pages, void* k_out, void* v_out, bool bf16,
-                            cudaStream_t s);
+                            int sms, cudaStream_t s);
 size_t attention_kv4_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int NB, int sms);
 cudaError_t launch_attention_kv4(const uint16_t* qkv, const uint8_t* cache, const int32_t* table, const int32_t* len,
                                  int B, int T, int Hq, int Hkv, int D, int NB, int pages, float scale, void* out,

@@ -59,6 +59,8 @@ _lock = threading.Lock()
 def load(path: str = LIB_PATH) -> ctypes.CDLL:
     """Load libqv.so (once). Raises if it has not been built."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -126,8 +128,15 @@ def _check(status: int):
         raise QVError(status, load().qv_last_error().decode())
 
 
+# The current stream's handle without the Stream object around it (a call on a
+# few rows is bound by its host time); the public way where it is missing.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream) -> int:
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -143,7 +152,7 @@ def _ptr(t):
         raise ValueError("tensor must live on a CUDA device")
     if not t.is_contiguous():
         raise ValueError("tensor must be contiguous")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _dtype(t: torch.Tensor) -> int:
@@ -356,15 +365,23 @@ def kv4_cache(pages: int, Hkv: int, D: int, device=None) -> torch.Tensor:
 def _kv4_shapes(cache, block_table, B):
     """Hkv, D, NB and pages of a cache and of its block table (None: sequence
     b's blocks are pages b * NB + i, with the pool divided evenly)."""
-    _need(cache.dtype == torch.uint8 and cache.dim() == 3 and cache.shape[2] % 34 == 0,
-          "cache must be uint8 [pages, Hkv, 34 * D]")
-    pages, Hkv, D = cache.shape[0], cache.shape[1], cache.shape[2] // 34
+    pages, Hkv, rec = cache.shape
+    if cache.dtype != torch.uint8 or rec % 34 != 0:
+        raise ValueError("cache must be uint8 [pages, Hkv, 34 * D]")
     if block_table is None:
-        _need(B > 0 and pages % B == 0, "without a block table the cache must hold the same number of pages per sequence")
-        return Hkv, D, pages // B, pages
-    _need(block_table.dtype == torch.int32 and block_table.dim() == 2 and block_table.shape[0] == B,
-          "block_table must be int32 [B, NB]")
-    return Hkv, D, block_table.shape[1], pages
+        if B < 1 or pages % B != 0:
+            raise ValueError("without a block table the cache must hold the same number of pages per sequence")
+        return Hkv, rec // 34, pages // B, pages
+    n, NB = block_table.shape
+    if n != B or block_table.dtype != torch.int32:
+        raise ValueError("block_table must be int32 [B, NB]")
+    return Hkv, rec // 34, NB, pages
+
+
+def _per_seq(t, B, name):
+    if t is not None and (t.shape != (B,) or t.dtype != torch.int32):
+        raise ValueError(f"{name} must be int32 [B]")
+    return _ptr(t)
 
 
 def qv_kv4_write(qkv, start, cache, T, Hq, Hkv, block_table=None, count=None, stream=None):
@@ -373,13 +390,12 @@ def qv_kv4_write(qkv, start, cache, T, Hq, Hkv, block_table=None, count=None, st
     j < count[b] (all T rows when count is None)."""
     B = start.shape[0]
     hkv, D, NB, pages = _kv4_shapes(cache, block_table, B)
-    _need(hkv == Hkv, "cache must have Hkv heads")
-    _need(qkv.shape == (B * T, (Hq + 2 * Hkv) * D), "qkv must be [B*T, (Hq+2Hkv)*D]")
-    _need(start.shape == (B,) and start.dtype == torch.int32, "start int32 [B]")
-    if count is not None:
-        _need(count.shape == (B,) and count.dtype == torch.int32, "count int32 [B]")
-    _check(load().qv_kv4_write(_ptr(qkv), _dtype(qkv), _ptr(start), _ptr(count), _ptr(block_table), B, T, Hq, Hkv, D,
-                               NB, pages, _ptr(cache), ctypes.c_void_p(_stream(stream))))
+    if hkv != Hkv:
+        raise ValueError("cache must have Hkv heads")
+    if qkv.shape != (B * T, (Hq + 2 * Hkv) * D):
+        raise ValueError("qkv must be [B*T, (Hq+2Hkv)*D]")
+    _check(load().qv_kv4_write(_ptr(qkv), _dtype(qkv), _per_seq(start, B, "start"), _per_seq(count, B, "count"),
+                               _ptr(block_table), B, T, Hq, Hkv, D, NB, pages, _ptr(cache), _stream(stream)))
 
 
 def qv_kv4_read(cache, start, k_out, v_out, block_table=None, count=None, stream=None):
@@ -388,13 +404,10 @@ def qv_kv4_read(cache, start, k_out, v_out, block_table=None, count=None, stream
     rows are left as they were."""
     B, T, hkv, d = k_out.shape
     Hkv, D, NB, pages = _kv4_shapes(cache, block_table, B)
-    _need((hkv, d) == (Hkv, D) and v_out.shape == k_out.shape and v_out.dtype == k_out.dtype,
-          "k_out, v_out must be [B, T, Hkv, D] of one dtype")
-    _need(start.shape == (B,) and start.dtype == torch.int32, "start int32 [B]")
-    if count is not None:
-        _need(count.shape == (B,) and count.dtype == torch.int32, "count int32 [B]")
-    _check(load().qv_kv4_read(_ptr(cache), _ptr(start), _ptr(count), _ptr(block_table), B, T, Hkv, D, NB, pages,
-                              _ptr(k_out), _ptr(v_out), _dtype(k_out), ctypes.c_void_p(_stream(stream))))
+    if hkv != Hkv or d != D or v_out.shape != k_out.shape or v_out.dtype != k_out.dtype:
+        raise ValueError("k_out, v_out must be [B, T, Hkv, D] of one dtype")
+    _check(load().qv_kv4_read(_ptr(cache), _per_seq(start, B, "start"), _per_seq(count, B, "count"), _ptr(block_table),
+                              B, T, Hkv, D, NB, pages, _ptr(k_out), _ptr(v_out), _dtype(k_out), _stream(stream)))
 
 
 def qv_attention_kv4_workspace_bytes(B, T, Hq, Hkv, D, NB) -> int:
@@ -408,15 +421,24 @@ def qv_attention_verify_kv4(qkv, cache, cache_len, T, Hq, Hkv, scale, out, works
     zero before its first use (they are left zero)."""
     B = cache_len.shape[0]
     hkv, D, NB, pages = _kv4_shapes(cache, block_table, B)
-    _need(hkv == Hkv, "cache must have Hkv heads")
-    _need(qkv.dtype == torch.bfloat16 and qkv.shape == (B * T, (Hq + 2 * Hkv) * D), "qkv bf16 [B*T, (Hq+2Hkv)*D]")
-    _need(cache_len.shape == (B,) and cache_len.dtype == torch.int32, "cache_len int32 [B]")
-    _need(out.shape == (B * T, Hq * D), "out [B*T, Hq*D]")
-    _need(workspace.dtype == torch.uint8, "workspace must be a uint8 tensor")
+    if hkv != Hkv:
+        raise ValueError("cache must have Hkv heads")
+    if qkv.dtype != torch.bfloat16 or qkv.shape != (B * T, (Hq + 2 * Hkv) * D):
+        raise ValueError("qkv must be bf16 [B*T, (Hq+2Hkv)*D]")
+    if out.shape != (B * T, Hq * D):
+        raise ValueError("out must be [B*T, Hq*D]")
+    if workspace.dtype != torch.uint8:
+        raise ValueError("workspace must be a uint8 tensor")
     _check(load().qv_attention_verify_kv4(_ptr(qkv), _ptr(cache) if NB > 0 and pages > 0 else None,
-                                          _ptr(block_table) if NB > 0 else None, _ptr(cache_len), B, T, Hq, Hkv, D,
-                                          NB, pages, ctypes.c_float(scale), _ptr(out), _dtype(out), _ptr(workspace),
-                                          workspace.numel(), ctypes.c_void_p(_stream(stream))))
+                                          _ptr(block_table) if NB > 0 else None, _per_seq(cache_len, B, "cache_len"),
+                                          B, T, Hq, Hkv, D, NB, pages, scale, _ptr(out), _dtype(out), _ptr(workspace),
+                                          workspace.numel(), _stream(stream)))
+
+
+def _per_row(t, M, dtype, name):
+    if t is not None and (t.shape != (M,) or t.dtype != dtype):
+        raise ValueError(f"{name} must be {dtype} [M]")
+    return _ptr(t)
 
 
 def qv_token_logprobs(logits, tokens, logprob, entropy=None, top_tokens=None, top_logprobs=None, stream=None):
@@ -424,21 +446,19 @@ def qv_token_logprobs(logits, tokens, logprob, entropy=None, top_tokens=None, to
     int32, entropy [M] (optional), and the most probable tokens top_tokens
     [M, K] int32 with top_logprobs [M, K] (optional, together)."""
     M, V = logits.shape
-    _need(tokens.shape == (M,) and tokens.dtype == torch.int32, "tokens int32 [M]")
-    _need(logprob.shape == (M,) and logprob.dtype == torch.float32, "logprob float32 [M]")
-    if entropy is not None:
-        _need(entropy.shape == (M,) and entropy.dtype == torch.float32, "entropy float32 [M]")
-    _need((top_tokens is None) == (top_logprobs is None), "top_tokens and top_logprobs go together")
     K = 0
-    if top_tokens is not None:
-        _need(top_tokens.dim() == 2 and top_tokens.shape[0] == M and top_tokens.dtype == torch.int32,
-              "top_tokens int32 [M, K]")
-        _need(top_logprobs.shape == top_tokens.shape and top_logprobs.dtype == torch.float32,
-              "top_logprobs float32 [M, K]")
-        K = top_tokens.shape[1]
-    _check(load().qv_token_logprobs(_ptr(logits), _dtype(logits), _ptr(tokens), M, V, K, _ptr(logprob), _ptr(entropy),
-                                    _ptr(top_tokens) if K else None, _ptr(top_logprobs) if K else None,
-                                    ctypes.c_void_p(_stream(stream))))
+    if top_tokens is not None or top_logprobs is not None:
+        if top_tokens is None or top_logprobs is None:
+            raise ValueError("top_tokens and top_logprobs go together")
+        m, K = top_tokens.shape
+        if m != M or top_tokens.dtype != torch.int32:
+            raise ValueError("top_tokens must be int32 [M, K]")
+        if top_logprobs.shape != (M, K) or top_logprobs.dtype != torch.float32:
+            raise ValueError("top_logprobs must be float32 [M, K]")
+    _check(load().qv_token_logprobs(_ptr(logits), _dtype(logits), _per_row(tokens, M, torch.int32, "tokens"), M, V, K,
+                                    _per_row(logprob, M, torch.float32, "logprob"),
+                                    _per_row(entropy, M, torch.float32, "entropy"), _ptr(top_tokens) if K else None,
+                                    _ptr(top_logprobs) if K else None, _stream(stream)))
 
 
 # --- W4A8: packed int4 weights [N, K/2] uint8 (even k in the low nibble) ---
