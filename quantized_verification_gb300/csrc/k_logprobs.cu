@@ -11,15 +11,16 @@
 // rescales them when its m grows by d: S *= 2^-d, T = 2^-d (T - d S). The
 // alternatives cost the pass nothing more: m is also the thread's largest
 // logit. Of the two largest maxima of each of the 16 warps the K-th largest,
-// tau, is a lower bound of the row's K-th largest logit, and few more than K
-// threads reach it. Only those threads' entries (1/512 of the slice each) are
-// read again, from L2, and the entries at or above tau are ordered by counting,
-// for each, those before it (by value, then by the lower index). Where ties or
+// tau, is a lower bound of the K-th largest logit, and few more than K threads
+// reach it. Only those threads' entries (1/512 of the slice each) are read
+// again, from L2, and the entries at or above tau are ordered by counting, for
+// each, those before it (by value, then by the lower index). Where ties or
 // masks leave too many of them, warps keep sorted lists of 32 instead.
 //
 // A row is the work of one CTA, or of a cluster of C of them that split it
-// (launch_token_logprobs) and combine through distributed shared memory: the
-// statistics and the largest tau, then the entries.
+// (launch_token_logprobs): each sends its statistics, its entries at or above
+// its own tau and its largest maxima to the first, which takes a tau of the
+// whole row from the latter before it counts. One cluster barrier in all.
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -41,8 +42,9 @@ constexpr int kLpMaxCluster = 16;
 constexpr int kLpUnroll = 4;                    // vectors in flight per thread
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kLpCand = 512;                    // entries of a row ordered by counting, kLpCand / C of a CTA
-static_assert(kLpCand / kLpMaxCluster >= 32 && kLpCand <= kLpThreads, "a CTA's K entries fit, one thread an entry");
+constexpr int kLpCand = 1024;                   // entries of a row ordered by counting, kLpCand / kLpMaxCluster of a CTA
+constexpr int kLpTops = 64;                     // maxima of a row that the CTAs of a cluster send, kLpTops / C each
+static_assert(kLpCand / kLpMaxCluster >= 32 && kLpCand >= kLpWarps * 32, "a CTA's K entries and the warps' lists fit");
 
 struct LpArgs {
     const uint8_t* x;          // logits [M][V]
@@ -227,14 +229,16 @@ template <bool BF16>
 __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const LpArgs a) {
     constexpr int E = Row<BF16>::E;
     __shared__ Stat s_stat[kLpWarps];
-    __shared__ Stat c_stat[kLpMaxCluster];                     // one per CTA of the row, in every CTA
-    __shared__ float c_tau[kLpMaxCluster];
-    __shared__ unsigned long long c_keys[kLpCand];             // entries of the row (in CTA 0), `cap` places per CTA
+    // written by every CTA of the row (in its first CTA)
+    __shared__ Stat c_stat[kLpMaxCluster];
+    __shared__ float c_top[kLpTops];
+    __shared__ unsigned long long c_keys[kLpCand];
     __shared__ int c_n[kLpMaxCluster];
-    __shared__ unsigned long long s_keys[kLpCand];             // this CTA's entries, or the warps' lists
-    __shared__ float s_top[32];
+    __shared__ unsigned long long s_keys[kLpCand];             // entries, or the warps' lists
+    __shared__ float s_top[32], s_sorted[32];
     __shared__ int s_who[kLpThreads];
     __shared__ int s_n, s_m;
+    __shared__ float s_tau, s_max, s_ls;
     cg::cluster_group cluster = cg::this_cluster();
     const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
     if (C > 1) cluster_arrive_relaxed();                       // waited for before the first store into another CTA
@@ -249,15 +253,16 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const LpA
     const int v0 = min(r.nvec, rank * per), v1 = min(r.nvec, v0 + per);
     if (tid == 0) s_n = s_m = 0;
     // the given token's logit, early: its two loads hide behind the pass
-    const int tok = rank == 0 && tid == 0 ? a.tok[row] : -1;
+    const int tok = rank == 0 && tid == kLpThreads - 32 ? a.tok[row] : -1;
     const bool in_range = tok >= 0 && tok < a.V;
     const float x_tok = in_range ? r.at(tok) : 0.f;
 
     // ---- the pass
     Stat st = {NEG_INF, 0.f, 0.f};
     const int own1 = rank == 0 ? r.single(tid) : -1;
+    const float x_own = own1 >= 0 ? r.at(own1) : 0.f;
     if (own1 >= 0) {
-        const float v[1] = {r.at(own1)};
+        const float v[1] = {x_own};
         add_entries(st, v);
     }
     int n = v0 + tid;
@@ -310,47 +315,55 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const LpA
         }
         return c;
     };
-    float tau = NEG_INF;
-    if (a.K > 0) {                                             // the K-th largest of the 32 maxima
-        const float v = s_top[lane];
+    // The place of p[i] among N numbers (N / 512 threads a number, all of which
+    // get it); ties by the index.
+    auto place_of = [&](const float* p, int N, int& i) {
+        const int G = kLpThreads / N;                          // threads a number
+        i = tid / G;
+        const float v = p[i];
         int before = 0;
-#pragma unroll
-        for (int j = 0; j < 32; ++j) {
-            const float o = __shfl_sync(0xffffffffu, v, j);
-            before += (o > v || (o == v && j < lane)) ? 1 : 0;
-        }
-        tau = __shfl_sync(0xffffffffu, v, __ffs(__ballot_sync(0xffffffffu, before == a.K - 1)) - 1);
-    }
+        for (int j = tid % G; j < N; j += G) before += (p[j] > v || (p[j] == v && j < i)) ? 1 : 0;
+        for (int off = 1; off < G; off <<= 1) before += __shfl_xor_sync(0xffffffffu, before, off);
+        return before;
+    };
     Stat c = {NEG_INF, 0.f, 0.f};
-    if (warp == 0) c = reduce16(s_stat, kLpWarps);
-    if (C > 1) {
-        cluster_wait();                                        // every CTA of the cluster has started
-        if (warp == 0 && lane < C) {
-            *cluster.map_shared_rank(c_stat + rank, lane) = c;
-            *cluster.map_shared_rank(c_tau + rank, lane) = tau;
-        }
-        cluster.sync();
-        if (a.K > 0)
-            for (int i = 0; i < C; ++i) tau = fmaxf(tau, c_tau[i]);
-        if (warp == 0) c = reduce16(c_stat, C);
-    }
-
-    // ---- the entries at or above tau
-    const int cap = kLpCand / C;
+    if (warp == kLpWarps - 1) c = reduce16(s_stat, kLpWarps);  // (warp 15, lane 0 finishes a row of one CTA)
+    int total = 0;
     if (a.K > 0) {
-        if (mine >= tau) s_who[atomicAdd(&s_m, 1)] = tid;      // (the order of the list does not matter)
+        {
+            int i;
+            const int place = place_of(s_top, 32, i);
+            if (tid % (kLpThreads / 32) == 0) s_sorted[place] = s_top[i];
+        }
         __syncthreads();
-        const int who = s_m;
-        for (int i = warp; i < who; i += kLpWarps)
-            for_thread(r, s_who[i], rank == 0, v0, v1, [&](float v, int idx, bool there) {
-                if (there && v >= tau) {
+        const float tau = s_sorted[a.K - 1];
+
+        // ---- the entries at or above tau
+        const int cap = C > 1 ? kLpCand / kLpMaxCluster : kLpCand;
+        if (mine >= tau) {
+            s_who[atomicAdd(&s_m, 1)] = tid;                   // (the order of the list does not matter)
+            if (own1 >= 0 && x_own >= tau) {
+                const int p = atomicAdd(&s_n, 1);
+                if (p < cap) s_keys[p] = entry_key(x_own, own1);
+            }
+        }
+        __syncthreads();
+        const int who = s_m, each = (v1 - v0 + kLpThreads - 1) / kLpThreads;   // vectors of a thread
+        for (int i = tid; i < who * each; i += kLpThreads) {
+            const int f = i / each, vn = v0 + s_who[f] + (i - f * each) * kLpThreads;
+            if (vn >= v1) continue;
+            float v[E];
+            Row<BF16>::unpack(r.vec(vn), v);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (v[e] >= tau) {
                     const int p = atomicAdd(&s_n, 1);
-                    if (p < cap) s_keys[p] = entry_key(v, idx);
+                    if (p < cap) s_keys[p] = entry_key(v[e], r.head + vn * E + e);
                 }
-            });
+        }
         __syncthreads();
-        int count = s_n;
-        if (count > cap) {                                     // ties or masks: the K first by sorted lists
+        total = s_n;
+        if (total > cap) {                                     // ties or masks: the K first by sorted lists
             unsigned long long list = 0;
             for (int i = warp; i < who; i += kLpWarps)
                 for_thread(r, s_who[i], rank == 0, v0, v1, [&](float v, int idx, bool there) {
@@ -363,56 +376,61 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const LpA
             list = block_merge_desc(list, s_keys, kLpWarps);
             __syncthreads();
             if (warp == 0) s_keys[lane] = list;
-            count = a.K;                                       // (cap >= 32 entries were there)
+            total = a.K;                                       // (cap >= 32 entries were there)
             __syncthreads();
         }
-        int total = count;
-        if (C > 1) {                                           // into CTA 0
-            if (tid < count) *cluster.map_shared_rank(c_keys + rank * cap + tid, 0) = s_keys[tid];
-            if (tid == 0) *cluster.map_shared_rank(c_n + rank, 0) = count;
-            cluster.sync();                                    // every push into CTA 0 has landed
-            if (rank != 0) return;
-            const int from = tid / cap;                        // side by side
-            int at = tid - from * cap;
-            const bool filled = at < c_n[from];
-            total = 0;
-            for (int i = 0; i < C; ++i) {
-                at += i < from ? c_n[i] : 0;
-                total += c_n[i];
-            }
-            if (filled) s_keys[at] = c_keys[tid];
+    }
+    if (C > 1) {                                               // into the first CTA
+        cluster_wait();                                        // every CTA of the cluster has started
+        const int part = kLpCand / kLpMaxCluster, tops = kLpTops / C;
+        if (tid == kLpThreads - 32) *cluster.map_shared_rank(c_stat + rank, 0) = c;
+        if (a.K > 0) {
+            if (tid < total) *cluster.map_shared_rank(c_keys + rank * part + tid, 0) = s_keys[tid];
+            if (tid >= 64 && tid < 64 + tops) *cluster.map_shared_rank(c_top + rank * tops + tid - 64, 0) = s_sorted[tid - 64];
+            if (tid == 0) *cluster.map_shared_rank(c_n + rank, 0) = total;
+        }
+        cluster.sync();                                        // every push has landed
+        if (rank != 0) return;
+        if (warp == kLpWarps - 1) c = reduce16(c_stat, C);
+        if (a.K > 0) {
+            int i;
+            const int place = place_of(c_top, kLpTops, i);
+            if (place == a.K - 1 && tid % (kLpThreads / kLpTops) == 0) s_tau = c_top[i];
+            if (tid == 0) s_n = 0;
             __syncthreads();
+            const unsigned long long least = entry_key(s_tau, 0x7FFFFFFF);
+            for (int e = tid; e < C * part; e += kLpThreads)
+                if (e % part < c_n[e / part] && c_keys[e] >= least) s_keys[atomicAdd(&s_n, 1)] = c_keys[e];
         }
-        // an entry's place is the number of entries before it
-        __shared__ float s_ml[2];
-        if (tid == 0) {
-            const bool none = c.m == NEG_INF;
-            s_ml[0] = none ? 0.f : c.m;
-            s_ml[1] = none ? c.S : logf(c.S);
+    }
+    if (tid == kLpThreads - 32) {
+        const bool none = c.m == NEG_INF;                      // every entry is -inf (or NaN, and then S is NaN)
+        s_max = none ? 0.f : c.m;
+        s_ls = none ? c.S : logf(c.S);
+        a.logprob[row] = in_range ? (x_tok - s_max) - s_ls : 0.f;   // tokens outside the vocabulary (padding) count 0
+        if (a.entropy) {
+            const float h = none ? s_ls : s_ls - kLn2 * (c.T / c.S);
+            a.entropy[row] = h < 0.f ? 0.f : h;                // (rounding below 0)
         }
-        __syncthreads();
-        const unsigned long long key = tid < total ? s_keys[tid] : 0ull;
+    }
+    if (a.K == 0) return;
+    __syncthreads();
+    if (C > 1) total = s_n;
+    // ---- an entry's place is the number of entries before it
+    const size_t o = row * (size_t)a.K;
+    for (int e = tid; e < total; e += kLpThreads) {
+        const unsigned long long key = s_keys[e];
         int place = 0;
 #pragma unroll 8
         for (int i = 0; i < total; ++i) place += s_keys[i] > key ? 1 : 0;
-        const size_t o = row * (size_t)a.K;
-        if (tid < total && place < a.K) {
+        if (place < a.K) {
             a.top_tok[o + place] = (int32_t)~(uint32_t)key;
-            a.top_lp[o + place] = (key_value(key) - s_ml[0]) - s_ml[1];
-        }
-        if (tid >= total && tid < a.K) {                       // a row with fewer numbers than K
-            a.top_tok[o + tid] = -1;
-            a.top_lp[o + tid] = __uint_as_float(0x7FC00000u);
+            a.top_lp[o + place] = (key_value(key) - s_max) - s_ls;
         }
     }
-    if (rank == 0 && tid == 0) {
-        const bool none = c.m == NEG_INF;                      // every entry is -inf (or NaN, and then S is NaN)
-        const float m = none ? 0.f : c.m, ls = none ? c.S : logf(c.S);
-        a.logprob[row] = in_range ? (x_tok - m) - ls : 0.f;    // tokens outside the vocabulary (padding) count 0
-        if (a.entropy) {
-            const float h = none ? ls : ls - kLn2 * (c.T / c.S);
-            a.entropy[row] = h < 0.f ? 0.f : h;                // (rounding below 0)
-        }
+    if (tid >= total && tid < a.K) {                           // a row with fewer numbers than K
+        a.top_tok[o + tid] = -1;
+        a.top_lp[o + tid] = __uint_as_float(0x7FC00000u);
     }
 }
 
