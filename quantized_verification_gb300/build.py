@@ -36,7 +36,7 @@ NVCC_FLAGS = ARCH + [
 # equal the oracle's bit for bit, so no expression there may be contracted
 # (explicit fused operations, where the definition has one, are written as
 # such).
-FMA_CONTRACTION_OK = {"k_attn.cu", "k_attn_kv4.cu", "k_fidelity.cu", "k_logprobs.cu"}
+FMA_CONTRACTION_OK = {"k_attn.cu", "k_attn_kv4.cu", "k_attn_kv4_tc.cu", "k_fidelity.cu", "k_logprobs.cu"}
 
 
 def flags_for(src: str) -> list[str]:

@@ -1,0 +1,654 @@
+// k_attn_kv4_tc.cu -- attention over the 4-bit paged KV cache for heads of 128
+// values, on the tcgen05 tensor cores.
+//
+//   What is computed, the cut of the work into tiles, units and places, and the
+//   arithmetic (exact unpacking, base-2 probabilities with a lazy whole-number
+//   maximum, two f16 parts of P for fp32 outputs) are k_attn_kv4.cu's; only the
+//   products are formed elsewhere. On mma.sync the 20 query rows of a 5-token
+//   step kept the legacy tensor pipe busy about as long as the unpacking the
+//   ALUs, with too few warps to overlap the two (137 us for one step of 5 tokens
+//   over 2 x 131071 positions; 42 us to read the cache).
+//
+// A CTA takes 128 positions (4 records) at a time, all 256 threads together:
+//   1. unpacks the keys (thread = position, half the dims) to bf16 pairs and
+//      stores them as the A operand in tensor memory;
+//   2. S^T = K Q^T: 8 tcgen05.mma, M = 128 positions, N = the query rows padded
+//      to 16 or 32, B = Q in shared memory;
+//   3. meanwhile unpacks the values to f16 (times 2^-6) into shared memory, as
+//      the M-major A operand of the second product (rows of positions, 128-byte
+//      swizzle; the unpacked order of 8 dims is just an order of output rows);
+//   4. softmax: thread = position, for the rows of every other n8 tile. The
+//      maxima of the rows belong to the CTA; whether one has to move is one
+//      vote in the barrier that is needed anyway;
+//   5. O^T += V^T P^T: 8 tcgen05.mma, M = 128 dims, N = the rows' first parts
+//      side by side with their second parts, accumulated in tensor memory; it
+//      runs while the next keys are unpacked.
+// Two CTAs share an SM, so that one's barriers fall into the other's work. The
+// step's own keys and values are few and are not of the cache's format: they
+// are attended to with plain fp32 arithmetic while the first records load, and
+// merged at the end.
+
+#include "attn_kv4_common.cuh"
+
+namespace qv {
+
+__device__ unsigned int g_attn_kv4_tc_error;
+
+namespace {
+
+using namespace kv4attn;
+
+constexpr int kTcThreads = 256;
+constexpr int kTcKeys = 128;                    // positions per step: 4 records
+constexpr int kTcStages = 3;
+constexpr int D = 128;
+
+template <int NR, bool OUTBF>
+struct TcLayout {
+    using Rec = Kv4Rec<D>;
+    static constexpr int RW = NR * 8;
+    static constexpr int NS = (RW + 15) / 16 * 16;        // columns of S
+    static constexpr int NO = OUTBF ? NS : 2 * RW;        // columns of O: first parts, then second parts
+    static constexpr int V = 0;                           // [2 halves][128 positions][128 B], and the own scores
+    static constexpr int P = V + 2 * kTcKeys * 128;       // [128 positions][128 B]
+    static constexpr int Q = P + kTcKeys * 128;           // [2 halves][NS rows][128 B]
+    static constexpr int Ring = Q + 2 * 32 * 128;
+    static constexpr int Bar = Ring + kTcStages * 4 * Rec::Bytes;   // full [stages], S done, O done
+    static constexpr int Cnt = Bar + (kTcStages + 3) * 8; // cached positions per record [stages][4]
+    static constexpr int Row = Cnt + kTcStages * 16;      // floats per row: c, limit, f, own m, own l, w1, w2, M, l
+    static constexpr int Red = Row + 9 * 32 * 4;          // [4][32]
+    static constexpr int Scan = Red + 4 * 32 * 4;
+    static constexpr int Misc = Scan + 16 * 4;
+    static constexpr int Bytes = Misc + 32;
+    static constexpr int Alloc = Bytes + 1024;            // slack to align the base to 1024 B
+    static constexpr int Slot = RW * D + 2 * RW;          // floats of a partial result: [row][lane], m, l
+    static constexpr int kK = 0, kS = 64, kO = 96;        // tensor memory columns
+    static constexpr int Cols = 256;
+    static_assert(Bar % 8 == 0 && Row % 16 == 0 && Ring % 16 == 0, "alignment");
+    static_assert(kRowTile * QV_ATTN_MAX_T * 4 <= 2 * kTcKeys * 128, "the own scores fit the value buffer");
+};
+
+// Shared-memory descriptor of an operand stored with the M (or N) dimension
+// contiguous: atoms of 64 16-bit elements x 8 k rows (128-byte swizzle), the
+// next 8 k rows 1024 bytes on, the next 64 elements `mn_stride` bytes on.
+__device__ __forceinline__ uint64_t sw128_mnmajor_desc(uint32_t saddr, uint32_t mn_stride) {
+    uint64_t d = 0;
+    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
+    d |= (uint64_t)(mn_stride >> 4) << 16;
+    d |= (uint64_t)(1024u >> 4) << 32;
+    d |= (uint64_t)1u << 46;
+    d |= (uint64_t)2u << 61;
+    return d;
+}
+// Instruction descriptor of kind::f16, M = 128, f32 accumulator. fmt: 0 f16, 1
+// bf16 (both operands); mn: both operands M/N-major instead of K-major.
+__host__ __device__ constexpr uint32_t idesc(int fmt, int N, bool mn) {
+    return (1u << 4) | ((uint32_t)fmt << 7) | ((uint32_t)fmt << 10) | (mn ? (1u << 15) | (1u << 16) : 0u) |
+           ((uint32_t)(N >> 3) << 17) | ((uint32_t)(128 >> 4) << 24);
+}
+// D[tmem] (+)= A[smem] * B[smem], one K = 16 step, issued by one thread.
+__device__ __forceinline__ void umma_f16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t id,
+                                            uint32_t accumulate) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(id), "r"(accumulate) : "memory");
+}
+__device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 :: "r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+
+template <int NR, bool OUTBF>
+__global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a, int tile_cost, int min_units) {
+    using Ly = TcLayout<NR, OUTBF>;
+    using Rec = Kv4Rec<D>;
+    constexpr int RW = Ly::RW, NT = (NR + 1) / 2;                // n8 tiles of a thread: hf, hf + 2
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    const uint32_t sbase = smem_u32(smem);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int q4 = warp & 3, hf = warp >> 2;                     // record (tensor memory lanes 32 q4 ..), half
+    const int key = 32 * q4 + lane;                              // this thread's position, and its lane of O
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + Ly::Bar);
+    uint64_t* bar_s = full + kTcStages;
+    uint64_t* bar_o = bar_s + 1;
+    volatile int* cnt = reinterpret_cast<volatile int*>(smem + Ly::Cnt);
+    float* s_c = reinterpret_cast<float*>(smem + Ly::Row);       // p = 2^(sl2 x + c), c = kBias - m
+    float* s_lim = s_c + 32;                                     // the product at which m moves
+    float* s_f = s_c + 64;
+    float* s_m2 = s_c + 96;
+    float* s_l2 = s_c + 128;
+    float* s_w1 = s_c + 160;
+    float* s_w2 = s_c + 192;
+    float* s_M = s_c + 224;
+    float* s_L = s_c + 256;
+    float* s_red = reinterpret_cast<float*>(smem + Ly::Red);
+    unsigned* s_scan = reinterpret_cast<unsigned*>(smem + Ly::Scan);
+    volatile int* abort = reinterpret_cast<volatile int*>(smem + Ly::Misc);
+    uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + Ly::Misc) + 1;
+    int* s_flag = reinterpret_cast<int*>(smem + Ly::Misc) + 2;
+    float* s_own = reinterpret_cast<float*>(smem + Ly::V);       // [R][T] own scores, before the first values
+    const float NEG_INF = -__uint_as_float(0x7F800000u);
+
+    // Tensor memory before dependents may start: one of theirs that held it
+    // while it waited for this grid would never let it go.
+    if (warp == 0) {
+        tmem_alloc(s_tmem, Ly::Cols);
+        tmem_relinquish();
+    }
+    if (tid == 32) {
+        for (int s = 0; s < kTcStages + 2; ++s) mbar_init(&full[s], 1);
+        *abort = 0;
+        fence_barrier_init();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *s_tmem;
+    const uint32_t tlane = tmem + ((uint32_t)(32 * q4) << 16);   // this warp's lanes
+    allow_dependent_launch();
+    grid_dependency_wait();
+
+    const int own_units = (a.T + 31) / 32, tps = a.Hkv * a.RT;
+    const float sl2 = a.scale * kLog2e;
+    const size_t rowlen = (size_t)(a.Hq + 2 * a.Hkv) * D;
+    uint32_t c4 = 4u, c8 = 8u, c64 = 64u;                        // multipliers the compiler may not turn into shifts
+    asm volatile("" : "+r"(c4), "+r"(c8), "+r"(c64));
+    unsigned steps_issued = 0, steps = 0;                        // 128-position steps requested / begun so far
+    Range rg;
+    bool work = find_range<kTcThreads>(a, own_units, tile_cost, min_units, s_scan, rg);
+    const unsigned per = rg.per, u1 = work ? rg.u1 : 0;
+    unsigned seq_at = rg.seq_at, u = work ? rg.u0 : 0;
+    int b_next = rg.b;
+
+    while (u < u1) {
+        // ---- the tile that place u belongs to, and this CTA's part [ua, ub) of it
+        const int b = b_next;
+        const int L = seq_len(a, b);
+        const int nc = (L + kKv4Block - 1) / kKv4Block, nu = nc + own_units;
+        const unsigned places = (unsigned)(nu + tile_cost);
+        const int ti = (int)((u - seq_at) / places);
+        const unsigned tile_at = seq_at + (unsigned)ti * places;
+        const int kh = ti / a.RT, rt = ti - kh * a.RT;
+        const int ua = (int)(u - tile_at), ub = (int)min((unsigned)(nc + 1), u1 - tile_at);   // (the own rows are one piece)
+        u = tile_at + places;                                    // where this CTA goes on
+        if (ti == tps - 1) {
+            seq_at = u;
+            ++b_next;
+        }
+        if (ua > nc) continue;                                   // (nothing but empty places)
+        const int r0 = rt * a.rows, R = min(a.rows, a.T * a.G - r0);   // query rows of this tile
+        const bool own = ub > nc;
+        const int last = min(ub, nc), nsteps = ua < last ? (last - ua + 3) / 4 : 0;
+
+        // ---- records: lane i of warp 0 requests record i of a step
+        int unit = ua + lane;                                    // its next unit, and that unit's page
+        auto page_of = [&](int x) {
+            return x >= last ? -1 : (a.table ? a.table[(size_t)b * a.NB + x] : b * a.NB + x);
+        };
+        int page = warp == 0 && lane < 4 ? page_of(unit) : -1;
+        int to_issue = nsteps;
+        auto issue = [&]() {                                     // warp 0
+            if (to_issue == 0) return;
+            --to_issue;
+            const int s = steps_issued % kTcStages;
+            const bool there = lane < 4 && unit < last && (unsigned)page < (unsigned)a.pages;
+            if (lane < 4) cnt[4 * s + lane] = there ? min(kKv4Block, L - unit * kKv4Block) : 0;
+            const unsigned who = __ballot_sync(0xffffffffu, there);
+            if (lane == 0 && !a.hold) {
+                if (who) mbar_arrive_expect_tx(&full[s], (unsigned)__popc(who) * Rec::Bytes);
+                else mbar_arrive(&full[s]);
+            }
+            __syncwarp();
+            if (there && !a.hold)
+                bulk_load(sbase + (uint32_t)(Ly::Ring + (4 * s + lane) * Rec::Bytes),
+                          a.cache + ((size_t)page * a.Hkv + kh) * Rec::Bytes, Rec::Bytes, &full[s]);
+            ++steps_issued;
+            unit += 4;
+            if (lane < 4) page = page_of(unit);
+        };
+        if (warp == 0)
+            for (int s = 0; s < kTcStages; ++s) issue();
+
+        // ---- Q, rows of 128-byte halves; 8 dims in the order 0 4 1 5 2 6 3 7
+        for (int e = tid; e < Ly::NS * 16; e += kTcThreads) {
+            const int n = e >> 4, ch = e & 15;
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            if (n < R) {
+                const int j = (r0 + n) / a.G, h = kh * a.G + (r0 + n) - j * a.G;
+                x = *reinterpret_cast<const uint4*>(a.qkv + ((size_t)b * a.T + j) * rowlen + (size_t)h * D + 8 * ch);
+            }
+            sts_v4_u32(sbase + (uint32_t)(Ly::Q + (ch >> 3) * Ly::NS * 128 + n * 128 + (((ch & 7) ^ (n & 7)) << 4)),
+                       __byte_perm(x.x, x.z, 0x5410), __byte_perm(x.x, x.z, 0x7632), __byte_perm(x.y, x.w, 0x5410),
+                       __byte_perm(x.y, x.w, 0x7632));
+        }
+        if (tid < 32) {
+            s_c[tid] = 0.f;
+            s_lim[tid] = NEG_INF;
+            s_m2[tid] = NEG_INF;
+            s_l2[tid] = 0.f;
+        }
+        float l[NT][8], o2[NT][8];                               // this position's sums; this dim's own-row outputs
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) l[t][i] = o2[t][i] = 0.f;
+        const int dim = (key & ~7) + ((key & 1) << 2) + ((key & 7) >> 1);   // the dim of O's lane `key`
+
+        // ---- the step's own rows, in fp32
+        if (own) {
+            const uint16_t* kb = a.qkv + (size_t)b * a.T * rowlen + (size_t)(a.Hq + kh) * D;
+            for (int e = tid; e < R * a.T; e += kTcThreads) {
+                const int r = e / a.T, j = e - r * a.T, tk = (r0 + r) / a.G;
+                float x = NEG_INF;
+                if (j <= tk) {
+                    const int h = kh * a.G + (r0 + r) - tk * a.G;
+                    const uint4* qp = reinterpret_cast<const uint4*>(a.qkv + ((size_t)b * a.T + tk) * rowlen + (size_t)h * D);
+                    const uint4* kp = reinterpret_cast<const uint4*>(kb + (size_t)j * rowlen);
+                    float s0 = 0.f, s1 = 0.f;
+#pragma unroll 4
+                    for (int i = 0; i < D / 8; ++i) {
+                        const uint4 x4 = qp[i], y4 = kp[i];
+                        const uint32_t xs[4] = {x4.x, x4.y, x4.z, x4.w}, ys[4] = {y4.x, y4.y, y4.z, y4.w};
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            s0 += __uint_as_float(xs[k] << 16) * __uint_as_float(ys[k] << 16);
+                            s1 += __uint_as_float(xs[k] & 0xFFFF0000u) * __uint_as_float(ys[k] & 0xFFFF0000u);
+                        }
+                    }
+                    x = (s0 + s1) * sl2;
+                }
+                s_own[e] = x;
+            }
+            __syncthreads();
+            for (int r = warp; r < R; r += kTcThreads / 32) {    // each row's maximum, probabilities and sum
+                float m = NEG_INF, sum = 0.f;
+                for (int j = lane; j < a.T; j += 32) m = fmaxf(m, s_own[r * a.T + j]);
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+                const float mm = m == NEG_INF ? 0.f : m;         // (only NaN scores)
+                for (int j = lane; j < a.T; j += 32) {
+                    const float p = ex2(s_own[r * a.T + j] - mm);
+                    s_own[r * a.T + j] = p;
+                    sum += p;
+                }
+#pragma unroll
+                for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+                if (lane == 0) {
+                    s_m2[r] = mm;
+                    s_l2[r] = sum;
+                }
+            }
+            __syncthreads();
+            const uint16_t* vb = a.qkv + (size_t)b * a.T * rowlen + (size_t)(a.Hq + a.Hkv + kh) * D + dim;
+            const int tmax = (r0 + R - 1) / a.G;
+            for (int j = 0; j <= tmax; ++j) {
+                const float v = __uint_as_float((uint32_t)vb[(size_t)j * rowlen] << 16);
+                const int rmin = max(0, j * a.G - r0);           // rows from there on see row j
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = 8 * (hf + 2 * t) + i;
+                        if (r >= rmin && r < R) o2[t][i] += s_own[r * a.T + j] * v;
+                    }
+            }
+        }
+        fence_proxy_async_smem();                                // Q, before the products read it
+        __syncthreads();
+
+        // ---- 128 positions at a time
+        const unsigned step0 = steps;
+#pragma unroll 1
+        for (int t0 = 0; t0 < nsteps; ++t0, ++steps) {
+            const int s = steps % kTcStages;
+            if (!bar_wait(&full[s], (steps / kTcStages) & 1u, abort, a.wait_ns)) atomicOr(&g_attn_kv4_tc_error, kErrFullWait);
+            const uint32_t stage = sbase + (uint32_t)(Ly::Ring + 4 * s * Rec::Bytes);
+            {   // keys: 32 bytes of codes (64 dims) of position `key` -> tensor memory columns 32 hf ..
+                const uint32_t rec = stage + (uint32_t)(q4 * Rec::Bytes);
+                const uint32_t at = rec + (uint32_t)(Rec::KC + lane * Rec::RowBytes + hf * 32);
+                const int sw = (lane >> 1) & 1;                  // neighbours start with different 16 bytes
+                uint32_t x[2][4];
+                lds_v4_u32(at + 16 * sw, x[0][0], x[0][1], x[0][2], x[0][3]);
+                lds_v4_u32(at + 16 * (1 - sw), x[1][0], x[1][1], x[1][2], x[1][3]);
+                const uint32_t sb = lds_u32(rec + (uint32_t)(Rec::KS + lane * 4)) >> (16 * hf);
+                uint32_t k32[32];
+#pragma unroll
+                for (int gr = 0; gr < 2; ++gr) {
+                    const KeyScale sc((sb >> (8 * gr)) & 255u);
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t y = sw == gr ? x[0][w] : x[1][w];
+                        k32[16 * gr + 4 * w] = key_pair<0>(y, sc, c8);
+                        k32[16 * gr + 4 * w + 1] = key_pair<1>(y, sc, c8);
+                        k32[16 * gr + 4 * w + 2] = key_pair<2>(y, sc, c8);
+                        k32[16 * gr + 4 * w + 3] = key_pair<3>(y, sc, c8);
+                    }
+                }
+                tmem_st_x32(tlane + Ly::kK + 32 * hf, k32);
+                tmem_st_wait();
+            }
+            tc_fence_before();
+            __syncthreads();
+            if (tid == 0) {
+                tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    umma_f16_ta(tmem + Ly::kS, tmem + Ly::kK + 8 * ks,
+                                sw128_kmajor_desc(sbase + (uint32_t)(Ly::Q + (ks >> 2) * Ly::NS * 128 + (ks & 3) * 32)),
+                                idesc(1, Ly::NS, false), ks != 0);
+                umma_commit(bar_s);
+            }
+            __syncwarp();
+            // values: the previous step's product has read the buffer
+            if (t0 > 0 && !bar_wait(bar_o, (steps - 1) & 1u, abort, kWaitLimitNs)) atomicOr(&g_attn_kv4_tc_error, kErrTcWait);
+#pragma unroll
+            for (int it = 0; it < 2; ++it) {
+                const int ch = tid & 3, pos = (tid >> 2) + 64 * it;   // 16 bytes of codes: 32 dims of one position
+                const uint32_t rec = stage + (uint32_t)((pos >> 5) * Rec::Bytes);
+                uint32_t x[4];
+                lds_v4_u32(rec + (uint32_t)(Rec::VC + (pos & 31) * Rec::RowBytes + ch * 16), x[0], x[1], x[2], x[3]);
+                const uint32_t sb = lds_u8(rec + (uint32_t)(Rec::VS + (pos & 31) * 4 + ch));
+                const ValScale sc(sb, sb);
+                // chunks 2, 3 (dims 64 ..) store their words in pairs the other
+                // way round: the four chunks then fall on different banks
+                const bool odd = (ch & 2) != 0;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const uint32_t y = odd ? x[w ^ 1] : x[w];
+                    const int c16 = (ch & 1) * 4 + (odd ? w ^ 1 : w);
+                    sts_v4_u32(sbase + (uint32_t)(Ly::V + (ch >> 1) * kTcKeys * 128 + pos * 128 + ((c16 ^ (pos & 7)) << 4)),
+                               val_pair<0>(y, sc, c4, c64), val_pair<1>(y, sc, c4, c64), val_pair<2>(y, sc, c4, c64),
+                               val_pair<3>(y, sc, c4, c64));
+                }
+            }
+            // softmax: this position's products with the rows of tiles hf, hf + 2
+            if (!bar_wait(bar_s, steps & 1u, abort, kWaitLimitNs)) atomicOr(&g_attn_kv4_tc_error, kErrTcWait);
+            tc_fence_after();
+            const bool there = lane < cnt[4 * s + q4];
+            uint32_t x[NT][8];
+            bool grow = false;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                if (hf + 2 * t < NR) tmem_ld<8>(tlane + Ly::kS + 8 * (hf + 2 * t), x[t]);
+            tmem_ld_wait();
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                if (hf + 2 * t < NR) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (!there) x[t][i] = __float_as_uint(NEG_INF);
+                        grow = grow || __uint_as_float(x[t][i]) > s_lim[8 * (hf + 2 * t) + i];
+                    }
+                }
+            fence_proxy_async_smem();                            // the values, before the second product reads them
+            const int any = __syncthreads_or(grow);              // every code of the stage has been read
+            if (warp == 0) issue();
+            if (any) {                                           // rare: some row's maximum moves
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    if (hf + 2 * t < NR) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            float v = __uint_as_float(x[t][i]);
+#pragma unroll
+                            for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+                            if (lane == 0) s_red[q4 * 32 + 8 * (hf + 2 * t) + i] = v;
+                        }
+                    }
+                __syncthreads();
+                if (tid < RW) {
+                    const float v = fmaxf(fmaxf(s_red[tid], s_red[32 + tid]), fmaxf(s_red[64 + tid], s_red[96 + tid]));
+                    float f = 1.f;
+                    if (v > s_lim[tid]) {
+                        const float m = rintf(v * sl2), cn = kBias - m;
+                        f = s_lim[tid] == NEG_INF ? 0.f : ex2(cn - s_c[tid]);
+                        s_c[tid] = cn;
+                        s_lim[tid] = (m + kLazy) / sl2;
+                    }
+                    s_f[tid] = f;
+                }
+                __syncthreads();
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    if (hf + 2 * t < NR) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) l[t][i] *= s_f[8 * (hf + 2 * t) + i];
+                        if (t0 > 0) {
+#pragma unroll
+                            for (int part = 0; part < (OUTBF ? 1 : 2); ++part) {
+                                uint32_t ov[8];
+                                tmem_ld<8>(tlane + Ly::kO + part * RW + 8 * (hf + 2 * t), ov);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * s_f[8 * (hf + 2 * t) + i]);
+                                tmem_st_x8(tlane + Ly::kO + part * RW + 8 * (hf + 2 * t), ov);
+                            }
+                            tmem_st_wait();
+                        }
+                    }
+            }
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                if (hf + 2 * t < NR) {
+                    const int tile = hf + 2 * t;
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float p0 = ex2(__uint_as_float(x[t][2 * i]) * sl2 + s_c[8 * tile + 2 * i]);
+                        const float p1 = ex2(__uint_as_float(x[t][2 * i + 1]) * sl2 + s_c[8 * tile + 2 * i + 1]);
+                        l[t][2 * i] += p0;
+                        l[t][2 * i + 1] += p1;
+                        hi[i] = pack_f16x2(p0, p1);
+                        const float2 h = unpack_f16x2(hi[i]);
+                        lo[i] = pack_f16x2(p0 - h.x, p1 - h.y);
+                    }
+                    const uint32_t prow = sbase + (uint32_t)(Ly::P + key * 128);
+                    sts_v4_u32(prow + (uint32_t)((tile ^ (key & 7)) << 4), hi[0], hi[1], hi[2], hi[3]);
+                    if (!OUTBF) sts_v4_u32(prow + (uint32_t)(((NR + tile) ^ (key & 7)) << 4), lo[0], lo[1], lo[2], lo[3]);
+                }
+            fence_proxy_async_smem();
+            tc_fence_before();
+            __syncthreads();
+            if (tid == 0) {
+                tc_fence_after();
+#pragma unroll
+                for (int ks = 0; ks < 8; ++ks)
+                    umma_f16_ss(tmem + Ly::kO, sw128_mnmajor_desc(sbase + (uint32_t)(Ly::V + ks * 2048), kTcKeys * 128),
+                                sw128_mnmajor_desc(sbase + (uint32_t)(Ly::P + ks * 2048), kTcKeys * 128),
+                                idesc(0, Ly::NO, true), (t0 != 0 || ks != 0) ? 1u : 0u);
+                umma_commit(bar_o);
+            }
+            __syncwarp();
+        }
+        (void)step0;
+
+        // ---- the rows' sums, and the weights of the cache's and the own part
+        if (nsteps > 0) {
+            if (!bar_wait(bar_o, (steps - 1) & 1u, abort, kWaitLimitNs)) atomicOr(&g_attn_kv4_tc_error, kErrTcWait);
+            tc_fence_after();
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+                if (hf + 2 * t < NR) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        float v = l[t][i];
+#pragma unroll
+                        for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+                        if (lane == 0) s_red[q4 * 32 + 8 * (hf + 2 * t) + i] = v;
+                    }
+                }
+        }
+        __syncthreads();
+        if (tid < RW) {
+            const float lc = nsteps > 0 ? (s_red[tid] + s_red[32 + tid]) + (s_red[64 + tid] + s_red[96 + tid]) : 0.f;
+            const float e1 = s_lim[tid] == NEG_INF ? NEG_INF : -s_c[tid], e2 = s_m2[tid];
+            const float M = fmaxf(e1, e2);
+            const float w1 = e1 == NEG_INF ? 0.f : ex2(e1 - M), w2 = e2 == NEG_INF ? 0.f : ex2(e2 - M);
+            s_w1[tid] = 64.f * w1;                               // (the values were taken times 2^-6)
+            s_w2[tid] = w2;
+            s_M[tid] = M;
+            s_L[tid] = lc * w1 + s_l2[tid] * w2;
+        }
+        __syncthreads();
+        float v[NT][8];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            uint32_t h8[8], l8[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) h8[i] = l8[i] = 0u;
+            if (hf + 2 * t < NR && nsteps > 0) {
+                tmem_ld<8>(tlane + Ly::kO + 8 * (hf + 2 * t), h8);
+                if (!OUTBF) tmem_ld<8>(tlane + Ly::kO + RW + 8 * (hf + 2 * t), l8);
+                tmem_ld_wait();
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int r = min(8 * (hf + 2 * t) + i, RW - 1);
+                v[t][i] = (__uint_as_float(h8[i]) + __uint_as_float(l8[i])) * s_w1[r] + o2[t][i] * s_w2[r];
+            }
+        }
+        auto store = [&](int r, float x, float sum) {            // this lane's dim of row r
+            const int j = (r0 + r) / a.G, h = kh * a.G + (r0 + r) - j * a.G;
+            const size_t at = ((size_t)b * a.T + j) * (size_t)a.Hq * D + (size_t)h * D + dim;
+            if (OUTBF) static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(x / sum);
+            else static_cast<float*>(a.out)[at] = x / sum;
+        };
+        if (ua == 0 && own) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = 8 * (hf + 2 * t) + i;
+                    if (r < R) store(r, v[t][i], s_L[r]);
+                }
+        } else {
+            float* slot = a.partials + ((size_t)blockIdx.x * 2 + (ua == 0 ? 1 : 0)) * Ly::Slot;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const int r = 8 * (hf + 2 * t) + i;
+                    if (r < R) slot[r * D + key] = v[t][i];
+                }
+            if (tid < RW) {
+                slot[RW * D + tid] = s_M[tid];
+                slot[RW * D + RW + tid] = s_L[tid];
+            }
+            const unsigned c0 = tile_at / per, c1 = (tile_at + (unsigned)nc) / per;   // the tile's CTAs
+            __syncthreads();                                     // (the part is written before thread 0's fence)
+            if (tid == 0) {
+                __threadfence();
+                const unsigned before_me = atomicAdd(a.counters + c0, 1u);
+                *s_flag = before_me == c1 - c0;
+                if (*s_flag) {
+                    a.counters[c0] = 0;
+                    __threadfence();
+                }
+            }
+            __syncthreads();
+            if (*s_flag) {
+                // the tile's parts, added in range order at the rows' common maxima
+                auto part = [&](unsigned ci) { return a.partials + ((size_t)ci * 2 + (ci == c0 ? 1 : 0)) * Ly::Slot; };
+                if (tid < RW) {
+                    float M = NEG_INF;
+#pragma unroll 8
+                    for (unsigned ci = c0; ci <= c1; ++ci) M = fmaxf(M, __ldcg(part(ci) + RW * D + tid));
+                    s_M[tid] = M;
+                }
+                __syncthreads();
+                float sum[NT][8];
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) v[t][i] = sum[t][i] = 0.f;
+#pragma unroll 1
+                for (unsigned ci = c0; ci <= c1; ++ci) {
+                    const float* pp = part(ci);
+                    float x[NT][8], pm[NT][8], pl[NT][8];
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int r = min(8 * (hf + 2 * t) + i, R - 1);
+                            x[t][i] = __ldcg(pp + r * D + key);
+                            pm[t][i] = __ldcg(pp + RW * D + r);
+                            pl[t][i] = __ldcg(pp + RW * D + RW + r);
+                        }
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const float f = pm[t][i] == NEG_INF ? 0.f : ex2(pm[t][i] - s_M[min(8 * (hf + 2 * t) + i, R - 1)]);
+                            v[t][i] += x[t][i] * f;
+                            sum[t][i] += pl[t][i] * f;
+                        }
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = 8 * (hf + 2 * t) + i;
+                        if (r < R) store(r, v[t][i], sum[t][i]);
+                    }
+            }
+        }
+        tc_fence_before();                                       // O has been read
+        __syncthreads();
+        tc_fence_after();
+    }
+    // after a wait that ran out: no copy and no product may be in flight when the CTA ends
+    if (work && *abort) {
+        volatile int none = 0;
+        if (!a.hold)
+            for (unsigned s = steps_issued > kTcStages ? steps_issued - kTcStages : 0; s < steps_issued && warp == 0; ++s)
+                bar_wait(&full[s % kTcStages], (s / kTcStages) & 1u, &none, kWaitLimitNs);
+        if (steps > 0) bar_wait(bar_o, (steps - 1) & 1u, &none, kWaitLimitNs);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 0) {
+        tc_fence_after();
+        tmem_dealloc(tmem, Ly::Cols);
+    }
+}
+
+template <int NR, bool OUTBF>
+cudaError_t launch(const Args& a, int grid, int tile_cost, int min_units, cudaStream_t s) {
+    using Ly = TcLayout<NR, OUTBF>;
+    static_assert(Ly::Alloc <= (int)(kMaxDynSmem / 2 - 1024), "two CTAs per SM");
+    cudaError_t e = cudaFuncSetAttribute(attn_kv4_tc_kernel<NR, OUTBF>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ly::Alloc);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)grid);
+    cfg.blockDim = dim3(kTcThreads);
+    cfg.dynamicSmemBytes = Ly::Alloc;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attn_kv4_tc_kernel<NR, OUTBF>, a, tile_cost, min_units);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_kv4_tc(const kv4attn::Args& a, int NR, bool out_bf16, int grid, int tile_cost, int min_units,
+                               cudaStream_t s) {
+#define QV_KV4_TC_CASE(NRV) \
+    if (NR == NRV) return out_bf16 ? launch<NRV, true>(a, grid, tile_cost, min_units, s) : launch<NRV, false>(a, grid, tile_cost, min_units, s);
+    QV_KV4_TC_CASE(1) QV_KV4_TC_CASE(2) QV_KV4_TC_CASE(3) QV_KV4_TC_CASE(4)
+#undef QV_KV4_TC_CASE
+    return cudaErrorInvalidValue;
+}
+
+cudaError_t read_and_clear_attn_kv4_tc_error(unsigned* code) {
+    cudaError_t e = cudaMemcpyFromSymbol(code, g_attn_kv4_tc_error, sizeof(unsigned));
+    if (e != cudaSuccess) return e;
+    const unsigned zero = 0;
+    return cudaMemcpyToSymbol(g_attn_kv4_tc_error, &zero, sizeof(unsigned));
+}
+
+}  // namespace qv
