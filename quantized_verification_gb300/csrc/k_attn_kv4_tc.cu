@@ -99,6 +99,35 @@ __device__ __forceinline__ void tmem_st_x8(uint32_t taddr, const uint32_t (&v)[8
                  : "memory");
 }
 
+// The 8 values of a row array for an n8 tile.
+__device__ __forceinline__ void row8(const float* p, int tile, float (&v)[8]) {
+    const float4 a = reinterpret_cast<const float4*>(p)[2 * tile], b = reinterpret_cast<const float4*>(p)[2 * tile + 1];
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+// True (in all its lanes) in the warp that comes last of the CTA's 8 (the count
+// only grows). What every warp did before is then visible to it; no warp waits
+// for another.
+__device__ __forceinline__ bool last_warp(unsigned* arrivals) {
+    tc_fence_before();
+    __syncwarp();
+    unsigned n = 0;
+    if ((threadIdx.x & 31) == 0) {
+        __threadfence_block();
+        n = atomicAdd(arrivals, 1u);
+        __threadfence_block();
+    }
+    n = __shfl_sync(0xffffffffu, n, 0);
+    tc_fence_after();
+    return (n & (kTcThreads / 32 - 1)) == kTcThreads / 32 - 1;
+}
+// True in one lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+
 template <int NR, bool OUTBF>
 __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a, int tile_cost, int min_units) {
     using Ly = TcLayout<NR, OUTBF>;
@@ -128,6 +157,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
     volatile int* abort = reinterpret_cast<volatile int*>(smem + Ly::Misc);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + Ly::Misc) + 1;
     int* s_flag = reinterpret_cast<int*>(smem + Ly::Misc) + 2;
+    unsigned* s_arr = reinterpret_cast<unsigned*>(smem + Ly::Misc) + 3;   // [2] warps that have arrived
     float* s_own = reinterpret_cast<float*>(smem + Ly::V);       // [R][T] own scores, before the first values
     const float NEG_INF = -__uint_as_float(0x7F800000u);
 
@@ -140,6 +170,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
     if (tid == 32) {
         for (int s = 0; s < kTcStages + 2; ++s) mbar_init(&full[s], 1);
         *abort = 0;
+        s_arr[0] = s_arr[1] = 0;
         fence_barrier_init();
     }
     tc_fence_before();
@@ -153,6 +184,9 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
     const int own_units = (a.T + 31) / 32, tps = a.Hkv * a.RT;
     const float sl2 = a.scale * kLog2e;
     const size_t rowlen = (size_t)(a.Hq + 2 * a.Hkv) * D;
+    const uint64_t q_desc = sw128_kmajor_desc(sbase + (uint32_t)Ly::Q);
+    const uint64_t v_desc = sw128_mnmajor_desc(sbase + (uint32_t)Ly::V, kTcKeys * 128);
+    const uint64_t p_desc = sw128_mnmajor_desc(sbase + (uint32_t)Ly::P, kTcKeys * 128);
     uint32_t c4 = 4u, c8 = 8u, c64 = 64u;                        // multipliers the compiler may not turn into shifts
     asm volatile("" : "+r"(c4), "+r"(c8), "+r"(c64));
     unsigned steps_issued = 0, steps = 0;                        // 128-position steps requested / begun so far
@@ -234,7 +268,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int i = 0; i < 8; ++i) l[t][i] = o2[t][i] = 0.f;
-        const int dim = (key & ~7) + ((key & 1) << 2) + ((key & 7) >> 1);   // the dim of O's lane `key`
+        const int dim = (key & 0x78) + ((key & 1) << 2) + ((key & 7) >> 1);   // the dim of O's lane `key`
 
         // ---- the step's own rows, in fp32
         if (own) {
@@ -299,7 +333,6 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
         __syncthreads();
 
         // ---- 128 positions at a time
-        const unsigned step0 = steps;
 #pragma unroll 1
         for (int t0 = 0; t0 < nsteps; ++t0, ++steps) {
             const int s = steps % kTcStages;
@@ -329,18 +362,17 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
                 tmem_st_x32(tlane + Ly::kK + 32 * hf, k32);
                 tmem_st_wait();
             }
-            tc_fence_before();
-            __syncthreads();
-            if (tid == 0) {
-                tc_fence_after();
+            if (last_warp(&s_arr[0])) {                          // the keys are all in tensor memory
+                if (elect_one()) {
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                    umma_f16_ta(tmem + Ly::kS, tmem + Ly::kK + 8 * ks,
-                                sw128_kmajor_desc(sbase + (uint32_t)(Ly::Q + (ks >> 2) * Ly::NS * 128 + (ks & 3) * 32)),
-                                idesc(1, Ly::NS, false), ks != 0);
-                umma_commit(bar_s);
+                    for (int ks = 0; ks < 8; ++ks)
+                        umma_f16_ta(tmem + Ly::kS, tmem + Ly::kK + 8 * ks,
+                                    q_desc + (uint64_t)(((ks >> 2) * Ly::NS * 128 + (ks & 3) * 32) >> 4),
+                                    idesc(1, Ly::NS, false), ks != 0);
+                    umma_commit(bar_s);
+                }
+                __syncwarp();
             }
-            __syncwarp();
             // values: the previous step's product has read the buffer
             if (t0 > 0 && !bar_wait(bar_o, (steps - 1) & 1u, abort, kWaitLimitNs)) atomicOr(&g_attn_kv4_tc_error, kErrTcWait);
 #pragma unroll
@@ -376,10 +408,12 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
 #pragma unroll
             for (int t = 0; t < NT; ++t)
                 if (hf + 2 * t < NR) {
+                    float lim[8];
+                    row8(s_lim, hf + 2 * t, lim);
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         if (!there) x[t][i] = __float_as_uint(NEG_INF);
-                        grow = grow || __uint_as_float(x[t][i]) > s_lim[8 * (hf + 2 * t) + i];
+                        grow |= __uint_as_float(x[t][i]) > lim[i];
                     }
                 }
             fence_proxy_async_smem();                            // the values, before the second product reads them
@@ -434,10 +468,12 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
                 if (hf + 2 * t < NR) {
                     const int tile = hf + 2 * t;
                     uint32_t hi[4], lo[4];
+                    float c[8];
+                    row8(s_c, tile, c);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float p0 = ex2(__uint_as_float(x[t][2 * i]) * sl2 + s_c[8 * tile + 2 * i]);
-                        const float p1 = ex2(__uint_as_float(x[t][2 * i + 1]) * sl2 + s_c[8 * tile + 2 * i + 1]);
+                        const float p0 = ex2(__uint_as_float(x[t][2 * i]) * sl2 + c[2 * i]);
+                        const float p1 = ex2(__uint_as_float(x[t][2 * i + 1]) * sl2 + c[2 * i + 1]);
                         l[t][2 * i] += p0;
                         l[t][2 * i + 1] += p1;
                         hi[i] = pack_f16x2(p0, p1);
@@ -449,20 +485,17 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
                     if (!OUTBF) sts_v4_u32(prow + (uint32_t)(((NR + tile) ^ (key & 7)) << 4), lo[0], lo[1], lo[2], lo[3]);
                 }
             fence_proxy_async_smem();
-            tc_fence_before();
-            __syncthreads();
-            if (tid == 0) {
-                tc_fence_after();
+            if (last_warp(&s_arr[1])) {                          // the values and probabilities are all in shared memory
+                if (elect_one()) {
 #pragma unroll
-                for (int ks = 0; ks < 8; ++ks)
-                    umma_f16_ss(tmem + Ly::kO, sw128_mnmajor_desc(sbase + (uint32_t)(Ly::V + ks * 2048), kTcKeys * 128),
-                                sw128_mnmajor_desc(sbase + (uint32_t)(Ly::P + ks * 2048), kTcKeys * 128),
-                                idesc(0, Ly::NO, true), (t0 != 0 || ks != 0) ? 1u : 0u);
-                umma_commit(bar_o);
+                    for (int ks = 0; ks < 8; ++ks)
+                        umma_f16_ss(tmem + Ly::kO, v_desc + (uint64_t)(ks * 2048 >> 4), p_desc + (uint64_t)(ks * 2048 >> 4),
+                                    idesc(0, Ly::NO, true), (t0 != 0 || ks != 0) ? 1u : 0u);
+                    umma_commit(bar_o);
+                }
+                __syncwarp();
             }
-            __syncwarp();
         }
-        (void)step0;
 
         // ---- the rows' sums, and the weights of the cache's and the own part
         if (nsteps > 0) {
