@@ -9,24 +9,26 @@
 //   ALUs, with too few warps to overlap the two (137 us for one step of 5 tokens
 //   over 2 x 131071 positions; 42 us to read the cache).
 //
-// A CTA takes 128 positions (4 records) at a time, all 256 threads together:
-//   1. unpacks the keys (thread = position, half the dims) to bf16 pairs and
-//      stores them as the A operand in tensor memory;
-//   2. S^T = K Q^T: 8 tcgen05.mma, M = 128 positions, N = the query rows padded
-//      to 16 or 32, B = Q in shared memory;
-//   3. meanwhile unpacks the values to f16 (times 2^-6) into shared memory, as
-//      the M-major A operand of the second product (rows of positions, 128-byte
-//      swizzle; the unpacked order of 8 dims is just an order of output rows);
-//   4. softmax: thread = position, for the rows of every other n8 tile. The
-//      maxima of the rows belong to the CTA; whether one has to move is one
-//      vote in the barrier that is needed anyway;
-//   5. O^T += V^T P^T: 8 tcgen05.mma, M = 128 dims, N = the rows' first parts
-//      side by side with their second parts, accumulated in tensor memory; it
-//      runs while the next keys are unpacked.
-// Two CTAs share an SM, so that one's barriers fall into the other's work. The
-// step's own keys and values are few and are not of the cache's format: they
-// are attended to with plain fp32 arithmetic while the first records load, and
-// merged at the end.
+// A CTA takes 128 positions (4 records) a step. 8 warps work on them, a ninth
+// requests records and issues the products; they meet at mbarriers, and the
+// order is such that nothing is waited for that was not begun long before:
+//   1. the keys of the NEXT step (thread = position, half the dims) become bf16
+//      pairs in tensor memory, the A operand of S^T = K Q^T: 8 tcgen05.mma, M =
+//      128 positions, N = the query rows padded to 16 or 32, B = Q in shared
+//      memory, two S buffers;
+//   2. this step's products are read (thread = position, the rows of every other
+//      n8 tile) and compared with the rows' limits: does a maximum have to move?
+//   3. the values become f16 (times 2^-6) in shared memory, the M-major A
+//      operand of the second product (rows of positions, 128-byte swizzle; the
+//      unpacked order of 8 dims is just an order of output rows);
+//   4. with every warp's answer to 2 there by now, the probabilities go to
+//      shared memory, and O^T += V^T P^T: 8 tcgen05.mma, M = 128 dims, N = the
+//      rows' first parts side by side with their second parts, accumulated in
+//      tensor memory while the next step begins.
+// Two CTAs share an SM. The step's own keys and values are few and are not of
+// the cache's format: they are attended to with plain fp32 arithmetic while the
+// first records load; their outputs wait in tensor memory and are merged at the
+// end.
 
 #include "attn_kv4_common.cuh"
 
@@ -38,7 +40,8 @@ namespace {
 
 using namespace kv4attn;
 
-constexpr int kTcThreads = 256;
+constexpr int kTcWorkers = 256;                 // threads that unpack and form the softmax
+constexpr int kTcThreads = kTcWorkers + 32;     // and the ninth warp
 constexpr int kTcKeys = 128;                    // positions per step: 4 records
 constexpr int kTcStages = 3;
 constexpr int D = 128;
@@ -53,8 +56,8 @@ struct TcLayout {
     static constexpr int P = V + 2 * kTcKeys * 128;       // [128 positions][128 B]
     static constexpr int Q = P + kTcKeys * 128;           // [2 halves][NS rows][128 B]
     static constexpr int Ring = Q + 2 * 32 * 128;
-    static constexpr int Bar = Ring + kTcStages * 4 * Rec::Bytes;   // full [stages], S done, O done
-    static constexpr int Cnt = Bar + (kTcStages + 3) * 8; // cached positions per record [stages][4]
+    static constexpr int Bar = Ring + kTcStages * 4 * Rec::Bytes;   // full [stages], then the kBar ones
+    static constexpr int Cnt = Bar + (kTcStages + 7) * 8; // cached positions per record [stages][4]
     static constexpr int Row = Cnt + kTcStages * 16;      // floats per row: c, limit, f, own m, own l, w1, w2, M, l
     static constexpr int Red = Row + 9 * 32 * 4;          // [4][32]
     static constexpr int Scan = Red + 4 * 32 * 4;
@@ -62,7 +65,7 @@ struct TcLayout {
     static constexpr int Bytes = Misc + 32;
     static constexpr int Alloc = Bytes + 1024;            // slack to align the base to 1024 B
     static constexpr int Slot = RW * D + 2 * RW;          // floats of a partial result: [row][lane], m, l
-    static constexpr int kK = 0, kS = 64, kO = 96;        // tensor memory columns
+    static constexpr int kK = 0, kS = 64, kO = 128, kOwn = 192;   // tensor memory columns (S twice 32)
     static constexpr int Cols = 256;
     static_assert(Bar % 8 == 0 && Row % 16 == 0 && Ring % 16 == 0, "alignment");
     static_assert(kRowTile * QV_ATTN_MAX_T * 4 <= 2 * kTcKeys * 128, "the own scores fit the value buffer");
@@ -105,21 +108,25 @@ __device__ __forceinline__ void row8(const float* p, int tile, float (&v)[8]) {
     v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
     v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
-// True (in all its lanes) in the warp that comes last of the CTA's 8 (the count
-// only grows). What every warp did before is then visible to it; no warp waits
-// for another.
-__device__ __forceinline__ bool last_warp(unsigned* arrivals) {
-    tc_fence_before();
-    __syncwarp();
-    unsigned n = 0;
-    if ((threadIdx.x & 31) == 0) {
-        __threadfence_block();
-        n = atomicAdd(arrivals, 1u);
-        __threadfence_block();
+// bar_wait that reports the error `bit` if this wait is the one that ran out.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, unsigned parity, volatile int* abort, unsigned long long limit_ns,
+                                         unsigned bit) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const unsigned long long t0 = global_timer_ns();
+    while (true) {
+        if (*abort) return false;
+        if (mbar_try_wait(bar, parity)) return true;
+        if (global_timer_ns() - t0 > limit_ns) {
+            *abort = 1;
+            atomicOr(&g_attn_kv4_tc_error, bit);
+            return false;
+        }
     }
-    n = __shfl_sync(0xffffffffu, n, 0);
-    tc_fence_after();
-    return (n & (kTcThreads / 32 - 1)) == kTcThreads / 32 - 1;
+}
+// One arrival per warp, for all its lanes.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar) {
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) mbar_arrive(bar);
 }
 // True in one lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
@@ -137,11 +144,16 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     const uint32_t sbase = smem_u32(smem);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int q4 = warp & 3, hf = warp >> 2;                     // record (tensor memory lanes 32 q4 ..), half
+    const bool worker = warp < kTcWorkers / 32;
+    const int q4 = warp & 3, hf = (warp >> 2) & 1;                     // record (tensor memory lanes 32 q4 ..), half
     const int key = 32 * q4 + lane;                              // this thread's position, and its lane of O
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + Ly::Bar);
-    uint64_t* bar_s = full + kTcStages;
-    uint64_t* bar_o = bar_s + 1;
+    uint64_t* bar_s = full + kTcStages;                          // S of a step is formed
+    uint64_t* bar_o = bar_s + 1;                                 // O has taken a step's values
+    uint64_t* bar_k = bar_s + 2;                                 // the keys of a step are in tensor memory (8 warps)
+    uint64_t* bar_g = bar_s + 3;                                 // every warp has compared a step's products (8 warps)
+    uint64_t* bar_p = bar_s + 4;                                 // the values and probabilities are in place (8 warps)
+    uint64_t* bar_end = bar_s + 5;
     volatile int* cnt = reinterpret_cast<volatile int*>(smem + Ly::Cnt);
     float* s_c = reinterpret_cast<float*>(smem + Ly::Row);       // p = 2^(sl2 x + c), c = kBias - m
     float* s_lim = s_c + 32;                                     // the product at which m moves
@@ -157,20 +169,24 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
     volatile int* abort = reinterpret_cast<volatile int*>(smem + Ly::Misc);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + Ly::Misc) + 1;
     int* s_flag = reinterpret_cast<int*>(smem + Ly::Misc) + 2;
-    unsigned* s_arr = reinterpret_cast<unsigned*>(smem + Ly::Misc) + 3;   // [2] warps that have arrived
+    volatile unsigned* s_grow = reinterpret_cast<volatile unsigned*>(smem + Ly::Misc) + 4;   // [2] the step whose maxima move, + 1
     float* s_own = reinterpret_cast<float*>(smem + Ly::V);       // [R][T] own scores, before the first values
     const float NEG_INF = -__uint_as_float(0x7F800000u);
 
     // Tensor memory before dependents may start: one of theirs that held it
     // while it waited for this grid would never let it go.
-    if (warp == 0) {
+    if (!worker) {
         tmem_alloc(s_tmem, Ly::Cols);
         tmem_relinquish();
     }
     if (tid == 32) {
         for (int s = 0; s < kTcStages + 2; ++s) mbar_init(&full[s], 1);
+        mbar_init(bar_k, kTcWorkers / 32);
+        mbar_init(bar_g, kTcWorkers / 32);
+        mbar_init(bar_p, kTcWorkers / 32);
+        mbar_init(bar_end, 1);
         *abort = 0;
-        s_arr[0] = s_arr[1] = 0;
+        s_grow[0] = s_grow[1] = 0;
         fence_barrier_init();
     }
     tc_fence_before();
@@ -216,15 +232,15 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
         const bool own = ub > nc;
         const int last = min(ub, nc), nsteps = ua < last ? (last - ua + 3) / 4 : 0;
 
-        // ---- records: lane i of warp 0 requests record i of a step
+        // ---- records: lane i of the ninth warp requests record i of a step
         int unit = ua + lane;                                    // its next unit, and that unit's page
         auto page_of = [&](int x) {
             return x >= last ? -1 : (a.table ? a.table[(size_t)b * a.NB + x] : b * a.NB + x);
         };
-        int page = warp == 0 && lane < 4 ? page_of(unit) : -1;
+        int page = !worker && lane < 4 ? page_of(unit) : -1;
         int to_issue = nsteps;
-        auto issue = [&]() {                                     // warp 0
-            if (to_issue == 0) return;
+        auto issue = [&]() {
+            if (to_issue == 0 || *abort) return;
             --to_issue;
             const int s = steps_issued % kTcStages;
             const bool there = lane < 4 && unit < last && (unsigned)page < (unsigned)a.pages;
@@ -242,7 +258,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
             unit += 4;
             if (lane < 4) page = page_of(unit);
         };
-        if (warp == 0)
+        if (!worker)
             for (int s = 0; s < kTcStages; ++s) issue();
 
         // ---- Q, rows of 128-byte halves; 8 dims in the order 0 4 1 5 2 6 3 7
@@ -263,11 +279,11 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
             s_m2[tid] = NEG_INF;
             s_l2[tid] = 0.f;
         }
-        float l[NT][8], o2[NT][8];                               // this position's sums; this dim's own-row outputs
+        float l[NT][8];                                          // this position's sums
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) l[t][i] = o2[t][i] = 0.f;
+            for (int i = 0; i < 8; ++i) l[t][i] = 0.f;
         const int dim = (key & 0x78) + ((key & 1) << 2) + ((key & 7) >> 1);   // the dim of O's lane `key`
 
         // ---- the step's own rows, in fp32
@@ -315,31 +331,77 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
                 }
             }
             __syncthreads();
-            const uint16_t* vb = a.qkv + (size_t)b * a.T * rowlen + (size_t)(a.Hq + a.Hkv + kh) * D + dim;
-            const int tmax = (r0 + R - 1) / a.G;
-            for (int j = 0; j <= tmax; ++j) {
-                const float v = __uint_as_float((uint32_t)vb[(size_t)j * rowlen] << 16);
-                const int rmin = max(0, j * a.G - r0);           // rows from there on see row j
+            if (worker) {
+                const uint16_t* vb = a.qkv + (size_t)b * a.T * rowlen + (size_t)(a.Hq + a.Hkv + kh) * D + dim;
+                const int tmax = (r0 + R - 1) / a.G;
+                float o2[NT][8];
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int r = 8 * (hf + 2 * t) + i;
-                        if (r >= rmin && r < R) o2[t][i] += s_own[r * a.T + j] * v;
+                    for (int i = 0; i < 8; ++i) o2[t][i] = 0.f;
+                for (int j = 0; j <= tmax; ++j) {
+                    const float v = __uint_as_float((uint32_t)vb[(size_t)j * rowlen] << 16);
+                    const int rmin = max(0, j * a.G - r0);       // rows from there on see row j
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            const int r = 8 * (hf + 2 * t) + i;
+                            if (r >= rmin && r < R) o2[t][i] += s_own[r * a.T + j] * v;
+                        }
+                }
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    if (hf + 2 * t < NR) {
+                        uint32_t ov[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) ov[i] = __float_as_uint(o2[t][i]);
+                        tmem_st_x8(tlane + Ly::kOwn + 8 * (hf + 2 * t), ov);
                     }
+                tmem_st_wait();
             }
         }
         fence_proxy_async_smem();                                // Q, before the products read it
         __syncthreads();
 
-        // ---- 128 positions at a time
+        // ---- 128 positions at a time. `steps` counts them over all tiles: the
+        // parity of every barrier follows from it
+        if (!worker) {
+            auto s_product = [&](int t0) {                       // S of step t0 of the tile
+                wait_for(bar_k, (steps + t0) & 1u, abort, kWaitLimitNs, kErrTcWait);
+                if (elect_one()) {
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        umma_f16_ta(tmem + Ly::kS + 32 * ((steps + t0) & 1u), tmem + Ly::kK + 8 * ks,
+                                    q_desc + (uint64_t)(((ks >> 2) * Ly::NS * 128 + (ks & 3) * 32) >> 4),
+                                    idesc(1, Ly::NS, false), ks != 0);
+                    umma_commit(bar_s);
+                }
+                __syncwarp();
+            };
+            if (nsteps > 0) s_product(0);
 #pragma unroll 1
-        for (int t0 = 0; t0 < nsteps; ++t0, ++steps) {
-            const int s = steps % kTcStages;
-            if (!bar_wait(&full[s], (steps / kTcStages) & 1u, abort, a.wait_ns)) atomicOr(&g_attn_kv4_tc_error, kErrFullWait);
-            const uint32_t stage = sbase + (uint32_t)(Ly::Ring + 4 * s * Rec::Bytes);
-            {   // keys: 32 bytes of codes (64 dims) of position `key` -> tensor memory columns 32 hf ..
-                const uint32_t rec = stage + (uint32_t)(q4 * Rec::Bytes);
+            for (int t0 = 0; t0 < nsteps; ++t0) {
+                if (t0 + 1 < nsteps) s_product(t0 + 1);
+                wait_for(bar_p, (steps + t0) & 1u, abort, kWaitLimitNs, kErrTcWait);
+                if (elect_one()) {
+                    tc_fence_after();
+#pragma unroll
+                    for (int ks = 0; ks < 8; ++ks)
+                        umma_f16_ss(tmem + Ly::kO, v_desc + (uint64_t)(ks * 2048 >> 4), p_desc + (uint64_t)(ks * 2048 >> 4),
+                                    idesc(0, Ly::NO, true), (t0 != 0 || ks != 0) ? 1u : 0u);
+                    umma_commit(bar_o);
+                }
+                __syncwarp();
+                issue();                                         // (the stage's codes have all been read)
+            }
+        } else {
+            auto unpack_keys = [&](int t0) {                     // of step t0 -> tensor memory, columns 32 hf ..
+                const unsigned st = steps + t0;
+                const int s = st % kTcStages;
+                wait_for(&full[s], (st / kTcStages) & 1u, abort, a.wait_ns, kErrFullWait);
+                const uint32_t rec = sbase + (uint32_t)(Ly::Ring + (4 * s + q4) * Rec::Bytes);
                 const uint32_t at = rec + (uint32_t)(Rec::KC + lane * Rec::RowBytes + hf * 32);
                 const int sw = (lane >> 1) & 1;                  // neighbours start with different 16 bytes
                 uint32_t x[2][4];
@@ -361,146 +423,143 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
                 }
                 tmem_st_x32(tlane + Ly::kK + 32 * hf, k32);
                 tmem_st_wait();
-            }
-            if (last_warp(&s_arr[0])) {                          // the keys are all in tensor memory
-                if (elect_one()) {
+                tc_fence_before();
+                warp_arrive(bar_k);
+            };
+            if (nsteps > 0) unpack_keys(0);
+#pragma unroll 1
+            for (int t0 = 0; t0 < nsteps; ++t0) {
+                const unsigned st = steps + t0;
+                const int s = st % kTcStages;
+                wait_for(bar_s, st & 1u, abort, kWaitLimitNs, kErrTcWait);   // (S is formed and the keys' columns are free)
+                tc_fence_after();
+                if (t0 + 1 < nsteps) unpack_keys(t0 + 1);
+                // this position's products with the rows of tiles hf, hf + 2
+                const bool there = lane < cnt[4 * s + q4];
+                uint32_t x[NT][8];
+                bool grow = false;
 #pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        umma_f16_ta(tmem + Ly::kS, tmem + Ly::kK + 8 * ks,
-                                    q_desc + (uint64_t)(((ks >> 2) * Ly::NS * 128 + (ks & 3) * 32) >> 4),
-                                    idesc(1, Ly::NS, false), ks != 0);
-                    umma_commit(bar_s);
-                }
-                __syncwarp();
-            }
-            // values: the previous step's product has read the buffer
-            if (t0 > 0 && !bar_wait(bar_o, (steps - 1) & 1u, abort, kWaitLimitNs)) atomicOr(&g_attn_kv4_tc_error, kErrTcWait);
-#pragma unroll
-            for (int it = 0; it < 2; ++it) {
-                const int ch = tid & 3, pos = (tid >> 2) + 64 * it;   // 16 bytes of codes: 32 dims of one position
-                const uint32_t rec = stage + (uint32_t)((pos >> 5) * Rec::Bytes);
-                uint32_t x[4];
-                lds_v4_u32(rec + (uint32_t)(Rec::VC + (pos & 31) * Rec::RowBytes + ch * 16), x[0], x[1], x[2], x[3]);
-                const uint32_t sb = lds_u8(rec + (uint32_t)(Rec::VS + (pos & 31) * 4 + ch));
-                const ValScale sc(sb, sb);
-                // chunks 2, 3 (dims 64 ..) store their words in pairs the other
-                // way round: the four chunks then fall on different banks
-                const bool odd = (ch & 2) != 0;
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const uint32_t y = odd ? x[w ^ 1] : x[w];
-                    const int c16 = (ch & 1) * 4 + (odd ? w ^ 1 : w);
-                    sts_v4_u32(sbase + (uint32_t)(Ly::V + (ch >> 1) * kTcKeys * 128 + pos * 128 + ((c16 ^ (pos & 7)) << 4)),
-                               val_pair<0>(y, sc, c4, c64), val_pair<1>(y, sc, c4, c64), val_pair<2>(y, sc, c4, c64),
-                               val_pair<3>(y, sc, c4, c64));
-                }
-            }
-            // softmax: this position's products with the rows of tiles hf, hf + 2
-            if (!bar_wait(bar_s, steps & 1u, abort, kWaitLimitNs)) atomicOr(&g_attn_kv4_tc_error, kErrTcWait);
-            tc_fence_after();
-            const bool there = lane < cnt[4 * s + q4];
-            uint32_t x[NT][8];
-            bool grow = false;
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-                if (hf + 2 * t < NR) tmem_ld<8>(tlane + Ly::kS + 8 * (hf + 2 * t), x[t]);
-            tmem_ld_wait();
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-                if (hf + 2 * t < NR) {
-                    float lim[8];
-                    row8(s_lim, hf + 2 * t, lim);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        if (!there) x[t][i] = __float_as_uint(NEG_INF);
-                        grow |= __uint_as_float(x[t][i]) > lim[i];
-                    }
-                }
-            fence_proxy_async_smem();                            // the values, before the second product reads them
-            const int any = __syncthreads_or(grow);              // every code of the stage has been read
-            if (warp == 0) issue();
-            if (any) {                                           // rare: some row's maximum moves
+                for (int t = 0; t < NT; ++t)
+                    if (hf + 2 * t < NR) tmem_ld<8>(tlane + Ly::kS + 32 * (st & 1u) + 8 * (hf + 2 * t), x[t]);
+                tmem_ld_wait();
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
                     if (hf + 2 * t < NR) {
+                        float lim[8];
+                        row8(s_lim, hf + 2 * t, lim);
 #pragma unroll
                         for (int i = 0; i < 8; ++i) {
-                            float v = __uint_as_float(x[t][i]);
-#pragma unroll
-                            for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
-                            if (lane == 0) s_red[q4 * 32 + 8 * (hf + 2 * t) + i] = v;
+                            if (!there) x[t][i] = __float_as_uint(NEG_INF);
+                            grow |= __uint_as_float(x[t][i]) > lim[i];
                         }
                     }
-                __syncthreads();
-                if (tid < RW) {
-                    const float v = fmaxf(fmaxf(s_red[tid], s_red[32 + tid]), fmaxf(s_red[64 + tid], s_red[96 + tid]));
-                    float f = 1.f;
-                    if (v > s_lim[tid]) {
-                        const float m = rintf(v * sl2), cn = kBias - m;
-                        f = s_lim[tid] == NEG_INF ? 0.f : ex2(cn - s_c[tid]);
-                        s_c[tid] = cn;
-                        s_lim[tid] = (m + kLazy) / sl2;
+                if (grow) s_grow[st & 1u] = st + 1;
+                tc_fence_before();
+                warp_arrive(bar_g);
+                // values: the previous step's product has read the buffer
+                if (t0 > 0) wait_for(bar_o, (st - 1) & 1u, abort, kWaitLimitNs, kErrTcWait);
+                const uint32_t stage = sbase + (uint32_t)(Ly::Ring + 4 * s * Rec::Bytes);
+#pragma unroll
+                for (int it = 0; it < 2; ++it) {
+                    const int ch = tid & 3, pos = (tid >> 2) + 64 * it;   // 16 bytes of codes: 32 dims of one position
+                    const uint32_t rec = stage + (uint32_t)((pos >> 5) * Rec::Bytes);
+                    uint32_t y4[4];
+                    lds_v4_u32(rec + (uint32_t)(Rec::VC + (pos & 31) * Rec::RowBytes + ch * 16), y4[0], y4[1], y4[2], y4[3]);
+                    const uint32_t sb = lds_u8(rec + (uint32_t)(Rec::VS + (pos & 31) * 4 + ch));
+                    const ValScale sc(sb, sb);
+                    // chunks 2, 3 (dims 64 ..) store their words in pairs the other
+                    // way round: the four chunks then fall on different banks
+                    const bool odd = (ch & 2) != 0;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const uint32_t y = odd ? y4[w ^ 1] : y4[w];
+                        const int c16 = (ch & 1) * 4 + (odd ? w ^ 1 : w);
+                        sts_v4_u32(sbase + (uint32_t)(Ly::V + (ch >> 1) * kTcKeys * 128 + pos * 128 + ((c16 ^ (pos & 7)) << 4)),
+                                   val_pair<0>(y, sc, c4, c64), val_pair<1>(y, sc, c4, c64), val_pair<2>(y, sc, c4, c64),
+                                   val_pair<3>(y, sc, c4, c64));
                     }
-                    s_f[tid] = f;
                 }
-                __syncthreads();
+                wait_for(bar_g, st & 1u, abort, kWaitLimitNs, kErrTcWait);
+                if (s_grow[st & 1u] == st + 1) {                 // rare: some row's maximum moves
+                    tc_fence_after();
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        if (hf + 2 * t < NR) {
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                float v = __uint_as_float(x[t][i]);
+#pragma unroll
+                                for (int off = 16; off > 0; off >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, off));
+                                if (lane == 0) s_red[q4 * 32 + 8 * (hf + 2 * t) + i] = v;
+                            }
+                        }
+                    named_bar_sync(1, kTcWorkers);
+                    if (tid < RW) {
+                        const float v = fmaxf(fmaxf(s_red[tid], s_red[32 + tid]), fmaxf(s_red[64 + tid], s_red[96 + tid]));
+                        float f = 1.f;
+                        if (v > s_lim[tid]) {
+                            const float m = rintf(v * sl2), cn = kBias - m;
+                            f = s_lim[tid] == NEG_INF ? 0.f : ex2(cn - s_c[tid]);
+                            s_c[tid] = cn;
+                            s_lim[tid] = (m + kLazy) / sl2;
+                        }
+                        s_f[tid] = f;
+                    }
+                    named_bar_sync(1, kTcWorkers);
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        if (hf + 2 * t < NR) {
+                            float f8[8];
+                            row8(s_f, hf + 2 * t, f8);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) l[t][i] *= f8[i];
+                            if (t0 > 0) {
+#pragma unroll
+                                for (int part = 0; part < (OUTBF ? 1 : 2); ++part) {
+                                    uint32_t ov[8];
+                                    tmem_ld<8>(tlane + Ly::kO + part * RW + 8 * (hf + 2 * t), ov);
+                                    tmem_ld_wait();
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * f8[i]);
+                                    tmem_st_x8(tlane + Ly::kO + part * RW + 8 * (hf + 2 * t), ov);
+                                }
+                                tmem_st_wait();
+                            }
+                        }
+                }
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
                     if (hf + 2 * t < NR) {
+                        const int tile = hf + 2 * t;
+                        uint32_t hi[4], lo[4];
+                        float c[8];
+                        row8(s_c, tile, c);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) l[t][i] *= s_f[8 * (hf + 2 * t) + i];
-                        if (t0 > 0) {
-#pragma unroll
-                            for (int part = 0; part < (OUTBF ? 1 : 2); ++part) {
-                                uint32_t ov[8];
-                                tmem_ld<8>(tlane + Ly::kO + part * RW + 8 * (hf + 2 * t), ov);
-                                tmem_ld_wait();
-#pragma unroll
-                                for (int i = 0; i < 8; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * s_f[8 * (hf + 2 * t) + i]);
-                                tmem_st_x8(tlane + Ly::kO + part * RW + 8 * (hf + 2 * t), ov);
-                            }
-                            tmem_st_wait();
+                        for (int i = 0; i < 4; ++i) {
+                            const float p0 = ex2(__uint_as_float(x[t][2 * i]) * sl2 + c[2 * i]);
+                            const float p1 = ex2(__uint_as_float(x[t][2 * i + 1]) * sl2 + c[2 * i + 1]);
+                            l[t][2 * i] += p0;
+                            l[t][2 * i + 1] += p1;
+                            hi[i] = pack_f16x2(p0, p1);
+                            const float2 h = unpack_f16x2(hi[i]);
+                            lo[i] = pack_f16x2(p0 - h.x, p1 - h.y);
                         }
+                        const uint32_t prow = sbase + (uint32_t)(Ly::P + key * 128);
+                        sts_v4_u32(prow + (uint32_t)((tile ^ (key & 7)) << 4), hi[0], hi[1], hi[2], hi[3]);
+                        if (!OUTBF) sts_v4_u32(prow + (uint32_t)(((NR + tile) ^ (key & 7)) << 4), lo[0], lo[1], lo[2], lo[3]);
                     }
-            }
-#pragma unroll
-            for (int t = 0; t < NT; ++t)
-                if (hf + 2 * t < NR) {
-                    const int tile = hf + 2 * t;
-                    uint32_t hi[4], lo[4];
-                    float c[8];
-                    row8(s_c, tile, c);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float p0 = ex2(__uint_as_float(x[t][2 * i]) * sl2 + c[2 * i]);
-                        const float p1 = ex2(__uint_as_float(x[t][2 * i + 1]) * sl2 + c[2 * i + 1]);
-                        l[t][2 * i] += p0;
-                        l[t][2 * i + 1] += p1;
-                        hi[i] = pack_f16x2(p0, p1);
-                        const float2 h = unpack_f16x2(hi[i]);
-                        lo[i] = pack_f16x2(p0 - h.x, p1 - h.y);
-                    }
-                    const uint32_t prow = sbase + (uint32_t)(Ly::P + key * 128);
-                    sts_v4_u32(prow + (uint32_t)((tile ^ (key & 7)) << 4), hi[0], hi[1], hi[2], hi[3]);
-                    if (!OUTBF) sts_v4_u32(prow + (uint32_t)(((NR + tile) ^ (key & 7)) << 4), lo[0], lo[1], lo[2], lo[3]);
-                }
-            fence_proxy_async_smem();
-            if (last_warp(&s_arr[1])) {                          // the values and probabilities are all in shared memory
-                if (elect_one()) {
-#pragma unroll
-                    for (int ks = 0; ks < 8; ++ks)
-                        umma_f16_ss(tmem + Ly::kO, v_desc + (uint64_t)(ks * 2048 >> 4), p_desc + (uint64_t)(ks * 2048 >> 4),
-                                    idesc(0, Ly::NO, true), (t0 != 0 || ks != 0) ? 1u : 0u);
-                    umma_commit(bar_o);
-                }
-                __syncwarp();
+                fence_proxy_async_smem();
+                tc_fence_before();
+                warp_arrive(bar_p);
             }
         }
+        steps += (unsigned)nsteps;
 
         // ---- the rows' sums, and the weights of the cache's and the own part
         if (nsteps > 0) {
-            if (!bar_wait(bar_o, (steps - 1) & 1u, abort, kWaitLimitNs)) atomicOr(&g_attn_kv4_tc_error, kErrTcWait);
+            wait_for(bar_o, (steps - 1) & 1u, abort, kWaitLimitNs, kErrTcWait);
             tc_fence_after();
+            if (worker)
 #pragma unroll
             for (int t = 0; t < NT; ++t)
                 if (hf + 2 * t < NR) {
@@ -528,18 +587,21 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
         float v[NT][8];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            uint32_t h8[8], l8[8];
+            uint32_t h8[8], l8[8], o8[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) h8[i] = l8[i] = 0u;
-            if (hf + 2 * t < NR && nsteps > 0) {
-                tmem_ld<8>(tlane + Ly::kO + 8 * (hf + 2 * t), h8);
-                if (!OUTBF) tmem_ld<8>(tlane + Ly::kO + RW + 8 * (hf + 2 * t), l8);
+            for (int i = 0; i < 8; ++i) h8[i] = l8[i] = o8[i] = 0u;
+            if (worker && hf + 2 * t < NR) {
+                if (nsteps > 0) {
+                    tmem_ld<8>(tlane + Ly::kO + 8 * (hf + 2 * t), h8);
+                    if (!OUTBF) tmem_ld<8>(tlane + Ly::kO + RW + 8 * (hf + 2 * t), l8);
+                }
+                if (own) tmem_ld<8>(tlane + Ly::kOwn + 8 * (hf + 2 * t), o8);
                 tmem_ld_wait();
             }
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int r = min(8 * (hf + 2 * t) + i, RW - 1);
-                v[t][i] = (__uint_as_float(h8[i]) + __uint_as_float(l8[i])) * s_w1[r] + o2[t][i] * s_w2[r];
+                v[t][i] = (__uint_as_float(h8[i]) + __uint_as_float(l8[i])) * s_w1[r] + __uint_as_float(o8[i]) * s_w2[r];
             }
         }
         auto store = [&](int r, float x, float sum) {            // this lane's dim of row r
@@ -554,7 +616,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int r = 8 * (hf + 2 * t) + i;
-                    if (r < R) store(r, v[t][i], s_L[r]);
+                    if (worker && r < R) store(r, v[t][i], s_L[r]);
                 }
         } else {
             float* slot = a.partials + ((size_t)blockIdx.x * 2 + (ua == 0 ? 1 : 0)) * Ly::Slot;
@@ -563,7 +625,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int r = 8 * (hf + 2 * t) + i;
-                    if (r < R) slot[r * D + key] = v[t][i];
+                    if (worker && r < R) slot[r * D + key] = v[t][i];
                 }
             if (tid < RW) {
                 slot[RW * D + tid] = s_M[tid];
@@ -623,7 +685,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int r = 8 * (hf + 2 * t) + i;
-                        if (r < R) store(r, v[t][i], sum[t][i]);
+                        if (worker && r < R) store(r, v[t][i], sum[t][i]);
                     }
             }
         }
@@ -632,16 +694,18 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
         tc_fence_after();
     }
     // after a wait that ran out: no copy and no product may be in flight when the CTA ends
-    if (work && *abort) {
+    if (work && *abort && !worker) {
         volatile int none = 0;
         if (!a.hold)
-            for (unsigned s = steps_issued > kTcStages ? steps_issued - kTcStages : 0; s < steps_issued && warp == 0; ++s)
+            for (unsigned s = steps_issued > kTcStages ? steps_issued - kTcStages : 0; s < steps_issued; ++s)
                 bar_wait(&full[s % kTcStages], (s / kTcStages) & 1u, &none, kWaitLimitNs);
-        if (steps > 0) bar_wait(bar_o, (steps - 1) & 1u, &none, kWaitLimitNs);
+        if (elect_one()) umma_commit(bar_end);
+        __syncwarp();
+        bar_wait(bar_end, 0u, &none, kWaitLimitNs);
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 0) {
+    if (!worker) {
         tc_fence_after();
         tmem_dealloc(tmem, Ly::Cols);
     }
