@@ -22,6 +22,9 @@ constexpr int kMinUnits = 16;                   // places of a CTA's range at le
 constexpr size_t kCounterBytes = 4096;         // at the workspace's start, whatever the shape
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTileCost = 12;                   // units' worth of a tile's own costs
+constexpr int kMaxCluster = 8;                  // CTAs of a cluster that share a tile
+constexpr int kClusterUnits = 8;                // a larger cluster while its CTAs have more units than this
+constexpr int kClusterMost = 48;                // no clusters above so many units a CTA
 constexpr int kTcMinUnits = 8;                  // the same for the tcgen05 kernel: two steps of 128 positions,
 constexpr int kTcTileCost = 12;                 // and a tile's costs
 constexpr float kLazy = 8.f;                    // log2 of the growth a running maximum may lag behind
@@ -34,6 +37,7 @@ struct Args {
     const int32_t* len;        // [B]
     int B, T, Hq, Hkv, G, NB, pages;
     int RT, rows;              // row tiles per head group, query rows per row tile
+    int C;                     // CTAs of the cluster that takes a tile, or 0 (k_attn_kv4.cu)
     float scale;
     void* out;                 // [B*T][Hq D] fp32 or bf16
     unsigned* counters;        // [grid] arrivals at the tile that begins in CTA i's range (zero between calls)
@@ -41,6 +45,11 @@ struct Args {
     int hold;                  // test hook: request no record
     unsigned long long wait_ns;
 };
+
+__device__ __forceinline__ void cluster_arrive_relaxed() {
+    asm volatile("barrier.cluster.arrive.relaxed.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 
 __device__ __forceinline__ float ex2(float x) {
     float y;

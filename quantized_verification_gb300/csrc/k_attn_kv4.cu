@@ -49,7 +49,11 @@
 // query rows must not see (padding): they are taken as 0 in the product and
 // added afterwards to the rows that do see them.
 
+#include <cooperative_groups.h>
+
 #include "attn_kv4_common.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace qv {
 
@@ -72,7 +76,7 @@ struct Layout {
     static constexpr int Ctas = ORegs <= 64 ? 2 : 1;
     static constexpr int Warps = ORegs <= 64 ? 8 : (ORegs <= 96 ? 12 : 8);
     static constexpr int Threads = Warps * 32;
-    static constexpr int Stages = D == 128 && Warps * Ctas >= 12 ? 3 : 4;
+    static constexpr int Stages = D == 64 ? 4 : (NR == 2 ? 2 : (Warps * Ctas >= 12 ? 3 : 4));
     // With 8 warps on an SM the products of the next 16 positions are formed
     // between those of P and V of the present ones.
     static constexpr bool Pipe = Warps * Ctas == 8;
@@ -83,7 +87,8 @@ struct Layout {
     static constexpr int AreaBytes = Warps * RW * D * 4; // the warps' outputs [Warps][NR*4*KS][32], in the drained ring
     static constexpr int Q = Ring + RingBytes;            // query fragments [NR][KS][32] uint2
     static constexpr int ML = Q + NR * KS * 32 * 8;       // m [Warps][RW], l [Warps][RW]
-    static constexpr int Bar = ML + 2 * Warps * RW * 4;
+    static constexpr int Recv = ML + 2 * Warps * RW * 4;  // from the cluster's CTAs: items [C][RW*D/4/C], m [C][RW], l [C][RW]
+    static constexpr int Bar = Recv + RW * D * 4 + 2 * kMaxCluster * RW * 4;
     static constexpr int Valid = Bar + Warps * Stages * 8;
     static constexpr int Scan = Valid + Warps * Stages * 4;    // unsigned [Warps], then [14], [15]: the first sequence's place and number
     static constexpr int Misc = Scan + 16 * 4;
@@ -91,7 +96,7 @@ struct Layout {
     static constexpr int Items = RW * D / 4;              // groups of 4 dims of one row
     static constexpr int Slot = RW * D + 2 * RW;          // floats of a partial result: items, m, l
     static_assert(AreaBytes <= RingBytes, "the warps' outputs fit the ring");
-    static_assert(Q % 16 == 0 && Bar % 8 == 0 && Scan % 4 == 0, "alignment");
+    static_assert(Q % 16 == 0 && Recv % 16 == 0 && Bar % 8 == 0 && Scan % 4 == 0, "alignment");
 };
 
 template <int D, int NR, bool OUTBF>
@@ -120,15 +125,18 @@ __global__ void __launch_bounds__(Layout<D, NR>::Threads, Layout<D, NR>::Ctas) a
         s_flag[0] = 0;
     }
     fence_barrier_init();
+    if (a.C > 1) cluster_arrive_relaxed();                       // waited for before the first store into another CTA
     allow_dependent_launch();
     grid_dependency_wait();
 
     const int own_units = (a.T + 31) / 32, tps = a.Hkv * a.RT;   // own units of a tile, tiles of a sequence
-    Range rg;
-    if (!find_range<kThreads>(a, own_units, kTileCost, kMinUnits, s_scan, rg)) return;
-    const unsigned per = rg.per, u1 = rg.u1;
+    const int C = a.C;                                           // CTAs of a cluster that share one tile, or 0
+    const int rank = C > 0 ? (int)(blockIdx.x % (unsigned)C) : 0;
+    Range rg = {0, 0, 1, 0, 0};
+    if (C == 0 && !find_range<kThreads>(a, own_units, kTileCost, kMinUnits, s_scan, rg)) return;
+    const unsigned per = rg.per, u1 = C > 0 ? 1 : rg.u1;
     unsigned seq_at = rg.seq_at, u = rg.u0;
-    int b_next = rg.b;
+    int b_next = C > 0 ? (int)(blockIdx.x / (unsigned)C) / tps : rg.b;
     unsigned issued = 0, used = 0;                               // this warp's records so far
     bool dead = false;                                           // a wait of this warp ran out: it takes no more units
     const size_t rowlen = (size_t)(a.Hq + 2 * a.Hkv) * D;
@@ -142,17 +150,28 @@ __global__ void __launch_bounds__(Layout<D, NR>::Threads, Layout<D, NR>::Ctas) a
         const int b = b_next;
         const int L = seq_len(a, b);
         const int nc = (L + kKv4Block - 1) / kKv4Block, nu = nc + own_units;
-        const unsigned places = (unsigned)(nu + kTileCost);
-        const int ti = (int)((u - seq_at) / places);
-        const unsigned tile_at = seq_at + (unsigned)ti * places;
-        const int kh = ti / a.RT, rt = ti - kh * a.RT;
-        const int ua = (int)(u - tile_at), ub = (int)min((unsigned)nu, u1 - tile_at);
-        u = tile_at + places;                                    // where this CTA goes on
-        if (ti == tps - 1) {
-            seq_at = u;
-            ++b_next;
+        unsigned tile_at = 0;
+        int ti, ua, ub;
+        if (C > 0) {                                             // the one tile, its units cut into C equal parts
+            ti = (int)(blockIdx.x / (unsigned)C) - b * tps;
+            const int part = (nu + C - 1) / C;
+            ua = min(nu, rank * part);
+            ub = min(nu, ua + part);
+            u = u1;
+        } else {
+            const unsigned places = (unsigned)(nu + kTileCost);
+            ti = (int)((u - seq_at) / places);
+            tile_at = seq_at + (unsigned)ti * places;
+            ua = (int)(u - tile_at);
+            ub = (int)min((unsigned)nu, u1 - tile_at);
+            u = tile_at + places;                                // where this CTA goes on
+            if (ti == tps - 1) {
+                seq_at = u;
+                ++b_next;
+            }
+            if (ua >= nu) continue;                              // (only empty places of the tile)
         }
-        if (ua >= nu) continue;                                  // (only empty places of the tile)
+        const int kh = ti / a.RT, rt = ti - kh * a.RT;
         const int r0 = rt * a.rows, R = min(a.rows, a.T * a.G - r0);   // query rows of this tile
 
         int next = ua + warp;                                    // next unit to request, and its page
@@ -626,7 +645,42 @@ __global__ void __launch_bounds__(Layout<D, NR>::Threads, Layout<D, NR>::Ctas) a
                 *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) =
                     make_float4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
         };
-        if (ua == 0 && ub == nu) {
+        if (C > 1) {
+            // into the CTAs that own the items, then the sum of this CTA's
+            cg::cluster_group cluster = cg::this_cluster();
+            float4* r_v = reinterpret_cast<float4*>(smem + Ly::Recv);
+            float* r_m = reinterpret_cast<float*>(smem + Ly::Recv) + RW * D;
+            float* r_l = r_m + kMaxCluster * RW;
+            const int mine = Ly::Items / C;
+            cluster_wait();                                      // every CTA of the cluster has started
+            for (int it = tid; it < Ly::Items; it += kThreads) {
+                int r, d0;
+                float v[4], M, l;
+                item_at(it, r, d0);
+                item_sum(it, r, d0, v, M, l);
+                const int k = it / mine;
+                *cluster.map_shared_rank(r_v + rank * mine + (it - k * mine), k) = make_float4(v[0], v[1], v[2], v[3]);
+                if (d0 == 0)
+                    for (int q = 0; q < C; ++q) {
+                        *cluster.map_shared_rank(r_m + rank * RW + r, q) = M;
+                        *cluster.map_shared_rank(r_l + rank * RW + r, q) = l;
+                    }
+            }
+            cluster.sync();                                      // every push has landed
+            for (int i = tid; i < mine; i += kThreads) {
+                int r, d0;
+                item_at(rank * mine + i, r, d0);
+                float M = NEG_INF, l = 0.f, v[4] = {0.f, 0.f, 0.f, 0.f};
+                for (int q = 0; q < C; ++q) M = fmaxf(M, r_m[q * RW + r]);
+                for (int q = 0; q < C; ++q) {
+                    const float m = r_m[q * RW + r], f = m == NEG_INF ? 0.f : ex2(m - M);
+                    const float4 x = r_v[q * mine + i];
+                    l += f * r_l[q * RW + r];
+                    v[0] += f * x.x; v[1] += f * x.y; v[2] += f * x.z; v[3] += f * x.w;
+                }
+                store(r, d0, v, l);
+            }
+        } else if (ua == 0 && ub == nu) {
             for (int it = tid; it < Ly::Items; it += kThreads) {
                 int r, d0;
                 float v[4], M, l;
@@ -729,7 +783,7 @@ __global__ void __launch_bounds__(Layout<D, NR>::Threads, Layout<D, NR>::Ctas) a
 }
 
 template <int D, int NR, bool OUTBF>
-cudaError_t launch(const Args& a, int grid, cudaStream_t s) {
+cudaError_t launch(const Args& a, int grid, cudaStream_t s) {                  // a.C > 1: clusters of a.C CTAs
     using Ly = Layout<D, NR>;
     static_assert(Ly::Bytes <= (int)(Ly::Ctas == 2 ? kMaxDynSmem / 2 - 1024 : kMaxDynSmem), "shared memory budget");
     cudaError_t e = cudaFuncSetAttribute(attn_kv4_kernel<D, NR, OUTBF>, cudaFuncAttributeMaxDynamicSharedMemorySize, Ly::Bytes);
@@ -739,13 +793,22 @@ cudaError_t launch(const Args& a, int grid, cudaStream_t s) {
     cfg.blockDim = dim3(Ly::Threads);
     cfg.dynamicSmemBytes = Ly::Bytes;
     cfg.stream = s;
-    cudaLaunchAttribute attr[1];
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = a.C > 1 ? a.C : 1;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = a.C > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, attn_kv4_kernel<D, NR, OUTBF>, a);
 }
+
+#ifndef KTCROWS
+#define KTCROWS 3
+#endif
+constexpr int kTcRows = KTCROWS;
 
 // Row tiles of a head group's T * G query rows, and rows per tile: as few
 // tiles of at most 32 rows as there can be, of equal size.
@@ -755,21 +818,31 @@ void row_tiles(int rows, int& RT, int& per) {
 }
 
 struct Plan {
-    int RT, rows, NR, grid, cost, min_units;
+    int RT, rows, NR;
+    int C;                       // CTAs of the cluster that takes a tile, or 0: one line of units cut into equal ranges
+    bool tc;                     // the tcgen05 kernel
+    int grid, cost, min_units;
     size_t total;                // workspace bytes; 0: more units than the kernel's 32-bit places can count
 };
 Plan plan(int B, int T, int Hq, int Hkv, int D, int NB, int sms) {
     Plan p;
     row_tiles(T * (Hq / Hkv), p.RT, p.rows);
     p.NR = (p.rows + 7) / 8;
-    p.cost = D == 128 ? kTcTileCost : kTileCost;
-    p.min_units = D == 128 ? kTcMinUnits : kMinUnits;
-    const long long most = (long long)B * Hkv * p.RT * ((long long)NB + (T + 31) / 32 + p.cost);   // places at most
-    long long ctas = 2LL * sms;                           // two CTAs on an SM
+    const long long tiles = (long long)B * Hkv * p.RT, units = (long long)NB + (T + 31) / 32;   // units of a tile at most
+    const int slots = sms * (D / 64 * p.NR <= 4 ? 2 : 1);      // CTAs the GPU holds
+    p.C = 1;
+    while (p.C < kMaxCluster && tiles * p.C * 2 <= slots && units > kClusterUnits * p.C) p.C *= 2;
+    if (tiles * p.C > slots || units > kClusterMost * p.C) p.C = 0;
+    p.tc = p.C == 0 && D == 128 && p.NR >= kTcRows;
+    p.cost = p.tc ? kTcTileCost : kTileCost;
+    p.min_units = p.tc ? kTcMinUnits : kMinUnits;
+    const long long most = tiles * (units + p.cost);           // places at most
+    long long ctas = p.tc ? 2LL * sms : slots;
     ctas = ctas < (long long)(kCounterBytes / 4) ? ctas : (long long)(kCounterBytes / 4);
     const long long want = (most + p.min_units - 1) / p.min_units;
-    p.grid = (int)(want < ctas ? want : ctas);
-    p.total = most < (1ll << 31) ? kCounterBytes + (size_t)p.grid * 2 * (p.NR * 8 * D + 2 * p.NR * 8) * 4 : 0;
+    p.grid = p.C > 0 ? (int)(tiles * p.C) : (int)(want < ctas ? want : ctas);
+    p.total = kCounterBytes + (p.C > 0 ? 0 : (size_t)p.grid * 2 * (p.NR * 8 * D + 2 * p.NR * 8) * 4);
+    if (most >= (1ll << 31)) p.total = 0;
     return p;
 }
 
@@ -787,14 +860,15 @@ cudaError_t launch_attention_kv4(const uint16_t* qkv, const uint8_t* cache, cons
     Args a;
     a.qkv = qkv; a.cache = cache; a.table = table; a.len = len;
     a.B = B; a.T = T; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv; a.NB = NB; a.pages = pages;
-    a.RT = p.RT; a.rows = p.rows;
+    a.RT = p.RT; a.rows = p.rows; a.C = p.C;
     a.scale = scale; a.out = out;
     a.counters = static_cast<unsigned*>(ws);
     a.partials = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + kCounterBytes);
     a.hold = hold; a.wait_ns = wait_ns ? wait_ns : kWaitLimitNs;
-    if (D == 128) return launch_attn_kv4_tc(a, p.NR, out_bf16, p.grid, p.cost, p.min_units, s);
+    if (p.tc) return launch_attn_kv4_tc(a, p.NR, out_bf16, p.grid, p.cost, p.min_units, s);
 #define QV_KV4_CASE(DV, NRV) \
     if (D == DV && p.NR == NRV) return out_bf16 ? launch<DV, NRV, true>(a, p.grid, s) : launch<DV, NRV, false>(a, p.grid, s);
+    QV_KV4_CASE(128, 1) QV_KV4_CASE(128, 2) QV_KV4_CASE(128, 3) QV_KV4_CASE(128, 4)
     QV_KV4_CASE(64, 1) QV_KV4_CASE(64, 2) QV_KV4_CASE(64, 3) QV_KV4_CASE(64, 4)
 #undef QV_KV4_CASE
     return cudaErrorInvalidValue;

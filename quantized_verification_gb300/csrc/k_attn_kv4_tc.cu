@@ -44,6 +44,7 @@ constexpr int kTcWorkers = 256;                 // threads that unpack and form 
 constexpr int kTcThreads = kTcWorkers + 32;     // and the ninth warp
 constexpr int kTcKeys = 128;                    // positions per step: 4 records
 constexpr int kTcStages = 3;
+constexpr int kTcMaxParts = 128;                // parts of a tile merged at once (their weights fill the value buffer)
 constexpr int D = 128;
 
 template <int NR, bool OUTBF>
@@ -68,6 +69,7 @@ struct TcLayout {
     static constexpr int kK = 0, kS = 64, kO = 128, kOwn = 192;   // tensor memory columns (S twice 32)
     static constexpr int Cols = 256;
     static_assert(Bar % 8 == 0 && Row % 16 == 0 && Ring % 16 == 0, "alignment");
+    static_assert(2 * kTcMaxParts * 32 * 4 <= 2 * kTcKeys * 128, "the parts' weights fit the value buffer");
     static_assert(kRowTile * QV_ATTN_MAX_T * 4 <= 2 * kTcKeys * 128, "the own scores fit the value buffer");
 };
 
@@ -625,7 +627,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int r = 8 * (hf + 2 * t) + i;
-                    if (worker && r < R) slot[r * D + key] = v[t][i];
+                    if (worker && r < RW) slot[r * D + key] = v[t][i];   // (rows past R too: they are read, not used)
                 }
             if (tid < RW) {
                 slot[RW * D + tid] = s_M[tid];
@@ -644,48 +646,80 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
             }
             __syncthreads();
             if (*s_flag) {
-                // the tile's parts, added in range order at the rows' common maxima
+                // The tile's parts, added in range order at the rows' common maxima:
+                // the weights first (in the value buffer, [part][32]), then four
+                // parts' rows at a time.
                 auto part = [&](unsigned ci) { return a.partials + ((size_t)ci * 2 + (ci == c0 ? 1 : 0)) * Ly::Slot; };
-                if (tid < RW) {
-                    float M = NEG_INF;
-#pragma unroll 8
-                    for (unsigned ci = c0; ci <= c1; ++ci) M = fmaxf(M, __ldcg(part(ci) + RW * D + tid));
-                    s_M[tid] = M;
-                }
-                __syncthreads();
-                float sum[NT][8];
+                const unsigned n = c1 - c0 + 1;
+                float* s_f2 = reinterpret_cast<float*>(smem + Ly::V);
+                float* s_l3 = s_f2 + kTcMaxParts * 32;
+                float run[NT][8];                                // this dim's sums so far, at the maxima s_M
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) v[t][i] = sum[t][i] = 0.f;
+                    for (int i = 0; i < 8; ++i) run[t][i] = 0.f;
+                if (tid < 32) {
+                    s_M[tid] = NEG_INF;
+                    s_L[tid] = 0.f;
+                }
 #pragma unroll 1
-                for (unsigned ci = c0; ci <= c1; ++ci) {
-                    const float* pp = part(ci);
-                    float x[NT][8], pm[NT][8], pl[NT][8];
+                for (unsigned n0 = 0; n0 < n; n0 += kTcMaxParts) {
+                    const unsigned nn = min(n - n0, (unsigned)kTcMaxParts);
+                    for (unsigned e = tid; e < nn * 32; e += kTcThreads) {
+                        const float* pp = part(c0 + n0 + (e >> 5));
+                        const int r = min((int)(e & 31), RW - 1);
+                        s_f2[e] = __ldcg(pp + RW * D + r);
+                        s_l3[e] = __ldcg(pp + RW * D + RW + r);
+                    }
+                    __syncthreads();
+                    if (tid < 32) {
+                        const float old = s_M[tid];
+                        float M = old, sum = 0.f;
+                        for (unsigned i = 0; i < nn; ++i) M = fmaxf(M, s_f2[i * 32 + tid]);
+                        for (unsigned i = 0; i < nn; ++i) {
+                            const float m = s_f2[i * 32 + tid], f = m == NEG_INF ? 0.f : ex2(m - M);
+                            s_f2[i * 32 + tid] = f;
+                            sum += f * s_l3[i * 32 + tid];
+                        }
+                        const float fo = old == NEG_INF ? 0.f : ex2(old - M);
+                        s_f[tid] = fo;
+                        s_M[tid] = M;
+                        s_L[tid] = s_L[tid] * fo + sum;
+                    }
+                    __syncthreads();
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
+                        if (worker && hf + 2 * t < NR) {
+                            float f8[8];
+                            row8(s_f, hf + 2 * t, f8);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int r = min(8 * (hf + 2 * t) + i, R - 1);
-                            x[t][i] = __ldcg(pp + r * D + key);
-                            pm[t][i] = __ldcg(pp + RW * D + r);
-                            pl[t][i] = __ldcg(pp + RW * D + RW + r);
+                            for (int i = 0; i < 8; ++i) run[t][i] *= f8[i];
+#pragma unroll 1
+                            for (unsigned i0 = 0; i0 < nn; i0 += 4) {
+                                float x[4][8];
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    const float* pp = part(c0 + n0 + min(i0 + k, nn - 1)) + 8 * (hf + 2 * t) * D + key;
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) x[k][i] = __ldcg(pp + i * D);
+                                }
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    if (i0 + k < nn) {
+                                        row8(s_f2 + (i0 + k) * 32, hf + 2 * t, f8);
+#pragma unroll
+                                        for (int i = 0; i < 8; ++i) run[t][i] += x[k][i] * f8[i];
+                                    }
+                            }
                         }
-#pragma unroll
-                    for (int t = 0; t < NT; ++t)
-#pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const float f = pm[t][i] == NEG_INF ? 0.f : ex2(pm[t][i] - s_M[min(8 * (hf + 2 * t) + i, R - 1)]);
-                            v[t][i] += x[t][i] * f;
-                            sum[t][i] += pl[t][i] * f;
-                        }
+                    __syncthreads();
                 }
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const int r = 8 * (hf + 2 * t) + i;
-                        if (worker && r < R) store(r, v[t][i], sum[t][i]);
+                        if (worker && r < R) store(r, run[t][i], s_L[r]);
                     }
             }
         }

@@ -334,7 +334,7 @@ def test_refusals_leave_outputs_untouched(qv):
     assert qv.qv_attention_kv4_workspace_bytes(1, 1, 4, 3, 64, 2) == 0
     out = torch.full((T, Hq * D), 7.0, device="cuda")
     for call in (lambda: qv.qv_attention_verify_kv4(qkv.cuda(), cu(cache), cu(ln), T, Hq, Hkv, 0.0, out, ws),
-                 lambda: qv.qv_attention_verify_kv4(qkv.cuda(), cu(cache), cu(ln), T, Hq, Hkv, 0.1, out, ws[:4096])):
+                 lambda: qv.qv_attention_verify_kv4(qkv.cuda(), cu(cache), cu(ln), T, Hq, Hkv, 0.1, out, ws[:-16])):
         with pytest.raises(qv.QVError):
             call()
     torch.cuda.synchronize()
