@@ -23,7 +23,7 @@ constexpr size_t kCounterBytes = 4096;         // at the workspace's start, what
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTileCost = 12;                   // units' worth of a tile's own costs
 constexpr int kMaxCluster = 8;                  // CTAs of a cluster that share a tile
-constexpr int kClusterUnits = 8;                // a larger cluster while its CTAs have more units than this
+constexpr int kClusterUnits = 6;                // a larger cluster while its CTAs have more units than this
 constexpr int kClusterMost = 48;                // no clusters above so many units a CTA
 constexpr int kTcMinUnits = 8;                  // the same for the tcgen05 kernel: two steps of 128 positions,
 constexpr int kTcTileCost = 12;                 // and a tile's costs

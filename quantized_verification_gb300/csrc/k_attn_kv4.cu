@@ -174,6 +174,20 @@ __global__ void __launch_bounds__(Layout<D, NR>::Threads, Layout<D, NR>::Ctas) a
         const int kh = ti / a.RT, rt = ti - kh * a.RT;
         const int r0 = rt * a.rows, R = min(a.rows, a.T * a.G - r0);   // query rows of this tile
 
+        // ---- the queries (word w of a row's 16-byte piece at dims t4 * D/4 + 8 w
+        // holds the pairs (d, d + 4) of two k steps), requested before anything waits
+        constexpr int QLoads = (NR * W * 32 + kThreads - 1) / kThreads;
+        uint4 qraw[QLoads];
+#pragma unroll
+        for (int i = 0; i < QLoads; ++i) {
+            const int e = tid + i * kThreads, ln = e & 31, w = (e >> 5) % W, r = 8 * ((e >> 5) / W) + (ln >> 2);
+            qraw[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < R) {
+                const int j = (r0 + r) / a.G, h = kh * a.G + (r0 + r) - j * a.G;
+                qraw[i] = *reinterpret_cast<const uint4*>(a.qkv + ((size_t)b * a.T + j) * rowlen + (size_t)h * D + (ln & 3) * (D / 4) + 8 * w);
+            }
+        }
+
         int next = ua + warp;                                    // next unit to request, and its page
         const int last = min(ub, nc);
         // (the table's entry is looked at only when it is used, a unit later)
@@ -204,19 +218,17 @@ __global__ void __launch_bounds__(Layout<D, NR>::Threads, Layout<D, NR>::Ctas) a
 #pragma unroll 1
         for (int s = 0; s < S; ++s) issue();
 
-        // ---- the query fragments: word w of the row's 16-byte piece at dims
-        // t4 * D/4 + 8 w holds the pairs (d, d + 4) of two k steps
-        for (int e = tid; e < NR * W * 32; e += kThreads) {
-            const int ln = e & 31, w = (e >> 5) % W, nt = (e >> 5) / W;
-            const int r = 8 * nt + (ln >> 2);
-            uint4 q = make_uint4(0u, 0u, 0u, 0u);
-            if (r < R) {
-                const int j = (r0 + r) / a.G, h = kh * a.G + (r0 + r) - j * a.G;
-                q = *reinterpret_cast<const uint4*>(a.qkv + ((size_t)b * a.T + j) * rowlen + (size_t)h * D + (ln & 3) * (D / 4) + 8 * w);
+        // ---- the query fragments, permuted to match
+#pragma unroll
+        for (int i = 0; i < QLoads; ++i) {
+            const int e = tid + i * kThreads;
+            if (e < NR * W * 32) {
+                const int ln = e & 31, w = (e >> 5) % W, nt = (e >> 5) / W;
+                const uint4 q = qraw[i];
+                uint2* dst = reinterpret_cast<uint2*>(smem + Ly::Q) + (nt * KS + 2 * w) * 32 + ln;
+                dst[0] = make_uint2(__byte_perm(q.x, q.z, 0x5410), __byte_perm(q.x, q.z, 0x7632));
+                dst[32] = make_uint2(__byte_perm(q.y, q.w, 0x5410), __byte_perm(q.y, q.w, 0x7632));
             }
-            uint2* dst = reinterpret_cast<uint2*>(smem + Ly::Q) + (nt * KS + 2 * w) * 32 + ln;
-            dst[0] = make_uint2(__byte_perm(q.x, q.z, 0x5410), __byte_perm(q.x, q.z, 0x7632));
-            dst[32] = make_uint2(__byte_perm(q.y, q.w, 0x5410), __byte_perm(q.y, q.w, 0x7632));
         }
         __syncthreads();
         uint2 qf[Ly::QRegs ? NR : 1][Ly::QRegs ? KS : 1];
@@ -587,13 +599,28 @@ __global__ void __launch_bounds__(Layout<D, NR>::Threads, Layout<D, NR>::Ctas) a
                 }
             }
         __syncthreads();
-        constexpr int Plane = NR * 4 * KS * 32;                  // [warp][(nt, c, tile)][lane]
+        constexpr int Plane = NR * 4 * (W / 2) * 32;             // float4: [warp][(nt, c, word)][lane], the word's 4 tiles
+        float4* s_area4 = reinterpret_cast<float4*>(s_area);
 #pragma unroll
         for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
             for (int q = 0; q < 4; ++q)
 #pragma unroll
-                for (int i = 0; i < KS; ++i) s_area[warp * Plane + ((nt * 4 + q) * KS + i) * 32 + lane] = o[i][nt][q];
+                for (int w = 0; w < W / 2; ++w)
+                    s_area4[warp * Plane + ((nt * 4 + q) * (W / 2) + w) * 32 + lane] =
+                        make_float4(o[4 * w][nt][q], o[4 * w + 1][nt][q], o[4 * w + 2][nt][q], o[4 * w + 3][nt][q]);
+        // each warp's weight for a row, the row's maximum and sum (m and l in place)
+        if (tid < RW) {
+            float M = s_wm[tid], l = 0.f;
+            for (int x = 1; x < kWarps; ++x) M = fmaxf(M, s_wm[x * RW + tid]);
+            for (int x = 0; x < kWarps; ++x) {
+                const float m = s_wm[x * RW + tid], f = m == NEG_INF ? 0.f : ex2(m - M);
+                l += f * s_wl[x * RW + tid];
+                s_wm[x * RW + tid] = f;
+            }
+            s_wl[tid] = M;
+            s_wl[RW + tid] = l;
+        }
         __syncthreads();
 
         // ---- items of 4 dims of one row: (nt, e, word, half, lane); the warps'
@@ -606,20 +633,15 @@ __global__ void __launch_bounds__(Layout<D, NR>::Threads, Layout<D, NR>::Ctas) a
         };
         auto item_sum = [&](int it, int r, int d0, float (&v)[4], float& M, float& l) {
             const int ln = it & 31, q = it >> 5, hf = q & 1, w = (q >> 1) % (W / 2), ne = (q >> 1) / (W / 2);
-            M = s_wm[r];
-#pragma unroll
-            for (int x = 1; x < kWarps; ++x) M = fmaxf(M, s_wm[x * RW + r]);
-            l = 0.f;
+            M = s_wl[r];
+            l = s_wl[RW + r];
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[j] = 0.f;
 #pragma unroll
             for (int x = 0; x < kWarps; ++x) {
-                const float m = s_wm[x * RW + r];
-                const float f = m == NEG_INF ? 0.f : ex2(m - M);
-                l += f * s_wl[x * RW + r];
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    v[j] += f * s_area[x * Plane + (((ne >> 1) * 4 + 2 * hf + (ne & 1)) * KS + 4 * w + j) * 32 + ln];
+                const float f = s_wm[x * RW + r];
+                const float4 y = s_area4[x * Plane + (((ne >> 1) * 4 + 2 * hf + (ne & 1)) * (W / 2) + w) * 32 + ln];
+                v[0] += f * y.x; v[1] += f * y.y; v[2] += f * y.z; v[3] += f * y.w;
             }
             if (s_flag[0] && r < R) {                            // rare: own value rows that are not finite
                 const int tk = (r0 + r) / a.G;
@@ -810,13 +832,6 @@ cudaError_t launch(const Args& a, int grid, cudaStream_t s) {                  /
 #endif
 constexpr int kTcRows = KTCROWS;
 
-// Row tiles of a head group's T * G query rows, and rows per tile: as few
-// tiles of at most 32 rows as there can be, of equal size.
-void row_tiles(int rows, int& RT, int& per) {
-    RT = (rows + kRowTile - 1) / kRowTile;
-    per = (rows + RT - 1) / RT;
-}
-
 struct Plan {
     int RT, rows, NR;
     int C;                       // CTAs of the cluster that takes a tile, or 0: one line of units cut into equal ranges
@@ -825,14 +840,32 @@ struct Plan {
     size_t total;                // workspace bytes; 0: more units than the kernel's 32-bit places can count
 };
 Plan plan(int B, int T, int Hq, int Hkv, int D, int NB, int sms) {
+    const int rows = T * (Hq / Hkv);
+    const long long units = (long long)NB + (T + 31) / 32;     // of a tile at most
     Plan p;
-    row_tiles(T * (Hq / Hkv), p.RT, p.rows);
-    p.NR = (p.rows + 7) / 8;
-    const long long tiles = (long long)B * Hkv * p.RT, units = (long long)NB + (T + 31) / 32;   // units of a tile at most
-    const int slots = sms * (D / 64 * p.NR <= 4 ? 2 : 1);      // CTAs the GPU holds
+    long long tiles = 0;
+    int slots = 0;
+    // The head group's rows in as few tiles of at most `most` rows as there can
+    // be, of equal size.
+    auto cut = [&](int most) {
+        p.RT = (rows + most - 1) / most;
+        p.rows = (rows + p.RT - 1) / p.RT;
+        p.NR = (p.rows + 7) / 8;
+        tiles = (long long)B * Hkv * p.RT;
+        slots = sms * (D / 64 * p.NR <= 4 ? 2 : 1);            // CTAs the GPU holds
+    };
+    // Short contexts: tiles of 8 rows (each reads the cache, from L2) while they
+    // and their clusters all fit the GPU at once. GB300, 5 tokens over 2043
+    // positions: 24 tiles of 7 rows 8.5 us, 8 tiles of 20 rows 10.9 us.
+    cut(8);
     p.C = 1;
-    while (p.C < kMaxCluster && tiles * p.C * 2 <= slots && units > kClusterUnits * p.C) p.C *= 2;
-    if (tiles * p.C > slots || units > kClusterMost * p.C) p.C = 0;
+    while (p.C < kMaxCluster && units > (long long)kClusterUnits * p.C) p.C *= 2;
+    if (tiles * p.C > slots || units > (long long)kClusterMost * p.C) {
+        cut(kRowTile);
+        p.C = 1;
+        while (p.C < kMaxCluster && tiles * p.C * 2 <= slots && units > (long long)kClusterUnits * p.C) p.C *= 2;
+        if (tiles * p.C > slots || units > (long long)kClusterMost * p.C) p.C = 0;
+    }
     p.tc = p.C == 0 && D == 128 && p.NR >= kTcRows;
     p.cost = p.tc ? kTcTileCost : kTileCost;
     p.min_units = p.tc ? kTcMinUnits : kMinUnits;
