@@ -1,7 +1,7 @@
 // attn_kv4_common.cuh -- what the two kernels of attention over the 4-bit cache
-// share (k_attn_kv4.cu: heads of 64 values on mma.sync; k_attn_kv4_tc.cu: heads
-// of 128 on tcgen05): the arguments, the cut of the work into places, the
-// unpacking of codes, and the waits.
+// share (k_attn_kv4.cu on mma.sync; k_attn_kv4_tc.cu on tcgen05, for heads of 128
+// values and long contexts): the arguments, the cut of the work into places,
+// the unpacking of codes, and the waits.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -18,15 +18,15 @@ namespace kv4attn {
 
 constexpr int kRowTile = 32;                    // query rows of a tile
 constexpr int kMinUnits = 16;                   // places of a CTA's range at least: two units a warp
-#define QV_ATTN_MAX_T 256                       // tokens of a step (QV_MAX_M)
+constexpr int kAttnMaxT = 256;                  // tokens of a step (QV_MAX_M)
 constexpr size_t kCounterBytes = 4096;         // at the workspace's start, whatever the shape
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kTileCost = 12;                   // units' worth of a tile's own costs
+constexpr int kTileCost = 26;                   // units' worth of a tile's own costs
 constexpr int kMaxCluster = 8;                  // CTAs of a cluster that share a tile
 constexpr int kClusterUnits = 6;                // a larger cluster while its CTAs have more units than this
 constexpr int kClusterMost = 48;                // no clusters above so many units a CTA
 constexpr int kTcMinUnits = 8;                  // the same for the tcgen05 kernel: two steps of 128 positions,
-constexpr int kTcTileCost = 12;                 // and a tile's costs
+constexpr int kTcTileCost = 32;                 // and a tile's costs
 constexpr float kLazy = 8.f;                    // log2 of the growth a running maximum may lag behind
 constexpr float kBias = 7.f;                    // log2 of p at the running maximum: 2^(kBias + kLazy + 0.5) < 65504
 
@@ -37,7 +37,7 @@ struct Args {
     const int32_t* len;        // [B]
     int B, T, Hq, Hkv, G, NB, pages;
     int RT, rows;              // row tiles per head group, query rows per row tile
-    int C;                     // CTAs of the cluster that takes a tile, or 0 (k_attn_kv4.cu)
+    int C;                     // CTAs of the cluster that takes a tile, or 0: the line of units
     float scale;
     void* out;                 // [B*T][Hq D] fp32 or bf16
     unsigned* counters;        // [grid] arrivals at the tile that begins in CTA i's range (zero between calls)
@@ -200,6 +200,24 @@ __device__ __forceinline__ bool find_range(const Args& a, int own_units, int cos
     static_assert(Threads / 32 <= 14, "s_scan");
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int tps = a.Hkv * a.RT;                              // tiles of a sequence
+    if (a.B <= 32) {                                           // each warp for itself: nothing to wait for
+        unsigned mine = 0;
+        if (lane < a.B) mine = (unsigned)(((seq_len(a, lane) + kKv4Block - 1) / kKv4Block + own_units + cost) * tps);
+        unsigned incl = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const unsigned v = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += v;
+        }
+        const unsigned total = __shfl_sync(0xffffffffu, incl, 31);
+        g.per = max((total + gridDim.x - 1) / gridDim.x, (unsigned)min_units);
+        g.u0 = g.per * blockIdx.x;
+        g.u1 = min(total, g.u0 + g.per);
+        if (g.u0 >= g.u1) return false;
+        g.b = __ffs(__ballot_sync(0xffffffffu, incl > g.u0)) - 1;   // the first sequence that ends behind u0
+        g.seq_at = __shfl_sync(0xffffffffu, incl - mine, g.b);
+        return true;
+    }
     const int seg = (a.B + Threads - 1) / Threads;             // sequences per thread
     unsigned mine = 0;
     for (int b = tid * seg; b < min(a.B, (tid + 1) * seg); ++b)

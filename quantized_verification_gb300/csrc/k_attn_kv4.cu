@@ -9,20 +9,27 @@
 //
 // Work split. A tile is one (sequence, key/value head, group of at most 32 of
 // its T * Hq/Hkv query rows); a unit is one record of 32 cached positions, or
-// 32 of the step's own rows. The units of all tiles, sequence by sequence,
-// form one line that the CTAs cut into equal ranges, so that ragged lengths
-// leave no SM idle. A tile that lies in one range is written by its CTA; one
-// that is cut leaves partial results (running maximum, running sum, weighted
-// values) in the workspace, and the last of its CTAs to arrive adds them in
-// range order. Nobody waits for anybody, and the order of arrival changes
-// nothing.
+// 32 of the step's own rows. Two ways to share the units, by plan():
+//   Clusters, where every tile can have CTAs of its own: up to 8 CTAs take
+//     equal parts of one tile and add their results through each other's shared
+//     memory (each owns a part of the outputs), one barrier. Short contexts.
+//   One line: the units of all tiles, sequence by sequence, form one line that
+//     the CTAs cut into equal ranges, so that ragged lengths leave no SM idle.
+//     A tile that lies in one range is written by its CTA; one that is cut
+//     leaves partial results (running maximum, running sum, weighted values) in
+//     the workspace, and the last of its CTAs to arrive adds them in range
+//     order. Nobody waits for anybody, and the order of arrival changes
+//     nothing. Every tile takes kTileCost places more than its units (its start
+//     and its end; GB300, 64 sequences of 1 to 2500 positions: 89 us with 12,
+//     67 us with 24 or more).
 //
 // Inside a CTA each of the W warps (8 or 12) takes every W-th unit of the range
-// and keeps its own online softmax. A record comes in one bulk copy into the warp's own
-// ring. Both products run on the tensor cores (mma.sync m16n8k16, bf16
-// operands, fp32 accumulation) with the keys, or the value dims, on the M side
-// and the query rows on the N side in tiles of 8: a verify step has 4 to 32
-// rows per head group, far too few to fill a tcgen05 tile's 128.
+// and keeps its own online softmax; the step's own rows are warp 0's, which
+// gets one unit less (76 us without that on the same batch). A record comes in
+// one bulk copy into the warp's own ring. Both products run on the tensor cores
+// (mma.sync m16n8k16, fp32 accumulation) with the keys, or the value dims, on
+// the M side and the query rows on the N side in tiles of 8: few rows do not
+// fill a tcgen05 tile's 128 (k_attn_kv4_tc.cu takes over from 17 rows, kTcRows).
 //   S^T = K Q^T:  in bf16. Codes become bf16 values exactly (kv4_common.cuh): a nibble
 //     shifted to bits 3..6 under the pattern of 16.0 is the number 24 + q, and
 //     one fused multiply-add gives (24 + q) s - 24 s = q s without rounding.
@@ -188,8 +195,16 @@ __global__ void __launch_bounds__(Layout<D, NR>::Threads, Layout<D, NR>::Ctas) a
             }
         }
 
-        int next = ua + warp;                                    // next unit to request, and its page
+        // The cached units go round the warps; the step's own rows, which take
+        // about as long as one, are warp 0's, which sits out the first round.
         const int last = min(ub, nc);
+        const bool own = ub > nc;
+        auto unit_of = [&](int round) {
+            const int slot = (round + (own && warp == 0 ? 1 : 0)) * kWarps + warp;
+            return ua + slot - (own ? 1 : 0);
+        };
+        int round_issue = 0;
+        int next = unit_of(0);                                   // next unit to request, and its page
         // (the table's entry is looked at only when it is used, a unit later)
         auto page_of = [&](int unit) {
             return unit >= last ? -1 : (a.table ? a.table[(size_t)b * a.NB + unit] : b * a.NB + unit);
@@ -212,7 +227,7 @@ __global__ void __launch_bounds__(Layout<D, NR>::Threads, Layout<D, NR>::Ctas) a
                 }
             }
             ++issued;
-            next += kWarps;
+            next = unit_of(++round_issue);
             page = page_of(next);
         };
 #pragma unroll 1
@@ -361,9 +376,8 @@ __global__ void __launch_bounds__(Layout<D, NR>::Threads, Layout<D, NR>::Ctas) a
 
         // ---- the step's own rows, straight from the qkv rows (bf16), while the
         // first records are on their way: unit nc + i holds rows 32 i .. 32 i + 31
-        // and belongs to the warp that comes next in the units' order
 #pragma unroll 1
-        for (int un = max(ua, nc) + (warp + kWarps - (max(ua, nc) - ua) % kWarps) % kWarps; un < ub; un += kWarps) {
+        for (int un = max(ua, nc) + warp; un < ub; un += kWarps) {
             const uint16_t* base = a.qkv + (size_t)b * a.T * rowlen + (size_t)(a.Hq + kh) * D;
             bool bad = false;
 #pragma unroll 1
@@ -501,7 +515,7 @@ __global__ void __launch_bounds__(Layout<D, NR>::Threads, Layout<D, NR>::Ctas) a
         };
         if constexpr (!Ly::Pipe) {
 #pragma unroll 1
-            for (int un = ua + warp; un < last && !dead; un += kWarps) {
+            for (int round = 0, un = unit_of(0); un < last && !dead; un = unit_of(++round)) {
                 const int left = take(un, used);
                 if (left < 0) break;
                 const uint32_t rec = ring + (uint32_t)((used % S) * Rec::Bytes);
@@ -524,13 +538,13 @@ __global__ void __launch_bounds__(Layout<D, NR>::Threads, Layout<D, NR>::Ctas) a
         } else {
             // acc: the products of the present step (record, p0); nxt: those of
             // the following one, formed between the present one's tiles of P V
-            int un = ua + warp;
+            int round = 0, un = unit_of(0);
             int left = 0;                                        // of the present record
             while (un < last && !dead) {                         // the first record with a page
                 left = take(un, used);
                 if (left != 0) break;
                 done();
-                un += kWarps;
+                un = unit_of(++round);
             }
             if (left > 0) {
                 uint32_t rec = ring + (uint32_t)((used % S) * Rec::Bytes);
@@ -554,7 +568,7 @@ __global__ void __launch_bounds__(Layout<D, NR>::Threads, Layout<D, NR>::Ctas) a
                     if (p0 >= left) {
                         fresh = true;
                         p0 = 0;
-                        un += kWarps;
+                        un = unit_of(++round);
                         if (un < last) {
                             left = take(un, used + 1);
                             if (left < 0) break;
@@ -736,51 +750,84 @@ __global__ void __launch_bounds__(Layout<D, NR>::Threads, Layout<D, NR>::Ctas) a
             }
             __syncthreads();
             if (s_flag[1]) {
-                // the tile's parts, added in range order at a running maximum;
-                // kAhead of them are loaded at a time
+                // The tile's parts, added in range order at the rows' maxima, kParts
+                // of them at a time: first their weights (in the ring), then their
+                // items, kAhead parts' loads in flight.
+                constexpr int kParts = 64;
                 constexpr int Own = (Ly::Items + kThreads - 1) / kThreads;    // items of a thread
-                constexpr int kAhead = Own >= 3 ? 2 : 4;
-                float v[Own][4], M[Own], l[Own];
+                constexpr int kAhead = Own >= 3 ? 3 : (Own == 2 ? 4 : 8);
+                static_assert((2 * kParts + 3) * RW * 4 <= Ly::RingBytes, "the parts' weights fit the ring");
+                float* w_f = s_area;                             // [kParts][RW] maxima, then weights
+                float* w_l = w_f + kParts * RW;
+                float* w_M = w_l + kParts * RW;                  // [RW] so far: maximum, sum, the last rescaling
+                float* w_L = w_M + RW;
+                float* w_r = w_L + RW;
+                const unsigned n = c1 - c0 + 1;
+                auto part = [&](unsigned ci) { return a.partials + ((size_t)ci * 2 + (ci == c0 ? 1 : 0)) * Ly::Slot; };
+                float v[Own][4];
 #pragma unroll
-                for (int k = 0; k < Own; ++k) {
-                    M[k] = NEG_INF;
-                    l[k] = 0.f;
+                for (int k = 0; k < Own; ++k)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) v[k][j] = 0.f;
+                if (tid < RW) {
+                    w_M[tid] = NEG_INF;
+                    w_L[tid] = 0.f;
                 }
 #pragma unroll 1
-                for (unsigned cc = c0; cc <= c1; cc += kAhead) {
-                    float4 x[kAhead][Own];
-                    float pm[kAhead][Own], pl[kAhead][Own];
-#pragma unroll
-                    for (int i = 0; i < kAhead; ++i) {
-                        const unsigned ci = min(cc + i, c1);
-                        const float* part = a.partials + ((size_t)ci * 2 + (ci == c0 ? 1 : 0)) * Ly::Slot;
-#pragma unroll
-                        for (int k = 0; k < Own; ++k) {
-                            const int it = min(tid + k * kThreads, Ly::Items - 1);
-                            int r, d0;
-                            item_at(it, r, d0);
-                            x[i][k] = __ldcg(reinterpret_cast<const float4*>(part + it * 4));
-                            pm[i][k] = cc + i <= c1 ? __ldcg(part + RW * D + r) : NEG_INF;
-                            pl[i][k] = __ldcg(part + RW * D + RW + r);
-                        }
+                for (unsigned n0 = 0; n0 < n; n0 += kParts) {
+                    const unsigned nn = min(n - n0, (unsigned)kParts);
+                    for (unsigned e = tid; e < nn * RW; e += kThreads) {
+                        const float* pp = part(c0 + n0 + e / RW) + RW * D + e % RW;
+                        w_f[e] = __ldcg(pp);
+                        w_l[e] = __ldcg(pp + RW);
                     }
-#pragma unroll
-                    for (int i = 0; i < kAhead; ++i)
-#pragma unroll
-                        for (int k = 0; k < Own; ++k) {
-                            const float Mn = fmaxf(M[k], pm[i][k]);
-                            const float fo = M[k] == NEG_INF ? 0.f : ex2(M[k] - Mn);
-                            const float fn = pm[i][k] == NEG_INF ? 0.f : ex2(pm[i][k] - Mn);
-                            M[k] = Mn;
-                            // (a part without a visible key adds 0, or NaN if its row saw one)
-                            l[k] = l[k] * fo + pl[i][k] * fn;
-                            v[k][0] = v[k][0] * fo + x[i][k].x * fn;
-                            v[k][1] = v[k][1] * fo + x[i][k].y * fn;
-                            v[k][2] = v[k][2] * fo + x[i][k].z * fn;
-                            v[k][3] = v[k][3] * fo + x[i][k].w * fn;
+                    __syncthreads();
+                    if (tid < RW) {
+                        const float old = w_M[tid];
+                        float M = old, sum = 0.f;
+                        for (unsigned i = 0; i < nn; ++i) M = fmaxf(M, w_f[i * RW + tid]);
+                        for (unsigned i = 0; i < nn; ++i) {
+                            const float m = w_f[i * RW + tid], f = m == NEG_INF ? 0.f : ex2(m - M);
+                            w_f[i * RW + tid] = f;
+                            sum += f * w_l[i * RW + tid];
                         }
+                        const float fo = old == NEG_INF ? 0.f : ex2(old - M);
+                        w_r[tid] = fo;
+                        w_M[tid] = M;
+                        w_L[tid] = w_L[tid] * fo + sum;
+                    }
+                    __syncthreads();
+                    int r[Own];
+#pragma unroll
+                    for (int k = 0; k < Own; ++k) {
+                        int d0;
+                        item_at(min(tid + k * kThreads, Ly::Items - 1), r[k], d0);
+                        const float fo = w_r[r[k]];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) v[k][j] *= fo;
+                    }
+#pragma unroll 1
+                    for (unsigned i0 = 0; i0 < nn; i0 += kAhead) {
+                        float4 x[kAhead][Own];
+#pragma unroll
+                        for (int i = 0; i < kAhead; ++i) {
+                            const float* pp = part(c0 + n0 + min(i0 + i, nn - 1));
+#pragma unroll
+                            for (int k = 0; k < Own; ++k)
+                                x[i][k] = __ldcg(reinterpret_cast<const float4*>(pp) + min(tid + k * kThreads, Ly::Items - 1));
+                        }
+#pragma unroll
+                        for (int i = 0; i < kAhead; ++i)
+                            if (i0 + i < nn) {
+#pragma unroll
+                                for (int k = 0; k < Own; ++k) {
+                                    const float f = w_f[(i0 + i) * RW + r[k]];
+                                    v[k][0] += f * x[i][k].x; v[k][1] += f * x[i][k].y;
+                                    v[k][2] += f * x[i][k].z; v[k][3] += f * x[i][k].w;
+                                }
+                            }
+                    }
+                    __syncthreads();
                 }
 #pragma unroll
                 for (int k = 0; k < Own; ++k) {
@@ -788,7 +835,7 @@ __global__ void __launch_bounds__(Layout<D, NR>::Threads, Layout<D, NR>::Ctas) a
                     if (it < Ly::Items) {
                         int r, d0;
                         item_at(it, r, d0);
-                        store(r, d0, v[k], l[k]);
+                        store(r, d0, v[k], w_L[r]);
                     }
                 }
             }
@@ -827,10 +874,12 @@ cudaError_t launch(const Args& a, int grid, cudaStream_t s) {                  /
     return cudaLaunchKernelEx(&cfg, attn_kv4_kernel<D, NR, OUTBF>, a);
 }
 
-#ifndef KTCROWS
-#define KTCROWS 3
-#endif
-constexpr int kTcRows = KTCROWS;
+// Tiles of so many groups of 8 rows, heads of 128, go to the tcgen05 kernel:
+// its time hardly depends on the rows of a tile, this kernel's grows with them.
+// GB300, fp32 out, here / there in us for 8, 16, 24, 32 rows: 2 sequences of
+// 131071 positions 78/108, 110/115, 135/129, 185/145; 24 of 8000 63/86, 89/93,
+// 115/107, 147/121.
+constexpr int kTcRows = 3;
 
 struct Plan {
     int RT, rows, NR;
@@ -856,7 +905,9 @@ Plan plan(int B, int T, int Hq, int Hkv, int D, int NB, int sms) {
     };
     // Short contexts: tiles of 8 rows (each reads the cache, from L2) while they
     // and their clusters all fit the GPU at once. GB300, 5 tokens over 2043
-    // positions: 24 tiles of 7 rows 8.5 us, 8 tiles of 20 rows 10.9 us.
+    // positions: 24 tiles of 7 rows 8.5 us, 8 tiles of 20 rows 10.9 us; where
+    // they do not fit it is the other way round (5 tokens, 16 sequences of 300:
+    // 17.3 us against 11.2).
     cut(8);
     p.C = 1;
     while (p.C < kMaxCluster && units > (long long)kClusterUnits * p.C) p.C *= 2;

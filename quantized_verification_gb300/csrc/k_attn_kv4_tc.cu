@@ -1,13 +1,16 @@
 // k_attn_kv4_tc.cu -- attention over the 4-bit paged KV cache for heads of 128
-// values, on the tcgen05 tensor cores.
+// values, tiles of 17 to 32 query rows and long contexts, on the tcgen05 tensor
+// cores.
 //
 //   What is computed, the cut of the work into tiles, units and places, and the
 //   arithmetic (exact unpacking, base-2 probabilities with a lazy whole-number
 //   maximum, two f16 parts of P for fp32 outputs) are k_attn_kv4.cu's; only the
-//   products are formed elsewhere. On mma.sync the 20 query rows of a 5-token
-//   step kept the legacy tensor pipe busy about as long as the unpacking the
-//   ALUs, with too few warps to overlap the two (137 us for one step of 5 tokens
-//   over 2 x 131071 positions; 42 us to read the cache).
+//   products are formed elsewhere. On mma.sync 17 to 32 query rows keep the legacy
+//   tensor pipe busy about as long as the unpacking the ALUs, with too few warps
+//   to overlap the two. GB300, fp32 out, 2 x 131071 positions, 8 key/value heads:
+//   24 rows 129 us against 135, 32 rows 145 us against 185 (41 us to read the
+//   cache); 24 x 8000 positions, 24 rows: 107 us against 115. Below 17 rows the
+//   other kernel is faster (its kTcRows has the figures).
 //
 // A CTA takes 128 positions (4 records) a step. 8 warps work on them, a ninth
 // requests records and issues the products; they meet at mbarriers, and the
@@ -70,7 +73,7 @@ struct TcLayout {
     static constexpr int Cols = 256;
     static_assert(Bar % 8 == 0 && Row % 16 == 0 && Ring % 16 == 0, "alignment");
     static_assert(2 * kTcMaxParts * 32 * 4 <= 2 * kTcKeys * 128, "the parts' weights fit the value buffer");
-    static_assert(kRowTile * QV_ATTN_MAX_T * 4 <= 2 * kTcKeys * 128, "the own scores fit the value buffer");
+    static_assert(kRowTile * kAttnMaxT * 4 <= 2 * kTcKeys * 128, "the own scores fit the value buffer");
 };
 
 // Shared-memory descriptor of an operand stored with the M (or N) dimension
@@ -770,7 +773,7 @@ cudaError_t launch_attn_kv4_tc(const kv4attn::Args& a, int NR, bool out_bf16, in
                                cudaStream_t s) {
 #define QV_KV4_TC_CASE(NRV) \
     if (NR == NRV) return out_bf16 ? launch<NRV, true>(a, grid, tile_cost, min_units, s) : launch<NRV, false>(a, grid, tile_cost, min_units, s);
-    QV_KV4_TC_CASE(1) QV_KV4_TC_CASE(2) QV_KV4_TC_CASE(3) QV_KV4_TC_CASE(4)
+    QV_KV4_TC_CASE(3) QV_KV4_TC_CASE(4)
 #undef QV_KV4_TC_CASE
     return cudaErrorInvalidValue;
 }

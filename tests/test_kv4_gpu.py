@@ -364,3 +364,144 @@ def test_a_wait_that_runs_out_is_reported(qv):
     want, vmax, smax = ref.attend(qkv.float().numpy(), cache, ln, T, Hq, Hkv, D, NB, scale, table)
     close(out, want, vmax, smax, D)
     assert qv.qv_device_error() == 0
+
+
+# Contexts that may be long, or more tiles than the GPU holds CTAs: the units of all tiles cut into equal ranges,
+# parts of tiles joined through the workspace.
+LINES = [  # B, T, Hq, Hkv, D, NB, lens, paged
+    (1, 1, 4, 1, 128, 420, [13440], False),
+    (2, 3, 8, 2, 128, 400, [12800, 77], True),                 # 12 rows a tile
+    (2, 5, 8, 2, 128, 400, [12345, 4097], True),               # 20 rows
+    (3, 5, 8, 2, 128, 390, [0, 31, 9000], False),
+    (1, 8, 8, 2, 128, 390, [12480], True),                     # 32 rows
+    (1, 9, 8, 2, 128, 400, [12001], False),                    # 36 rows: two tiles of 18
+    (2, 256, 2, 1, 128, 400, [50, 6000], True),                # the longest step, 16 tiles of 32 rows
+    (1, 2, 4, 1, 64, 400, [12799], True),
+    (2, 4, 8, 2, 64, 400, [1, 12001], False),                  # 16 rows
+    (3, 6, 8, 2, 64, 400, [12800, 1, 5000], True),             # 24 rows
+    (1, 8, 8, 2, 64, 400, [12333], False),                     # 32 rows
+    (200, 2, 4, 4, 128, 3, None, True),                        # 800 tiles of 2 rows
+    (160, 5, 8, 2, 128, 5, None, True),                        # 320 tiles of 20 rows
+    (31, 20, 40, 20, 128, 2, None, False),                     # 40 rows a head group
+    (700, 1, 4, 1, 128, 2, None, True),
+    (200, 7, 6, 2, 64, 3, None, True),                         # 21 rows
+]
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B,T,Hq,Hkv,D,NB,lens,paged", LINES)
+def test_attention_on_one_line(qv, B, T, Hq, Hkv, D, NB, lens, paged, out_dtype):
+    assert qv.qv_attention_kv4_workspace_bytes(B, T, Hq, Hkv, D, NB) > 4096      # parts of tiles have room there
+    test_attention(qv, B, T, Hq, Hkv, D, NB, lens, paged, out_dtype)
+
+
+@pytest.mark.parametrize("T,Hq", [(1, 8), (5, 8), (8, 8)])
+def test_long_attention_ignores_what_is_not_there(qv, T, Hq):
+    """Blocks without a page inside a long context, whole runs of them, and a sequence with nothing else."""
+    B, Hkv, D, NB = 3, 2, 128, 400
+    qkv, cache, ln, table = attend_inputs(B, T, Hq, Hkv, D, NB, [6000, 12800, 900], True)
+    scale = float(np.float32(D ** -0.5))
+    table[0, ::3] = -1
+    table[1, 8:200] = 2 ** 30
+    table[2] = -5
+    args = (qkv.cuda(), cu(cache), cu(ln), T, Hq, Hkv, scale)
+    ws = torch.zeros(qv.qv_attention_kv4_workspace_bytes(B, T, Hq, Hkv, D, NB), dtype=torch.uint8, device="cuda")
+    want, vmax, smax = ref.attend(qkv.float().numpy(), cache, ln, T, Hq, Hkv, D, NB, scale, table)
+    for dt in (torch.float32, torch.bfloat16):
+        out = torch.empty(B * T, Hq * D, dtype=dt, device="cuda")
+        qv.qv_attention_verify_kv4(*args, out, ws, block_table=cu(table))
+        close(out, want, vmax, smax, D)
+
+
+@pytest.mark.parametrize("D,T,Hq,Hkv", [(128, 5, 8, 2), (128, 3, 4, 2), (128, 40, 4, 2), (64, 40, 4, 2)])
+def test_long_attention_keeps_later_rows_out(qv, D, T, Hq, Hkv):
+    """As test_attention_keeps_later_rows_out, where tiles are cut anywhere."""
+    B, NB, j0 = 2, 400, T - 2
+    qkv, cache, ln, table = attend_inputs(B, T, Hq, Hkv, D, NB, [1500, 40], True)
+    scale = float(np.float32(D ** -0.5))
+    ws = torch.zeros(qv.qv_attention_kv4_workspace_bytes(B, T, Hq, Hkv, D, NB), dtype=torch.uint8, device="cuda")
+    want, vmax, smax = ref.attend(qkv.float().numpy(), cache, ln, T, Hq, Hkv, D, NB, scale, table)
+    bad = qkv.clone()
+    for j in (j0, T - 1):
+        bad[j, Hq * D:] = float("nan")
+    bad[T + j0, (Hq + Hkv) * D + 3] = float("inf")
+    G = Hq // Hkv
+    for dt in (torch.float32, torch.bfloat16):
+        out = torch.empty(B * T, Hq * D, dtype=dt, device="cuda")
+        qv.qv_attention_verify_kv4(bad.cuda(), cu(cache), cu(ln), T, Hq, Hkv, scale, out, ws, block_table=cu(table))
+        o = out.view(B, T, Hq, D)
+        keep = torch.ones(B, T, dtype=torch.bool)
+        keep[:, j0:] = False
+        k = keep.view(-1)
+        close(out[k.cuda()], want[k.numpy()], vmax, smax, D)
+        assert bool(o[0, j0:].isnan().all())
+        assert bool((o[1, j0:, :G, 3] == float("inf")).all())
+        rest = o[1, j0:].clone()
+        rest[:, :G, 3] = 0
+        assert bool(rest.isfinite().all())
+
+
+@pytest.mark.parametrize("D,T,Hq", [(128, 1, 4), (128, 5, 4), (128, 8, 4), (64, 6, 4)])
+def test_long_attention_extreme_scores(qv, D, T, Hq):
+    """Scores whose size grows 4000-fold along the cache, so that maxima move all the time, and the format's end
+    scales among the values."""
+    NB = 400
+    qkv, cache, ln, table = attend_inputs(1, T, Hq, 1, D, NB, [32 * NB], False, seed=4)
+    for i in range(NB):
+        cache[i, :, 32 * D: 33 * D] = 60 + i // 4
+    cache[:, :, 33 * D:] = np.where(np.arange(D) % 2 == 0, 255, 0)
+    scale = float(np.float32(D ** -0.5))
+    ws = torch.zeros(qv.qv_attention_kv4_workspace_bytes(1, T, Hq, 1, D, NB), dtype=torch.uint8, device="cuda")
+    want, vmax, smax = ref.attend(qkv.float().numpy(), cache, ln, T, Hq, 1, D, NB, scale, table)
+    out = torch.empty(T, Hq * D, device="cuda")
+    qv.qv_attention_verify_kv4(qkv.cuda(), cu(cache), cu(ln), T, Hq, 1, scale, out, ws)
+    close(out, want, vmax, smax, D)
+
+
+@pytest.mark.parametrize("T,D", [(1, 128), (5, 128), (5, 64)])
+def test_a_wait_that_runs_out_on_one_line(qv, T, D):
+    B, Hq, Hkv, NB = 2, 8, 2, 400
+    qkv, cache, ln, table = attend_inputs(B, T, Hq, Hkv, D, NB, [1280, 700], True)
+    scale = D ** -0.5
+    ws = torch.zeros(qv.qv_attention_kv4_workspace_bytes(B, T, Hq, Hkv, D, NB), dtype=torch.uint8, device="cuda")
+    out = torch.empty(B * T, Hq * D, device="cuda")
+    args = (qkv.cuda(), cu(cache), cu(ln), T, Hq, Hkv, scale, out, ws)
+    assert qv.qv_device_error() == 0
+    try:
+        qv.qv_debug_set_slot_wait_ns(2_000_000)
+        qv.qv_debug_hold_attention_loads(1)
+        qv.qv_attention_verify_kv4(*args, block_table=cu(table))
+        assert qv.qv_device_error() == qv.QV_DEVICE_ERR_FULL_WAIT
+    finally:
+        qv.qv_debug_set_slot_wait_ns(0)
+        qv.qv_debug_hold_attention_loads(0)
+    assert int(ws[:4096].max()) == 0
+    qv.qv_attention_verify_kv4(*args, block_table=cu(table))
+    want, vmax, smax = ref.attend(qkv.float().numpy(), cache, ln, T, Hq, Hkv, D, NB, scale, table)
+    close(out, want, vmax, smax, D)
+    assert qv.qv_device_error() == 0
+
+
+def test_a_pool_of_more_than_4_gib(qv):
+    """Records whose byte offsets pass 32 bits are written, read and attended to like others."""
+    B, T, Hq, Hkv, D, NB = 2, 5, 16, 8, 128, 3
+    pages = 2 ** 32 // (Hkv * 34 * D) + 40
+    far = torch.zeros(pages, Hkv, 34 * D, dtype=torch.uint8, device="cuda")
+    near = torch.zeros(B * NB, Hkv, 34 * D, dtype=torch.uint8, device="cuda")
+    t_near = torch.arange(B * NB, dtype=torch.int32, device="cuda").view(B, NB)
+    t_far = pages - 1 - t_near
+    rows = torch.randn(B * 90, (Hq + 2 * Hkv) * D, generator=gen(1)).to(torch.bfloat16).cuda()
+    step = rows[: B * T].contiguous()
+    zero, ln = cu(np.zeros(B, np.int32)), cu(np.full(B, 90, np.int32))
+    ws = torch.zeros(qv.qv_attention_kv4_workspace_bytes(B, T, Hq, Hkv, D, NB), dtype=torch.uint8, device="cuda")
+    got = []
+    for cache, table in ((near, t_near), (far, t_far)):
+        qv.qv_kv4_write(rows, zero, cache, 90, Hq, Hkv, block_table=table)
+        k = torch.empty(B, 90, Hkv, D, dtype=torch.bfloat16, device="cuda")
+        v, out = torch.empty_like(k), torch.empty(B * T, Hq * D, device="cuda")
+        qv.qv_kv4_read(cache, zero, k, v, block_table=table)
+        qv.qv_attention_verify_kv4(step, cache, ln, T, Hq, Hkv, 0.1, out, ws, block_table=table)
+        got.append((k, v, out))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+    assert torch.equal(far[t_far.long()], near[t_near.long()]) and bool((got[0][0] != 0).any())
+    assert int(far[: pages - B * NB].max()) == 0
