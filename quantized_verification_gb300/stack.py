@@ -255,14 +255,32 @@ class VerifyStack:
                      self.accept_len, self.out_tokens, stream=stream)
 
     # ------------------------------------------------------------------ chained layers
-    def prepare_chain(self, eps: float = 1e-6, cache_len: int | None = None, head_dim: int = 128):
+    def prepare_chain(self, eps: float = 1e-6, cache_len: int | None = None, head_dim: int = 128,
+                      kv_bits: int = 16, room: int | None = None):
         """Norm weights, the step's input residual stream and the output
         buffers of the chained step (enqueue_chain). With cache_len, every
         layer also gets a seeded bf16 KV cache of cache_len positions per
         sequence ([B, cache_len, Hkv, head_dim], N(0, 1)) and the chain runs
         attention over it between the qkv and o projections; without it the
-        o projection takes the layer's seeded input."""
+        o projection takes the layer's seeded input.
+
+        kv_bits=4: the same seeded positions go into 4-bit paged caches
+        (qv_kv4_write; one pool of pages per layer, one block table for all),
+        with space for `room` more positions per sequence (default: one step's).
+        The chain then attends with qv_attention_verify_kv4 and writes each
+        layer's rows of the step behind the cached positions; advance_chain
+        makes the accepted ones part of them."""
         self._w8_only("the layer chain")
+        if kv_bits not in (16, 4):
+            raise ValueError("kv_bits must be 16 or 4")
+        if cache_len is None and (kv_bits != 16 or room is not None):
+            raise ValueError("kv_bits and room need a cache_len")
+        if kv_bits == 16 and room is not None:
+            raise ValueError("room needs kv_bits=4: the chain does not write the bf16 cache")
+        if cache_len is not None and (cache_len < 0 or (room or 0) < 0):
+            raise ValueError("cache_len and room must not be negative")
+        if kv_bits == 4 and cache_len + (self.gamma + 1 if room is None else room) < 1:
+            raise ValueError("a 4-bit cache needs space for at least one position")
         h, M, F = self.model["hidden"], self.M, self.model["ffn"]
         dev = self.device
         self.eps = eps
@@ -282,6 +300,10 @@ class VerifyStack:
             kv = self.model["kv"]
             assert q % head_dim == 0 and kv % head_dim == 0
             self.head_dim, self.Hq, self.Hkv = head_dim, q // head_dim, kv // head_dim
+            self.kv_bits = kv_bits
+            if kv_bits == 4:
+                self._prepare_kv4(cache_len, self.gamma + 1 if room is None else room)
+                return
             shape = (self.B, cache_len, self.Hkv, head_dim)
             self.k_cache = [synth.activations(self.B * cache_len, self.Hkv * head_dim,
                                               synth.subseed(self.seed, "k_cache", l), device=dev,
@@ -297,6 +319,55 @@ class VerifyStack:
             self.attn_out = [torch.empty(M, self.Hq * head_dim, dtype=torch.float32, device=dev)
                              for _ in range(self.layers)]
 
+    def _prepare_kv4(self, cache_len, room):
+        B, T, D, dev = self.B, self.gamma + 1, self.head_dim, self.device
+        kv = self.Hkv * D
+        nb = (cache_len + room + qv.QV_KV4_BLOCK - 1) // qv.QV_KV4_BLOCK
+        # the pages of a sequence lie anywhere in the pool, as a server's allocator leaves them
+        g = torch.Generator().manual_seed(synth.subseed(self.seed, "pages"))
+        self.block_table = torch.randperm(B * nb, generator=g).to(torch.int32).view(B, nb).to(dev)
+        start = torch.zeros(B, dtype=torch.int32, device=dev)
+        self.kv4_cache = []
+        for l in range(self.layers):
+            cache = qv.kv4_cache(B * nb, self.Hkv, D, dev)
+            if cache_len > 0:
+                rows = torch.cat([synth.activations(B * cache_len, kv, synth.subseed(self.seed, name, l), device=dev,
+                                                    outlier_frac=0.0) for name in ("k_cache", "v_cache")], dim=1)
+                qv.qv_kv4_write(rows, start, cache, cache_len, 0, self.Hkv, block_table=self.block_table)
+            self.kv4_cache.append(cache)
+        self.cache_lens = torch.full((B,), cache_len, dtype=torch.int32, device=dev)
+        self.ws_attn = torch.zeros(qv.qv_attention_kv4_workspace_bytes(B, T, self.Hq, self.Hkv, D, nb),
+                                   dtype=torch.uint8, device=dev)
+        self.attn_out = [torch.empty(self.M, self.Hq * D, dtype=torch.float32, device=dev)
+                         for _ in range(self.layers)]
+
+    def cached(self, l: int):
+        """Keys and values of layer l's cache as bf16 tensors [B, positions,
+        Hkv, head_dim] (the 4-bit cache's are read back with qv_kv4_read:
+        every position it has space for; those past cache_lens hold rejected
+        rows or nothing)."""
+        if getattr(self, "cache_len", None) is None:
+            raise ValueError("the chain has no cache")
+        if self.kv_bits == 16:
+            return self.k_cache[l], self.v_cache[l]
+        B, nb = self.block_table.shape
+        k = torch.empty(B, nb * qv.QV_KV4_BLOCK, self.Hkv, self.head_dim, dtype=torch.bfloat16, device=self.device)
+        v = torch.empty_like(k)
+        qv.qv_kv4_read(self.kv4_cache[l], torch.zeros(B, dtype=torch.int32, device=self.device), k, v,
+                       block_table=self.block_table)
+        return k, v
+
+    def advance_chain(self, stream=None):
+        """After a chained step over 4-bit caches: the rows of the accepted
+        tokens (row 0 and the drafts that were kept, accept_len together)
+        become cached positions. Rows that no block has space for were not
+        written and do not count."""
+        if getattr(self, "cache_len", None) is None or self.kv_bits != 4:
+            raise ValueError("advance_chain needs prepare_chain(cache_len=..., kv_bits=4)")
+        cur = torch.cuda.current_stream() if stream is None else stream
+        with torch.cuda.stream(cur):
+            self.cache_lens.add_(self.accept_len).clamp_(max=self.block_table.shape[1] * qv.QV_KV4_BLOCK)
+
     def enqueue_chain(self, stream=None):
         """One verify step through chained decoder layers: the bf16 residual
         stream h runs through every layer, with the non-linear steps between
@@ -304,14 +375,31 @@ class VerifyStack:
         (gist.science/ja summary, section 2.2 item 3):
           attention block: x = RMSNorm(h += down_prev) -> qkv (bf16); with a
             KV cache, causal grouped-query attention of the verify tokens
-            over the cache and their own keys (qv_attention_verify, fp32),
-            its per-token quantization -> o; without one, o takes the
+            over the cache and their own keys (qv_attention_verify, fp32; with
+            4-bit caches qv_attention_verify_kv4, then the step's rows into
+            the cache), its per-token quantization -> o; without one, o takes the
             layer's seeded input; h += o's bf16 output, next block;
           MLP block: x = RMSNorm(h) -> gate|up with SiLU(gate)*up in its
             epilogue (fp32) -> per-token quantization -> down (bf16 output,
             added to h by the next RMSNorm);
           head: x = RMSNorm(h += down_last) -> LM head argmax -> acceptance.
         Eight launches per layer (ten with attention), plus the final three."""
+        self._enqueue_chain_layers(stream)
+        xq = self._xq(self.model["hidden"])
+        qv.qv_lm_head_argmax(xq, self.sx, self.lm_wq, self.lm_sw, self.tokens, self.ws,
+                             max_logit=self.max_logit, stream=stream)
+        qv.qv_accept(self.tokens.view(self.B, self.gamma + 1), self.drafts if self.gamma > 0 else None,
+                     self.accept_len, self.out_tokens, stream=stream)
+
+    def enqueue_chain_sampled(self, stream=None):
+        """The chained step at temperature T > 0 (prepare_chain and
+        prepare_sampling): enqueue_chain's layers, then enqueue_sampled's
+        head over their output."""
+        self._enqueue_chain_layers(stream)
+        self._enqueue_sampled_head(stream)
+
+    def _enqueue_chain_layers(self, stream):
+        """The layers and the final norm; leaves the LM head's codes in xq, sx."""
         M, h, F = self.M, self.model["hidden"], self.model["ffn"]
         ws = self.ws
         cur = torch.cuda.current_stream() if stream is None else stream
@@ -326,7 +414,14 @@ class VerifyStack:
             wq, sw = self.weights[l][0]
             qv.qv_w8a8_linear(xq, self.sx, wq, sw, self.y_qkv, ws, stream=stream)
             xq = self._xq(self.phases[1][1])
-            if attn:
+            if attn and self.kv_bits == 4:
+                qv.qv_attention_verify_kv4(self.y_qkv, self.kv4_cache[l], self.cache_lens, self.gamma + 1, self.Hq,
+                                           self.Hkv, 1.0 / self.head_dim ** 0.5, self.attn_out[l], self.ws_attn,
+                                           block_table=self.block_table, stream=stream)
+                qv.qv_kv4_write(self.y_qkv, self.cache_lens, self.kv4_cache[l], self.gamma + 1, self.Hq, self.Hkv,
+                                block_table=self.block_table, stream=stream)
+                qv.qv_quantize_act(self.attn_out[l], xq, self.sx, stream=stream)
+            elif attn:
                 qv.qv_attention_verify(self.y_qkv, self.k_cache[l], self.v_cache[l], self.cache_lens,
                                        self.gamma + 1, self.Hq, self.Hkv, 1.0 / self.head_dim ** 0.5,
                                        self.attn_out[l], self.ws_attn, stream=stream)
@@ -346,10 +441,6 @@ class VerifyStack:
         xq = self._xq(h)
         qv.qv_rmsnorm_quant(self.h_res, self.norm_final, xq, self.sx, delta=self.y_down, eps=self.eps,
                             stream=stream)
-        qv.qv_lm_head_argmax(xq, self.sx, self.lm_wq, self.lm_sw, self.tokens, ws,
-                             max_logit=self.max_logit, stream=stream)
-        qv.qv_accept(self.tokens.view(self.B, self.gamma + 1), self.drafts if self.gamma > 0 else None,
-                     self.accept_len, self.out_tokens, stream=stream)
 
     # ------------------------------------------------------------------ draft tree
     def prepare_tree(self, parent: torch.Tensor, draft: torch.Tensor):
@@ -387,10 +478,15 @@ class VerifyStack:
         return self.graph_tree
 
     # ------------------------------------------------------------------ T > 0
-    def prepare_sampling(self, temperature: float = 0.8, seed: int = 1234):
+    def prepare_sampling(self, temperature: float = 0.8, seed: int = 1234, top_logprobs: int | None = None):
         """Buffers of the T > 0 step (enqueue_sampled): fp32 logits, seeded
         draft distributions q (softmax of N(0, 2) logits) and drafts drawn
-        from them, the qv_spec_sample workspace."""
+        from them, the qv_spec_sample workspace. With top_logprobs (0 or
+        more) the step also reports, under the model's own distribution
+        (temperature 1), the log probability of every token it puts out, the
+        entropy of its row and the row's top_logprobs most probable tokens
+        (qv_token_logprobs): logprob and entropy [B, gamma+1], top_tokens and
+        top_logprobs [B, gamma+1, top_logprobs]."""
         self._w8_only("the sampled step")
         B, g, V, M = self.B, self.gamma, self.V, self.M
         dev = self.device
@@ -401,6 +497,12 @@ class VerifyStack:
         self.q = torch.softmax(zq, dim=1)[: B * g].contiguous().to(dev)
         self.q_drafts = (torch.multinomial(self.q.cpu().double(), 1, generator=gen).view(B, g).to(torch.int32)
                          .to(dev) if g > 0 else torch.zeros(B, 0, dtype=torch.int32, device=dev))
+        self.want_logprobs = top_logprobs is not None
+        if self.want_logprobs:
+            self.logprob = torch.empty(B, g + 1, dtype=torch.float32, device=dev)
+            self.entropy = torch.empty_like(self.logprob)
+            self.top_tokens = torch.empty(B, g + 1, top_logprobs, dtype=torch.int32, device=dev)
+            self.top_logprobs = torch.empty(B, g + 1, top_logprobs, dtype=torch.float32, device=dev)
         self.ws_spec = torch.empty(qv.qv_workspace_bytes(qv.QV_OP_SPEC_SAMPLE, M, 16, V), dtype=torch.uint8,
                                    device=dev)
 
@@ -419,9 +521,21 @@ class VerifyStack:
                 qv.qv_w8a8_linear(xq, self.sx, wq, sw, self.y[: M * N].view(M, N), ws, stream=stream)
         xq = self._xq(self.model["hidden"])
         qv.qv_quantize_act(self.h_final, xq, self.sx, stream=stream)
-        qv.qv_w8a8_linear(xq, self.sx, self.lm_wq, self.lm_sw, self.logits, ws, stream=stream)
+        self._enqueue_sampled_head(stream)
+
+    def _enqueue_sampled_head(self, stream):
+        """From the LM head's codes (xq, sx) to the tokens and their log probabilities."""
+        M = self.M
+        qv.qv_w8a8_linear(self._xq(self.model["hidden"]), self.sx, self.lm_wq, self.lm_sw, self.logits, self.ws,
+                          stream=stream)
         qv.qv_spec_sample(self.logits, self.q_drafts, self.q, self.temperature, self.sample_seed,
                           self.accept_len, self.out_tokens, self.ws_spec, stream=stream)
+        if self.want_logprobs:
+            k = self.top_tokens.shape[2]
+            qv.qv_token_logprobs(self.logits, self.out_tokens.view(M), self.logprob.view(M),
+                                 entropy=self.entropy.view(M),
+                                 top_tokens=self.top_tokens.view(M, k) if k else None,
+                                 top_logprobs=self.top_logprobs.view(M, k) if k else None, stream=stream)
 
     def capture_sampled(self):
         self.graph_sampled = self._capture(self.enqueue_sampled, self.device)
@@ -430,6 +544,10 @@ class VerifyStack:
     def capture_chain(self):
         self.graph_chain = self._capture(self.enqueue_chain, self.device)
         return self.graph_chain
+
+    def capture_chain_sampled(self):
+        self.graph_chain_sampled = self._capture(self.enqueue_chain_sampled, self.device)
+        return self.graph_chain_sampled
 
     def launches_per_step(self, fused: bool = False) -> int:
         """Kernels one step launches. fused: the persistent qv_verify_stack

@@ -3,10 +3,10 @@ profiler's launch list or a per-kernel capture.
 
     python -m quantized_verification_gb300.tour [--passes 2]
 
-Each pass makes the same 18 launches in the same order. Before the first
+Each pass makes the same 23 launches in the same order. Before the first
 pass the set-up quantizes the weights (one quantize_rows_kernel and one
 quantize_weight_w4_kernel launch), so a capture of the second pass filtered
-with ``-k`` on the kernels below skips 19 matching launches (``-s 19 -c 18``):
+with ``-k`` on the kernels below skips 24 matching launches (``-s 24 -c 23``):
 
     quantize_rows_kernel                  per-token int8 activation codes, 5 x 4096
     w8a8_stream_kernel<1, Linear>         5 x 4096 -> 24576 (Qwen3-8B gate+up), fp32 out
@@ -23,6 +23,12 @@ with ``-k`` on the kernels below skips 19 matching launches (``-s 19 -c 18``):
     attn_cluster_kernel<128, 8, 3>        attention of 5 tokens over a 2048-position
                                           cache, 32/8 heads, D = 128
     logit_fidelity_kernel                 KL and top-1 of 5 rows x 151936 logits
+    kv4_write_kernel                      2048 rows into a 4-bit paged cache, 8 heads, D = 128
+    kv4_read_kernel                       the same positions as bf16
+    attn_kv4_kernel<128, 1>               attention of 5 tokens over them, clusters
+    attn_kv4_tc_kernel<3>                 the same where the context may reach 16384 positions
+    token_logprobs_kernel                 log probabilities, entropies and the top 8 of
+                                          5 rows x 151936 logits
 
 Inputs are seeded and synthetic and sit on the device before the first
 launch; the whole run holds about 0.6 GB.
@@ -33,7 +39,7 @@ import torch
 
 from . import build, qv, synth
 
-LAUNCHES_PER_PASS = 18
+LAUNCHES_PER_PASS = 23
 
 
 def main(argv=None):
@@ -94,6 +100,14 @@ def main(argv=None):
     kv_len = torch.full((1,), L, dtype=torch.int32, device=dev)
     wsa = torch.empty(qv.qv_attention_workspace_bytes(1, gm + 1, Hq, Hkv, D, L), dtype=torch.uint8, device=dev)
     attn = torch.empty(gm + 1, Hq * D, device=dev)
+    rows = torch.randn(L, 2 * Hkv * D, device=dev, generator=g).to(torch.bfloat16)
+    c4, zero = qv.kv4_cache(L // 32, Hkv, D, dev), torch.zeros(1, dtype=torch.int32, device=dev)
+    long_table = torch.full((1, 512), -1, dtype=torch.int32, device=dev)
+    long_table[0, : L // 32] = torch.arange(L // 32, device=dev)
+    ws4 = torch.zeros(qv.qv_attention_kv4_workspace_bytes(1, gm + 1, Hq, Hkv, D, 512), dtype=torch.uint8, device=dev)
+    lp, ent = torch.empty(B * (gm + 1), device=dev), torch.empty(B * (gm + 1), device=dev)
+    tops = torch.empty(B * (gm + 1), 8, dtype=torch.int32, device=dev)
+    top_lp = torch.empty(B * (gm + 1), 8, device=dev)
     logits2 = logits + torch.randn(logits.shape, device=dev, generator=g) * 0.1
     kl = torch.empty(B * (gm + 1), device=dev)
     t1 = torch.empty(B * (gm + 1), dtype=torch.int32, device=dev)
@@ -113,6 +127,12 @@ def main(argv=None):
         qv.qv_accept(vt, drafts, ln, out)
         qv.qv_attention_verify(qkv, kc, vc, kv_len, gm + 1, Hq, Hkv, 1.0 / D ** 0.5, attn, wsa)
         qv.qv_logit_fidelity(logits, logits2, kl, t1, t2)
+        qv.qv_kv4_write(rows, zero, c4, L, 0, Hkv)
+        qv.qv_kv4_read(c4, zero, kc, vc)
+        qv.qv_attention_verify_kv4(qkv, c4, kv_len, gm + 1, Hq, Hkv, 1.0 / D ** 0.5, attn, ws4)
+        qv.qv_attention_verify_kv4(qkv, c4, kv_len, gm + 1, Hq, Hkv, 1.0 / D ** 0.5, attn, ws4,
+                                   block_table=long_table)
+        qv.qv_token_logprobs(logits, vt.view(-1), lp, entropy=ent, top_tokens=tops, top_logprobs=top_lp)
         torch.cuda.synchronize()
     print(f"ok: {LAUNCHES_PER_PASS} launches per pass, {args.passes} passes")
 
