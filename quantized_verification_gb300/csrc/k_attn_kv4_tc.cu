@@ -48,6 +48,12 @@ constexpr int kTcThreads = kTcWorkers + 32;     // and the ninth warp
 constexpr int kTcKeys = 128;                    // positions per step: 4 records
 constexpr int kTcStages = 3;
 constexpr int kTcMaxParts = 128;                // parts of a tile merged at once (their weights fill the value buffer)
+// Steps that O accumulates before it is added to the sums, for fp32 outputs. The
+// tensor cores cut the accumulator off below its last bit at every product, so
+// that a long run drifts towards zero, 1.6e-8 of its result a product: 8e-6 for
+// 7000 positions without these sums, 7e-7 with 4 steps (32 products), 4e-7 with
+// 2, for 5 and 7 % of the time (24 x 8000 positions: 107, 112 and 113 us).
+constexpr int kTcFlush = 4;
 constexpr int D = 128;
 
 template <int NR, bool OUTBF>
@@ -69,7 +75,7 @@ struct TcLayout {
     static constexpr int Bytes = Misc + 32;
     static constexpr int Alloc = Bytes + 1024;            // slack to align the base to 1024 B
     static constexpr int Slot = RW * D + 2 * RW;          // floats of a partial result: [row][lane], m, l
-    static constexpr int kK = 0, kS = 64, kO = 128, kOwn = 192;   // tensor memory columns (S twice 32)
+    static constexpr int kK = 0, kS = 64, kO = 128, kOwn = 192, kSum = 224;   // tensor memory columns (S twice 32)
     static constexpr int Cols = 256;
     static_assert(Bar % 8 == 0 && Row % 16 == 0 && Ring % 16 == 0, "alignment");
     static_assert(2 * kTcMaxParts * 32 * 4 <= 2 * kTcKeys * 128, "the parts' weights fit the value buffer");
@@ -395,7 +401,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
                         umma_f16_ss(tmem + Ly::kO, v_desc + (uint64_t)(ks * 2048 >> 4), p_desc + (uint64_t)(ks * 2048 >> 4),
-                                    idesc(0, Ly::NO, true), (t0 != 0 || ks != 0) ? 1u : 0u);
+                                    idesc(0, Ly::NO, true), ks != 0 || (OUTBF ? t0 != 0 : t0 % kTcFlush != 0) ? 1u : 0u);
                     umma_commit(bar_o);
                 }
                 __syncwarp();
@@ -528,9 +534,36 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
                                     for (int i = 0; i < 8; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * f8[i]);
                                     tmem_st_x8(tlane + Ly::kO + part * RW + 8 * (hf + 2 * t), ov);
                                 }
+                                if (!OUTBF && t0 > kTcFlush) {
+                                    uint32_t ov[8];
+                                    tmem_ld<8>(tlane + Ly::kSum + 8 * (hf + 2 * t), ov);
+                                    tmem_ld_wait();
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i) ov[i] = __float_as_uint(__uint_as_float(ov[i]) * f8[i]);
+                                    tmem_st_x8(tlane + Ly::kSum + 8 * (hf + 2 * t), ov);
+                                }
                                 tmem_st_wait();
                             }
                         }
+                }
+                if (!OUTBF && t0 > 0 && t0 % kTcFlush == 0) {    // the next product begins O afresh
+                    tc_fence_after();
+#pragma unroll
+                    for (int t = 0; t < NT; ++t)
+                        if (hf + 2 * t < NR) {
+                            uint32_t h8[8], l8[8], s8[8];
+                            tmem_ld<8>(tlane + Ly::kO + 8 * (hf + 2 * t), h8);
+                            tmem_ld<8>(tlane + Ly::kO + RW + 8 * (hf + 2 * t), l8);
+                            if (t0 > kTcFlush) tmem_ld<8>(tlane + Ly::kSum + 8 * (hf + 2 * t), s8);
+                            tmem_ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const float y = __uint_as_float(h8[i]) + __uint_as_float(l8[i]);
+                                s8[i] = __float_as_uint(t0 > kTcFlush ? __uint_as_float(s8[i]) + y : y);
+                            }
+                            tmem_st_x8(tlane + Ly::kSum + 8 * (hf + 2 * t), s8);
+                        }
+                    tmem_st_wait();
                 }
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
@@ -592,13 +625,14 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
         float v[NT][8];
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            uint32_t h8[8], l8[8], o8[8];
+            uint32_t h8[8], l8[8], o8[8], s8[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) h8[i] = l8[i] = o8[i] = 0u;
+            for (int i = 0; i < 8; ++i) h8[i] = l8[i] = o8[i] = s8[i] = 0u;
             if (worker && hf + 2 * t < NR) {
                 if (nsteps > 0) {
                     tmem_ld<8>(tlane + Ly::kO + 8 * (hf + 2 * t), h8);
                     if (!OUTBF) tmem_ld<8>(tlane + Ly::kO + RW + 8 * (hf + 2 * t), l8);
+                    if (!OUTBF && nsteps > kTcFlush) tmem_ld<8>(tlane + Ly::kSum + 8 * (hf + 2 * t), s8);
                 }
                 if (own) tmem_ld<8>(tlane + Ly::kOwn + 8 * (hf + 2 * t), o8);
                 tmem_ld_wait();
@@ -606,7 +640,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int r = min(8 * (hf + 2 * t) + i, RW - 1);
-                v[t][i] = (__uint_as_float(h8[i]) + __uint_as_float(l8[i])) * s_w1[r] + __uint_as_float(o8[i]) * s_w2[r];
+                v[t][i] = (__uint_as_float(s8[i]) + (__uint_as_float(h8[i]) + __uint_as_float(l8[i]))) * s_w1[r] + __uint_as_float(o8[i]) * s_w2[r];
             }
         }
         auto store = [&](int r, float x, float sum) {            // this lane's dim of row r

@@ -505,3 +505,34 @@ def test_a_pool_of_more_than_4_gib(qv):
     assert all(torch.equal(a, b) for a, b in zip(*got))
     assert torch.equal(far[t_far.long()], near[t_near.long()]) and bool((got[0][0] != 0).any())
     assert int(far[: pages - B * NB].max()) == 0
+
+
+@pytest.mark.parametrize("D,T,Hq", [(128, 1, 64), (128, 4, 32), (128, 5, 32), (128, 8, 32), (64, 1, 8), (64, 8, 32)])
+def test_long_sums_do_not_drift(qv, D, T, Hq):
+    """Queries of zero: every output is the mean of the values it sees, all of them positive here, over ranges of
+    thousands of positions per thread block. A product of the tensor cores may cut its sum off below the last bit
+    (2^-23 of it at most, half of that on average), so a run of n products from zero loses n 2^-25 on average, its sums
+    being half of its result on average: 2^-20 for 32 products. Rounded additions err both ways: over at most 1100 of
+    them 2^-24 sqrt(1100 / 9) at one standard deviation, 2^-18.5 at four. Without an end to the runs the loss would be
+    above 2^-16 (500 products or more)."""
+    B, Hkv, NB, L = 38, 8, 250, 8000
+    g = gen(3)
+    codes = torch.randint(1, 8, (NB, Hkv, 16 * D), generator=g) | (torch.randint(1, 8, (NB, Hkv, 16 * D), generator=g) << 4)
+    scales = torch.randint(11 * 8, 13 * 8, (NB, Hkv, D), generator=g)
+    cache = torch.cat([torch.zeros(NB, Hkv, 16 * D), codes, torch.zeros(NB, Hkv, D), scales], 2).to(torch.uint8).cuda()
+    table = torch.stack([torch.randperm(NB, generator=g) for _ in range(B)]).to(torch.int32).cuda()
+    qkv = torch.zeros(B, T, Hq + 2 * Hkv, D, dtype=torch.bfloat16)
+    qkv[:, :, Hq + Hkv:] = torch.rand(B, T, Hkv, D, generator=g).to(torch.bfloat16)
+    qkv = qkv.cuda()
+    ws = torch.zeros(qv.qv_attention_kv4_workspace_bytes(B, T, Hq, Hkv, D, NB), dtype=torch.uint8, device="cuda")
+    out = torch.empty(B * T, Hq * D, device="cuda")
+    qv.qv_attention_verify_kv4(qkv.view(B * T, -1), cache, cu(np.full(B, L, np.int32)), T, Hq, Hkv, 1.0, out, ws,
+                               block_table=table)
+    k = torch.empty(1, L, Hkv, D, device="cuda")
+    v = torch.empty_like(k)
+    qv.qv_kv4_read(cache, cu(np.zeros(1, np.int32)), k, v, block_table=table[:1].contiguous())
+    own = qkv[:, :, Hq + Hkv:].double().cumsum(1)
+    n = L + 1 + torch.arange(T, device="cuda").view(1, T, 1, 1)
+    want = ((v[0].double().sum(0) + own) / n).repeat_interleave(Hq // Hkv, 2).reshape(B * T, Hq * D)
+    err = (out.double() / want - 1).abs().max()
+    assert float(err) <= 2.0 ** -20 + 2.0 ** -18.5, float(err)
