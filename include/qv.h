@@ -538,8 +538,11 @@ QV_API qv_status qv_kv4_read(const uint8_t* cache, const int32_t* start, const i
  *             [0, 32 NB]). Positions at and past it are not attended to and may
  *             hold anything, as may whole pages past it.
  *   out       [B*T][Hq * D] fp32 or bf16 (out_dtype), 16-byte aligned
- *   T in [1, QV_MAX_M], Hq a multiple of Hkv; any T * Hq / Hkv (groups of 32
- *   query rows read the cache once each).
+ *   scale     in (0, 2e38]
+ *   T in [1, QV_MAX_M], Hq a multiple of Hkv; any T * Hq / Hkv. Groups of up to
+ *   32 query rows of a head group (8 where the context can only be short) read
+ *   the cache once each. QV_ERR_UNSUPPORTED where the blocks of all sequences,
+ *   heads and groups together reach about 2^31.
  *   workspace: qv_attention_kv4_workspace_bytes(...) bytes (a host function;
  *             0 for an invalid shape), 16-byte aligned. Its first 4096 bytes
  *             must be ZERO-FILLED before its first use and are zero again
@@ -548,6 +551,10 @@ QV_API qv_status qv_kv4_read(const uint8_t* cache, const int32_t* start, const i
  *             enough for. It must not be shared with calls that may run at the
  *             same time (another stream, another captured graph), nor with the
  *             GEMM calls, whose whole workspace has to stay zero-filled.
+ *   The work is cut by T, the heads and NB, not by the lengths, which only the
+ *   device knows: a table no wider than the longest sequence needs (NB) lets
+ *   short contexts use the faster of the two cuts. One launch; it may use
+ *   clusters of up to 8 thread blocks, or tensor memory (256 columns a block).
  *   A later row's key or value that is not finite (padding) does not reach the
  *   rows before it; what a row does see, it sees: its output is then not
  *   finite either.
@@ -556,7 +563,10 @@ QV_API qv_status qv_kv4_read(const uint8_t* cache, const int32_t* start, const i
  *   stays usable.
  * fp32 outputs are within about 1e-6 (2-norm) of the binary64 definition over
  * the values the cache holds; for bf16 outputs the probabilities are rounded to
- * bf16 before the product with the values.
+ * 11 bits before the product with the values. Results are the same from call
+ * to call on one GPU. A row whose largest score has a magnitude of 2^27 * ln 2
+ * = 9.3e7 or more (scale included; binary32 no longer tells its scores apart) is
+ * NaN.
  */
 QV_API size_t qv_attention_kv4_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int NB);
 QV_API qv_status qv_attention_verify_kv4(const uint16_t* qkv, const uint8_t* cache, const int32_t* block_table,

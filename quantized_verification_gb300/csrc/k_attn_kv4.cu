@@ -39,7 +39,7 @@
 //   P in base 2, kept unnormalised: p = 2^(7 + s - m). m is a whole number (so
 //     that every rescaling factor is an exact power of two) that follows the
 //     row's maximum lazily: it moves only when a score exceeds it by more than
-//     8 (p is below 2^15.6 then), so the usual step needs no reduction across
+//     8 (p is below 2^15.6 then; RowMax), so the usual step needs no reduction across
 //     lanes and no rescaling. P is split into two f16 parts (an error of 2^-22 P, and
 //     2^-32 of the largest P below f16's normal range) for fp32 outputs; for
 //     bf16 outputs one part is enough (2^-11 P, an eighth of the output's own
@@ -255,7 +255,7 @@ __global__ void __launch_bounds__(Layout<D, NR>::Threads, Layout<D, NR>::Ctas) a
                     lds_v2_u32(sbase + (uint32_t)(Ly::Q + ((nt * KS + kk) * 32 + lane) * 8), qf[nt][kk].x, qf[nt][kk].y);
         }
         float o[KS][NR][4];                                      // O^T: dims x rows
-        // rows 8 nt + 2 t4 + e: p = 2^(sl2 x + c) of the product x, c = kBias - m;
+        // rows 8 nt + 2 t4 + e: p = 2^(sl2 x + c) of the product x (RowMax);
         // limit: the product at which m moves (-inf before the first key)
         float c[NR][2], limit[NR][2], l_run[NR][2];
 #pragma unroll
@@ -290,10 +290,10 @@ __global__ void __launch_bounds__(Layout<D, NR>::Threads, Layout<D, NR>::Ctas) a
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
                         v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
                         if (v > limit[nt][e]) {                  // (the same in the row's 8 lanes)
-                            const float m = rintf(v * sl2), cn = kBias - m;
-                            const float f = limit[nt][e] == NEG_INF ? 0.f : ex2(cn - c[nt][e]);
-                            c[nt][e] = cn;
-                            limit[nt][e] = (m + kLazy) / sl2;
+                            const RowMax to(v, sl2);
+                            const float f = limit[nt][e] == NEG_INF ? 0.f : ex2(to.c - c[nt][e]);
+                            c[nt][e] = to.c;
+                            limit[nt][e] = to.limit;
                             l_run[nt][e] *= f;
 #pragma unroll
                             for (int i = 0; i < KS; ++i) {
@@ -620,7 +620,7 @@ __global__ void __launch_bounds__(Layout<D, NR>::Threads, Layout<D, NR>::Ctas) a
                 l += __shfl_xor_sync(0xffffffffu, l, 8);
                 l += __shfl_xor_sync(0xffffffffu, l, 16);
                 if (g == 0) {
-                    s_wm[warp * RW + 8 * nt + 2 * t4 + e] = limit[nt][e] == NEG_INF ? NEG_INF : kBias - c[nt][e];
+                    s_wm[warp * RW + 8 * nt + 2 * t4 + e] = limit[nt][e] == NEG_INF ? NEG_INF : -c[nt][e];
                     s_wl[warp * RW + 8 * nt + 2 * t4 + e] = l;
                 }
             }

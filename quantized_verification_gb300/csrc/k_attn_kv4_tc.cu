@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
     uint64_t* bar_p = bar_s + 4;                                 // the values and probabilities are in place (8 warps)
     uint64_t* bar_end = bar_s + 5;
     volatile int* cnt = reinterpret_cast<volatile int*>(smem + Ly::Cnt);
-    float* s_c = reinterpret_cast<float*>(smem + Ly::Row);       // p = 2^(sl2 x + c), c = kBias - m
+    float* s_c = reinterpret_cast<float*>(smem + Ly::Row);       // p = 2^(sl2 x + c) of the product x (RowMax)
     float* s_lim = s_c + 32;                                     // the product at which m moves
     float* s_f = s_c + 64;
     float* s_m2 = s_c + 96;
@@ -509,10 +509,10 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
                         const float v = fmaxf(fmaxf(s_red[tid], s_red[32 + tid]), fmaxf(s_red[64 + tid], s_red[96 + tid]));
                         float f = 1.f;
                         if (v > s_lim[tid]) {
-                            const float m = rintf(v * sl2), cn = kBias - m;
-                            f = s_lim[tid] == NEG_INF ? 0.f : ex2(cn - s_c[tid]);
-                            s_c[tid] = cn;
-                            s_lim[tid] = (m + kLazy) / sl2;
+                            const RowMax to(v, sl2);
+                            f = s_lim[tid] == NEG_INF ? 0.f : ex2(to.c - s_c[tid]);
+                            s_c[tid] = to.c;
+                            s_lim[tid] = to.limit;
                         }
                         s_f[tid] = f;
                     }

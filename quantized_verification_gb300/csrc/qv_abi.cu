@@ -798,7 +798,7 @@ qv_status qv_attention_verify_kv4(const uint16_t* qkv, const uint8_t* cache, con
     if (!qkv || !cache_len || !out) return fail(QV_ERR_INVALID_ARG, "null pointer");
     if (NB > 0 && !cache) return fail(QV_ERR_INVALID_ARG, "cache is null with NB > 0");
     if (!is_dtype(out_dtype)) return fail(QV_ERR_INVALID_ARG, "out_dtype must be QV_F32 or QV_BF16");
-    if (!(scale > 0.0f) || scale > 3.0e38f) return fail(QV_ERR_INVALID_ARG, "scale must be finite and > 0");
+    if (!(scale > 0.0f) || scale > 2.0e38f) return fail(QV_ERR_INVALID_ARG, "scale must be in (0, 2e38]");
     if (!aligned(qkv, 16) || (cache && !aligned(cache, 16)) || !aligned(out, 16) || !aligned(cache_len, 4) ||
         (block_table && !aligned(block_table, 4)))
         return fail(QV_ERR_INVALID_ARG, "qkv, cache and out must be 16-byte aligned, int32 buffers 4-byte aligned");

@@ -107,7 +107,7 @@ def test_refusals_without_gpu(lib):
                                                            "NB", "pages", "scale", "out", "dt", "ws", "n", "s")])
     for k in (dict(qkv=None), dict(cache=None), dict(ln=None), dict(out=None), dict(T=0), dict(T=257), dict(Hq=9),
               dict(Hq=1), dict(Hq=65538), dict(D=96), dict(pages=7), dict(scale=F(0.0)), dict(scale=F(-1.0)),
-              dict(scale=F(float("nan"))), dict(scale=F(float("inf"))), dict(out=bad), dict(qkv=bad), dict(cache=bad),
+              dict(scale=F(float("nan"))), dict(scale=F(float("inf"))), dict(scale=F(2.5e38)), dict(out=bad), dict(qkv=bad), dict(cache=bad),
               dict(dt=3), dict(ln=P(0x1001)), dict(B=0)):
         assert A(**k) == qv.QV_ERR_INVALID_ARG, k
     T = lambda **k: lib.qv_token_logprobs(*[{**dict(x=f, dt=0, tok=f, M=2, V=10, K=3, lp=f, ent=None, tt=f, tl=f,

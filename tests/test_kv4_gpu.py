@@ -536,3 +536,39 @@ def test_long_sums_do_not_drift(qv, D, T, Hq):
     want = ((v[0].double().sum(0) + own) / n).repeat_interleave(Hq // Hkv, 2).reshape(B * T, Hq * D)
     err = (out.double() / want - 1).abs().max()
     assert float(err) <= 2.0 ** -20 + 2.0 ** -18.5, float(err)
+
+
+@pytest.mark.parametrize("NB", [9, 400])
+@pytest.mark.parametrize("D,T,Hq", [(128, 1, 2), (128, 5, 4), (128, 8, 4), (64, 3, 4)])
+def test_scores_of_millions(qv, NB, D, T, Hq):
+    """Keys at the format's largest scale and queries that fit them: the best score is far above the others and lies at
+    1e5 to 9e7, where binary32 has few bits or none behind the point. The output is the best key's value: every other
+    probability is 2^-10000 or less, and the weight of the best is one f16 number or two over their own sum (2^-11 of
+    it for bf16 outputs, which are rounded by 2^-9 more). Beyond 2^27 ln 2 it is NaN."""
+    n = 32 * NB
+    g = gen(8)
+    codes = torch.randint(-2, 3, (NB, 1, 64 * D), generator=g).numpy()
+    steps = np.linspace(3, n - 2, 5).astype(int)               # ever better keys along the cache
+    for i, p in enumerate(steps):
+        codes[p // 32, 0, (p % 32) * D:(p % 32 + 1) * D] = 3 + i
+    cache = np.concatenate([ref.pack(codes), np.full((NB, 1, D), 255, np.uint8),
+                            np.random.default_rng(1).integers(80, 130, (NB, 1, D)).astype(np.uint8)], axis=2)
+    _, vc, _, vs = ref.parts(cache, D)
+    p = steps[-1]
+    best = ref.values(ref.unpack(vc[p // 32, 0, p % 32]), vs[p // 32, 0, p % 32])
+    ws = torch.zeros(qv.qv_attention_kv4_workspace_bytes(1, T, Hq, 1, D, NB), dtype=torch.uint8, device="cuda")
+    scale = 1.0 / D
+    for want_max in (1e5, 6.9e5, 7.6e5, 3e6, 1.4e7, 5e7, 9e7, 1e8, 1e12):
+        qkv = torch.randn(T, (Hq + 2) * D, generator=g)
+        qkv[:, : Hq * D] = want_max / (7 * 122880)
+        qkv = qkv.to(torch.bfloat16)
+        top = float(qkv[0, 0]) * 7 * 122880
+        for dt in (torch.float32, torch.bfloat16):
+            out = torch.empty(T, Hq * D, dtype=dt, device="cuda")
+            qv.qv_attention_verify_kv4(qkv.cuda(), cu(cache), cu(np.array([n], np.int32)), T, Hq, 1, scale, out, ws)
+            o = np_(out.double()).reshape(T * Hq, D)
+            if top >= 2 ** 27 * np.log(2):
+                assert np.isnan(o).all()
+            else:
+                tol = 2.0 ** -20 if dt == torch.float32 else 2.0 ** -11 + 2.0 ** -8
+                assert np.all(np.abs(o - best) <= tol * np.abs(best) + 1e-30), (want_max, np.abs(o - best).max())
