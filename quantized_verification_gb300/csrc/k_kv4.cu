@@ -92,11 +92,26 @@ struct Raw {                   // 8 elements as they are in memory
     }
 };
 
+// The largest magnitude of three, NaN if one is NaN.
+__device__ __forceinline__ float max_abs_nan3(float a, float b, float c) {
+    float y;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+
 // The scale byte of a group whose largest magnitude is amax: the nearest scale
 // to fl32(amax / 7), ties to the even byte. Rounding adds half of the last
 // kept bit (and the kept bit itself, for ties) to the binary32 pattern.
+//
+// A bf16 amax has 8 significant bits, and its seventh is either halfway between
+// two scales or further than 2^-11 of itself from there: the product with
+// fl32(1/7), within 2 units of the last place, decides as the quotient does
+// once its last 4 bits are rounded away (checked for every bf16 number).
+template <bool BF16>
 __device__ __forceinline__ uint32_t scale_byte(float amax) {
-    const uint32_t u = __float_as_uint(__fdiv_rn(amax, 7.0f));
+    uint32_t u;
+    if (BF16) u = (__float_as_uint(__fmul_rn(amax, 1.0f / 7.0f)) + 8u) & ~15u;
+    else u = __float_as_uint(__fdiv_rn(amax, 7.0f));
     const int b = (int)((u + 0x7FFFFu + ((u >> 20) & 1u)) >> 20) - 896;
     return (uint32_t)(b < 0 ? 0 : (b > 255 ? 255 : b));
 }
@@ -111,10 +126,18 @@ __device__ __forceinline__ uint32_t scale_byte(float amax) {
 // rounds it half to even and leaves q + 8 in the low bits; the eight sums are
 // weighted by 16^i, and one subtraction takes the constant parts off.
 // |x / s| < 7.5 by the choice of s, but for scales cut off at the largest one.
+//
+// A bf16 x has 8 significant bits and s has 4, so that x / s is either halfway
+// between two integers or further than 2^-11 from there. x r with an r within 2
+// units of the last place of 1 / s, rounded to a multiple of 2^-11 by adding
+// 1.5 * 2^12, is then on the quotient's side of every halfway point, or on it
+// (checked for every such x and s and five r). That takes two operations an
+// element in place of four; with the reciprocal and the product with 1/7 in
+// place of two divisions the prompt-length write is no longer bound by
+// instruction issue.
+template <bool BF16>
 __device__ __forceinline__ uint32_t encode8(float (&v)[8], unsigned mask, uint32_t& sb) {
-    float am = fabsf(v[0]);
-#pragma unroll
-    for (int i = 1; i < 8; ++i) am = max_abs_nan(am, v[i]);
+    float am = max_abs_nan3(max_abs_nan3(v[0], v[1], v[2]), max_abs_nan3(v[3], v[4], v[5]), max_abs_nan(fabsf(v[6]), v[7]));
     am = max_abs_nan(am, __shfl_xor_sync(mask, am, 1));
     am = max_abs_nan(am, __shfl_xor_sync(mask, am, 2));
     if (!(am <= 7.f * 122880.f)) {                             // rare: NaN counts as 0, large magnitudes saturate
@@ -127,14 +150,22 @@ __device__ __forceinline__ uint32_t encode8(float (&v)[8], unsigned mask, uint32
         am = fmaxf(am, __shfl_xor_sync(mask, am, 1));
         am = fmaxf(am, __shfl_xor_sync(mask, am, 2));
     }
-    sb = scale_byte(am);
-    const float s = kv4_scale(sb), r = __fdiv_rn(1.0f, s);
+    sb = scale_byte<BF16>(am);
+    const float s = kv4_scale(sb);
+    float r;
+    if (BF16) asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(s));
+    else r = __fdiv_rn(1.0f, s);
     uint32_t w = 0;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        const float q0 = __fmul_rn(v[i], r);
-        const float q = __fmaf_rn(__fmaf_rn(-q0, s, v[i]), r, q0);
-        w += __float_as_uint(__fadd_rn(q, 12582920.0f)) * (1u << (4 * i));
+        float q;
+        if (BF16) {
+            q = __fadd_rn(__fmaf_rn(v[i], r, 6144.0f), 12582920.0f - 6144.0f);
+        } else {
+            const float q0 = __fmul_rn(v[i], r);
+            q = __fadd_rn(__fmaf_rn(__fmaf_rn(-q0, s, v[i]), r, q0), 12582920.0f);
+        }
+        w += __float_as_uint(q) * (1u << (4 * i));
     }
     constexpr uint32_t ones = 0x11111111u;
     return (w - 0x4B400000u * ones) ^ 0x88888888u;             // q + 8, then two's complement
@@ -171,7 +202,7 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_write_kernel(const Kv4Args a)
             float v[8];
             raw[i].values(v);
             uint32_t sb;
-            const uint32_t w = encode8(v, mask, sb);
+            const uint32_t w = encode8<BF16>(v, mask, sb);
             *reinterpret_cast<uint32_t*>(rec + (kv ? Rec::VC : Rec::KC) + slot * Rec::RowBytes + c * 4) = w;
             if ((c & 3) == 0) rec[(kv ? Rec::VS : Rec::KS) + slot * Rec::RowScales + (c >> 2)] = (uint8_t)sb;
         }

@@ -131,12 +131,13 @@ def _check(status: int):
 # The current stream's handle without the Stream object around it (a call on a
 # few rows is bound by its host time); the public way where it is missing.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream) -> int:
     if stream is None:
         if _raw_stream is not None:
-            return _raw_stream(torch.cuda.current_device())
+            return _raw_stream(_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
@@ -146,13 +147,12 @@ def _stream(stream) -> int:
 def _ptr(t):
     if t is None:
         return None
-    if not isinstance(t, torch.Tensor):
-        raise TypeError("expected a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError("tensor must live on a CUDA device")
-    if not t.is_contiguous():
-        raise ValueError("tensor must be contiguous")
-    return t.data_ptr()
+    try:
+        if t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        raise TypeError("expected a torch.Tensor") from None
+    raise ValueError("tensor must be contiguous" if t.is_cuda else "tensor must live on a CUDA device")
 
 
 def _dtype(t: torch.Tensor) -> int:

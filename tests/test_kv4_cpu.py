@@ -138,3 +138,27 @@ def test_binding_refusals_without_gpu():
                  lambda: qv.qv_token_logprobs(torch.zeros(4, 9), i32(4), torch.zeros(4), top_tokens=i32(4, 2))):
         with pytest.raises(ValueError):
             call()
+
+
+def test_shortcuts_for_bf16_rows():
+    """What the write kernel does for bf16 rows in place of two divisions gives the same bytes and codes: for every
+    bf16 maximum, and for every significand of x, every one of s and reciprocals up to two units off."""
+    f32 = np.float32
+    am = (np.arange(0x7F80, dtype=np.uint32) << 16).view(f32)
+    am = am[am <= 7 * 122880]
+
+    def byte(u):
+        return np.clip(((u + 0x7FFFF + ((u >> 20) & 1)) >> 20) - 896, 0, 255)
+    bits = lambda t: t.view(np.uint32).astype(np.int64)  # noqa: E731
+    assert np.array_equal(byte(bits(am / f32(7))), byte((bits(am * f32(1 / f32(7))) + 8) & ~15))
+    for m in range(8):
+        s = f32(1 + m / 8)
+        for off in range(-2, 3):
+            r = (np.array([f32(1) / s]).view(np.int32) + np.int32(off)).view(f32).astype(np.float64)
+            for e in range(-24, 4):
+                x = ((1 + np.arange(128) / 128) * 2.0 ** e).astype(f32)
+                x = x[x <= 7.5 * s]
+                x = np.concatenate([x, -x])
+                t = (x.astype(np.float64) * r + 6144.0).astype(f32)
+                q = (t.astype(np.float64) + (12582920.0 - 6144.0)).astype(f32)
+                assert np.array_equal(bits(q) - 0x4B400000 - 8, np.rint(x / s).astype(np.int64)), (m, off, e)
