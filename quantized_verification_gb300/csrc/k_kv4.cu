@@ -8,12 +8,14 @@
 //   outlier channel costs its own 32 neighbours precision and no others.
 //
 // A CTA takes the positions of one sequence in one block, for one head or a
-// few, so that the chain start -> block table -> record is walked once for up
-// to 64 KB. A thread moves 8 elements (16 bytes of bf16), four threads a scale
+// few, so that the chain start -> block table -> record is walked once for all
+// of them. A thread moves 8 elements (16 bytes of bf16), four threads a scale
 // group, consecutive threads on consecutive elements: the wide side moves in
 // runs of 256 bytes (a head's row at D = 128), the codes in whole sectors, and
 // the four rows of a thread are requested before the first is worked on. Bound
-// by memory at prompt lengths and by launch latency at a step's few rows.
+// by launch latency at a step's few rows (2.4 us), by memory and its latency at
+// prompt lengths: 85 MB in 15.6 us (5.4 TB/s) for the two prompts below, 113 MB
+// in 19.4 us (5.8 TB/s) for the four caches; a plain copy runs at 6.8.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -171,8 +173,10 @@ __device__ __forceinline__ uint32_t encode8(float (&v)[8], unsigned mask, uint32
     return (w - 0x4B400000u * ones) ^ 0x88888888u;             // q + 8, then two's complement
 }
 
+// Five CTAs an SM for bf16 rows (48 registers): two prompts of 8190 tokens, 8
+// heads, D = 128, in 15.6 us (17.2 with four CTAs, 16.7 with six, which spill).
 template <int D, bool BF16>
-__global__ void __launch_bounds__(kKv4Threads) kv4_write_kernel(const Kv4Args a) {
+__global__ void __launch_bounds__(kKv4Threads, BF16 ? 5 : 3) kv4_write_kernel(const Kv4Args a) {
     using Rec = Kv4Rec<D>;
     constexpr int Chunks = D / 8;                              // threads of a row
     constexpr int Rows = kKv4Threads / Chunks;                 // rows the CTA takes at once
@@ -263,12 +267,16 @@ __global__ void __launch_bounds__(kKv4Threads) kv4_read_kernel(const Kv4Args a) 
 }
 
 // One CTA per sequence, block that its T rows can touch, and group of heads:
-// as many heads as leave 8 CTAs an SM (or one head each).
+// as many heads as leave `ctas_per_sm` CTAs an SM (or one head each). Writing
+// takes 8: with 16 the two prompts above take 18.7 us for 17.2. Reading takes 32,
+// since with ragged counts many CTAs find nothing to do: four caches of up to
+// 16384 positions 19.4 us, 22.5 with 8, 25.6 with one head a CTA.
 template <class Kernel>
-cudaError_t launch_rows(Kernel kernel, Kv4Args& a, int B, int sms, cudaStream_t s) {
+cudaError_t launch_rows(Kernel kernel, Kv4Args& a, int B, int sms, int ctas_per_sm, cudaStream_t s) {
     const int blocks = (a.T + kKv4Block - 2) / kKv4Block + 1;
     a.heads = 1;
-    while (a.heads * 2 <= a.Hkv && (long long)blocks * B * ceil_div(a.Hkv, a.heads * 2) >= 8LL * sms) a.heads *= 2;
+    while (a.heads * 2 <= a.Hkv && (long long)blocks * B * ceil_div(a.Hkv, a.heads * 2) >= (long long)ctas_per_sm * sms)
+        a.heads *= 2;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)blocks, (unsigned)ceil_div(a.Hkv, a.heads), (unsigned)B);
     cfg.blockDim = dim3(kKv4Threads);
@@ -290,8 +298,8 @@ cudaError_t launch_kv4_write(const void* x, bool bf16, const int32_t* start, con
     a.x = static_cast<const uint8_t*>(x);
     a.cache = cache; a.table = table; a.start = start; a.count = count;
     a.T = T; a.Hq = Hq; a.Hkv = Hkv; a.NB = NB; a.pages = pages;
-    if (D == 128) return bf16 ? launch_rows(kv4_write_kernel<128, true>, a, B, sms, s) : launch_rows(kv4_write_kernel<128, false>, a, B, sms, s);
-    return bf16 ? launch_rows(kv4_write_kernel<64, true>, a, B, sms, s) : launch_rows(kv4_write_kernel<64, false>, a, B, sms, s);
+    if (D == 128) return bf16 ? launch_rows(kv4_write_kernel<128, true>, a, B, sms, 8, s) : launch_rows(kv4_write_kernel<128, false>, a, B, sms, 8, s);
+    return bf16 ? launch_rows(kv4_write_kernel<64, true>, a, B, sms, 8, s) : launch_rows(kv4_write_kernel<64, false>, a, B, sms, 8, s);
 }
 
 cudaError_t launch_kv4_read(const uint8_t* cache, const int32_t* start, const int32_t* count, const int32_t* table,
@@ -301,8 +309,8 @@ cudaError_t launch_kv4_read(const uint8_t* cache, const int32_t* start, const in
     a.k_out = static_cast<uint8_t*>(k_out); a.v_out = static_cast<uint8_t*>(v_out);
     a.cache = const_cast<uint8_t*>(cache); a.table = table; a.start = start; a.count = count;
     a.T = T; a.Hkv = Hkv; a.NB = NB; a.pages = pages;
-    if (D == 128) return bf16 ? launch_rows(kv4_read_kernel<128, true>, a, B, sms, s) : launch_rows(kv4_read_kernel<128, false>, a, B, sms, s);
-    return bf16 ? launch_rows(kv4_read_kernel<64, true>, a, B, sms, s) : launch_rows(kv4_read_kernel<64, false>, a, B, sms, s);
+    if (D == 128) return bf16 ? launch_rows(kv4_read_kernel<128, true>, a, B, sms, 32, s) : launch_rows(kv4_read_kernel<128, false>, a, B, sms, 32, s);
+    return bf16 ? launch_rows(kv4_read_kernel<64, true>, a, B, sms, 32, s) : launch_rows(kv4_read_kernel<64, false>, a, B, sms, 32, s);
 }
 
 }  // namespace qv
