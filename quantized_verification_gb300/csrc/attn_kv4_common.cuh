@@ -26,7 +26,7 @@ constexpr int kMaxCluster = 8;                  // CTAs of a cluster that share 
 constexpr int kClusterUnits = 6;                // a larger cluster while its CTAs have more units than this
 constexpr int kClusterMost = 48;                // no clusters above so many units a CTA
 constexpr int kTcMinUnits = 8;                  // the same for the tcgen05 kernel: two steps of 128 positions,
-constexpr int kTcTileCost = 32;                 // and a tile's costs
+constexpr int kTcTileCost = 18;                 // and a tile's costs
 constexpr float kLazy = 8.f;                    // log2 of the growth a running maximum may lag behind
 constexpr float kBias = 7.f;                    // log2 of p at the running maximum: 2^(kBias + kLazy + 0.5) < 65504
 

@@ -20,16 +20,16 @@
 //     the workspace, and the last of its CTAs to arrive adds them in range
 //     order. Nobody waits for anybody, and the order of arrival changes
 //     nothing. Every tile takes kTileCost places more than its units (its start
-//     and its end; GB300, 64 sequences of 1 to 2500 positions: 89 us with 12,
-//     67 us with 24 or more).
+//     and its end; GB300, 5 tokens for 24 sequences of 33 to 16001 positions: 89
+//     us with 12, 74 us with 26 or more).
 //
 // Inside a CTA each of the W warps (8 or 12) takes every W-th unit of the range
 // and keeps its own online softmax; the step's own rows are warp 0's, which
-// gets one unit less (76 us without that on the same batch). A record comes in
+// gets one unit less (10 % on the same batch). A record comes in
 // one bulk copy into the warp's own ring. Both products run on the tensor cores
 // (mma.sync m16n8k16, fp32 accumulation) with the keys, or the value dims, on
 // the M side and the query rows on the N side in tiles of 8: few rows do not
-// fill a tcgen05 tile's 128 (k_attn_kv4_tc.cu takes over from 17 rows, kTcRows).
+// fill a tcgen05 tile's 128 (k_attn_kv4_tc.cu takes over from 9 or 17 rows, tc_rows).
 //   S^T = K Q^T:  in bf16. Codes become bf16 values exactly (kv4_common.cuh): a nibble
 //     shifted to bits 3..6 under the pattern of 16.0 is the number 24 + q, and
 //     one fused multiply-add gives (24 + q) s - 24 s = q s without rounding.
@@ -887,11 +887,12 @@ cudaError_t launch(const Args& a, int grid, cudaStream_t s) {                  /
 }
 
 // Tiles of so many groups of 8 rows, heads of 128, go to the tcgen05 kernel:
-// its time hardly depends on the rows of a tile, this kernel's grows with them.
-// GB300, fp32 out, here / there in us for 8, 16, 24, 32 rows: 2 sequences of
-// 131071 positions 78/108, 110/115, 135/129, 185/145; 24 of 8000 63/86, 89/93,
-// 115/107, 147/121.
-constexpr int kTcRows = 3;
+// its time hardly depends on the rows of a tile or on P's parts, this kernel's
+// grows with them. GB300, here / there in us for 8, 16, 24, 32 rows, 24
+// sequences of 8000 positions: fp32 out 69/83, 95/88, 127/103, 168/108; bf16 out
+// 61/80, 77/84, 99/98, 126/101. 2 of 131071, fp32, from 16 rows: 117/112,
+// 150/133, 202/136.
+constexpr int tc_rows(bool out_bf16) { return out_bf16 ? 3 : 2; }
 
 struct Plan {
     int RT, rows, NR;
@@ -900,7 +901,7 @@ struct Plan {
     int grid, cost, min_units;
     size_t total;                // workspace bytes; 0: more units than the kernel's 32-bit places can count
 };
-Plan plan(int B, int T, int Hq, int Hkv, int D, int NB, int sms) {
+Plan plan(int B, int T, int Hq, int Hkv, int D, int NB, int sms, bool out_bf16) {
     const int rows = T * (Hq / Hkv);
     const long long units = (long long)NB + (T + 31) / 32;     // of a tile at most
     Plan p;
@@ -929,7 +930,7 @@ Plan plan(int B, int T, int Hq, int Hkv, int D, int NB, int sms) {
         while (p.C < kMaxCluster && tiles * p.C * 2 <= slots && units > (long long)kClusterUnits * p.C) p.C *= 2;
         if (tiles * p.C > slots || units > (long long)kClusterMost * p.C) p.C = 0;
     }
-    p.tc = p.C == 0 && D == 128 && p.NR >= kTcRows;
+    p.tc = p.C == 0 && D == 128 && p.NR >= tc_rows(out_bf16);
     p.cost = p.tc ? kTcTileCost : kTileCost;
     p.min_units = p.tc ? kTcMinUnits : kMinUnits;
     const long long most = tiles * (units + p.cost);           // places at most
@@ -945,14 +946,15 @@ Plan plan(int B, int T, int Hq, int Hkv, int D, int NB, int sms) {
 }  // namespace
 
 size_t attention_kv4_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int NB, int sms) {
-    return plan(B, T, Hq, Hkv, D, NB, sms).total;
+    const size_t f = plan(B, T, Hq, Hkv, D, NB, sms, false).total, h = plan(B, T, Hq, Hkv, D, NB, sms, true).total;
+    return f == 0 || h == 0 ? 0 : (f > h ? f : h);             // enough for both output types
 }
 
 cudaError_t launch_attention_kv4(const uint16_t* qkv, const uint8_t* cache, const int32_t* table, const int32_t* len,
                                  int B, int T, int Hq, int Hkv, int D, int NB, int pages, float scale, void* out,
                                  bool out_bf16, void* ws, int sms, int hold, unsigned long long wait_ns,
                                  cudaStream_t s) {
-    const Plan p = plan(B, T, Hq, Hkv, D, NB, sms);
+    const Plan p = plan(B, T, Hq, Hkv, D, NB, sms, out_bf16);
     Args a;
     a.qkv = qkv; a.cache = cache; a.table = table; a.len = len;
     a.B = B; a.T = T; a.Hq = Hq; a.Hkv = Hkv; a.G = Hq / Hkv; a.NB = NB; a.pages = pages;

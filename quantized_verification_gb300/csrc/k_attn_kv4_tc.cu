@@ -1,16 +1,16 @@
 // k_attn_kv4_tc.cu -- attention over the 4-bit paged KV cache for heads of 128
-// values, tiles of 17 to 32 query rows and long contexts, on the tcgen05 tensor
-// cores.
+// values, tiles of 9 (bf16 outputs: 17) to 32 query rows and long contexts, on
+// the tcgen05 tensor cores.
 //
 //   What is computed, the cut of the work into tiles, units and places, and the
 //   arithmetic (exact unpacking, base-2 probabilities with a lazy whole-number
 //   maximum, two f16 parts of P for fp32 outputs) are k_attn_kv4.cu's; only the
-//   products are formed elsewhere. On mma.sync 17 to 32 query rows keep the legacy
+//   products are formed elsewhere. On mma.sync many query rows keep the legacy
 //   tensor pipe busy about as long as the unpacking the ALUs, with too few warps
-//   to overlap the two. GB300, fp32 out, 2 x 131071 positions, 8 key/value heads:
-//   24 rows 129 us against 135, 32 rows 145 us against 185 (41 us to read the
-//   cache); 24 x 8000 positions, 24 rows: 107 us against 115. Below 17 rows the
-//   other kernel is faster (its kTcRows has the figures).
+//   to overlap the two. GB300, fp32 out, 24 sequences of 8000 positions, 8
+//   key/value heads: 24 rows 103 us against 127, 32 rows 108 us against 168 (31
+//   us to read the cache). What is left is the ALUs' and the issue slots' (50 and
+//   55 % busy in the main loop) and the waits of 4 unpacking warps a scheduler.
 //
 // A CTA takes 128 positions (4 records) a step. 8 warps work on them, a ninth
 // requests records and issues the products; they meet at mbarriers, and the
@@ -31,7 +31,9 @@
 // Two CTAs share an SM. The step's own keys and values are few and are not of
 // the cache's format: they are attended to with plain fp32 arithmetic while the
 // first records load; their outputs wait in tensor memory and are merged at the
-// end.
+// end. A tile's start, own rows and end take as long as about kTcTileCost units:
+// 24 sequences of 33 to 16001 positions, 24 rows, 60 us with 18, 62 with 22, 63
+// with 14.
 
 #include "attn_kv4_common.cuh"
 
@@ -52,8 +54,9 @@ constexpr int kTcMaxParts = 128;                // parts of a tile merged at onc
 // tensor cores cut the accumulator off below its last bit at every product, so
 // that a long run drifts towards zero, 1.6e-8 of its result a product: 8e-6 for
 // 7000 positions without these sums, 7e-7 with 4 steps (32 products), 4e-7 with
-// 2, for 5 and 7 % of the time (24 x 8000 positions: 107, 112 and 113 us).
+// 2, for 2 % more of the time.
 constexpr int kTcFlush = 4;
+constexpr int kTcOwnStride = 36;                // floats from one own row's scores to the next one's
 constexpr int D = 128;
 
 template <int NR, bool OUTBF>
@@ -79,7 +82,7 @@ struct TcLayout {
     static constexpr int Cols = 256;
     static_assert(Bar % 8 == 0 && Row % 16 == 0 && Ring % 16 == 0, "alignment");
     static_assert(2 * kTcMaxParts * 32 * 4 <= 2 * kTcKeys * 128, "the parts' weights fit the value buffer");
-    static_assert(kRowTile * kAttnMaxT * 4 <= 2 * kTcKeys * 128, "the own scores fit the value buffer");
+    static_assert(kTcOwnStride * kAttnMaxT * 4 <= 3 * kTcKeys * 128, "the own scores fit the buffers of V and P");
 };
 
 // Shared-memory descriptor of an operand stored with the M (or N) dimension
@@ -181,7 +184,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + Ly::Misc) + 1;
     int* s_flag = reinterpret_cast<int*>(smem + Ly::Misc) + 2;
     volatile unsigned* s_grow = reinterpret_cast<volatile unsigned*>(smem + Ly::Misc) + 4;   // [2] the step whose maxima move, + 1
-    float* s_own = reinterpret_cast<float*>(smem + Ly::V);       // [R][T] own scores, before the first values
+    float* s_own = reinterpret_cast<float*>(smem + Ly::V);       // [T][kTcOwnStride] own scores, before the first values
     const float NEG_INF = -__uint_as_float(0x7F800000u);
 
     // Tensor memory before dependents may start: one of theirs that held it
@@ -300,16 +303,22 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
         // ---- the step's own rows, in fp32
         if (own) {
             const uint16_t* kb = a.qkv + (size_t)b * a.T * rowlen + (size_t)(a.Hq + kh) * D;
-            for (int e = tid; e < R * a.T; e += kTcThreads) {
+            const uint16_t* vb = kb + (size_t)a.Hkv * D + dim;
+            const int tmax = (r0 + R - 1) / a.G;                 // the last row seen here
+            uint32_t v[8];                                       // 8 rows' values; the first 8 arrive during the scores
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[k] = vb[(size_t)min(k, tmax) * rowlen];
+            for (int e = tid >> 1; e < R * a.T; e += kTcThreads / 2) {   // two lanes a score, half the dims each
                 const int r = e / a.T, j = e - r * a.T, tk = (r0 + r) / a.G;
                 float x = NEG_INF;
                 if (j <= tk) {
                     const int h = kh * a.G + (r0 + r) - tk * a.G;
-                    const uint4* qp = reinterpret_cast<const uint4*>(a.qkv + ((size_t)b * a.T + tk) * rowlen + (size_t)h * D);
-                    const uint4* kp = reinterpret_cast<const uint4*>(kb + (size_t)j * rowlen);
+                    const int d0 = (tid & 1) * (D / 2);
+                    const uint4* qp = reinterpret_cast<const uint4*>(a.qkv + ((size_t)b * a.T + tk) * rowlen + (size_t)h * D + d0);
+                    const uint4* kp = reinterpret_cast<const uint4*>(kb + (size_t)j * rowlen + d0);
                     float s0 = 0.f, s1 = 0.f;
 #pragma unroll 4
-                    for (int i = 0; i < D / 8; ++i) {
+                    for (int i = 0; i < D / 16; ++i) {
                         const uint4 x4 = qp[i], y4 = kp[i];
                         const uint32_t xs[4] = {x4.x, x4.y, x4.z, x4.w}, ys[4] = {y4.x, y4.y, y4.z, y4.w};
 #pragma unroll
@@ -318,48 +327,67 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
                             s1 += __uint_as_float(xs[k] & 0xFFFF0000u) * __uint_as_float(ys[k] & 0xFFFF0000u);
                         }
                     }
-                    x = (s0 + s1) * sl2;
+                    s0 += s1;
+                    x = (s0 + __shfl_xor_sync(3u << (lane & 30), s0, 1)) * sl2;
                 }
-                s_own[e] = x;
+                s_own[j * kTcOwnStride + r] = x;
             }
             __syncthreads();
-            for (int r = warp; r < R; r += kTcThreads / 32) {    // each row's maximum, probabilities and sum
+            // each row's maximum, probabilities and sum: 2^lg lanes a row
+            const int lg = a.T <= 8 ? 3 : 5, sub = lane >> lg, l0 = lane & ((1 << lg) - 1);
+            for (int rw = warp << (5 - lg); rw < R; rw += (kTcThreads / 32) << (5 - lg)) {
+                const int r = rw + sub;
                 float m = NEG_INF, sum = 0.f;
-                for (int j = lane; j < a.T; j += 32) m = fmaxf(m, s_own[r * a.T + j]);
+                if (r < R)
+                    for (int j = l0; j < a.T; j += 1 << lg) m = fmaxf(m, s_own[j * kTcOwnStride + r]);
 #pragma unroll
-                for (int off = 16; off > 0; off >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
+                for (int off = 16; off > 0; off >>= 1)
+                    if (off < 1 << lg) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
                 const float mm = m == NEG_INF ? 0.f : m;         // (only NaN scores)
-                for (int j = lane; j < a.T; j += 32) {
-                    const float p = ex2(s_own[r * a.T + j] - mm);
-                    s_own[r * a.T + j] = p;
-                    sum += p;
-                }
+                if (r < R)
+                    for (int j = l0; j < a.T; j += 1 << lg) {
+                        const float p = ex2(s_own[j * kTcOwnStride + r] - mm);
+                        s_own[j * kTcOwnStride + r] = p;
+                        sum += p;
+                    }
 #pragma unroll
-                for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-                if (lane == 0) {
+                for (int off = 16; off > 0; off >>= 1)
+                    if (off < 1 << lg) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+                if (l0 == 0 && r < R) {
                     s_m2[r] = mm;
                     s_l2[r] = sum;
                 }
             }
             __syncthreads();
             if (worker) {
-                const uint16_t* vb = a.qkv + (size_t)b * a.T * rowlen + (size_t)(a.Hq + a.Hkv + kh) * D + dim;
-                const int tmax = (r0 + R - 1) / a.G;
                 float o2[NT][8];
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) o2[t][i] = 0.f;
-                for (int j = 0; j <= tmax; ++j) {
-                    const float v = __uint_as_float((uint32_t)vb[(size_t)j * rowlen] << 16);
-                    const int rmin = max(0, j * a.G - r0);       // rows from there on see row j
+#pragma unroll 1
+                for (int j0 = 0; j0 <= tmax; j0 += 8) {
+                    if (j0 > 0) {
 #pragma unroll
-                    for (int t = 0; t < NT; ++t)
+                        for (int k = 0; k < 8; ++k) v[k] = vb[(size_t)min(j0 + k, tmax) * rowlen];
+                    }
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) {
-                            const int r = 8 * (hf + 2 * t) + i;
-                            if (r >= rmin && r < R) o2[t][i] += s_own[r * a.T + j] * v;
-                        }
+                    for (int k = 0; k < 8; ++k) {
+                        if (j0 + k > tmax) continue;             // (the same in all threads)
+                        const int j = j0 + k, rmin = j * a.G - r0;   // rows from rmin on see row j
+                        const float y = __uint_as_float(v[k] << 16);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+                            if (hf + 2 * t < NR) {
+                                float p8[8];
+                                row8(s_own + j * kTcOwnStride, hf + 2 * t, p8);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i) {
+                                    const float sum = o2[t][i] + p8[i] * y;
+                                    o2[t][i] = 8 * (hf + 2 * t) + i >= rmin ? sum : o2[t][i];
+                                }
+                            }
+                    }
                 }
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
@@ -602,12 +630,17 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
             for (int t = 0; t < NT; ++t)
                 if (hf + 2 * t < NR) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        float v = l[t][i];
+                    for (int w = 4; w > 0; w >>= 1)              // half the values stay, the other lane has the rest
 #pragma unroll
-                        for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-                        if (lane == 0) s_red[q4 * 32 + 8 * (hf + 2 * t) + i] = v;
-                    }
+                        for (int i = 0; i < w; ++i) {
+                            const bool up = (lane & (4 * w)) != 0;
+                            const float give = up ? l[t][i] : l[t][i + w];
+                            l[t][i] = (up ? l[t][i + w] : l[t][i]) + __shfl_xor_sync(0xffffffffu, give, 4 * w);
+                        }
+                    float y = l[t][0];
+                    y += __shfl_xor_sync(0xffffffffu, y, 2);
+                    y += __shfl_xor_sync(0xffffffffu, y, 1);
+                    if ((lane & 3) == 0) s_red[q4 * 32 + 8 * (hf + 2 * t) + (lane >> 2)] = y;
                 }
         }
         __syncthreads();
@@ -620,6 +653,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
             s_w2[tid] = w2;
             s_M[tid] = M;
             s_L[tid] = lc * w1 + s_l2[tid] * w2;
+            s_f[tid] = 1.f / s_L[tid];
         }
         __syncthreads();
         float v[NT][8];
@@ -643,20 +677,29 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
                 v[t][i] = (__uint_as_float(s8[i]) + (__uint_as_float(h8[i]) + __uint_as_float(l8[i]))) * s_w1[r] + __uint_as_float(o8[i]) * s_w2[r];
             }
         }
-        auto store = [&](int r, float x, float sum) {            // this lane's dim of row r
-            const int j = (r0 + r) / a.G, h = kh * a.G + (r0 + r) - j * a.G;
-            const size_t at = ((size_t)b * a.T + j) * (size_t)a.Hq * D + (size_t)h * D + dim;
-            if (OUTBF) static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(x / sum);
-            else static_cast<float*>(a.out)[at] = x / sum;
-        };
-        if (ua == 0 && own) {
+        // this lane's dim of the rows; inv holds one over their sums
+        auto store = [&](const float (&x)[NT][8], const float* inv) {
 #pragma unroll
-            for (int t = 0; t < NT; ++t)
+            for (int t = 0; t < NT; ++t) {
+                const int ra = r0 + 8 * (hf + 2 * t);
+                int j = ra / a.G, hg = ra - j * a.G;             // token, head of the group
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const int r = 8 * (hf + 2 * t) + i;
-                    if (worker && r < R) store(r, v[t][i], s_L[r]);
+                    if (worker && r < R) {
+                        const size_t at = ((size_t)b * a.T + j) * (size_t)a.Hq * D + (size_t)(kh * a.G + hg) * D + dim;
+                        if (OUTBF) static_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(x[t][i] * inv[r]);
+                        else static_cast<float*>(a.out)[at] = x[t][i] * inv[r];
+                    }
+                    if (++hg == a.G) {
+                        hg = 0;
+                        ++j;
+                    }
                 }
+            }
+        };
+        if (ua == 0 && own) {
+            store(v, s_f);
         } else {
             float* slot = a.partials + ((size_t)blockIdx.x * 2 + (ua == 0 ? 1 : 0)) * Ly::Slot;
 #pragma unroll
@@ -722,6 +765,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
                         s_f[tid] = fo;
                         s_M[tid] = M;
                         s_L[tid] = s_L[tid] * fo + sum;
+                        s_w1[tid] = 1.f / s_L[tid];
                     }
                     __syncthreads();
 #pragma unroll
@@ -751,13 +795,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
                         }
                     __syncthreads();
                 }
-#pragma unroll
-                for (int t = 0; t < NT; ++t)
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const int r = 8 * (hf + 2 * t) + i;
-                        if (worker && r < R) store(r, run[t][i], s_L[r]);
-                    }
+                store(run, s_w1);
             }
         }
         tc_fence_before();                                       // O has been read
@@ -805,6 +843,7 @@ cudaError_t launch(const Args& a, int grid, int tile_cost, int min_units, cudaSt
 
 cudaError_t launch_attn_kv4_tc(const kv4attn::Args& a, int NR, bool out_bf16, int grid, int tile_cost, int min_units,
                                cudaStream_t s) {
+    if (NR == 2 && !out_bf16) return launch<2, false>(a, grid, tile_cost, min_units, s);
 #define QV_KV4_TC_CASE(NRV) \
     if (NR == NRV) return out_bf16 ? launch<NRV, true>(a, grid, tile_cost, min_units, s) : launch<NRV, false>(a, grid, tile_cost, min_units, s);
     QV_KV4_TC_CASE(3) QV_KV4_TC_CASE(4)
