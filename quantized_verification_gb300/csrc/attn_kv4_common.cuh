@@ -33,7 +33,7 @@ constexpr float kBias = 7.f;                    // log2 of p at the running maxi
 // A row's running maximum moves to product v: c, with p = 2^(sl2 x + c) for a
 // product x, and the product at which it moves next. Up to |m| = 2^20 the
 // roundings of sl2 x + c and of the limit stay below 2^-1, and p in f16's
-// range. Above, the last bit of sl2 x nears 1 and more: no lag, no bias (-m is
+// range (65504). Above, the last bit of sl2 x nears 1 and more: no lag, no bias (-m is
 // exact), and p <= 2^8 as long as m's last bit is 16 at most. From 2^27 on the
 // scores hold no information that fp32 keeps: the row becomes NaN.
 struct RowMax {
@@ -42,7 +42,7 @@ struct RowMax {
         const float m = rintf(v * sl2);
         if (fabsf(m) < 1048576.f) {
             c = kBias - m;
-            limit = (m + kLazy) / sl2;
+            limit = __fdividef(m + kLazy, sl2);              // (2 ulp: p < 2^15.5 all the same)
         } else {
             c = fabsf(m) < 134217728.f ? -m : __uint_as_float(0x7FC00000u);
             limit = v;

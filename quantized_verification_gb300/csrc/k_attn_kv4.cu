@@ -245,6 +245,9 @@ __global__ void __launch_bounds__(Layout<D, NR>::Threads, Layout<D, NR>::Ctas) a
                 dst[32] = make_uint2(__byte_perm(q.y, q.w, 0x5410), __byte_perm(q.y, q.w, 0x7632));
             }
         }
+        // the step's last row that a query row sees (in warp 0's part of s_wm, until that is written)
+        int* s_tok = reinterpret_cast<int*>(s_wm);
+        if (tid < RW) s_tok[tid] = tid < R ? (r0 + tid) / a.G : -1;
         __syncthreads();
         uint2 qf[Ly::QRegs ? NR : 1][Ly::QRegs ? KS : 1];
         if constexpr (Ly::QRegs) {
@@ -414,7 +417,7 @@ __global__ void __launch_bounds__(Layout<D, NR>::Threads, Layout<D, NR>::Ctas) a
                 for (int nt = 0; nt < NR; ++nt)
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int r = 8 * nt + 2 * t4 + e, tok = r < R ? (r0 + r) / a.G : -1;   // rows 0..tok are visible
+                        const int tok = s_tok[8 * nt + 2 * t4 + e];      // rows 0..tok are visible
                         if (j0 + key_g > tok) acc[nt][e] = NEG_INF;
                         if (j0 + 8 + key_g > tok) acc[nt][2 + e] = NEG_INF;
                     }
