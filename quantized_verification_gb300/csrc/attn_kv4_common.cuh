@@ -127,21 +127,25 @@ __device__ __forceinline__ float2 unpack_f16x2(uint32_t x) {
     return make_float2(lo, hi);
 }
 
-// A key scale as a bf16 pair, and -24 times it (exact: 2 + 4 bits).
+// A key scale as a bf16 pair, and -24 and -136 times it (exact: 2 + 4 and 4 + 4 bits).
 struct KeyScale {
-    uint32_t s, off;
+    uint32_t s, off, off0;
     __device__ __forceinline__ KeyScale() {}
     __device__ __forceinline__ explicit KeyScale(uint32_t b) {
         s = b * 0x00100010u + 0x38003800u;
         off = hmul2_bf16(s, 0xC1C0C1C0u);                 // -24.0
+        off0 = hmul2_bf16(s, 0xC308C308u);                // -136.0
     }
 };
 // Nibbles J of the two 16-bit halves of x as bf16 values q * s: shifted to bits
 // 3..6 with the sign bit flipped, under 16.0 (0x4180), a nibble is 24 + q.
 // Left shifts are multiplications by a register (the FMA pipe has room, the
-// ALU, which does the masking and the right shifts, is the busiest pipe).
-template <int J>
+// ALU, which does the masking and the right shifts, is the busiest pipe). Low:
+// the lowest nibble stays where it is, under 128.0 (0x4300), as 136 + q; one
+// instruction less for one register more a scale.
+template <int J, bool Low>
 __device__ __forceinline__ uint32_t key_pair(uint32_t x, const KeyScale& sc, uint32_t eight) {
+    if (Low && J == 0) return hfma2_bf16(and_xor(x, 0x000F000Fu, 0x43084308u), sc.s, sc.off0);
     const uint32_t y = J == 0 ? x * eight : x >> (J == 0 ? 0 : 4 * J - 3);
     return hfma2_bf16(and_xor(y, 0x00780078u, 0x41C041C0u), sc.s, sc.off);
 }

@@ -52,7 +52,7 @@
 //     in f16, gives the A fragments of the dims a thread owns.
 // What bounds it (GB300). Long contexts: the ALUs, which unpack 256 codes a
 // position (55 % busy, with 61 % of the issue slots; DRAM 45 %): one token over
-// 131071 and 120000 positions, 8 key/value heads, bf16 out, 73 us, 3.8 TB/s of
+// 131071 and 120000 positions, 8 key/value heads, bf16 out, 72 us, 3.9 TB/s of
 // cache. Short ones: the chain launch, lengths, table, record, products, merge:
 // one token over 517 positions 5.9 us, 5 tokens over 2043 8.7 us.
 //
@@ -473,11 +473,12 @@ __global__ void __launch_bounds__(Layout<D, NR>::Threads, Layout<D, NR>::Ctas) a
                 k2.sc[k] = KeyScale(lds_u8(rec + (uint32_t)(Rec::KS + key * Rec::RowScales + (D == 128 ? t4 : t4 >> 1))));
             }
         };
+        constexpr bool kLow = NR == 1;                           // (larger tiles have no registers to spare)
         auto qk_word = [&](float (&acc)[NR][4], const Keys<W>& k2, int w) {
-            qk(acc, 2 * w, key_pair<0>(k2.x[0][w], k2.sc[0], c8), key_pair<0>(k2.x[1][w], k2.sc[1], c8),
-               key_pair<1>(k2.x[0][w], k2.sc[0], c8), key_pair<1>(k2.x[1][w], k2.sc[1], c8));
-            qk(acc, 2 * w + 1, key_pair<2>(k2.x[0][w], k2.sc[0], c8), key_pair<2>(k2.x[1][w], k2.sc[1], c8),
-               key_pair<3>(k2.x[0][w], k2.sc[0], c8), key_pair<3>(k2.x[1][w], k2.sc[1], c8));
+            qk(acc, 2 * w, key_pair<0, kLow>(k2.x[0][w], k2.sc[0], c8), key_pair<0, kLow>(k2.x[1][w], k2.sc[1], c8),
+               key_pair<1, kLow>(k2.x[0][w], k2.sc[0], c8), key_pair<1, kLow>(k2.x[1][w], k2.sc[1], c8));
+            qk(acc, 2 * w + 1, key_pair<2, kLow>(k2.x[0][w], k2.sc[0], c8), key_pair<2, kLow>(k2.x[1][w], k2.sc[1], c8),
+               key_pair<3, kLow>(k2.x[0][w], k2.sc[0], c8), key_pair<3, kLow>(k2.x[1][w], k2.sc[1], c8));
         };
         auto mask = [&](float (&acc)[NR][4], int p0, int left) {
             if (p0 + 16 > left) {

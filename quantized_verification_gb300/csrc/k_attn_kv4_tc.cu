@@ -454,10 +454,10 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
 #pragma unroll
                     for (int w = 0; w < 4; ++w) {
                         const uint32_t y = sw == gr ? x[0][w] : x[1][w];
-                        k32[16 * gr + 4 * w] = key_pair<0>(y, sc, c8);
-                        k32[16 * gr + 4 * w + 1] = key_pair<1>(y, sc, c8);
-                        k32[16 * gr + 4 * w + 2] = key_pair<2>(y, sc, c8);
-                        k32[16 * gr + 4 * w + 3] = key_pair<3>(y, sc, c8);
+                        k32[16 * gr + 4 * w] = key_pair<0, true>(y, sc, c8);
+                        k32[16 * gr + 4 * w + 1] = key_pair<1, true>(y, sc, c8);
+                        k32[16 * gr + 4 * w + 2] = key_pair<2, true>(y, sc, c8);
+                        k32[16 * gr + 4 * w + 3] = key_pair<3, true>(y, sc, c8);
                     }
                 }
                 tmem_st_x32(tlane + Ly::kK + 32 * hf, k32);
