@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
 #pragma unroll
                 for (int off = 16; off > 0; off >>= 1)
                     if (off < 1 << lg) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, off));
-                const float mm = m == NEG_INF ? 0.f : m;         // (only NaN scores)
+                const float mm = m == NEG_INF ? 0.f : m;         // (no score above -inf)
                 if (r < R)
                     for (int j = l0; j < a.T; j += 1 << lg) {
                         const float p = ex2(s_own[j * kTcOwnStride + r] - mm);
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
                 for (int off = 16; off > 0; off >>= 1)
                     if (off < 1 << lg) sum += __shfl_xor_sync(0xffffffffu, sum, off);
                 if (l0 == 0 && r < R) {
-                    s_m2[r] = mm;
+                    s_m2[r] = sum == 0.f ? NEG_INF : mm;         // (a NaN goes on)
                     s_l2[r] = sum;
                 }
             }

@@ -572,3 +572,30 @@ def test_scores_of_millions(qv, NB, D, T, Hq):
             else:
                 tol = 2.0 ** -20 if dt == torch.float32 else 2.0 ** -11 + 2.0 ** -8
                 assert np.all(np.abs(o - best) <= tol * np.abs(best) + 1e-30), (want_max, np.abs(o - best).max())
+
+
+@pytest.mark.parametrize("NB", [9, 400])
+@pytest.mark.parametrize("D,T,Hq", [(128, 1, 2), (128, 5, 4), (128, 8, 4), (64, 5, 4)])
+def test_own_scores_of_minus_infinity(qv, NB, D, T, Hq):
+    """Own keys with an infinity that makes every own score -inf, over cached scores far below 0 (about -300): the own
+    rows have no part in the output, which is the mean of the cached values (all cached keys are equal, and so are the
+    probabilities). Sums round by 2^-24 each, 300 of them a range at most. A probability is 2^(7 + f), f a score's part
+    behind the point, so that its f16 parts are off by 2^-22 of it, or 2^-11 where bf16 outputs keep one part (the sum of
+    the probabilities is not rounded along with them); bf16 outputs are rounded by 2^-8 once more."""
+    n = 32 * NB - 5
+    g = gen(12)
+    codes = np.concatenate([np.full((NB, 1, 32 * D), -7), torch.randint(-7, 8, (NB, 1, 32 * D), generator=g).numpy()], axis=2)
+    scales = np.concatenate([np.full((NB, 1, D), 17 * 8), np.full((NB, 1, D), 15 * 8)], axis=2).astype(np.uint8)
+    cache = np.concatenate([ref.pack(codes), scales], axis=2)
+    qkv = torch.randn(T, (Hq + 2) * D, generator=g)
+    qkv[:, : Hq * D] = 1.0
+    qkv[:, Hq * D + 3] = -float("inf")
+    qkv = qkv.to(torch.bfloat16)
+    ws = torch.zeros(qv.qv_attention_kv4_workspace_bytes(1, T, Hq, 1, D, NB), dtype=torch.uint8, device="cuda")
+    want = codes[:, 0, 32 * D:].reshape(NB * 32, D)[:n].mean(0)
+    for dt in (torch.float32, torch.bfloat16):
+        out = torch.empty(T, Hq * D, dtype=dt, device="cuda")
+        qv.qv_attention_verify_kv4(qkv.cuda(), cu(cache), cu(np.array([n], np.int32)), T, Hq, 1, 12.0 / D, out, ws)
+        err = np.abs(np_(out.double()).reshape(T * Hq, D) - want)
+        rounding = 2.0 ** -8 + 2.0 ** -11 if dt == torch.bfloat16 else 2.0 ** -22
+        assert np.all(err <= 7 * 300 * 2.0 ** -24 + rounding * np.abs(want)), err.max()
