@@ -565,8 +565,8 @@ QV_API qv_status qv_kv4_read(const uint8_t* cache, const int32_t* start, const i
  * the values the cache holds; for bf16 outputs the probabilities are rounded to
  * 11 bits before the product with the values. Results are the same from call
  * to call on one GPU. A row whose largest score has a magnitude of 2^27 * ln 2
- * = 9.3e7 or more (scale included; binary32 no longer tells its scores apart) is
- * NaN.
+ * = 9.3e7 or more (scale included; binary32 no longer tells its scores apart)
+ * can be NaN.
  */
 QV_API size_t qv_attention_kv4_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int NB);
 QV_API qv_status qv_attention_verify_kv4(const uint16_t* qkv, const uint8_t* cache, const int32_t* block_table,

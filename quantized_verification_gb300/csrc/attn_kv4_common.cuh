@@ -35,7 +35,10 @@ constexpr float kBias = 7.f;                    // log2 of p at the running maxi
 // roundings of sl2 x + c and of the limit stay below 2^-1, and p in f16's
 // range (65504). Above, the last bit of sl2 x nears 1 and more: no lag, no bias (-m is
 // exact), and p <= 2^8 as long as m's last bit is 16 at most. From 2^27 on the
-// scores hold no information that fp32 keeps: the row becomes NaN.
+// scores hold no information that fp32 keeps: the row becomes NaN. Down from
+// -2^27 they count as none at all (p = 0, and the row has seen no key yet): any
+// other score is above them by more than fp32's exponents span, and a row with
+// no other ends as 0 / 0.
 struct RowMax {
     float c, limit;
     __device__ __forceinline__ RowMax(float v, float sl2) {
@@ -44,8 +47,9 @@ struct RowMax {
             c = kBias - m;
             limit = __fdividef(m + kLazy, sl2);              // (2 ulp: p < 2^15.5 all the same)
         } else {
-            c = fabsf(m) < 134217728.f ? -m : __uint_as_float(0x7FC00000u);
-            limit = v;
+            const float NEG_INF = -__uint_as_float(0x7F800000u);
+            c = fabsf(m) < 134217728.f ? -m : (m < 0.f ? NEG_INF : __uint_as_float(0x7FC00000u));
+            limit = m > -134217728.f ? v : NEG_INF;
         }
     }
 };

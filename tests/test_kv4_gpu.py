@@ -599,3 +599,28 @@ def test_own_scores_of_minus_infinity(qv, NB, D, T, Hq):
         err = np.abs(np_(out.double()).reshape(T * Hq, D) - want)
         rounding = 2.0 ** -8 + 2.0 ** -11 if dt == torch.bfloat16 else 2.0 ** -22
         assert np.all(err <= 7 * 300 * 2.0 ** -24 + rounding * np.abs(want)), err.max()
+
+
+@pytest.mark.parametrize("NB", [9, 400])
+@pytest.mark.parametrize("D,T,Hq", [(128, 1, 2), (128, 5, 4), (128, 8, 4), (64, 5, 4)])
+def test_keys_of_no_weight_at_all(qv, NB, D, T, Hq):
+    """Every other block's scores are about -1e8, beyond what the running maxima hold: the result is that of the other
+    blocks alone, within their bound."""
+    n, g, odd = 32 * NB - 5, gen(13), np.arange(NB) % 2
+    codes = torch.randint(-7, 8, (NB, 1, 64 * D), generator=g).numpy()
+    codes[odd == 0, :, : 32 * D] = -7
+    scales = np.full((NB, 1, 2 * D), 15 * 8, np.uint8)
+    scales[:, :, :D] = np.where(odd == 0, 255, 8 * 5)[:, None, None]
+    cache = np.concatenate([ref.pack(codes), scales], axis=2)
+    qkv = torch.randn(T, (Hq + 2) * D, generator=g)
+    qkv[:, : Hq * D] = 16.0
+    qkv = qkv.to(torch.bfloat16)
+    table = np.arange(NB, dtype=np.int32)[None]
+    alone = np.where(odd == 0, -1, table).astype(np.int32)
+    scale, ln = 12.0 / D, np.array([n], np.int32)
+    ws = torch.zeros(qv.qv_attention_kv4_workspace_bytes(1, T, Hq, 1, D, NB), dtype=torch.uint8, device="cuda")
+    want, vmax, smax = ref.attend(qkv.float().numpy(), cache, ln, T, Hq, 1, D, NB, scale, alone)
+    for dt in (torch.float32, torch.bfloat16):
+        out = torch.empty(T, Hq * D, dtype=dt, device="cuda")
+        qv.qv_attention_verify_kv4(qkv.cuda(), cu(cache), cu(ln), T, Hq, 1, scale, out, ws, block_table=cu(table))
+        close(out, want, vmax, smax, D)
