@@ -21,7 +21,7 @@ constexpr int kMinUnits = 16;                   // places of a CTA's range at le
 constexpr int kAttnMaxT = 256;                  // tokens of a step (QV_MAX_M)
 constexpr size_t kCounterBytes = 4096;         // at the workspace's start, whatever the shape
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kTileCost = 26;                   // units' worth of a tile's own costs
+constexpr int kTileCost = 20;                   // units' worth of a tile's own costs
 constexpr int kMaxCluster = 8;                  // CTAs of a cluster that share a tile
 constexpr int kClusterUnits = 6;                // a larger cluster while its CTAs have more units than this
 constexpr int kClusterMost = 48;                // no clusters above so many units a CTA
