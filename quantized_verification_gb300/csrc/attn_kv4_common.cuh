@@ -10,6 +10,7 @@
 #include <cstdint>
 
 #include "kv4_common.cuh"
+#include "qv.h"
 #include "qv_internal.h"
 #include "qv_ptx.cuh"
 
@@ -18,7 +19,7 @@ namespace kv4attn {
 
 constexpr int kRowTile = 32;                    // query rows of a tile
 constexpr int kMinUnits = 16;                   // places of a CTA's range at least: two units a warp
-constexpr int kAttnMaxT = 256;                  // tokens of a step (QV_MAX_M)
+constexpr int kAttnMaxT = QV_MAX_M;             // tokens of a step
 constexpr size_t kCounterBytes = 4096;         // at the workspace's start, whatever the shape
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTileCost = 20;                   // units' worth of a tile's own costs
@@ -35,21 +36,19 @@ constexpr float kBias = 7.f;                    // log2 of p at the running maxi
 // roundings of sl2 x + c and of the limit stay below 2^-1, and p in f16's
 // range (65504). Above, the last bit of sl2 x nears 1 and more: no lag, no bias (-m is
 // exact), and p <= 2^8 as long as m's last bit is 16 at most. From 2^27 on the
-// scores hold no information that fp32 keeps: the row becomes NaN. Down from
-// -2^27 they count as none at all (p = 0, and the row has seen no key yet): any
-// other score is above them by more than fp32's exponents span, and a row with
-// no other ends as 0 / 0.
+// scores hold no information that fp32 keeps: the row becomes NaN. m stays above
+// -2^27: scores below that have p = 0 next to any others, and a row with no
+// others ends as 0 / 0.
 struct RowMax {
     float c, limit;
     __device__ __forceinline__ RowMax(float v, float sl2) {
-        const float m = rintf(v * sl2);
+        const float m = fmaxf(rintf(v * sl2), -134217728.f);
         if (fabsf(m) < 1048576.f) {
             c = kBias - m;
             limit = __fdividef(m + kLazy, sl2);              // (2 ulp: p < 2^15.5 all the same)
         } else {
-            const float NEG_INF = -__uint_as_float(0x7F800000u);
-            c = fabsf(m) < 134217728.f ? -m : (m < 0.f ? NEG_INF : __uint_as_float(0x7FC00000u));
-            limit = m > -134217728.f ? v : NEG_INF;
+            c = m < 134217728.f ? -m : __uint_as_float(0x7FC00000u);
+            limit = v;
         }
     }
 };
@@ -133,12 +132,11 @@ __device__ __forceinline__ float2 unpack_f16x2(uint32_t x) {
 
 // A key scale as a bf16 pair, and -24 and -136 times it (exact: 2 + 4 and 4 + 4 bits).
 struct KeyScale {
-    uint32_t s, off, off0;
+    uint32_t s, off;
     __device__ __forceinline__ KeyScale() {}
     __device__ __forceinline__ explicit KeyScale(uint32_t b) {
         s = b * 0x00100010u + 0x38003800u;
         off = hmul2_bf16(s, 0xC1C0C1C0u);                 // -24.0
-        off0 = hmul2_bf16(s, 0xC308C308u);                // -136.0
     }
 };
 // Nibbles J of the two 16-bit halves of x as bf16 values q * s: shifted to bits
@@ -149,7 +147,8 @@ struct KeyScale {
 // instruction less for one register more a scale.
 template <int J, bool Low>
 __device__ __forceinline__ uint32_t key_pair(uint32_t x, const KeyScale& sc, uint32_t eight) {
-    if (Low && J == 0) return hfma2_bf16(and_xor(x, 0x000F000Fu, 0x43084308u), sc.s, sc.off0);
+    if constexpr (Low && J == 0)
+        return hfma2_bf16(and_xor(x, 0x000F000Fu, 0x43084308u), sc.s, hmul2_bf16(sc.s, 0xC308C308u));   // -136.0
     const uint32_t y = J == 0 ? x * eight : x >> (J == 0 ? 0 : 4 * J - 3);
     return hfma2_bf16(and_xor(y, 0x00780078u, 0x41C041C0u), sc.s, sc.off);
 }
