@@ -17,7 +17,8 @@
 // each, those before it (by value, then by the lower index). Where ties or
 // masks leave too many of them, warps keep sorted lists of 32 instead.
 //
-// A row is the work of one CTA, or of a cluster of C of them that split it
+// A row is the work of one CTA (of 512 threads, or 128 for many short rows,
+// whose 32 maxima are then those of every 4 lanes), or of a cluster of C that split it
 // (launch_token_logprobs): each sends its statistics, its entries at or above
 // its own tau and its largest maxima to the first, which takes a tau of the
 // whole row from the latter before it counts. One cluster barrier in all.
@@ -41,15 +42,17 @@ namespace cg = cooperative_groups;
 namespace qv {
 namespace {
 
-constexpr int kLpThreads = 512;
-constexpr int kLpWarps = kLpThreads / 32;
+constexpr int kLpThreads = 512;                 // of a CTA that has a long row, or a part of it
+constexpr int kLpSmall = 128;                   // of a CTA that has a short one (launch_token_logprobs)
 constexpr int kLpMaxCluster = 16;
 constexpr int kLpUnroll = 4;                    // vectors in flight per thread
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-constexpr int kLpCand = 1024;                   // entries of a row ordered by counting, kLpCand / kLpMaxCluster of a CTA
 constexpr int kLpTops = 64;                     // maxima of a row that the CTAs of a cluster send, kLpTops / C each
-static_assert(kLpCand / kLpMaxCluster >= 32 && kLpCand >= kLpWarps * 32, "a CTA's K entries and the warps' lists fit");
+// Entries of a row ordered by counting (of a CTA of a cluster: 1 / kLpMaxCluster of that).
+__host__ __device__ constexpr int lp_cand(int threads) { return threads == kLpThreads ? 1024 : 256; }
+static_assert(lp_cand(kLpThreads) / kLpMaxCluster >= 32 && lp_cand(kLpThreads) >= kLpThreads &&
+              lp_cand(kLpSmall) >= kLpSmall, "a CTA's K entries and its warps' lists of 32 fit");
 
 struct LpArgs {
     const uint8_t* x;          // logits [M][V]
@@ -142,7 +145,7 @@ __device__ __forceinline__ T warp_merge_desc(T v, T o) {
 // Merges the descending lists of warps 0..n-1 (n a power of two) into warp
 // 0's. All threads of the CTA call it.
 template <class T>
-__device__ __forceinline__ T block_merge_desc(T v, T* sm /* [kLpWarps][32] */, int n) {
+__device__ __forceinline__ T block_merge_desc(T v, T* sm /* [n][32] */, int n) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     for (int h = n >> 1; h > 0; h >>= 1) {
         if (warp >= h && warp < 2 * h) sm[warp * 32 + lane] = v;
@@ -213,14 +216,14 @@ __device__ __forceinline__ void warp_insert(unsigned long long& list, unsigned l
 
 // Visits the entries that thread t of the CTA owns, 32 vectors at a time (the
 // whole warp calls it): fn(value, index, there).
-template <bool BF16, class F>
+template <int Threads, bool BF16, class F>
 __device__ __forceinline__ void for_thread(const Row<BF16>& r, int t, bool first_cta, int v0, int v1, F&& fn) {
     constexpr int E = Row<BF16>::E;
     const int lane = threadIdx.x & 31;
     const int one = first_cta ? r.single(t) : -1;
     if (one >= 0) fn(r.at(one), one, lane == 0);
-    for (int base = v0 + t; base < v1; base += 32 * kLpThreads) {
-        const int vn = base + lane * kLpThreads;
+    for (int base = v0 + t; base < v1; base += 32 * Threads) {
+        const int vn = base + lane * Threads;
         float v[E];
 #pragma unroll
         for (int e = 0; e < E; ++e) v[e] = 0.f;
@@ -230,22 +233,24 @@ __device__ __forceinline__ void for_thread(const Row<BF16>& r, int t, bool first
     }
 }
 
-template <bool BF16>
-__global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const LpArgs a) {
+template <bool BF16, int Threads>
+__global__ void __launch_bounds__(Threads, Threads == kLpThreads ? 2 : 10) token_logprobs_kernel(const LpArgs a) {
+    constexpr int Warps = Threads / 32, Cand = lp_cand(Threads);
+    constexpr bool Clusters = Threads == kLpThreads;           // CTAs of short rows have theirs to themselves
     constexpr int E = Row<BF16>::E;
-    __shared__ Stat s_stat[kLpWarps];
+    __shared__ Stat s_stat[Warps];
     // written by every CTA of the row (in its first CTA)
     __shared__ Stat c_stat[kLpMaxCluster];
     __shared__ float c_top[kLpTops];
-    __shared__ unsigned long long c_keys[kLpCand];
+    __shared__ unsigned long long c_keys[Clusters ? Cand : 1];
     __shared__ int c_n[kLpMaxCluster];
-    __shared__ unsigned long long s_keys[kLpCand];             // entries, or the warps' lists
+    __shared__ unsigned long long s_keys[Cand];             // entries, or the warps' lists
     __shared__ float s_top[32], s_sorted[32];
-    __shared__ int s_who[kLpThreads];
+    __shared__ int s_who[Threads];
     __shared__ int s_n, s_m;
     __shared__ float s_tau, s_max, s_ls;
     cg::cluster_group cluster = cg::this_cluster();
-    const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+    const int C = Clusters ? (int)cluster.num_blocks() : 1, rank = Clusters ? (int)cluster.block_rank() : 0;
     if (C > 1) cluster_arrive_relaxed();                       // waited for before the first store into another CTA
     allow_dependent_launch();
     grid_dependency_wait();
@@ -258,7 +263,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const LpA
     const int v0 = min(r.nvec, rank * per), v1 = min(r.nvec, v0 + per);
     if (tid == 0) s_n = s_m = 0;
     // the given token's logit, early: its two loads hide behind the pass
-    const int tok = rank == 0 && tid == kLpThreads - 32 ? a.tok[row] : -1;
+    const int tok = rank == 0 && tid == Threads - 32 ? a.tok[row] : -1;
     const bool in_range = tok >= 0 && tok < a.V;
     const float x_tok = in_range ? r.at(tok) : 0.f;
 
@@ -271,16 +276,16 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const LpA
         add_entries(st, v);
     }
     int n = v0 + tid;
-    for (; n + (kLpUnroll - 1) * kLpThreads < v1; n += kLpUnroll * kLpThreads) {
+    for (; n + (kLpUnroll - 1) * Threads < v1; n += kLpUnroll * Threads) {
         uint4 u[kLpUnroll];
 #pragma unroll
-        for (int i = 0; i < kLpUnroll; ++i) u[i] = r.vec(n + i * kLpThreads);
+        for (int i = 0; i < kLpUnroll; ++i) u[i] = r.vec(n + i * Threads);
         float v[kLpUnroll * E];
 #pragma unroll
         for (int i = 0; i < kLpUnroll; ++i) Row<BF16>::unpack(u[i], v + i * E);
         add_entries(st, v);
     }
-    for (; n < v1; n += kLpThreads) {
+    for (; n < v1; n += Threads) {
         float v[E];
         Row<BF16>::unpack(r.vec(n), v);
         add_entries(st, v);
@@ -297,13 +302,20 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const LpA
         st = combine(st, o);
     }
     if (a.K > 0) {
-        const unsigned at = __ballot_sync(0xffffffffu, mine == st.m);
-        float second = lane == __ffs(at) - 1 ? NEG_INF : mine;
+        if constexpr (Warps == 16) {                           // the two largest of a warp
+            const unsigned at = __ballot_sync(0xffffffffu, mine == st.m);
+            float second = lane == __ffs(at) - 1 ? NEG_INF : mine;
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) second = fmaxf(second, __shfl_xor_sync(0xffffffffu, second, off));
-        if (lane == 0) {
-            s_top[warp] = st.m;
-            s_top[16 + warp] = second;
+            for (int off = 16; off > 0; off >>= 1) second = fmaxf(second, __shfl_xor_sync(0xffffffffu, second, off));
+            if (lane == 0) {
+                s_top[warp] = st.m;
+                s_top[16 + warp] = second;
+            }
+        } else {                                               // the largest of every Warps lanes
+            float top = mine;
+#pragma unroll
+            for (int off = 1; off < Warps; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            if (lane % Warps == 0) s_top[(warp * 32 + lane) / Warps] = top;
         }
     }
     if (lane == 0) s_stat[warp] = st;
@@ -323,7 +335,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const LpA
     // The place of p[i] among N numbers (N / 512 threads a number, all of which
     // get it); ties by the index.
     auto place_of = [&](const float* p, int N, int& i) {
-        const int G = kLpThreads / N;                          // threads a number
+        const int G = Threads / N;                          // threads a number
         i = tid / G;
         const float v = p[i];
         int before = 0;
@@ -332,19 +344,19 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const LpA
         return before;
     };
     Stat c = {NEG_INF, 0.f, 0.f};
-    if (warp == kLpWarps - 1) c = reduce16(s_stat, kLpWarps);  // (warp 15, lane 0 finishes a row of one CTA)
+    if (warp == Warps - 1) c = reduce16(s_stat, Warps);     // (the last warp's lane 0 finishes a row of one CTA)
     int total = 0;
     if (a.K > 0) {
         {
             int i;
             const int place = place_of(s_top, 32, i);
-            if (tid % (kLpThreads / 32) == 0) s_sorted[place] = s_top[i];
+            if (tid % (Threads / 32) == 0) s_sorted[place] = s_top[i];
         }
         __syncthreads();
         const float tau = s_sorted[a.K - 1];
 
         // ---- the entries at or above tau
-        const int cap = C > 1 ? kLpCand / kLpMaxCluster : kLpCand;
+        const int cap = C > 1 ? Cand / kLpMaxCluster : Cand;
         if (mine >= tau) {
             s_who[atomicAdd(&s_m, 1)] = tid;                   // (the order of the list does not matter)
             if (own1 >= 0 && x_own >= tau) {
@@ -353,9 +365,9 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const LpA
             }
         }
         __syncthreads();
-        const int who = s_m, each = (v1 - v0 + kLpThreads - 1) / kLpThreads;   // vectors of a thread
-        for (int i = tid; i < who * each; i += kLpThreads) {
-            const int f = i / each, vn = v0 + s_who[f] + (i - f * each) * kLpThreads;
+        const int who = s_m, each = (v1 - v0 + Threads - 1) / Threads;   // vectors of a thread
+        for (int i = tid; i < who * each; i += Threads) {
+            const int f = i / each, vn = v0 + s_who[f] + (i - f * each) * Threads;
             if (vn >= v1) continue;
             float v[E];
             Row<BF16>::unpack(r.vec(vn), v);
@@ -370,15 +382,15 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const LpA
         total = s_n;
         if (total > cap) {                                     // ties or masks: the K first by sorted lists
             unsigned long long list = 0;
-            for (int i = warp; i < who; i += kLpWarps)
-                for_thread(r, s_who[i], rank == 0, v0, v1, [&](float v, int idx, bool there) {
+            for (int i = warp; i < who; i += Warps)
+                for_thread<Threads>(r, s_who[i], rank == 0, v0, v1, [&](float v, int idx, bool there) {
                     const bool in = there && v >= tau;
                     if (!__any_sync(0xffffffffu, in)) return;
                     const unsigned long long k = in ? entry_key(v, idx) : 0ull;
                     const unsigned long long least = __shfl_sync(0xffffffffu, list, a.K - 1);
                     warp_insert(list, k, in && k > least);
                 });
-            list = block_merge_desc(list, s_keys, kLpWarps);
+            list = block_merge_desc(list, s_keys, Warps);
             __syncthreads();
             if (warp == 0) s_keys[lane] = list;
             total = a.K;                                       // (cap >= 32 entries were there)
@@ -387,8 +399,8 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const LpA
     }
     if (C > 1) {                                               // into the first CTA
         cluster_wait();                                        // every CTA of the cluster has started
-        const int part = kLpCand / kLpMaxCluster, tops = kLpTops / C;
-        if (tid == kLpThreads - 32) *cluster.map_shared_rank(c_stat + rank, 0) = c;
+        const int part = Cand / kLpMaxCluster, tops = kLpTops / C;
+        if (tid == Threads - 32) *cluster.map_shared_rank(c_stat + rank, 0) = c;
         if (a.K > 0) {
             if (tid < total) *cluster.map_shared_rank(c_keys + rank * part + tid, 0) = s_keys[tid];
             if (tid >= 64 && tid < 64 + tops) *cluster.map_shared_rank(c_top + rank * tops + tid - 64, 0) = s_sorted[tid - 64];
@@ -396,19 +408,19 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const LpA
         }
         cluster.sync();                                        // every push has landed
         if (rank != 0) return;
-        if (warp == kLpWarps - 1) c = reduce16(c_stat, C);
+        if (warp == Warps - 1) c = reduce16(c_stat, C);
         if (a.K > 0) {
             int i;
             const int place = place_of(c_top, kLpTops, i);
-            if (place == a.K - 1 && tid % (kLpThreads / kLpTops) == 0) s_tau = c_top[i];
+            if (place == a.K - 1 && tid % (Threads / kLpTops) == 0) s_tau = c_top[i];
             if (tid == 0) s_n = 0;
             __syncthreads();
             const unsigned long long least = entry_key(s_tau, 0x7FFFFFFF);
-            for (int e = tid; e < C * part; e += kLpThreads)
+            for (int e = tid; e < C * part; e += Threads)
                 if (e % part < c_n[e / part] && c_keys[e] >= least) s_keys[atomicAdd(&s_n, 1)] = c_keys[e];
         }
     }
-    if (tid == kLpThreads - 32) {
+    if (tid == Threads - 32) {
         const bool none = c.m == NEG_INF;                      // every entry is -inf (or NaN, and then S is NaN)
         s_max = none ? 0.f : c.m;
         s_ls = none ? c.S : logf(c.S);
@@ -423,7 +435,7 @@ __global__ void __launch_bounds__(kLpThreads, 2) token_logprobs_kernel(const LpA
     if (C > 1) total = s_n;
     // ---- an entry's place is the number of entries before it
     const size_t o = row * (size_t)a.K;
-    for (int e = tid; e < total; e += kLpThreads) {
+    for (int e = tid; e < total; e += Threads) {
         const unsigned long long key = s_keys[e];
         int place = 0;
 #pragma unroll 8
@@ -446,16 +458,23 @@ cudaError_t launch_token_logprobs(const void* x, bool bf16, const int32_t* tok, 
     LpArgs a;
     a.x = static_cast<const uint8_t*>(x);
     a.tok = tok; a.V = V; a.K = K; a.logprob = logprob; a.entropy = entropy; a.top_tok = top_tok; a.top_lp = top_lp;
+    // Many short rows: CTAs of 128 threads, ten an SM. A row's reductions and
+    // barriers are then most of its time, and overlap. GB300, us with 512 / 128
+    // threads: 3859 rows of 3245 bf16 logits, 20 tokens, 57/24; fp32: 600 of 3245
+    // 10.0/6.8 (300: 5.6/5.9), 2000 of 8000 34/19, 2000 of 16000 46/34, 1200 of
+    // 32003 37/28 (600: 14.8/15.5), 2000 of 65000 98/100, 2000 of 151936 197/231.
+    const bool small = V <= (1 << 15) && M > 2 * sms * (V >> 13 > 1 ? V >> 13 : 1);
     int C = 1;
-    while (C < kLpMaxCluster && (long long)M * C * 2 <= 2 * sms && V / (C * 2) >= 2 * kLpThreads * (bf16 ? 8 : 4)) C *= 2;
-    auto kernel = bf16 ? token_logprobs_kernel<true> : token_logprobs_kernel<false>;
+    while (!small && C < kLpMaxCluster && (long long)M * C * 2 <= 2 * sms && V / (C * 2) >= 2 * kLpThreads * (bf16 ? 8 : 4)) C *= 2;
+    auto kernel = small ? (bf16 ? token_logprobs_kernel<true, kLpSmall> : token_logprobs_kernel<false, kLpSmall>)
+                        : (bf16 ? token_logprobs_kernel<true, kLpThreads> : token_logprobs_kernel<false, kLpThreads>);
     if (C > 8) {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(M * C));
-    cfg.blockDim = dim3(kLpThreads);
+    cfg.blockDim = dim3(small ? kLpSmall : kLpThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -1,7 +1,7 @@
 """qv_token_logprobs against 64 bits. Tolerances: a logit's difference from the
 maximum is exact to half an ulp of binary32 and its exponential within
 2^-22 + 2^-24 |z|, |z| <= 150 only where the term is nothing; per-thread sums of
-n terms add n 2^-24 at most, n <= V / 512 + 32; S and T are combined over at most
+n terms add n 2^-24 at most, n <= V / 512 + 32 (V / 128 + 32 for many short rows); S and T are combined over at most
 13 + 16 steps. So ln S is within (n + 40) 2^-23, a log probability within that and
 2^-22 of its own and the logits' size, and the entropy within (n + 40) 2^-22 of
 1 + its size (T's terms are at most 0.54 each)."""
@@ -33,14 +33,14 @@ def call(qv, x, tok, K, entropy=True, stream=None):
     return lp, ent, tt, tl
 
 
-def check(x, tok, K, got):
+def check(x, tok, K, got, threads=512):
     lp, ent, tt, tl = got
     M, V = x.shape
     xf = x.float().cpu().numpy()
     wlp, went, wtt, wtl = ref.logprobs(xf, tok.cpu().numpy(), K)
     fin = xf[np.isfinite(xf)]
     size = float(np.abs(fin).max()) if fin.size else 0.0
-    n = V / 512 + 32
+    n = V / threads + 32
     tol = (n + 40) * 2.0 ** -23 + 2.0 ** -22 * size
 
     def near(a, w, t):
@@ -149,3 +149,40 @@ def test_refusals_leave_outputs_untouched(qv):
         qv.qv_token_logprobs(x[:, ::2], tok, lp)
     torch.cuda.synchronize()
     assert bool((lp == 7.0).all())
+
+
+@pytest.mark.parametrize("M,V,K,dtype", [
+    (305, 3245, 20, torch.bfloat16), (700, 1, 1, torch.float32), (400, 33, 32, torch.bfloat16),
+    (2000, 1000, 5, torch.float32), (611, 16384, 32, torch.bfloat16), (1300, 32003, 7, torch.float32),
+    (900, 127, 0, torch.float32), (3859, 517, 20, torch.bfloat16),
+])
+def test_many_short_rows(qv, M, V, K, dtype):
+    """A CTA of 128 threads a row: random rows, among them rows of equal logits, masked rows and ascending ones."""
+    g = torch.Generator().manual_seed(M + V)
+    x = torch.randn(M, V, generator=g) * 3
+    x[::7] = 1.5
+    x[1::7][torch.rand(x[1::7].shape, generator=g) < 0.9] = -float("inf")
+    x[2::7] = -float("inf")
+    x[3::7] = torch.linspace(-9, 9, V)
+    x = x.to(dtype).cuda()
+    tok = torch.randint(-1, V + 1, (M,), generator=g, dtype=torch.int32).cuda()
+    got = call(qv, x, tok, K)
+    check(x, tok, K, got, threads=128)
+    assert all(a is None or torch.equal(a, b) for a, b in zip(got, call(qv, x, tok, K)))
+
+
+def test_not_a_number_among_many_short_rows(qv):
+    M, V = 400, 777
+    g = torch.Generator().manual_seed(1)
+    x = torch.randn(M, V, generator=g)
+    clean = x.clone()
+    x[1::9, V // 2], x[2::9, 5] = float("nan"), float("inf")
+    bad = torch.zeros(M, dtype=torch.bool)
+    bad[1::9] = bad[2::9] = True
+    tok = torch.zeros(M, dtype=torch.int32, device="cuda")
+    got = call(qv, x.cuda(), tok, 5)
+    lp, ent, tt, tl = (t[bad.cuda()] for t in got)
+    assert bool(lp.isnan().all()) and bool(ent.isnan().all()) and bool(tl.isnan().all())
+    assert int(tt.min()) >= -1 and int(tt.max()) < V
+    keep = ~bad
+    check(clean[keep].cuda(), tok[keep.cuda()], 5, [t[keep.cuda()] for t in got], threads=128)
