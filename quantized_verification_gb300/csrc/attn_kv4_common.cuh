@@ -21,6 +21,9 @@ constexpr int kRowTile = 32;                    // query rows of a tile
 constexpr int kMinUnits = 16;                   // places of a CTA's range at least: two units a warp
 constexpr int kAttnMaxT = QV_MAX_M;             // tokens of a step
 constexpr size_t kCounterBytes = 4096;         // at the workspace's start, whatever the shape
+constexpr int kJoinSlots = (int)(kCounterBytes / 12);   // three arrays of counters; also the most CTAs
+constexpr unsigned kJoinAll = 32;               // parts of a tile that are joined at once (Join)
+constexpr unsigned kJoinFan = 16;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kTileCost = 20;                   // units' worth of a tile's own costs
 constexpr int kMaxCluster = 8;                  // CTAs of a cluster that share a tile
@@ -63,7 +66,7 @@ struct Args {
     int C;                     // CTAs of the cluster that takes a tile, or 0: the line of units
     float scale;
     void* out;                 // [B*T][Hq D] fp32 or bf16
-    unsigned* counters;        // [grid] arrivals at the tile that begins in CTA i's range (zero between calls)
+    unsigned* counters;        // arrivals (Join), zero between calls
     float* partials;           // [grid][2][slot]
     int hold;                  // test hook: request no record
     unsigned long long wait_ns;
@@ -204,6 +207,48 @@ __device__ __forceinline__ uint32_t lds_u32(uint32_t addr) {
     asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(addr));
     return v;
 }
+
+// How the parts of a tile, those of CTAs c0 .. c0 + n - 1, are joined: by the
+// last CTA to arrive, or, above kJoinAll, in groups of about kJoinFan by the
+// last of each group, which leaves the sum in its first part's place, and the
+// groups by the last of those. Groups follow from n alone: the same sums from
+// call to call. GB300, one sequence of 131071 positions, 1 key/value head, 5
+// tokens of 4 heads: 304 parts in one go 149 us, in groups 37 us;
+// one token 36 and 18 us. Up to 32 parts one join is as fast as two.
+// In shared memory, kept by one thread: registers are dear.
+struct Join {
+    unsigned c0, groups, size;
+    unsigned first, count, step;                // the present join's parts: first, first + step, ..
+    unsigned last;                              // this CTA is the last of them to arrive
+    __device__ __forceinline__ void begin(unsigned c0_, unsigned c1) {
+        const unsigned n = c1 - c0_ + 1;
+        c0 = c0_;
+        groups = n <= kJoinAll ? 1 : (n + kJoinFan - 1) / kJoinFan;
+        size = (n + groups - 1) / groups;
+        groups = (n + size - 1) / size;
+        const unsigned g = (blockIdx.x - c0) / size;
+        first = c0 + g * size;
+        count = min(size, n - g * size);
+        step = 1;
+    }
+    // This CTA's part is written. A tile's first group may begin where another
+    // tile's later group does, hence three arrays of counters.
+    __device__ __forceinline__ void arrive(unsigned* counters) {
+        unsigned* counter = counters + (step != 1 ? 2 * kJoinSlots + c0 : (first == c0 ? c0 : kJoinSlots + first));
+        __threadfence();
+        last = atomicAdd(counter, 1u) == count - 1;
+        if (last) {
+            *counter = 0;
+            __threadfence();
+        }
+    }
+    __device__ __forceinline__ bool final() const { return groups == 1 || step != 1; }
+    __device__ __forceinline__ void next() {
+        first = c0;
+        count = groups;
+        step = size;
+    }
+};
 
 // The cached positions of sequence b.
 __device__ __forceinline__ int seq_len(const Args& a, int b) {

@@ -18,8 +18,8 @@
 //     A tile that lies in one range is written by its CTA; one that is cut
 //     leaves partial results (running maximum, running sum, weighted values) in
 //     the workspace, and the last of its CTAs to arrive adds them in range
-//     order. Nobody waits for anybody, and the order of arrival changes
-//     nothing. Every tile takes kTileCost places more than its units (its start
+//     order (many of them in groups first, Join). Nobody waits for anybody, and
+//     the order of arrival changes nothing. Every tile takes kTileCost places more than its units (its start
 //     and its end; GB300, 24 sequences of 33 to 16001 positions, 5 tokens, 32/8
 //     heads of 64, bf16 out: 41 us with 10, 37 with 20, 39 with 34).
 //
@@ -127,7 +127,8 @@ __global__ void __launch_bounds__(Layout<D, NR>::Threads, Layout<D, NR>::Ctas) a
     float* s_wl = s_wm + kWarps * RW;
     unsigned* s_scan = reinterpret_cast<unsigned*>(smem + Ly::Scan);
     volatile int* abort = reinterpret_cast<volatile int*>(smem + Ly::Misc);
-    int* s_flag = reinterpret_cast<int*>(smem + Ly::Misc) + 1;       // [0] bad value row, [1] last arrival
+    int* s_flag = reinterpret_cast<int*>(smem + Ly::Misc) + 1;       // an own value row is not finite
+    Join* s_join = reinterpret_cast<Join*>(smem + Ly::Misc + 16);
     const float NEG_INF = -__uint_as_float(0x7F800000u);
     const uint32_t ring = sbase + (uint32_t)(Ly::Ring + warp * S * Rec::Bytes);
 
@@ -760,19 +761,15 @@ __global__ void __launch_bounds__(Layout<D, NR>::Threads, Layout<D, NR>::Ctas) a
                 }
             }
             const unsigned c0 = tile_at / per, c1 = (tile_at + (unsigned)nu - 1) / per;   // the tile's CTAs
-            __syncthreads();                                     // (the parts are written before thread 0's fence)
-            if (tid == 0) {
-                __threadfence();
-                const unsigned before_me = atomicAdd(a.counters + c0, 1u);
-                s_flag[1] = before_me == c1 - c0;
-                if (s_flag[1]) {
-                    a.counters[c0] = 0;
-                    __threadfence();
-                }
-            }
-            __syncthreads();
-            if (s_flag[1]) {
-                // The tile's parts, added in range order at the rows' maxima, kParts
+            if (tid == 0) s_join->begin(c0, c1);
+            // (called twice below: as a loop it cost the main loop registers, 74 us
+            // against 72 for one token over 131071 and 120000 positions)
+            auto join_once = [&]() {                             // true: nothing left to do
+                __syncthreads();                                 // (the parts are written before thread 0's fence)
+                if (tid == 0) s_join->arrive(a.counters);
+                __syncthreads();
+                if (!s_join->last) return true;
+                // The parts, added in range order at the rows' maxima, kParts
                 // of them at a time: first their weights (in the ring), then their
                 // items, kAhead parts' loads in flight.
                 constexpr int kParts = 64;
@@ -784,8 +781,11 @@ __global__ void __launch_bounds__(Layout<D, NR>::Threads, Layout<D, NR>::Ctas) a
                 float* w_M = w_l + kParts * RW;                  // [RW] so far: maximum, sum, the last rescaling
                 float* w_L = w_M + RW;
                 float* w_r = w_L + RW;
-                const unsigned n = c1 - c0 + 1;
-                auto part = [&](unsigned ci) { return a.partials + ((size_t)ci * 2 + (ci == c0 ? 1 : 0)) * Ly::Slot; };
+                const unsigned n = s_join->count, first = s_join->first, step = s_join->step, begin = s_join->c0;
+                auto part = [&](unsigned i) {
+                    const unsigned ci = first + i * step;
+                    return a.partials + ((size_t)ci * 2 + (ci == begin ? 1 : 0)) * Ly::Slot;
+                };
                 float v[Own][4];
 #pragma unroll
                 for (int k = 0; k < Own; ++k)
@@ -799,7 +799,7 @@ __global__ void __launch_bounds__(Layout<D, NR>::Threads, Layout<D, NR>::Ctas) a
                 for (unsigned n0 = 0; n0 < n; n0 += kParts) {
                     const unsigned nn = min(n - n0, (unsigned)kParts);
                     for (unsigned e = tid; e < nn * RW; e += kThreads) {
-                        const float* pp = part(c0 + n0 + e / RW) + RW * D + e % RW;
+                        const float* pp = part(n0 + e / RW) + RW * D + e % RW;
                         w_f[e] = __ldcg(pp);
                         w_l[e] = __ldcg(pp + RW);
                     }
@@ -833,7 +833,7 @@ __global__ void __launch_bounds__(Layout<D, NR>::Threads, Layout<D, NR>::Ctas) a
                         float4 x[kAhead][Own];
 #pragma unroll
                         for (int i = 0; i < kAhead; ++i) {
-                            const float* pp = part(c0 + n0 + min(i0 + i, nn - 1));
+                            const float* pp = part(n0 + min(i0 + i, nn - 1));
 #pragma unroll
                             for (int k = 0; k < Own; ++k)
                                 x[i][k] = __ldcg(reinterpret_cast<const float4*>(pp) + min(tid + k * kThreads, Ly::Items - 1));
@@ -851,16 +851,28 @@ __global__ void __launch_bounds__(Layout<D, NR>::Threads, Layout<D, NR>::Ctas) a
                     }
                     __syncthreads();
                 }
+                const bool final = s_join->final();
+                float* sum = part(0);
 #pragma unroll
                 for (int k = 0; k < Own; ++k) {
                     const int it = tid + k * kThreads;
                     if (it < Ly::Items) {
                         int r, d0;
                         item_at(it, r, d0);
-                        store(r, d0, v[k], w_L[r]);
+                        if (final) store(r, d0, v[k], w_L[r]);
+                        else *reinterpret_cast<float4*>(sum + it * 4) = make_float4(v[k][0], v[k][1], v[k][2], v[k][3]);
                     }
                 }
-            }
+                if (final) return true;
+                if (tid < RW) {
+                    sum[RW * D + tid] = w_M[tid];
+                    sum[RW * D + RW + tid] = w_L[tid];
+                }
+                __syncthreads();                                 // (everyone has read the join's state)
+                if (tid == 0) s_join->next();
+                return false;
+            };
+            if (!join_once()) join_once();
         }
         fence_proxy_async_smem();                                // before the ring's next copies
         __syncthreads();                                         // the ring, Q and the flags are free again
@@ -945,7 +957,7 @@ Plan plan(int B, int T, int Hq, int Hkv, int D, int NB, int sms, bool out_bf16) 
     p.min_units = p.tc ? kTcMinUnits : kMinUnits;
     const long long most = tiles * (units + p.cost);           // places at most
     long long ctas = p.tc ? 2LL * sms : slots;
-    ctas = ctas < (long long)(kCounterBytes / 4) ? ctas : (long long)(kCounterBytes / 4);
+    ctas = ctas < kJoinSlots ? ctas : kJoinSlots;
     const long long want = (most + p.min_units - 1) / p.min_units;
     p.grid = p.C > 0 ? (int)(tiles * p.C) : (int)(want < ctas ? want : ctas);
     p.total = kCounterBytes + (p.C > 0 ? 0 : (size_t)p.grid * 2 * (p.NR * 8 * D + 2 * p.NR * 8) * 4);

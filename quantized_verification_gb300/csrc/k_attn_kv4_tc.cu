@@ -75,7 +75,7 @@ struct TcLayout {
     static constexpr int Red = Row + 9 * 32 * 4;          // [4][32]
     static constexpr int Scan = Red + 4 * 32 * 4;
     static constexpr int Misc = Scan + 16 * 4;
-    static constexpr int Bytes = Misc + 32;
+    static constexpr int Bytes = Misc + 64;
     static constexpr int Alloc = Bytes + 1024;            // slack to align the base to 1024 B
     static constexpr int Slot = RW * D + 2 * RW;          // floats of a partial result: [row][lane], m, l
     static constexpr int kK = 0, kS = 64, kO = 128, kOwn = 192, kSum = 224;   // tensor memory columns (S twice 32)
@@ -182,7 +182,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
     unsigned* s_scan = reinterpret_cast<unsigned*>(smem + Ly::Scan);
     volatile int* abort = reinterpret_cast<volatile int*>(smem + Ly::Misc);
     uint32_t* s_tmem = reinterpret_cast<uint32_t*>(smem + Ly::Misc) + 1;
-    int* s_flag = reinterpret_cast<int*>(smem + Ly::Misc) + 2;
+    Join* s_join = reinterpret_cast<Join*>(smem + Ly::Misc + 32);
     volatile unsigned* s_grow = reinterpret_cast<volatile unsigned*>(smem + Ly::Misc) + 4;   // [2] the step whose maxima move, + 1
     float* s_own = reinterpret_cast<float*>(smem + Ly::V);       // [T][kTcOwnStride] own scores, before the first values
     const float NEG_INF = -__uint_as_float(0x7F800000u);
@@ -714,23 +714,21 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
                 slot[RW * D + RW + tid] = s_L[tid];
             }
             const unsigned c0 = tile_at / per, c1 = (tile_at + (unsigned)nc) / per;   // the tile's CTAs
-            __syncthreads();                                     // (the part is written before thread 0's fence)
-            if (tid == 0) {
-                __threadfence();
-                const unsigned before_me = atomicAdd(a.counters + c0, 1u);
-                *s_flag = before_me == c1 - c0;
-                if (*s_flag) {
-                    a.counters[c0] = 0;
-                    __threadfence();
-                }
-            }
-            __syncthreads();
-            if (*s_flag) {
-                // The tile's parts, added in range order at the rows' common maxima:
+            if (tid == 0) s_join->begin(c0, c1);
+#pragma unroll 1
+            while (true) {
+                __syncthreads();                                 // (the part is written before thread 0's fence)
+                if (tid == 0) s_join->arrive(a.counters);
+                __syncthreads();
+                if (!s_join->last) break;
+                // The parts, added in range order at the rows' common maxima:
                 // the weights first (in the value buffer, [part][32]), then four
                 // parts' rows at a time.
-                auto part = [&](unsigned ci) { return a.partials + ((size_t)ci * 2 + (ci == c0 ? 1 : 0)) * Ly::Slot; };
-                const unsigned n = c1 - c0 + 1;
+                const unsigned n = s_join->count, first = s_join->first, step = s_join->step, begin = s_join->c0;
+                auto part = [&](unsigned i) {
+                    const unsigned ci = first + i * step;
+                    return a.partials + ((size_t)ci * 2 + (ci == begin ? 1 : 0)) * Ly::Slot;
+                };
                 float* s_f2 = reinterpret_cast<float*>(smem + Ly::V);
                 float* s_l3 = s_f2 + kTcMaxParts * 32;
                 float run[NT][8];                                // this dim's sums so far, at the maxima s_M
@@ -746,7 +744,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
                 for (unsigned n0 = 0; n0 < n; n0 += kTcMaxParts) {
                     const unsigned nn = min(n - n0, (unsigned)kTcMaxParts);
                     for (unsigned e = tid; e < nn * 32; e += kTcThreads) {
-                        const float* pp = part(c0 + n0 + (e >> 5));
+                        const float* pp = part(n0 + (e >> 5));
                         const int r = min((int)(e & 31), RW - 1);
                         s_f2[e] = __ldcg(pp + RW * D + r);
                         s_l3[e] = __ldcg(pp + RW * D + RW + r);
@@ -780,7 +778,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
                                 float x[4][8];
 #pragma unroll
                                 for (int k = 0; k < 4; ++k) {
-                                    const float* pp = part(c0 + n0 + min(i0 + k, nn - 1)) + 8 * (hf + 2 * t) * D + key;
+                                    const float* pp = part(n0 + min(i0 + k, nn - 1)) + 8 * (hf + 2 * t) * D + key;
 #pragma unroll
                                     for (int i = 0; i < 8; ++i) x[k][i] = __ldcg(pp + i * D);
                                 }
@@ -795,7 +793,24 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
                         }
                     __syncthreads();
                 }
-                store(run, s_w1);
+                if (s_join->final()) {
+                    store(run, s_w1);
+                    break;
+                }
+                float* sum = part(0);
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = 8 * (hf + 2 * t) + i;
+                        if (worker && r < RW) sum[r * D + key] = run[t][i];
+                    }
+                if (tid < RW) {
+                    sum[RW * D + tid] = s_M[tid];
+                    sum[RW * D + RW + tid] = s_L[tid];
+                }
+                __syncthreads();                                 // (everyone has read the join's state)
+                if (tid == 0) s_join->next();
             }
         }
         tc_fence_before();                                       // O has been read

@@ -624,3 +624,14 @@ def test_keys_of_no_weight_at_all(qv, NB, D, T, Hq):
         out = torch.empty(T, Hq * D, dtype=dt, device="cuda")
         qv.qv_attention_verify_kv4(qkv.cuda(), cu(cache), cu(ln), T, Hq, 1, scale, out, ws, block_table=cu(table))
         close(out, want, vmax, smax, D)
+
+
+@pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("B,T,Hq,Hkv,D,NB,lens", [
+    (1, 1, 4, 1, 128, 2000, [63990]), (1, 5, 4, 1, 128, 2000, [63990]), (1, 8, 4, 1, 128, 1400, [44800]),
+    (1, 6, 4, 1, 64, 2000, [64000]), (2, 1, 8, 1, 64, 1500, [48000, 33]), (3, 5, 4, 1, 128, 1500, [47000, 200, 48000]),
+    (2, 2, 8, 2, 128, 1100, [1, 35200]),
+])
+def test_attention_over_hundreds_of_parts(qv, B, T, Hq, Hkv, D, NB, lens, out_dtype):
+    """Few heads over long contexts: so many thread blocks share a tile that their results are joined in groups."""
+    test_attention(qv, B, T, Hq, Hkv, D, NB, lens, True, out_dtype)
