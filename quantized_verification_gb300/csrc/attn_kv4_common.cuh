@@ -29,6 +29,7 @@ constexpr int kTileCost = 20;                   // units' worth of a tile's own 
 constexpr int kMaxCluster = 8;                  // CTAs of a cluster that share a tile
 constexpr int kClusterUnits = 6;                // a larger cluster while its CTAs have more units than this
 constexpr int kClusterMost = 48;                // no clusters above so many units a CTA
+constexpr int kAloneMost = 40;                  // units of a tile that has a CTA to itself, though not all fit at once
 constexpr int kTcMinUnits = 8;                  // the same for the tcgen05 kernel: two steps of 128 positions,
 constexpr int kTcTileCost = 18;                 // and a tile's costs
 constexpr float kLazy = 8.f;                    // log2 of the growth a running maximum may lag behind

@@ -950,7 +950,13 @@ Plan plan(int B, int T, int Hq, int Hkv, int D, int NB, int sms, bool out_bf16) 
         cut(kRowTile);
         p.C = 1;
         while (p.C < kMaxCluster && tiles * p.C * 2 <= slots && units > (long long)kClusterUnits * p.C) p.C *= 2;
-        if (tiles * p.C > slots || units > (long long)kClusterMost * p.C) p.C = 0;
+        // More tiles than CTAs fit at once: still a CTA each, one after the other,
+        // where contexts are short and two CTAs share an SM. GB300, one line / a
+        // CTA each: 64 sequences of 100 to 300 positions, 8 key/value heads, 1 token
+        // of 4 heads 16.7/13.6 us, 5 tokens with heads of 64 21.3/18.2; up to 1200
+        // positions 28.1/25.3. With one CTA an SM (5 tokens, heads of 128) 32/39.
+        const bool alone = p.C == 1 && slots == 2 * sms && units <= kAloneMost;
+        if ((tiles * p.C > slots && !alone) || units > (long long)kClusterMost * p.C) p.C = 0;
     }
     p.tc = p.C == 0 && D == 128 && p.NR >= tc_rows(out_bf16);
     p.cost = p.tc ? kTcTileCost : kTileCost;

@@ -385,13 +385,15 @@ LINES = [  # B, T, Hq, Hkv, D, NB, lens, paged
     (31, 20, 40, 20, 128, 2, None, False),                     # 40 rows a head group
     (700, 1, 4, 1, 128, 2, None, True),
     (200, 7, 6, 2, 64, 3, None, True),                         # 21 rows
+    (80, 1, 8, 4, 64, 42, None, True),
 ]
 
 
 @pytest.mark.parametrize("out_dtype", [torch.float32, torch.bfloat16])
 @pytest.mark.parametrize("B,T,Hq,Hkv,D,NB,lens,paged", LINES)
 def test_attention_on_one_line(qv, B, T, Hq, Hkv, D, NB, lens, paged, out_dtype):
-    assert qv.qv_attention_kv4_workspace_bytes(B, T, Hq, Hkv, D, NB) > 4096      # parts of tiles have room there
+    if NB > 40 or (D == 128 and T * Hq // Hkv > 16):           # (else the many tiles have a thread block each)
+        assert qv.qv_attention_kv4_workspace_bytes(B, T, Hq, Hkv, D, NB) > 4096  # parts of tiles have room there
     test_attention(qv, B, T, Hq, Hkv, D, NB, lens, paged, out_dtype)
 
 
