@@ -24,8 +24,9 @@
 //     heads of 64, bf16 out: 41 us with 10, 37 with 20, 39 with 34).
 //
 // Inside a CTA each of the W warps (8 or 12) takes every W-th unit of the range
-// and keeps its own online softmax; the step's own rows are warp 0's, which
-// gets one unit less (10 % on the same batch). A record comes in
+// and keeps its own online softmax; the step's first 32 own rows are warp 0's,
+// which gets one unit less (10 % on the same batch), and a longer step's next
+// ones those of warps 1, 2, .. A record comes in
 // one bulk copy into the warp's own ring. Both products run on the tensor cores
 // (mma.sync m16n8k16, fp32 accumulation) with the keys, or the value dims, on
 // the M side and the query rows on the N side in tiles of 8: few rows do not
@@ -105,7 +106,8 @@ struct Layout {
     static constexpr int Valid = Bar + Warps * Stages * 8;
     static constexpr int Scan = Valid + Warps * Stages * 4;    // unsigned [Warps], then [14], [15]: the first sequence's place and number
     static constexpr int Misc = Scan + 16 * 4;
-    static constexpr int Bytes = Misc + 64;
+    static constexpr int Tok = Misc + 64;                 // int [RW]: the step's last row that a query row sees
+    static constexpr int Bytes = Tok + RW * 4;
     static constexpr int Items = RW * D / 4;              // groups of 4 dims of one row
     static constexpr int Slot = RW * D + 2 * RW;          // floats of a partial result: items, m, l
     static_assert(AreaBytes <= RingBytes, "the warps' outputs fit the ring");
@@ -129,6 +131,7 @@ __global__ void __launch_bounds__(Layout<D, NR>::Threads, Layout<D, NR>::Ctas) a
     volatile int* abort = reinterpret_cast<volatile int*>(smem + Ly::Misc);
     int* s_flag = reinterpret_cast<int*>(smem + Ly::Misc) + 1;       // an own value row is not finite
     Join* s_join = reinterpret_cast<Join*>(smem + Ly::Misc + 16);
+    int* s_tok = reinterpret_cast<int*>(smem + Ly::Tok);
     const float NEG_INF = -__uint_as_float(0x7F800000u);
     const uint32_t ring = sbase + (uint32_t)(Ly::Ring + warp * S * Rec::Bytes);
 
@@ -202,8 +205,8 @@ __global__ void __launch_bounds__(Layout<D, NR>::Threads, Layout<D, NR>::Ctas) a
             }
         }
 
-        // The cached units go round the warps; the step's own rows, which take
-        // about as long as one, are warp 0's, which sits out the first round.
+        // The cached units go round the warps; the step's first 32 own rows, which
+        // take about as long as one, are warp 0's, which sits out the first round.
         const int last = min(ub, nc);
         const bool own = ub > nc;
         auto unit_of = [&](int round) {
@@ -252,8 +255,6 @@ __global__ void __launch_bounds__(Layout<D, NR>::Threads, Layout<D, NR>::Ctas) a
                 dst[32] = make_uint2(__byte_perm(q.y, q.w, 0x5410), __byte_perm(q.y, q.w, 0x7632));
             }
         }
-        // the step's last row that a query row sees (in warp 0's part of s_wm, until that is written)
-        int* s_tok = reinterpret_cast<int*>(s_wm);
         if (tid < RW) s_tok[tid] = tid < R ? (r0 + tid) / a.G : -1;
         __syncthreads();
         uint2 qf[Ly::QRegs ? NR : 1][Ly::QRegs ? KS : 1];
