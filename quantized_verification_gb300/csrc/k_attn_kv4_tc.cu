@@ -260,6 +260,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
             const bool there = lane < 4 && unit < last && (unsigned)page < (unsigned)a.pages;
             if (lane < 4) cnt[4 * s + lane] = there ? min(kKv4Block, L - unit * kKv4Block) : 0;
             const unsigned who = __ballot_sync(0xffffffffu, there);
+            __syncwarp();                                        // the counts, before lane 0 arrives (a ballot orders no memory)
             if (lane == 0 && !a.hold) {
                 if (who) mbar_arrive_expect_tx(&full[s], (unsigned)__popc(who) * Rec::Bytes);
                 else mbar_arrive(&full[s]);
