@@ -70,7 +70,7 @@ struct TcLayout {
     static constexpr int Q = P + kTcKeys * 128;           // [2 halves][NS rows][128 B]
     static constexpr int Ring = Q + 2 * 32 * 128;
     static constexpr int Bar = Ring + kTcStages * 4 * Rec::Bytes;   // full [stages], then the kBar ones
-    static constexpr int Cnt = Bar + (kTcStages + 7) * 8; // cached positions per record [stages][4]
+    static constexpr int Cnt = Bar + (kTcStages + 9) * 8; // cached positions per record [stages][4]
     static constexpr int Row = Cnt + kTcStages * 16;      // floats per row: c, limit, f, own m, own l, w1, w2, M, l
     static constexpr int Red = Row + 9 * 32 * 4;          // [4][32]
     static constexpr int Scan = Red + 4 * 32 * 4;
@@ -168,6 +168,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
     uint64_t* bar_g = bar_s + 3;                                 // every warp has compared a step's products (8 warps)
     uint64_t* bar_p = bar_s + 4;                                 // the values and probabilities are in place (8 warps)
     uint64_t* bar_end = bar_s + 5;
+    uint64_t* bar_r = bar_s + 6;                                 // the products' maxima are in place (8 warps)
+    uint64_t* bar_m = bar_s + 7;                                 // the rows' maxima have moved (8 warps)
     volatile int* cnt = reinterpret_cast<volatile int*>(smem + Ly::Cnt);
     float* s_c = reinterpret_cast<float*>(smem + Ly::Row);       // p = 2^(sl2 x + c) of the product x (RowMax)
     float* s_lim = s_c + 32;                                     // the product at which m moves
@@ -199,6 +201,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
         mbar_init(bar_g, kTcWorkers / 32);
         mbar_init(bar_p, kTcWorkers / 32);
         mbar_init(bar_end, 1);
+        mbar_init(bar_r, kTcWorkers / 32);
+        mbar_init(bar_m, kTcWorkers / 32);
         *abort = 0;
         s_grow[0] = s_grow[1] = 0;
         fence_barrier_init();
@@ -220,6 +224,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
     uint32_t c4 = 4u, c8 = 8u, c64 = 64u;                        // multipliers the compiler may not turn into shifts
     asm volatile("" : "+r"(c4), "+r"(c8), "+r"(c64));
     unsigned steps_issued = 0, steps = 0;                        // 128-position steps requested / begun so far
+    unsigned moves = 0;                                          // steps in which some row's maximum moved
     Range rg;
     bool work = find_range<kTcThreads>(a, own_units, tile_cost, min_units, s_scan, rg);
     const unsigned per = rg.per, u1 = work ? rg.u1 : 0;
@@ -254,7 +259,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
         int page = !worker && lane < 4 ? page_of(unit) : -1;
         int to_issue = nsteps;
         auto issue = [&]() {
-            if (to_issue == 0 || *abort) return;
+            if (to_issue == 0 || __any_sync(0xffffffffu, *abort)) return;
             --to_issue;
             const int s = steps_issued % kTcStages;
             const bool there = lane < 4 && unit < last && (unsigned)page < (unsigned)a.pages;
@@ -405,11 +410,14 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
         __syncthreads();
 
         // ---- 128 positions at a time. `steps` counts them over all tiles: the
-        // parity of every barrier follows from it
+        // parity of every barrier follows from it. Between here and the barrier
+        // behind the steps every wait has a limit, and warps whose waits ran out
+        // may be at different places: they decide as whole warps (votes), and no
+        // barrier without a limit stands on a way that some of them may not take.
         if (!worker) {
             auto s_product = [&](int t0) {                       // S of step t0 of the tile
-                wait_for(bar_k, (steps + t0) & 1u, abort, kWaitLimitNs, kErrTcWait);
-                if (elect_one()) {
+                const bool ok = wait_for(bar_k, (steps + t0) & 1u, abort, kWaitLimitNs, kErrTcWait);
+                if (__all_sync(0xffffffffu, ok) && elect_one()) {
                     tc_fence_after();
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
@@ -424,8 +432,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
 #pragma unroll 1
             for (int t0 = 0; t0 < nsteps; ++t0) {
                 if (t0 + 1 < nsteps) s_product(t0 + 1);
-                wait_for(bar_p, (steps + t0) & 1u, abort, kWaitLimitNs, kErrTcWait);
-                if (elect_one()) {
+                const bool ok = wait_for(bar_p, (steps + t0) & 1u, abort, kWaitLimitNs, kErrTcWait);
+                if (__all_sync(0xffffffffu, ok) && elect_one()) {
                     tc_fence_after();
 #pragma unroll
                     for (int ks = 0; ks < 8; ++ks)
@@ -520,7 +528,7 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
                     }
                 }
                 wait_for(bar_g, st & 1u, abort, kWaitLimitNs, kErrTcWait);
-                if (s_grow[st & 1u] == st + 1) {                 // rare: some row's maximum moves
+                if (__any_sync(0xffffffffu, s_grow[st & 1u] == st + 1)) {   // rare: some row's maximum moves
                     tc_fence_after();
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
@@ -533,7 +541,8 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
                                 if (lane == 0) s_red[q4 * 32 + 8 * (hf + 2 * t) + i] = v;
                             }
                         }
-                    named_bar_sync(1, kTcWorkers);
+                    warp_arrive(bar_r);
+                    wait_for(bar_r, moves & 1u, abort, kWaitLimitNs, kErrTcWait);
                     if (tid < RW) {
                         const float v = fmaxf(fmaxf(s_red[tid], s_red[32 + tid]), fmaxf(s_red[64 + tid], s_red[96 + tid]));
                         float f = 1.f;
@@ -545,7 +554,9 @@ __global__ void __launch_bounds__(kTcThreads, 2) attn_kv4_tc_kernel(const Args a
                         }
                         s_f[tid] = f;
                     }
-                    named_bar_sync(1, kTcWorkers);
+                    warp_arrive(bar_m);
+                    wait_for(bar_m, moves & 1u, abort, kWaitLimitNs, kErrTcWait);
+                    ++moves;
 #pragma unroll
                     for (int t = 0; t < NT; ++t)
                         if (hf + 2 * t < NR) {
