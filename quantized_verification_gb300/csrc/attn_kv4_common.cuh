@@ -49,7 +49,9 @@ struct RowMax {
         const float m = fmaxf(rintf(v * sl2), -134217728.f);
         if (fabsf(m) < 1048576.f) {
             c = kBias - m;
-            limit = __fdividef(m + kLazy, sl2);              // (2 ulp: p < 2^15.5 all the same)
+            // (2 ulp: p < 2^15.5 all the same; by quarters, since __fdividef is 0 for
+            // divisors above 2^126, and sl2 may be up to 2^127.8)
+            limit = __fdividef(0.25f * (m + kLazy), 0.25f * sl2);
         } else {
             c = m < 134217728.f ? -m : __uint_as_float(0x7FC00000u);
             limit = v;
