@@ -595,8 +595,11 @@ QV_API qv_status qv_attention_verify_kv4(const uint16_t* qkv, const uint8_t* cac
  * entropy is 0. A NaN or +inf makes the row's logprob (of a token in range),
  * entropy and top_logprobs NaN; its top_tokens are then unspecified (in [0, V),
  * or -1 where fewer than top_k logits are numbers).
- * Sums are binary32 per thread (relative error about 1e-7), combined in a fixed
- * order. One launch: a CTA per row, or a cluster of up to 16 CTAs (a
+ * Sums are binary32, combined in a fixed order; their error does not grow with
+ * V (above 2^19 logits a row they are compensated). A log probability is within
+ * (30 + ln V) 2^-22, about 1e-5, plus 2^-22 of its own and the logits' size;
+ * measured at most 2.3e-6 over rows of 3245 to 2^24 logits of any shape, 6e-8 in
+ * the 2-norm on random ones. One launch: a CTA per row, or a cluster of up to 16 CTAs (a
  * non-portable size) when there are few rows; no workspace.
  */
 #define QV_MAX_TOP_K 32

@@ -8,25 +8,26 @@
 // With m = max_v x_v, z_v = (x_v - m) log2 e, S = sum 2^z_v, T = sum z_v 2^z_v:
 //   log p_v = (x_v - m) - ln S,   H = ln S - ln 2 * T / S.
 // One pass over the row: each thread keeps its own running m, S and T and
-// rescales them when its m grows by d: S *= 2^-d, T = 2^-d (T - d S). The
-// alternatives cost the pass nothing more: m is also the thread's largest
-// logit. Of the two largest maxima of each of the 16 warps the K-th largest,
-// tau, is a lower bound of the K-th largest logit, and few more than K threads
-// reach it. Only those threads' entries (1/512 of the slice each) are read
-// again, from L2, and the entries at or above tau are ordered by counting, for
-// each, those before it (by value, then by the lower index). Where ties or
-// masks leave too many of them, warps keep sorted lists of 32 instead.
+// rescales the sums when m has grown by d (Run): S *= 2^-d, T = 2^-d (T - d S).
+// The alternatives cost the pass nothing more: m is also the thread's largest
+// logit. Of 32 of these maxima (the two largest of each of 16 warps; with 4 warps
+// the largest of every 4 lanes) the K-th largest, tau, is a lower bound of the
+// K-th largest logit, and few more than K threads reach it. Only those threads'
+// entries (1/512 or 1/128 of the slice each) are read again, from L2, and the
+// entries at or above tau are ordered by counting, for each, those before it (by
+// value, then by the lower index). Where ties or masks leave too many of them,
+// warps keep sorted lists of 32 instead.
 //
-// A row is the work of one CTA (of 512 threads, or 128 for many short rows,
-// whose 32 maxima are then those of every 4 lanes), or of a cluster of C that split it
-// (launch_token_logprobs): each sends its statistics, its entries at or above
-// its own tau and its largest maxima to the first, which takes a tau of the
-// whole row from the latter before it counts. One cluster barrier in all.
+// A row is the work of one CTA (of 512 threads, or 128 for many short rows), or
+// of a cluster of C that split it (launch_token_logprobs): each sends its
+// statistics, its entries at or above its own tau and its largest maxima to the
+// first, which takes a tau of the whole row from the latter before it counts. One
+// cluster barrier in all.
 //
 // Bound by memory when there are many rows (GB300: 2000 rows of 151936 fp32
-// logits with their 5 most probable tokens 196 us, 6.2 TB/s; a plain copy runs
+// logits with their 5 most probable tokens 194 us, 6.3 TB/s; a plain copy runs
 // at 6.8) and by the chain of loads, reductions and barriers when there are few
-// (5 such rows with 20 tokens each 6.9 us).
+// (5 such rows with 20 tokens each 7.0 us).
 
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
@@ -93,28 +94,77 @@ __device__ __forceinline__ Stat combine(Stat a, Stat b) {
     return r;
 }
 
-template <int N>
-__device__ __forceinline__ void add_entries(Stat& st, const float (&v)[N]) {
-    float mx = v[0];
-#pragma unroll
-    for (int i = 1; i < N; ++i) mx = fmaxf(mx, v[i]);
-    if (mx > st.m) {
-        const float d = (st.m - mx) * kLog2e;                  // -inf on the first entries (S = T = 0)
+// A thread's running statistics: as Stat, but S and T relative to `ref`, which
+// lags up to kLpLag behind the maximum m. A ref that followed every new maximum
+// would rescale S up to once every group of entries of a rising row, 2^-22 off
+// each time. Where a maximum lies more than kLpLag above the rest, ref is the
+// maximum itself: S is 1 and a certain token's log probability 0, never above.
+//
+// Entries are added group by group (16 or 32 of them). A plain sum of n groups is
+// off by up to n 2^-24; Exact keeps what the additions lost (Kahan) for rows of
+// more than kLpPlain entries. With one running sum and no lag log probabilities
+// of 2^22 logits a row were off by up to 8e-5, now by 1e-6. GB300, us without /
+// with the second sums: 2000 rows of 151936 bf16 logits 129/131, of 60000 71/73,
+// fp32 194/196, 1 row of 32003 bf16 6.1/6.4.
+constexpr float kLpLag = 8.f;
+constexpr int kLpPlain = 1 << 19;               // 68 groups of a thread at most
+template <bool Exact>
+struct Run {
+    float m, ref, S, T, cS, cT;                                // (-inf and -inf before the first entry, then zeros)
+    // S and T relative to `to`, ref or more.
+    __device__ __forceinline__ void move(float to) {
+        const float d = (ref - to) * kLog2e;                   // -inf on the first entries (S = T = 0)
         const float f = ex2(d);
-        st.T = f == 0.f ? 0.f : f * (st.T + d * st.S);
-        st.S *= f;
-        st.m = mx;
+        T = f == 0.f ? 0.f : f * (T + d * S);
+        S *= f;
+        if (Exact) {
+            cT = f == 0.f ? 0.f : f * (cT + d * cS);
+            cS *= f;
+        }
+        ref = to;
     }
-    // nothing above -inf yet: subtract 0, so that -inf entries count 0
-    const float ref = st.m == -__uint_as_float(0x7F800000u) ? 0.f : st.m;
+    static __device__ __forceinline__ void add(float& sum, float& lost, float x) {
+        if (Exact) {
+            const float y = x - lost, t = sum + y;
+            lost = (t - sum) - y;
+            sum = t;
+        } else {
+            sum += x;
+        }
+    }
+    template <int N>
+    __device__ __forceinline__ void entries(const float (&v)[N]) {
+        float mx = v[0];
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const float z = max_nan((v[i] - ref) * kLog2e, -150.f);   // 2^-150 is 0 in binary32; keeps 0 * z finite
-        const float e = ex2(z);
-        st.S += e;
-        st.T += z * e;
+        for (int i = 1; i < N; ++i) mx = fmaxf(mx, v[i]);
+        m = fmaxf(m, mx);
+        if (mx > ref + kLpLag) move(mx);
+        // nothing above -inf yet: subtract 0, so that -inf entries count 0
+        const float r = ref < -3.4028235e38f ? 0.f : ref;
+        constexpr int P = N < 4 ? N : 4;                       // the group's own sums, in P parts
+        float s[P], t[P];
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const float z = max_nan((v[i] - r) * kLog2e, -150.f);   // 2^-150 is 0 in binary32; keeps 0 * z finite
+            const float e = ex2(z);
+            s[i % P] = i < P ? e : s[i % P] + e;
+            t[i % P] = i < P ? z * e : t[i % P] + z * e;
+        }
+#pragma unroll
+        for (int n = P / 2; n > 0; n >>= 1)
+#pragma unroll
+            for (int i = 0; i < n; ++i) {
+                s[i] += s[i + n];
+                t[i] += t[i + n];
+            }
+        add(S, cS, s[0]);
+        add(T, cT, t[0]);
     }
-}
+    __device__ __forceinline__ Stat stat() {                   // relative to m
+        if (m > ref) move(m);
+        return Exact ? Stat{m, S - cS, T - cT} : Stat{m, S, T};
+    }
+};
 
 // A key that orders entries by value, then by the lower index; 0 is below all.
 // -0 counts as +0. (A NaN's key is 1: below every number's.)
@@ -233,7 +283,7 @@ __device__ __forceinline__ void for_thread(const Row<BF16>& r, int t, bool first
     }
 }
 
-template <bool BF16, int Threads>
+template <bool BF16, int Threads, bool Exact>
 __global__ void __launch_bounds__(Threads, Threads == kLpThreads ? 2 : 10) token_logprobs_kernel(const LpArgs a) {
     constexpr int Warps = Threads / 32, Cand = lp_cand(Threads);
     constexpr bool Clusters = Threads == kLpThreads;           // CTAs of short rows have theirs to themselves
@@ -268,12 +318,12 @@ __global__ void __launch_bounds__(Threads, Threads == kLpThreads ? 2 : 10) token
     const float x_tok = in_range ? r.at(tok) : 0.f;
 
     // ---- the pass
-    Stat st = {NEG_INF, 0.f, 0.f};
+    Run<Exact> run = {NEG_INF, NEG_INF, 0.f, 0.f, 0.f, 0.f};
     const int own1 = rank == 0 ? r.single(tid) : -1;
     const float x_own = own1 >= 0 ? r.at(own1) : 0.f;
     if (own1 >= 0) {
         const float v[1] = {x_own};
-        add_entries(st, v);
+        run.entries(v);
     }
     int n = v0 + tid;
     for (; n + (kLpUnroll - 1) * Threads < v1; n += kLpUnroll * Threads) {
@@ -283,13 +333,14 @@ __global__ void __launch_bounds__(Threads, Threads == kLpThreads ? 2 : 10) token
         float v[kLpUnroll * E];
 #pragma unroll
         for (int i = 0; i < kLpUnroll; ++i) Row<BF16>::unpack(u[i], v + i * E);
-        add_entries(st, v);
+        run.entries(v);
     }
     for (; n < v1; n += Threads) {
         float v[E];
         Row<BF16>::unpack(r.vec(n), v);
-        add_entries(st, v);
+        run.entries(v);
     }
+    Stat st = run.stat();
     const float mine = st.m;
 
     // ---- each warp's statistics and two largest maxima, then the CTA's
@@ -332,8 +383,8 @@ __global__ void __launch_bounds__(Threads, Threads == kLpThreads ? 2 : 10) token
         }
         return c;
     };
-    // The place of p[i] among N numbers (N / 512 threads a number, all of which
-    // get it); ties by the index.
+    // The place of p[i] among N numbers (Threads / N threads a number, all of
+    // which get it); ties by the index.
     auto place_of = [&](const float* p, int N, int& i) {
         const int G = Threads / N;                          // threads a number
         i = tid / G;
@@ -466,8 +517,9 @@ cudaError_t launch_token_logprobs(const void* x, bool bf16, const int32_t* tok, 
     const bool small = V <= (1 << 15) && M > 2 * sms * (V >> 13 > 1 ? V >> 13 : 1);
     int C = 1;
     while (!small && C < kLpMaxCluster && (long long)M * C * 2 <= 2 * sms && V / (C * 2) >= 2 * kLpThreads * (bf16 ? 8 : 4)) C *= 2;
-    auto kernel = small ? (bf16 ? token_logprobs_kernel<true, kLpSmall> : token_logprobs_kernel<false, kLpSmall>)
-                        : (bf16 ? token_logprobs_kernel<true, kLpThreads> : token_logprobs_kernel<false, kLpThreads>);
+    auto kernel = small ? (bf16 ? token_logprobs_kernel<true, kLpSmall, false> : token_logprobs_kernel<false, kLpSmall, false>)
+                : V <= kLpPlain ? (bf16 ? token_logprobs_kernel<true, kLpThreads, false> : token_logprobs_kernel<false, kLpThreads, false>)
+                                : (bf16 ? token_logprobs_kernel<true, kLpThreads, true> : token_logprobs_kernel<false, kLpThreads, true>);
     if (C > 8) {
         cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
         if (e != cudaSuccess) return e;
