@@ -562,7 +562,9 @@ QV_API qv_status qv_kv4_read(const uint8_t* cache, const int32_t* start, const i
  *   (qv_device_error); the call's outputs are then undefined, the workspace
  *   stays usable.
  * fp32 outputs are within about 1e-6 (2-norm) of the binary64 definition over
- * the values the cache holds; for bf16 outputs the probabilities are rounded to
+ * the values the cache holds (measured 0.5 to 6e-7 up to 131071 positions). The
+ * sums are binary32: where all scores are equal their roundings may all go one
+ * way, 6e-6 for 131071 positions in one thread block's range. For bf16 outputs the probabilities are rounded to
  * 11 bits before the product with the values. Results are the same from call
  * to call on one GPU. A row whose largest score has a magnitude of 2^27 * ln 2
  * = 9.3e7 or more (scale included; binary32 no longer tells its scores apart)
