@@ -19,9 +19,10 @@
 //     leaves partial results (running maximum, running sum, weighted values) in
 //     the workspace, and the last of its CTAs to arrive adds them in range
 //     order (many of them in groups first, Join). Nobody waits for anybody, and
-//     the order of arrival changes nothing. Every tile takes kTileCost places more than its units (its start
-//     and its end; GB300, 24 sequences of 33 to 16001 positions, 5 tokens, 32/8
-//     heads of 64, bf16 out: 41 us with 10, 37 with 20, 39 with 34).
+//     the order of arrival changes nothing. Every tile takes kTileCost places more
+//     than its units (its start and its end; GB300, 24 sequences of 33 to 16001
+//     positions, 5 tokens, 32/8 heads of 64, bf16 out: 41 us with 10, 37 with 20,
+//     39 with 34).
 //
 // Inside a CTA each of the W warps (8 or 12) takes every W-th unit of the range
 // and keeps its own online softmax; the step's first 32 own rows are warp 0's,
@@ -52,7 +53,7 @@
 //     interleave (prmt), after which the nibble step, with the pattern of 16.0
 //     in f16, gives the A fragments of the dims a thread owns.
 // What bounds it (GB300). Long contexts: the ALUs, which unpack 256 codes a
-// position (55 % busy, with 61 % of the issue slots; DRAM 45 %): one token over
+// position (55 % busy, with 61 % of the issue slots; DRAM 47 %): one token over
 // 131071 and 120000 positions, 8 key/value heads, bf16 out, 72 us, 3.9 TB/s of
 // cache. Short ones: the chain launch, lengths, table, record, products, merge:
 // one token over 517 positions 5.9 us, 5 tokens over 2043 8.7 us.
@@ -912,9 +913,9 @@ cudaError_t launch(const Args& a, int grid, cudaStream_t s) {                  /
 // Tiles of so many groups of 8 rows, heads of 128, go to the tcgen05 kernel:
 // its time hardly depends on the rows of a tile or on P's parts, this kernel's
 // grows with them. GB300, here / there in us for 8, 16, 24, 32 rows, 24
-// sequences of 8000 positions: fp32 out 69/83, 95/88, 127/103, 168/108; bf16 out
-// 61/80, 77/84, 99/98, 126/101. 2 of 131071, fp32, from 16 rows: 117/112,
-// 150/133, 202/136.
+// sequences of 8000 positions: fp32 out 67/83, 94/89, 127/105, 170/109; bf16 out
+// 59/80, 76/84, 100/99, 126/102. 2 of 131071, fp32, from 16 rows: 116/113,
+// 151/136, 203/137.
 constexpr int tc_rows(bool out_bf16) { return out_bf16 ? 3 : 2; }
 
 struct Plan {

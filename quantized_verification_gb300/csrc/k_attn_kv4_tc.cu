@@ -8,8 +8,8 @@
 //   products are formed elsewhere. On mma.sync many query rows keep the legacy
 //   tensor pipe busy about as long as the unpacking the ALUs, with too few warps
 //   to overlap the two. GB300, fp32 out, 24 sequences of 8000 positions, 8
-//   key/value heads: 24 rows 103 us against 127, 32 rows 108 us against 168 (31
-//   us to read the cache). What is left is the ALUs' and the issue slots' (47 and
+//   key/value heads: 24 rows 105 us against 127, 32 rows 109 us against 170 (31
+//   us to read the cache). What is left is the ALUs' and the issue slots' (49 and
 //   54 % busy) and the waits of 4 unpacking warps a scheduler.
 //
 // A CTA takes 128 positions (4 records) a step. 8 warps work on them, a ninth
@@ -32,7 +32,7 @@
 // the cache's format: they are attended to with plain fp32 arithmetic while the
 // first records load; their outputs wait in tensor memory and are merged at the
 // end. A tile's start, own rows and end take as long as about kTcTileCost units:
-// 24 sequences of 33 to 16001 positions, 24 rows, 60 us with 18, 62 with 22, 63
+// 24 sequences of 33 to 16001 positions, 20 rows, 61 us with 18, 63 with 22, 64
 // with 14.
 
 #include "attn_kv4_common.cuh"

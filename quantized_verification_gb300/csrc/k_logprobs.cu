@@ -510,10 +510,12 @@ cudaError_t launch_token_logprobs(const void* x, bool bf16, const int32_t* tok, 
     a.x = static_cast<const uint8_t*>(x);
     a.tok = tok; a.V = V; a.K = K; a.logprob = logprob; a.entropy = entropy; a.top_tok = top_tok; a.top_lp = top_lp;
     // Many short rows: CTAs of 128 threads, ten an SM. A row's reductions and
-    // barriers are then most of its time, and overlap. GB300, us with 512 / 128
-    // threads: 3859 rows of 3245 bf16 logits, 20 tokens, 57/24; fp32: 600 of 3245
-    // 10.0/6.8 (300: 5.6/5.9), 2000 of 8000 34/19, 2000 of 16000 46/34, 1200 of
-    // 32003 37/28 (600: 14.8/15.5), 2000 of 65000 98/100, 2000 of 151936 197/231.
+    // barriers are then most of its time, and overlap. GB300, 20 tokens, us with
+    // 512 / 128 threads: fp32: 600 rows of 3245 9.6/6.2 (300: 5.3/5.5), 2000 of 8000
+    // 32/18, of 16000 44/33, 1200 of 32003 37.8/39.6 (600: 15.3/21.5), 2000 of 65000
+    // 102/152, of 151936 221/349; bf16: 3859 of 3245 57/24, 600 10.2/6.8 (300:
+    // 5.6/6.0), 2000 of 8000 34/17, of 16000 39/24, of 32003 53/41, 1200 of 32003
+    // 27.6/24.4 (600: 14.3/17.5), 2000 of 60000 71/77, of 151936 129/193.
     const bool small = V <= (1 << 15) && M > 2 * sms * (V >> 13 > 1 ? V >> 13 : 1);
     int C = 1;
     while (!small && C < kLpMaxCluster && (long long)M * C * 2 <= 2 * sms && V / (C * 2) >= 2 * kLpThreads * (bf16 ? 8 : 4)) C *= 2;
