@@ -577,6 +577,98 @@ QV_API qv_status qv_attention_verify_kv4(const uint16_t* qkv, const uint8_t* cac
                                          size_t workspace_bytes, cudaStream_t stream);
 
 /*
+ * qv_rotary -- rotary positions of the query and key heads of qkv rows, after an
+ * optional RMS norm of every head: what the attention calls above expect to have
+ * happened to their rows.
+ *   The Quasar summaries do not spell the layer out; the non-GEMM computation
+ *   stays in high precision (gist.science/ja summary, section 2.2 item 3).
+ *   qkv       [M][(Hq + 2 Hkv) * D] fp32 or bf16 (dtype), 16-byte aligned
+ *   positions [M] int32, any values (negative ones rotate back)
+ *   inv_freq  [rot / 2] fp32: pair i of a head (a, b) becomes
+ *             (a c - b s, b c + a s), c and s the magnitude times the cosine and
+ *             sine of positions[m] * inv_freq[i]. The product is not rounded: an
+ *             angle is off by 2e-7 at most, at any position.
+ *   Pairs are values i and i + rot / 2 of a head, or 2 i and 2 i + 1
+ *   (interleaved != 0); values from rot on are not rotated.
+ *   q_gamma, k_gamma [D] bf16, 16-byte aligned, or both NULL: a head x is first
+ *             x * gamma / sqrt(mean(x^2) + eps); the sum of a head's squares must
+ *             be a binary32 number
+ *   out       qkv itself (the value heads are then not touched) or a buffer that
+ *             does not overlap it (they are copied)
+ *   All in binary32 with one rounding at the end.
+ *   1 <= M <= 2^24, 0 <= Hq, Hkv <= 65535, not both 0; D a multiple of 8 in [8,
+ *   256], rot a multiple of 8 in [8, D]. One launch, no workspace.
+ *
+ * qv_rotary_frequencies -- inv_freq and magnitude for qv_rotary (host function,
+ * host pointers; magnitude may be NULL). f_i = base^(-2 i / rot), and
+ *   QV_ROTARY_PLAIN   f_i
+ *   QV_ROTARY_LINEAR  f_i / factor
+ *   QV_ROTARY_BASE    f_i of the base base * factor^(rot / (rot - 2))
+ *   QV_ROTARY_PARTS   f_i where a pair makes fast_turns turns or more within
+ *             trained_length positions, f_i / factor where it makes slow_turns or
+ *             fewer, a linear blend between; magnitude 0.1 ln(factor) + 1
+ * The magnitude is 1 otherwise. rot even in [2, 256], base > 1, factor >= 1.
+ */
+typedef enum { QV_ROTARY_PLAIN = 0, QV_ROTARY_LINEAR = 1, QV_ROTARY_BASE = 2, QV_ROTARY_PARTS = 3 } qv_rotary_scaling;
+QV_API qv_status qv_rotary(const void* qkv, qv_dtype dtype, const int32_t* positions, const float* inv_freq, int M,
+                           int Hq, int Hkv, int D, int rot, int interleaved, float magnitude, const uint16_t* q_gamma,
+                           const uint16_t* k_gamma, float eps, void* out, cudaStream_t stream);
+QV_API qv_status qv_rotary_frequencies(int rot, double base, qv_rotary_scaling scaling, double factor,
+                                       double trained_length, double fast_turns, double slow_turns, float* inv_freq,
+                                       float* magnitude);
+
+/*
+ * qv_attention_prompt -- causal grouped-query attention of whole prompts, packed
+ * one behind the other in one buffer: the attention that comes before the first
+ * verify step. A row attends to its own sequence's rows up to itself.
+ *   qkv       [M][(Hq + 2 Hkv) * D] bf16, 16-byte aligned, as in
+ *             qv_attention_verify (rows already rotated, if the model rotates)
+ *   cu_rows   [B + 1] int32, not falling: sequence b is rows cu_rows[b] ..
+ *             cu_rows[b + 1] - 1 (none where the two are equal). Rows before
+ *             cu_rows[0] and from cu_rows[B] on belong to no sequence: they may
+ *             hold anything and their outputs are left as they were. Values
+ *             outside [0, M] are clamped; falling ones give unspecified outputs.
+ *   out       [M][Hq * D] fp32 or bf16 (out_dtype), 16-byte aligned; must not
+ *             overlap qkv
+ *   scale     in (0, 2e38]
+ *   Hq a multiple of Hkv, Hq / Hkv <= 128, D in {64, 128}, 1 <= M, B <= 2^24.
+ *   One launch, no workspace; it uses all 512 columns of tensor memory of an SM.
+ *   A key or value that is not finite does not reach the rows that do not see it;
+ *   a row that does see one is not finite.
+ *   A wait inside the kernel that runs out sets QV_DEVICE_ERR_FULL_WAIT
+ *   (qv_device_error); the call's outputs are then undefined.
+ * fp32 outputs are within about 3e-6 (2-norm) of the binary64 definition; for
+ * bf16 outputs the probabilities are rounded to bf16 before the product with the
+ * values. Results are the same from call to call.
+ *
+ * qv_attention_verify_prefix -- qv_attention_verify for a batch whose sequences
+ * all begin with the same prefix (a system prompt, a document), which is stored
+ * and read once for all of them. Token j of sequence b attends to the prefix, to
+ * the cache_len[b] cached positions behind it and to the step's tokens 0..j.
+ *   prefix_k, prefix_v [P][Hkv][D] bf16, 16-byte aligned (for one sequence, the
+ *             layout of k_cache and v_cache, and what qv_kv4_read gives)
+ *   prefix_len [1] int32 on the device (clamped to [0, P]); positions from it on
+ *             may hold anything
+ *   out       [B*T][Hq * D] fp32 or bf16 (out_dtype), 16-byte aligned
+ *   workspace qv_attention_prefix_workspace_bytes(...) bytes (a host function; 0
+ *             for an invalid shape), 16-byte aligned, scratch: needs no initial
+ *             value, and must not be shared with calls that may run at the same
+ *             time
+ *   1 <= P <= 2^24; the other arguments, their limits and the errors are
+ *   qv_attention_verify's.
+ *   Two launches: partial results over the prefix for the query rows of all
+ *   sequences together, then qv_attention_verify's kernel, which adds them.
+ */
+QV_API qv_status qv_attention_prompt(const uint16_t* qkv, const int32_t* cu_rows, int B, int M, int Hq, int Hkv, int D,
+                                     float scale, void* out, qv_dtype out_dtype, cudaStream_t stream);
+QV_API size_t qv_attention_prefix_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int P);
+QV_API qv_status qv_attention_verify_prefix(const uint16_t* qkv, const uint16_t* prefix_k, const uint16_t* prefix_v,
+                                            const int32_t* prefix_len, int P, const uint16_t* k_cache,
+                                            const uint16_t* v_cache, const int32_t* cache_len, int B, int T, int Hq,
+                                            int Hkv, int D, int Lmax, float scale, void* out, qv_dtype out_dtype,
+                                            void* workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/*
  * qv_token_logprobs -- log probability of one given token per row of logits,
  * the row's entropy and its most probable tokens: what a server reports for
  * the tokens of a verify step (or of a scored text).

@@ -30,13 +30,14 @@ NVCC_FLAGS = ARCH + [
     "-I", INCLUDE, "-I", CSRC,
 ]
 # Translation units whose floating point results are checked against a
-# tolerance (attention, the logit-fidelity diagnostic, the token log
-# probabilities) may contract a*b+c
+# tolerance (attention, rotary positions, the logit-fidelity diagnostic, the
+# token log probabilities) may contract a*b+c
 # into one fused multiply-add; every other unit computes results that must
 # equal the oracle's bit for bit, so no expression there may be contracted
 # (explicit fused operations, where the definition has one, are written as
 # such).
-FMA_CONTRACTION_OK = {"k_attn.cu", "k_attn_kv4.cu", "k_attn_kv4_tc.cu", "k_fidelity.cu", "k_logprobs.cu"}
+FMA_CONTRACTION_OK = {"k_attn.cu", "k_attn_kv4.cu", "k_attn_kv4_tc.cu", "k_attn_prompt.cu", "k_fidelity.cu",
+                      "k_logprobs.cu", "k_rotary.cu"}
 
 
 def flags_for(src: str) -> list[str]:

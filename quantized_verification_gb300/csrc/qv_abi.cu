@@ -11,6 +11,7 @@
 #include <cstdint>
 #include <cstdio>
 #include <atomic>
+#include <cmath>
 #include <mutex>
 
 #include "qv.h"
@@ -128,6 +129,33 @@ qv_status encode_kv_cache(CUtensorMap* map, const void* base, int B, int Lmax, i
                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     if (r != CUDA_SUCCESS) return fail(QV_ERR_CUDA, "cuTensorMapEncodeTiled (KV cache) failed (CUresult %d)", (int)r);
     return QV_OK;
+}
+
+// [rows][heads][D] bf16 (qkv rows, a prefix) as a 3-D tensor map (D, heads,
+// rows) with a box of 64 values x box_heads x box_rows and the 128-byte
+// swizzle; rows past the last read as zero.
+qv_status encode_heads(CUtensorMap* map, const void* base, int rows, int heads, int D, int box_heads, int box_rows) {
+    qv_status st = get_encoder();
+    if (st != QV_OK) return st;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)heads * D * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_rows};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                          CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                          CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(QV_ERR_CUDA, "cuTensorMapEncodeTiled (rows of heads) failed (CUresult %d)", (int)r);
+    return QV_OK;
+}
+
+// The four maps of qv_attention_verify's caches (none when Lmax == 0).
+qv_status encode_cache_maps(qv::KvMaps* maps, const void* k, const void* v, int B, int Lmax, int Hkv, int D) {
+    if (Lmax == 0) return QV_OK;
+    qv_status st = encode_kv_cache(&maps->k64, k, B, Lmax, Hkv, D, 64);
+    if (st == QV_OK) st = encode_kv_cache(&maps->v64, v, B, Lmax, Hkv, D, 64);
+    if (st == QV_OK) st = encode_kv_cache(&maps->k16, k, B, Lmax, Hkv, D, 16);
+    if (st == QV_OK) st = encode_kv_cache(&maps->v16, v, B, Lmax, Hkv, D, 16);
+    return st;
 }
 
 // W8A8 streaming GEMM kernel by padded token count. Up to 16 tokens the
@@ -660,16 +688,10 @@ qv_status qv_attention_verify(const uint16_t* qkv, const uint16_t* k_cache, cons
     QV_CHECK_DEV(cache_len);
     QV_CHECK_DEV(out);
     qv::KvMaps maps;
-    if (Lmax > 0) {
-        st = encode_kv_cache(&maps.k64, k_cache, B, Lmax, Hkv, D, 64);
-        if (st == QV_OK) st = encode_kv_cache(&maps.v64, v_cache, B, Lmax, Hkv, D, 64);
-        if (st == QV_OK) st = encode_kv_cache(&maps.k16, k_cache, B, Lmax, Hkv, D, 16);
-        if (st == QV_OK) st = encode_kv_cache(&maps.v16, v_cache, B, Lmax, Hkv, D, 16);
-        if (st != QV_OK) return st;
-    }
+    if ((st = encode_cache_maps(&maps, k_cache, v_cache, B, Lmax, Hkv, D)) != QV_OK) return st;
     const int hold = qv::debug_take_hold_attention() ? 1 : 0;
     cudaError_t e = qv::launch_attention_verify(qkv, Lmax > 0 ? &maps : nullptr, cache_len, B, T, Hq, Hkv, D, Lmax,
-                                                scale, out, hold, qv::debug_slot_wait_ns(), stream);
+                                                scale, out, hold, qv::debug_slot_wait_ns(), nullptr, false, stream);
     if (e != cudaSuccess) return cuda_fail(e, "qv_attention_verify launch");
     return ok();
 }
@@ -820,6 +842,189 @@ qv_status qv_attention_verify_kv4(const uint16_t* qkv, const uint8_t* cache, con
     e = qv::launch_attention_kv4(qkv, cache, block_table, cache_len, B, T, Hq, Hkv, D, NB, pages, scale, out,
                                  out_dtype == QV_BF16, workspace, sms, hold, qv::debug_slot_wait_ns(), stream);
     if (e != cudaSuccess) return cuda_fail(e, "qv_attention_verify_kv4 launch");
+    return ok();
+}
+
+namespace {
+// Query rows of one attention call over whole prompts or a prefix.
+constexpr int kPromptMaxRows = 1 << 24;
+constexpr int kPromptMaxGroup = 128;
+
+bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return x < y + nb && y < x + na;
+}
+}  // namespace
+
+qv_status qv_attention_prompt(const uint16_t* qkv, const int32_t* cu_rows, int B, int M, int Hq, int Hkv, int D,
+                              float scale, void* out, qv_dtype out_dtype, cudaStream_t stream) {
+    if (B < 1 || B > kPromptMaxRows) return fail(QV_ERR_INVALID_ARG, "B=%d outside [1, 2^24]", B);
+    if (M < 1 || M > kPromptMaxRows) return fail(QV_ERR_INVALID_ARG, "M=%d outside [1, 2^24]", M);
+    if (Hkv < 1 || Hkv > 65535 || Hq < Hkv || Hq > 65535 || Hq % Hkv != 0)
+        return fail(QV_ERR_INVALID_ARG, "Hq=%d must be a positive multiple of Hkv=%d and <= 65535", Hq, Hkv);
+    if (Hq / Hkv > kPromptMaxGroup) return fail(QV_ERR_INVALID_ARG, "Hq / Hkv must be <= %d", kPromptMaxGroup);
+    if (D != 64 && D != 128) return fail(QV_ERR_INVALID_ARG, "D=%d must be 64 or 128", D);
+    if (!qkv || !cu_rows || !out) return fail(QV_ERR_INVALID_ARG, "null pointer");
+    if (!is_dtype(out_dtype)) return fail(QV_ERR_INVALID_ARG, "out_dtype must be QV_F32 or QV_BF16");
+    if (!(scale > 0.0f) || scale > 2.0e38f) return fail(QV_ERR_INVALID_ARG, "scale must be in (0, 2e38]");
+    if (!aligned(qkv, 16) || !aligned(out, 16) || !aligned(cu_rows, 4))
+        return fail(QV_ERR_INVALID_ARG, "qkv and out must be 16-byte aligned, cu_rows 4-byte aligned");
+    const int tokens = qv::attention_prompt_tokens(Hq / Hkv);
+    if ((long long)((M + tokens - 1) / tokens) * Hkv > 0x7FFFFFFFll)
+        return fail(QV_ERR_UNSUPPORTED, "M * Hq is too large for one call");
+    QV_CHECK_DEV(qkv);
+    QV_CHECK_DEV(cu_rows);
+    QV_CHECK_DEV(out);
+    cudaError_t e;
+    const int sms = sms_of_current_device(&e);
+    if (e != cudaSuccess) return cuda_fail(e, "device query");
+    CUtensorMap q, kv;
+    qv_status st = encode_heads(&q, qkv, M, Hq + 2 * Hkv, D, Hq / Hkv, tokens);
+    if (st == QV_OK) st = encode_heads(&kv, qkv, M, Hq + 2 * Hkv, D, 1, 128);
+    if (st != QV_OK) return st;
+    const int hold = qv::debug_take_hold_attention() ? 1 : 0;
+    e = qv::launch_attention_prompt(q, kv, cu_rows, B, M, Hq, Hkv, D, scale, out, out_dtype == QV_BF16, sms, hold,
+                                    qv::debug_slot_wait_ns(), stream);
+    if (e != cudaSuccess) return cuda_fail(e, "qv_attention_prompt launch");
+    return ok();
+}
+
+namespace {
+qv_status check_attention_prefix_shape(int B, int T, int Hq, int Hkv, int D, int P) {
+    qv_status st = check_attention_shape(B, T, Hq, Hkv, D, 0);
+    if (st != QV_OK) return st;
+    if (P < 1 || P > (1 << 24)) return fail(QV_ERR_INVALID_ARG, "P=%d outside [1, 2^24]", P);
+    return QV_OK;
+}
+}  // namespace
+
+size_t qv_attention_prefix_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int P) {
+    if (check_attention_prefix_shape(B, T, Hq, Hkv, D, P) != QV_OK) return 0;
+    cudaError_t e;
+    const int sms = sms_of_current_device(&e);
+    if (e != cudaSuccess) {
+        cuda_fail(e, "device query");
+        return 0;
+    }
+    return qv::attention_prefix_workspace_bytes(B * T, Hq, Hkv, D, P, sms);
+}
+
+qv_status qv_attention_verify_prefix(const uint16_t* qkv, const uint16_t* prefix_k, const uint16_t* prefix_v,
+                                     const int32_t* prefix_len, int P, const uint16_t* k_cache,
+                                     const uint16_t* v_cache, const int32_t* cache_len, int B, int T, int Hq, int Hkv,
+                                     int D, int Lmax, float scale, void* out, qv_dtype out_dtype, void* workspace,
+                                     size_t workspace_bytes, cudaStream_t stream) {
+    qv_status st = check_attention_prefix_shape(B, T, Hq, Hkv, D, P);
+    if (st != QV_OK) return st;
+    if ((st = check_attention_shape(B, T, Hq, Hkv, D, Lmax)) != QV_OK) return st;
+    if (!qkv || !prefix_k || !prefix_v || !prefix_len || !cache_len || !out)
+        return fail(QV_ERR_INVALID_ARG, "null pointer");
+    if (Lmax > 0 && (!k_cache || !v_cache)) return fail(QV_ERR_INVALID_ARG, "k_cache / v_cache null with Lmax > 0");
+    if (!is_dtype(out_dtype)) return fail(QV_ERR_INVALID_ARG, "out_dtype must be QV_F32 or QV_BF16");
+    if (!(scale > 0.0f) || scale > 2.0e38f) return fail(QV_ERR_INVALID_ARG, "scale must be in (0, 2e38]");
+    if (!aligned(qkv, 16) || !aligned(prefix_k, 16) || !aligned(prefix_v, 16) || (k_cache && !aligned(k_cache, 16)) ||
+        (v_cache && !aligned(v_cache, 16)) || !aligned(cache_len, 4) || !aligned(prefix_len, 4) || !aligned(out, 16))
+        return fail(QV_ERR_INVALID_ARG, "qkv, the prefix, the caches and out must be 16-byte aligned");
+    cudaError_t e;
+    const int sms = sms_of_current_device(&e);
+    if (e != cudaSuccess) return cuda_fail(e, "device query");
+    const size_t need = qv::attention_prefix_workspace_bytes(B * T, Hq, Hkv, D, P, sms);
+    if (!workspace) return fail(QV_ERR_WORKSPACE, "workspace is null (%zu bytes needed)", need);
+    if (!aligned(workspace, 16)) return fail(QV_ERR_WORKSPACE, "workspace must be 16-byte aligned");
+    if (workspace_bytes < need) return fail(QV_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
+    QV_CHECK_DEV(qkv);
+    QV_CHECK_DEV(prefix_k);
+    QV_CHECK_DEV(prefix_v);
+    QV_CHECK_DEV(prefix_len);
+    QV_CHECK_DEV(k_cache);
+    QV_CHECK_DEV(v_cache);
+    QV_CHECK_DEV(cache_len);
+    QV_CHECK_DEV(out);
+    QV_CHECK_DEV(workspace);
+    CUtensorMap q, k, v;
+    qv::KvMaps maps;
+    st = encode_heads(&q, qkv, B * T, Hq + 2 * Hkv, D, Hq / Hkv, qv::attention_prompt_tokens(Hq / Hkv));
+    if (st == QV_OK) st = encode_heads(&k, prefix_k, P, Hkv, D, 1, 128);
+    if (st == QV_OK) st = encode_heads(&v, prefix_v, P, Hkv, D, 1, 128);
+    if (st == QV_OK) st = encode_cache_maps(&maps, k_cache, v_cache, B, Lmax, Hkv, D);
+    if (st != QV_OK) return st;
+    const int hold = qv::debug_take_hold_attention() ? 1 : 0;
+    qv::PrefixParts parts;
+    e = qv::launch_attention_prefix(q, k, v, prefix_len, B * T, Hq, Hkv, D, P, scale, out_dtype == QV_F32, workspace,
+                                    sms, hold, qv::debug_slot_wait_ns(), &parts, stream);
+    if (e == cudaSuccess)
+        e = qv::launch_attention_verify(qkv, Lmax > 0 ? &maps : nullptr, cache_len, B, T, Hq, Hkv, D, Lmax, scale, out,
+                                        hold, qv::debug_slot_wait_ns(), &parts, out_dtype == QV_BF16, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "qv_attention_verify_prefix launch");
+    return ok();
+}
+
+qv_status qv_rotary(const void* qkv, qv_dtype dtype, const int32_t* positions, const float* inv_freq, int M, int Hq,
+                    int Hkv, int D, int rot, int interleaved, float magnitude, const uint16_t* q_gamma,
+                    const uint16_t* k_gamma, float eps, void* out, cudaStream_t stream) {
+    if (M < 1 || M > kPromptMaxRows) return fail(QV_ERR_INVALID_ARG, "M=%d outside [1, 2^24]", M);
+    if (Hq < 0 || Hkv < 0 || Hq > 65535 || Hkv > 65535 || Hq + Hkv < 1)
+        return fail(QV_ERR_INVALID_ARG, "Hq=%d and Hkv=%d must be in [0, 65535] and not both 0", Hq, Hkv);
+    if (D < 8 || D > 256 || D % 8 != 0) return fail(QV_ERR_INVALID_ARG, "D=%d must be a multiple of 8 in [8, 256]", D);
+    if (rot < 8 || rot > D || rot % 8 != 0)
+        return fail(QV_ERR_INVALID_ARG, "rot=%d must be a multiple of 8 in [8, D]", rot);
+    if (!is_dtype(dtype)) return fail(QV_ERR_INVALID_ARG, "dtype must be QV_F32 or QV_BF16");
+    if (!qkv || !positions || !inv_freq || !out) return fail(QV_ERR_INVALID_ARG, "null pointer");
+    if (!q_gamma != !k_gamma) return fail(QV_ERR_INVALID_ARG, "q_gamma and k_gamma go together");
+    if (!(magnitude > -3.0e38f && magnitude < 3.0e38f)) return fail(QV_ERR_INVALID_ARG, "magnitude must be finite");
+    if (q_gamma && !(eps >= 0.0f && eps < 3.0e38f)) return fail(QV_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    if (!aligned(qkv, 16) || !aligned(out, 16) || !aligned(positions, 4) || !aligned(inv_freq, 4) ||
+        (q_gamma && (!aligned(q_gamma, 16) || !aligned(k_gamma, 16))))
+        return fail(QV_ERR_INVALID_ARG, "qkv, out and the norm weights must be 16-byte aligned, the rest 4-byte aligned");
+    const size_t bytes = (size_t)M * (Hq + 2 * (size_t)Hkv) * D * (dtype == QV_F32 ? 4 : 2);
+    if (out != qkv && overlap(qkv, bytes, out, bytes))
+        return fail(QV_ERR_INVALID_ARG, "out must be qkv itself or not overlap it");
+    QV_CHECK_DEV(qkv);
+    QV_CHECK_DEV(positions);
+    QV_CHECK_DEV(inv_freq);
+    QV_CHECK_DEV(q_gamma);
+    QV_CHECK_DEV(k_gamma);
+    QV_CHECK_DEV(out);
+    cudaError_t e;
+    const int sms = sms_of_current_device(&e);
+    if (e != cudaSuccess) return cuda_fail(e, "device query");
+    qv::RotaryArgs a;
+    a.x = qkv; a.out = out; a.pos = positions; a.freq = inv_freq;
+    a.q_gamma = q_gamma; a.k_gamma = k_gamma;
+    a.eps = eps; a.magnitude = magnitude;
+    a.M = M; a.Hq = Hq; a.Hkv = Hkv; a.D = D; a.rot = rot; a.interleaved = interleaved ? 1 : 0;
+    e = qv::launch_rotary(a, dtype == QV_BF16, sms, stream);
+    if (e != cudaSuccess) return cuda_fail(e, "qv_rotary launch");
+    return ok();
+}
+
+qv_status qv_rotary_frequencies(int rot, double base, qv_rotary_scaling scaling, double factor, double trained_length,
+                                double fast_turns, double slow_turns, float* inv_freq, float* magnitude) {
+    if (rot < 2 || rot > 256 || rot % 2 != 0) return fail(QV_ERR_INVALID_ARG, "rot=%d must be even and in [2, 256]", rot);
+    if (!(base > 1.0) || !(base < 1e30)) return fail(QV_ERR_INVALID_ARG, "base must be in (1, 1e30)");
+    if (!inv_freq) return fail(QV_ERR_INVALID_ARG, "null pointer");
+    if (scaling != QV_ROTARY_PLAIN && (!(factor >= 1.0) || !(factor < 1e6)))
+        return fail(QV_ERR_INVALID_ARG, "factor must be in [1, 1e6)");
+    if (scaling == QV_ROTARY_PARTS &&
+        (!(trained_length > 0.0) || !(trained_length < 1e12) || !(fast_turns > slow_turns) || !(slow_turns >= 0.0) ||
+         !(fast_turns < 1e12)))
+        return fail(QV_ERR_INVALID_ARG, "trained_length must be > 0 and fast_turns > slow_turns >= 0");
+    if (scaling != QV_ROTARY_PLAIN && scaling != QV_ROTARY_LINEAR && scaling != QV_ROTARY_BASE &&
+        scaling != QV_ROTARY_PARTS)
+        return fail(QV_ERR_INVALID_ARG, "unknown scaling %d", (int)scaling);
+    if (scaling == QV_ROTARY_BASE && rot > 2) base *= pow(factor, (double)rot / (rot - 2));
+    for (int i = 0; i < rot / 2; ++i) {
+        double f = pow(base, -2.0 * i / rot);
+        if (scaling == QV_ROTARY_LINEAR) f /= factor;
+        if (scaling == QV_ROTARY_PARTS) {
+            const double turns = trained_length * f / 6.283185307179586;
+            double keep = (turns - slow_turns) / (fast_turns - slow_turns);
+            keep = keep < 0.0 ? 0.0 : (keep > 1.0 ? 1.0 : keep);
+            f = f * keep + f / factor * (1.0 - keep);
+        }
+        inv_freq[i] = (float)f;
+    }
+    if (magnitude) *magnitude = scaling == QV_ROTARY_PARTS ? (float)(0.1 * log(factor) + 1.0) : 1.0f;
     return ok();
 }
 
@@ -1017,13 +1222,14 @@ qv_status qv_device_error(unsigned int* code) {
     if (!code) return fail(QV_ERR_INVALID_ARG, "code is null");
     cudaError_t e = cudaDeviceSynchronize();
     if (e != cudaSuccess) return cuda_fail(e, "cudaDeviceSynchronize");
-    unsigned tc = 0, at = 0, a4 = 0;
+    unsigned tc = 0, at = 0, a4 = 0, ap = 0;
     e = qv::read_and_clear_stream_gemm_error(code);
     if (e == cudaSuccess) e = qv::read_and_clear_tc_gemm_error(&tc);
     if (e == cudaSuccess) e = qv::read_and_clear_attn_error(&at);
     if (e == cudaSuccess) e = qv::read_and_clear_attn_kv4_error(&a4);
+    if (e == cudaSuccess) e = qv::read_and_clear_attn_prompt_error(&ap);
     if (e != cudaSuccess) return cuda_fail(e, "reading the device error word");
-    *code |= tc | at | a4;
+    *code |= tc | at | a4 | ap;
     return ok();
 }
 

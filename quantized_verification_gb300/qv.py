@@ -32,11 +32,13 @@ EXPORTS = ("qv_quantize_act", "qv_w8a8_linear", "qv_lm_head_argmax", "qv_accept"
            "qv_tree_accept", "qv_quantize_weight_w4", "qv_w4a8_linear", "qv_w4a8_swiglu",
            "qv_w4a8_lm_head_argmax", "qv_logit_fidelity", "qv_attention_workspace_bytes",
            "qv_attention_verify", "qv_kv4_write", "qv_kv4_read", "qv_attention_kv4_workspace_bytes",
-           "qv_attention_verify_kv4", "qv_token_logprobs", "qv_debug_set_slot_wait_ns", "qv_debug_drop_partials",
+           "qv_attention_verify_kv4", "qv_rotary", "qv_rotary_frequencies", "qv_attention_prompt",
+           "qv_attention_prefix_workspace_bytes", "qv_attention_verify_prefix", "qv_token_logprobs", "qv_debug_set_slot_wait_ns", "qv_debug_drop_partials",
            "qv_debug_hold_attention_loads")
 MAX_STACK_M = 16
 QV_KV4_BLOCK = 32        # positions of a 4-bit cache block
 QV_MAX_TOP_K = 32
+QV_ROTARY_PLAIN, QV_ROTARY_LINEAR, QV_ROTARY_BASE, QV_ROTARY_PARTS = range(4)
 
 
 class LinearDesc(ctypes.Structure):
@@ -97,6 +99,13 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
         L.qv_attention_kv4_workspace_bytes.argtypes = [I, I, I, I, I, I]
         L.qv_attention_kv4_workspace_bytes.restype = S
         L.qv_attention_verify_kv4.argtypes = [P, P, P, P, I, I, I, I, I, I, I, ctypes.c_float, P, I, P, S, P]
+        F, DBL = ctypes.c_float, ctypes.c_double
+        L.qv_rotary.argtypes = [P, I, P, P, I, I, I, I, I, I, F, P, P, F, P, P]
+        L.qv_rotary_frequencies.argtypes = [I, DBL, I, DBL, DBL, DBL, DBL, P, P]
+        L.qv_attention_prompt.argtypes = [P, P, I, I, I, I, I, F, P, I, P]
+        L.qv_attention_prefix_workspace_bytes.argtypes = [I, I, I, I, I, I]
+        L.qv_attention_prefix_workspace_bytes.restype = S
+        L.qv_attention_verify_prefix.argtypes = [P, P, P, P, I, P, P, P, I, I, I, I, I, I, F, P, I, P, S, P]
         L.qv_token_logprobs.argtypes = [P, I, P, I, I, I, P, P, P, P, P]
         L.qv_w4a8_linear.argtypes = [P, P, I, I, P, P, I, P, I, P, P, S, P]
         L.qv_w4a8_swiglu.argtypes = [P, P, I, I, P, P, I, P, P, S, P]
@@ -433,6 +442,98 @@ def qv_attention_verify_kv4(qkv, cache, cache_len, T, Hq, Hkv, scale, out, works
                                           _ptr(block_table) if NB > 0 else None, _per_seq(cache_len, B, "cache_len"),
                                           B, T, Hq, Hkv, D, NB, pages, scale, _ptr(out), _dtype(out), _ptr(workspace),
                                           workspace.numel(), _stream(stream)))
+
+
+# --- rotary positions, whole prompts, a shared prefix ---
+def _head_dim(row: int, Hq: int, Hkv: int) -> int:
+    heads = Hq + 2 * Hkv
+    if heads < 1 or row % heads != 0:
+        raise ValueError("qkv must be [M, (Hq+2Hkv)*D]")
+    return row // heads
+
+
+def qv_rotary(qkv, positions, inv_freq, Hq, Hkv, out=None, interleaved=False, magnitude=1.0, q_gamma=None,
+              k_gamma=None, eps=1e-6, stream=None):
+    """Rotate the query and key heads of qkv [M, (Hq+2Hkv)*D] (fp32 or bf16)
+    by positions [M] int32: pair i by positions[m] * inv_freq[i], inv_freq
+    [rot/2] fp32, cos and sin times magnitude. With q_gamma and k_gamma [D]
+    bf16 every head is RMS-normed first. In place, or to out (value heads are
+    then copied)."""
+    M, W = qkv.shape
+    D = _head_dim(W, Hq, Hkv)
+    if out is None:
+        out = qkv
+    elif out.shape != qkv.shape or out.dtype != qkv.dtype:
+        raise ValueError("out must have qkv's shape and dtype")
+    if inv_freq.dim() != 1 or inv_freq.dtype != torch.float32:
+        raise ValueError("inv_freq must be float32 [rot / 2]")
+    for name, g in (("q_gamma", q_gamma), ("k_gamma", k_gamma)):
+        if g is not None and (g.shape != (D,) or g.dtype != torch.bfloat16):
+            raise ValueError(f"{name} must be bf16 [D]")
+    _check(load().qv_rotary(_ptr(qkv), _dtype(qkv), _per_row(positions, M, torch.int32, "positions"), _ptr(inv_freq), M,
+                            Hq, Hkv, D, 2 * inv_freq.shape[0], 1 if interleaved else 0, magnitude, _ptr(q_gamma),
+                            _ptr(k_gamma), eps, _ptr(out), _stream(stream)))
+
+
+def qv_rotary_frequencies(rot, base=10000.0, scaling=QV_ROTARY_PLAIN, factor=1.0, trained_length=0.0, fast_turns=32.0,
+                          slow_turns=1.0):
+    """(inv_freq [rot/2] fp32 on the host, magnitude) for qv_rotary: plain
+    frequencies or ones stretched by `factor` for long contexts."""
+    inv_freq = torch.empty(max(rot, 0) // 2, dtype=torch.float32)
+    magnitude = ctypes.c_float()
+    _check(load().qv_rotary_frequencies(rot, base, scaling, factor, trained_length, fast_turns, slow_turns,
+                                        inv_freq.data_ptr() or None, ctypes.byref(magnitude)))
+    return inv_freq, magnitude.value
+
+
+def qv_attention_prompt(qkv, cu_rows, Hq, Hkv, scale, out, stream=None):
+    """Causal grouped-query attention of whole prompts packed in one buffer:
+    qkv [M, (Hq+2Hkv)*D] bf16, sequence b in rows cu_rows[b] to cu_rows[b+1] - 1
+    (cu_rows [B+1] int32) -> out [M, Hq*D] fp32 or bf16; rows of no sequence are
+    left as they were."""
+    M, W = qkv.shape
+    D = _head_dim(W, Hq, Hkv)
+    if qkv.dtype != torch.bfloat16:
+        raise ValueError("qkv must be bf16 [M, (Hq+2Hkv)*D]")
+    if cu_rows.dim() != 1 or cu_rows.dtype != torch.int32 or cu_rows.shape[0] < 2:
+        raise ValueError("cu_rows must be int32 [B+1]")
+    if out.shape != (M, Hq * D):
+        raise ValueError("out must be [M, Hq*D]")
+    _check(load().qv_attention_prompt(_ptr(qkv), _ptr(cu_rows), cu_rows.shape[0] - 1, M, Hq, Hkv, D, scale, _ptr(out),
+                                      _dtype(out), _stream(stream)))
+
+
+def qv_attention_prefix_workspace_bytes(B, T, Hq, Hkv, D, P) -> int:
+    return int(load().qv_attention_prefix_workspace_bytes(B, T, Hq, Hkv, D, P))
+
+
+def qv_attention_verify_prefix(qkv, prefix_k, prefix_v, prefix_len, k_cache, v_cache, cache_len, T, Hq, Hkv, scale, out,
+                               workspace, stream=None):
+    """qv_attention_verify for a batch whose sequences all begin with the same
+    prefix, prefix_k / prefix_v [P, Hkv, D] bf16 of prefix_len [1] int32
+    positions; k_cache / v_cache [B, Lmax, Hkv, D] hold what follows it ->
+    out [B*T, Hq*D] fp32 or bf16."""
+    P, hkv, D = prefix_k.shape
+    B, Lmax = k_cache.shape[:2]
+    if hkv != Hkv or prefix_v.shape != prefix_k.shape:
+        raise ValueError("prefix_k, prefix_v must be [P, Hkv, D]")
+    if k_cache.shape != (B, Lmax, Hkv, D) or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache, v_cache must be [B, Lmax, Hkv, D]")
+    if qkv.dtype != torch.bfloat16 or qkv.shape != (B * T, (Hq + 2 * Hkv) * D):
+        raise ValueError("qkv must be bf16 [B*T, (Hq+2Hkv)*D]")
+    for t in (prefix_k, prefix_v, k_cache, v_cache):
+        if t.dtype != torch.bfloat16:
+            raise ValueError("the prefix and the caches must be bf16")
+    if out.shape != (B * T, Hq * D):
+        raise ValueError("out must be [B*T, Hq*D]")
+    if workspace.dtype != torch.uint8:
+        raise ValueError("workspace must be a uint8 tensor")
+    _check(load().qv_attention_verify_prefix(_ptr(qkv), _ptr(prefix_k), _ptr(prefix_v),
+                                             _per_seq(prefix_len, 1, "prefix_len"), P,
+                                             _ptr(k_cache) if Lmax > 0 else None, _ptr(v_cache) if Lmax > 0 else None,
+                                             _per_seq(cache_len, B, "cache_len"), B, T, Hq, Hkv, D, Lmax, scale,
+                                             _ptr(out), _dtype(out), _ptr(workspace), workspace.numel(),
+                                             _stream(stream)))
 
 
 def _per_row(t, M, dtype, name):
