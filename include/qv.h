@@ -637,7 +637,7 @@ QV_API qv_status qv_rotary_frequencies(int rot, double base, qv_rotary_scaling s
  *   a row that does see one is not finite.
  *   A wait inside the kernel that runs out sets QV_DEVICE_ERR_FULL_WAIT
  *   (qv_device_error); the call's outputs are then undefined.
- * fp32 outputs are within about 3e-6 (2-norm) of the binary64 definition; for
+ * fp32 outputs are within about 5e-6 (2-norm) of the binary64 definition; for
  * bf16 outputs the probabilities are rounded to bf16 before the product with the
  * values. Results are the same from call to call.
  *
@@ -654,10 +654,11 @@ QV_API qv_status qv_rotary_frequencies(int rot, double base, qv_rotary_scaling s
  *             for an invalid shape), 16-byte aligned, scratch: needs no initial
  *             value, and must not be shared with calls that may run at the same
  *             time
- *   1 <= P <= 2^24; the other arguments, their limits and the errors are
- *   qv_attention_verify's.
- *   Two launches: partial results over the prefix for the query rows of all
- *   sequences together, then qv_attention_verify's kernel, which adds them.
+ *   1 <= P <= 2^24, T * Hq / Hkv <= 128, B * T * Hq <= 2^27; the other arguments,
+ *   their limits and the errors are qv_attention_verify's.
+ *   Two launches: partial results over parts of the prefix, for the query rows of
+ *   all sequences together, and of the caches; then their sums with the step's own
+ *   keys. The accuracy, what is not finite and waits: as qv_attention_prompt.
  */
 QV_API qv_status qv_attention_prompt(const uint16_t* qkv, const int32_t* cu_rows, int B, int M, int Hq, int Hkv, int D,
                                      float scale, void* out, qv_dtype out_dtype, cudaStream_t stream);

@@ -91,9 +91,6 @@ struct AttnArgs {
     float* out;              // [B*T][Hq*D]
     int hold_loads;          // test hook: request no stage, so every stage wait runs out
     unsigned long long wait_ns;   // limit of a stage wait (kWaitLimitNs by default)
-    PrefixParts parts;       // with a prefix: its partial results, and bf16 outputs or not
-    int out_bf16;
-    int rows;                // B * T
 };
 
 template <int D>
@@ -120,7 +117,6 @@ struct AttnLayout {
     static_assert(kAttnWarps * kAttnMaxRows * D * 4 <= kStages * StageBytes, "partials fit the stages");
     static_assert(Bar % 8 == 0 && RV % 16 == 0, "mbarrier and vector alignment");
     static_assert(DC % 4 == 0, "whole float4 slices");
-    static_assert((kPrefixMaxSplits + DC) * kAttnMaxRows * 4 <= kStages * StageBytes, "the prefix's weights and sums fit too");
 };
 
 // Byte offset of 16-byte chunk c (of D / 8) of row r (0..63) of tensor kv
@@ -257,7 +253,7 @@ __device__ __forceinline__ void cluster_arrive_relaxed() {
 }
 __device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.aligned;" ::: "memory"); }
 
-template <int D, int C, int NR, bool PFX>
+template <int D, int C, int NR>
 __global__ void __launch_bounds__(kAttnThreads, 1)
 attn_cluster_kernel(const __grid_constant__ KvMaps tm, const AttnArgs a) {
     using Ly = AttnLayout<D>;
@@ -596,28 +592,11 @@ attn_cluster_kernel(const __grid_constant__ KvMaps tm, const AttnArgs a) {
     cluster.sync();                                          // every push has landed
 
     // ---- the cluster merge of this CTA's dims [rank DC, (rank + 1) DC) from its receive buffer
-    // and, with a prefix, from its parts' results: their weights per row [splits][32] and their
-    // weighted sums [DC][32] take the drained ring (every push has been read from it)
-    float* s_pw = s_part;
-    float* s_px = s_part + kPrefixMaxSplits * kAttnMaxRows;
     if (tid < R) {
         float M = NEG_INF;
 #pragma unroll
         for (int c = 0; c < C; ++c) M = fmaxf(M, s_rm[c * kAttnMaxRows + tid]);
         float den = 0.f;
-        if constexpr (PFX) {
-            const int j = tid / G;
-            const float* ml = a.parts.ml + 2 * (((size_t)b * a.T + j) * a.Hq + kh * G + (tid - j * G));
-            const size_t step = 2 * (size_t)a.rows * a.Hq;
-            for (int s = 0; s < a.parts.splits; ++s) M = fmaxf(M, ml[s * step]);
-            for (int s = 0; s < a.parts.splits; ++s) {
-                const float2 v = *reinterpret_cast<const float2*>(ml + s * step);
-                const bool none = v.x == NEG_INF && v.y == 0.f;                        // no position: nothing written
-                const float w = none ? 0.f : exp2f(v.x - M);
-                s_pw[s * kAttnMaxRows + tid] = none ? -1.f : w;
-                den += w * v.y;
-            }
-        }
 #pragma unroll
         for (int c = 0; c < C; ++c) {
             const float mc = s_rm[c * kAttnMaxRows + tid];
@@ -628,51 +607,21 @@ attn_cluster_kernel(const __grid_constant__ KvMaps tm, const AttnArgs a) {
         s_cw[tid * (C + 1) + C] = den;
     }
     __syncthreads();
-    if constexpr (PFX) {
-        for (int e = tid; e < R * (DC / 4); e += kAttnThreads) {
-            const int r = e / (DC / 4), d4 = 4 * (e - r * (DC / 4));
-            const int j = r / G;
-            const size_t step = (size_t)a.rows * a.Hq * D;
-            const float* p = a.parts.o + (((size_t)b * a.T + j) * a.Hq + kh * G + (r - j * G)) * D + rank * DC + d4;
-            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-            for (int s = 0; s < a.parts.splits; ++s) {
-                const float w = s_pw[s * kAttnMaxRows + r];
-                if (w < 0.f) continue;
-                const float4 v = *reinterpret_cast<const float4*>(p + s * step);
-                x.x += w * v.x;
-                x.y += w * v.y;
-                x.z += w * v.z;
-                x.w += w * v.w;
-            }
-            s_px[d4 * kAttnMaxRows + r] = x.x;
-            s_px[(d4 + 1) * kAttnMaxRows + r] = x.y;
-            s_px[(d4 + 2) * kAttnMaxRows + r] = x.z;
-            s_px[(d4 + 3) * kAttnMaxRows + r] = x.w;
-        }
-        __syncthreads();
-    }
     for (int e = tid; e < R * DC; e += kAttnThreads) {
         const int dl = e / R, r = e - dl * R;
         float num = 0.f;
-        if constexpr (PFX) num = s_px[dl * kAttnMaxRows + r];
 #pragma unroll
         for (int c = 0; c < C; ++c) num += s_cw[r * (C + 1) + c] * s_rv[(c * DC + dl) * kAttnMaxRows + r];
         const int j = r / G, h = kh * G + (r - j * G);
-        const size_t at = ((size_t)b * a.T + j) * (size_t)a.Hq * D + (size_t)h * D + rank * DC + dl;
-        const float o = num / s_cw[r * (C + 1) + C];
-        if (PFX && a.out_bf16)
-            reinterpret_cast<__nv_bfloat16*>(a.out)[at] = __float2bfloat16_rn(o);
-        else
-            a.out[at] = o;
+        a.out[((size_t)b * a.T + j) * (size_t)a.Hq * D + (size_t)h * D + rank * DC + dl] = num / s_cw[r * (C + 1) + C];
     }
     // nothing reads another CTA's memory after the cluster barrier: no second one
 }
 
-template <int D, int C, int NR, bool PFX>
+template <int D, int C, int NR>
 cudaError_t launch_cluster(const KvMaps& tm, const AttnArgs& args, int B, cudaStream_t s) {
     using Ly = AttnLayout<D>;
-    cudaError_t e = cudaFuncSetAttribute(attn_cluster_kernel<D, C, NR, PFX>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    cudaError_t e = cudaFuncSetAttribute(attn_cluster_kernel<D, C, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                          Ly::Alloc);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -689,7 +638,7 @@ cudaError_t launch_cluster(const KvMaps& tm, const AttnArgs& args, int B, cudaSt
     attr[1].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 2;
-    return cudaLaunchKernelEx(&cfg, attn_cluster_kernel<D, C, NR, PFX>, tm, args);
+    return cudaLaunchKernelEx(&cfg, attn_cluster_kernel<D, C, NR>, tm, args);
 }
 
 static_assert(AttnLayout<128>::Alloc <= (int)kMaxDynSmem, "shared memory budget");
@@ -699,28 +648,22 @@ static_assert(AttnLayout<128>::Alloc <= (int)kMaxDynSmem, "shared memory budget"
 size_t attention_workspace_bytes(int, int, int, int, int, int) { return 16; }
 
 cudaError_t launch_attention_verify(const uint16_t* qkv, const KvMaps* maps, const int32_t* len, int B, int T, int Hq,
-                                    int Hkv, int D, int Lmax, float scale, void* out, int hold_loads,
-                                    unsigned long long wait_ns, const PrefixParts* parts, bool out_bf16,
-                                    cudaStream_t s) {
-    AttnArgs a = {};
+                                    int Hkv, int D, int Lmax, float scale, float* out, int hold_loads,
+                                    unsigned long long wait_ns, cudaStream_t s) {
+    AttnArgs a;
     a.hold_loads = hold_loads;
     a.wait_ns = wait_ns ? wait_ns : kWaitLimitNs;
     a.qkv = qkv; a.len = len;
     a.T = T; a.Hq = Hq; a.Hkv = Hkv; a.Lmax = Lmax;
     a.has_cache = maps ? 1 : 0;
     a.scale = scale;
-    a.out = static_cast<float*>(out);
-    if (parts) a.parts = *parts;
-    a.out_bf16 = out_bf16 ? 1 : 0;
-    a.rows = B * T;
+    a.out = out;
     KvMaps none;
     memset(&none, 0, sizeof(none));
     const KvMaps& tm = maps ? *maps : none;
     const int nr = (T * (Hq / Hkv) + 7) / 8;                 // n8 tiles of query rows
 #define QV_ATTN_CASE(DV, NRV) \
-    if (D == DV && nr == NRV)                                                   \
-        return parts ? launch_cluster<DV, kAttnCluster, NRV, true>(tm, a, B, s) \
-                     : launch_cluster<DV, kAttnCluster, NRV, false>(tm, a, B, s);
+    if (D == DV && nr == NRV) return launch_cluster<DV, kAttnCluster, NRV>(tm, a, B, s);
     QV_ATTN_CASE(128, 1) QV_ATTN_CASE(128, 2) QV_ATTN_CASE(128, 3) QV_ATTN_CASE(128, 4)
     QV_ATTN_CASE(64, 1) QV_ATTN_CASE(64, 2) QV_ATTN_CASE(64, 3) QV_ATTN_CASE(64, 4)
 #undef QV_ATTN_CASE

@@ -14,16 +14,15 @@
 // Packed prompts need no list of tiles: a tile of tokens that reaches over the end
 // of a sequence runs over both sequences' keys, each row between its own limits.
 //
-// Roles: warps 0-3 and 4-7 form the softmax of a tile each (thread = row, the
-// whole row of 128 scores in registers: no shuffles), the next warp's elected
-// thread issues the products, the last one the TMA loads of keys and values,
-// 128 positions each, into one ring. Per tile and 128 keys:
+// Roles: 8 warps form the softmax of a tile (two threads a row, 64 of its 128 scores
+// in registers each: no shuffles), one warp issues the products, one the TMA loads
+// of keys and values, 128 positions each, into one ring. Per tile and 128 keys:
 //   S = Q K^T      8 tcgen05.mma (D = 128), M = N = 128, both operands K-major
 //                  in shared memory, the accumulator in tensor memory
-//   P = 2^(cS-m)   rounded to bf16 over S's columns in tensor memory; the
-//                  maximum m lags (up to 2^8), so that O is rarely rescaled; the
-//                  rescaling is done by the softmax threads themselves, at a time
-//                  when no product writes O
+//   P = 2^(cS-m)   rounded to bf16 over S's columns in tensor memory. The reference
+//                  m moves only when a score lies more than 2^40 above it; O is
+//                  then rescaled by the softmax threads themselves, at a time when
+//                  no product writes it
 //   O += P V       8 tcgen05.mma, P from tensor memory, V as stored (M/N-major)
 // With two tiles one's softmax runs under the other's products; with one tile S
 // has two buffers.
@@ -52,10 +51,13 @@ __device__ unsigned int g_attn_prompt_error;
 
 namespace {
 
+constexpr int kPrefixMaxSplits = 64;       // parts of a prefix, and of a cache
 constexpr int kKeys = 128;                 // key positions per step
 constexpr int kTileRows = 128;             // query rows per tile
 constexpr int kFlush = 8;                  // steps O accumulates for fp32 outputs
-constexpr float kLag = 8.0f;               // how far (log2) scores may rise above m
+// How far (log2) a score may lie above m: P is a floating-point number and keeps
+// its relative precision, only 2^40 times its sums must not overflow.
+constexpr float kLag = 40.0f;
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D, int NT>
@@ -66,16 +68,19 @@ struct Layout {
     static constexpr int Q = 0;
     static constexpr int Ring = NT * Tile;
     static constexpr int Bar = Ring + Stages * Tile;
-    // barriers: full, empty [Stages], Q, S full [2], P full [2], PV done [2], scan joint, scan alone [2], drain
-    static constexpr int bEmpty = Stages, bQ = 2 * Stages, bS = bQ + 1, bP = bS + 2, bPV = bP + 2, bJoint = bPV + 2,
-                         bAlone = bJoint + 1, bDrain = bAlone + 2, kBars = bDrain + 1;
-    static constexpr int Bad = Bar + (kBars + 1) / 2 * 16;             // keys with values that are not finite [3][4] words
-    static constexpr int Misc = Bad + 3 * 16;               // tensor memory base, abort word
-    static constexpr int Bytes = Misc + 16;
+    // barriers: full, empty [Stages], Q, S full [2], P full [2], PV done [2], scan [2], drain
+    static constexpr int bEmpty = Stages, bQ = 2 * Stages, bS = bQ + 1, bP = bS + 2, bPV = bP + 2, bScan = bPV + 2,
+                         bDrain = bScan + 2, kBars = bDrain + 1;
+    static constexpr int Bad = Bar + (kBars + 1) / 2 * 16;  // keys with values that are not finite [4][4] words
+    static constexpr int Misc = Bad + 4 * 16;               // tensor memory base, abort word
+    static constexpr int Xch = Misc + 16;                   // exchange between the threads of a row [NT][128]
+    static constexpr int Bytes = Xch + NT * 128 * 4;
     static constexpr int Alloc = Bytes + 1024;              // slack to align the base to 1024 B
-    // with two tiles the other warps fill a warpgroup, which hands registers over:
-    // 384 threads of 168 become 256 of 208 and 128 of 88
-    static constexpr int Threads = NT == 2 ? 384 : 192;
+    // softmax warps, then a warpgroup with the products' and the loads' warps. With
+    // two tiles it hands registers over: 640 threads of 96 become 512 of 104 and
+    // 128 of 64
+    static constexpr int Warps = NT * 8;
+    static constexpr int Threads = Warps * 32 + 128;
     // tensor memory columns: S (P over it) of both tiles or buffers, then O
     static constexpr int kO = 256;
     static constexpr int Cols = 512;
@@ -85,31 +90,52 @@ struct Layout {
 
 struct Maps {
     CUtensorMap q, k, v;      // [rows][heads][D] bf16, boxes 64 x G x TM and 64 x 1 x 128
+    CUtensorMap kc, vc;       // [B][Lmax][Hkv][D] bf16, boxes 64 x 1 x 128 x 1
 };
 
 struct Args {
     const int32_t* cu;        // prompts: [B + 1] first rows; prefix: [1] its length
-    int B;
+    const int32_t* len;       // prefix: [B] cached positions behind it
+    int B, T;
     int M;                    // qkv rows
     int G, TM;                // query heads per key/value head, tokens per tile
     int Hkv, Hq;
     int k_head, v_head;       // head index of key/value head 0 in the k and v maps
-    int P;                    // prefix: positions there is room for
-    int blocks;               // prompts: groups of NT tiles; prefix: the same
-    int splits;               // prefix: parts its positions are cut into
+    int P, Lmax;              // prefix, caches: positions there is room for
+    int blocks;               // groups of NT tiles
+    int splits, own_splits;   // parts the prefix and a cache are cut into
     float c;                  // scale * log2 e
     void* out;                // prompts: [M][Hq * D]
-    float* part_o;            // prefix: [splits][M][Hq][D]
-    float2* part_ml;          // prefix: [splits][M][Hq] (m, l)
+    float* part_o;            // prefix: [parts][M][Hq][D]
+    float2* part_ml;          // prefix: [parts][M][Hq] (m, l)
     int hold;                 // test hook: request no load
     unsigned long long wait_ns;
 };
 
-__device__ __forceinline__ void umma_bf16_ss(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t id,
-                                             uint32_t accumulate) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                 :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(id), "r"(accumulate) : "memory");
+// One K = 16 step of D[tmem] (+)= A B^T, A from shared memory or from tensor
+// memory. The whole warp calls, one lane (`lead`) issues: control flow and
+// descriptors stay uniform, which a branch on the lane would not leave them.
+__device__ __forceinline__ void umma_ss(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t id,
+                                        uint32_t accumulate) {
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+                 :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(id), "r"(accumulate), "r"(lead) : "memory");
+}
+__device__ __forceinline__ void umma_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t id,
+                                        uint32_t accumulate) {
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 :: "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(id), "r"(accumulate), "r"(lead) : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t lead, uint64_t* bar) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+                 :: "r"(smem_u32(bar)), "r"(lead) : "memory");
+}
+__device__ __forceinline__ uint32_t elect_lane() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p;
 }
 // Instruction descriptor of kind::f16 with bf16 operands, M = 128, f32
 // accumulator; b_mn: B stored N-major.
@@ -136,7 +162,20 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
                  :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(head), "r"(row), "r"(smem_u32(bar))
                  : "memory");
 }
-__device__ __forceinline__ void tmem_st_x16(uint32_t taddr, const uint32_t (&v)[16]) {
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int x, int head, int pos, int seq,
+                                            uint64_t* bar) {
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+                 " [%0], [%1, {%2, %3, %4, %5}], [%6];"
+                 :: "r"(dst), "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(head), "r"(pos), "r"(seq),
+                    "r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+                 :: "r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st(uint32_t taddr, const uint32_t (&v)[16]) {
     asm volatile("tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
                  "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
                  :: "r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
@@ -153,6 +192,37 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+__device__ __forceinline__ uint64_t pair(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+// Two binary32 operations in one instruction.
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// Barrier `id` of 64 threads (two whole warps); whether any of them has p.
+__device__ __forceinline__ bool pair_or(int id, bool p) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred.aligned q, %2, 64, p;\n\t"
+                 "selp.u32 %0, 1, 0, q;\n\t}" : "=r"(r) : "r"((uint32_t)p), "r"(id) : "memory");
+    return r != 0;
 }
 __device__ __forceinline__ float neg_inf() { return __uint_as_float(0xFF800000u); }
 
@@ -208,9 +278,11 @@ __device__ __forceinline__ int sequence_start(const int32_t* __restrict__ cu, in
     return min(max(start, 0), tok);
 }
 
-// What a CTA does: tiles' first tokens and the key positions they run over.
+// What a CTA does: the tiles' first tokens and the key positions they run over.
 struct Item {
-    int kh, t0, split;
+    int kh, t0;
+    int seq;                  // prefix: the sequence whose cache this is, or -1 for the prefix itself
+    int part;                 // prefix: the index of the partial results
     int first, end;           // tokens [first, end) are rows to compute
     int k0, k1;               // prefix: the part's positions; prompts: k0 only
     int nt[2];                // steps of each tile
@@ -222,22 +294,35 @@ __device__ __forceinline__ Item item_of(const Args& a, int item) {
     Item it;
     it.kh = item % a.Hkv;
     item /= a.Hkv;
-    const int blk = item % a.blocks;
-    it.split = item / a.blocks;
-    // prompts: the last rows, which see most, first
-    it.t0 = (PREFIX ? blk : a.blocks - 1 - blk) * (NT * a.TM);
+    it.seq = -1;
     it.nt[0] = it.nt[1] = 0;
     if (PREFIX) {
+        int len, parts, at;
+        if (item < a.blocks * a.splits) {
+            it.t0 = item % a.blocks * (NT * a.TM);
+            it.end = min(it.t0 + NT * a.TM, a.M);
+            it.part = at = item / a.blocks;
+            len = min(max(a.cu[0], 0), a.P);
+            parts = a.splits;
+        } else {
+            item -= a.blocks * a.splits;
+            it.seq = item % a.B;
+            it.t0 = it.seq * a.T;
+            it.end = it.t0 + a.T;
+            at = item / a.B;
+            it.part = a.splits + at;
+            len = min(max(a.len[it.seq], 0), a.Lmax);
+            parts = a.own_splits;
+        }
         it.first = it.t0;
-        it.end = min(it.t0 + NT * a.TM, a.M);
-        const int len = min(max(a.cu[0], 0), a.P);
-        const int tiles = (len + kKeys - 1) / kKeys, per = (tiles + a.splits - 1) / a.splits;
-        it.k0 = min(it.split * per, tiles) * kKeys;
+        const int tiles = (len + kKeys - 1) / kKeys, per = (tiles + parts - 1) / parts;
+        it.k0 = min(at * per, tiles) * kKeys;
         it.k1 = min(len, it.k0 + per * kKeys);
-        const int n = it.k1 > it.k0 ? (it.k1 - it.k0 + kKeys - 1) / kKeys : 0;
-        it.nt[0] = n;
-        if (NT == 2) it.nt[1] = it.t0 + a.TM < a.M ? n : 0;
+        it.nt[0] = it.k1 > it.k0 ? (it.k1 - it.k0 + kKeys - 1) / kKeys : 0;
+        if (NT == 2) it.nt[1] = it.t0 + a.TM < it.end ? it.nt[0] : 0;
     } else {
+        it.part = 0;
+        it.t0 = (a.blocks - 1 - item) * (NT * a.TM);          // the last rows, which see most, first
         const int c0 = min(max(a.cu[0], 0), a.M), cB = min(max(a.cu[a.B], 0), a.M);
         it.first = max(it.t0, c0);
         it.end = min(it.t0 + NT * a.TM, cB);
@@ -266,7 +351,7 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
     uint32_t* bad = reinterpret_cast<uint32_t*>(smem + Ly::Bad);
     uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(smem + Ly::Misc);
     volatile int* abort = reinterpret_cast<volatile int*>(smem + Ly::Misc + 4);
-    constexpr int kMmaWarp = NT * 4, kLoadWarp = kMmaWarp + 1;
+    constexpr int kMmaWarp = Ly::Warps, kLoadWarp = kMmaWarp + 1;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < Ly::Stages; ++s) {
@@ -276,13 +361,12 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
         mbar_init(&bar[Ly::bQ], 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar[Ly::bS + i], 1);
-            mbar_init(&bar[Ly::bP + i], 4);
+            mbar_init(&bar[Ly::bP + i], 8);
             mbar_init(&bar[Ly::bPV + i], 1);
-            mbar_init(&bar[Ly::bAlone + i], 4);
+            mbar_init(&bar[Ly::bScan + i], 8);
         }
-        mbar_init(&bar[Ly::bJoint], 8);
         mbar_init(&bar[Ly::bDrain], 1);
-        for (int i = 0; i < 12; ++i) bad[i] = 0;
+        for (int i = 0; i < 16; ++i) bad[i] = 0;
         *abort = 0;
         fence_barrier_init();
     }
@@ -300,13 +384,13 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
     const int nmax = NT == 2 ? max(it.nt[0], it.nt[1]) : it.nt[0];
 
     if (warp >= kMmaWarp) {
-    if (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
     if (warp == kLoadWarp) {
         // -------------------------------------------------------------- loads
         if (lane == 0 && nmax > 0 && !a.hold) {
             prefetch_tensormap(&maps.q);
-            prefetch_tensormap(&maps.k);
-            prefetch_tensormap(&maps.v);
+            prefetch_tensormap(PREFIX && it.seq >= 0 ? &maps.kc : &maps.k);
+            prefetch_tensormap(PREFIX && it.seq >= 0 ? &maps.vc : &maps.v);
             mbar_arrive_expect_tx(&bar[Ly::bQ], (unsigned)(NT * Ly::H * 128 * a.G * a.TM));
             for (int i = 0; i < NT; ++i)
                 for (int h = 0; h < Ly::H; ++h)
@@ -317,11 +401,16 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                 const int s = n % Ly::Stages, use = n / Ly::Stages;
                 if (use > 0 && !lane_wait(&bar[Ly::bEmpty + s], (use - 1) & 1, abort, a.wait_ns)) break;
                 mbar_arrive_expect_tx(&bar[s], Ly::Tile);
-                const CUtensorMap* m = n & 1 ? &maps.v : &maps.k;
-                const int head = (n & 1 ? a.v_head : a.k_head) + it.kh;
-                for (int h = 0; h < Ly::H; ++h)
-                    tma_load_3d(sbase + Ly::Ring + s * Ly::Tile + h * 16384, m, 64 * h, head, it.k0 + (n >> 1) * kKeys,
-                                &bar[s]);
+                const uint32_t dst = sbase + Ly::Ring + s * Ly::Tile;
+                const int pos = it.k0 + (n >> 1) * kKeys;
+                if (PREFIX && it.seq >= 0) {
+                    for (int h = 0; h < Ly::H; ++h)
+                        tma_load_4d(dst + h * 16384, n & 1 ? &maps.vc : &maps.kc, 64 * h, it.kh, pos, it.seq, &bar[s]);
+                } else {
+                    for (int h = 0; h < Ly::H; ++h)
+                        tma_load_3d(dst + h * 16384, n & 1 ? &maps.v : &maps.k, 64 * h, (n & 1 ? a.v_head : a.k_head) + it.kh,
+                                    pos, &bar[s]);
+                }
             }
             // no copy is in flight when the block ends
             const unsigned long long t0 = global_timer_ns();
@@ -333,14 +422,15 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
         }
     } else if (warp == kMmaWarp) {
         // ----------------------------------------------------------- products
-        if (lane == 0 && nmax > 0) {
+        if (nmax > 0) {
+            const uint32_t lead = elect_lane();
             constexpr uint32_t id_s = idesc_bf16(kKeys, false), id_o = idesc_bf16(D, true);
-            auto full = [&](int load) { return lane_wait(&bar[load % Ly::Stages], (load / Ly::Stages) & 1, abort, a.wait_ns); };
+            auto full = [&](int load) { return warp_wait(&bar[load % Ly::Stages], (load / Ly::Stages) & 1, abort, a.wait_ns); };
             auto scores = [&](int i, int load, int col) {
                 const uint32_t q = sbase + Ly::Q + i * Ly::Tile, k = sbase + Ly::Ring + (load % Ly::Stages) * Ly::Tile;
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    umma_bf16_ss(tm + col, sw128_kmajor_desc(q + (kk >> 2) * 16384 + (kk & 3) * 32),
+                    umma_ss(lead, tm + col, sw128_kmajor_desc(q + (kk >> 2) * 16384 + (kk & 3) * 32),
                                  sw128_kmajor_desc(k + (kk >> 2) * 16384 + (kk & 3) * 32), id_s, kk > 0);
             };
             auto outputs = [&](int i, int load, int col, bool add) {
@@ -348,12 +438,12 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
 #pragma unroll
                 for (int part = 0; part < PARTS; ++part)
 #pragma unroll
-                    for (int kk = 0; kk < kKeys / 16; ++kk)
-                        umma_f16_ta(tm + Ly::kO + i * D, tm + col + part * 64 + kk * 8, v_desc(v + kk * 2048, 16384), id_o,
-                                    add || part > 0 || kk > 0);
+                    for (int kk = 0; kk < kKeys / 16; ++kk)  // each half of P lies over its half of S
+                        umma_ts(lead, tm + Ly::kO + i * D, tm + col + (kk >> 2) * 64 + part * 32 + (kk & 3) * 8,
+                                v_desc(v + kk * 2048, 16384), id_o, add || part > 0 || kk > 0);
             };
-            auto release = [&](int load) { umma_commit(&bar[Ly::bEmpty + load % Ly::Stages]); };
-            bool ok = lane_wait(&bar[Ly::bQ], 0, abort, a.wait_ns) && full(0);
+            auto release = [&](int load) { commit(lead, &bar[Ly::bEmpty + load % Ly::Stages]); };
+            bool ok = warp_wait(&bar[Ly::bQ], 0, abort, a.wait_ns) && full(0);
             tc_fence_after();
             if (NT == 2) {
                 if (ok) {
@@ -361,7 +451,7 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                     for (int i = 0; i < NT; ++i)
                         if (it.nt[i] > 0) {
                             scores(i, 0, i * 128);
-                            umma_commit(&bar[Ly::bS + i]);
+                            commit(lead, &bar[Ly::bS + i]);
                         }
                     release(0);
                 }
@@ -370,17 +460,17 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                     for (int i = 0; i < NT; ++i) {
                         if (!ok || n >= it.nt[i]) continue;
                         const bool last = i == 1 || n >= it.nt[1];       // the last tile to use values n
-                        ok = lane_wait(&bar[Ly::bP + i], n & 1, abort, a.wait_ns) && full(2 * n + 1);
+                        // (P last: it is what the next products wait for)
+                        ok = full(2 * n + 1) && (n + 1 >= it.nt[i] || full(2 * n + 2)) &&
+                             warp_wait(&bar[Ly::bP + i], n & 1, abort, a.wait_ns);
                         if (!ok) break;
                         tc_fence_after();
                         outputs(i, 2 * n + 1, i * 128, PARTS == 2 ? n % kFlush != 0 : n > 0);
-                        if (n == it.nt[i] - 1) umma_commit(&bar[Ly::bPV + i]);
+                        if (n == it.nt[i] - 1) commit(lead, &bar[Ly::bPV + i]);
                         if (last) release(2 * n + 1);
                         if (n + 1 < it.nt[i]) {
-                            ok = full(2 * n + 2);
-                            if (!ok) break;
                             scores(i, 2 * n + 2, i * 128);
-                            umma_commit(&bar[Ly::bS + i]);
+                            commit(lead, &bar[Ly::bS + i]);
                             if (i == 1 || n + 1 >= it.nt[1]) release(2 * n + 2);
                         }
                     }
@@ -388,7 +478,7 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
             } else {
                 if (ok) {
                     scores(0, 0, 0);
-                    umma_commit(&bar[Ly::bS]);
+                    commit(lead, &bar[Ly::bS]);
                     release(0);
                 }
                 for (int n = 0; ok && n < nmax; ++n) {
@@ -396,19 +486,20 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                         ok = full(2 * n + 2);
                         if (!ok) break;
                         scores(0, 2 * n + 2, ((n + 1) & 1) * 128);
-                        umma_commit(&bar[Ly::bS + ((n + 1) & 1)]);
+                        commit(lead, &bar[Ly::bS + ((n + 1) & 1)]);
                         release(2 * n + 2);
                     }
-                    ok = lane_wait(&bar[Ly::bP], n & 1, abort, a.wait_ns) && full(2 * n + 1);
+                    // (a barrier for each buffer: a warp may be a step ahead of another)
+                    ok = full(2 * n + 1) && warp_wait(&bar[Ly::bP + (n & 1)], (n >> 1) & 1, abort, a.wait_ns);
                     if (!ok) break;
                     tc_fence_after();
                     outputs(0, 2 * n + 1, (n & 1) * 128, PARTS == 2 ? n % kFlush != 0 : n > 0);
-                    umma_commit(&bar[Ly::bPV]);
+                    commit(lead, &bar[Ly::bPV]);
                     release(2 * n + 1);
                 }
             }
             // nothing reads operands or writes tensor memory when the block ends
-            umma_commit(&bar[Ly::bDrain]);
+            commit(lead, &bar[Ly::bDrain]);
             const unsigned long long t0 = global_timer_ns();
             while (!mbar_try_wait(&bar[Ly::bDrain], 0) && global_timer_ns() - t0 < kWaitLimitNs) {
             }
@@ -416,8 +507,11 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
     }
     } else {
         // ------------------------------------------------------------ softmax
-        if (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
-        const int i = NT == 2 ? warp >> 2 : 0, r = threadIdx.x & 127;
+        if (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
+        // two threads share a row: the halves of its scores, of its outputs
+        const int i = NT == 2 ? warp >> 3 : 0, half = (warp >> 2) & 1, r = threadIdx.x & 127;
+        const int pair_id = 1 + i * 4 + (warp & 3);          // the barrier of the two warps of these rows
+        float* xch = reinterpret_cast<float*>(smem + Ly::Xch) + i * 128 + r;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const int tile_t0 = it.t0 + i * a.TM;
         const int tok = tile_t0 + r / a.G, head = it.kh * a.G + r % a.G;
@@ -430,8 +524,8 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
             lo = all_lo = it.k0;
             hi = all_hi = it.k1 - 1;
         } else if (nmax > 0) {
-            lo = sequence_start(a.cu, a.B, min(max(tok, it.first), it.end - 1));
             hi = min(max(tok, it.first), it.end - 1);
+            lo = sequence_start(a.cu, a.B, hi);
             all_lo = sequence_start(a.cu, a.B, it.end - 1);
             all_hi = it.first;
         } else {
@@ -439,22 +533,24 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
             hi = all_hi = -1;
         }
         const size_t row = (size_t)tok * a.Hq + head;        // of the outputs
+        constexpr int DH = D / 2;                            // this thread's dims: half * DH ..
         float* acc = nullptr;                                // where the sums of fp32 outputs lie
         if (PREFIX)
-            acc = a.part_o + ((size_t)it.split * a.M * a.Hq + row) * D;
+            acc = a.part_o + ((size_t)it.part * a.M * a.Hq + row) * D + half * DH;
         else if (PARTS == 2)
-            acc = reinterpret_cast<float*>(a.out) + row * D;
-        const uint32_t o_col = tm + lanes + Ly::kO + i * D;
+            acc = reinterpret_cast<float*>(a.out) + row * D + half * DH;
+        const uint32_t o_col = tm + lanes + Ly::kO + i * D + half * DH;
 
-        float m = neg_inf(), m_acc = neg_inf(), l = 0.f;
+        float m = neg_inf(), m_acc = neg_inf(), l = 0.f;     // l: of this thread's half
+        // After a wait that ran out (ok false) a warp still joins the pair's
+        // barriers, which tell the other: both stop at the same one.
         bool ok = true;
-        int masked = 0;                                      // tiles scanned
-        unsigned joint = 0, alone = 0;
-        // O added to the sums: o 1 (and what was there times 2^(m_acc - m), unless it is the first)
+        unsigned scans = 0;                                  // tiles whose values were looked at
+        // O added to the sums (what was there times 2^(m_acc - m), unless it is the first time), times mul
         auto flush = [&](bool fresh, float mul) {
             const float f = m_acc == neg_inf() ? 0.f : ex2(m_acc - m);
 #pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += 32) {
+            for (int c0 = 0; c0 < DH; c0 += 32) {
                 uint32_t o[32];
                 tmem_ld<32>(o_col + c0, o);
                 tmem_ld_wait();
@@ -478,157 +574,176 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
 
         for (int n = 0; n < nt; ++n) {
             const int buf = NT == 2 ? i : n & 1;
-            ok = warp_wait(&bar[Ly::bS + buf], (NT == 2 ? n : n >> 1) & 1, abort, a.wait_ns);
-            if (!ok) break;
-            tc_fence_after();
-            const uint32_t s_col = tm + lanes + buf * 128;
-            uint32_t s[4][32];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) tmem_ld<32>(s_col + 32 * q, s[q]);
+            const uint32_t s_col = tm + lanes + buf * 128 + half * 64;
             const int kb = it.k0 + n * kKeys;
-            const bool part = kb < all_lo || kb + kKeys - 1 > all_hi;
-            tmem_ld_wait();
-            float poison = 0.f;
-            if (part) {
-                const int from = lo - kb, to = hi - kb;
+            const bool flushed = PARTS == 2 && n > 0 && n % kFlush == 0;
+            uint32_t s[2][32];
+            float poison = 0.f, top = neg_inf();
+            if (ok) ok = warp_wait(&bar[Ly::bS + buf], (NT == 2 ? n : n >> 1) & 1, abort, a.wait_ns);
+            if (ok) {
+                tc_fence_after();
+                tmem_ld<32>(s_col, s[0]);
+                tmem_ld<32>(s_col + 32, s[1]);
+                tmem_ld_wait();
+                if (kb < all_lo || kb + kKeys - 1 > all_hi) {
+                    const int from = lo - kb, to = hi - kb;
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
+                    for (int q = 0; q < 2; ++q) {
+                        // bits of the keys that are seen among these 32
+                        const int f0 = max(from - half * 64 - 32 * q, 0), t0 = min(to - half * 64 - 32 * q, 31);
+                        const uint32_t see = f0 <= t0 && f0 < 32 ? 0xFFFFFFFFu >> (31 - t0) >> f0 << f0 : 0u;
 #pragma unroll
-                    for (int j = 0; j < 32; ++j)
-                        if (32 * q + j < from || 32 * q + j > to) s[q][j] = 0xFF800000u;
-                // values that are not finite: 0 in shared memory, their keys noted
-                const int load = 2 * n + 1;
-                ok = warp_wait(&bar[load % Ly::Stages], (load / Ly::Stages) & 1, abort, a.wait_ns);
-                if (!ok) break;
-                const bool both = NT == 2 && n < other;
-                uint32_t* mark = bad + (masked % 3) * 4;
-                const uint32_t v = sbase + Ly::Ring + (load % Ly::Stages) * Ly::Tile;
-                const int step = both ? 256 : 128;
-                for (int e = both ? threadIdx.x : r; e < Ly::Tile / 16; e += step) {
-                    uint32_t w[4];
-                    lds_v4_u32(v + e * 16, w[0], w[1], w[2], w[3]);
-                    bool any = false;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint32_t h0 = w[j] & 0x7F80u, h1 = w[j] & 0x7F800000u;
-                        if (h0 == 0x7F80u) w[j] &= 0xFFFF0000u, any = true;
-                        if (h1 == 0x7F800000u) w[j] &= 0x0000FFFFu, any = true;
+                        for (int j = 0; j < 32; ++j)
+                            if (!(see >> j & 1u)) s[q][j] = 0xFF800000u;
                     }
-                    if (any) {
-                        const int key = (e >> 3) & 127;      // 8 chunks a row; the halves one behind the other
-                        sts_v4_u32(v + e * 16, w[0], w[1], w[2], w[3]);
-                        atomicOr(&mark[key >> 5], 1u << (key & 31));
+                    // values that are not finite: their keys noted, then 0 in shared memory. Both tiles'
+                    // warps may do so at the same time; marks come first, so that who finds a 0 finds the mark
+                    const int load = 2 * n + 1;
+                    ok = warp_wait(&bar[load % Ly::Stages], (load / Ly::Stages) & 1, abort, a.wait_ns);
+                    uint32_t* mark = bad + (n & 3) * 4;
+                    if (ok) {
+                        const uint32_t v = sbase + Ly::Ring + (load % Ly::Stages) * Ly::Tile;
+#pragma unroll 4
+                        for (int e = threadIdx.x & 255; e < Ly::Tile / 16; e += 256) {
+                            uint32_t w[4], inf = 0;
+                            lds_v4_u32(v + e * 16, w[0], w[1], w[2], w[3]);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) inf |= (w[j] & 0x7F807F80u) + 0x00800080u;   // carries out of all ones
+                            if (inf & 0x80008000u) {
+                                const int key = (e >> 3) & 127;      // 8 chunks a row; the halves one behind the other
+                                atomicOr(&mark[key >> 5], 1u << (key & 31));
+                                __threadfence_block();
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) {
+                                    if ((w[j] & 0x7F80u) == 0x7F80u) w[j] &= 0xFFFF0000u;
+                                    if ((w[j] & 0x7F800000u) == 0x7F800000u) w[j] &= 0x0000FFFFu;
+                                }
+                                sts_v4_u32(v + e * 16, w[0], w[1], w[2], w[3]);
+                            }
+                        }
+                        fence_proxy_async_smem();
+                        warp_arrive(&bar[Ly::bScan + i]);
+                        ok = warp_wait(&bar[Ly::bScan + i], scans & 1, abort, a.wait_ns);
+                        ++scans;
+                    }
+                    if (ok) {
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) {
+                            const uint32_t b = *reinterpret_cast<volatile uint32_t*>(mark + w);
+                            const int f0 = max(from - 32 * w, 0), t0 = min(to - 32 * w, 31);
+                            if (b != 0 && f0 <= t0 && (b >> f0 << f0 << (31 - t0)) != 0) poison = __uint_as_float(0x7FC00000u);
+                        }
                     }
                 }
-                fence_proxy_async_smem();
-                if (both) {
-                    warp_arrive(&bar[Ly::bJoint]);
-                    ok = warp_wait(&bar[Ly::bJoint], joint++ & 1, abort, a.wait_ns);
-                } else {
-                    warp_arrive(&bar[Ly::bAlone + i]);
-                    ok = warp_wait(&bar[Ly::bAlone + i], alone++ & 1, abort, a.wait_ns);
-                }
-                if (!ok) break;
-#pragma unroll
-                for (int w = 0; w < 4; ++w) {
-                    const uint32_t b = mark[w];
-                    if (b == 0) continue;
-                    // the row's keys among these 32
-                    const int f0 = max(from - 32 * w, 0), t0 = min(to - 32 * w, 31);
-                    if (f0 <= t0 && f0 < 32 && (b >> f0 << f0 << (31 - t0)) != 0) poison = __uint_as_float(0x7FC00000u);
-                }
-                // the marks of the tile after the next: the tiles' larger count of steps clears them
-                if (r == 0 && (nt > other || (nt == other && i == 0))) {
-                    uint32_t* next = bad + ((masked + 2) % 3) * 4;
-                    next[0] = next[1] = next[2] = next[3] = 0;
-                }
-                ++masked;
-            }
-            if (PARTS == 2 && n > 0 && n % kFlush == 0) {
-                if (NT == 1) {                               // with two tiles S's barrier stands for it
-                    ok = warp_wait(&bar[Ly::bPV], (n - 1) & 1, abort, a.wait_ns);
-                    if (!ok) break;
+                // the marks of the step after the next: no warp is that far, none still at the one before the last
+                if (half == 0 && r == 0 && (i == 0 || n >= other))
+                    *reinterpret_cast<uint4*>(bad + ((n + 2) & 3) * 4) = make_uint4(0u, 0u, 0u, 0u);
+                if (flushed && ok) {
+                    if (NT == 1) ok = warp_wait(&bar[Ly::bPV], (n - 1) & 1, abort, a.wait_ns);
                     tc_fence_after();
+                    if (ok) flush(n == kFlush, 1.f);
                 }
-                flush(n == kFlush, 1.f);
-            }
-
-            float mx0 = neg_inf(), mx1 = mx0, mx2 = mx0, mx3 = mx0;
+                float mx[4];
 #pragma unroll
-            for (int j = 0; j < 32; ++j) {
-                mx0 = fmaxf(mx0, __uint_as_float(s[0][j]));
-                mx1 = fmaxf(mx1, __uint_as_float(s[1][j]));
-                mx2 = fmaxf(mx2, __uint_as_float(s[2][j]));
-                mx3 = fmaxf(mx3, __uint_as_float(s[3][j]));
+                for (int q = 0; q < 4; ++q) mx[q] = neg_inf();
+#pragma unroll
+                for (int j = 0; j < 16; ++j)
+#pragma unroll
+                    for (int q = 0; q < 2; ++q)
+                        mx[2 * q + (j & 1)] = max3(mx[2 * q + (j & 1)], __uint_as_float(s[q][2 * j]),
+                                                   __uint_as_float(s[q][2 * j + 1]));
+                top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * a.c;
             }
-            const float top = fmaxf(fmaxf(mx0, mx1), fmaxf(mx2, mx3)) * a.c;
-            const bool move = top > m + kLag || (m == neg_inf() && top > m);
-            const float f = !move ? 1.f : (m == neg_inf() ? 0.f : ex2(m - top));
-            if (move) m = top;
-            l = l * f + poison;
-            if (__any_sync(0xffffffffu, move) && n > 0 && !(PARTS == 2 && n % kFlush == 0)) {
-                if (NT == 1) {
-                    ok = warp_wait(&bar[Ly::bPV], (n - 1) & 1, abort, a.wait_ns);
-                    if (!ok) break;
-                    tc_fence_after();
+            if (pair_or(pair_id, !ok || top > m + kLag || (m == neg_inf() && top > m))) {
+                // the row's maximum; a warp that has stopped says so to the other
+                if (half == 1) *xch = top;
+                if (pair_or(pair_id, !ok)) {
+                    ok = false;
+                    break;
                 }
+                if (half == 0) *xch = fmaxf(top, *xch);
+                pair_or(pair_id, false);
+                const float all = *xch;
+                const bool move = all > m + kLag || (m == neg_inf() && all > m);
+                const float f = !move ? 1.f : (m == neg_inf() ? 0.f : ex2(m - all));
+                if (move) m = all;
+                l *= f;
+                if (n > 0 && !flushed) {
+                    if (NT == 1) ok = warp_wait(&bar[Ly::bPV], (n - 1) & 1, abort, a.wait_ns);
+                    tc_fence_after();
+                    if (ok) {
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 32) {
-                    uint32_t o[32];
-                    tmem_ld<32>(o_col + c0, o);
-                    tmem_ld_wait();
+                        for (int c0 = 0; c0 < DH; c0 += 16) {
+                            uint32_t o[16];
+                            tmem_ld<16>(o_col + c0, o);
+                            tmem_ld_wait();
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                    tmem_st_x32(o_col + c0, o);
+                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                            tmem_st(o_col + c0, o);
+                        }
+                    }
                 }
             }
+            if (!ok) continue;
             const float ms = m == neg_inf() ? 0.f : m;       // a row that has seen no key yet
-            float l0 = 0.f, l1 = 0.f;
+            const uint64_t c2 = pair(a.c, a.c), m2 = pair(-ms, -ms);
+            uint64_t l2 = pair(poison, 0.f), l3 = pair(0.f, 0.f);
+            constexpr int CH = PARTS == 2 ? 8 : 16;          // pairs stored at once
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint32_t hi2[16];
-                uint32_t lo2[PARTS == 2 ? 16 : 1];
+            for (int q = 0; q < 32 / CH; ++q) {
+                uint32_t hi2[CH], lo2[CH];
 #pragma unroll
-                for (int j = 0; j < 16; ++j) {
-                    const float p0 = ex2(fmaf(__uint_as_float(s[q][2 * j]), a.c, -ms));
-                    const float p1 = ex2(fmaf(__uint_as_float(s[q][2 * j + 1]), a.c, -ms));
+                for (int j = 0; j < CH; ++j) {
+                    const int at = q * CH + j;
+                    float p0, p1;
+                    unpair(fma2(pair(__uint_as_float(s[at >> 4][2 * (at & 15)]), __uint_as_float(s[at >> 4][2 * (at & 15) + 1])),
+                                c2, m2), p0, p1);
+                    p0 = ex2(p0);
+                    p1 = ex2(p1);
                     hi2[j] = pack2(p0, p1);
+                    uint64_t p = pair(p0, p1);
                     if (PARTS == 2) {
                         // the sum takes what the product takes
                         const float h0 = __uint_as_float(hi2[j] << 16), h1 = __uint_as_float(hi2[j] & 0xFFFF0000u);
                         lo2[j] = pack2(p0 - h0, p1 - h1);
-                        l0 += h0 + __uint_as_float(lo2[j] << 16);
-                        l1 += h1 + __uint_as_float(lo2[j] & 0xFFFF0000u);
-                    } else {
-                        l0 += p0;
-                        l1 += p1;
+                        p = add2(pair(h0, h1), pair(__uint_as_float(lo2[j] << 16), __uint_as_float(lo2[j] & 0xFFFF0000u)));
                     }
+                    if (j & 1) l3 = add2(l3, p); else l2 = add2(l2, p);
                 }
-                tmem_st_x16(s_col + 16 * q, hi2);
-                if constexpr (PARTS == 2) tmem_st_x16(s_col + 64 + 16 * q, lo2);
+                tmem_st(s_col + CH * q, hi2);
+                if constexpr (PARTS == 2) tmem_st(s_col + 32 + CH * q, lo2);
             }
-            l += l0 + l1;
+            float x0, x1;
+            unpair(add2(l2, l3), x0, x1);
+            l += x0 + x1;
             tmem_st_wait();
             tc_fence_before();
-            warp_arrive(&bar[Ly::bP + i]);
+            warp_arrive(&bar[Ly::bP + buf]);
         }
 
         // ------------------------------------------------------------ outputs
-        if (ok && nt > 0) {
-            // (one tile: its last product but one may not have completed either)
-            if (NT == 1 && nt > 1) ok = warp_wait(&bar[Ly::bPV], nt & 1, abort, a.wait_ns);
-            ok = ok && warp_wait(&bar[Ly::bPV + i], NT == 2 ? 0 : (nt - 1) & 1, abort, a.wait_ns);
+        if (nt > 0) {
+            if (ok) {
+                // (one tile: its last product but one may not have completed either)
+                if (NT == 1 && nt > 1) ok = warp_wait(&bar[Ly::bPV], nt & 1, abort, a.wait_ns);
+                ok = ok && warp_wait(&bar[Ly::bPV + i], NT == 2 ? 0 : (nt - 1) & 1, abort, a.wait_ns);
+            }
             tc_fence_after();
+            if (half == 1) *xch = l;
+            if (pair_or(pair_id, !ok)) ok = false;
+            if (half == 0) *xch += l;
+            pair_or(pair_id, false);
+            l = *xch;
         }
         if (ok && nt > 0) {
             const float inv = PREFIX ? 1.f : 1.f / l;
             if (PREFIX || PARTS == 2) {
                 flush(PARTS == 1 || nt <= kFlush, inv);
-                if (PREFIX && valid) a.part_ml[(size_t)it.split * a.M * a.Hq + row] = make_float2(m, l);
+                if (PREFIX && valid && half == 0) a.part_ml[(size_t)it.part * a.M * a.Hq + row] = make_float2(m, l);
             } else {
-                uint4* p = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + row * D);
+                uint4* p = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + row * D + half * DH);
 #pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 32) {
+                for (int c0 = 0; c0 < DH; c0 += 32) {
                     uint32_t o[32];
                     tmem_ld<32>(o_col + c0, o);
                     tmem_ld_wait();
@@ -646,8 +761,8 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                     __syncwarp();
                 }
             }
-        } else if (PREFIX && valid && nt == 0) {
-            a.part_ml[(size_t)it.split * a.M * a.Hq + row] = make_float2(neg_inf(), 0.f);
+        } else if (PREFIX && valid && nt == 0 && half == 0) {
+            a.part_ml[(size_t)it.part * a.M * a.Hq + row] = make_float2(neg_inf(), 0.f);
         }
         tc_fence_before();
     }
@@ -656,6 +771,144 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
         tc_fence_after();
         tmem_dealloc(tm, Ly::Cols);
     }
+}
+
+// The parts' results over the prefix and the caches, and the step's own keys, of
+// which there are few: a warp takes a query head of a token, each lane D / 32
+// values of it; own scores and products in binary32.
+constexpr int kMergeThreads = 256;
+struct MergeArgs {
+    const uint16_t* qkv;
+    const float* part_o;
+    const float2* part_ml;
+    int parts, rows;          // rows: B * T * Hq
+    int T, Hq, Hkv;
+    float c;
+    void* out;
+    int out_bf16;
+};
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const MergeArgs a) {
+    constexpr int N = D / 32;                                 // values of a lane
+    constexpr int kOwn = kTileRows / 32;                      // own scores of a lane: up to 128 tokens
+    constexpr int kParts = 2 * kPrefixMaxSplits / 32;
+    const int w = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+    allow_dependent_launch();
+    grid_dependency_wait();
+    if (w >= a.rows) return;
+    const int tok = w / a.Hq, head = w - tok * a.Hq, first = tok / a.T * a.T, own = tok - first + 1;
+    const size_t W = (size_t)(a.Hq + 2 * a.Hkv) * D;
+    const uint16_t* key = a.qkv + (size_t)first * W + (size_t)(a.Hq + head / (a.Hq / a.Hkv)) * D + lane * N;
+    const uint16_t* val = key + (size_t)a.Hkv * D;
+    auto load = [&](const uint16_t* p, float (&x)[N]) {
+        uint32_t v[N / 2];
+        if constexpr (N == 4) {
+            const uint2 t = *reinterpret_cast<const uint2*>(p);
+            v[0] = t.x;
+            v[1] = t.y;
+        } else {
+            v[0] = *reinterpret_cast<const uint32_t*>(p);
+        }
+#pragma unroll
+        for (int j = 0; j < N / 2; ++j) {
+            x[2 * j] = __uint_as_float(v[j] << 16);
+            x[2 * j + 1] = __uint_as_float(v[j] & 0xFFFF0000u);
+        }
+    };
+    float q[N], top = neg_inf();
+    load(a.qkv + (size_t)tok * W + (size_t)head * D + lane * N, q);
+    float2 ml[kParts];
+#pragma unroll
+    for (int u = 0; u < kParts; ++u) {
+        ml[u] = make_float2(neg_inf(), 0.f);
+        if (u * 32 + lane < a.parts) ml[u] = a.part_ml[(size_t)(u * 32 + lane) * a.rows + w];
+        top = fmaxf(top, ml[u].x);
+    }
+    float s[kOwn];
+#pragma unroll
+    for (int u = 0; u < kOwn; ++u) {
+        s[u] = neg_inf();
+        for (int j = 32 * u; j < min(own, 32 * u + 32); ++j) {
+            float k[N], d = 0.f;
+            load(key + (size_t)j * W, k);
+#pragma unroll
+            for (int x = 0; x < N; ++x) d += q[x] * k[x];
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+            if (j - 32 * u == lane) s[u] = d * a.c;
+        }
+        top = fmaxf(top, s[u]);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (top == neg_inf()) top = 0.f;
+    float o[N], l = 0.f;
+#pragma unroll
+    for (int x = 0; x < N; ++x) o[x] = 0.f;
+#pragma unroll
+    for (int u = 0; u < kParts; ++u) {
+        if (32 * u >= a.parts) break;
+        const bool none = ml[u].x == neg_inf() && ml[u].y == 0.f;   // no position, nothing written
+        const float f = none ? 0.f : ex2(ml[u].x - top);
+        l += f * ml[u].y;
+        const unsigned there = __ballot_sync(0xffffffffu, !none && 32 * u + lane < a.parts);
+#pragma unroll 4
+        for (int j = 0; j < min(a.parts - 32 * u, 32); ++j) {
+            const float g = __shfl_sync(0xffffffffu, f, j);
+            if (!(there >> j & 1u)) continue;
+            const float* p = a.part_o + ((size_t)(32 * u + j) * a.rows + w) * D + lane * N;
+            if constexpr (N == 4) {
+                const float4 v = *reinterpret_cast<const float4*>(p);
+                o[0] += g * v.x;
+                o[1] += g * v.y;
+                o[2] += g * v.z;
+                o[3] += g * v.w;
+            } else {
+                const float2 v = *reinterpret_cast<const float2*>(p);
+                o[0] += g * v.x;
+                o[1] += g * v.y;
+            }
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < kOwn; ++u) {
+        if (32 * u >= own) break;
+        const float f = 32 * u + lane < own ? ex2(s[u] - top) : 0.f;
+        l += f;
+        for (int j = 32 * u; j < min(own, 32 * u + 32); ++j) {
+            const float g = __shfl_sync(0xffffffffu, f, j - 32 * u);
+            float v[N];
+            load(val + (size_t)j * W, v);
+#pragma unroll
+            for (int x = 0; x < N; ++x) o[x] += g * v[x];
+        }
+    }
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+    const float inv = 1.f / l;
+    if (a.out_bf16) {
+        uint32_t* p = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + (size_t)w * D + lane * N);
+#pragma unroll
+        for (int x = 0; x < N / 2; ++x) p[x] = pack2(o[2 * x] * inv, o[2 * x + 1] * inv);
+    } else {
+        float* p = static_cast<float*>(a.out) + (size_t)w * D + lane * N;
+#pragma unroll
+        for (int x = 0; x < N; ++x) p[x] = o[x] * inv;
+    }
+}
+
+template <int D>
+cudaError_t launch_merge(const MergeArgs& a, cudaStream_t s) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(ceil_div(a.rows, kMergeThreads / 32));
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, prefix_merge_kernel<D>, a);
 }
 
 template <int D, int NT, int PARTS, bool PREFIX>
@@ -700,7 +953,7 @@ cudaError_t launch_attention_prompt(const CUtensorMap& q, const CUtensorMap& kv,
                                     unsigned long long wait_ns, cudaStream_t s) {
     Maps maps;
     maps.q = q;
-    maps.k = maps.v = kv;
+    maps.k = maps.v = maps.kc = maps.vc = kv;
     Args a = {};
     a.cu = cu; a.B = B; a.M = M;
     a.G = Hq / Hkv; a.TM = attention_prompt_tokens(a.G);
@@ -714,47 +967,57 @@ cudaError_t launch_attention_prompt(const CUtensorMap& q, const CUtensorMap& kv,
     return dispatch<false>(maps, a, D, nt, out_bf16 ? 1 : 2, a.blocks * Hkv, s);
 }
 
-// The cut of a prefix of P positions under M rows: enough parts that every SM
-// has one, of at least 4 steps where that leaves enough.
-static void prefix_cut(int M, int Hq, int Hkv, int P, int sms, int* nt, int* blocks, int* splits) {
-    const int TM = attention_prompt_tokens(Hq / Hkv), tiles = ceil_div(M, TM);
-    *nt = tiles >= 2 ? 2 : 1;
-    *blocks = ceil_div(tiles, *nt);
-    const long long items = (long long)*blocks * Hkv;
-    const int steps = ceil_div(P, kKeys);
-    long long n = items >= sms ? 1 : sms / items;
-    if (n > kPrefixMaxSplits) n = kPrefixMaxSplits;
-    if (n > steps) n = steps;
-    *splits = n < 1 ? 1 : (int)n;
+// How the work of a batch behind a prefix is cut: enough parts of the prefix
+// that every SM has one, and of each cache where the sequences alone leave SMs idle.
+struct PrefixCut {
+    int nt, blocks, splits, own_max;
+};
+static PrefixCut prefix_cut(int B, int T, int Hq, int Hkv, int P, int sms) {
+    PrefixCut c;
+    const int M = B * T, TM = attention_prompt_tokens(Hq / Hkv), tiles = ceil_div(M, TM);
+    c.nt = tiles >= 2 ? 2 : 1;
+    c.blocks = ceil_div(tiles, c.nt);
+    const long long items = (long long)c.blocks * Hkv, own = (long long)B * Hkv;
+    auto clamp = [](long long n, long long hi) { return (int)(n < 1 ? 1 : n > hi ? hi : n); };
+    c.splits = clamp(sms / items, P < kKeys * kPrefixMaxSplits ? ceil_div(P, kKeys) : kPrefixMaxSplits);
+    c.own_max = clamp(sms / own, kPrefixMaxSplits);
+    return c;
 }
 
-size_t attention_prefix_workspace_bytes(int M, int Hq, int Hkv, int D, int P, int sms) {
-    int nt, blocks, splits;
-    prefix_cut(M, Hq, Hkv, P, sms, &nt, &blocks, &splits);
-    return (size_t)splits * M * Hq * (D * sizeof(float) + sizeof(float2));
+size_t attention_prefix_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int P, int sms) {
+    const PrefixCut c = prefix_cut(B, T, Hq, Hkv, P, sms);
+    return (size_t)(c.splits + c.own_max) * B * T * Hq * (D * sizeof(float) + sizeof(float2));
 }
 
-cudaError_t launch_attention_prefix(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const int32_t* len,
-                                    int M, int Hq, int Hkv, int D, int P, float scale, bool exact, void* ws, int sms,
-                                    int hold, unsigned long long wait_ns, PrefixParts* parts, cudaStream_t s) {
+cudaError_t launch_attention_prefix(const PrefixCall& c, int sms, int hold, unsigned long long wait_ns, cudaStream_t s) {
+    const PrefixCut cut = prefix_cut(c.B, c.T, c.Hq, c.Hkv, c.P, sms);
     Maps maps;
-    maps.q = q;
-    maps.k = k;
-    maps.v = v;
+    maps.q = c.q;
+    maps.k = c.pk;
+    maps.v = c.pv;
+    maps.kc = c.kc;
+    maps.vc = c.vc;
     Args a = {};
-    a.cu = len; a.B = 0; a.M = M;
-    a.G = Hq / Hkv; a.TM = attention_prompt_tokens(a.G);
-    a.Hkv = Hkv; a.Hq = Hq; a.P = P;
-    a.c = scale * kLog2e;
+    a.cu = c.prefix_len; a.len = c.cache_len;
+    a.B = c.B; a.T = c.T; a.M = c.B * c.T;
+    a.G = c.Hq / c.Hkv; a.TM = attention_prompt_tokens(a.G);
+    a.Hkv = c.Hkv; a.Hq = c.Hq; a.P = c.P; a.Lmax = c.Lmax;
+    a.blocks = cut.blocks; a.splits = cut.splits;
+    const int steps = ceil_div(c.Lmax, kKeys);
+    a.own_splits = steps < cut.own_max ? steps : cut.own_max;
+    a.c = c.scale * kLog2e;
     a.hold = hold; a.wait_ns = wait_ns ? wait_ns : kWaitLimitNs;
-    int nt;
-    prefix_cut(M, Hq, Hkv, P, sms, &nt, &a.blocks, &a.splits);
-    a.part_o = static_cast<float*>(ws);
-    a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)a.splits * M * Hq * D);
-    parts->o = a.part_o;
-    parts->ml = reinterpret_cast<const float*>(a.part_ml);
-    parts->splits = a.splits;
-    return dispatch<true>(maps, a, D, nt, exact ? 2 : 1, a.blocks * Hkv * a.splits, s);
+    a.part_o = static_cast<float*>(c.ws);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + (size_t)(a.splits + a.own_splits) * a.M * a.Hq * c.D);
+    const long long grid = ((long long)a.blocks * a.splits + (long long)c.B * a.own_splits) * c.Hkv;
+    cudaError_t e = dispatch<true>(maps, a, c.D, cut.nt, c.out_bf16 ? 1 : 2, (int)grid, s);
+    if (e != cudaSuccess) return e;
+    MergeArgs m;
+    m.qkv = c.qkv; m.part_o = a.part_o; m.part_ml = a.part_ml;
+    m.parts = a.splits + a.own_splits; m.rows = a.M * c.Hq;
+    m.T = c.T; m.Hq = c.Hq; m.Hkv = c.Hkv;
+    m.c = a.c; m.out = c.out; m.out_bf16 = c.out_bf16 ? 1 : 0;
+    return c.D == 128 ? launch_merge<128>(m, s) : launch_merge<64>(m, s);
 }
 
 cudaError_t read_and_clear_attn_prompt_error(unsigned* code) {

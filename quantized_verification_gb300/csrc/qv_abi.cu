@@ -148,16 +148,6 @@ qv_status encode_heads(CUtensorMap* map, const void* base, int rows, int heads, 
     return QV_OK;
 }
 
-// The four maps of qv_attention_verify's caches (none when Lmax == 0).
-qv_status encode_cache_maps(qv::KvMaps* maps, const void* k, const void* v, int B, int Lmax, int Hkv, int D) {
-    if (Lmax == 0) return QV_OK;
-    qv_status st = encode_kv_cache(&maps->k64, k, B, Lmax, Hkv, D, 64);
-    if (st == QV_OK) st = encode_kv_cache(&maps->v64, v, B, Lmax, Hkv, D, 64);
-    if (st == QV_OK) st = encode_kv_cache(&maps->k16, k, B, Lmax, Hkv, D, 16);
-    if (st == QV_OK) st = encode_kv_cache(&maps->v16, v, B, Lmax, Hkv, D, 16);
-    return st;
-}
-
 // W8A8 streaming GEMM kernel by padded token count. Up to 16 tokens the
 // int8 (8) or f16 (16) mma.sync kernel keeps pace with HBM; from 32 tokens
 // mma.sync is latency- or compute-bound and the tcgen05 kernel (exact f16
@@ -688,10 +678,16 @@ qv_status qv_attention_verify(const uint16_t* qkv, const uint16_t* k_cache, cons
     QV_CHECK_DEV(cache_len);
     QV_CHECK_DEV(out);
     qv::KvMaps maps;
-    if ((st = encode_cache_maps(&maps, k_cache, v_cache, B, Lmax, Hkv, D)) != QV_OK) return st;
+    if (Lmax > 0) {
+        st = encode_kv_cache(&maps.k64, k_cache, B, Lmax, Hkv, D, 64);
+        if (st == QV_OK) st = encode_kv_cache(&maps.v64, v_cache, B, Lmax, Hkv, D, 64);
+        if (st == QV_OK) st = encode_kv_cache(&maps.k16, k_cache, B, Lmax, Hkv, D, 16);
+        if (st == QV_OK) st = encode_kv_cache(&maps.v16, v_cache, B, Lmax, Hkv, D, 16);
+        if (st != QV_OK) return st;
+    }
     const int hold = qv::debug_take_hold_attention() ? 1 : 0;
     cudaError_t e = qv::launch_attention_verify(qkv, Lmax > 0 ? &maps : nullptr, cache_len, B, T, Hq, Hkv, D, Lmax,
-                                                scale, out, hold, qv::debug_slot_wait_ns(), nullptr, false, stream);
+                                                scale, out, hold, qv::debug_slot_wait_ns(), stream);
     if (e != cudaSuccess) return cuda_fail(e, "qv_attention_verify launch");
     return ok();
 }
@@ -890,23 +886,30 @@ qv_status qv_attention_prompt(const uint16_t* qkv, const int32_t* cu_rows, int B
 }
 
 namespace {
-qv_status check_attention_prefix_shape(int B, int T, int Hq, int Hkv, int D, int P) {
-    qv_status st = check_attention_shape(B, T, Hq, Hkv, D, 0);
-    if (st != QV_OK) return st;
+qv_status check_attention_prefix_shape(int B, int T, int Hq, int Hkv, int D, int P, int Lmax) {
+    if (B < 1 || B > 65535) return fail(QV_ERR_INVALID_ARG, "B=%d outside [1, 65535]", B);
+    if (T < 1) return fail(QV_ERR_INVALID_ARG, "T=%d must be >= 1", T);
+    if (Hkv < 1 || Hkv > 65535 || Hq < Hkv || Hq > 65535 || Hq % Hkv != 0)
+        return fail(QV_ERR_INVALID_ARG, "Hq=%d must be a positive multiple of Hkv=%d and <= 65535", Hq, Hkv);
+    if ((long long)T * (Hq / Hkv) > kPromptMaxGroup)
+        return fail(QV_ERR_INVALID_ARG, "T * Hq / Hkv must be <= %d", kPromptMaxGroup);
+    if (D != 64 && D != 128) return fail(QV_ERR_INVALID_ARG, "D=%d must be 64 or 128", D);
     if (P < 1 || P > (1 << 24)) return fail(QV_ERR_INVALID_ARG, "P=%d outside [1, 2^24]", P);
+    if (Lmax < 0 || Lmax > (1 << 24)) return fail(QV_ERR_INVALID_ARG, "Lmax=%d outside [0, 2^24]", Lmax);
+    if ((long long)B * T * Hq > (1 << 27)) return fail(QV_ERR_UNSUPPORTED, "B * T * Hq is too large for one call");
     return QV_OK;
 }
 }  // namespace
 
 size_t qv_attention_prefix_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int P) {
-    if (check_attention_prefix_shape(B, T, Hq, Hkv, D, P) != QV_OK) return 0;
+    if (check_attention_prefix_shape(B, T, Hq, Hkv, D, P, 0) != QV_OK) return 0;
     cudaError_t e;
     const int sms = sms_of_current_device(&e);
     if (e != cudaSuccess) {
         cuda_fail(e, "device query");
         return 0;
     }
-    return qv::attention_prefix_workspace_bytes(B * T, Hq, Hkv, D, P, sms);
+    return qv::attention_prefix_workspace_bytes(B, T, Hq, Hkv, D, P, sms);
 }
 
 qv_status qv_attention_verify_prefix(const uint16_t* qkv, const uint16_t* prefix_k, const uint16_t* prefix_v,
@@ -914,9 +917,8 @@ qv_status qv_attention_verify_prefix(const uint16_t* qkv, const uint16_t* prefix
                                      const uint16_t* v_cache, const int32_t* cache_len, int B, int T, int Hq, int Hkv,
                                      int D, int Lmax, float scale, void* out, qv_dtype out_dtype, void* workspace,
                                      size_t workspace_bytes, cudaStream_t stream) {
-    qv_status st = check_attention_prefix_shape(B, T, Hq, Hkv, D, P);
+    qv_status st = check_attention_prefix_shape(B, T, Hq, Hkv, D, P, Lmax);
     if (st != QV_OK) return st;
-    if ((st = check_attention_shape(B, T, Hq, Hkv, D, Lmax)) != QV_OK) return st;
     if (!qkv || !prefix_k || !prefix_v || !prefix_len || !cache_len || !out)
         return fail(QV_ERR_INVALID_ARG, "null pointer");
     if (Lmax > 0 && (!k_cache || !v_cache)) return fail(QV_ERR_INVALID_ARG, "k_cache / v_cache null with Lmax > 0");
@@ -924,11 +926,11 @@ qv_status qv_attention_verify_prefix(const uint16_t* qkv, const uint16_t* prefix
     if (!(scale > 0.0f) || scale > 2.0e38f) return fail(QV_ERR_INVALID_ARG, "scale must be in (0, 2e38]");
     if (!aligned(qkv, 16) || !aligned(prefix_k, 16) || !aligned(prefix_v, 16) || (k_cache && !aligned(k_cache, 16)) ||
         (v_cache && !aligned(v_cache, 16)) || !aligned(cache_len, 4) || !aligned(prefix_len, 4) || !aligned(out, 16))
-        return fail(QV_ERR_INVALID_ARG, "qkv, the prefix, the caches and out must be 16-byte aligned");
+        return fail(QV_ERR_INVALID_ARG, "qkv, the prefix, the caches and out must be 16-byte aligned, lengths 4-byte aligned");
     cudaError_t e;
     const int sms = sms_of_current_device(&e);
     if (e != cudaSuccess) return cuda_fail(e, "device query");
-    const size_t need = qv::attention_prefix_workspace_bytes(B * T, Hq, Hkv, D, P, sms);
+    const size_t need = qv::attention_prefix_workspace_bytes(B, T, Hq, Hkv, D, P, sms);
     if (!workspace) return fail(QV_ERR_WORKSPACE, "workspace is null (%zu bytes needed)", need);
     if (!aligned(workspace, 16)) return fail(QV_ERR_WORKSPACE, "workspace must be 16-byte aligned");
     if (workspace_bytes < need) return fail(QV_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
@@ -941,20 +943,23 @@ qv_status qv_attention_verify_prefix(const uint16_t* qkv, const uint16_t* prefix
     QV_CHECK_DEV(cache_len);
     QV_CHECK_DEV(out);
     QV_CHECK_DEV(workspace);
-    CUtensorMap q, k, v;
-    qv::KvMaps maps;
-    st = encode_heads(&q, qkv, B * T, Hq + 2 * Hkv, D, Hq / Hkv, qv::attention_prompt_tokens(Hq / Hkv));
-    if (st == QV_OK) st = encode_heads(&k, prefix_k, P, Hkv, D, 1, 128);
-    if (st == QV_OK) st = encode_heads(&v, prefix_v, P, Hkv, D, 1, 128);
-    if (st == QV_OK) st = encode_cache_maps(&maps, k_cache, v_cache, B, Lmax, Hkv, D);
+    qv::PrefixCall c = {};
+    st = encode_heads(&c.q, qkv, B * T, Hq + 2 * Hkv, D, Hq / Hkv, qv::attention_prompt_tokens(Hq / Hkv));
+    if (st == QV_OK) st = encode_heads(&c.pk, prefix_k, P, Hkv, D, 1, 128);
+    if (st == QV_OK) st = encode_heads(&c.pv, prefix_v, P, Hkv, D, 1, 128);
+    if (st == QV_OK && Lmax > 0) st = encode_kv_cache(&c.kc, k_cache, B, Lmax, Hkv, D, 128);
+    if (st == QV_OK && Lmax > 0) st = encode_kv_cache(&c.vc, v_cache, B, Lmax, Hkv, D, 128);
     if (st != QV_OK) return st;
+    c.qkv = qkv;
+    c.prefix_len = prefix_len;
+    c.cache_len = cache_len;
+    c.B = B; c.T = T; c.Hq = Hq; c.Hkv = Hkv; c.D = D; c.P = P; c.Lmax = Lmax;
+    c.scale = scale;
+    c.out = out;
+    c.out_bf16 = out_dtype == QV_BF16;
+    c.ws = workspace;
     const int hold = qv::debug_take_hold_attention() ? 1 : 0;
-    qv::PrefixParts parts;
-    e = qv::launch_attention_prefix(q, k, v, prefix_len, B * T, Hq, Hkv, D, P, scale, out_dtype == QV_F32, workspace,
-                                    sms, hold, qv::debug_slot_wait_ns(), &parts, stream);
-    if (e == cudaSuccess)
-        e = qv::launch_attention_verify(qkv, Lmax > 0 ? &maps : nullptr, cache_len, B, T, Hq, Hkv, D, Lmax, scale, out,
-                                        hold, qv::debug_slot_wait_ns(), &parts, out_dtype == QV_BF16, stream);
+    e = qv::launch_attention_prefix(c, sms, hold, qv::debug_slot_wait_ns(), stream);
     if (e != cudaSuccess) return cuda_fail(e, "qv_attention_verify_prefix launch");
     return ok();
 }

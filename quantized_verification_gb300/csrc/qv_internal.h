@@ -149,18 +149,9 @@ struct KvMaps {
 size_t attention_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int Lmax);
 // hold_loads, wait_ns: test hook (qv_debug_hold_attention_loads) and the
 // stage-wait limit (0: kWaitLimitNs).
-// parts: partial results over a prefix all sequences share, or null (fp32
-// outputs only then).
-constexpr int kPrefixMaxSplits = 64;
-struct PrefixParts {
-    const float* o;           // [splits][B*T][Hq][D], not divided by l
-    const float* ml;          // [splits][B*T][Hq][2]: log2 reference m (-inf: no position) and sum l
-    int splits;
-};
 cudaError_t launch_attention_verify(const uint16_t* qkv, const KvMaps* maps, const int32_t* len, int B, int T, int Hq,
-                                    int Hkv, int D, int Lmax, float scale, void* out, int hold_loads,
-                                    unsigned long long wait_ns, const PrefixParts* parts, bool out_bf16,
-                                    cudaStream_t s);
+                                    int Hkv, int D, int Lmax, float scale, float* out, int hold_loads,
+                                    unsigned long long wait_ns, cudaStream_t s);
 cudaError_t read_and_clear_attn_error(unsigned* code);
 
 // The 4-bit paged KV cache: rows written (k_kv4.cu), positions read back, and
@@ -180,18 +171,29 @@ cudaError_t launch_attention_kv4(const uint16_t* qkv, const uint8_t* cache, cons
 cudaError_t read_and_clear_attn_kv4_error(unsigned* code);
 
 // Attention of many query rows (k_attn_prompt.cu): whole prompts packed in one
-// buffer, and partial results over a shared prefix for launch_attention_verify.
+// buffer, and the rows of a batch behind a shared prefix.
 // q: the qkv rows as a 3-D tensor map (dims D, heads, rows; bf16, 128-byte
 // swizzle) with a box of 64 values x G heads x attention_prompt_tokens(G) rows;
-// kv, k, v: [rows][heads][D] maps with boxes of 64 values x 1 head x 128 rows.
+// kv, pk, pv: [rows][heads][D] maps with boxes of 64 values x 1 head x 128 rows;
+// kc, vc: 4-D maps of the caches with boxes of 64 values x 1 head x 128
+// positions x 1 sequence (unused when Lmax == 0).
 int attention_prompt_tokens(int G);
 cudaError_t launch_attention_prompt(const CUtensorMap& q, const CUtensorMap& kv, const int32_t* cu, int B, int M, int Hq,
                                     int Hkv, int D, float scale, void* out, bool out_bf16, int sms, int hold,
                                     unsigned long long wait_ns, cudaStream_t s);
-size_t attention_prefix_workspace_bytes(int M, int Hq, int Hkv, int D, int P, int sms);
-cudaError_t launch_attention_prefix(const CUtensorMap& q, const CUtensorMap& k, const CUtensorMap& v, const int32_t* len,
-                                    int M, int Hq, int Hkv, int D, int P, float scale, bool exact, void* ws, int sms,
-                                    int hold, unsigned long long wait_ns, PrefixParts* parts, cudaStream_t s);
+size_t attention_prefix_workspace_bytes(int B, int T, int Hq, int Hkv, int D, int P, int sms);   // any Lmax
+struct PrefixCall {
+    CUtensorMap q, pk, pv, kc, vc;
+    const uint16_t* qkv;
+    const int32_t* prefix_len;
+    const int32_t* cache_len;
+    int B, T, Hq, Hkv, D, P, Lmax;
+    float scale;
+    void* out;
+    bool out_bf16;
+    void* ws;
+};
+cudaError_t launch_attention_prefix(const PrefixCall& c, int sms, int hold, unsigned long long wait_ns, cudaStream_t s);
 cudaError_t read_and_clear_attn_prompt_error(unsigned* code);
 
 // Rotary positions of the query and key heads of qkv rows, after an optional

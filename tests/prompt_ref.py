@@ -73,3 +73,13 @@ def bound(o, a, dtype):
     if dtype == torch.bfloat16:
         return 2.0 ** -8 * (a + o.abs()) * 1.01 + 1e-5 * a
     return (2.0 ** -17 + 1e-5) * a
+
+
+def norm_bound(dtype):
+    """The same for the 2-norm of the difference over the 2-norm of the outputs. fp32: errors of single probabilities are
+    independent, so that their share of the mean is that of one of them, whether or not the values cancel: the residue of
+    two bf16 parts, at most 2^-17 of a probability, evenly spread, is 2^-17 / sqrt(3) = 4.4e-6; the sum of a score's 128
+    products, cut off 8 times at 2^-24 of scores up to about 8, 2e-6; the cut sums of at most 128 products, 1.6e-8 each on a
+    sum that grows from 0, 1e-6: 5e-6 together. bf16: half a step of the probabilities and of the outputs, evenly spread,
+    2^-8 / sqrt(3) each: 3.2e-3."""
+    return 4e-3 if dtype == torch.bfloat16 else 5e-6

@@ -39,10 +39,9 @@ def run(x, pk, pv, plen, kc, vc, lens, T, Hq, Hkv, scale, dtype, ws=None):
 def check(out, x, pk, pv, plen, kc, vc, lens, T, Hq, Hkv, scale):
     o, a = ref.verify_prefix(x, pk, pv, plen, kc, vc, lens, T, Hq, Hkv, scale)
     got = out.double().view(o.shape)
-    # the step's own kernel keeps scores and sums to about 1e-5 of the values
-    assert ((got - o).abs() <= ref.bound(o, a, out.dtype) + 1e-5 * a).all(), float((got - o).abs().max())
+    assert ((got - o).abs() <= ref.bound(o, a, out.dtype)).all(), float((got - o).abs().max())
     rel = float((got - o).norm() / o.norm())
-    assert rel <= (4e-3 if out.dtype == torch.bfloat16 else 5e-6), rel
+    assert rel <= ref.norm_bound(out.dtype), rel
     assert qv.qv_device_error() == 0
 
 
@@ -61,7 +60,7 @@ def test_lengths_of_the_prefix(plen, dtype):
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("B,T,Hq,Hkv", [(1, 1, 1, 1), (3, 5, 32, 8), (7, 3, 12, 4), (5, 1, 32, 1), (2, 32, 2, 2), (40, 4, 16, 2),
-                                        (3, 2, 14, 2), (64, 1, 8, 1)])
+                                        (3, 2, 14, 2), (64, 1, 8, 1), (3, 33, 3, 1), (2, 128, 2, 2), (2, 1, 128, 1)])
 def test_shapes(B, T, Hq, Hkv, D, dtype):
     P, Lmax = 700, 50
     g = torch.Generator().manual_seed(B)
@@ -71,6 +70,17 @@ def test_shapes(B, T, Hq, Hkv, D, dtype):
         kc[b, n:], vc[b, n:] = float("nan"), float("nan")
     s = D ** -0.5
     check(run(x, pk, pv, 690, kc, vc, lens, T, Hq, Hkv, s, dtype), x, pk, pv, 690, kc, vc, lens, T, Hq, Hkv, s)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("B,T,Hq,Hkv,Lmax", [(1, 1, 4, 1, 3000), (3, 5, 32, 8, 1500), (24, 2, 16, 8, 1000)])
+def test_long_caches(B, T, Hq, Hkv, Lmax, dtype):
+    P = 150
+    x, pk, pv, kc, vc = case(B, T, Hq, Hkv, 128, P, Lmax, 6)
+    lens = [Lmax - 131 * b % Lmax for b in range(B)]
+    for b, n in enumerate(lens):
+        kc[b, n:], vc[b, n:] = float("inf"), float("nan")
+    check(run(x, pk, pv, P, kc, vc, lens, T, Hq, Hkv, 0.09, dtype), x, pk, pv, P, kc, vc, lens, T, Hq, Hkv, 0.09)
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -127,6 +137,33 @@ def test_what_is_not_finite_in_the_prefix_reaches_every_row(dtype):
         assert torch.isfinite(out).all()
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_what_is_not_finite_in_one_cache_or_token_stays_with_those_that_see_it(dtype):
+    B, T, Hq, Hkv, D, P = 3, 3, 8, 2, 128, 200
+    x, pk, pv, kc, vc = case(B, T, Hq, Hkv, D, P, 30)
+    lens = [30, 11, 0]
+    vc[1, 10, :, 7] = float("nan")
+    x.view(B, T, Hq + 2 * Hkv, D)[2, 1, Hq:] = float("inf")        # the middle token of the last sequence
+    out = run(x, pk, pv, P, kc, vc, lens, T, Hq, Hkv, 0.1, dtype).view(B, T, Hq, D)
+    assert not torch.isfinite(out[1, :, :, 7]).any() and not torch.isfinite(out[2, 1:]).any()
+    assert torch.isfinite(out[0]).all() and torch.isfinite(out[2, 0]).all()
+
+
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right():
+    for B, T, Hq, Hkv in ((2, 1, 8, 2), (20, 5, 32, 8)):
+        x, pk, pv, kc, vc = case(B, T, Hq, Hkv, 128, 300, 20)
+        args = (x, pk, pv, 300, kc, vc, [b % 21 for b in range(B)], T, Hq, Hkv, 0.1)
+        qv.qv_debug_set_slot_wait_ns(2_000_000)
+        qv.qv_debug_hold_attention_loads(1)
+        try:
+            run(*args, torch.float32)
+            assert qv.qv_device_error() == qv.QV_DEVICE_ERR_FULL_WAIT
+        finally:
+            qv.qv_debug_hold_attention_loads(0)
+            qv.qv_debug_set_slot_wait_ns(0)
+        check(run(*args, torch.float32), *args)
+
+
 def test_lengths_outside_are_clamped_and_graphs_read_them():
     B, T, Hq, Hkv, D, P = 2, 1, 8, 2, 128, 200
     x, pk, pv, kc, vc = case(B, T, Hq, Hkv, D, P, 20)
@@ -168,7 +205,7 @@ def test_refusals():
                 dict(prefix_len=torch.zeros(2, dtype=torch.int32, device="cuda"))):
         with pytest.raises((ValueError, TypeError)):
             qv.qv_attention_verify_prefix(**{**ok, **bad})
-    assert qv.qv_attention_prefix_workspace_bytes(1, 33, 1, 1, 64, 10) == 0        # more than 32 rows a head group
+    assert qv.qv_attention_prefix_workspace_bytes(1, 129, 1, 1, 64, 10) == 0       # more than 128 rows a head group
     assert qv.qv_attention_prefix_workspace_bytes(1, 1, 1, 1, 64, 0) == 0
     assert qv.qv_attention_prefix_workspace_bytes(1, 1, 1, 1, 96, 10) == 0
     assert (out == 7.0).all()

@@ -39,7 +39,7 @@ def prefix(B=1, T=1, Hq=4, Hkv=2, D=64, Pm=10, Lmax=5, scale=0.1, out_dtype=0, n
                   out_dtype, FAKE, 1 << 30, None)
 
 
-@pytest.mark.parametrize("kw", [dict(B=0), dict(T=0), dict(T=17), dict(Hq=3), dict(D=32), dict(Pm=0), dict(Pm=2 ** 24 + 1),
+@pytest.mark.parametrize("kw", [dict(B=0), dict(T=0), dict(T=65), dict(Hq=3), dict(D=32), dict(Pm=0), dict(Pm=2 ** 24 + 1),
                                 dict(Lmax=-1), dict(scale=0.0), dict(scale=math.nan), dict(out_dtype=3), dict(n=None),
                                 dict(kc=None), dict(pk=None), dict(pk=FAKE + 2), dict(out=None), dict(out=FAKE + 4)])
 def test_prefix_refusals(kw):

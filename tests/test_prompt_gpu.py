@@ -44,7 +44,7 @@ def check(out, x, cu, Hq, Hkv, scale, fill=7.0):
     assert (d <= ref.bound(o, a, out.dtype)[inside]).all(), f"off by {float(d.max())}"
     if inside.any():
         rel = float((got - o)[inside].norm() / o[inside].norm())
-        assert rel <= (4e-3 if out.dtype == torch.bfloat16 else 3e-6), rel
+        assert rel <= ref.norm_bound(out.dtype), rel
     assert qv.qv_device_error() == 0
 
 
@@ -160,8 +160,8 @@ def test_sums_of_one_sign_do_not_drift():
     x[:, 2 * D:] = x[:, 2 * D:].abs()
     out = run(x, [0, n], 1, 1, D, 0.125, torch.float32)
     o, a = ref.prompt(x, [0, n], 1, 1, 0.125)
-    # the sums are truncated by 1.6e-8 a product, 128 products between two rounded additions
-    assert float((out.double().view(o.shape) - o).norm() / o.norm()) <= 3e-6
+    # (without the rounded additions between them the sums would be off by 1e-5)
+    assert float((out.double().view(o.shape) - o).norm() / o.norm()) <= ref.norm_bound(out.dtype)
 
 
 def test_views_streams_graphs_and_repeats():
@@ -237,13 +237,12 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right():
     Hq, Hkv, D = 32, 8, 128
     for n in (64, 700):
         x = rows(n, Hq, Hkv, D, 12)
-        lib = qv.load()
-        lib.qv_debug_set_slot_wait_ns(2_000_000)
-        lib.qv_debug_hold_attention_loads(1)
+        qv.qv_debug_set_slot_wait_ns(2_000_000)
+        qv.qv_debug_hold_attention_loads(1)
         try:
             run(x, [0, n], Hq, Hkv, D, 0.1, torch.bfloat16)
-            assert qv.qv_device_error() & 1
+            assert qv.qv_device_error() == qv.QV_DEVICE_ERR_FULL_WAIT
         finally:
-            lib.qv_debug_hold_attention_loads(0)
-            lib.qv_debug_set_slot_wait_ns(0)
+            qv.qv_debug_hold_attention_loads(0)
+            qv.qv_debug_set_slot_wait_ns(0)
         check(run(x, [0, n], Hq, Hkv, D, 0.1, torch.bfloat16), x, [0, n], Hq, Hkv, 0.1)
