@@ -14,9 +14,9 @@
 // Packed prompts need no list of tiles: a tile of tokens that reaches over the end
 // of a sequence runs over both sequences' keys, each row between its own limits.
 //
-// Roles: 8 warps form the softmax of a tile (two threads a row, 64 of its 128 scores
-// in registers each: no shuffles), one warp issues the products, one the TMA loads
-// of keys and values, 128 positions each, into one ring. Per tile and 128 keys:
+// Roles: 4 warps form the softmax of a tile (thread = row, its 128 scores in
+// registers: no shuffles), one warp issues the products, one the TMA loads of keys
+// and values, 128 positions each, into one ring. Per tile and 128 keys:
 //   S = Q K^T      8 tcgen05.mma (D = 128), M = N = 128, both operands K-major
 //                  in shared memory, the accumulator in tensor memory
 //   P = 2^(cS-m)   rounded to bf16 over S's columns in tensor memory. The reference
@@ -58,6 +58,7 @@ constexpr int kFlush = 8;                  // steps O accumulates for fp32 outpu
 // How far (log2) a score may lie above m: P is a floating-point number and keeps
 // its relative precision, only 2^40 times its sums must not overflow.
 constexpr float kLag = 40.0f;
+constexpr int kPolls = 32;                 // of a barrier, before a wait looks at the timer
 constexpr float kLog2e = 1.4426950408889634f;
 
 template <int D, int NT>
@@ -68,18 +69,17 @@ struct Layout {
     static constexpr int Q = 0;
     static constexpr int Ring = NT * Tile;
     static constexpr int Bar = Ring + Stages * Tile;
-    // barriers: full, empty [Stages], Q, S full [2], P full [2], PV done [2], scan [2], drain
-    static constexpr int bEmpty = Stages, bQ = 2 * Stages, bS = bQ + 1, bP = bS + 2, bPV = bP + 2, bScan = bPV + 2,
+    // barriers: full, empty [Stages], Q, S full [2], halves of P [2][2], PV done [2], scan [2], drain
+    static constexpr int bEmpty = Stages, bQ = 2 * Stages, bS = bQ + 1, bP = bS + 2, bPV = bP + 4, bScan = bPV + 2,
                          bDrain = bScan + 2, kBars = bDrain + 1;
     static constexpr int Bad = Bar + (kBars + 1) / 2 * 16;  // keys with values that are not finite [4][4] words
     static constexpr int Misc = Bad + 4 * 16;               // tensor memory base, abort word
-    static constexpr int Xch = Misc + 16;                   // exchange between the threads of a row [NT][128]
-    static constexpr int Bytes = Xch + NT * 128 * 4;
+    static constexpr int Bytes = Misc + 16;
     static constexpr int Alloc = Bytes + 1024;              // slack to align the base to 1024 B
     // softmax warps, then a warpgroup with the products' and the loads' warps. With
-    // two tiles it hands registers over: 640 threads of 96 become 512 of 104 and
-    // 128 of 64
-    static constexpr int Warps = NT * 8;
+    // two tiles it hands registers over: 384 threads of 168 become 256 of 208 and
+    // 128 of 88
+    static constexpr int Warps = NT * 4;
     static constexpr int Threads = Warps * 32 + 128;
     // tensor memory columns: S (P over it) of both tiles or buffers, then O
     static constexpr int kO = 256;
@@ -112,25 +112,33 @@ struct Args {
     unsigned long long wait_ns;
 };
 
+// Shared-memory descriptors, 128-byte swizzle: the high word is the same for all
+// (8-row groups 1024 bytes apart, the format's version, the swizzle); the low
+// word is the address / 16 and, for V as the N-major B operand (atoms of 64 dims x
+// 8 positions), the distance of the next 64 dims, a half of the tile.
+constexpr uint32_t kDescHigh = (1024u >> 4) | 1u << 14 | 2u << 29;
+constexpr uint32_t kDescK = 1u << 16, kDescV = (16384u >> 4) << 16;
 // One K = 16 step of D[tmem] (+)= A B^T, A from shared memory or from tensor
 // memory. The whole warp calls, one lane (`lead`) issues: control flow and
 // descriptors stay uniform, which a branch on the lane would not leave them.
-__device__ __forceinline__ void umma_ss(uint32_t lead, uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t id,
+__device__ __forceinline__ void umma_ss(uint32_t lead, uint32_t d_tmem, uint32_t a_desc, uint32_t b_desc, uint32_t id,
                                         uint32_t accumulate) {
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                 :: "r"(d_tmem), "l"(a_desc), "l"(b_desc), "r"(id), "r"(accumulate), "r"(lead) : "memory");
+    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+                 "mov.b64 a, {%1, %6};\n\tmov.b64 b, {%2, %6};\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}"
+                 :: "r"(d_tmem), "r"(a_desc), "r"(b_desc), "r"(id), "r"(accumulate), "r"(lead), "n"(kDescHigh) : "memory");
 }
-__device__ __forceinline__ void umma_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t id,
+__device__ __forceinline__ void umma_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint32_t b_desc, uint32_t id,
                                         uint32_t accumulate) {
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
-                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-                 :: "r"(d_tmem), "r"(a_tmem), "l"(b_desc), "r"(id), "r"(accumulate), "r"(lead) : "memory");
+    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\tsetp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+                 "mov.b64 b, {%2, %6};\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}"
+                 :: "r"(d_tmem), "r"(a_tmem), "r"(b_desc), "r"(id), "r"(accumulate), "r"(lead), "n"(kDescHigh) : "memory");
 }
-__device__ __forceinline__ void commit(uint32_t lead, uint64_t* bar) {
+__device__ __forceinline__ void commit(uint32_t lead, uint32_t bar) {
     asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
                  "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
-                 :: "r"(smem_u32(bar)), "r"(lead) : "memory");
+                 :: "r"(bar), "r"(lead) : "memory");
 }
 __device__ __forceinline__ uint32_t elect_lane() {
     uint32_t p;
@@ -142,18 +150,6 @@ __device__ __forceinline__ uint32_t elect_lane() {
 __host__ __device__ constexpr uint32_t idesc_bf16(int N, bool b_mn) {
     return (1u << 4) | (1u << 7) | (1u << 10) | (b_mn ? 1u << 16 : 0u) | ((uint32_t)(N >> 3) << 17) |
            ((uint32_t)(128 >> 4) << 24);
-}
-// Descriptor of V as the N-major B operand: atoms of 64 dims x 8 positions
-// (128-byte swizzle), the next 8 positions 1024 bytes on, the next 64 dims
-// `half` bytes on.
-__device__ __forceinline__ uint64_t v_desc(uint32_t saddr, uint32_t half) {
-    uint64_t d = 0;
-    d |= (uint64_t)((saddr >> 4) & 0x3FFFu);
-    d |= (uint64_t)(half >> 4) << 16;
-    d |= (uint64_t)(1024u >> 4) << 32;
-    d |= (uint64_t)1u << 46;
-    d |= (uint64_t)2u << 61;
-    return d;
 }
 __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map, int x, int head, int row,
                                             uint64_t* bar) {
@@ -217,20 +213,32 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
-// Barrier `id` of 64 threads (two whole warps); whether any of them has p.
-__device__ __forceinline__ bool pair_or(int id, bool p) {
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred.aligned q, %2, 64, p;\n\t"
-                 "selp.u32 %0, 1, 0, q;\n\t}" : "=r"(r) : "r"((uint32_t)p), "r"(id) : "memory");
-    return r != 0;
+// tcgen05.wait::ld that the loaded values pass through, so that no use of them is moved before it.
+__device__ __forceinline__ void tmem_ld_done(uint32_t (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
+                   "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]), "+r"(v[23]),
+                   "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29])
+                 :: "memory");
+    asm volatile("" : "+r"(v[30]), "+r"(v[31]) :: "memory");
 }
 __device__ __forceinline__ float neg_inf() { return __uint_as_float(0xFF800000u); }
 
+// mbar_try_wait that may sleep for about 20 us before it answers.
+__device__ __forceinline__ bool long_try_wait(uint64_t* bar, unsigned parity) {
+    unsigned ok;
+    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity), "r"(20000u) : "memory");
+    return ok != 0;
+}
 // A wait of at most limit_ns; false (and *abort set, the error noted) when it
 // runs out, false at once when another wait has.
 __device__ __forceinline__ bool lane_wait(uint64_t* bar, unsigned parity, volatile int* abort,
                                           unsigned long long limit_ns) {
-    if (mbar_try_wait(bar, parity)) return true;
+    // reading the timer takes longer than most waits: not before a wait has been a long one
+    for (int k = 0; k < kPolls; ++k)
+        if (long_try_wait(bar, parity)) return true;
     const unsigned long long t0 = global_timer_ns();
     while (true) {
         if (mbar_try_wait(bar, parity)) return true;
@@ -361,9 +369,10 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
         mbar_init(&bar[Ly::bQ], 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&bar[Ly::bS + i], 1);
-            mbar_init(&bar[Ly::bP + i], 8);
+            mbar_init(&bar[Ly::bP + 2 * i], 4);
+            mbar_init(&bar[Ly::bP + 2 * i + 1], 4);
             mbar_init(&bar[Ly::bPV + i], 1);
-            mbar_init(&bar[Ly::bScan + i], 8);
+            mbar_init(&bar[Ly::bScan + i], 4);
         }
         mbar_init(&bar[Ly::bDrain], 1);
         for (int i = 0; i < 16; ++i) bad[i] = 0;
@@ -384,7 +393,7 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
     const int nmax = NT == 2 ? max(it.nt[0], it.nt[1]) : it.nt[0];
 
     if (warp >= kMmaWarp) {
-    if (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
+    if (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kLoadWarp) {
         // -------------------------------------------------------------- loads
         if (lane == 0 && nmax > 0 && !a.hold) {
@@ -425,93 +434,118 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
         if (nmax > 0) {
             const uint32_t lead = elect_lane();
             constexpr uint32_t id_s = idesc_bf16(kKeys, false), id_o = idesc_bf16(D, true);
-            auto full = [&](int load) { return warp_wait(&bar[load % Ly::Stages], (load / Ly::Stages) & 1, abort, a.wait_ns); };
-            auto scores = [&](int i, int load, int col) {
-                const uint32_t q = sbase + Ly::Q + i * Ly::Tile, k = sbase + Ly::Ring + (load % Ly::Stages) * Ly::Tile;
+            const uint32_t t0 = __shfl_sync(0xffffffffu, tm, 0);        // uniform, and known to be
+            const uint32_t bars = sbase + Ly::Bar, ring = (sbase + Ly::Ring) >> 4;
+            auto at = [&](int b) { return bars + 8 * b; };
+            // which stage holds a load and whether it has been filled an even number of times: what step n
+            // uses are keys n + 1 and values n, two loads on each time
+            struct Slot {
+                int s = 0;
+                uint32_t parity = 0;
+                __device__ __forceinline__ void advance() {
+                    s += 2;
+                    if (s >= Ly::Stages) {
+                        s -= Ly::Stages;
+                        parity ^= 1;
+                    }
+                }
+            } k, v;
+            v.s = 1;
+            auto wait = [&](int b, uint32_t parity) { return lane_wait(&bar[b], parity, abort, a.wait_ns); };
+            auto scores = [&](int i, int col) {
+                const uint32_t q = ((sbase + Ly::Q + i * Ly::Tile) >> 4) | kDescK, kd = (ring + k.s * (Ly::Tile >> 4)) | kDescK;
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk)
-                    umma_ss(lead, tm + col, sw128_kmajor_desc(q + (kk >> 2) * 16384 + (kk & 3) * 32),
-                                 sw128_kmajor_desc(k + (kk >> 2) * 16384 + (kk & 3) * 32), id_s, kk > 0);
+                    umma_ss(lead, t0 + col, q + (kk >> 2) * 1024 + (kk & 3) * 2, kd + (kk >> 2) * 1024 + (kk & 3) * 2, id_s,
+                            kk > 0);
             };
-            auto outputs = [&](int i, int load, int col, bool add) {
-                const uint32_t v = sbase + Ly::Ring + (load % Ly::Stages) * Ly::Tile;
+            auto outputs = [&](int i, int col, int half, uint32_t add) {
+                const uint32_t vd = (ring + v.s * (Ly::Tile >> 4)) | kDescV;
 #pragma unroll
                 for (int part = 0; part < PARTS; ++part)
 #pragma unroll
-                    for (int kk = 0; kk < kKeys / 16; ++kk)  // each half of P lies over its half of S
-                        umma_ts(lead, tm + Ly::kO + i * D, tm + col + (kk >> 2) * 64 + part * 32 + (kk & 3) * 8,
-                                v_desc(v + kk * 2048, 16384), id_o, add || part > 0 || kk > 0);
+                    for (int kk = 0; kk < kKeys / 32; ++kk)  // each half of P lies over its half of S
+                        umma_ts(lead, t0 + Ly::kO + i * D, t0 + col + half * 64 + part * 32 + kk * 8,
+                                vd + (half * 4 + kk) * 128, id_o, half > 0 || part > 0 || kk > 0 ? 1u : add);
             };
-            auto release = [&](int load) { commit(lead, &bar[Ly::bEmpty + load % Ly::Stages]); };
-            bool ok = warp_wait(&bar[Ly::bQ], 0, abort, a.wait_ns) && full(0);
+            bool ok = __all_sync(0xffffffffu, wait(Ly::bQ, 0) && wait(0, 0));
             tc_fence_after();
-            if (NT == 2) {
-                if (ok) {
+            if (ok) {
 #pragma unroll
-                    for (int i = 0; i < NT; ++i)
-                        if (it.nt[i] > 0) {
-                            scores(i, 0, i * 128);
-                            commit(lead, &bar[Ly::bS + i]);
-                        }
-                    release(0);
-                }
-                for (int n = 0; ok && n < nmax; ++n) {
+                for (int i = 0; i < NT; ++i)
+                    if (it.nt[i] > 0) {
+                        scores(i, i * 128);
+                        commit(lead, at(Ly::bS + i));
+                    }
+                commit(lead, at(Ly::bEmpty));
+                k.advance();
+            }
+            if (NT == 2) {
+                // tiles do the same but for the first one's last step, which may come earlier
+                const int n0 = __shfl_sync(0xffffffffu, it.nt[0], 0), n1 = __shfl_sync(0xffffffffu, it.nt[1], 0);
+                for (int n = 0; ok && n < max(n0, n1); ++n) {
 #pragma unroll
                     for (int i = 0; i < NT; ++i) {
-                        if (!ok || n >= it.nt[i]) continue;
-                        const bool last = i == 1 || n >= it.nt[1];       // the last tile to use values n
+                        const int ni = i ? n1 : n0;
+                        if (!ok || n >= ni) continue;
                         // (P last: it is what the next products wait for)
-                        ok = full(2 * n + 1) && (n + 1 >= it.nt[i] || full(2 * n + 2)) &&
-                             warp_wait(&bar[Ly::bP + i], n & 1, abort, a.wait_ns);
+                        ok = wait(v.s, v.parity) && (n + 1 >= ni || wait(k.s, k.parity)) && wait(Ly::bP + 2 * i, n & 1);
+                        ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
                         tc_fence_after();
-                        outputs(i, 2 * n + 1, i * 128, PARTS == 2 ? n % kFlush != 0 : n > 0);
-                        if (n == it.nt[i] - 1) commit(lead, &bar[Ly::bPV + i]);
-                        if (last) release(2 * n + 1);
-                        if (n + 1 < it.nt[i]) {
-                            scores(i, 2 * n + 2, i * 128);
-                            commit(lead, &bar[Ly::bS + i]);
-                            if (i == 1 || n + 1 >= it.nt[1]) release(2 * n + 2);
+                        outputs(i, i * 128, 0, PARTS == 2 ? n % kFlush != 0 : n > 0);
+                        ok = __all_sync(0xffffffffu, wait(Ly::bP + 2 * i + 1, n & 1));
+                        if (!ok) break;
+                        tc_fence_after();
+                        outputs(i, i * 128, 1, 1);
+                        if (n + 1 < ni) {
+                            scores(i, i * 128);
+                            commit(lead, at(Ly::bS + i));
+                            if (i == 1 || n + 1 >= n1) commit(lead, at(Ly::bEmpty + k.s));
+                        } else {
+                            commit(lead, at(Ly::bPV + i));
                         }
+                        if (i == 1 || n >= n1) commit(lead, at(Ly::bEmpty + v.s));   // the last tile to use values n
                     }
+                    k.advance();
+                    v.advance();
                 }
             } else {
-                if (ok) {
-                    scores(0, 0, 0);
-                    commit(lead, &bar[Ly::bS]);
-                    release(0);
-                }
-                for (int n = 0; ok && n < nmax; ++n) {
-                    if (n + 1 < nmax) {
-                        ok = full(2 * n + 2);
+                const int n0 = __shfl_sync(0xffffffffu, it.nt[0], 0);
+                for (int n = 0; ok && n < n0; ++n) {
+                    if (n + 1 < n0) {
+                        ok = __all_sync(0xffffffffu, wait(k.s, k.parity));
                         if (!ok) break;
-                        scores(0, 2 * n + 2, ((n + 1) & 1) * 128);
-                        commit(lead, &bar[Ly::bS + ((n + 1) & 1)]);
-                        release(2 * n + 2);
+                        scores(0, ((n + 1) & 1) * 128);
+                        commit(lead, at(Ly::bS + ((n + 1) & 1)));
+                        commit(lead, at(Ly::bEmpty + k.s));
                     }
                     // (a barrier for each buffer: a warp may be a step ahead of another)
-                    ok = full(2 * n + 1) && warp_wait(&bar[Ly::bP + (n & 1)], (n >> 1) & 1, abort, a.wait_ns);
+                    ok = __all_sync(0xffffffffu, wait(v.s, v.parity) && wait(Ly::bP + 2 * (n & 1), (n >> 1) & 1));
                     if (!ok) break;
                     tc_fence_after();
-                    outputs(0, 2 * n + 1, (n & 1) * 128, PARTS == 2 ? n % kFlush != 0 : n > 0);
-                    commit(lead, &bar[Ly::bPV]);
-                    release(2 * n + 1);
+                    outputs(0, (n & 1) * 128, 0, PARTS == 2 ? n % kFlush != 0 : n > 0);
+                    ok = __all_sync(0xffffffffu, wait(Ly::bP + 2 * (n & 1) + 1, (n >> 1) & 1));
+                    if (!ok) break;
+                    tc_fence_after();
+                    outputs(0, (n & 1) * 128, 1, 1);
+                    commit(lead, at(Ly::bPV));
+                    commit(lead, at(Ly::bEmpty + v.s));
+                    k.advance();
+                    v.advance();
                 }
             }
             // nothing reads operands or writes tensor memory when the block ends
-            commit(lead, &bar[Ly::bDrain]);
-            const unsigned long long t0 = global_timer_ns();
-            while (!mbar_try_wait(&bar[Ly::bDrain], 0) && global_timer_ns() - t0 < kWaitLimitNs) {
+            commit(lead, at(Ly::bDrain));
+            const unsigned long long now = global_timer_ns();
+            while (!mbar_try_wait(&bar[Ly::bDrain], 0) && global_timer_ns() - now < kWaitLimitNs) {
             }
         }
     }
     } else {
         // ------------------------------------------------------------ softmax
-        if (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 104;");
-        // two threads share a row: the halves of its scores, of its outputs
-        const int i = NT == 2 ? warp >> 3 : 0, half = (warp >> 2) & 1, r = threadIdx.x & 127;
-        const int pair_id = 1 + i * 4 + (warp & 3);          // the barrier of the two warps of these rows
-        float* xch = reinterpret_cast<float*>(smem + Ly::Xch) + i * 128 + r;
+        if (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        const int i = NT == 2 ? warp >> 2 : 0, r = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const int tile_t0 = it.t0 + i * a.TM;
         const int tok = tile_t0 + r / a.G, head = it.kh * a.G + r % a.G;
@@ -533,27 +567,24 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
             hi = all_hi = -1;
         }
         const size_t row = (size_t)tok * a.Hq + head;        // of the outputs
-        constexpr int DH = D / 2;                            // this thread's dims: half * DH ..
         float* acc = nullptr;                                // where the sums of fp32 outputs lie
         if (PREFIX)
-            acc = a.part_o + ((size_t)it.part * a.M * a.Hq + row) * D + half * DH;
+            acc = a.part_o + ((size_t)it.part * a.M * a.Hq + row) * D;
         else if (PARTS == 2)
-            acc = reinterpret_cast<float*>(a.out) + row * D + half * DH;
-        const uint32_t o_col = tm + lanes + Ly::kO + i * D + half * DH;
+            acc = reinterpret_cast<float*>(a.out) + row * D;
+        const uint32_t o_col = tm + lanes + Ly::kO + i * D;
 
-        float m = neg_inf(), m_acc = neg_inf(), l = 0.f;     // l: of this thread's half
-        // After a wait that ran out (ok false) a warp still joins the pair's
-        // barriers, which tell the other: both stop at the same one.
+        float m = neg_inf(), m_acc = neg_inf(), l = 0.f;
         bool ok = true;
         unsigned scans = 0;                                  // tiles whose values were looked at
         // O added to the sums (what was there times 2^(m_acc - m), unless it is the first time), times mul
         auto flush = [&](bool fresh, float mul) {
             const float f = m_acc == neg_inf() ? 0.f : ex2(m_acc - m);
 #pragma unroll 1
-            for (int c0 = 0; c0 < DH; c0 += 32) {
+            for (int c0 = 0; c0 < D; c0 += 32) {
                 uint32_t o[32];
                 tmem_ld<32>(o_col + c0, o);
-                tmem_ld_wait();
+                tmem_ld_done(o);
                 if (valid) {
                     float4* p = reinterpret_cast<float4*>(acc + c0);
 #pragma unroll
@@ -574,74 +605,81 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
 
         for (int n = 0; n < nt; ++n) {
             const int buf = NT == 2 ? i : n & 1;
-            const uint32_t s_col = tm + lanes + buf * 128 + half * 64;
+            const uint32_t s_col = tm + lanes + buf * 128;
             const int kb = it.k0 + n * kKeys;
+            const bool part = kb < all_lo || kb + kKeys - 1 > all_hi;   // a row does not see all keys
             const bool flushed = PARTS == 2 && n > 0 && n % kFlush == 0;
-            uint32_t s[2][32];
-            float poison = 0.f, top = neg_inf();
-            if (ok) ok = warp_wait(&bar[Ly::bS + buf], (NT == 2 ? n : n >> 1) & 1, abort, a.wait_ns);
-            if (ok) {
-                tc_fence_after();
-                tmem_ld<32>(s_col, s[0]);
-                tmem_ld<32>(s_col + 32, s[1]);
-                tmem_ld_wait();
-                if (kb < all_lo || kb + kKeys - 1 > all_hi) {
-                    const int from = lo - kb, to = hi - kb;
+            float poison = 0.f;
+            uint32_t see[4];                                 // which of the keys the row sees
+            ok = warp_wait(&bar[Ly::bS + buf], (NT == 2 ? n : n >> 1) & 1, abort, a.wait_ns);
+            if (!ok) break;
+            if (part) {
+                const int from = lo - kb, to = hi - kb;
 #pragma unroll
-                    for (int q = 0; q < 2; ++q) {
-                        // bits of the keys that are seen among these 32
-                        const int f0 = max(from - half * 64 - 32 * q, 0), t0 = min(to - half * 64 - 32 * q, 31);
-                        const uint32_t see = f0 <= t0 && f0 < 32 ? 0xFFFFFFFFu >> (31 - t0) >> f0 << f0 : 0u;
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (!(see >> j & 1u)) s[q][j] = 0xFF800000u;
-                    }
-                    // values that are not finite: their keys noted, then 0 in shared memory. Both tiles'
-                    // warps may do so at the same time; marks come first, so that who finds a 0 finds the mark
-                    const int load = 2 * n + 1;
-                    ok = warp_wait(&bar[load % Ly::Stages], (load / Ly::Stages) & 1, abort, a.wait_ns);
-                    uint32_t* mark = bad + (n & 3) * 4;
-                    if (ok) {
-                        const uint32_t v = sbase + Ly::Ring + (load % Ly::Stages) * Ly::Tile;
+                for (int q = 0; q < 4; ++q) {
+                    const int f0 = max(from - 32 * q, 0), t0 = min(to - 32 * q, 31);
+                    see[q] = f0 <= t0 && f0 < 32 ? 0xFFFFFFFFu >> (31 - t0) >> f0 << f0 : 0u;
+                }
+                // values that are not finite: their keys noted, then 0 in shared memory. Both tiles'
+                // warps may do so at the same time; marks come first, so that who finds a 0 finds the mark
+                const int load = 2 * n + 1;
+                ok = warp_wait(&bar[load % Ly::Stages], (load / Ly::Stages) & 1, abort, a.wait_ns);
+                if (!ok) break;
+                uint32_t* mark = bad + (n & 3) * 4;
+                const uint32_t v = sbase + Ly::Ring + (load % Ly::Stages) * Ly::Tile;
 #pragma unroll 4
-                        for (int e = threadIdx.x & 255; e < Ly::Tile / 16; e += 256) {
-                            uint32_t w[4], inf = 0;
-                            lds_v4_u32(v + e * 16, w[0], w[1], w[2], w[3]);
+                for (int e = r; e < Ly::Tile / 16; e += 128) {
+                    uint32_t w[4], inf = 0;
+                    lds_v4_u32(v + e * 16, w[0], w[1], w[2], w[3]);
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) inf |= (w[j] & 0x7F807F80u) + 0x00800080u;   // carries out of all ones
-                            if (inf & 0x80008000u) {
-                                const int key = (e >> 3) & 127;      // 8 chunks a row; the halves one behind the other
-                                atomicOr(&mark[key >> 5], 1u << (key & 31));
-                                __threadfence_block();
+                    for (int j = 0; j < 4; ++j) inf |= (w[j] & 0x7F807F80u) + 0x00800080u;   // carries out of all ones
+                    if (inf & 0x80008000u) {
+                        const int key = (e >> 3) & 127;      // 8 chunks a row; the halves one behind the other
+                        atomicOr(&mark[key >> 5], 1u << (key & 31));
+                        __threadfence_block();
 #pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    if ((w[j] & 0x7F80u) == 0x7F80u) w[j] &= 0xFFFF0000u;
-                                    if ((w[j] & 0x7F800000u) == 0x7F800000u) w[j] &= 0x0000FFFFu;
-                                }
-                                sts_v4_u32(v + e * 16, w[0], w[1], w[2], w[3]);
-                            }
+                        for (int j = 0; j < 4; ++j) {
+                            if ((w[j] & 0x7F80u) == 0x7F80u) w[j] &= 0xFFFF0000u;
+                            if ((w[j] & 0x7F800000u) == 0x7F800000u) w[j] &= 0x0000FFFFu;
                         }
-                        fence_proxy_async_smem();
-                        warp_arrive(&bar[Ly::bScan + i]);
-                        ok = warp_wait(&bar[Ly::bScan + i], scans & 1, abort, a.wait_ns);
-                        ++scans;
-                    }
-                    if (ok) {
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            const uint32_t b = *reinterpret_cast<volatile uint32_t*>(mark + w);
-                            const int f0 = max(from - 32 * w, 0), t0 = min(to - 32 * w, 31);
-                            if (b != 0 && f0 <= t0 && (b >> f0 << f0 << (31 - t0)) != 0) poison = __uint_as_float(0x7FC00000u);
-                        }
+                        sts_v4_u32(v + e * 16, w[0], w[1], w[2], w[3]);
                     }
                 }
-                // the marks of the step after the next: no warp is that far, none still at the one before the last
-                if (half == 0 && r == 0 && (i == 0 || n >= other))
-                    *reinterpret_cast<uint4*>(bad + ((n + 2) & 3) * 4) = make_uint4(0u, 0u, 0u, 0u);
-                if (flushed && ok) {
-                    if (NT == 1) ok = warp_wait(&bar[Ly::bPV], (n - 1) & 1, abort, a.wait_ns);
-                    tc_fence_after();
-                    if (ok) flush(n == kFlush, 1.f);
+                fence_proxy_async_smem();
+                warp_arrive(&bar[Ly::bScan + i]);
+                ok = warp_wait(&bar[Ly::bScan + i], scans & 1, abort, a.wait_ns);
+                if (!ok) break;
+                ++scans;
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+                    if (*reinterpret_cast<volatile uint32_t*>(mark + w) & see[w]) poison = __uint_as_float(0x7FC00000u);
+            }
+            // the marks of the step after the next: no warp is that far, none still at the one before the last
+            if (r == 0 && (i == 0 || n >= other))
+                *reinterpret_cast<uint4*>(bad + ((n + 2) & 3) * 4) = make_uint4(0u, 0u, 0u, 0u);
+            if (flushed) {
+                if (NT == 1) ok = warp_wait(&bar[Ly::bPV], (n - 1) & 1, abort, a.wait_ns);
+                if (!ok) break;
+                tc_fence_after();
+                flush(n == kFlush, 1.f);
+            }
+
+            // P with the reference so far, or, where a score lies too far above it, with the rows' maxima
+            bool raise = n == 0;
+#pragma unroll 1
+            while (true) {
+                uint32_t s[4][32];
+                tc_fence_after();
+#pragma unroll
+                for (int q = 0; q < 4; ++q) tmem_ld<32>(s_col + 32 * q, s[q]);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) tmem_ld_done(s[q]);
+                if (part) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int j = 0; j < 32; ++j)
+                            if (!(see[q] >> j & 1u)) s[q][j] = 0xFF800000u;
                 }
                 float mx[4];
 #pragma unroll
@@ -649,104 +687,103 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
 #pragma unroll
                 for (int j = 0; j < 16; ++j)
 #pragma unroll
-                    for (int q = 0; q < 2; ++q)
-                        mx[2 * q + (j & 1)] = max3(mx[2 * q + (j & 1)], __uint_as_float(s[q][2 * j]),
-                                                   __uint_as_float(s[q][2 * j + 1]));
-                top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * a.c;
-            }
-            if (pair_or(pair_id, !ok || top > m + kLag || (m == neg_inf() && top > m))) {
-                // the row's maximum; a warp that has stopped says so to the other
-                if (half == 1) *xch = top;
-                if (pair_or(pair_id, !ok)) {
-                    ok = false;
-                    break;
-                }
-                if (half == 0) *xch = fmaxf(top, *xch);
-                pair_or(pair_id, false);
-                const float all = *xch;
-                const bool move = all > m + kLag || (m == neg_inf() && all > m);
-                const float f = !move ? 1.f : (m == neg_inf() ? 0.f : ex2(m - all));
-                if (move) m = all;
-                l *= f;
-                if (n > 0 && !flushed) {
-                    if (NT == 1) ok = warp_wait(&bar[Ly::bPV], (n - 1) & 1, abort, a.wait_ns);
-                    tc_fence_after();
-                    if (ok) {
+                    for (int q = 0; q < 4; ++q)
+                        mx[q] = max3(mx[q], __uint_as_float(s[q][2 * j]), __uint_as_float(s[q][2 * j + 1]));
+                const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * a.c;
+                if (raise) {
+                    const float all = fmaxf(m, top);
+                    const float f = m == neg_inf() ? (all == m ? 1.f : 0.f) : ex2(m - all);
+                    m = all;
+                    l *= f;
+                    if (n > 0 && !flushed) {
+                        if (NT == 1) ok = warp_wait(&bar[Ly::bPV], (n - 1) & 1, abort, a.wait_ns);
+                        if (!ok) break;
+                        tc_fence_after();
 #pragma unroll 1
-                        for (int c0 = 0; c0 < DH; c0 += 16) {
-                            uint32_t o[16];
-                            tmem_ld<16>(o_col + c0, o);
+                        for (int c0 = 0; c0 < D; c0 += 8) {
+                            uint32_t o[8];
+                            tmem_ld<8>(o_col + c0, o);
                             tmem_ld_wait();
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                            for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
                             tmem_st(o_col + c0, o);
                         }
                     }
                 }
-            }
-            if (!ok) continue;
-            const float ms = m == neg_inf() ? 0.f : m;       // a row that has seen no key yet
-            const uint64_t c2 = pair(a.c, a.c), m2 = pair(-ms, -ms);
-            uint64_t l2 = pair(poison, 0.f), l3 = pair(0.f, 0.f);
-            constexpr int CH = PARTS == 2 ? 8 : 16;          // pairs stored at once
+                const float ms = m == neg_inf() ? 0.f : m;   // a row that has seen no key yet
+                const uint64_t c2 = pair(a.c, a.c), m2 = pair(-ms, -ms);
+                uint64_t l2 = pair(poison, 0.f), l3 = pair(0.f, 0.f);
+                bool again = false;
 #pragma unroll
-            for (int q = 0; q < 32 / CH; ++q) {
-                uint32_t hi2[CH], lo2[CH];
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t hi2[2][16], lo2[2][16];
 #pragma unroll
-                for (int j = 0; j < CH; ++j) {
-                    const int at = q * CH + j;
-                    float p0, p1;
-                    unpair(fma2(pair(__uint_as_float(s[at >> 4][2 * (at & 15)]), __uint_as_float(s[at >> 4][2 * (at & 15) + 1])),
-                                c2, m2), p0, p1);
-                    p0 = ex2(p0);
-                    p1 = ex2(p1);
-                    hi2[j] = pack2(p0, p1);
-                    uint64_t p = pair(p0, p1);
-                    if (PARTS == 2) {
-                        // the sum takes what the product takes
-                        const float h0 = __uint_as_float(hi2[j] << 16), h1 = __uint_as_float(hi2[j] & 0xFFFF0000u);
-                        lo2[j] = pack2(p0 - h0, p1 - h1);
-                        p = add2(pair(h0, h1), pair(__uint_as_float(lo2[j] << 16), __uint_as_float(lo2[j] & 0xFFFF0000u)));
+                    for (int q = 0; q < 2; ++q)
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            float p0, p1;
+                            unpair(fma2(pair(__uint_as_float(s[2 * h + q][2 * j]), __uint_as_float(s[2 * h + q][2 * j + 1])),
+                                        c2, m2), p0, p1);
+                            p0 = ex2(p0);
+                            p1 = ex2(p1);
+                            const uint32_t x = pack2(p0, p1);
+                            hi2[q][j] = x;
+                            uint64_t p = pair(p0, p1);
+                            if (PARTS == 2) {
+                                // the sum takes what the product takes
+                                const float h0 = __uint_as_float(x << 16), h1 = __uint_as_float(x & 0xFFFF0000u);
+                                const uint32_t y = pack2(p0 - h0, p1 - h1);
+                                lo2[q][j] = y;
+                                p = add2(pair(h0, h1), pair(__uint_as_float(y << 16), __uint_as_float(y & 0xFFFF0000u)));
+                            }
+                            if (j & 1) l3 = add2(l3, p); else l2 = add2(l2, p);
+                        }
+                    // (only now, so that the maximum is taken while the exponentials are)
+                    if (h == 0 && !raise &&
+                        __any_sync(0xffffffffu, top > m + kLag || (m == neg_inf() && top > m))) {
+                        again = true;
+                        break;
                     }
-                    if (j & 1) l3 = add2(l3, p); else l2 = add2(l2, p);
+#pragma unroll
+                    for (int q = 0; q < 2; ++q) {
+                        tmem_st(s_col + 64 * h + 16 * q, hi2[q]);
+                        if constexpr (PARTS == 2) tmem_st(s_col + 64 * h + 32 + 16 * q, lo2[q]);
+                    }
+                    tmem_st_wait();
+                    tc_fence_before();
+                    warp_arrive(&bar[Ly::bP + 2 * buf + h]);
                 }
-                tmem_st(s_col + CH * q, hi2);
-                if constexpr (PARTS == 2) tmem_st(s_col + 32 + CH * q, lo2);
+                if (again) {
+                    raise = true;
+                    continue;
+                }
+                float x0, x1;
+                unpair(add2(l2, l3), x0, x1);
+                l += x0 + x1;
+                break;
             }
-            float x0, x1;
-            unpair(add2(l2, l3), x0, x1);
-            l += x0 + x1;
-            tmem_st_wait();
-            tc_fence_before();
-            warp_arrive(&bar[Ly::bP + buf]);
+            if (!ok) break;
         }
 
         // ------------------------------------------------------------ outputs
         if (nt > 0) {
-            if (ok) {
-                // (one tile: its last product but one may not have completed either)
-                if (NT == 1 && nt > 1) ok = warp_wait(&bar[Ly::bPV], nt & 1, abort, a.wait_ns);
-                ok = ok && warp_wait(&bar[Ly::bPV + i], NT == 2 ? 0 : (nt - 1) & 1, abort, a.wait_ns);
-            }
+            // (one tile: its last product but one may not have completed either)
+            if (ok && NT == 1 && nt > 1) ok = warp_wait(&bar[Ly::bPV], nt & 1, abort, a.wait_ns);
+            if (ok) ok = warp_wait(&bar[Ly::bPV + i], NT == 2 ? 0 : (nt - 1) & 1, abort, a.wait_ns);
             tc_fence_after();
-            if (half == 1) *xch = l;
-            if (pair_or(pair_id, !ok)) ok = false;
-            if (half == 0) *xch += l;
-            pair_or(pair_id, false);
-            l = *xch;
         }
         if (ok && nt > 0) {
             const float inv = PREFIX ? 1.f : 1.f / l;
             if (PREFIX || PARTS == 2) {
                 flush(PARTS == 1 || nt <= kFlush, inv);
-                if (PREFIX && valid && half == 0) a.part_ml[(size_t)it.part * a.M * a.Hq + row] = make_float2(m, l);
+                if (PREFIX && valid) a.part_ml[(size_t)it.part * a.M * a.Hq + row] = make_float2(m, l);
             } else {
-                uint4* p = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + row * D + half * DH);
+                uint4* p = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + row * D);
 #pragma unroll 1
-                for (int c0 = 0; c0 < DH; c0 += 32) {
+                for (int c0 = 0; c0 < D; c0 += 32) {
                     uint32_t o[32];
                     tmem_ld<32>(o_col + c0, o);
-                    tmem_ld_wait();
+                    tmem_ld_done(o);
                     if (valid) {
 #pragma unroll
                         for (int j = 0; j < 4; ++j) {
@@ -761,7 +798,7 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                     __syncwarp();
                 }
             }
-        } else if (PREFIX && valid && nt == 0 && half == 0) {
+        } else if (PREFIX && valid && nt == 0) {
             a.part_ml[(size_t)it.part * a.M * a.Hq + row] = make_float2(neg_inf(), 0.f);
         }
         tc_fence_before();
