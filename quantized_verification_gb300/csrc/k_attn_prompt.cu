@@ -61,6 +61,8 @@ constexpr float kLag = 40.0f;
 constexpr int kPolls = 32;                 // of a barrier, before a wait looks at the timer
 constexpr float kLog2e = 1.4426950408889634f;
 
+constexpr int kItemBytes = 64;
+
 template <int D, int NT>
 struct Layout {
     static constexpr int H = D / 64;                        // 128-byte halves of a row
@@ -69,11 +71,15 @@ struct Layout {
     static constexpr int Q = 0;
     static constexpr int Ring = NT * Tile;
     static constexpr int Bar = Ring + Stages * Tile;
-    // barriers: full, empty [Stages], Q, S full [2], halves of P [2][2], PV done [2], scan [2], drain
-    static constexpr int bEmpty = Stages, bQ = 2 * Stages, bS = bQ + 1, bP = bS + 2, bPV = bP + 4, bScan = bPV + 2,
-                         bDrain = bScan + 2, kBars = bDrain + 1;
-    static constexpr int Bad = Bar + (kBars + 1) / 2 * 16;  // keys with values that are not finite [4][4] words
-    static constexpr int Misc = Bad + 4 * 16;               // tensor memory base, abort word
+    // barriers: full, empty [Stages], Q full, empty, S full [2], halves of P [2][2], PV done [2], scan [2], items full,
+    // empty [2], next item, drain
+    static constexpr int bEmpty = Stages, bQ = 2 * Stages, bQEmpty = bQ + 1, bS = bQEmpty + 1, bP = bS + 2, bPV = bP + 4,
+                         bScan = bPV + 2, bItem = bScan + 2, bItemEmpty = bItem + 2, bNext = bItemEmpty + 2,
+                         bDrain = bNext + 1, kBars = bDrain + 1;
+    static constexpr int Bad = Bar + (kBars + 1) / 2 * 16;  // keys with values that are not finite [8][4] words
+    static constexpr int Items = Bad + 8 * 16;              // what the CTA works on and what comes next
+    static constexpr int Next = Items + 2 * kItemBytes;     // the answer to a request for another block's item
+    static constexpr int Misc = Next + 16;                  // tensor memory base, abort word
     static constexpr int Bytes = Misc + 16;
     static constexpr int Alloc = Bytes + 1024;              // slack to align the base to 1024 B
     // softmax warps, then a warpgroup with the products' and the loads' warps. With
@@ -286,15 +292,18 @@ __device__ __forceinline__ int sequence_start(const int32_t* __restrict__ cu, in
     return min(max(start, 0), tok);
 }
 
-// What a CTA does: the tiles' first tokens and the key positions they run over.
+// One piece of work: the tiles' first tokens and the key positions they run over.
 struct Item {
-    int kh, t0;
+    int kh;                   // key/value head, -1: no more work
+    int t0;
     int seq;                  // prefix: the sequence whose cache this is, or -1 for the prefix itself
     int part;                 // prefix: the index of the partial results
     int first, end;           // tokens [first, end) are rows to compute
     int k0, k1;               // prefix: the part's positions; prompts: k0 only
+    int all_lo, all_hi;       // keys that every row sees
     int nt[2];                // steps of each tile
 };
+static_assert(sizeof(Item) <= kItemBytes, "items fit their slots");
 
 // The whole warp calls.
 template <int NT, bool PREFIX>
@@ -328,15 +337,21 @@ __device__ __forceinline__ Item item_of(const Args& a, int item) {
         it.k1 = min(len, it.k0 + per * kKeys);
         it.nt[0] = it.k1 > it.k0 ? (it.k1 - it.k0 + kKeys - 1) / kKeys : 0;
         if (NT == 2) it.nt[1] = it.t0 + a.TM < it.end ? it.nt[0] : 0;
+        it.all_lo = it.k0;
+        it.all_hi = it.k1 - 1;
     } else {
         it.part = 0;
         it.t0 = (a.blocks - 1 - item) * (NT * a.TM);          // the last rows, which see most, first
         const int c0 = min(max(a.cu[0], 0), a.M), cB = min(max(a.cu[a.B], 0), a.M);
         it.first = max(it.t0, c0);
         it.end = min(it.t0 + NT * a.TM, cB);
-        it.k0 = it.k1 = 0;
+        it.k0 = it.k1 = it.all_lo = it.all_hi = 0;
         if (it.first < it.end) {
-            it.k0 = sequence_start(a.cu, a.B, it.first);
+            // (the lanes' rows do not fall: the first row in the lower half of the warp, the last in the upper)
+            const int start = sequence_start(a.cu, a.B, (threadIdx.x & 16) ? it.end - 1 : it.first);
+            it.k0 = __shfl_sync(0xffffffffu, start, 0);
+            it.all_lo = __shfl_sync(0xffffffffu, start, 31);
+            it.all_hi = it.first;
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
                 const int e = min(it.t0 + (i + 1) * a.TM, it.end);
@@ -345,6 +360,42 @@ __device__ __forceinline__ Item item_of(const Args& a, int item) {
         }
     }
     return it;
+}
+
+// Asks for the item of a block of this launch that has not started yet: such a
+// block then never starts. The answer arrives at `next` (16 bytes) and `bar`.
+__device__ __forceinline__ void request_item(uint32_t next, uint64_t* bar) {
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];"
+                 :: "r"(next), "r"(smem_u32(bar)) : "memory");
+}
+// The block's index, or -1 if none was left.
+__device__ __forceinline__ int requested_item(uint32_t next) {
+    int item;
+    asm volatile("{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t.reg .b32 x;\n\tld.shared.b128 h, [%1];\n\t"
+                 "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\tmov.b32 x, -1;\n\t"
+                 "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 x, h;\n\tmov.b32 %0, x;\n\t}"
+                 : "=r"(item) : "r"(next) : "memory");
+    return item;
+}
+
+// Four pieces of 16 bytes of a row in each lane become one piece (lane % 4) of
+// the rows of each of four neighbouring lanes: 64 bytes of a row side by side.
+__device__ __forceinline__ void transpose4(uint32_t (&v)[16]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int d = 1; d <= 2; d *= 2) {
+        const bool up = lane & d;
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            if (c & d) continue;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t &x = v[4 * c + j], &y = v[4 * (c + d) + j];
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, up ? x : y, d);
+                if (up) x = got; else y = got;
+            }
+        }
+    }
 }
 
 template <int D, int NT, int PARTS, bool PREFIX>
@@ -362,20 +413,12 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
     constexpr int kMmaWarp = Ly::Warps, kLoadWarp = kMmaWarp + 1;
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < Ly::Stages; ++s) {
-            mbar_init(&bar[s], 1);
-            mbar_init(&bar[Ly::bEmpty + s], 1);
+        for (int s = 0; s < Ly::kBars; ++s) {
+            const bool halves = s >= Ly::bP && s < Ly::bP + 4, scan = s >= Ly::bScan && s < Ly::bScan + 2;
+            const bool taken = s >= Ly::bItemEmpty && s < Ly::bItemEmpty + 2;
+            mbar_init(&bar[s], halves || scan ? 4 : taken ? Ly::Warps + 1 : 1);
         }
-        mbar_init(&bar[Ly::bQ], 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&bar[Ly::bS + i], 1);
-            mbar_init(&bar[Ly::bP + 2 * i], 4);
-            mbar_init(&bar[Ly::bP + 2 * i + 1], 4);
-            mbar_init(&bar[Ly::bPV + i], 1);
-            mbar_init(&bar[Ly::bScan + i], 4);
-        }
-        mbar_init(&bar[Ly::bDrain], 1);
-        for (int i = 0; i < 16; ++i) bad[i] = 0;
+        for (int i = 0; i < 32; ++i) bad[i] = 0;
         *abort = 0;
         fence_barrier_init();
     }
@@ -389,69 +432,129 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
     const uint32_t tm = *tmem_ptr;
     allow_dependent_launch();
     grid_dependency_wait();
-    const Item it = item_of<NT, PREFIX>(a, blockIdx.x);
-    const int nmax = NT == 2 ? max(it.nt[0], it.nt[1]) : it.nt[0];
+
+    // Item k of the CTA, as the loading warp has left it.
+    auto take = [&](int k, Item& it) {
+        if (!warp_wait(&bar[Ly::bItem + (k & 1)], (k >> 1) & 1, abort, a.wait_ns)) return false;
+        it = *reinterpret_cast<const Item*>(smem + Ly::Items + (k & 1) * kItemBytes);
+        warp_arrive(&bar[Ly::bItemEmpty + (k & 1)]);
+        return it.kh >= 0;
+    };
 
     if (warp >= kMmaWarp) {
     if (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
     if (warp == kLoadWarp) {
-        // -------------------------------------------------------------- loads
-        if (lane == 0 && nmax > 0 && !a.hold) {
+        // ------------------------------------------------------ items and loads
+        if (lane == 0) {
             prefetch_tensormap(&maps.q);
-            prefetch_tensormap(PREFIX && it.seq >= 0 ? &maps.kc : &maps.k);
-            prefetch_tensormap(PREFIX && it.seq >= 0 ? &maps.vc : &maps.v);
-            mbar_arrive_expect_tx(&bar[Ly::bQ], (unsigned)(NT * Ly::H * 128 * a.G * a.TM));
-            for (int i = 0; i < NT; ++i)
-                for (int h = 0; h < Ly::H; ++h)
-                    tma_load_3d(sbase + Ly::Q + i * Ly::Tile + h * 16384, &maps.q, 64 * h, it.kh * a.G, it.t0 + i * a.TM,
-                                &bar[Ly::bQ]);
-            int n = 0;                                       // loads requested: keys 0, values 0, keys 1, ...
-            for (; n < 2 * nmax; ++n) {
-                const int s = n % Ly::Stages, use = n / Ly::Stages;
-                if (use > 0 && !lane_wait(&bar[Ly::bEmpty + s], (use - 1) & 1, abort, a.wait_ns)) break;
-                mbar_arrive_expect_tx(&bar[s], Ly::Tile);
-                const uint32_t dst = sbase + Ly::Ring + s * Ly::Tile;
-                const int pos = it.k0 + (n >> 1) * kKeys;
-                if (PREFIX && it.seq >= 0) {
-                    for (int h = 0; h < Ly::H; ++h)
-                        tma_load_4d(dst + h * 16384, n & 1 ? &maps.vc : &maps.kc, 64 * h, it.kh, pos, it.seq, &bar[s]);
-                } else {
-                    for (int h = 0; h < Ly::H; ++h)
-                        tma_load_3d(dst + h * 16384, n & 1 ? &maps.v : &maps.k, 64 * h, (n & 1 ? a.v_head : a.k_head) + it.kh,
-                                    pos, &bar[s]);
+            prefetch_tensormap(&maps.k);
+            prefetch_tensormap(&maps.v);
+        }
+        int cur = blockIdx.x, published = 0, asked = 0;
+        int loads = 0, queries = 0, s = 0;                   // s: the next load's stage
+        uint32_t refill = 0;                                 // parity of the stages' release this time round
+        bool ok = true;
+        while (ok) {
+            Item it;
+            it.kh = -1;
+            it.nt[0] = it.nt[1] = 0;
+            if (cur >= 0) it = item_of<NT, PREFIX>(a, cur);
+            const int nmax = max(it.nt[0], it.nt[1]);
+            if (PREFIX || nmax > 0 || cur < 0) {             // (rows of no sequence: nothing to do)
+                if (published >= 2)
+                    ok = warp_wait(&bar[Ly::bItemEmpty + (published & 1)], ((published >> 1) - 1) & 1, abort, a.wait_ns);
+                if (!ok) break;
+                if (lane == 0) {
+                    *reinterpret_cast<Item*>(smem + Ly::Items + (published & 1) * kItemBytes) = it;
+                    mbar_arrive(&bar[Ly::bItem + (published & 1)]);
+                }
+                ++published;
+            }
+            if (cur < 0) break;
+            if (lane == 0 && nmax > 0 && !a.hold) {
+                if (queries > 0) ok = lane_wait(&bar[Ly::bQEmpty], (queries - 1) & 1, abort, a.wait_ns);
+                if (ok) {
+                    mbar_arrive_expect_tx(&bar[Ly::bQ], (unsigned)(NT * Ly::H * 128 * a.G * a.TM));
+                    for (int i = 0; i < NT; ++i)
+                        for (int h = 0; h < Ly::H; ++h)
+                            tma_load_3d(sbase + Ly::Q + i * Ly::Tile + h * 16384, &maps.q, 64 * h, it.kh * a.G,
+                                        it.t0 + i * a.TM, &bar[Ly::bQ]);
+                    ++queries;
+                }
+                for (int n = 0; ok && n < 2 * nmax; ++n) {   // keys 0, values 0, keys 1, ...
+                    if (loads >= Ly::Stages) ok = lane_wait(&bar[Ly::bEmpty + s], refill, abort, a.wait_ns);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&bar[s], Ly::Tile);
+                    const uint32_t dst = sbase + Ly::Ring + s * Ly::Tile;
+                    const int pos = it.k0 + (n >> 1) * kKeys;
+                    if (PREFIX && it.seq >= 0) {
+                        for (int h = 0; h < Ly::H; ++h)
+                            tma_load_4d(dst + h * 16384, n & 1 ? &maps.vc : &maps.kc, 64 * h, it.kh, pos, it.seq, &bar[s]);
+                    } else {
+                        for (int h = 0; h < Ly::H; ++h)
+                            tma_load_3d(dst + h * 16384, n & 1 ? &maps.v : &maps.k, 64 * h,
+                                        (n & 1 ? a.v_head : a.k_head) + it.kh, pos, &bar[s]);
+                    }
+                    ++loads;
+                    if (++s == Ly::Stages) {
+                        s = 0;
+                        if (loads > Ly::Stages) refill ^= 1;
+                    }
                 }
             }
-            // no copy is in flight when the block ends
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+            if (!ok) break;
+            // the next item, once all of this one's loads are under way: asked for earlier, the first blocks would
+            // take the long items of a short launch for themselves
+            if (lane == 0) {
+                fence_proxy_async_smem();                    // the last answer has been read
+                mbar_arrive_expect_tx(&bar[Ly::bNext], 16);
+                request_item(sbase + Ly::Next, &bar[Ly::bNext]);
+            }
+            ++asked;
+            ok = warp_wait(&bar[Ly::bNext], (asked - 1) & 1, abort, a.wait_ns);
+            if (ok) cur = requested_item(sbase + Ly::Next);
+        }
+        // no copy and no answer is in flight when the block ends
+        if (lane == 0) {
             const unsigned long long t0 = global_timer_ns();
-            while (!mbar_try_wait(&bar[Ly::bQ], 0) && global_timer_ns() - t0 < kWaitLimitNs) {
-            }
-            for (int j = max(0, n - Ly::Stages); j < n; ++j)
-                while (!mbar_try_wait(&bar[j % Ly::Stages], (j / Ly::Stages) & 1) && global_timer_ns() - t0 < 2 * kWaitLimitNs) {
+            auto drain = [&](uint64_t* b, unsigned parity) {
+                while (!mbar_try_wait(b, parity) && global_timer_ns() - t0 < 2 * kWaitLimitNs) {
                 }
+            };
+            if (asked > 0) drain(&bar[Ly::bNext], (asked - 1) & 1);
+            if (queries > 0) drain(&bar[Ly::bQ], (queries - 1) & 1);
+            for (int j = max(0, loads - Ly::Stages); j < loads; ++j) drain(&bar[j % Ly::Stages], (j / Ly::Stages) & 1);
         }
     } else if (warp == kMmaWarp) {
         // ----------------------------------------------------------- products
-        if (nmax > 0) {
-            const uint32_t lead = elect_lane();
-            constexpr uint32_t id_s = idesc_bf16(kKeys, false), id_o = idesc_bf16(D, true);
-            const uint32_t t0 = __shfl_sync(0xffffffffu, tm, 0);        // uniform, and known to be
-            const uint32_t bars = sbase + Ly::Bar, ring = (sbase + Ly::Ring) >> 4;
-            auto at = [&](int b) { return bars + 8 * b; };
-            // which stage holds a load and whether it has been filled an even number of times: what step n
-            // uses are keys n + 1 and values n, two loads on each time
-            struct Slot {
-                int s = 0;
-                uint32_t parity = 0;
-                __device__ __forceinline__ void advance() {
-                    s += 2;
-                    if (s >= Ly::Stages) {
-                        s -= Ly::Stages;
-                        parity ^= 1;
-                    }
+        const uint32_t lead = elect_lane();
+        constexpr uint32_t id_s = idesc_bf16(kKeys, false), id_o = idesc_bf16(D, true);
+        const uint32_t t0 = __shfl_sync(0xffffffffu, tm, 0);            // uniform, and known to be
+        const uint32_t bars = sbase + Ly::Bar, ring = (sbase + Ly::Ring) >> 4;
+        auto at = [&](int b) { return bars + 8 * b; };
+        // the stage that holds a load, and the parity of its being filled
+        struct Slot {
+            int s;
+            uint32_t parity;
+            __device__ __forceinline__ void advance(int by) {
+                s += by;
+                if (s >= Ly::Stages) {
+                    s -= Ly::Stages;
+                    parity ^= 1;
                 }
-            } k, v;
-            v.s = 1;
-            auto wait = [&](int b, uint32_t parity) { return lane_wait(&bar[b], parity, abort, a.wait_ns); };
+            }
+        } next = {0, 0};                                     // the item's first load
+        auto wait = [&](int b, uint32_t parity) { return lane_wait(&bar[b], parity, abort, a.wait_ns); };
+        uint32_t c0 = 0, c1 = 0;                             // steps of the tiles so far
+        bool ok = true;
+        Item it;
+        for (int k_item = 0, q_item = 0; ok && take(k_item, it); ++k_item) {
+            const int n0 = __shfl_sync(0xffffffffu, it.nt[0], 0), n1 = NT == 2 ? __shfl_sync(0xffffffffu, it.nt[1], 0) : 0;
+            const int nmax = max(n0, n1);
+            if (nmax == 0) continue;
+            Slot k = next, v = next;
+            v.advance(1);
             auto scores = [&](int i, int col) {
                 const uint32_t q = ((sbase + Ly::Q + i * Ly::Tile) >> 4) | kDescK, kd = (ring + k.s * (Ly::Tile >> 4)) | kDescK;
 #pragma unroll
@@ -468,78 +571,91 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                         umma_ts(lead, t0 + Ly::kO + i * D, t0 + col + half * 64 + part * 32 + kk * 8,
                                 vd + (half * 4 + kk) * 128, id_o, half > 0 || part > 0 || kk > 0 ? 1u : add);
             };
-            bool ok = __all_sync(0xffffffffu, wait(Ly::bQ, 0) && wait(0, 0));
+            ok = __all_sync(0xffffffffu, wait(Ly::bQ, q_item & 1) && wait(k.s, k.parity));
+            ++q_item;
+            if (!ok) break;
             tc_fence_after();
-            if (ok) {
+            if (NT == 2) {
 #pragma unroll
                 for (int i = 0; i < NT; ++i)
-                    if (it.nt[i] > 0) {
+                    if ((i ? n1 : n0) > 0) {
                         scores(i, i * 128);
                         commit(lead, at(Ly::bS + i));
                     }
-                commit(lead, at(Ly::bEmpty));
-                k.advance();
-            }
-            if (NT == 2) {
-                // tiles do the same but for the first one's last step, which may come earlier
-                const int n0 = __shfl_sync(0xffffffffu, it.nt[0], 0), n1 = __shfl_sync(0xffffffffu, it.nt[1], 0);
-                for (int n = 0; ok && n < max(n0, n1); ++n) {
+                commit(lead, at(Ly::bEmpty + k.s));
+                if (nmax == 1) commit(lead, at(Ly::bQEmpty));
+                k.advance(2);
+                for (int n = 0; ok && n < nmax; ++n) {
 #pragma unroll
                     for (int i = 0; i < NT; ++i) {
                         const int ni = i ? n1 : n0;
                         if (!ok || n >= ni) continue;
+                        const uint32_t c = (i ? c1 : c0) + n;
                         // (P last: it is what the next products wait for)
-                        ok = wait(v.s, v.parity) && (n + 1 >= ni || wait(k.s, k.parity)) && wait(Ly::bP + 2 * i, n & 1);
+                        ok = wait(v.s, v.parity) && (n + 1 >= ni || wait(k.s, k.parity)) && wait(Ly::bP + 2 * i, c & 1);
                         ok = __all_sync(0xffffffffu, ok);
                         if (!ok) break;
                         tc_fence_after();
                         outputs(i, i * 128, 0, PARTS == 2 ? n % kFlush != 0 : n > 0);
-                        ok = __all_sync(0xffffffffu, wait(Ly::bP + 2 * i + 1, n & 1));
+                        ok = __all_sync(0xffffffffu, wait(Ly::bP + 2 * i + 1, c & 1));
                         if (!ok) break;
                         tc_fence_after();
                         outputs(i, i * 128, 1, 1);
                         if (n + 1 < ni) {
                             scores(i, i * 128);
                             commit(lead, at(Ly::bS + i));
-                            if (i == 1 || n + 1 >= n1) commit(lead, at(Ly::bEmpty + k.s));
+                            if (i == 1 || n + 1 >= n1) {                 // the last tile to use these keys
+                                commit(lead, at(Ly::bEmpty + k.s));
+                                if (n + 2 == nmax) commit(lead, at(Ly::bQEmpty));
+                            }
                         } else {
                             commit(lead, at(Ly::bPV + i));
                         }
-                        if (i == 1 || n >= n1) commit(lead, at(Ly::bEmpty + v.s));   // the last tile to use values n
+                        if (i == 1 || n >= n1) commit(lead, at(Ly::bEmpty + v.s));
                     }
-                    k.advance();
-                    v.advance();
+                    k.advance(2);
+                    v.advance(2);
+                    next.advance(2);
                 }
+                c0 += n0;
+                c1 += n1;
             } else {
-                const int n0 = __shfl_sync(0xffffffffu, it.nt[0], 0);
-                for (int n = 0; ok && n < n0; ++n) {
+                scores(0, (c0 & 1) * 128);
+                commit(lead, at(Ly::bS + (c0 & 1)));
+                commit(lead, at(Ly::bEmpty + k.s));
+                if (nmax == 1) commit(lead, at(Ly::bQEmpty));
+                k.advance(2);
+                for (int n = 0; n < n0; ++n, ++c0) {
+                    const int buf = c0 & 1;
                     if (n + 1 < n0) {
                         ok = __all_sync(0xffffffffu, wait(k.s, k.parity));
                         if (!ok) break;
-                        scores(0, ((n + 1) & 1) * 128);
-                        commit(lead, at(Ly::bS + ((n + 1) & 1)));
+                        scores(0, (buf ^ 1) * 128);
+                        commit(lead, at(Ly::bS + (buf ^ 1)));
                         commit(lead, at(Ly::bEmpty + k.s));
+                        if (n + 2 == n0) commit(lead, at(Ly::bQEmpty));
                     }
                     // (a barrier for each buffer: a warp may be a step ahead of another)
-                    ok = __all_sync(0xffffffffu, wait(v.s, v.parity) && wait(Ly::bP + 2 * (n & 1), (n >> 1) & 1));
+                    ok = __all_sync(0xffffffffu, wait(v.s, v.parity) && wait(Ly::bP + 2 * buf, (c0 >> 1) & 1));
                     if (!ok) break;
                     tc_fence_after();
-                    outputs(0, (n & 1) * 128, 0, PARTS == 2 ? n % kFlush != 0 : n > 0);
-                    ok = __all_sync(0xffffffffu, wait(Ly::bP + 2 * (n & 1) + 1, (n >> 1) & 1));
+                    outputs(0, buf * 128, 0, PARTS == 2 ? n % kFlush != 0 : n > 0);
+                    ok = __all_sync(0xffffffffu, wait(Ly::bP + 2 * buf + 1, (c0 >> 1) & 1));
                     if (!ok) break;
                     tc_fence_after();
-                    outputs(0, (n & 1) * 128, 1, 1);
-                    commit(lead, at(Ly::bPV));
+                    outputs(0, buf * 128, 1, 1);
+                    commit(lead, at(Ly::bPV + buf));
                     commit(lead, at(Ly::bEmpty + v.s));
-                    k.advance();
-                    v.advance();
+                    k.advance(2);
+                    v.advance(2);
+                    next.advance(2);
                 }
             }
-            // nothing reads operands or writes tensor memory when the block ends
-            commit(lead, at(Ly::bDrain));
-            const unsigned long long now = global_timer_ns();
-            while (!mbar_try_wait(&bar[Ly::bDrain], 0) && global_timer_ns() - now < kWaitLimitNs) {
-            }
+        }
+        // nothing reads operands or writes tensor memory when the block ends
+        commit(lead, at(Ly::bDrain));
+        const unsigned long long now = global_timer_ns();
+        while (!mbar_try_wait(&bar[Ly::bDrain], 0) && global_timer_ns() - now < kWaitLimitNs) {
         }
     }
     } else {
@@ -547,261 +663,279 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
         if (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
         const int i = NT == 2 ? warp >> 2 : 0, r = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const int tile_t0 = it.t0 + i * a.TM;
-        const int tok = tile_t0 + r / a.G, head = it.kh * a.G + r % a.G;
-        const bool valid = r < a.TM * a.G && tok >= it.first && tok < it.end;
-        const int nt = NT == 2 && i == 1 ? it.nt[1] : it.nt[0];
-        const int other = NT == 2 ? (i == 1 ? it.nt[0] : it.nt[1]) : 0;
-        // keys [lo, hi] are seen by this row; tiles inside [all_lo, all_hi] by every row of the CTA
-        int lo, hi, all_lo, all_hi;
-        if (PREFIX) {
-            lo = all_lo = it.k0;
-            hi = all_hi = it.k1 - 1;
-        } else if (nmax > 0) {
-            hi = min(max(tok, it.first), it.end - 1);
-            lo = sequence_start(a.cu, a.B, hi);
-            all_lo = sequence_start(a.cu, a.B, it.end - 1);
-            all_hi = it.first;
-        } else {
-            lo = all_lo = 0;
-            hi = all_hi = -1;
-        }
-        const size_t row = (size_t)tok * a.Hq + head;        // of the outputs
-        float* acc = nullptr;                                // where the sums of fp32 outputs lie
-        if (PREFIX)
-            acc = a.part_o + ((size_t)it.part * a.M * a.Hq + row) * D;
-        else if (PARTS == 2)
-            acc = reinterpret_cast<float*>(a.out) + row * D;
         const uint32_t o_col = tm + lanes + Ly::kO + i * D;
-
-        float m = neg_inf(), m_acc = neg_inf(), l = 0.f;
+        const int row_token = r / a.G, row_head = r - row_token * a.G;
+        unsigned steps = 0;                                  // of this tile, in the items before
+        unsigned all_steps = 0;                              // of the CTA
+        unsigned scans = 0, ends = 0;                        // tiles whose values were looked at; items with steps
         bool ok = true;
-        unsigned scans = 0;                                  // tiles whose values were looked at
-        // O added to the sums (what was there times 2^(m_acc - m), unless it is the first time), times mul
-        auto flush = [&](bool fresh, float mul) {
-            const float f = m_acc == neg_inf() ? 0.f : ex2(m_acc - m);
-#pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += 32) {
-                uint32_t o[32];
-                tmem_ld<32>(o_col + c0, o);
-                tmem_ld_done(o);
-                if (valid) {
-                    float4* p = reinterpret_cast<float4*>(acc + c0);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
-                        if (!fresh) w = p[j];
-                        w.x = (w.x * f + __uint_as_float(o[4 * j])) * mul;
-                        w.y = (w.y * f + __uint_as_float(o[4 * j + 1])) * mul;
-                        w.z = (w.z * f + __uint_as_float(o[4 * j + 2])) * mul;
-                        w.w = (w.w * f + __uint_as_float(o[4 * j + 3])) * mul;
-                        p[j] = w;
-                    }
-                }
-                __syncwarp();
+        Item it;
+        for (int k_item = 0; ok && take(k_item, it); ++k_item) {
+            const int tok = it.t0 + i * a.TM + row_token, head = it.kh * a.G + row_head;
+            const bool valid = r < a.TM * a.G && tok >= it.first && tok < it.end;
+            const int nt = NT == 2 && i == 1 ? it.nt[1] : it.nt[0];
+            const int other = NT == 2 ? (i == 1 ? it.nt[0] : it.nt[1]) : 0;
+            // keys [lo, hi] are seen by this row
+            int lo = it.k0, hi = it.k1 - 1;
+            if (!PREFIX) {
+                hi = min(max(tok, it.first), it.end - 1);
+                if (it.all_lo != it.k0) lo = sequence_start(a.cu, a.B, hi);
             }
-            m_acc = m;
-        };
+            const long long row = valid ? (long long)tok * a.Hq + head : -1;         // of the outputs
+            float m = neg_inf(), m_acc = neg_inf(), l = 0.f;
 
-        for (int n = 0; n < nt; ++n) {
-            const int buf = NT == 2 ? i : n & 1;
-            const uint32_t s_col = tm + lanes + buf * 128;
-            const int kb = it.k0 + n * kKeys;
-            const bool part = kb < all_lo || kb + kKeys - 1 > all_hi;   // a row does not see all keys
-            const bool flushed = PARTS == 2 && n > 0 && n % kFlush == 0;
-            float poison = 0.f;
-            uint32_t see[4];                                 // which of the keys the row sees
-            ok = warp_wait(&bar[Ly::bS + buf], (NT == 2 ? n : n >> 1) & 1, abort, a.wait_ns);
-            if (!ok) break;
-            if (part) {
-                const int from = lo - kb, to = hi - kb;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const int f0 = max(from - 32 * q, 0), t0 = min(to - 32 * q, 31);
-                    see[q] = f0 <= t0 && f0 < 32 ? 0xFFFFFFFFu >> (31 - t0) >> f0 << f0 : 0u;
-                }
-                // values that are not finite: their keys noted, then 0 in shared memory. Both tiles'
-                // warps may do so at the same time; marks come first, so that who finds a 0 finds the mark
-                const int load = 2 * n + 1;
-                ok = warp_wait(&bar[load % Ly::Stages], (load / Ly::Stages) & 1, abort, a.wait_ns);
-                if (!ok) break;
-                uint32_t* mark = bad + (n & 3) * 4;
-                const uint32_t v = sbase + Ly::Ring + (load % Ly::Stages) * Ly::Tile;
-#pragma unroll 4
-                for (int e = r; e < Ly::Tile / 16; e += 128) {
-                    uint32_t w[4], inf = 0;
-                    lds_v4_u32(v + e * 16, w[0], w[1], w[2], w[3]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) inf |= (w[j] & 0x7F807F80u) + 0x00800080u;   // carries out of all ones
-                    if (inf & 0x80008000u) {
-                        const int key = (e >> 3) & 127;      // 8 chunks a row; the halves one behind the other
-                        atomicOr(&mark[key >> 5], 1u << (key & 31));
-                        __threadfence_block();
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            if ((w[j] & 0x7F80u) == 0x7F80u) w[j] &= 0xFFFF0000u;
-                            if ((w[j] & 0x7F800000u) == 0x7F800000u) w[j] &= 0x0000FFFFu;
-                        }
-                        sts_v4_u32(v + e * 16, w[0], w[1], w[2], w[3]);
-                    }
-                }
-                fence_proxy_async_smem();
-                warp_arrive(&bar[Ly::bScan + i]);
-                ok = warp_wait(&bar[Ly::bScan + i], scans & 1, abort, a.wait_ns);
-                if (!ok) break;
-                ++scans;
-#pragma unroll
-                for (int w = 0; w < 4; ++w)
-                    if (*reinterpret_cast<volatile uint32_t*>(mark + w) & see[w]) poison = __uint_as_float(0x7FC00000u);
-            }
-            // the marks of the step after the next: no warp is that far, none still at the one before the last
-            if (r == 0 && (i == 0 || n >= other))
-                *reinterpret_cast<uint4*>(bad + ((n + 2) & 3) * 4) = make_uint4(0u, 0u, 0u, 0u);
-            if (flushed) {
-                if (NT == 1) ok = warp_wait(&bar[Ly::bPV], (n - 1) & 1, abort, a.wait_ns);
-                if (!ok) break;
-                tc_fence_after();
-                flush(n == kFlush, 1.f);
-            }
-
-            // P with the reference so far, or, where a score lies too far above it, with the rows' maxima
-            bool raise = n == 0;
+            // O, 32 columns at a time, to where fp32 sums or partial results lie: what is there times 2^(m_acc - m)
+            // (unless this is the first time) plus O, times mul
+            auto flush = [&](bool fresh, float mul) {
+                float* acc = PREFIX ? a.part_o + (size_t)it.part * a.M * a.Hq * D : reinterpret_cast<float*>(a.out);
+                const float f = (m_acc == neg_inf() ? 0.f : ex2(m_acc - m)) * mul;
 #pragma unroll 1
-            while (true) {
-                uint32_t s[4][32];
-                tc_fence_after();
-#pragma unroll
-                for (int q = 0; q < 4; ++q) tmem_ld<32>(s_col + 32 * q, s[q]);
-#pragma unroll
-                for (int q = 0; q < 4; ++q) tmem_ld_done(s[q]);
-                if (part) {
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-#pragma unroll
-                        for (int j = 0; j < 32; ++j)
-                            if (!(see[q] >> j & 1u)) s[q][j] = 0xFF800000u;
-                }
-                float mx[4];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) mx[q] = neg_inf();
-#pragma unroll
-                for (int j = 0; j < 16; ++j)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q)
-                        mx[q] = max3(mx[q], __uint_as_float(s[q][2 * j]), __uint_as_float(s[q][2 * j + 1]));
-                const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * a.c;
-                if (raise) {
-                    const float all = fmaxf(m, top);
-                    const float f = m == neg_inf() ? (all == m ? 1.f : 0.f) : ex2(m - all);
-                    m = all;
-                    l *= f;
-                    if (n > 0 && !flushed) {
-                        if (NT == 1) ok = warp_wait(&bar[Ly::bPV], (n - 1) & 1, abort, a.wait_ns);
-                        if (!ok) break;
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int c0 = 0; c0 < D; c0 += 8) {
-                            uint32_t o[8];
-                            tmem_ld<8>(o_col + c0, o);
-                            tmem_ld_wait();
-#pragma unroll
-                            for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-                            tmem_st(o_col + c0, o);
-                        }
-                    }
-                }
-                const float ms = m == neg_inf() ? 0.f : m;   // a row that has seen no key yet
-                const uint64_t c2 = pair(a.c, a.c), m2 = pair(-ms, -ms);
-                uint64_t l2 = pair(poison, 0.f), l3 = pair(0.f, 0.f);
-                bool again = false;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t hi2[2][16], lo2[2][16];
-#pragma unroll
-                    for (int q = 0; q < 2; ++q)
-#pragma unroll
-                        for (int j = 0; j < 16; ++j) {
-                            float p0, p1;
-                            unpair(fma2(pair(__uint_as_float(s[2 * h + q][2 * j]), __uint_as_float(s[2 * h + q][2 * j + 1])),
-                                        c2, m2), p0, p1);
-                            p0 = ex2(p0);
-                            p1 = ex2(p1);
-                            const uint32_t x = pack2(p0, p1);
-                            hi2[q][j] = x;
-                            uint64_t p = pair(p0, p1);
-                            if (PARTS == 2) {
-                                // the sum takes what the product takes
-                                const float h0 = __uint_as_float(x << 16), h1 = __uint_as_float(x & 0xFFFF0000u);
-                                const uint32_t y = pack2(p0 - h0, p1 - h1);
-                                lo2[q][j] = y;
-                                p = add2(pair(h0, h1), pair(__uint_as_float(y << 16), __uint_as_float(y & 0xFFFF0000u)));
-                            }
-                            if (j & 1) l3 = add2(l3, p); else l2 = add2(l2, p);
-                        }
-                    // (only now, so that the maximum is taken while the exponentials are)
-                    if (h == 0 && !raise &&
-                        __any_sync(0xffffffffu, top > m + kLag || (m == neg_inf() && top > m))) {
-                        again = true;
-                        break;
-                    }
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t o[2][16];
+                    tmem_ld<16>(o_col + c, o[0]);
+                    tmem_ld<16>(o_col + c + 16, o[1]);
+                    tmem_ld_wait();
 #pragma unroll
                     for (int q = 0; q < 2; ++q) {
-                        tmem_st(s_col + 64 * h + 16 * q, hi2[q]);
-                        if constexpr (PARTS == 2) tmem_st(s_col + 64 * h + 32 + 16 * q, lo2[q]);
-                    }
-                    tmem_st_wait();
-                    tc_fence_before();
-                    warp_arrive(&bar[Ly::bP + 2 * buf + h]);
-                }
-                if (again) {
-                    raise = true;
-                    continue;
-                }
-                float x0, x1;
-                unpair(add2(l2, l3), x0, x1);
-                l += x0 + x1;
-                break;
-            }
-            if (!ok) break;
-        }
-
-        // ------------------------------------------------------------ outputs
-        if (nt > 0) {
-            // (one tile: its last product but one may not have completed either)
-            if (ok && NT == 1 && nt > 1) ok = warp_wait(&bar[Ly::bPV], nt & 1, abort, a.wait_ns);
-            if (ok) ok = warp_wait(&bar[Ly::bPV + i], NT == 2 ? 0 : (nt - 1) & 1, abort, a.wait_ns);
-            tc_fence_after();
-        }
-        if (ok && nt > 0) {
-            const float inv = PREFIX ? 1.f : 1.f / l;
-            if (PREFIX || PARTS == 2) {
-                flush(PARTS == 1 || nt <= kFlush, inv);
-                if (PREFIX && valid) a.part_ml[(size_t)it.part * a.M * a.Hq + row] = make_float2(m, l);
-            } else {
-                uint4* p = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + row * D);
-#pragma unroll 1
-                for (int c0 = 0; c0 < D; c0 += 32) {
-                    uint32_t o[32];
-                    tmem_ld<32>(o_col + c0, o);
-                    tmem_ld_done(o);
-                    if (valid) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            uint4 w;
-                            w.x = pack2(__uint_as_float(o[8 * j]) * inv, __uint_as_float(o[8 * j + 1]) * inv);
-                            w.y = pack2(__uint_as_float(o[8 * j + 2]) * inv, __uint_as_float(o[8 * j + 3]) * inv);
-                            w.z = pack2(__uint_as_float(o[8 * j + 4]) * inv, __uint_as_float(o[8 * j + 5]) * inv);
-                            w.w = pack2(__uint_as_float(o[8 * j + 6]) * inv, __uint_as_float(o[8 * j + 7]) * inv);
-                            p[c0 / 8 + j] = w;
+                        for (int j = 0; j < 16; ++j) o[q][j] = __float_as_uint(__uint_as_float(o[q][j]) * mul);
+                        transpose4(o[q]);
+                    }
+#pragma unroll
+                    for (int t = 0; t < 4; ++t) {
+                        const int src = (lane & ~3) + t;
+                        const long long to = __shfl_sync(0xffffffffu, row, src);
+                        const float g = __shfl_sync(0xffffffffu, f, src);
+                        if (to < 0) continue;
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            float4* p = reinterpret_cast<float4*>(acc + to * D + c + 16 * q) + (lane & 3);
+                            float4 w = make_float4(0.f, 0.f, 0.f, 0.f);
+                            if (!fresh) w = *p;
+                            w.x = w.x * g + __uint_as_float(o[q][4 * t]);
+                            w.y = w.y * g + __uint_as_float(o[q][4 * t + 1]);
+                            w.z = w.z * g + __uint_as_float(o[q][4 * t + 2]);
+                            w.w = w.w * g + __uint_as_float(o[q][4 * t + 3]);
+                            *p = w;
                         }
                     }
                     __syncwarp();
                 }
+                m_acc = m;
+            };
+
+            for (int n = 0; n < nt; ++n) {
+                const unsigned step = steps + n;
+                const int buf = NT == 2 ? i : step & 1;
+                const uint32_t s_col = tm + lanes + buf * 128;
+                const int kb = it.k0 + n * kKeys;
+                const bool part = kb < it.all_lo || kb + kKeys - 1 > it.all_hi;      // a row does not see all keys
+                const bool flushed = PARTS == 2 && n > 0 && n % kFlush == 0;
+                uint32_t see[4];                             // which of the keys the row sees
+                uint32_t* mark = bad + ((all_steps + n) & 7) * 4;
+                ok = warp_wait(&bar[Ly::bS + buf], (NT == 2 ? step : step >> 1) & 1, abort, a.wait_ns);
+                if (!ok) break;
+                if (part) {
+                    const int from = lo - kb, to = hi - kb;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        const int f0 = max(from - 32 * q, 0), t0 = min(to - 32 * q, 31);
+                        see[q] = f0 <= t0 && f0 < 32 ? 0xFFFFFFFFu >> (31 - t0) >> f0 << f0 : 0u;
+                    }
+                    // values that are not finite: their keys noted, then 0 in shared memory. Both tiles'
+                    // warps may do so at the same time; marks come first, so that who finds a 0 finds the mark
+                    const unsigned load = 2 * (all_steps + n) + 1;
+                    ok = warp_wait(&bar[load % Ly::Stages], (load / Ly::Stages) & 1, abort, a.wait_ns);
+                    if (!ok) break;
+                    const uint32_t v = sbase + Ly::Ring + (load % Ly::Stages) * Ly::Tile;
+                    uint32_t inf = 0;
+#pragma unroll 8
+                    for (int e = 0; e < Ly::Tile / 16 / 128; ++e) {
+                        uint32_t w[4];
+                        lds_v4_u32(v + (e * 128 + r) * 16, w[0], w[1], w[2], w[3]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) inf |= (w[j] & 0x7F807F80u) + 0x00800080u;   // carries out of all ones
+                    }
+                    if (inf & 0x80008000u) {
+#pragma unroll 1
+                        for (int e = r; e < Ly::Tile / 16; e += 128) {
+                            uint32_t w[4];
+                            lds_v4_u32(v + e * 16, w[0], w[1], w[2], w[3]);
+                            bool any = false;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                if ((w[j] & 0x7F80u) == 0x7F80u) w[j] &= 0xFFFF0000u, any = true;
+                                if ((w[j] & 0x7F800000u) == 0x7F800000u) w[j] &= 0x0000FFFFu, any = true;
+                            }
+                            if (!any) continue;
+                            const int key = (e >> 3) & 127;  // 8 chunks a row; the halves one behind the other
+                            atomicOr(&mark[key >> 5], 1u << (key & 31));
+                            __threadfence_block();
+                            sts_v4_u32(v + e * 16, w[0], w[1], w[2], w[3]);
+                        }
+                        fence_proxy_async_smem();
+                    }
+                    warp_arrive(&bar[Ly::bScan + i]);
+                }
+                // the marks of four steps on: no warp is that far, none still at four steps ago
+                if (r == 0 && (i == 0 || n >= other))
+                    *reinterpret_cast<uint4*>(bad + ((all_steps + n + 4) & 7) * 4) = make_uint4(0u, 0u, 0u, 0u);
+                if (flushed) {
+                    if (NT == 1) ok = warp_wait(&bar[Ly::bPV + (buf ^ 1)], ((step - 1) >> 1) & 1, abort, a.wait_ns);
+                    if (!ok) break;
+                    tc_fence_after();
+                    flush(n == kFlush, 1.f);
+                }
+
+                // P with the reference so far, or, where a score lies too far above it, with the rows' maxima
+                bool raise = n == 0;
+#pragma unroll 1
+                while (true) {
+                    uint32_t s[4][32];
+                    tc_fence_after();
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tmem_ld<32>(s_col + 32 * q, s[q]);
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) tmem_ld_done(s[q]);
+                    if (part) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+#pragma unroll
+                            for (int j = 0; j < 32; ++j)
+                                if (!(see[q] >> j & 1u)) s[q][j] = 0xFF800000u;
+                    }
+                    float mx[4];
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) mx[q] = neg_inf();
+#pragma unroll
+                    for (int j = 0; j < 16; ++j)
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            mx[q] = max3(mx[q], __uint_as_float(s[q][2 * j]), __uint_as_float(s[q][2 * j + 1]));
+                    const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * a.c;
+                    if (raise) {
+                        const float all = fmaxf(m, top);
+                        const float f = m == neg_inf() ? (all == m ? 1.f : 0.f) : ex2(m - all);
+                        m = all;
+                        l *= f;
+                        if (n > 0 && !flushed) {
+                            if (NT == 1) ok = warp_wait(&bar[Ly::bPV + (buf ^ 1)], ((step - 1) >> 1) & 1, abort, a.wait_ns);
+                            if (!ok) break;
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c0 = 0; c0 < D; c0 += 8) {
+                                uint32_t o[8];
+                                tmem_ld<8>(o_col + c0, o);
+                                tmem_ld_wait();
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+                                tmem_st(o_col + c0, o);
+                            }
+                        }
+                    }
+                    const float ms = m == neg_inf() ? 0.f : m;   // a row that has seen no key yet
+                    const uint64_t c2 = pair(a.c, a.c), m2 = pair(-ms, -ms);
+                    uint64_t l2 = pair(0.f, 0.f), l3 = l2;
+                    bool again = false;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t hi2[2][16], lo2[2][16];
+#pragma unroll
+                        for (int q = 0; q < 2; ++q)
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                float p0, p1;
+                                unpair(fma2(pair(__uint_as_float(s[2 * h + q][2 * j]), __uint_as_float(s[2 * h + q][2 * j + 1])),
+                                            c2, m2), p0, p1);
+                                p0 = ex2(p0);
+                                p1 = ex2(p1);
+                                const uint32_t x = pack2(p0, p1);
+                                hi2[q][j] = x;
+                                uint64_t p = pair(p0, p1);
+                                if (PARTS == 2) {
+                                    // the sum takes what the product takes
+                                    const float h0 = __uint_as_float(x << 16), h1 = __uint_as_float(x & 0xFFFF0000u);
+                                    const uint32_t y = pack2(p0 - h0, p1 - h1);
+                                    lo2[q][j] = y;
+                                    p = add2(pair(h0, h1), pair(__uint_as_float(y << 16), __uint_as_float(y & 0xFFFF0000u)));
+                                }
+                                if (j & 1) l3 = add2(l3, p); else l2 = add2(l2, p);
+                            }
+                        // (only now, so that the maximum is taken while the exponentials are)
+                        if (h == 0 && !raise &&
+                            __any_sync(0xffffffffu, top > m + kLag || (m == neg_inf() && top > m))) {
+                            again = true;
+                            break;
+                        }
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            tmem_st(s_col + 64 * h + 16 * q, hi2[q]);
+                            if constexpr (PARTS == 2) tmem_st(s_col + 64 * h + 32 + 16 * q, lo2[q]);
+                        }
+                        tmem_st_wait();
+                        tc_fence_before();
+                        warp_arrive(&bar[Ly::bP + 2 * buf + h]);
+                    }
+                    if (again) {
+                        raise = true;
+                        continue;
+                    }
+                    float x0, x1;
+                    unpair(add2(l2, l3), x0, x1);
+                    l += x0 + x1;
+                    break;
+                }
+                if (!ok) break;
+                if (part) {                                  // a row that sees a key with such a value is NaN
+                    ok = warp_wait(&bar[Ly::bScan + i], scans & 1, abort, a.wait_ns);
+                    if (!ok) break;
+                    ++scans;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w)
+                        if (*reinterpret_cast<volatile uint32_t*>(mark + w) & see[w]) l = __uint_as_float(0x7FC00000u);
+                }
             }
-        } else if (PREFIX && valid && nt == 0) {
-            a.part_ml[(size_t)it.part * a.M * a.Hq + row] = make_float2(neg_inf(), 0.f);
+
+            // -------------------------------------------------------- outputs
+            if (ok && nt > 0) {
+                const unsigned last = steps + nt - 1;
+                ok = NT == 2 ? warp_wait(&bar[Ly::bPV + i], ends & 1, abort, a.wait_ns)
+                             : warp_wait(&bar[Ly::bPV + (last & 1)], (last >> 1) & 1, abort, a.wait_ns);
+                ++ends;
+                tc_fence_after();
+            }
+            if (ok && nt > 0) {
+                const float inv = PREFIX ? 1.f : 1.f / l;
+                if (PREFIX || PARTS == 2) {
+                    flush(PARTS == 1 || nt <= kFlush, inv);
+                    if (PREFIX && valid) a.part_ml[(size_t)it.part * a.M * a.Hq + row] = make_float2(m, l);
+                } else {
+#pragma unroll 1
+                    for (int c = 0; c < D; c += 32) {
+                        uint32_t o[32], w[16];
+                        tmem_ld<32>(o_col + c, o);
+                        tmem_ld_done(o);
+#pragma unroll
+                        for (int j = 0; j < 16; ++j)
+                            w[j] = pack2(__uint_as_float(o[2 * j]) * inv, __uint_as_float(o[2 * j + 1]) * inv);
+                        transpose4(w);
+#pragma unroll
+                        for (int t = 0; t < 4; ++t) {
+                            const long long to = __shfl_sync(0xffffffffu, row, (lane & ~3) + t);
+                            if (to >= 0)
+                                *(reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + to * D + c) + (lane & 3)) =
+                                    make_uint4(w[4 * t], w[4 * t + 1], w[4 * t + 2], w[4 * t + 3]);
+                        }
+                        __syncwarp();
+                    }
+                }
+            } else if (PREFIX && valid && nt == 0) {
+                a.part_ml[(size_t)it.part * a.M * a.Hq + row] = make_float2(neg_inf(), 0.f);
+            }
+            tc_fence_before();
+            steps += nt;
+            all_steps += max(it.nt[0], it.nt[1]);
         }
-        tc_fence_before();
     }
     __syncthreads();
     if (warp == kMmaWarp) {
