@@ -231,20 +231,13 @@ __device__ __forceinline__ void tmem_ld_done(uint32_t (&v)[32]) {
 }
 __device__ __forceinline__ float neg_inf() { return __uint_as_float(0xFF800000u); }
 
-// mbar_try_wait that may sleep for about 20 us before it answers.
-__device__ __forceinline__ bool long_try_wait(uint64_t* bar, unsigned parity) {
-    unsigned ok;
-    asm volatile("{\n\t.reg .pred p;\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-                 "selp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok) : "r"(smem_u32(bar)), "r"(parity), "r"(20000u) : "memory");
-    return ok != 0;
-}
 // A wait of at most limit_ns; false (and *abort set, the error noted) when it
 // runs out, false at once when another wait has.
 __device__ __forceinline__ bool lane_wait(uint64_t* bar, unsigned parity, volatile int* abort,
                                           unsigned long long limit_ns) {
     // reading the timer takes longer than most waits: not before a wait has been a long one
     for (int k = 0; k < kPolls; ++k)
-        if (long_try_wait(bar, parity)) return true;
+        if (mbar_try_wait(bar, parity)) return true;
     const unsigned long long t0 = global_timer_ns();
     while (true) {
         if (mbar_try_wait(bar, parity)) return true;
@@ -442,7 +435,7 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
     };
 
     if (warp >= kMmaWarp) {
-    if (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+    if (NT == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == kLoadWarp) {
         // ------------------------------------------------------ items and loads
         if (lane == 0) {
@@ -660,7 +653,7 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
     }
     } else {
         // ------------------------------------------------------------ softmax
-        if (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
+        if (NT == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
         const int i = NT == 2 ? warp >> 2 : 0, r = threadIdx.x & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t o_col = tm + lanes + Ly::kO + i * D;
@@ -947,7 +940,7 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
 // The parts' results over the prefix and the caches, and the step's own keys, of
 // which there are few: a warp takes a query head of a token, each lane D / 32
 // values of it; own scores and products in binary32.
-constexpr int kMergeThreads = 256;
+constexpr int kMergeThreads = 128;
 struct MergeArgs {
     const uint16_t* qkv;
     const float* part_o;
@@ -963,6 +956,7 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const Merge
     constexpr int N = D / 32;                                 // values of a lane
     constexpr int kOwn = kTileRows / 32;                      // own scores of a lane: up to 128 tokens
     constexpr int kParts = 2 * kPrefixMaxSplits / 32;
+    constexpr int kAhead = 8;
     const int w = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
     allow_dependent_launch();
     grid_dependency_wait();
@@ -999,6 +993,7 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const Merge
 #pragma unroll
     for (int u = 0; u < kOwn; ++u) {
         s[u] = neg_inf();
+#pragma unroll 4
         for (int j = 32 * u; j < min(own, 32 * u + 32); ++j) {
             float k[N], d = 0.f;
             load(key + (size_t)j * W, k);
@@ -1023,21 +1018,28 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const Merge
         const float f = none ? 0.f : ex2(ml[u].x - top);
         l += f * ml[u].y;
         const unsigned there = __ballot_sync(0xffffffffu, !none && 32 * u + lane < a.parts);
-#pragma unroll 4
-        for (int j = 0; j < min(a.parts - 32 * u, 32); ++j) {
-            const float g = __shfl_sync(0xffffffffu, f, j);
-            if (!(there >> j & 1u)) continue;
-            const float* p = a.part_o + ((size_t)(32 * u + j) * a.rows + w) * D + lane * N;
-            if constexpr (N == 4) {
-                const float4 v = *reinterpret_cast<const float4*>(p);
-                o[0] += g * v.x;
-                o[1] += g * v.y;
-                o[2] += g * v.z;
-                o[3] += g * v.w;
-            } else {
-                const float2 v = *reinterpret_cast<const float2*>(p);
-                o[0] += g * v.x;
-                o[1] += g * v.y;
+        // kAhead parts' values are requested before the first is used
+        for (int j0 = 0; j0 < min(a.parts - 32 * u, 32); j0 += kAhead) {
+            float v[kAhead][N];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+#pragma unroll
+                for (int x = 0; x < N; ++x) v[j][x] = 0.f;
+                if (!(there >> (j0 + j) & 1u)) continue;
+                const float* p = a.part_o + ((size_t)(32 * u + j0 + j) * a.rows + w) * D + lane * N;
+                if constexpr (N == 4) {
+                    const float4 t = *reinterpret_cast<const float4*>(p);
+                    v[j][0] = t.x, v[j][1] = t.y, v[j][2] = t.z, v[j][3] = t.w;
+                } else {
+                    const float2 t = *reinterpret_cast<const float2*>(p);
+                    v[j][0] = t.x, v[j][1] = t.y;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const float g = __shfl_sync(0xffffffffu, f, j0 + j);
+#pragma unroll
+                for (int x = 0; x < N; ++x) o[x] += g * v[j][x];
             }
         }
     }
@@ -1046,6 +1048,7 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const Merge
         if (32 * u >= own) break;
         const float f = 32 * u + lane < own ? ex2(s[u] - top) : 0.f;
         l += f;
+#pragma unroll 4
         for (int j = 32 * u; j < min(own, 32 * u + 32); ++j) {
             const float g = __shfl_sync(0xffffffffu, f, j - 32 * u);
             float v[N];
