@@ -10,11 +10,12 @@
 //   themselves), and only the result's top 32 bits are converted, so that an
 //   angle is off by 2^-25 turns at most at any int32 position.
 //
-// Bound by memory: a row is read and written once. A block takes one or
-// kTokens tokens, forms their cosines and sines once for all heads in shared
-// memory, then a group of lanes takes a head: a lane holds two vectors whose
+// Bound by memory: a row is read and written once. A warp takes a row (or, of few
+// rows, some of its heads): it forms the row's cosines and sines once, two or so a
+// lane, then a group of lanes takes a head at a time: a lane holds two vectors whose
 // values pair up (i and i + rot / 2, or neighbours), so that the rotation needs no
-// exchange and the norm a few shuffles.
+// exchange and the norm a few shuffles; what a lane needs of the row stays in its
+// registers from head to head. Several heads are requested ahead.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -28,9 +29,8 @@
 namespace qv {
 namespace {
 
-constexpr int kThreads = 128;
+constexpr int kWarps = 4;                  // of a block
 constexpr int kMaxRot = 256;
-constexpr int kTokens = 4;
 
 // freq / (2 pi) as a fraction of 2^64, whole turns dropped.
 __device__ __forceinline__ uint64_t turns_of(float freq) {
@@ -68,11 +68,6 @@ template <>
 __device__ __forceinline__ void unpack<float4>(const float4& v, float* x) {
     x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
 }
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
 __device__ __forceinline__ void pack(const float* x, uint4& v) {
     v = make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
 }
@@ -80,23 +75,16 @@ __device__ __forceinline__ void pack(const float* x, uint2& v) { v = make_uint2(
 __device__ __forceinline__ void pack(const float* x, float4& v) { v = make_float4(x[0], x[1], x[2], x[3]); }
 
 // V: a lane's vector of VEC values. GS: lanes of a head (a power of two), of
-// which D / (2 VEC) have values. TB: tokens of a block.
-template <typename V, int VEC, int TB>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, int GS, int heads) {
-    __shared__ float2 cs[TB][kMaxRot / 2];
-    const int t0 = blockIdx.x * TB, nt = min(TB, a.M - t0), half = a.rot / 2;
+// which D / (2 VEC) have values. parts: pieces a row's heads are cut into.
+template <typename V, int VEC, int kAhead>
+__global__ void __launch_bounds__(kWarps * 32) rotary_kernel(const RotaryArgs a, int GS, int heads, int parts) {
+    __shared__ float2 tables[kWarps][kMaxRot / 2];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const long long job = (long long)blockIdx.x * kWarps + warp;
+    const int row = (int)(job / parts), part = (int)(job - (long long)row * parts), half = a.rot / 2;
     allow_dependent_launch();
-    grid_dependency_wait();
-    for (int e = threadIdx.x; e < nt * half; e += kThreads) {
-        const int t = e / half, i = e - t * half;
-        const int64_t turn = (int64_t)(turns_of(a.freq[i]) * (uint64_t)(int64_t)a.pos[t0 + t]);
-        float s, c;
-        sincospif((float)(int32_t)(turn >> 32) * 0x1p-31f, &s, &c);
-        cs[t][i] = make_float2(c * a.magnitude, s * a.magnitude);
-    }
-    __syncthreads();
-
-    const int group = threadIdx.x / GS, u = threadIdx.x & (GS - 1);
+    if (row >= a.M) return;
+    const int group = lane / GS, u = lane & (GS - 1), wide = 32 / GS;      // heads a warp takes at a time
     const int nr = a.rot / (2 * VEC), units = a.D / (2 * VEC);
     const bool rotated = u < nr, there = u < units;
     int oa, ob;                                               // the lane's two vectors
@@ -107,107 +95,146 @@ __global__ void __launch_bounds__(kThreads) rotary_kernel(const RotaryArgs a, in
         oa = 2 * VEC * u;
         ob = oa + VEC;
     }
-    const size_t W = (size_t)(a.Hq + 2 * a.Hkv) * a.D;
-    const int wh = 32 / GS, last = (heads + wh - 1) / wh * wh;  // a warp's heads run together
-    for (int t = 0; t < nt; ++t) {
-        float c[VEC], s[VEC];
-#pragma unroll
-        for (int i = 0; i < VEC; ++i) {
-            const float2 v = rotated ? cs[t][VEC * u + i] : make_float2(1.f, 0.f);
-            c[i] = v.x;
-            s[i] = v.y;
+    grid_dependency_wait();
+    float2* cs = tables[warp];
+    {
+        const uint64_t pos = (uint64_t)(int64_t)a.pos[row];
+        for (int i = lane; i < half; i += 32) {
+            float s, c;
+            sincospif((float)(int32_t)((turns_of(a.freq[i]) * pos) >> 32) * 0x1p-31f, &s, &c);
+            cs[i] = make_float2(c * a.magnitude, s * a.magnitude);
         }
-        const V* x = static_cast<const V*>(a.x);
-        V* out = static_cast<V*>(a.out);
-        const size_t row = (size_t)(t0 + t) * W;
-        for (int h = blockIdx.y * (kThreads / GS) + group; h < last; h += gridDim.y * (kThreads / GS)) {
-            const bool in = there && h < heads;
-            const size_t pa = (row + (size_t)h * a.D + oa) / VEC, pb = (row + (size_t)h * a.D + ob) / VEC;
-            V va{}, vb{};
-            if (in) {
-                va = x[pa];
-                vb = x[pb];
+        __syncwarp();
+    }
+    uint64_t c2[VEC / 2], s2[VEC / 2];                        // cosines and sines of the lane's pairs, two by two
+#pragma unroll
+    for (int i = 0; i < VEC / 2; ++i) {
+        const float2 v0 = rotated ? cs[VEC * u + 2 * i] : make_float2(1.f, 0.f);
+        const float2 v1 = rotated ? cs[VEC * u + 2 * i + 1] : make_float2(1.f, 0.f);
+        c2[i] = pair(v0.x, v1.x);
+        s2[i] = pair(v0.y, v1.y);
+    }
+    const float inv_d = 1.f / (float)a.D;
+    const V* x = static_cast<const V*>(a.x) + (size_t)row * (a.Hq + 2 * a.Hkv) * (a.D / VEC);
+    V* out = static_cast<V*>(a.out) + (size_t)row * (a.Hq + 2 * a.Hkv) * (a.D / VEC);
+    const int last = (heads + wide - 1) / wide * wide, stride = parts * wide;
+    for (int h0 = part * wide + group; h0 < last; h0 += kAhead * stride) {
+        V va[kAhead], vb[kAhead];
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int h = h0 + k * stride;
+            va[k] = V{};
+            vb[k] = V{};
+            if (there && h < heads) {
+                va[k] = x[(h * a.D + oa) / VEC];
+                vb[k] = x[(h * a.D + ob) / VEC];
             }
-            if (h >= a.Hq + a.Hkv) {                          // a value head: copied
-                if (in) {
-                    out[pa] = va;
-                    out[pb] = vb;
-                }
-                if (a.q_gamma == nullptr) continue;
+        }
+#pragma unroll
+        for (int k = 0; k < kAhead; ++k) {
+            const int h = h0 + k * stride;
+            if (h - group >= last) break;                     // (the warp's heads run together)
+            const bool in = there && h < heads, value = h >= a.Hq + a.Hkv;   // value heads: copied
+            float px[VEC], qx[VEC];
+            unpack(va[k], px);
+            unpack(vb[k], qx);
+            uint64_t p[VEC / 2], q[VEC / 2];
+#pragma unroll
+            for (int i = 0; i < VEC / 2; ++i) {
+                p[i] = pair(px[2 * i], px[2 * i + 1]);
+                q[i] = pair(qx[2 * i], qx[2 * i + 1]);
             }
-            float p[VEC], q[VEC];
-            unpack(va, p);
-            unpack(vb, q);
             if (a.q_gamma) {
-                float ss = 0.f;
+                uint64_t ss = mul2(p[0], p[0]);
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) ss += p[i] * p[i] + q[i] * q[i];
-                for (int o = GS / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-                const float r = __frcp_rn(__fsqrt_rn(ss / (float)a.D + a.eps));
+                for (int i = 0; i < VEC / 2; ++i) {
+                    if (i > 0) ss = fma2(p[i], p[i], ss);
+                    ss = fma2(q[i], q[i], ss);
+                }
+                float sum, odd;
+                unpair(ss, sum, odd);
+                sum += odd;
+                for (int o = GS / 2; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+                const float r = rsqrtf(sum * inv_d + a.eps);
+                const uint64_t r2 = pair(r, r);
                 const uint16_t* g = h < a.Hq ? a.q_gamma : a.k_gamma;
-                if (in) {
+                if (in && !value) {
 #pragma unroll
-                    for (int i = 0; i < VEC; ++i) {
-                        p[i] = p[i] * r * __uint_as_float((uint32_t)g[oa + i] << 16);
-                        q[i] = q[i] * r * __uint_as_float((uint32_t)g[ob + i] << 16);
+                    for (int i = 0; i < VEC / 2; ++i) {
+                        const uint32_t ga = reinterpret_cast<const uint32_t*>(g + oa)[i];
+                        const uint32_t gb = reinterpret_cast<const uint32_t*>(g + ob)[i];
+                        p[i] = mul2(p[i], mul2(r2, pair(__uint_as_float(ga << 16), __uint_as_float(ga & 0xFFFF0000u))));
+                        q[i] = mul2(q[i], mul2(r2, pair(__uint_as_float(gb << 16), __uint_as_float(gb & 0xFFFF0000u))));
                     }
                 }
             }
-            if (!in || h >= a.Hq + a.Hkv) continue;
-            float y[VEC], z[VEC];
-            if (a.interleaved) {
+            if (!in) continue;
+            if (!value) {
+                float y[VEC], z[VEC];
+                if (a.interleaved) {
+                    float c[VEC], s[VEC], pv[VEC], qv[VEC];
 #pragma unroll
-                for (int i = 0; i < VEC / 2; ++i) {
-                    y[2 * i] = p[2 * i] * c[i] - p[2 * i + 1] * s[i];
-                    y[2 * i + 1] = p[2 * i + 1] * c[i] + p[2 * i] * s[i];
-                    z[2 * i] = q[2 * i] * c[VEC / 2 + i] - q[2 * i + 1] * s[VEC / 2 + i];
-                    z[2 * i + 1] = q[2 * i + 1] * c[VEC / 2 + i] + q[2 * i] * s[VEC / 2 + i];
-                }
-            } else {
+                    for (int i = 0; i < VEC / 2; ++i) {
+                        unpair(c2[i], c[2 * i], c[2 * i + 1]);
+                        unpair(s2[i], s[2 * i], s[2 * i + 1]);
+                        unpair(p[i], pv[2 * i], pv[2 * i + 1]);
+                        unpair(q[i], qv[2 * i], qv[2 * i + 1]);
+                    }
 #pragma unroll
-                for (int i = 0; i < VEC; ++i) {
-                    y[i] = p[i] * c[i] - q[i] * s[i];
-                    z[i] = q[i] * c[i] + p[i] * s[i];
+                    for (int i = 0; i < VEC / 2; ++i) {
+                        y[2 * i] = pv[2 * i] * c[i] - pv[2 * i + 1] * s[i];
+                        y[2 * i + 1] = pv[2 * i + 1] * c[i] + pv[2 * i] * s[i];
+                        z[2 * i] = qv[2 * i] * c[VEC / 2 + i] - qv[2 * i + 1] * s[VEC / 2 + i];
+                        z[2 * i + 1] = qv[2 * i + 1] * c[VEC / 2 + i] + qv[2 * i] * s[VEC / 2 + i];
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < VEC / 2; ++i) {
+                        // (the sign goes into a product's operand: a packed subtraction is an addition)
+                        const uint64_t minus = q[i] ^ 0x8000000080000000ull;
+                        unpair(fma2(minus, s2[i], mul2(p[i], c2[i])), y[2 * i], y[2 * i + 1]);
+                        unpair(fma2(p[i], s2[i], mul2(q[i], c2[i])), z[2 * i], z[2 * i + 1]);
+                    }
                 }
+                pack(y, va[k]);
+                pack(z, vb[k]);
             }
-            pack(y, va);
-            pack(z, vb);
-            out[pa] = va;
-            out[pb] = vb;
+            out[(h * a.D + oa) / VEC] = va[k];
+            out[(h * a.D + ob) / VEC] = vb[k];
         }
     }
 }
 
-template <typename V, int VEC, int TB>
+template <typename V, int VEC, int kAhead>
 cudaError_t launch(const RotaryArgs& a, int GS, int heads, int parts, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ceil_div(a.M, TB), parts);
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3(ceil_div((long long)a.M * parts, kWarps));
+    cfg.blockDim = dim3(kWarps * 32);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, rotary_kernel<V, VEC, TB>, a, GS, heads);
+    return cudaLaunchKernelEx(&cfg, rotary_kernel<V, VEC, kAhead>, a, GS, heads, parts);
 }
 
 template <typename V, int VEC>
-cudaError_t by_tokens(const RotaryArgs& a, int sms, cudaStream_t s) {
+cudaError_t by_rows(const RotaryArgs& a, int sms, cudaStream_t s) {
     int GS = 1;
     while (GS < a.D / (2 * VEC)) GS *= 2;
     const int heads = a.Hq + (a.out == a.x ? 1 : 2) * a.Hkv;
-    // few rows: a head per group, so that the heads of a row are in flight at once
-    if (a.M < 4 * sms) return launch<V, VEC, 1>(a, GS, heads, ceil_div(heads, kThreads / GS), s);
-    return launch<V, VEC, kTokens>(a, GS, heads, 1, s);
+    // few rows: a warp for every 32 / GS heads, so that all heads of a row are in flight at once
+    if (a.M < 4 * sms) return launch<V, VEC, 1>(a, GS, heads, ceil_div(heads, 32 / GS), s);
+    return launch<V, VEC, 4>(a, GS, heads, 1, s);
 }
 
 }  // namespace
 
 cudaError_t launch_rotary(const RotaryArgs& a, bool bf16, int sms, cudaStream_t s) {
-    if (!bf16) return by_tokens<float4, 4>(a, sms, s);
-    if (a.rot % 16 == 0 && a.D % 16 == 0) return by_tokens<uint4, 8>(a, sms, s);
-    return by_tokens<uint2, 4>(a, sms, s);
+    if (!bf16) return by_rows<float4, 4>(a, sms, s);
+    if (a.rot % 16 == 0 && a.D % 16 == 0) return by_rows<uint4, 8>(a, sms, s);
+    return by_rows<uint2, 4>(a, sms, s);
 }
 
 }  // namespace qv

@@ -445,8 +445,9 @@ def qv_attention_verify_kv4(qkv, cache, cache_len, T, Hq, Hkv, scale, out, works
 
 
 # --- rotary positions, whole prompts, a shared prefix ---
-def _head_dim(row: int, Hq: int, Hkv: int) -> int:
-    heads = Hq + 2 * Hkv
+# (calls on few rows are bound by their host time: shapes are taken once, and
+# checks go over locals)
+def _head_dim(row: int, heads: int) -> int:
     if heads < 1 or row % heads != 0:
         raise ValueError("qkv must be [M, (Hq+2Hkv)*D]")
     return row // heads
@@ -459,20 +460,26 @@ def qv_rotary(qkv, positions, inv_freq, Hq, Hkv, out=None, interleaved=False, ma
     [rot/2] fp32, cos and sin times magnitude. With q_gamma and k_gamma [D]
     bf16 every head is RMS-normed first. In place, or to out (value heads are
     then copied)."""
-    M, W = qkv.shape
-    D = _head_dim(W, Hq, Hkv)
-    if out is None:
-        out = qkv
-    elif out.shape != qkv.shape or out.dtype != qkv.dtype:
-        raise ValueError("out must have qkv's shape and dtype")
-    if inv_freq.dim() != 1 or inv_freq.dtype != torch.float32:
+    shape = qkv.shape
+    M, W = shape
+    D = _head_dim(W, Hq + 2 * Hkv)
+    x = _ptr(qkv)
+    y = x
+    if out is not None and out is not qkv:
+        if out.shape != shape or out.dtype != qkv.dtype:
+            raise ValueError("out must have qkv's shape and dtype")
+        y = _ptr(out)
+    half, = inv_freq.shape
+    if inv_freq.dtype != torch.float32:
         raise ValueError("inv_freq must be float32 [rot / 2]")
-    for name, g in (("q_gamma", q_gamma), ("k_gamma", k_gamma)):
-        if g is not None and (g.shape != (D,) or g.dtype != torch.bfloat16):
-            raise ValueError(f"{name} must be bf16 [D]")
-    _check(load().qv_rotary(_ptr(qkv), _dtype(qkv), _per_row(positions, M, torch.int32, "positions"), _ptr(inv_freq), M,
-                            Hq, Hkv, D, 2 * inv_freq.shape[0], 1 if interleaved else 0, magnitude, _ptr(q_gamma),
-                            _ptr(k_gamma), eps, _ptr(out), _stream(stream)))
+    qg = kg = None
+    if q_gamma is not None or k_gamma is not None:
+        for name, g in (("q_gamma", q_gamma), ("k_gamma", k_gamma)):
+            if g is not None and (g.shape != (D,) or g.dtype != torch.bfloat16):
+                raise ValueError(f"{name} must be bf16 [D]")
+        qg, kg = _ptr(q_gamma), _ptr(k_gamma)
+    _check(load().qv_rotary(x, _dtype(qkv), _per_row(positions, M, torch.int32, "positions"), _ptr(inv_freq), M, Hq, Hkv,
+                            D, 2 * half, 1 if interleaved else 0, magnitude, qg, kg, eps, y, _stream(stream)))
 
 
 def qv_rotary_frequencies(rot, base=10000.0, scaling=QV_ROTARY_PLAIN, factor=1.0, trained_length=0.0, fast_turns=32.0,
@@ -492,15 +499,16 @@ def qv_attention_prompt(qkv, cu_rows, Hq, Hkv, scale, out, stream=None):
     (cu_rows [B+1] int32) -> out [M, Hq*D] fp32 or bf16; rows of no sequence are
     left as they were."""
     M, W = qkv.shape
-    D = _head_dim(W, Hq, Hkv)
+    D = _head_dim(W, Hq + 2 * Hkv)
     if qkv.dtype != torch.bfloat16:
         raise ValueError("qkv must be bf16 [M, (Hq+2Hkv)*D]")
-    if cu_rows.dim() != 1 or cu_rows.dtype != torch.int32 or cu_rows.shape[0] < 2:
+    n, = cu_rows.shape
+    if n < 2 or cu_rows.dtype != torch.int32:
         raise ValueError("cu_rows must be int32 [B+1]")
     if out.shape != (M, Hq * D):
         raise ValueError("out must be [M, Hq*D]")
-    _check(load().qv_attention_prompt(_ptr(qkv), _ptr(cu_rows), cu_rows.shape[0] - 1, M, Hq, Hkv, D, scale, _ptr(out),
-                                      _dtype(out), _stream(stream)))
+    _check(load().qv_attention_prompt(_ptr(qkv), _ptr(cu_rows), n - 1, M, Hq, Hkv, D, scale, _ptr(out), _dtype(out),
+                                      _stream(stream)))
 
 
 def qv_attention_prefix_workspace_bytes(B, T, Hq, Hkv, D, P) -> int:
@@ -513,17 +521,17 @@ def qv_attention_verify_prefix(qkv, prefix_k, prefix_v, prefix_len, k_cache, v_c
     prefix, prefix_k / prefix_v [P, Hkv, D] bf16 of prefix_len [1] int32
     positions; k_cache / v_cache [B, Lmax, Hkv, D] hold what follows it ->
     out [B*T, Hq*D] fp32 or bf16."""
-    P, hkv, D = prefix_k.shape
-    B, Lmax = k_cache.shape[:2]
-    if hkv != Hkv or prefix_v.shape != prefix_k.shape:
+    shape, cached, bf16 = prefix_k.shape, k_cache.shape, torch.bfloat16
+    P, hkv, D = shape
+    B, Lmax, khkv, kd = cached
+    if hkv != Hkv or prefix_v.shape != shape:
         raise ValueError("prefix_k, prefix_v must be [P, Hkv, D]")
-    if k_cache.shape != (B, Lmax, Hkv, D) or v_cache.shape != k_cache.shape:
+    if khkv != Hkv or kd != D or v_cache.shape != cached:
         raise ValueError("k_cache, v_cache must be [B, Lmax, Hkv, D]")
-    if qkv.dtype != torch.bfloat16 or qkv.shape != (B * T, (Hq + 2 * Hkv) * D):
+    if qkv.dtype != bf16 or qkv.shape != (B * T, (Hq + 2 * Hkv) * D):
         raise ValueError("qkv must be bf16 [B*T, (Hq+2Hkv)*D]")
-    for t in (prefix_k, prefix_v, k_cache, v_cache):
-        if t.dtype != torch.bfloat16:
-            raise ValueError("the prefix and the caches must be bf16")
+    if prefix_k.dtype != bf16 or prefix_v.dtype != bf16 or k_cache.dtype != bf16 or v_cache.dtype != bf16:
+        raise ValueError("the prefix and the caches must be bf16")
     if out.shape != (B * T, Hq * D):
         raise ValueError("out must be [B*T, Hq*D]")
     if workspace.dtype != torch.uint8:
