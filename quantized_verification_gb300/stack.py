@@ -256,7 +256,8 @@ class VerifyStack:
 
     # ------------------------------------------------------------------ chained layers
     def prepare_chain(self, eps: float = 1e-6, cache_len: int | None = None, head_dim: int = 128,
-                      kv_bits: int = 16, room: int | None = None):
+                      kv_bits: int = 16, room: int | None = None, prefix_len: int | None = None,
+                      rope_base: float | None = None):
         """Norm weights, the step's input residual stream and the output
         buffers of the chained step (enqueue_chain). With cache_len, every
         layer also gets a seeded bf16 KV cache of cache_len positions per
@@ -269,7 +270,16 @@ class VerifyStack:
         with space for `room` more positions per sequence (default: one step's).
         The chain then attends with qv_attention_verify_kv4 and writes each
         layer's rows of the step behind the cached positions; advance_chain
-        makes the accepted ones part of them."""
+        makes the accepted ones part of them.
+
+        prefix_len (bf16 caches): every sequence begins with the same
+        prefix_len positions, which each layer keeps once (prefix_k, prefix_v:
+        seeded, or from a prompt with fill_prefix); the caches hold what
+        follows them, and the chain attends with qv_attention_verify_prefix.
+
+        rope_base: the query and key heads of every layer's rows are RMS-normed
+        and rotated by their positions (qv_rotary) before they are attended to;
+        a row's position counts the prefix and the cached positions."""
         self._w8_only("the layer chain")
         if kv_bits not in (16, 4):
             raise ValueError("kv_bits must be 16 or 4")
@@ -281,6 +291,10 @@ class VerifyStack:
             raise ValueError("cache_len and room must not be negative")
         if kv_bits == 4 and cache_len + (self.gamma + 1 if room is None else room) < 1:
             raise ValueError("a 4-bit cache needs space for at least one position")
+        if prefix_len is not None and (cache_len is None or kv_bits != 16 or prefix_len < 1):
+            raise ValueError("prefix_len must be at least 1 and needs a bf16 cache (cache_len may be 0)")
+        if rope_base is not None and cache_len is None:
+            raise ValueError("rope_base needs a cache_len: without one the chain has no attention")
         h, M, F = self.model["hidden"], self.M, self.model["ffn"]
         dev = self.device
         self.eps = eps
@@ -301,6 +315,8 @@ class VerifyStack:
             assert q % head_dim == 0 and kv % head_dim == 0
             self.head_dim, self.Hq, self.Hkv = head_dim, q // head_dim, kv // head_dim
             self.kv_bits = kv_bits
+            self.prefix_len = prefix_len
+            self._prepare_rotary(rope_base)
             if kv_bits == 4:
                 self._prepare_kv4(cache_len, self.gamma + 1 if room is None else room)
                 return
@@ -313,11 +329,90 @@ class VerifyStack:
                                               outlier_frac=0.0).view(shape) for l in range(self.layers)]
             self.cache_lens = torch.full((self.B,), cache_len, dtype=torch.int32, device=dev)
             T = self.gamma + 1
-            self.ws_attn = torch.empty(qv.qv_attention_workspace_bytes(self.B, T, self.Hq, self.Hkv, head_dim,
-                                                                       cache_len), dtype=torch.uint8, device=dev)
+            if prefix_len is None:
+                n = qv.qv_attention_workspace_bytes(self.B, T, self.Hq, self.Hkv, head_dim, cache_len)
+            else:
+                n = qv.qv_attention_prefix_workspace_bytes(self.B, T, self.Hq, self.Hkv, head_dim, prefix_len)
+                self.prefix_lens = torch.full((1,), prefix_len, dtype=torch.int32, device=dev)
+                self.prefix_k, self.prefix_v = (
+                    [synth.activations(prefix_len, kv, synth.subseed(self.seed, name, l), device=dev,
+                                       outlier_frac=0.0).view(prefix_len, self.Hkv, head_dim)
+                     for l in range(self.layers)] for name in ("prefix_k", "prefix_v"))
+            self.ws_attn = torch.empty(n, dtype=torch.uint8, device=dev)
             # one output buffer per layer (kept for inspection; the chain reads each once)
             self.attn_out = [torch.empty(M, self.Hq * head_dim, dtype=torch.float32, device=dev)
                              for _ in range(self.layers)]
+
+    def _prepare_rotary(self, base):
+        self.rope = None
+        if base is None:
+            return
+        D, dev, T = self.head_dim, self.device, self.gamma + 1
+        self.rope = qv.qv_rotary_frequencies(D, base)[0].to(dev)
+        self.head_norms = [tuple(synth.norm_weights(D, synth.subseed(self.seed, "g", l, name), device=dev)
+                                 for name in ("q", "k")) for l in range(self.layers)]
+        # a row's place in its step, behind the prefix; the cached positions are added at every step
+        self.row_offset = ((self.prefix_len or 0) + torch.arange(T, dtype=torch.int32, device=dev)).view(1, T)
+        self.positions = torch.empty(self.B, T, dtype=torch.int32, device=dev)
+
+    def _rotate(self, rows, positions, l, stream):
+        qg, kg = self.head_norms[l]
+        qv.qv_rotary(rows, positions, self.rope, self.Hq, self.Hkv, q_gamma=qg, k_gamma=kg, eps=self.eps, stream=stream)
+
+    def fill_prefix(self, h: torch.Tensor, stream=None):
+        """Run a prompt's rows h [n, hidden] bf16 (n <= prefix_len) through the
+        chain's layers and keep every layer's keys and values as the prefix that
+        all sequences share: the linears in slices of QV_MAX_M rows, rotary
+        positions, causal attention over the whole prompt (qv_attention_prompt).
+        Returns the residual stream behind the last layer [n, hidden]."""
+        if getattr(self, "prefix_len", None) is None:
+            raise ValueError("fill_prefix needs prepare_chain(cache_len=..., prefix_len=...)")
+        n, hidden = h.shape
+        if hidden != self.model["hidden"] or h.dtype != torch.bfloat16 or not 1 <= n <= self.prefix_len:
+            raise ValueError("h must be bf16 [n, hidden] with 1 <= n <= prefix_len")
+        F, Hq, Hkv, D, dev = self.model["ffn"], self.Hq, self.Hkv, self.head_dim, self.device
+        cur = torch.cuda.current_stream() if stream is None else stream
+        with torch.cuda.stream(cur):
+            step = min(n, qv.QV_MAX_M)
+            ws = torch.zeros(max(qv.qv_workspace_bytes(qv.QV_OP_LINEAR, step, K, N) for _, K, N in self.phases),
+                             dtype=torch.uint8, device=dev)
+            codes = torch.empty(n * max(K for _, K, _ in self.phases), dtype=torch.int8, device=dev)
+            xq = lambda K: codes[: n * K].view(n, K)  # noqa: E731
+            sx = torch.empty(n, device=dev)
+            new = lambda w, dt=torch.bfloat16: torch.empty(n, w, dtype=dt, device=dev)  # noqa: E731
+            res, qkv, y, a = h.clone(), new((Hq + 2 * Hkv) * D), new(hidden), new(F, torch.float32)
+            attn = new(Hq * D)
+            cu = torch.tensor([0, n], dtype=torch.int32, device=dev)
+            positions = torch.arange(n, dtype=torch.int32, device=dev)
+
+            def linear(l, p, out):
+                wq, sw = self.weights[l][p]
+                for r in range(0, n, step):
+                    e = min(n, r + step)
+                    call = qv.qv_w8a8_swiglu if p == 2 else qv.qv_w8a8_linear
+                    call(xq(wq.shape[1])[r:e], sx[r:e], wq, sw, out[r:e], ws)
+
+            for l in range(self.layers):
+                g1, g2 = self.norm_w[l]
+                qv.qv_rmsnorm_quant(res, g1, xq(hidden), sx, delta=None if l == 0 else y, eps=self.eps)
+                linear(l, 0, qkv)
+                if self.rope is not None:
+                    self._rotate(qkv, positions, l, None)
+                heads = qkv.view(n, Hq + 2 * Hkv, D)
+                self.prefix_k[l][:n].copy_(heads[:, Hq:Hq + Hkv])
+                self.prefix_v[l][:n].copy_(heads[:, Hq + Hkv:])
+                qv.qv_attention_prompt(qkv, cu, Hq, Hkv, 1.0 / D ** 0.5, attn)
+                qv.qv_quantize_act(attn, xq(Hq * D), sx)
+                linear(l, 1, y)
+                qv.qv_rmsnorm_quant(res, g2, xq(hidden), sx, delta=y, eps=self.eps)
+                linear(l, 2, a)
+                qv.qv_quantize_act(a, xq(F), sx)
+                linear(l, 3, y)
+            res.add_(y)
+            self.prefix_lens.fill_(n)
+            if self.rope is not None:
+                self.row_offset.copy_(n + torch.arange(self.gamma + 1, dtype=torch.int32, device=dev).view(1, -1))
+        return res
 
     def _prepare_kv4(self, cache_len, room):
         B, T, D, dev = self.B, self.gamma + 1, self.head_dim, self.device
@@ -377,13 +472,15 @@ class VerifyStack:
             KV cache, causal grouped-query attention of the verify tokens
             over the cache and their own keys (qv_attention_verify, fp32; with
             4-bit caches qv_attention_verify_kv4, then the step's rows into
-            the cache), its per-token quantization -> o; without one, o takes the
+            the cache; behind a shared prefix qv_attention_verify_prefix; with
+            rope_base after qv_rotary), its per-token quantization -> o; without one, o takes the
             layer's seeded input; h += o's bf16 output, next block;
           MLP block: x = RMSNorm(h) -> gate|up with SiLU(gate)*up in its
             epilogue (fp32) -> per-token quantization -> down (bf16 output,
             added to h by the next RMSNorm);
           head: x = RMSNorm(h += down_last) -> LM head argmax -> acceptance.
-        Eight launches per layer (ten with attention), plus the final three."""
+        Eight launches per layer (ten with attention, one more for rotary
+        positions and one for a shared prefix), plus the final three."""
         self._enqueue_chain_layers(stream)
         xq = self._xq(self.model["hidden"])
         qv.qv_lm_head_argmax(xq, self.sx, self.lm_wq, self.lm_sw, self.tokens, self.ws,
@@ -406,6 +503,9 @@ class VerifyStack:
         with torch.cuda.stream(cur):
             self.h_res.copy_(self.h0)
         attn = getattr(self, "cache_len", None) is not None
+        if attn and self.rope is not None:
+            with torch.cuda.stream(cur):
+                torch.add(self.cache_lens.view(-1, 1), self.row_offset, out=self.positions)
         for l in range(self.layers):
             g1, g2 = self.norm_w[l]
             xq = self._xq(h)
@@ -414,12 +514,20 @@ class VerifyStack:
             wq, sw = self.weights[l][0]
             qv.qv_w8a8_linear(xq, self.sx, wq, sw, self.y_qkv, ws, stream=stream)
             xq = self._xq(self.phases[1][1])
+            if attn and self.rope is not None:
+                self._rotate(self.y_qkv, self.positions.view(-1), l, stream)
             if attn and self.kv_bits == 4:
                 qv.qv_attention_verify_kv4(self.y_qkv, self.kv4_cache[l], self.cache_lens, self.gamma + 1, self.Hq,
                                            self.Hkv, 1.0 / self.head_dim ** 0.5, self.attn_out[l], self.ws_attn,
                                            block_table=self.block_table, stream=stream)
                 qv.qv_kv4_write(self.y_qkv, self.cache_lens, self.kv4_cache[l], self.gamma + 1, self.Hq, self.Hkv,
                                 block_table=self.block_table, stream=stream)
+                qv.qv_quantize_act(self.attn_out[l], xq, self.sx, stream=stream)
+            elif attn and self.prefix_len is not None:
+                qv.qv_attention_verify_prefix(self.y_qkv, self.prefix_k[l], self.prefix_v[l], self.prefix_lens,
+                                              self.k_cache[l], self.v_cache[l], self.cache_lens, self.gamma + 1,
+                                              self.Hq, self.Hkv, 1.0 / self.head_dim ** 0.5, self.attn_out[l],
+                                              self.ws_attn, stream=stream)
                 qv.qv_quantize_act(self.attn_out[l], xq, self.sx, stream=stream)
             elif attn:
                 qv.qv_attention_verify(self.y_qkv, self.k_cache[l], self.v_cache[l], self.cache_lens,

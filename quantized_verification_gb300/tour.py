@@ -3,10 +3,10 @@ profiler's launch list or a per-kernel capture.
 
     python -m quantized_verification_gb300.tour [--passes 2]
 
-Each pass makes the same 23 launches in the same order. Before the first
+Each pass makes the same 27 launches in the same order. Before the first
 pass the set-up quantizes the weights (one quantize_rows_kernel and one
 quantize_weight_w4_kernel launch), so a capture of the second pass filtered
-with ``-k`` on the kernels below skips 24 matching launches (``-s 24 -c 23``):
+with ``-k`` on the kernels below skips 28 matching launches (``-s 28 -c 27``):
 
     quantize_rows_kernel                  per-token int8 activation codes, 5 x 4096
     w8a8_stream_kernel<1, Linear>         5 x 4096 -> 24576 (Qwen3-8B gate+up), fp32 out
@@ -27,6 +27,10 @@ with ``-k`` on the kernels below skips 24 matching launches (``-s 24 -c 23``):
     kv4_read_kernel                       the same positions as bf16
     attn_kv4_kernel<128, 1>               attention of 5 tokens over them, clusters
     attn_kv4_tc_kernel<3>                 the same where the context may reach 16384 positions
+    rotary_kernel                         2048 rows of 32/8 heads rotated and RMS-normed
+    attn_prompt_kernel<128, 2, 1, 0>      attention over them as one prompt, bf16 outputs
+    attn_prompt_kernel<128, 1, 2, 1>      5 tokens behind them as a shared prefix, in parts
+    prefix_merge_kernel<128>              the parts and the own keys together
     token_logprobs_kernel                 log probabilities, entropies and the top 8 of
                                           5 rows x 151936 logits
 
@@ -39,7 +43,7 @@ import torch
 
 from . import build, qv, synth
 
-LAUNCHES_PER_PASS = 23
+LAUNCHES_PER_PASS = 27
 
 
 def main(argv=None):
@@ -105,6 +109,15 @@ def main(argv=None):
     long_table = torch.full((1, 512), -1, dtype=torch.int32, device=dev)
     long_table[0, : L // 32] = torch.arange(L // 32, device=dev)
     ws4 = torch.zeros(qv.qv_attention_kv4_workspace_bytes(1, gm + 1, Hq, Hkv, D, 512), dtype=torch.uint8, device=dev)
+    prompt = torch.randn(L, (Hq + 2 * Hkv) * D, device=dev, generator=g).to(torch.bfloat16)
+    pos = torch.arange(L, dtype=torch.int32, device=dev)
+    freq = qv.qv_rotary_frequencies(D, 1e6)[0].to(dev)
+    gq, gk = synth.norm_weights(D, 6, device=dev), synth.norm_weights(D, 7, device=dev)
+    cu = torch.tensor([0, L], dtype=torch.int32, device=dev)
+    ap = torch.empty(L, Hq * D, dtype=torch.bfloat16, device=dev)
+    own = torch.zeros(1, dtype=torch.int32, device=dev)
+    behind = torch.empty(1, 0, Hkv, D, dtype=torch.bfloat16, device=dev)
+    wsp = torch.empty(qv.qv_attention_prefix_workspace_bytes(1, gm + 1, Hq, Hkv, D, L), dtype=torch.uint8, device=dev)
     lp, ent = torch.empty(B * (gm + 1), device=dev), torch.empty(B * (gm + 1), device=dev)
     tops = torch.empty(B * (gm + 1), 8, dtype=torch.int32, device=dev)
     top_lp = torch.empty(B * (gm + 1), 8, device=dev)
@@ -132,6 +145,10 @@ def main(argv=None):
         qv.qv_attention_verify_kv4(qkv, c4, kv_len, gm + 1, Hq, Hkv, 1.0 / D ** 0.5, attn, ws4)
         qv.qv_attention_verify_kv4(qkv, c4, kv_len, gm + 1, Hq, Hkv, 1.0 / D ** 0.5, attn, ws4,
                                    block_table=long_table)
+        qv.qv_rotary(prompt, pos, freq, Hq, Hkv, q_gamma=gq, k_gamma=gk)
+        qv.qv_attention_prompt(prompt, cu, Hq, Hkv, 1.0 / D ** 0.5, ap)
+        qv.qv_attention_verify_prefix(qkv, kc[0], vc[0], kv_len, behind, behind, own, gm + 1, Hq, Hkv, 1.0 / D ** 0.5,
+                                      attn, wsp)
         qv.qv_token_logprobs(logits, vt.view(-1), lp, entropy=ent, top_tokens=tops, top_logprobs=top_lp)
         torch.cuda.synchronize()
     print(f"ok: {LAUNCHES_PER_PASS} launches per pass, {args.passes} passes")
