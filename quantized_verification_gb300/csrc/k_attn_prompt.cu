@@ -515,6 +515,7 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
             }
         } next = {0, 0};                                     // the item's first load
         auto wait = [&](int b, uint32_t parity) { return lane_wait(&bar[b], parity, abort, a.wait_ns); };
+        auto test = [&](int b, uint32_t parity) { return mbar_test_wait(&bar[b], parity); };
         uint32_t c0 = 0, c1 = 0;                             // steps of the tiles so far
         bool ok = true;
         Item it;
@@ -554,15 +555,18 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                 commit(lead, at(Ly::bEmpty + k.s));
                 if (nmax == 1) commit(lead, at(Ly::bQEmpty));
                 k.advance(2);
+                bool filled = false;                         // whether values n and keys n + 1 are known to be there
                 for (int n = 0; ok && n < nmax; ++n) {
+                    if (!filled) {
+                        ok = __all_sync(0xffffffffu, wait(v.s, v.parity) && (n + 1 >= nmax || wait(k.s, k.parity)));
+                        if (!ok) break;
+                    }
 #pragma unroll
                     for (int i = 0; i < NT; ++i) {
                         const int ni = i ? n1 : n0;
                         if (!ok || n >= ni) continue;
                         const uint32_t c = (i ? c1 : c0) + n;
-                        // (P last: it is what the next products wait for)
-                        ok = wait(v.s, v.parity) && (n + 1 >= ni || wait(k.s, k.parity)) && wait(Ly::bP + 2 * i, c & 1);
-                        ok = __all_sync(0xffffffffu, ok);
+                        ok = __all_sync(0xffffffffu, wait(Ly::bP + 2 * i, c & 1));
                         if (!ok) break;
                         tc_fence_after();
                         outputs(i, i * 128, 0, PARTS == 2 ? n % kFlush != 0 : n > 0);
@@ -570,15 +574,19 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                         if (!ok) break;
                         tc_fence_after();
                         outputs(i, i * 128, 1, 1);
-                        if (n + 1 < ni) {
-                            scores(i, i * 128);
-                            commit(lead, at(Ly::bS + i));
-                            if (i == 1 || n + 1 >= n1) {                 // the last tile to use these keys
-                                commit(lead, at(Ly::bEmpty + k.s));
-                                if (n + 2 == nmax) commit(lead, at(Ly::bQEmpty));
-                            }
-                        } else {
-                            commit(lead, at(Ly::bPV + i));
+                        if (n + 1 < ni) scores(i, i * 128);
+                        if (i == 1 || n >= n1) {             // the last tile to use these keys and values
+                            // a look at the next step's, before the commits wait for the queue of products
+                            Slot kn = k, vn = v;
+                            kn.advance(2);
+                            vn.advance(2);
+                            filled = __all_sync(0xffffffffu, (n + 1 >= nmax || test(vn.s, vn.parity)) &
+                                                                 (n + 2 >= nmax || test(kn.s, kn.parity)));
+                        }
+                        commit(lead, at(n + 1 < ni ? Ly::bS + i : Ly::bPV + i));
+                        if (n + 1 < ni && (i == 1 || n + 1 >= n1)) {
+                            commit(lead, at(Ly::bEmpty + k.s));
+                            if (n + 2 == nmax) commit(lead, at(Ly::bQEmpty));
                         }
                         if (i == 1 || n >= n1) commit(lead, at(Ly::bEmpty + v.s));
                     }
