@@ -1137,8 +1137,9 @@ cudaError_t launch_attention_prompt(const CUtensorMap& q, const CUtensorMap& kv,
     return dispatch<false>(maps, a, D, nt, out_bf16 ? 1 : 2, a.blocks * Hkv, s);
 }
 
-// How the work of a batch behind a prefix is cut: enough parts of the prefix
-// that every SM has one, and of each cache where the sequences alone leave SMs idle.
+// How the work of a batch behind a prefix is cut: enough parts of the prefix that
+// every SM has one; enough of each cache that every SM has one, or up to four of
+// at least three steps, so that a long cache among short ones does not end last.
 struct PrefixCut {
     int nt, blocks, splits, own_max;
 };
@@ -1150,7 +1151,8 @@ static PrefixCut prefix_cut(int B, int T, int Hq, int Hkv, int P, int sms) {
     const long long items = (long long)c.blocks * Hkv, own = (long long)B * Hkv;
     auto clamp = [](long long n, long long hi) { return (int)(n < 1 ? 1 : n > hi ? hi : n); };
     c.splits = clamp(sms / items, P < kKeys * kPrefixMaxSplits ? ceil_div(P, kKeys) : kPrefixMaxSplits);
-    c.own_max = clamp(sms / own, kPrefixMaxSplits);
+    const long long even = 4ll * sms / own < 4 ? 4ll * sms / own : 4;
+    c.own_max = clamp(sms / own > even ? sms / own : even, kPrefixMaxSplits);
     return c;
 }
 
@@ -1173,8 +1175,9 @@ cudaError_t launch_attention_prefix(const PrefixCall& c, int sms, int hold, unsi
     a.G = c.Hq / c.Hkv; a.TM = attention_prompt_tokens(a.G);
     a.Hkv = c.Hkv; a.Hq = c.Hq; a.P = c.P; a.Lmax = c.Lmax;
     a.blocks = cut.blocks; a.splits = cut.splits;
-    const int steps = ceil_div(c.Lmax, kKeys);
-    a.own_splits = steps < cut.own_max ? steps : cut.own_max;
+    // parts of one step where there are SMs for them, else of three
+    const int steps = ceil_div(c.Lmax, kKeys), parts = sms >= c.B * c.Hkv * steps ? steps : ceil_div(steps, 3);
+    a.own_splits = parts < cut.own_max ? parts : cut.own_max;
     a.c = c.scale * kLog2e;
     a.hold = hold; a.wait_ns = wait_ns ? wait_ns : kWaitLimitNs;
     a.part_o = static_cast<float*>(c.ws);

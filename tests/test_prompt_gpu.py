@@ -70,9 +70,9 @@ def test_head_layouts(Hq, Hkv, D, dtype):
 
 @pytest.mark.parametrize("dtype", DTYPES)
 @pytest.mark.parametrize("D", [64, 128])
-@pytest.mark.parametrize("n", [1000, 2100])
+@pytest.mark.parametrize("n", [1000, 1300, 2100])
 def test_many_rows_take_two_tiles(n, D, dtype):
-    # more tiles than SMs: two tiles a thread block, several steps, sums flushed for fp32
+    # above two tiles an SM a thread block takes two, several steps, sums flushed for fp32
     Hq, Hkv = 32, 8
     x = rows(n, Hq, Hkv, D, n)
     check(run(x, [0, n], Hq, Hkv, D, D ** -0.5, dtype), x, [0, n], Hq, Hkv, D ** -0.5)
@@ -86,7 +86,7 @@ def test_long_prompt_one_head(dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("Hq,Hkv", [(4, 1), (32, 8)])
+@pytest.mark.parametrize("Hq,Hkv", [(4, 1), (64, 16)])
 @pytest.mark.parametrize("lens", [[5, 5, 5, 5, 900, 3, 3], [0, 0, 1, 0, 640, 0], [129] * 9, [1] * 300, [64, 64, 127, 1, 65, 500]])
 def test_packed_prompts(lens, Hq, Hkv, dtype):
     cu = cumulated(lens)
@@ -103,7 +103,7 @@ def test_thousands_of_sequences():
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("Hq,Hkv,lens", [(8, 2, [100, 30]), (32, 8, [300, 333])])
+@pytest.mark.parametrize("Hq,Hkv,lens", [(8, 2, [100, 30]), (64, 16, [300, 333])])
 def test_rows_of_no_sequence_may_hold_anything(Hq, Hkv, lens, dtype):
     cu = cumulated(lens, first=45)
     M = cu[-1] + 77
@@ -113,7 +113,7 @@ def test_rows_of_no_sequence_may_hold_anything(Hq, Hkv, lens, dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-@pytest.mark.parametrize("Hq,Hkv,lens", [(8, 2, [150, 60, 40]), (32, 8, [300, 333])])
+@pytest.mark.parametrize("Hq,Hkv,lens", [(8, 2, [150, 60, 40]), (64, 16, [300, 333])])
 @pytest.mark.parametrize("what", ["key", "value", "both"])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
 def test_what_is_not_finite_reaches_only_rows_that_see_it(Hq, Hkv, lens, what, bad, dtype):
@@ -191,6 +191,49 @@ def test_views_streams_graphs_and_repeats():
     check(out, x, [0, 7, 320], Hq, Hkv, 0.1)
 
 
+def test_two_calls_at_once_and_two_graphs():
+    # no workspace: calls on two streams, and graphs replayed at once, do not touch each other
+    Hq, Hkv, D = 16, 4, 128
+    xs = [rows(n, Hq, Hkv, D, n) for n in (500, 777)]
+    cus = [torch.tensor([0, 123, n], dtype=torch.int32, device="cuda") for n in (500, 777)]
+    outs = [torch.zeros(x.shape[0], Hq * D, device="cuda") for x in xs]
+    want = [run(x, c.tolist(), Hq, Hkv, D, 0.1, torch.float32) for x, c in zip(xs, cus)]
+    streams = [torch.cuda.Stream() for _ in xs]
+    graphs = []
+    for k in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            for _ in range(3):
+                qv.qv_attention_prompt(xs[k], cus[k], Hq, Hkv, 0.1, outs[k])
+        graphs.append(g)
+    torch.cuda.synchronize()
+    for k in range(2):
+        with torch.cuda.stream(streams[k]):
+            for _ in range(4):
+                qv.qv_attention_prompt(xs[k], cus[k], Hq, Hkv, 0.1, outs[k], stream=streams[k])
+    torch.cuda.synchronize()
+    for k in range(2):
+        assert torch.equal(outs[k], want[k])
+        outs[k].zero_()
+    torch.cuda.synchronize()
+    for k in range(2):
+        with torch.cuda.stream(streams[k]):
+            graphs[k].replay()
+    torch.cuda.synchronize()
+    for k in range(2):
+        assert torch.equal(outs[k], want[k])
+    assert qv.qv_device_error() == 0
+
+
+def test_results_are_the_same_from_call_to_call():
+    Hq, Hkv, D, n = 32, 8, 128, 2500
+    x = rows(n, Hq, Hkv, D, 14)
+    for dtype in DTYPES:
+        first = run(x, [0, 900, n], Hq, Hkv, D, 0.09, dtype)
+        for _ in range(5):
+            assert torch.equal(run(x, [0, 900, n], Hq, Hkv, D, 0.09, dtype), first)
+
+
 def test_bounds_outside_the_buffer_are_clamped():
     Hq, Hkv, D, n = 4, 2, 64, 90
     x = rows(n, Hq, Hkv, D, 10)
@@ -234,7 +277,7 @@ def test_refusals():
 
 
 def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right():
-    Hq, Hkv, D = 32, 8, 128
+    Hq, Hkv, D = 64, 16, 128
     for n in (64, 700):
         x = rows(n, Hq, Hkv, D, 12)
         qv.qv_debug_set_slot_wait_ns(2_000_000)
