@@ -584,7 +584,7 @@ QV_API qv_status qv_attention_verify_kv4(const uint16_t* qkv, const uint8_t* cac
  *   stays in high precision (gist.science/ja summary, section 2.2 item 3).
  *   qkv       [M][(Hq + 2 Hkv) * D] fp32 or bf16 (dtype), 16-byte aligned
  *   positions [M] int32, any values (negative ones rotate back)
- *   inv_freq  [rot / 2] fp32: pair i of a head (a, b) becomes
+ *   inv_freq  [rot / 2] fp32, finite: pair i of a head (a, b) becomes
  *             (a c - b s, b c + a s), c and s the magnitude times the cosine and
  *             sine of positions[m] * inv_freq[i]. The product is not rounded: an
  *             angle is off by 2e-7 at most, at any position.
@@ -649,7 +649,8 @@ QV_API qv_status qv_rotary_frequencies(int rot, double base, qv_rotary_scaling s
  *             layout of k_cache and v_cache, and what qv_kv4_read gives)
  *   prefix_len [1] int32 on the device (clamped to [0, P]); positions from it on
  *             may hold anything
- *   out       [B*T][Hq * D] fp32 or bf16 (out_dtype), 16-byte aligned
+ *   out       [B*T][Hq * D] fp32 or bf16 (out_dtype), 16-byte aligned; must not
+ *             overlap qkv or the workspace
  *   workspace qv_attention_prefix_workspace_bytes(...) bytes (a host function; 0
  *             for an invalid shape), 16-byte aligned, scratch: needs no initial
  *             value, and must not be shared with calls that may run at the same
@@ -853,8 +854,9 @@ QV_API qv_status qv_device_error(unsigned int* code);
  *   qv_debug_drop_partials(n): the next n such launches publish no split-K
  *     partial sums, so every split tile's head waits out its limit, sets
  *     QV_DEVICE_ERR_SLOT_WAIT and finishes with incomplete sums.
- *   qv_debug_hold_attention_loads(n): the next n qv_attention_verify or
- *     qv_attention_verify_kv4 calls request none of their key/value stages, so every stage wait runs out
+ *   qv_debug_hold_attention_loads(n): the next n qv_attention_verify,
+ *     qv_attention_verify_kv4, qv_attention_prompt or
+ *     qv_attention_verify_prefix calls request none of their key/value stages, so every stage wait runs out
  *     (after the qv_debug_set_slot_wait_ns limit, else 1 s), sets
  *     QV_DEVICE_ERR_FULL_WAIT and the outputs are undefined; no copy is left
  *     in flight, and later calls are unaffected.

@@ -39,7 +39,6 @@
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
-#include <atomic>
 #include <climits>
 #include <cstdint>
 
@@ -261,6 +260,20 @@ __device__ __forceinline__ int sequence_start(const int32_t* __restrict__ cu, in
     return min(max(start, 0), tok);
 }
 
+// The stage that holds a load, and the parity of its being filled.
+struct Slot {
+    int s;
+    uint32_t parity;
+    template <int STAGES>
+    __device__ __forceinline__ void advance(int by) {
+        s += by;
+        if (s >= STAGES) {
+            s -= STAGES;
+            parity ^= 1;
+        }
+    }
+};
+
 // One piece of work: the tiles' first tokens and the key positions they run over.
 struct Item {
     int kh;                   // key/value head, -1: no more work
@@ -420,8 +433,8 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
             prefetch_tensormap(&maps.v);
         }
         int cur = blockIdx.x, published = 0, asked = 0;
-        int loads = 0, queries = 0, s = 0;                   // s: the next load's stage
-        uint32_t refill = 0;                                 // parity of the stages' release this time round
+        int queries = 0, s = 0;                              // s: the next load's stage
+        uint32_t round = 0;                                  // times round the ring, as far as they matter: 0, then 1, 2, 1, ...
         bool ok = true;
         while (ok) {
             Item it;
@@ -451,7 +464,7 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                     ++queries;
                 }
                 for (int n = 0; ok && n < 2 * nmax; ++n) {   // keys 0, values 0, keys 1, ...
-                    if (loads >= Ly::Stages) ok = lane_wait(&bar[Ly::bEmpty + s], refill, abort, a.wait_ns);
+                    if (round > 0) ok = lane_wait(&bar[Ly::bEmpty + s], (round - 1) & 1, abort, a.wait_ns);
                     if (!ok) break;
                     mbar_arrive_expect_tx(&bar[s], Ly::Tile);
                     const uint32_t dst = sbase + Ly::Ring + s * Ly::Tile;
@@ -464,10 +477,9 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                             tma_load_3d(dst + h * 16384, n & 1 ? &maps.v : &maps.k, 64 * h,
                                         (n & 1 ? a.v_head : a.k_head) + it.kh, pos, &bar[s]);
                     }
-                    ++loads;
                     if (++s == Ly::Stages) {
                         s = 0;
-                        if (loads > Ly::Stages) refill ^= 1;
+                        round = round == 1 ? 2 : 1;
                     }
                 }
             }
@@ -493,7 +505,8 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
             };
             if (asked > 0) drain(&bar[Ly::bNext], (asked - 1) & 1);
             if (queries > 0) drain(&bar[Ly::bQ], (queries - 1) & 1);
-            for (int j = max(0, loads - Ly::Stages); j < loads; ++j) drain(&bar[j % Ly::Stages], (j / Ly::Stages) & 1);
+            for (int j = 0; j < Ly::Stages; ++j)             // stages from s on were last filled the time before
+                if (j < s || round > 0) drain(&bar[j], (j < s ? round : round - 1) & 1);
         }
     } else if (warp == kMmaWarp) {
         // ----------------------------------------------------------- products
@@ -502,18 +515,7 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
         const uint32_t t0 = __shfl_sync(0xffffffffu, tm, 0);            // uniform, and known to be
         const uint32_t bars = sbase + Ly::Bar, ring = (sbase + Ly::Ring) >> 4;
         auto at = [&](int b) { return bars + 8 * b; };
-        // the stage that holds a load, and the parity of its being filled
-        struct Slot {
-            int s;
-            uint32_t parity;
-            __device__ __forceinline__ void advance(int by) {
-                s += by;
-                if (s >= Ly::Stages) {
-                    s -= Ly::Stages;
-                    parity ^= 1;
-                }
-            }
-        } next = {0, 0};                                     // the item's first load
+        Slot next = {0, 0};                                  // the item's first load
         auto wait = [&](int b, uint32_t parity) { return lane_wait(&bar[b], parity, abort, a.wait_ns); };
         auto test = [&](int b, uint32_t parity) { return mbar_test_wait(&bar[b], parity); };
         uint32_t c0 = 0, c1 = 0;                             // steps of the tiles so far
@@ -524,7 +526,7 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
             const int nmax = max(n0, n1);
             if (nmax == 0) continue;
             Slot k = next, v = next;
-            v.advance(1);
+            v.template advance<Ly::Stages>(1);
             auto scores = [&](int i, int col) {
                 const uint32_t q = ((sbase + Ly::Q + i * Ly::Tile) >> 4) | kDescK, kd = (ring + k.s * (Ly::Tile >> 4)) | kDescK;
 #pragma unroll
@@ -554,7 +556,7 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                     }
                 commit(lead, at(Ly::bEmpty + k.s));
                 if (nmax == 1) commit(lead, at(Ly::bQEmpty));
-                k.advance(2);
+                k.template advance<Ly::Stages>(2);
                 bool filled = false;                         // whether values n and keys n + 1 are known to be there
                 for (int n = 0; ok && n < nmax; ++n) {
                     if (!filled) {
@@ -578,8 +580,8 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                         if (i == 1 || n >= n1) {             // the last tile to use these keys and values
                             // a look at the next step's, before the commits wait for the queue of products
                             Slot kn = k, vn = v;
-                            kn.advance(2);
-                            vn.advance(2);
+                            kn.template advance<Ly::Stages>(2);
+                            vn.template advance<Ly::Stages>(2);
                             filled = __all_sync(0xffffffffu, (n + 1 >= nmax || test(vn.s, vn.parity)) &
                                                                  (n + 2 >= nmax || test(kn.s, kn.parity)));
                         }
@@ -590,9 +592,9 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                         }
                         if (i == 1 || n >= n1) commit(lead, at(Ly::bEmpty + v.s));
                     }
-                    k.advance(2);
-                    v.advance(2);
-                    next.advance(2);
+                    k.template advance<Ly::Stages>(2);
+                    v.template advance<Ly::Stages>(2);
+                    next.template advance<Ly::Stages>(2);
                 }
                 c0 += n0;
                 c1 += n1;
@@ -601,7 +603,7 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                 commit(lead, at(Ly::bS + (c0 & 1)));
                 commit(lead, at(Ly::bEmpty + k.s));
                 if (nmax == 1) commit(lead, at(Ly::bQEmpty));
-                k.advance(2);
+                k.template advance<Ly::Stages>(2);
                 for (int n = 0; n < n0; ++n, ++c0) {
                     const int buf = c0 & 1;
                     if (n + 1 < n0) {
@@ -623,9 +625,9 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                     outputs(0, buf * 128, 1, 1);
                     commit(lead, at(Ly::bPV + buf));
                     commit(lead, at(Ly::bEmpty + v.s));
-                    k.advance(2);
-                    v.advance(2);
-                    next.advance(2);
+                    k.template advance<Ly::Stages>(2);
+                    v.template advance<Ly::Stages>(2);
+                    next.template advance<Ly::Stages>(2);
                 }
             }
         }
@@ -644,6 +646,7 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
         const int row_token = r / a.G, row_head = r - row_token * a.G;
         unsigned steps = 0;                                  // of this tile, in the items before
         unsigned all_steps = 0;                              // of the CTA
+        Slot values = {1, 0};                                // the stage of the item's first values
         unsigned scans = 0, ends = 0;                        // tiles whose values were looked at; items with steps
         bool ok = true;
         Item it;
@@ -721,10 +724,10 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                     }
                     // values that are not finite: their keys noted, then 0 in shared memory. Both tiles'
                     // warps may do so at the same time; marks come first, so that who finds a 0 finds the mark
-                    const unsigned load = 2 * (all_steps + n) + 1;
-                    ok = warp_wait(&bar[load % Ly::Stages], (load / Ly::Stages) & 1, abort, a.wait_ns);
+                    const int at = values.s + 2 * n, turns = at / Ly::Stages, stage = at - turns * Ly::Stages;
+                    ok = warp_wait(&bar[stage], (values.parity + turns) & 1, abort, a.wait_ns);
                     if (!ok) break;
-                    const uint32_t v = sbase + Ly::Ring + (load % Ly::Stages) * Ly::Tile;
+                    const uint32_t v = sbase + Ly::Ring + stage * Ly::Tile;
                     uint32_t inf = 0;
 #pragma unroll 8
                     for (int e = 0; e < Ly::Tile / 16 / 128; ++e) {
@@ -911,7 +914,11 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
             }
             tc_fence_before();
             steps += nt;
-            all_steps += max(it.nt[0], it.nt[1]);
+            const int nmax = max(it.nt[0], it.nt[1]);
+            all_steps += nmax;
+            const int at = values.s + 2 * nmax, turns = at / Ly::Stages;
+            values.s = at - turns * Ly::Stages;
+            values.parity = (values.parity + turns) & 1;
         }
     }
     __syncthreads();
@@ -1072,18 +1079,9 @@ cudaError_t launch_merge(const MergeArgs& a, cudaStream_t s) {
 template <int D, int NT, int PARTS, bool PREFIX>
 cudaError_t launch(const Maps& maps, const Args& a, int grid, cudaStream_t s) {
     using Ly = Layout<D, NT>;
-    // once for a device, the call costs as much as a small launch
-    static std::atomic<unsigned long long> allowed{0};
-    int dev = 0;
-    cudaError_t e = cudaGetDevice(&dev);
+    cudaError_t e = cudaFuncSetAttribute(attn_prompt_kernel<D, NT, PARTS, PREFIX>,
+                                         cudaFuncAttributeMaxDynamicSharedMemorySize, Ly::Alloc);
     if (e != cudaSuccess) return e;
-    const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
-    if (!(allowed.load(std::memory_order_relaxed) & bit)) {
-        e = cudaFuncSetAttribute(attn_prompt_kernel<D, NT, PARTS, PREFIX>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 Ly::Alloc);
-        if (e != cudaSuccess) return e;
-        allowed.fetch_or(bit, std::memory_order_relaxed);
-    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(Ly::Threads);
@@ -1176,7 +1174,7 @@ cudaError_t launch_attention_prefix(const PrefixCall& c, int sms, int hold, unsi
     a.Hkv = c.Hkv; a.Hq = c.Hq; a.P = c.P; a.Lmax = c.Lmax;
     a.blocks = cut.blocks; a.splits = cut.splits;
     // parts of one step where there are SMs for them, else of three
-    const int steps = ceil_div(c.Lmax, kKeys), parts = sms >= c.B * c.Hkv * steps ? steps : ceil_div(steps, 3);
+    const int steps = ceil_div(c.Lmax, kKeys), parts = sms >= (long long)c.B * c.Hkv * steps ? steps : ceil_div(steps, 3);
     a.own_splits = parts < cut.own_max ? parts : cut.own_max;
     a.c = c.scale * kLog2e;
     a.hold = hold; a.wait_ns = wait_ns ? wait_ns : kWaitLimitNs;

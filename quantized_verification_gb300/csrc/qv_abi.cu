@@ -865,6 +865,8 @@ qv_status qv_attention_prompt(const uint16_t* qkv, const int32_t* cu_rows, int B
     if (!(scale > 0.0f) || scale > 2.0e38f) return fail(QV_ERR_INVALID_ARG, "scale must be in (0, 2e38]");
     if (!aligned(qkv, 16) || !aligned(out, 16) || !aligned(cu_rows, 4))
         return fail(QV_ERR_INVALID_ARG, "qkv and out must be 16-byte aligned, cu_rows 4-byte aligned");
+    if (overlap(qkv, (size_t)M * (Hq + 2 * (size_t)Hkv) * D * 2, out, (size_t)M * Hq * D * (out_dtype == QV_F32 ? 4 : 2)))
+        return fail(QV_ERR_INVALID_ARG, "out must not overlap qkv");
     const int tokens = qv::attention_prompt_tokens(Hq / Hkv);
     if ((long long)((M + tokens - 1) / tokens) * Hkv > 0x7FFFFFFFll)
         return fail(QV_ERR_UNSUPPORTED, "M * Hq is too large for one call");
@@ -927,6 +929,9 @@ qv_status qv_attention_verify_prefix(const uint16_t* qkv, const uint16_t* prefix
     if (!aligned(qkv, 16) || !aligned(prefix_k, 16) || !aligned(prefix_v, 16) || (k_cache && !aligned(k_cache, 16)) ||
         (v_cache && !aligned(v_cache, 16)) || !aligned(cache_len, 4) || !aligned(prefix_len, 4) || !aligned(out, 16))
         return fail(QV_ERR_INVALID_ARG, "qkv, the prefix, the caches and out must be 16-byte aligned, lengths 4-byte aligned");
+    const size_t out_bytes = (size_t)B * T * Hq * D * (out_dtype == QV_F32 ? 4 : 2);
+    if (overlap(qkv, (size_t)B * T * (Hq + 2 * (size_t)Hkv) * D * 2, out, out_bytes))
+        return fail(QV_ERR_INVALID_ARG, "out must not overlap qkv");
     cudaError_t e;
     const int sms = sms_of_current_device(&e);
     if (e != cudaSuccess) return cuda_fail(e, "device query");
@@ -934,6 +939,7 @@ qv_status qv_attention_verify_prefix(const uint16_t* qkv, const uint16_t* prefix
     if (!workspace) return fail(QV_ERR_WORKSPACE, "workspace is null (%zu bytes needed)", need);
     if (!aligned(workspace, 16)) return fail(QV_ERR_WORKSPACE, "workspace must be 16-byte aligned");
     if (workspace_bytes < need) return fail(QV_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
+    if (overlap(workspace, need, out, out_bytes)) return fail(QV_ERR_INVALID_ARG, "out must not overlap the workspace");
     QV_CHECK_DEV(qkv);
     QV_CHECK_DEV(prefix_k);
     QV_CHECK_DEV(prefix_v);

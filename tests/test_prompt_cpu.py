@@ -24,14 +24,14 @@ def prompt(B=1, M=4, Hq=4, Hkv=2, D=64, scale=0.1, out_dtype=0, qkv=FAKE, cu=FAK
 @pytest.mark.parametrize("kw", [dict(B=0), dict(M=0), dict(M=2 ** 24 + 1), dict(Hq=3), dict(Hq=0), dict(Hkv=0), dict(D=96),
                                 dict(Hq=129, Hkv=1), dict(scale=0.0), dict(scale=math.nan), dict(scale=math.inf),
                                 dict(out_dtype=2), dict(qkv=None), dict(cu=None), dict(out=None), dict(qkv=FAKE + 8),
-                                dict(out=FAKE + 8), dict(cu=FAKE + 2)])
+                                dict(out=FAKE + 8), dict(cu=FAKE + 2), dict(out=FAKE + 64), dict(out=FAKE - 16)])
 def test_prompt_refusals(kw):
     assert prompt(**kw) == qv.QV_ERR_INVALID_ARG
     assert qv.load().qv_last_error()
 
 
 def test_prompt_too_many_blocks():
-    assert prompt(M=2 ** 24, Hq=65535, Hkv=65535) == qv.QV_ERR_UNSUPPORTED
+    assert prompt(M=2 ** 24, Hq=65535, Hkv=65535, out=2 ** 50) == qv.QV_ERR_UNSUPPORTED
 
 
 def prefix(B=1, T=1, Hq=4, Hkv=2, D=64, Pm=10, Lmax=5, scale=0.1, out_dtype=0, n=FAKE, kc=FAKE, pk=FAKE, out=FAKE):
@@ -41,7 +41,7 @@ def prefix(B=1, T=1, Hq=4, Hkv=2, D=64, Pm=10, Lmax=5, scale=0.1, out_dtype=0, n
 
 @pytest.mark.parametrize("kw", [dict(B=0), dict(T=0), dict(T=65), dict(Hq=3), dict(D=32), dict(Pm=0), dict(Pm=2 ** 24 + 1),
                                 dict(Lmax=-1), dict(scale=0.0), dict(scale=math.nan), dict(out_dtype=3), dict(n=None),
-                                dict(kc=None), dict(pk=None), dict(pk=FAKE + 2), dict(out=None), dict(out=FAKE + 4)])
+                                dict(kc=None), dict(pk=None), dict(pk=FAKE + 2), dict(out=None), dict(out=FAKE + 4), dict(out=FAKE + 16)])
 def test_prefix_refusals(kw):
     assert prefix(**kw) == qv.QV_ERR_INVALID_ARG
 
