@@ -31,6 +31,18 @@
 // one way), so every kFlush steps O is added in binary32 to the row's sums, which
 // lie where the output goes.
 //
+// Bound by the tensor cores from about 1000 rows on, where S, P and O pass through
+// tensor memory in time. GB300, causal, bf16 outputs: one prompt of 16001 tokens, 64/8
+// heads of 128, 2.45 ms (1710 TFLOP/s, 0.90 of a measured cuBLAS product; 2.67 ms
+// = 0.82 of it where the power limit is reached); 6000 tokens, 32/8 heads, 0.193 ms
+// (heads of 64 0.162, fp32 outputs 0.345); 2043 tokens 31 us; 24 prompts of 33 to
+// 4001 tokens 341 us (1130 TFLOP/s). A step of two tiles takes about 2500 cycles of
+// the 2080 that its 32 products need; a block's first and last steps, whose code and
+// data are cold, 2 to 4 thousand more. 97 tokens: 6 us, of which 2.4 are start and
+// first loads.
+// Prefixes: 64 tokens, 64/8 heads behind 100001 positions 160 us (1310 TFLOP/s with
+// the caches' parts and the merge), 24 sequences of 5 tokens behind 8190, fp32, 50 us.
+//
 // Masked tiles. A key that some row of the CTA does not see may hold anything;
 // its score is replaced before use, and its value must not be multiplied by
 // that row's 0. In tiles with such keys the values that are not finite are
@@ -929,9 +941,14 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
 }
 
 // The parts' results over the prefix and the caches, and the step's own keys, of
-// which there are few: a warp takes a query head of a token, each lane D / 32
-// values of it; own scores and products in binary32.
-constexpr int kMergeThreads = 128;
+// which there are few, become a row's outputs. Of few rows a block takes one: its
+// first warp the own keys, the others every third part, so that the chain is two
+// loads deep however many parts there are. Of many rows a warp takes one, with
+// less to do in all. One pass of qv_attention_verify_prefix, block against warp: 252 rows
+// of 27 parts 11.4 and 14.8 us, 1024 rows of 21 33.0 and 34.9, 3840 rows of 11 59
+// and 54, 4096 rows of 10 163 and 160.
+constexpr int kMergeWarps = 4;
+constexpr int kMergeFewRows = 2048;
 struct MergeArgs {
     const uint16_t* qkv;
     const float* part_o;
@@ -942,16 +959,33 @@ struct MergeArgs {
     void* out;
     int out_bf16;
 };
+// Sums with a reference of their own: outputs (N values a lane) and l (a lane's
+// share), times 2^-top; top is -inf where nothing lies above it (o and l then 0 or
+// NaN as they are).
+template <int N>
+struct Sums {
+    float o[N], l, top;
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int x = 0; x < N; ++x) o[x] = 0.f;
+        l = 0.f;
+        top = neg_inf();
+    }
+    // The lanes' highest, and the reference it gives.
+    __device__ __forceinline__ float reference() {
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+        return top == neg_inf() ? 0.f : top;
+    }
+};
+__device__ __forceinline__ float weight(float top, float of) { return top == neg_inf() ? 1.f : ex2(top - of); }
+
+// Row w over the step's own keys: scores and products in binary32.
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const MergeArgs a) {
-    constexpr int N = D / 32;                                 // values of a lane
+__device__ __forceinline__ void merge_own(const MergeArgs& a, int w, Sums<D / 32>& r) {
+    constexpr int N = D / 32;
     constexpr int kOwn = kTileRows / 32;                      // own scores of a lane: up to 128 tokens
-    constexpr int kParts = 2 * kPrefixMaxSplits / 32;
-    constexpr int kAhead = 8;
-    const int w = blockIdx.x * (kMergeThreads / 32) + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-    allow_dependent_launch();
-    grid_dependency_wait();
-    if (w >= a.rows) return;
+    const int lane = threadIdx.x & 31;
     const int tok = w / a.Hq, head = w - tok * a.Hq, first = tok / a.T * a.T, own = tok - first + 1;
     const size_t W = (size_t)(a.Hq + 2 * a.Hkv) * D;
     const uint16_t* key = a.qkv + (size_t)first * W + (size_t)(a.Hq + head / (a.Hq / a.Hkv)) * D + lane * N;
@@ -971,16 +1005,9 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const Merge
             x[2 * j + 1] = __uint_as_float(v[j] & 0xFFFF0000u);
         }
     };
-    float q[N], top = neg_inf();
+    r.clear();
+    float q[N], s[kOwn];
     load(a.qkv + (size_t)tok * W + (size_t)head * D + lane * N, q);
-    float2 ml[kParts];
-#pragma unroll
-    for (int u = 0; u < kParts; ++u) {
-        ml[u] = make_float2(neg_inf(), 0.f);
-        if (u * 32 + lane < a.parts) ml[u] = a.part_ml[(size_t)(u * 32 + lane) * a.rows + w];
-        top = fmaxf(top, ml[u].x);
-    }
-    float s[kOwn];
 #pragma unroll
     for (int u = 0; u < kOwn; ++u) {
         s[u] = neg_inf();
@@ -991,33 +1018,61 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const Merge
 #pragma unroll
             for (int x = 0; x < N; ++x) d += q[x] * k[x];
 #pragma unroll
-            for (int o = 16; o > 0; o >>= 1) d += __shfl_xor_sync(0xffffffffu, d, o);
+            for (int x = 16; x > 0; x >>= 1) d += __shfl_xor_sync(0xffffffffu, d, x);
             if (j - 32 * u == lane) s[u] = d * a.c;
         }
-        top = fmaxf(top, s[u]);
+        r.top = fmaxf(r.top, s[u]);
     }
+    const float ref = r.reference();
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (top == neg_inf()) top = 0.f;
-    float o[N], l = 0.f;
+    for (int u = 0; u < kOwn; ++u) {
+        if (32 * u >= own) break;
+        const float f = 32 * u + lane < own ? ex2(s[u] - ref) : 0.f;
+        r.l += f;
+#pragma unroll 4
+        for (int j = 32 * u; j < min(own, 32 * u + 32); ++j) {
+            const float g = __shfl_sync(0xffffffffu, f, j - 32 * u);
+            float v[N];
+            load(val + (size_t)j * W, v);
 #pragma unroll
-    for (int x = 0; x < N; ++x) o[x] = 0.f;
+            for (int x = 0; x < N; ++x) r.o[x] += g * v[x];
+        }
+    }
+}
+
+// Row w over the parts at, at + STEP, ...
+template <int D, int STEP>
+__device__ __forceinline__ void merge_parts(const MergeArgs& a, int w, int at, Sums<D / 32>& r) {
+    constexpr int N = D / 32;
+    constexpr int kParts = (2 * kPrefixMaxSplits + STEP * 32 - 1) / (STEP * 32);
+    constexpr int kAhead = 8;
+    const int lane = threadIdx.x & 31, count = (a.parts - at + STEP - 1) / STEP;
+    r.clear();
+    float2 ml[kParts];
 #pragma unroll
     for (int u = 0; u < kParts; ++u) {
-        if (32 * u >= a.parts) break;
-        const bool none = ml[u].x == neg_inf() && ml[u].y == 0.f;   // no position, nothing written
-        const float f = none ? 0.f : ex2(ml[u].x - top);
-        l += f * ml[u].y;
-        const unsigned there = __ballot_sync(0xffffffffu, !none && 32 * u + lane < a.parts);
+        const int j = 32 * u + lane;
+        ml[u] = make_float2(neg_inf(), 0.f);
+        if (j < count) ml[u] = a.part_ml[(size_t)(at + j * STEP) * a.rows + w];
+        r.top = fmaxf(r.top, ml[u].x);
+    }
+    const float ref = r.reference();
+#pragma unroll
+    for (int u = 0; u < kParts; ++u) {
+        if (32 * u >= count) break;
+        const bool none = ml[u].x == neg_inf() && ml[u].y == 0.f;        // no position, nothing written
+        const float f = none ? 0.f : ex2(ml[u].x - ref);
+        r.l += f * ml[u].y;
+        const unsigned there = __ballot_sync(0xffffffffu, !none && 32 * u + lane < count);
         // kAhead parts' values are requested before the first is used
-        for (int j0 = 0; j0 < min(a.parts - 32 * u, 32); j0 += kAhead) {
+        for (int j0 = 0; j0 < min(count - 32 * u, 32); j0 += kAhead) {
             float v[kAhead][N];
 #pragma unroll
             for (int j = 0; j < kAhead; ++j) {
 #pragma unroll
                 for (int x = 0; x < N; ++x) v[j][x] = 0.f;
                 if (!(there >> (j0 + j) & 1u)) continue;
-                const float* p = a.part_o + ((size_t)(32 * u + j0 + j) * a.rows + w) * D + lane * N;
+                const float* p = a.part_o + ((size_t)(at + (32 * u + j0 + j) * STEP) * a.rows + w) * D + lane * N;
                 if constexpr (N == 4) {
                     const float4 t = *reinterpret_cast<const float4*>(p);
                     v[j][0] = t.x, v[j][1] = t.y, v[j][2] = t.z, v[j][3] = t.w;
@@ -1030,50 +1085,86 @@ __global__ void __launch_bounds__(kMergeThreads) prefix_merge_kernel(const Merge
             for (int j = 0; j < kAhead; ++j) {
                 const float g = __shfl_sync(0xffffffffu, f, j0 + j);
 #pragma unroll
-                for (int x = 0; x < N; ++x) o[x] += g * v[j][x];
+                for (int x = 0; x < N; ++x) r.o[x] += g * v[j][x];
             }
         }
     }
+}
+
+template <int D, bool FEW>
+__global__ void __launch_bounds__(kMergeWarps * 32) prefix_merge_kernel(const MergeArgs a) {
+    constexpr int N = D / 32;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    allow_dependent_launch();
+    grid_dependency_wait();
+    auto sum = [](float l) {
 #pragma unroll
-    for (int u = 0; u < kOwn; ++u) {
-        if (32 * u >= own) break;
-        const float f = 32 * u + lane < own ? ex2(s[u] - top) : 0.f;
-        l += f;
-#pragma unroll 4
-        for (int j = 32 * u; j < min(own, 32 * u + 32); ++j) {
-            const float g = __shfl_sync(0xffffffffu, f, j - 32 * u);
-            float v[N];
-            load(val + (size_t)j * W, v);
+        for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+        return l;
+    };
+    Sums<N> r;
+    if constexpr (FEW) {
+        __shared__ float s_o[kMergeWarps][D];
+        __shared__ float2 s_ml[kMergeWarps];
+        const int w = blockIdx.x;
+        if (warp == 0)
+            merge_own<D>(a, w, r);
+        else
+            merge_parts<D, kMergeWarps - 1>(a, w, warp - 1, r);
+        r.l = sum(r.l);
+        if (lane == 0) s_ml[warp] = make_float2(r.top, r.l);
 #pragma unroll
-            for (int x = 0; x < N; ++x) o[x] += g * v[x];
+        for (int x = 0; x < N; ++x) s_o[warp][lane * N + x] = r.o[x];
+        __syncthreads();
+        const int d = threadIdx.x;
+        if (d >= D) return;
+        float m = neg_inf(), num = 0.f, den = 0.f;
+#pragma unroll
+        for (int k = 0; k < kMergeWarps; ++k) m = fmaxf(m, s_ml[k].x);
+#pragma unroll
+        for (int k = 0; k < kMergeWarps; ++k) {
+            const float f = weight(s_ml[k].x, m);
+            num += f * s_o[k][d];
+            den += f * s_ml[k].y;
         }
-    }
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-    const float inv = 1.f / l;
-    if (a.out_bf16) {
-        uint32_t* p = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + (size_t)w * D + lane * N);
-#pragma unroll
-        for (int x = 0; x < N / 2; ++x) p[x] = pack2(o[2 * x] * inv, o[2 * x + 1] * inv);
+        if (a.out_bf16)
+            static_cast<__nv_bfloat16*>(a.out)[(size_t)w * D + d] = __float2bfloat16_rn(num / den);
+        else
+            static_cast<float*>(a.out)[(size_t)w * D + d] = num / den;
     } else {
-        float* p = static_cast<float*>(a.out) + (size_t)w * D + lane * N;
+        const long long w = (long long)blockIdx.x * kMergeWarps + warp;
+        if (w >= a.rows) return;
+        Sums<N> own;
+        merge_own<D>(a, (int)w, own);
+        merge_parts<D, 1>(a, (int)w, 0, r);
+        const float m = fmaxf(r.top, own.top), f = weight(r.top, m), g = weight(own.top, m);
+        const float inv = 1.f / (sum(r.l) * f + sum(own.l) * g);
 #pragma unroll
-        for (int x = 0; x < N; ++x) p[x] = o[x] * inv;
+        for (int x = 0; x < N; ++x) r.o[x] = (r.o[x] * f + own.o[x] * g) * inv;
+        if (a.out_bf16) {
+            uint32_t* p = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + (size_t)w * D + lane * N);
+#pragma unroll
+            for (int x = 0; x < N / 2; ++x) p[x] = pack2(r.o[2 * x], r.o[2 * x + 1]);
+        } else {
+            float* p = static_cast<float*>(a.out) + (size_t)w * D + lane * N;
+#pragma unroll
+            for (int x = 0; x < N; ++x) p[x] = r.o[x];
+        }
     }
 }
 
-template <int D>
+template <int D, bool FEW>
 cudaError_t launch_merge(const MergeArgs& a, cudaStream_t s) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(ceil_div(a.rows, kMergeThreads / 32));
-    cfg.blockDim = dim3(kMergeThreads);
+    cfg.gridDim = dim3(FEW ? a.rows : ceil_div(a.rows, kMergeWarps));
+    cfg.blockDim = dim3(kMergeWarps * 32);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, prefix_merge_kernel<D>, a);
+    return cudaLaunchKernelEx(&cfg, prefix_merge_kernel<D, FEW>, a);
 }
 
 template <int D, int NT, int PARTS, bool PREFIX>
@@ -1188,7 +1279,8 @@ cudaError_t launch_attention_prefix(const PrefixCall& c, int sms, int hold, unsi
     m.parts = a.splits + a.own_splits; m.rows = a.M * c.Hq;
     m.T = c.T; m.Hq = c.Hq; m.Hkv = c.Hkv;
     m.c = a.c; m.out = c.out; m.out_bf16 = c.out_bf16 ? 1 : 0;
-    return c.D == 128 ? launch_merge<128>(m, s) : launch_merge<64>(m, s);
+    if (m.rows <= kMergeFewRows) return c.D == 128 ? launch_merge<128, true>(m, s) : launch_merge<64, true>(m, s);
+    return c.D == 128 ? launch_merge<128, false>(m, s) : launch_merge<64, false>(m, s);
 }
 
 cudaError_t read_and_clear_attn_prompt_error(unsigned* code) {

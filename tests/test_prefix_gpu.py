@@ -138,15 +138,16 @@ def test_what_is_not_finite_in_the_prefix_reaches_every_row(dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
-def test_what_is_not_finite_in_one_cache_or_token_stays_with_those_that_see_it(dtype):
-    B, T, Hq, Hkv, D, P = 3, 3, 8, 2, 128, 200
+@pytest.mark.parametrize("B", [3, 100])                          # few rows and many: two merges
+def test_what_is_not_finite_in_one_cache_or_token_stays_with_those_that_see_it(B, dtype):
+    T, Hq, Hkv, D, P = 3, 8, 2, 128, 200
     x, pk, pv, kc, vc = case(B, T, Hq, Hkv, D, P, 30)
-    lens = [30, 11, 0]
+    lens = [30, 11, 0] + [5] * (B - 3)
     vc[1, 10, :, 7] = float("nan")
     x.view(B, T, Hq + 2 * Hkv, D)[2, 1, Hq:] = float("inf")        # the middle token of the last sequence
     out = run(x, pk, pv, P, kc, vc, lens, T, Hq, Hkv, 0.1, dtype).view(B, T, Hq, D)
     assert not torch.isfinite(out[1, :, :, 7]).any() and not torch.isfinite(out[2, 1:]).any()
-    assert torch.isfinite(out[0]).all() and torch.isfinite(out[2, 0]).all()
+    assert torch.isfinite(out[0]).all() and torch.isfinite(out[2, 0]).all() and torch.isfinite(out[3:]).all()
 
 
 def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right():
@@ -162,6 +163,22 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right():
             qv.qv_debug_hold_attention_loads(0)
             qv.qv_debug_set_slot_wait_ns(0)
         check(run(*args, torch.float32), *args)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("B", [2, 150])
+def test_scores_of_minus_infinity_on_one_side(B, dtype):
+    # own keys that count for nothing beside a prefix, and a prefix that counts for nothing beside own keys
+    T, Hq, Hkv, D, P = 1, 16, 4, 64, 300
+    for own in (True, False):
+        x, pk, pv, kc, vc = case(B, T, Hq, Hkv, D, P, 4)
+        x[:, : Hq * D] = x[:, : Hq * D].abs() + 0.25             # positive queries
+        if own:
+            x[:, Hq * D: (Hq + Hkv) * D], kc[:] = float("-inf"), float("-inf")
+        else:
+            pk[:] = float("-inf")
+        lens = [b % 5 for b in range(B)]
+        check(run(x, pk, pv, P, kc, vc, lens, T, Hq, Hkv, 0.1, dtype), x, pk, pv, P, kc, vc, lens, T, Hq, Hkv, 0.1)
 
 
 def test_lengths_outside_are_clamped_and_graphs_read_them():
