@@ -34,19 +34,21 @@
 // Bound by the tensor cores from about 1000 rows on, where S, P and O pass through
 // tensor memory in time. GB300, causal, bf16 outputs: one prompt of 16001 tokens, 64/8
 // heads of 128, 2.45 ms (1710 TFLOP/s, 0.90 of a measured cuBLAS product; 2.67 ms
-// = 0.82 of it where the power limit is reached); 6000 tokens, 32/8 heads, 0.193 ms
-// (heads of 64 0.162, fp32 outputs 0.345); 2043 tokens 31 us; 24 prompts of 33 to
-// 4001 tokens 341 us (1130 TFLOP/s). A step of two tiles takes about 2500 cycles of
+// = 0.82 of it where the power limit is reached); 6000 tokens, 32/8 heads, 0.188 ms
+// (heads of 64 0.162, fp32 outputs 0.342); 2043 tokens 31 us; 24 prompts of 33 to
+// 4001 tokens 324 us (1190 TFLOP/s). A step of two tiles takes about 2500 cycles of
 // the 2080 that its 32 products need; a block's first and last steps, whose code and
 // data are cold, 2 to 4 thousand more. 97 tokens: 6 us, of which 2.4 are start and
 // first loads.
-// Prefixes: 64 tokens, 64/8 heads behind 100001 positions 160 us (1310 TFLOP/s with
+// Prefixes: 64 tokens, 64/8 heads behind 100001 positions 163 us (1290 TFLOP/s with
 // the caches' parts and the merge), 24 sequences of 5 tokens behind 8190, fp32, 50 us.
 //
 // Masked tiles. A key that some row of the CTA does not see may hold anything;
 // its score is replaced before use, and its value must not be multiplied by
-// that row's 0. In tiles with such keys the values that are not finite are
-// replaced by 0 in shared memory and noted; a row that does see one gets NaN.
+// that row's 0. In a prompt's steps with such keys two more warps replace the values
+// that are not finite by 0 in shared memory and note them; a row that does see one
+// gets NaN. (In the softmax warps the same took 6 % longer over packed prompts.) Behind
+// the end of a prefix or cache lies what no row sees: the softmax warps write 0 over it.
 
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
@@ -83,20 +85,20 @@ struct Layout {
     static constexpr int Q = 0;
     static constexpr int Ring = NT * Tile;
     static constexpr int Bar = Ring + Stages * Tile;
-    // barriers: full, empty [Stages], Q full, empty, S full [2], halves of P [2][2], PV done [2], scan [2], items full,
-    // empty [2], next item, drain
+    // barriers: full, empty [Stages], Q full, empty, S full [2], halves of P [2][2], PV done [2], values looked at [8],
+    // items full, empty [2], next item, drain
     static constexpr int bEmpty = Stages, bQ = 2 * Stages, bQEmpty = bQ + 1, bS = bQEmpty + 1, bP = bS + 2, bPV = bP + 4,
-                         bScan = bPV + 2, bItem = bScan + 2, bItemEmpty = bItem + 2, bNext = bItemEmpty + 2,
+                         bScan = bPV + 2, bItem = bScan + 8, bItemEmpty = bItem + 2, bNext = bItemEmpty + 2,
                          bDrain = bNext + 1, kBars = bDrain + 1;
-    static constexpr int Bad = Bar + (kBars + 1) / 2 * 16;  // keys with values that are not finite [8][4] words
-    static constexpr int Items = Bad + 8 * 16;              // what the CTA works on and what comes next
+    static constexpr int Bad = Bar + (kBars + 1) / 2 * 16;  // keys with values that are not finite [16][4] words
+    static constexpr int Items = Bad + 16 * 16;              // what the CTA works on and what comes next
     static constexpr int Next = Items + 2 * kItemBytes;     // the answer to a request for another block's item
     static constexpr int Misc = Next + 16;                  // tensor memory base, abort word
     static constexpr int Bytes = Misc + 16;
     static constexpr int Alloc = Bytes + 1024;              // slack to align the base to 1024 B
-    // softmax warps, then a warpgroup with the products' and the loads' warps. With
-    // two tiles it hands registers over: 384 threads of 168 become 256 of 208 and
-    // 128 of 88
+    // softmax warps, then a warpgroup with the products', the loads' and two values'
+    // warps. With two tiles it hands registers over: 384 threads of 168 become 256 of
+    // 216 and 128 of 72
     static constexpr int Warps = NT * 4;
     static constexpr int Threads = Warps * 32 + 128;
     // tensor memory columns: S (P over it) of both tiles or buffers, then O
@@ -294,10 +296,14 @@ struct Item {
     int part;                 // prefix: the index of the partial results
     int first, end;           // tokens [first, end) are rows to compute
     int k0, k1;               // prefix: the part's positions; prompts: k0 only
-    int all_lo, all_hi;       // keys that every row sees
+    int all_lo;               // where the last row's sequence begins
+    int whole, rest;          // in steps [whole, rest) every row sees every key
     int nt[2];                // steps of each tile
 };
 static_assert(sizeof(Item) <= kItemBytes, "items fit their slots");
+
+// Whether some row of the item does not see some key of step n.
+__device__ __forceinline__ bool partly(const Item& it, int n) { return n < it.whole || n >= it.rest; }
 
 // The whole warp calls.
 template <int NT, bool PREFIX>
@@ -332,20 +338,22 @@ __device__ __forceinline__ Item item_of(const Args& a, int item) {
         it.nt[0] = it.k1 > it.k0 ? (it.k1 - it.k0 + kKeys - 1) / kKeys : 0;
         if (NT == 2) it.nt[1] = it.t0 + a.TM < it.end ? it.nt[0] : 0;
         it.all_lo = it.k0;
-        it.all_hi = it.k1 - 1;
+        it.whole = 0;
+        it.rest = (it.k1 - it.k0) / kKeys;
     } else {
         it.part = 0;
         it.t0 = (a.blocks - 1 - item) * (NT * a.TM);          // the last rows, which see most, first
         const int c0 = min(max(a.cu[0], 0), a.M), cB = min(max(a.cu[a.B], 0), a.M);
         it.first = max(it.t0, c0);
         it.end = min(it.t0 + NT * a.TM, cB);
-        it.k0 = it.k1 = it.all_lo = it.all_hi = 0;
+        it.k0 = it.k1 = it.all_lo = it.whole = it.rest = 0;
         if (it.first < it.end) {
             // (the lanes' rows do not fall: the first row in the lower half of the warp, the last in the upper)
             const int start = sequence_start(a.cu, a.B, (threadIdx.x & 16) ? it.end - 1 : it.first);
             it.k0 = __shfl_sync(0xffffffffu, start, 0);
             it.all_lo = __shfl_sync(0xffffffffu, start, 31);
-            it.all_hi = it.first;
+            it.whole = (it.all_lo - it.k0 + kKeys - 1) / kKeys;
+            it.rest = (it.first - it.k0 + 1) / kKeys;
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
                 const int e = min(it.t0 + (i + 1) * a.TM, it.end);
@@ -404,15 +412,15 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
     uint32_t* bad = reinterpret_cast<uint32_t*>(smem + Ly::Bad);
     uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(smem + Ly::Misc);
     volatile int* abort = reinterpret_cast<volatile int*>(smem + Ly::Misc + 4);
-    constexpr int kMmaWarp = Ly::Warps, kLoadWarp = kMmaWarp + 1;
+    constexpr int kMmaWarp = Ly::Warps, kLoadWarp = kMmaWarp + 1, kScanWarp = kMmaWarp + 2;   // two of those
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < Ly::kBars; ++s) {
-            const bool halves = s >= Ly::bP && s < Ly::bP + 4, scan = s >= Ly::bScan && s < Ly::bScan + 2;
+            const bool halves = s >= Ly::bP && s < Ly::bP + 4, scan = s >= Ly::bScan && s < Ly::bScan + 8;
             const bool taken = s >= Ly::bItemEmpty && s < Ly::bItemEmpty + 2;
-            mbar_init(&bar[s], halves || scan ? 4 : taken ? Ly::Warps + 1 : 1);
+            mbar_init(&bar[s], halves ? 4 : scan ? 2 : taken ? Ly::Warps + (PREFIX ? 1 : 3) : 1);
         }
-        for (int i = 0; i < 32; ++i) bad[i] = 0;
+        for (int i = 0; i < 64; ++i) bad[i] = 0;
         *abort = 0;
         fence_barrier_init();
     }
@@ -531,6 +539,7 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
         auto wait = [&](int b, uint32_t parity) { return lane_wait(&bar[b], parity, abort, a.wait_ns); };
         auto test = [&](int b, uint32_t parity) { return mbar_test_wait(&bar[b], parity); };
         uint32_t c0 = 0, c1 = 0;                             // steps of the tiles so far
+        uint32_t looks = 0;                                  // steps so far: whose values have been looked at
         bool ok = true;
         Item it;
         for (int k_item = 0, q_item = 0; ok && take(k_item, it); ++k_item) {
@@ -539,6 +548,10 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
             if (nmax == 0) continue;
             Slot k = next, v = next;
             v.template advance<Ly::Stages>(1);
+            // that step looks' values are there, and have been looked at
+            auto there = [&](const Slot& v) {
+                return PREFIX ? wait(v.s, v.parity) : wait(Ly::bScan + (looks & 7), (looks >> 3) & 1);
+            };
             auto scores = [&](int i, int col) {
                 const uint32_t q = ((sbase + Ly::Q + i * Ly::Tile) >> 4) | kDescK, kd = (ring + k.s * (Ly::Tile >> 4)) | kDescK;
 #pragma unroll
@@ -572,9 +585,10 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                 bool filled = false;                         // whether values n and keys n + 1 are known to be there
                 for (int n = 0; ok && n < nmax; ++n) {
                     if (!filled) {
-                        ok = __all_sync(0xffffffffu, wait(v.s, v.parity) && (n + 1 >= nmax || wait(k.s, k.parity)));
+                        ok = __all_sync(0xffffffffu, there(v) && (n + 1 >= nmax || wait(k.s, k.parity)));
                         if (!ok) break;
                     }
+                    ++looks;
 #pragma unroll
                     for (int i = 0; i < NT; ++i) {
                         const int ni = i ? n1 : n0;
@@ -594,8 +608,8 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                             Slot kn = k, vn = v;
                             kn.template advance<Ly::Stages>(2);
                             vn.template advance<Ly::Stages>(2);
-                            filled = __all_sync(0xffffffffu, (n + 1 >= nmax || test(vn.s, vn.parity)) &
-                                                                 (n + 2 >= nmax || test(kn.s, kn.parity)));
+                            const bool vt = PREFIX ? test(vn.s, vn.parity) : test(Ly::bScan + (looks & 7), (looks >> 3) & 1);
+                            filled = __all_sync(0xffffffffu, (n + 1 >= nmax || vt) & (n + 2 >= nmax || test(kn.s, kn.parity)));
                         }
                         commit(lead, at(n + 1 < ni ? Ly::bS + i : Ly::bPV + i));
                         if (n + 1 < ni && (i == 1 || n + 1 >= n1)) {
@@ -627,7 +641,8 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                         if (n + 2 == n0) commit(lead, at(Ly::bQEmpty));
                     }
                     // (a barrier for each buffer: a warp may be a step ahead of another)
-                    ok = __all_sync(0xffffffffu, wait(v.s, v.parity) && wait(Ly::bP + 2 * buf, (c0 >> 1) & 1));
+                    ok = __all_sync(0xffffffffu, there(v) && wait(Ly::bP + 2 * buf, (c0 >> 1) & 1));
+                    ++looks;
                     if (!ok) break;
                     tc_fence_after();
                     outputs(0, buf * 128, 0, PARTS == 2 ? n % kFlush != 0 : n > 0);
@@ -648,6 +663,57 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
         const unsigned long long now = global_timer_ns();
         while (!mbar_try_wait(&bar[Ly::bDrain], 0) && global_timer_ns() - now < kWaitLimitNs) {
         }
+    } else if (!PREFIX) {
+        // ---------------------------------------------- values that are not finite
+        // In steps with keys that some row does not see: noted by key, then 0 in shared memory. The products wait for
+        // these warps in every step, so that the ring is never ahead of them.
+        Slot values = {1, 0};                                // the stage of the step's values
+        uint32_t looks = 0;
+        bool ok = true;
+        Item it;
+        for (int k_item = 0; ok && take(k_item, it); ++k_item) {
+            const int nmax = max(it.nt[0], it.nt[1]);
+            for (int n = 0; n < nmax; ++n, ++looks, values.template advance<Ly::Stages>(2)) {
+                ok = warp_wait(&bar[values.s], values.parity, abort, a.wait_ns);
+                if (!ok) break;
+                if (partly(it, n)) {
+                    uint32_t* mark = bad + (looks & 15) * 4;
+                    const uint32_t at = (warp - kScanWarp) * 32 + lane, v = sbase + Ly::Ring + values.s * Ly::Tile + at * 16;
+#pragma unroll 1
+                    for (int e0 = 0; e0 < Ly::Tile / 1024; e0 += 8) {
+                        uint32_t inf = 0;
+#pragma unroll
+                        for (int e = e0; e < e0 + 8; ++e) {
+                            uint32_t w[4];
+                            lds_v4_u32(v + e * 1024, w[0], w[1], w[2], w[3]);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) inf |= (w[j] & 0x7F807F80u) + 0x00800080u;   // carries out of all ones
+                        }
+                        if (!(inf & 0x80008000u)) continue;
+#pragma unroll 1
+                        for (int e = e0; e < e0 + 8; ++e) {
+                            uint32_t w[4];
+                            lds_v4_u32(v + e * 1024, w[0], w[1], w[2], w[3]);
+                            bool any = false;
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) {
+                                if ((w[j] & 0x7F80u) == 0x7F80u) w[j] &= 0xFFFF0000u, any = true;
+                                if ((w[j] & 0x7F800000u) == 0x7F800000u) w[j] &= 0x0000FFFFu, any = true;
+                            }
+                            if (!any) continue;
+                            const int key = (e * 64 + at) >> 3 & 127;        // 8 chunks a row; the halves one behind the other
+                            sts_v4_u32(v + e * 1024, w[0], w[1], w[2], w[3]);
+                            atomicOr(&mark[key >> 5], 1u << (key & 31));
+                        }
+                    }
+                }
+                fence_proxy_async_smem();
+                // the marks of eight steps on: those of eight steps ago, whose products, which wait for every row's look at
+                // the marks, are done (the ring holds four steps at most)
+                if (warp == kScanWarp && lane < 4) bad[((looks + 8) & 15) * 4 + lane] = 0;
+                warp_arrive(&bar[Ly::bScan + (looks & 7)]);
+            }
+        }
     }
     } else {
         // ------------------------------------------------------------ softmax
@@ -657,16 +723,14 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
         const uint32_t o_col = tm + lanes + Ly::kO + i * D;
         const int row_token = r / a.G, row_head = r - row_token * a.G;
         unsigned steps = 0;                                  // of this tile, in the items before
-        unsigned all_steps = 0;                              // of the CTA
-        Slot values = {1, 0};                                // the stage of the item's first values
-        unsigned scans = 0, ends = 0;                        // tiles whose values were looked at; items with steps
+        unsigned looks = 0, ends = 0;                        // steps of both tiles so far; items with steps of this one
+        Slot values = {1, 0};                                // prefix: the stage of the item's first values
         bool ok = true;
         Item it;
         for (int k_item = 0; ok && take(k_item, it); ++k_item) {
             const int tok = it.t0 + i * a.TM + row_token, head = it.kh * a.G + row_head;
             const bool valid = r < a.TM * a.G && tok >= it.first && tok < it.end;
             const int nt = NT == 2 && i == 1 ? it.nt[1] : it.nt[0];
-            const int other = NT == 2 ? (i == 1 ? it.nt[0] : it.nt[1]) : 0;
             // keys [lo, hi] are seen by this row
             int lo = it.k0, hi = it.k1 - 1;
             if (!PREFIX) {
@@ -721,10 +785,9 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                 const int buf = NT == 2 ? i : step & 1;
                 const uint32_t s_col = tm + lanes + buf * 128;
                 const int kb = it.k0 + n * kKeys;
-                const bool part = kb < it.all_lo || kb + kKeys - 1 > it.all_hi;      // a row does not see all keys
+                const bool part = partly(it, n);
                 const bool flushed = PARTS == 2 && n > 0 && n % kFlush == 0;
                 uint32_t see[4];                             // which of the keys the row sees
-                uint32_t* mark = bad + ((all_steps + n) & 7) * 4;
                 ok = warp_wait(&bar[Ly::bS + buf], (NT == 2 ? step : step >> 1) & 1, abort, a.wait_ns);
                 if (!ok) break;
                 if (part) {
@@ -734,44 +797,7 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                         const int f0 = max(from - 32 * q, 0), t0 = min(to - 32 * q, 31);
                         see[q] = f0 <= t0 && f0 < 32 ? 0xFFFFFFFFu >> (31 - t0) >> f0 << f0 : 0u;
                     }
-                    // values that are not finite: their keys noted, then 0 in shared memory. Both tiles'
-                    // warps may do so at the same time; marks come first, so that who finds a 0 finds the mark
-                    const int at = values.s + 2 * n, turns = at / Ly::Stages, stage = at - turns * Ly::Stages;
-                    ok = warp_wait(&bar[stage], (values.parity + turns) & 1, abort, a.wait_ns);
-                    if (!ok) break;
-                    const uint32_t v = sbase + Ly::Ring + stage * Ly::Tile;
-                    uint32_t inf = 0;
-#pragma unroll 8
-                    for (int e = 0; e < Ly::Tile / 16 / 128; ++e) {
-                        uint32_t w[4];
-                        lds_v4_u32(v + (e * 128 + r) * 16, w[0], w[1], w[2], w[3]);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) inf |= (w[j] & 0x7F807F80u) + 0x00800080u;   // carries out of all ones
-                    }
-                    if (inf & 0x80008000u) {
-#pragma unroll 1
-                        for (int e = r; e < Ly::Tile / 16; e += 128) {
-                            uint32_t w[4];
-                            lds_v4_u32(v + e * 16, w[0], w[1], w[2], w[3]);
-                            bool any = false;
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                if ((w[j] & 0x7F80u) == 0x7F80u) w[j] &= 0xFFFF0000u, any = true;
-                                if ((w[j] & 0x7F800000u) == 0x7F800000u) w[j] &= 0x0000FFFFu, any = true;
-                            }
-                            if (!any) continue;
-                            const int key = (e >> 3) & 127;  // 8 chunks a row; the halves one behind the other
-                            atomicOr(&mark[key >> 5], 1u << (key & 31));
-                            __threadfence_block();
-                            sts_v4_u32(v + e * 16, w[0], w[1], w[2], w[3]);
-                        }
-                        fence_proxy_async_smem();
-                    }
-                    warp_arrive(&bar[Ly::bScan + i]);
                 }
-                // the marks of four steps on: no warp is that far, none still at four steps ago
-                if (r == 0 && (i == 0 || n >= other))
-                    *reinterpret_cast<uint4*>(bad + ((all_steps + n + 4) & 7) * 4) = make_uint4(0u, 0u, 0u, 0u);
                 if (flushed) {
                     if (NT == 1) ok = warp_wait(&bar[Ly::bPV + (buf ^ 1)], ((step - 1) >> 1) & 1, abort, a.wait_ns);
                     if (!ok) break;
@@ -864,6 +890,25 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                             tmem_st(s_col + 64 * h + 16 * q, hi2[q]);
                             if constexpr (PARTS == 2) tmem_st(s_col + 64 * h + 32 + 16 * q, lo2[q]);
                         }
+                        if (PREFIX && h == 0 && part) {      // values behind the end, which may be anything, are 0
+                            const int at = values.s + 2 * n, turns = at / Ly::Stages, stage = at - turns * Ly::Stages;
+                            ok = warp_wait(&bar[stage], (values.parity + turns) & 1, abort, a.wait_ns);
+                            if (!ok) break;
+#pragma unroll 4
+                            for (int e = r; e < Ly::Tile / 16; e += 128)     // 8 chunks a row; the halves one behind the other
+                                if ((e >> 3 & 127) >= it.k1 - kb)
+                                    sts_v4_u32(sbase + Ly::Ring + stage * Ly::Tile + e * 16, 0u, 0u, 0u, 0u);
+                            fence_proxy_async_smem();
+                        }
+                        if (!PREFIX && h == 1 && part) {     // a row that sees a key whose value is not finite is NaN
+                            const unsigned look = looks + n;
+                            ok = warp_wait(&bar[Ly::bScan + (look & 7)], (look >> 3) & 1, abort, a.wait_ns);
+                            if (!ok) break;
+                            const volatile uint32_t* mark = bad + (look & 15) * 4;
+#pragma unroll
+                            for (int w = 0; w < 4; ++w)
+                                if (mark[w] & see[w]) l = __uint_as_float(0x7FC00000u);
+                        }
                         tmem_st_wait();
                         tc_fence_before();
                         warp_arrive(&bar[Ly::bP + 2 * buf + h]);
@@ -878,14 +923,6 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                     break;
                 }
                 if (!ok) break;
-                if (part) {                                  // a row that sees a key with such a value is NaN
-                    ok = warp_wait(&bar[Ly::bScan + i], scans & 1, abort, a.wait_ns);
-                    if (!ok) break;
-                    ++scans;
-#pragma unroll
-                    for (int w = 0; w < 4; ++w)
-                        if (*reinterpret_cast<volatile uint32_t*>(mark + w) & see[w]) l = __uint_as_float(0x7FC00000u);
-                }
             }
 
             // -------------------------------------------------------- outputs
@@ -927,7 +964,7 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
             tc_fence_before();
             steps += nt;
             const int nmax = max(it.nt[0], it.nt[1]);
-            all_steps += nmax;
+            looks += nmax;
             const int at = values.s + 2 * nmax, turns = at / Ly::Stages;
             values.s = at - turns * Ly::Stages;
             values.parity = (values.parity + turns) & 1;

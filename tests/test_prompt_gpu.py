@@ -289,3 +289,27 @@ def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_right():
             qv.qv_debug_hold_attention_loads(0)
             qv.qv_debug_set_slot_wait_ns(0)
         check(run(x, [0, n], Hq, Hkv, D, 0.1, torch.bfloat16), x, [0, n], Hq, Hkv, 0.1)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("lens", [[1500], [700, 801], [2100, 3, 40]])
+def test_values_that_are_not_finite_far_into_a_prompt(lens, D, dtype):
+    # steps in which every row sees every key lie between those whose values are looked at; blocks of one and of two tiles
+    for Hq, Hkv in ((8, 2), (32, 8)):
+        cu = cumulated(lens)
+        x = rows(cu[-1], Hq, Hkv, D, sum(lens))
+        clean = run(x, cu, Hq, Hkv, D, 0.1, dtype)
+        check(clean, x, cu, Hq, Hkv, 0.1)
+        v = x.view(-1, Hq + 2 * Hkv, D)[:, Hq + Hkv:]
+        for seq, n in enumerate(lens):
+            for at in sorted({n - 1, n * 3 // 4, n // 2 + 1}):
+                tok = cu[seq] + at
+                kept = v[tok].clone()
+                v[tok] = float("inf") if at % 2 else float("nan")
+                out = run(x, cu, Hq, Hkv, D, 0.1, dtype)
+                v[tok] = kept
+                saw = torch.zeros(cu[-1], dtype=torch.bool, device="cuda")
+                saw[tok:cu[seq + 1]] = True
+                assert torch.equal(out[~saw], clean[~saw]) and not torch.isfinite(out[saw]).any()
+    assert qv.qv_device_error() == 0
