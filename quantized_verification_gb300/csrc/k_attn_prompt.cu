@@ -805,7 +805,7 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                     flush(n == kFlush, 1.f);
                 }
 
-                // P with the reference so far, or, where a score lies too far above it, with the rows' maxima
+                // P with the reference so far, or, in rows where a score lies too far above it, with their maxima
                 bool raise = n == 0;
 #pragma unroll 1
                 while (true) {
@@ -831,10 +831,12 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                         for (int q = 0; q < 4; ++q)
                             mx[q] = max3(mx[q], __uint_as_float(s[q][2 * j]), __uint_as_float(s[q][2 * j + 1]));
                     const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * a.c;
+                    // a row's reference goes by its own scores alone, whatever the rows beside it hold (the shared memory
+                    // of a tile that 128 / G tokens do not fill is never written); rows that are not computed have no say
+                    const bool above = top > m + kLag;
                     if (raise) {
-                        const float all = fmaxf(m, top);
-                        const float f = m == neg_inf() ? (all == m ? 1.f : 0.f) : ex2(m - all);
-                        m = all;
+                        const float f = !above ? 1.f : m == neg_inf() ? 0.f : ex2(m - top);
+                        if (above) m = top;
                         l *= f;
                         if (n > 0 && !flushed) {
                             if (NT == 1) ok = warp_wait(&bar[Ly::bPV + (buf ^ 1)], ((step - 1) >> 1) & 1, abort, a.wait_ns);
@@ -880,8 +882,7 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                                 if (j & 1) l3 = add2(l3, p); else l2 = add2(l2, p);
                             }
                         // (only now, so that the maximum is taken while the exponentials are)
-                        if (h == 0 && !raise &&
-                            __any_sync(0xffffffffu, top > m + kLag || (m == neg_inf() && top > m))) {
+                        if (h == 0 && !raise && __any_sync(0xffffffffu, valid && above)) {
                             again = true;
                             break;
                         }
