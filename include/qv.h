@@ -631,6 +631,9 @@ QV_API qv_status qv_rotary_frequencies(int rot, double base, qv_rotary_scaling s
  *   out       [M][Hq * D] fp32 or bf16 (out_dtype), 16-byte aligned; must not
  *             overlap qkv
  *   scale     in (0, 2e38]
+ *   Scores, times scale and log2 e, and the largest value times the positions that
+ *   a row sees have to be binary32 numbers: a row's sums are formed with weights
+ *   of at most 1, and divided at the end.
  *   Hq a multiple of Hkv, Hq / Hkv <= 128, D in {64, 128}, 1 <= M, B <= 2^24.
  *   One launch, no workspace; it uses all 512 columns of tensor memory of an SM.
  *   A key or value that is not finite does not reach the rows that do not see it;
@@ -659,7 +662,8 @@ QV_API qv_status qv_rotary_frequencies(int rot, double base, qv_rotary_scaling s
  *   their limits and the errors are qv_attention_verify's.
  *   Two launches: partial results over parts of the prefix, for the query rows of
  *   all sequences together, and of the caches; then their sums with the step's own
- *   keys. The accuracy, what is not finite and waits: as qv_attention_prompt.
+ *   keys. The accuracy, sizes of scores and values, what is not
+ *   finite and waits: as qv_attention_prompt.
  */
 QV_API qv_status qv_attention_prompt(const uint16_t* qkv, const int32_t* cu_rows, int B, int M, int Hq, int Hkv, int D,
                                      float scale, void* out, qv_dtype out_dtype, cudaStream_t stream);

@@ -20,9 +20,10 @@
 //   S = Q K^T      8 tcgen05.mma (D = 128), M = N = 128, both operands K-major
 //                  in shared memory, the accumulator in tensor memory
 //   P = 2^(cS-m)   rounded to bf16 over S's columns in tensor memory. The reference
-//                  m moves only when a score lies more than 2^40 above it; O is
-//                  then rescaled by the softmax threads themselves, at a time when
-//                  no product writes it
+//                  m lies 8 above a row's first maximum and moves only when a score
+//                  passes it, to 8 above that: no P is above 1, and O is hardly
+//                  ever rescaled. When it is, the softmax threads do it
+//                  themselves, at a time when no product writes it
 //   O += P V       8 tcgen05.mma, P from tensor memory, V as stored (M/N-major)
 // With two tiles one's softmax runs under the other's products; with one tile S
 // has two buffers.
@@ -69,9 +70,12 @@ constexpr int kPrefixMaxSplits = 64;       // parts of a prefix, and of a cache
 constexpr int kKeys = 128;                 // key positions per step
 constexpr int kTileRows = 128;             // query rows per tile
 constexpr int kFlush = 8;                  // steps O accumulates for fp32 outputs
-// How far (log2) a score may lie above m: P is a floating-point number and keeps
-// its relative precision, only 2^40 times its sums must not overflow.
-constexpr float kLag = 40.0f;
+// How far (log2) m lies above the maximum that set it. P is a floating-point number
+// and keeps its relative precision; with m above every score the sums overflow no
+// earlier than those with a running maximum (a reference that lagged 2^40 behind
+// gave infinities for values from 3e26 on), and 2^-8 costs nothing: weights below
+// 2^-118 of a row's largest are 0.
+constexpr float kRoom = 8.0f;
 constexpr int kPolls = 32;                 // of a barrier, before a wait looks at the timer
 constexpr float kLog2e = 1.4426950408889634f;
 
@@ -805,7 +809,7 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                     flush(n == kFlush, 1.f);
                 }
 
-                // P with the reference so far, or, in rows where a score lies too far above it, with their maxima
+                // P with the reference so far, or, in rows where a score passes it, with a new one
                 bool raise = n == 0;
 #pragma unroll 1
                 while (true) {
@@ -833,10 +837,10 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                     const float top = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * a.c;
                     // a row's reference goes by its own scores alone, whatever the rows beside it hold (the shared memory
                     // of a tile that 128 / G tokens do not fill is never written); rows that are not computed have no say
-                    const bool above = top > m + kLag;
+                    const bool above = top > m;
                     if (raise) {
-                        const float f = !above ? 1.f : m == neg_inf() ? 0.f : ex2(m - top);
-                        if (above) m = top;
+                        const float f = !above ? 1.f : m == neg_inf() ? 0.f : ex2(m - (top + kRoom));
+                        if (above) m = top + kRoom;
                         l *= f;
                         if (n > 0 && !flushed) {
                             if (NT == 1) ok = warp_wait(&bar[Ly::bPV + (buf ^ 1)], ((step - 1) >> 1) & 1, abort, a.wait_ns);
