@@ -359,12 +359,17 @@ class VerifyStack:
         qg, kg = self.head_norms[l]
         qv.qv_rotary(rows, positions, self.rope, self.Hq, self.Hkv, q_gamma=qg, k_gamma=kg, eps=self.eps, stream=stream)
 
+    # rows of a prompt that go through norms and quantizations together (which take 65535 at most): whole slices of the
+    # linears, and their codes and SwiGLU outputs are all that a slice holds (400 MB fp32 at 12288 features)
+    FILL_ROWS = 32 * qv.QV_MAX_M
+
     def fill_prefix(self, h: torch.Tensor, stream=None):
         """Run a prompt's rows h [n, hidden] bf16 (n <= prefix_len) through the
         chain's layers and keep every layer's keys and values as the prefix that
-        all sequences share: the linears in slices of QV_MAX_M rows, rotary
-        positions, causal attention over the whole prompt (qv_attention_prompt).
-        Returns the residual stream behind the last layer [n, hidden]."""
+        all sequences share: norms and quantizations in slices of FILL_ROWS rows,
+        the linears in slices of QV_MAX_M, rotary positions and causal attention
+        over the whole prompt (qv_attention_prompt). Returns the residual stream
+        behind the last layer [n, hidden]."""
         if getattr(self, "prefix_len", None) is None:
             raise ValueError("fill_prefix needs prepare_chain(cache_len=..., prefix_len=...)")
         n, hidden = h.shape
@@ -373,41 +378,45 @@ class VerifyStack:
         F, Hq, Hkv, D, dev = self.model["ffn"], self.Hq, self.Hkv, self.head_dim, self.device
         cur = torch.cuda.current_stream() if stream is None else stream
         with torch.cuda.stream(cur):
-            step = min(n, qv.QV_MAX_M)
+            step, part = min(n, qv.QV_MAX_M), min(n, self.FILL_ROWS)
+            slices = [(r, min(n, r + part)) for r in range(0, n, part)]
             ws = torch.zeros(max(qv.qv_workspace_bytes(qv.QV_OP_LINEAR, step, K, N) for _, K, N in self.phases),
                              dtype=torch.uint8, device=dev)
-            codes = torch.empty(n * max(K for _, K, _ in self.phases), dtype=torch.int8, device=dev)
-            xq = lambda K: codes[: n * K].view(n, K)  # noqa: E731
-            sx = torch.empty(n, device=dev)
-            new = lambda w, dt=torch.bfloat16: torch.empty(n, w, dtype=dt, device=dev)  # noqa: E731
-            res, qkv, y, a = h.clone(), new((Hq + 2 * Hkv) * D), new(hidden), new(F, torch.float32)
-            attn = new(Hq * D)
+            codes = torch.empty(part * max(K for _, K, _ in self.phases), dtype=torch.int8, device=dev)
+            scales = torch.empty(part, device=dev)
+            new = lambda w: torch.empty(n, w, dtype=torch.bfloat16, device=dev)  # noqa: E731
+            res, qkv, y, attn = h.clone(), new((Hq + 2 * Hkv) * D), new(hidden), new(Hq * D)
+            glu = torch.empty(part, F, dtype=torch.float32, device=dev)
             cu = torch.tensor([0, n], dtype=torch.int32, device=dev)
             positions = torch.arange(n, dtype=torch.int32, device=dev)
 
-            def linear(l, p, out):
+            def linear(l, p, xq, sx, out):
                 wq, sw = self.weights[l][p]
-                for r in range(0, n, step):
-                    e = min(n, r + step)
-                    call = qv.qv_w8a8_swiglu if p == 2 else qv.qv_w8a8_linear
-                    call(xq(wq.shape[1])[r:e], sx[r:e], wq, sw, out[r:e], ws)
+                call = qv.qv_w8a8_swiglu if p == 2 else qv.qv_w8a8_linear
+                for r in range(0, len(out), step):
+                    call(xq[r:r + step], sx[r:r + step], wq, sw, out[r:r + step], ws)
 
             for l in range(self.layers):
                 g1, g2 = self.norm_w[l]
-                qv.qv_rmsnorm_quant(res, g1, xq(hidden), sx, delta=None if l == 0 else y, eps=self.eps)
-                linear(l, 0, qkv)
+                for r, e in slices:
+                    xq, sx = codes[: (e - r) * hidden].view(e - r, hidden), scales[: e - r]
+                    qv.qv_rmsnorm_quant(res[r:e], g1, xq, sx, delta=None if l == 0 else y[r:e], eps=self.eps)
+                    linear(l, 0, xq, sx, qkv[r:e])
                 if self.rope is not None:
                     self._rotate(qkv, positions, l, None)
                 heads = qkv.view(n, Hq + 2 * Hkv, D)
                 self.prefix_k[l][:n].copy_(heads[:, Hq:Hq + Hkv])
                 self.prefix_v[l][:n].copy_(heads[:, Hq + Hkv:])
                 qv.qv_attention_prompt(qkv, cu, Hq, Hkv, 1.0 / D ** 0.5, attn)
-                qv.qv_quantize_act(attn, xq(Hq * D), sx)
-                linear(l, 1, y)
-                qv.qv_rmsnorm_quant(res, g2, xq(hidden), sx, delta=y, eps=self.eps)
-                linear(l, 2, a)
-                qv.qv_quantize_act(a, xq(F), sx)
-                linear(l, 3, y)
+                for r, e in slices:
+                    xo, xh, xf = (codes[: (e - r) * K].view(e - r, K) for K in (Hq * D, hidden, F))
+                    sx, a = scales[: e - r], glu[: e - r]
+                    qv.qv_quantize_act(attn[r:e], xo, sx)
+                    linear(l, 1, xo, sx, y[r:e])
+                    qv.qv_rmsnorm_quant(res[r:e], g2, xh, sx, delta=y[r:e], eps=self.eps)
+                    linear(l, 2, xh, sx, a)
+                    qv.qv_quantize_act(a, xf, sx)
+                    linear(l, 3, xf, sx, y[r:e])
             res.add_(y)
             self.prefix_lens.fill_(n)
             if self.rope is not None:
