@@ -385,7 +385,9 @@ class VerifyStack:
             codes = torch.empty(part * max(K for _, K, _ in self.phases), dtype=torch.int8, device=dev)
             scales = torch.empty(part, device=dev)
             new = lambda w: torch.empty(n, w, dtype=torch.bfloat16, device=dev)  # noqa: E731
-            res, qkv, y, attn = h.clone(), new((Hq + 2 * Hkv) * D), new(hidden), new(Hq * D)
+            res, qkv, y = h.clone(), new((Hq + 2 * Hkv) * D), new(hidden)
+            # fp32, as a step's: its rows and a prompt's are quantized from the same precision
+            attn = torch.empty(n, Hq * D, dtype=torch.float32, device=dev)
             glu = torch.empty(part, F, dtype=torch.float32, device=dev)
             cu = torch.tensor([0, n], dtype=torch.int32, device=dev)
             positions = torch.arange(n, dtype=torch.int32, device=dev)

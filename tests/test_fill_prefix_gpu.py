@@ -54,3 +54,30 @@ def test_more_rows_than_one_call_takes(qv):
     st.enqueue_chain()
     torch.cuda.synchronize()
     assert qv.qv_device_error() == 0
+
+
+def test_attention_outputs_are_quantized_from_fp32_as_a_step_s_are(qv):
+    from quantized_verification_gb300 import synth
+    n = 300
+    st = make(n)
+    prompt, quantize, seen = qv.qv_attention_prompt, qv.qv_quantize_act, []
+
+    def spy_prompt(qkv, cu, hq, hkv, scale, out, **kw):
+        prompt(qkv, cu, hq, hkv, scale, out, **kw)
+        seen.append([qkv.clone(), out.clone()])
+
+    def spy_quantize(x, xq, sx, **kw):
+        quantize(x, xq, sx, **kw)
+        if x.shape[1] == HQ * D:
+            seen[-1].append(x.clone())
+
+    qv.qv_attention_prompt, qv.qv_quantize_act = spy_prompt, spy_quantize
+    try:
+        st.fill_prefix(synth.activations(n, MODEL["hidden"], 78, device="cuda"))
+    finally:
+        qv.qv_attention_prompt, qv.qv_quantize_act = prompt, quantize
+    assert len(seen) == MODEL["layers"]
+    for qkv, out, quantized in seen:
+        assert out.dtype == st.attn_out[0].dtype == torch.float32 and torch.equal(out, quantized)
+        o, a = ref.prompt(qkv, [0, n], HQ, HKV, D ** -0.5)
+        assert ((out.double().view(o.shape) - o).abs() <= ref.bound(o, a, torch.float32)).all()
