@@ -594,7 +594,7 @@ QV_API qv_status qv_attention_verify_kv4(const uint16_t* qkv, const uint8_t* cac
  *             x * gamma / sqrt(mean(x^2) + eps); the sum of a head's squares must
  *             be a binary32 number
  *   out       qkv itself (the value heads are then not touched) or a buffer that
- *             does not overlap it (they are copied)
+ *             does not overlap it (they are copied); it overlaps no other input
  *   All in binary32 with one rounding at the end.
  *   1 <= M <= 2^24, 0 <= Hq, Hkv <= 65535, not both 0; D a multiple of 8 in [8,
  *   256], rot a multiple of 8 in [8, D]. One launch, no workspace.
@@ -629,7 +629,7 @@ QV_API qv_status qv_rotary_frequencies(int rot, double base, qv_rotary_scaling s
  *             hold anything and their outputs are left as they were. Values
  *             outside [0, M] are clamped; falling ones give unspecified outputs.
  *   out       [M][Hq * D] fp32 or bf16 (out_dtype), 16-byte aligned; must not
- *             overlap qkv
+ *             overlap qkv or cu_rows
  *   scale     in (0, 2e38]
  *   Scores, times scale and log2 e, and the largest value times the positions that
  *   a row sees have to be binary32 numbers: a row's sums are formed with weights
@@ -653,11 +653,11 @@ QV_API qv_status qv_rotary_frequencies(int rot, double base, qv_rotary_scaling s
  *   prefix_len [1] int32 on the device (clamped to [0, P]); positions from it on
  *             may hold anything
  *   out       [B*T][Hq * D] fp32 or bf16 (out_dtype), 16-byte aligned; must not
- *             overlap qkv or the workspace
+ *             overlap the inputs or the workspace
  *   workspace qv_attention_prefix_workspace_bytes(...) bytes (a host function; 0
  *             for an invalid shape), 16-byte aligned, scratch: needs no initial
- *             value, and must not be shared with calls that may run at the same
- *             time
+ *             value, must not overlap the inputs, and must not be shared with
+ *             calls that may run at the same time
  *   1 <= P <= 2^24, T * Hq / Hkv <= 128, B * T * Hq <= 2^27; the other arguments,
  *   their limits and the errors are qv_attention_verify's.
  *   Two launches: partial results over parts of the prefix, for the query rows of

@@ -846,7 +846,9 @@ namespace {
 constexpr int kPromptMaxRows = 1 << 24;
 constexpr int kPromptMaxGroup = 128;
 
+// (nothing overlaps what has no bytes)
 bool overlap(const void* a, size_t na, const void* b, size_t nb) {
+    if (na == 0 || nb == 0) return false;
     const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
     return x < y + nb && y < x + na;
 }
@@ -865,8 +867,10 @@ qv_status qv_attention_prompt(const uint16_t* qkv, const int32_t* cu_rows, int B
     if (!(scale > 0.0f) || scale > 2.0e38f) return fail(QV_ERR_INVALID_ARG, "scale must be in (0, 2e38]");
     if (!aligned(qkv, 16) || !aligned(out, 16) || !aligned(cu_rows, 4))
         return fail(QV_ERR_INVALID_ARG, "qkv and out must be 16-byte aligned, cu_rows 4-byte aligned");
-    if (overlap(qkv, (size_t)M * (Hq + 2 * (size_t)Hkv) * D * 2, out, (size_t)M * Hq * D * (out_dtype == QV_F32 ? 4 : 2)))
-        return fail(QV_ERR_INVALID_ARG, "out must not overlap qkv");
+    const size_t out_bytes = (size_t)M * Hq * D * (out_dtype == QV_F32 ? 4 : 2);
+    if (overlap(qkv, (size_t)M * (Hq + 2 * (size_t)Hkv) * D * 2, out, out_bytes) ||
+        overlap(cu_rows, ((size_t)B + 1) * 4, out, out_bytes))
+        return fail(QV_ERR_INVALID_ARG, "out must not overlap qkv or cu_rows");
     const int tokens = qv::attention_prompt_tokens(Hq / Hkv);
     if ((long long)((M + tokens - 1) / tokens) * Hkv > 0x7FFFFFFFll)
         return fail(QV_ERR_UNSUPPORTED, "M * Hq is too large for one call");
@@ -930,8 +934,17 @@ qv_status qv_attention_verify_prefix(const uint16_t* qkv, const uint16_t* prefix
         (v_cache && !aligned(v_cache, 16)) || !aligned(cache_len, 4) || !aligned(prefix_len, 4) || !aligned(out, 16))
         return fail(QV_ERR_INVALID_ARG, "qkv, the prefix, the caches and out must be 16-byte aligned, lengths 4-byte aligned");
     const size_t out_bytes = (size_t)B * T * Hq * D * (out_dtype == QV_F32 ? 4 : 2);
-    if (overlap(qkv, (size_t)B * T * (Hq + 2 * (size_t)Hkv) * D * 2, out, out_bytes))
-        return fail(QV_ERR_INVALID_ARG, "out must not overlap qkv");
+    const size_t prefix_bytes = (size_t)P * Hkv * D * 2, cache_bytes = (size_t)B * Lmax * Hkv * D * 2;
+    const struct { const void* p; size_t bytes; } read[] = {
+        {qkv, (size_t)B * T * (Hq + 2 * (size_t)Hkv) * D * 2}, {prefix_k, prefix_bytes}, {prefix_v, prefix_bytes},
+        {prefix_len, 4}, {k_cache, cache_bytes}, {v_cache, cache_bytes}, {cache_len, (size_t)B * 4}};
+    auto over_read = [&](const void* p, size_t bytes) {
+        for (const auto& r : read)
+            if (overlap(r.p, r.bytes, p, bytes)) return true;
+        return false;
+    };
+    if (over_read(out, out_bytes))
+        return fail(QV_ERR_INVALID_ARG, "out must not overlap qkv, the prefix, the caches or their lengths");
     cudaError_t e;
     const int sms = sms_of_current_device(&e);
     if (e != cudaSuccess) return cuda_fail(e, "device query");
@@ -939,7 +952,8 @@ qv_status qv_attention_verify_prefix(const uint16_t* qkv, const uint16_t* prefix
     if (!workspace) return fail(QV_ERR_WORKSPACE, "workspace is null (%zu bytes needed)", need);
     if (!aligned(workspace, 16)) return fail(QV_ERR_WORKSPACE, "workspace must be 16-byte aligned");
     if (workspace_bytes < need) return fail(QV_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed", workspace_bytes, need);
-    if (overlap(workspace, need, out, out_bytes)) return fail(QV_ERR_INVALID_ARG, "out must not overlap the workspace");
+    if (overlap(workspace, need, out, out_bytes) || over_read(workspace, need))
+        return fail(QV_ERR_INVALID_ARG, "the workspace must not overlap out, qkv, the prefix, the caches or their lengths");
     QV_CHECK_DEV(qkv);
     QV_CHECK_DEV(prefix_k);
     QV_CHECK_DEV(prefix_v);
@@ -990,6 +1004,9 @@ qv_status qv_rotary(const void* qkv, qv_dtype dtype, const int32_t* positions, c
     const size_t bytes = (size_t)M * (Hq + 2 * (size_t)Hkv) * D * (dtype == QV_F32 ? 4 : 2);
     if (out != qkv && overlap(qkv, bytes, out, bytes))
         return fail(QV_ERR_INVALID_ARG, "out must be qkv itself or not overlap it");
+    if (overlap(positions, (size_t)M * 4, out, bytes) || overlap(inv_freq, (size_t)rot * 2, out, bytes) ||
+        (q_gamma && (overlap(q_gamma, (size_t)D * 2, out, bytes) || overlap(k_gamma, (size_t)D * 2, out, bytes))))
+        return fail(QV_ERR_INVALID_ARG, "out must not overlap the positions, the frequencies or the norm weights");
     QV_CHECK_DEV(qkv);
     QV_CHECK_DEV(positions);
     QV_CHECK_DEV(inv_freq);
