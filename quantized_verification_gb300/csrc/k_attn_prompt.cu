@@ -79,6 +79,10 @@ constexpr float kRoom = 8.0f;
 constexpr int kPolls = 32;                 // of a barrier, before a wait looks at the timer
 constexpr float kLog2e = 1.4426950408889634f;
 
+// l of a part without positions, which writes no outputs. (A part whose scores are all -inf has l = 0, and outputs of 0,
+// or NaN where a value is not finite.)
+constexpr float kNoPositions = -1.0f;
+
 constexpr int kItemBytes = 64;
 
 template <int D, int NT>
@@ -964,7 +968,7 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                     }
                 }
             } else if (PREFIX && valid && nt == 0) {
-                a.part_ml[(size_t)it.part * a.M * a.Hq + row] = make_float2(neg_inf(), 0.f);
+                a.part_ml[(size_t)it.part * a.M * a.Hq + row] = make_float2(neg_inf(), kNoPositions);
             }
             tc_fence_before();
             steps += nt;
@@ -1094,7 +1098,7 @@ __device__ __forceinline__ void merge_parts(const MergeArgs& a, int w, int at, S
 #pragma unroll
     for (int u = 0; u < kParts; ++u) {
         const int j = 32 * u + lane;
-        ml[u] = make_float2(neg_inf(), 0.f);
+        ml[u] = make_float2(neg_inf(), kNoPositions);
         if (j < count) ml[u] = a.part_ml[(size_t)(at + j * STEP) * a.rows + w];
         r.top = fmaxf(r.top, ml[u].x);
     }
@@ -1102,10 +1106,10 @@ __device__ __forceinline__ void merge_parts(const MergeArgs& a, int w, int at, S
 #pragma unroll
     for (int u = 0; u < kParts; ++u) {
         if (32 * u >= count) break;
-        const bool none = ml[u].x == neg_inf() && ml[u].y == 0.f;        // no position, nothing written
+        const bool none = ml[u].y == kNoPositions;
         const float f = none ? 0.f : ex2(ml[u].x - ref);
-        r.l += f * ml[u].y;
-        const unsigned there = __ballot_sync(0xffffffffu, !none && 32 * u + lane < count);
+        if (!none) r.l += f * ml[u].y;
+        const unsigned there = __ballot_sync(0xffffffffu, !none);
         // kAhead parts' values are requested before the first is used
         for (int j0 = 0; j0 < min(count - 32 * u, 32); j0 += kAhead) {
             float v[kAhead][N];
