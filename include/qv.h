@@ -636,8 +636,11 @@ QV_API qv_status qv_rotary_frequencies(int rot, double base, qv_rotary_scaling s
  *   of at most 1, and divided at the end.
  *   Hq a multiple of Hkv, Hq / Hkv <= 128, D in {64, 128}, 1 <= M, B <= 2^24.
  *   One launch, no workspace; it uses all 512 columns of tensor memory of an SM.
- *   A key or value that is not finite does not reach the rows that do not see it;
- *   a row that does see one is not finite (of a value, at least in its elements).
+ *   A key or value that is not finite does not reach the rows that do not see it.
+ *   A row that sees such a key is the softmax of the scores that it gives: NaN
+ *   where one is NaN or +inf, while a score of -inf weighs 0. A value that is not
+ *   finite makes a row that sees it not finite whatever its weight, at least in
+ *   the value's elements.
  *   A wait inside the kernel that runs out sets QV_DEVICE_ERR_FULL_WAIT
  *   (qv_device_error); the call's outputs are then undefined.
  * fp32 outputs are within about 5e-6 (2-norm) of the binary64 definition; for
