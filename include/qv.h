@@ -586,8 +586,10 @@ QV_API qv_status qv_attention_verify_kv4(const uint16_t* qkv, const uint8_t* cac
  *   positions [M] int32, any values (negative ones rotate back)
  *   inv_freq  [rot / 2] fp32, finite: pair i of a head (a, b) becomes
  *             (a c - b s, b c + a s), c and s the magnitude times the cosine and
- *             sine of positions[m] * inv_freq[i]. The product is not rounded: an
- *             angle is off by 2e-7 at most, at any position.
+ *             sine of positions[m] * inv_freq[i]. The product is not rounded: for
+ *             frequencies up to 32 (five turns a position) an angle is off by 2e-7
+ *             at most, at any position; above, by up to 1.4e-18 |positions[m] *
+ *             inv_freq[i]| more, and from 2^63 on a pair is not turned.
  *   Pairs are values i and i + rot / 2 of a head, or 2 i and 2 i + 1
  *   (interleaved != 0); values from rot on are not rotated.
  *   q_gamma, k_gamma [D] bf16, 16-byte aligned, or both NULL: a head x is first

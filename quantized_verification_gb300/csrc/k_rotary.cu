@@ -7,8 +7,10 @@
 //   with the angle's product not rounded: in binary32 it would be off by 2^-24 of
 //   itself, 0.004 at position 65536. Here a frequency becomes a 64-bit fraction
 //   of a turn, the position multiplies it modulo 2^64 (whole turns fall off by
-//   themselves), and only the result's top 32 bits are converted, so that an
-//   angle is off by 2^-25 turns at most at any int32 position.
+//   themselves), and only the result's top 32 bits are converted (half a step of
+//   binary32, 2^-26 turns). The fraction is off by 2^-62 of the frequency in turns
+//   at most: by 2^-26 turns at the farthest int32 position for frequencies up to 32,
+//   in proportion above.
 //
 // Bound by memory: a row is read and written once. A warp takes a row (or, of few
 // rows, some of its heads): it forms the row's cosines and sines once, two or so a
