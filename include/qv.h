@@ -608,7 +608,10 @@ QV_API qv_status qv_attention_verify_kv4(const uint16_t* qkv, const uint8_t* cac
  *   QV_ROTARY_BASE    f_i of the base base * factor^(rot / (rot - 2))
  *   QV_ROTARY_PARTS   f_i where a pair makes fast_turns turns or more within
  *             trained_length positions, f_i / factor where it makes slow_turns or
- *             fewer, a linear blend between; magnitude 0.1 ln(factor) + 1
+ *             fewer, a blend between that is linear in the turns; magnitude 0.1
+ *             ln(factor) + 1. Models that blend linearly over the pair's index i,
+ *             or that were trained with another magnitude, have other tables:
+ *             qv_rotary takes any inv_freq and magnitude.
  * The magnitude is 1 otherwise. rot even in [2, 256], base > 1, factor >= 1.
  */
 typedef enum { QV_ROTARY_PLAIN = 0, QV_ROTARY_LINEAR = 1, QV_ROTARY_BASE = 2, QV_ROTARY_PARTS = 3 } qv_rotary_scaling;

@@ -485,7 +485,10 @@ def qv_rotary(qkv, positions, inv_freq, Hq, Hkv, out=None, interleaved=False, ma
 def qv_rotary_frequencies(rot, base=10000.0, scaling=QV_ROTARY_PLAIN, factor=1.0, trained_length=0.0, fast_turns=32.0,
                           slow_turns=1.0):
     """(inv_freq [rot/2] fp32 on the host, magnitude) for qv_rotary: plain
-    frequencies or ones stretched by `factor` for long contexts."""
+    frequencies or ones stretched by `factor` for long contexts. QV_ROTARY_PARTS
+    blends linearly in the turns that a pair makes within trained_length and
+    gives the magnitude 0.1 ln(factor) + 1; models that blend over the pair's
+    index, or with another magnitude, need tables of their own."""
     inv_freq = torch.empty(max(rot, 0) // 2, dtype=torch.float32)
     magnitude = ctypes.c_float()
     _check(load().qv_rotary_frequencies(rot, base, scaling, factor, trained_length, fast_turns, slow_turns,
