@@ -308,14 +308,13 @@ class VerifyStack:
         self.y_o = torch.empty(M, h, dtype=torch.bfloat16, device=dev)
         self.a_glu = torch.empty(M, F, dtype=torch.float32, device=dev)
         self.y_down = torch.empty(M, h, dtype=torch.bfloat16, device=dev)
-        self.cache_len = cache_len
+        self.cache_len, self.prefix_len = cache_len, prefix_len
         if cache_len is not None:
             q = self.model.get("q", h)
             kv = self.model["kv"]
             assert q % head_dim == 0 and kv % head_dim == 0
             self.head_dim, self.Hq, self.Hkv = head_dim, q // head_dim, kv // head_dim
             self.kv_bits = kv_bits
-            self.prefix_len = prefix_len
             self._prepare_rotary(rope_base)
             if kv_bits == 4:
                 self._prepare_kv4(cache_len, self.gamma + 1 if room is None else room)

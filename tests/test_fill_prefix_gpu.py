@@ -81,3 +81,16 @@ def test_attention_outputs_are_quantized_from_fp32_as_a_step_s_are(qv):
         assert out.dtype == st.attn_out[0].dtype == torch.float32 and torch.equal(out, quantized)
         o, a = ref.prompt(qkv, [0, n], HQ, HKV, D ** -0.5)
         assert ((out.double().view(o.shape) - o).abs() <= ref.bound(o, a, torch.float32)).all()
+
+
+def test_a_chain_prepared_again_without_a_prefix_has_none(qv):
+    h = torch.zeros(4, MODEL["hidden"], dtype=torch.bfloat16, device="cuda")
+    for kw in (dict(), dict(cache_len=20), dict(cache_len=20, kv_bits=4)):
+        st = make(8)
+        st.fill_prefix(h)
+        st.prepare_chain(head_dim=D, **kw)
+        with pytest.raises(ValueError, match="prefix_len"):
+            st.fill_prefix(h)
+        st.enqueue_chain()
+    torch.cuda.synchronize()
+    assert qv.qv_device_error() == 0
