@@ -29,8 +29,10 @@
 // has two buffers.
 // fp32 outputs: P as two bf16 parts (residue 2^-18), twice the second product;
 // the tensor cores cut the accumulator off at every product (1.6e-8 of it, all
-// one way), so every kFlush steps O is added in binary32 to the row's sums, which
-// lie where the output goes.
+// one way, and more as the sums outgrow what is added), so every kFlush steps O is
+// added in binary32 to the row's sums, which lie where the output goes. bf16 outputs
+// have one part, and flush to a prefix's partial results every kFlushLong steps; a
+// prompt's have no room for sums there, and keep their high part (carry).
 //
 // Bound by the tensor cores from about 1000 rows on, where S, P and O pass through
 // tensor memory in time. GB300, causal, bf16 outputs: one prompt of 16001 tokens, 64/8
@@ -70,6 +72,9 @@ constexpr int kPrefixMaxSplits = 64;       // parts of a prefix, and of a cache
 constexpr int kKeys = 128;                 // key positions per step
 constexpr int kTileRows = 128;             // query rows per tile
 constexpr int kFlush = 8;                  // steps O accumulates for fp32 outputs
+// The same for bf16 ones, whose rounding hides more: the cuts of 2^20 positions of one sign made them 4.3e-3 too small,
+// those of 2^15 are below 1e-4.
+constexpr int kFlushLong = 256;
 // How far (log2) m lies above the maximum that set it. P is a floating-point number
 // and keeps its relative precision; with m above every score the sums overflow no
 // earlier than those with a running maximum (a reference that lagged 2^40 behind
@@ -408,6 +413,47 @@ __device__ __forceinline__ void transpose4(uint32_t (&v)[16]) {
     }
 }
 
+// bf16 outputs of long sequences: where a row's outputs go lies the high part of its sums (kept), O has the rest, so
+// that the products' cuts are those of a small sum. f: what the row's reference has moved by since `kept` was written,
+// 0 before that. The sum of both goes apart again, or, to end with, whole into O. The whole warp calls (kept is null
+// in rows that are not computed); out of line, so that the steps' code stays together.
+template <int D>
+__device__ __noinline__ void carry(uint32_t o_col, uint16_t* kept, float f, bool whole) {
+#pragma unroll 1
+    for (int c = 0; c < D; c += 32) {
+        uint32_t o[32], rest[2][16];
+        tmem_ld<32>(o_col + c, o);
+        tmem_ld_done(o);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            uint32_t w[4] = {};
+            uint4* p = reinterpret_cast<uint4*>(kept + c) + j;
+            if (kept && f != 0.f) {
+                const uint4 x = *p;
+                w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const int e = 8 * j + 2 * k;
+                float a = __uint_as_float(w[k] << 16) * f + __uint_as_float(o[e]);
+                float b = __uint_as_float(w[k] & 0xFFFF0000u) * f + __uint_as_float(o[e + 1]);
+                if (!whole) {
+                    w[k] = __float_as_uint(a) >> 16 | (__float_as_uint(b) & 0xFFFF0000u);
+                    a -= __uint_as_float(w[k] << 16);
+                    b -= __uint_as_float(w[k] & 0xFFFF0000u);
+                }
+                rest[e / 16][e % 16] = __float_as_uint(a);
+                rest[e / 16][e % 16 + 1] = __float_as_uint(b);
+            }
+            if (kept && !whole) *p = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        __syncwarp();
+        tmem_st(o_col + c, rest[0]);
+        tmem_st(o_col + c + 16, rest[1]);
+    }
+    tmem_st_wait();
+}
+
 template <int D, int NT, int PARTS, bool PREFIX>
 __global__ void __launch_bounds__(Layout<D, NT>::Threads, 1)
 attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
@@ -420,6 +466,10 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
     uint32_t* bad = reinterpret_cast<uint32_t*>(smem + Ly::Bad);
     uint32_t* tmem_ptr = reinterpret_cast<uint32_t*>(smem + Ly::Misc);
     volatile int* abort = reinterpret_cast<volatile int*>(smem + Ly::Misc + 4);
+    // steps O accumulates, and whether it then starts anew (fp32 sums elsewhere) or goes on with what its high part,
+    // kept where the outputs go, leaves
+    constexpr int kSteps = PARTS == 2 ? kFlush : kFlushLong;
+    constexpr bool kAnew = PREFIX || PARTS == 2;
     constexpr int kMmaWarp = Ly::Warps, kLoadWarp = kMmaWarp + 1, kScanWarp = kMmaWarp + 2;   // two of those
 
     if (threadIdx.x == 0) {
@@ -605,7 +655,7 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                         ok = __all_sync(0xffffffffu, wait(Ly::bP + 2 * i, c & 1));
                         if (!ok) break;
                         tc_fence_after();
-                        outputs(i, i * 128, 0, PARTS == 2 ? n % kFlush != 0 : n > 0);
+                        outputs(i, i * 128, 0, kAnew ? n % kSteps != 0 : n > 0);
                         ok = __all_sync(0xffffffffu, wait(Ly::bP + 2 * i + 1, c & 1));
                         if (!ok) break;
                         tc_fence_after();
@@ -653,7 +703,7 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                     ++looks;
                     if (!ok) break;
                     tc_fence_after();
-                    outputs(0, buf * 128, 0, PARTS == 2 ? n % kFlush != 0 : n > 0);
+                    outputs(0, buf * 128, 0, kAnew ? n % kSteps != 0 : n > 0);
                     ok = __all_sync(0xffffffffu, wait(Ly::bP + 2 * buf + 1, (c0 >> 1) & 1));
                     if (!ok) break;
                     tc_fence_after();
@@ -788,13 +838,40 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                 m_acc = m;
             };
 
-            for (int n = 0; n < nt; ++n) {
+            // all products of this item's steps before n are done
+            auto products_done = [&](int n) {
+                const unsigned before = steps + n - 1;
+                const bool done = NT == 1  ? warp_wait(&bar[Ly::bPV + (before & 1)], (before >> 1) & 1, abort, a.wait_ns)
+                                  : n < nt ? warp_wait(&bar[Ly::bS + i], (before + 1) & 1, abort, a.wait_ns)
+                                           : warp_wait(&bar[Ly::bPV + i], ends & 1, abort, a.wait_ns);
+                tc_fence_after();
+                return done;
+            };
+
+            auto carry_on = [&](bool whole) {
+                carry<D>(o_col, row < 0 ? nullptr : reinterpret_cast<uint16_t*>(a.out) + row * D,
+                         m_acc == neg_inf() ? 0.f : ex2(m_acc - m), whole);
+                m_acc = m;
+            };
+
+            // (fp32 outputs: one stretch, and a flush every kFlush steps within it)
+            for (int n0 = 0; n0 < nt; n0 = PARTS == 2 ? nt : n0 + kFlushLong) {
+            if (PARTS == 1 && n0 > 0) {
+                ok = products_done(n0);
+                if (!ok) break;
+                if constexpr (PREFIX)
+                    flush(n0 == kFlushLong, 1.f);
+                else
+                    carry_on(false);
+            }
+            const int n1 = PARTS == 2 ? nt : min(nt, n0 + kFlushLong);
+            for (int n = n0; n < n1; ++n) {
                 const unsigned step = steps + n;
                 const int buf = NT == 2 ? i : step & 1;
                 const uint32_t s_col = tm + lanes + buf * 128;
                 const int kb = it.k0 + n * kKeys;
                 const bool part = partly(it, n);
-                const bool flushed = PARTS == 2 && n > 0 && n % kFlush == 0;
+                const bool flushed = PARTS == 2 ? n > 0 && n % kFlush == 0 : kAnew && n == n0;
                 uint32_t see[4];                             // which of the keys the row sees
                 ok = warp_wait(&bar[Ly::bS + buf], (NT == 2 ? step : step >> 1) & 1, abort, a.wait_ns);
                 if (!ok) break;
@@ -806,7 +883,7 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                         see[q] = f0 <= t0 && f0 < 32 ? 0xFFFFFFFFu >> (31 - t0) >> f0 << f0 : 0u;
                     }
                 }
-                if (flushed) {
+                if (PARTS == 2 && flushed) {
                     if (NT == 1) ok = warp_wait(&bar[Ly::bPV + (buf ^ 1)], ((step - 1) >> 1) & 1, abort, a.wait_ns);
                     if (!ok) break;
                     tc_fence_after();
@@ -933,19 +1010,19 @@ attn_prompt_kernel(const __grid_constant__ Maps maps, const Args a) {
                 }
                 if (!ok) break;
             }
+            if (!ok) break;
+            }
 
             // -------------------------------------------------------- outputs
             if (ok && nt > 0) {
-                const unsigned last = steps + nt - 1;
-                ok = NT == 2 ? warp_wait(&bar[Ly::bPV + i], ends & 1, abort, a.wait_ns)
-                             : warp_wait(&bar[Ly::bPV + (last & 1)], (last >> 1) & 1, abort, a.wait_ns);
+                ok = products_done(nt);
                 ++ends;
-                tc_fence_after();
+                if (!kAnew && nt > kFlushLong && ok) carry_on(true);
             }
             if (ok && nt > 0) {
                 const float inv = PREFIX ? 1.f : 1.f / l;
-                if (PREFIX || PARTS == 2) {
-                    flush(PARTS == 1 || nt <= kFlush, inv);
+                if constexpr (kAnew) {
+                    flush(nt <= kSteps, inv);
                     if (PREFIX && valid) a.part_ml[(size_t)it.part * a.M * a.Hq + row] = make_float2(m, l);
                 } else {
 #pragma unroll 1
