@@ -648,9 +648,9 @@ QV_API qv_status qv_rotary_frequencies(int rot, double base, qv_rotary_scaling s
  *   the value's elements.
  *   A wait inside the kernel that runs out sets QV_DEVICE_ERR_FULL_WAIT
  *   (qv_device_error); the call's outputs are then undefined.
- * fp32 outputs are within about 5e-6 (2-norm) of the binary64 definition; for
+ * fp32 outputs are within about 5e-6 (2-norm) of the binary64 definition. For
  * bf16 outputs the probabilities are rounded to bf16 before the product with the
- * values. Results are the same from call to call.
+ * values: 2e-3, where the outputs' own rounding makes 1.6e-3. Results are the same from call to call.
  *
  * qv_attention_verify_prefix -- qv_attention_verify for a batch whose sequences
  * all begin with the same prefix (a system prompt, a document), which is stored

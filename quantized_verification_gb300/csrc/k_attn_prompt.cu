@@ -1,7 +1,8 @@
 // k_attn_prompt.cu -- attention of many query rows on the tcgen05 tensor cores:
 // whole prompts, packed one behind the other (causal), and the rows of a batch
-// over a prefix that all its sequences share (partial results, merged by
-// k_attn.cu's kernel with each sequence's own cache).
+// over a prefix that all its sequences share (partial results over its parts and
+// over parts of each sequence's cache, merged with the step's own keys by a second
+// kernel).
 //
 //   o_r = sum_j p_rj v_j / sum_j p_rj,  p_rj = 2^(c s_rj - m_r),  s = q_r . k_j,
 //   c = scale * log2 e, over the keys that row r sees.
@@ -27,24 +28,33 @@
 //   O += P V       8 tcgen05.mma, P from tensor memory, V as stored (M/N-major)
 // With two tiles one's softmax runs under the other's products; with one tile S
 // has two buffers.
-// fp32 outputs: P as two bf16 parts (residue 2^-18), twice the second product;
-// the tensor cores cut the accumulator off at every product (1.6e-8 of it, all
-// one way, and more as the sums outgrow what is added), so every kFlush steps O is
-// added in binary32 to the row's sums, which lie where the output goes. bf16 outputs
-// have one part, and flush to a prefix's partial results every kFlushLong steps; a
-// prompt's have no room for sums there, and keep their high part (carry).
+// Rounding of P. The product takes operands of one type, V's bf16. For bf16 outputs P
+// is one part: half a step (2^-8) of each probability makes them 2.0e-3 off in the
+// 2-norm, where their own rounding alone makes 1.6e-3 (with the rounded P in l as well
+// the same to 2 %). Two parts would take the 1.8 times as long that fp32 outputs take
+// (6000 tokens 0.34 ms, 0.19): who needs the bits asks for those. fp32 outputs: P as
+// two parts (residue 2^-17), twice the second product, 1.5 to 3.4e-6 off. A third part
+// has room in tensor memory with one tile a CTA only (heads of 128) and was 0.3 to
+// 3.6e-6 off by the cuts that follow: 6000 tokens 0.57 ms, five prompts of up to 1500
+// tokens 39 us instead of 31.
+// Sums. The tensor cores cut the accumulator off at every product (1.6e-8 of it, all
+// one way, more as it outgrows what is added). For fp32 outputs O is added in binary32
+// every kFlush steps to the row's sums, which lie where the output goes (every 4 steps
+// 1.5 to 2.7e-6 off, 8 to 20 % slower); for bf16 ones every kFlushLong steps to a
+// prefix's partial results. A prompt's bf16 outputs have no room for sums: there O's
+// high part is kept and O goes on with the rest (carry).
 //
 // Bound by the tensor cores from about 1000 rows on, where S, P and O pass through
 // tensor memory in time. GB300, causal, bf16 outputs: one prompt of 16001 tokens, 64/8
 // heads of 128, 2.45 ms (1710 TFLOP/s, 0.90 of a measured cuBLAS product; 2.67 ms
 // = 0.82 of it where the power limit is reached); 6000 tokens, 32/8 heads, 0.188 ms
-// (heads of 64 0.162, fp32 outputs 0.342); 2043 tokens 31 us; 24 prompts of 33 to
-// 4001 tokens 324 us (1190 TFLOP/s). A step of two tiles takes about 2500 cycles of
+// (heads of 64 0.160, fp32 outputs 0.344); 2043 tokens 31 us; 24 prompts of 33 to
+// 4001 tokens 322 to 325 us (1190 TFLOP/s; 339 in a stream of calls). A step of two tiles takes about 2500 cycles of
 // the 2080 that its 32 products need; a block's first and last steps, whose code and
 // data are cold, 2 to 4 thousand more. 97 tokens: 6 us, of which 2.4 are start and
 // first loads.
 // Prefixes: 64 tokens, 64/8 heads behind 100001 positions 163 us (1290 TFLOP/s with
-// the caches' parts and the merge), 24 sequences of 5 tokens behind 8190, fp32, 50 us.
+// the caches' parts and the merge; 176 in a stream of calls), 24 sequences of 5 tokens behind 8190, fp32, 50 us.
 //
 // Masked tiles. A key that some row of the CTA does not see may hold anything;
 // its score is replaced before use, and its value must not be multiplied by

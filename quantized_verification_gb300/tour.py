@@ -30,7 +30,7 @@ with ``-k`` on the kernels below skips 28 matching launches (``-s 28 -c 27``):
     rotary_kernel                         2048 rows of 32/8 heads rotated and RMS-normed
     attn_prompt_kernel<128, 2, 1, 0>      attention over them as one prompt, bf16 outputs
     attn_prompt_kernel<128, 1, 2, 1>      5 tokens behind them as a shared prefix, in parts
-    prefix_merge_kernel<128>              the parts and the own keys together
+    prefix_merge_kernel<128, 1>           the parts and the own keys together, a block a row
     token_logprobs_kernel                 log probabilities, entropies and the top 8 of
                                           5 rows x 151936 logits
 
