@@ -51,9 +51,9 @@ def test_long_prompts(n, Hq, Hkv, D):
 
 
 @pytest.mark.parametrize("D", [64, 128])
-def test_long_prompts_whose_scores_rise_late(D):
-    # the reference moves after sums have been carried on: 40000 positions that then weigh 2^-29 each, and 40000 that count
-    n, half = 80001, 40000
+@pytest.mark.parametrize("n,half", [(80001, 40000), (38801, 33000)])       # blocks of two tiles and of one
+def test_long_prompts_whose_scores_rise_late(n, half, D):
+    # the reference moves after sums have been carried on: positions that then weigh 2^-29 each, and some that count
     g = torch.Generator(device="cuda").manual_seed(5)
     x = torch.zeros(n, 3, D, device="cuda")
     x[:, 0, 0] = 1.0
@@ -86,3 +86,25 @@ def test_long_prefix(D):
     own = x[:, 2 * D:].double().view(B, T, D).cumsum(1)
     want = (pv.double().sum(0) + own) / (P + torch.arange(1, T + 1, device="cuda")[:, None])
     near(out.view(B, T, D), want)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_long_prefix_behind_few_rows(D):
+    # blocks of one tile, again without a cut into parts; the scores rise where the sums have been written once
+    P, H, rise = 40001, 152, 33000
+    g = torch.Generator(device="cuda").manual_seed(10)
+    pk, pv = torch.zeros(P, H, D, dtype=torch.bfloat16, device="cuda"), positive(g, P, H, D)
+    x = torch.zeros(1, 3 * H, D, dtype=torch.bfloat16, device="cuda")
+    x[:, :H, 0], pk[rise:, :, 0] = 1.0, 20.0
+    x[:, H:2 * H, 0], x[:, 2 * H:] = 20.0, positive(g, 1, H, D)
+    kc = torch.empty(1, 0, H, D, dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros(1, H * D, dtype=torch.bfloat16, device="cuda")
+    ws = torch.empty(qv.qv_attention_prefix_workspace_bytes(1, 1, H, H, D, P), dtype=torch.uint8, device="cuda")
+    qv.qv_attention_verify_prefix(x.view(1, -1), pk, pv, i32([P]), kc, kc, i32([0]), 1, H, H, 1.0, out, ws)
+    e = float(torch.exp(torch.tensor(20.0, dtype=torch.float64)))
+    want = pv[:rise].double().sum(0) + e * (pv[rise:].double().sum(0) + x[0, 2 * H:].double())
+    want = want / (rise + e * (P - rise + 1))
+    off = ((out.view(H, D).double() - want) / want).abs()
+    # as above: two different weights, and the output's rounding
+    assert float(off.max()) <= 2 * 2.0 ** -8 + 1.5e-4, float(off.max())
+    assert qv.qv_device_error() == 0
