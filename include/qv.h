@@ -651,7 +651,8 @@ QV_API qv_status qv_rotary_frequencies(int rot, double base, qv_rotary_scaling s
  *   (qv_device_error); the call's outputs are then undefined.
  * fp32 outputs are within about 5e-6 (2-norm) of the binary64 definition. For
  * bf16 outputs the probabilities are rounded to bf16 before the product with the
- * values: 2e-3, where the outputs' own rounding makes 1.6e-3. Results are the same from call to call.
+ * values: 2e-3, where the outputs' own rounding makes 1.6e-3. Results are the
+ * same from call to call.
  *
  * qv_attention_verify_prefix -- qv_attention_verify for a batch whose sequences
  * all begin with the same prefix (a system prompt, a document), which is stored
@@ -671,8 +672,8 @@ QV_API qv_status qv_rotary_frequencies(int rot, double base, qv_rotary_scaling s
  *   their limits and the errors are qv_attention_verify's.
  *   Two launches: partial results over parts of the prefix, for the query rows of
  *   all sequences together, and of the caches; then their sums with the step's own
- *   keys. The accuracy, sizes of scores and values, what is not
- *   finite and waits: as qv_attention_prompt.
+ *   keys. The accuracy, sizes of scores and values, what is not finite and waits:
+ *   as qv_attention_prompt.
  */
 QV_API qv_status qv_attention_prompt(const uint16_t* qkv, const int32_t* cu_rows, int B, int M, int Hq, int Hkv, int D,
                                      float scale, void* out, qv_dtype out_dtype, cudaStream_t stream);

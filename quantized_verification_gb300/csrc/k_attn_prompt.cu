@@ -31,12 +31,11 @@
 // Rounding of P. The product takes operands of one type, V's bf16. For bf16 outputs P
 // is one part: half a step (2^-8) of each probability makes them 2.0e-3 off in the
 // 2-norm, where their own rounding alone makes 1.6e-3 (with the rounded P in l as well
-// the same to 2 %). Two parts would take the 1.8 times as long that fp32 outputs take
-// (6000 tokens 0.34 ms, 0.19): who needs the bits asks for those. fp32 outputs: P as
-// two parts (residue 2^-17), twice the second product, 1.5 to 3.4e-6 off. A third part
-// has room in tensor memory with one tile a CTA only (heads of 128) and was 0.3 to
-// 3.6e-6 off by the cuts that follow: 6000 tokens 0.57 ms, five prompts of up to 1500
-// tokens 39 us instead of 31.
+// the same to 2 %). fp32 outputs take two parts (residue 2^-17), twice the second
+// product, and are 1.5 to 3.4e-6 off, at 1.8 times the time (6000 tokens 0.34 ms, 0.19
+// for bf16). A third part has room in tensor memory with one tile a CTA only (heads of
+// 128) and was still 0.3 to 3.6e-6 off by the cuts that follow: 6000 tokens 0.57 ms,
+// five prompts of up to 1500 tokens 39 us instead of 31.
 // Sums. The tensor cores cut the accumulator off at every product (1.6e-8 of it, all
 // one way, more as it outgrows what is added). For fp32 outputs O is added in binary32
 // every kFlush steps to the row's sums, which lie where the output goes (every 4 steps
@@ -47,14 +46,15 @@
 // Bound by the tensor cores from about 1000 rows on, where S, P and O pass through
 // tensor memory in time. GB300, causal, bf16 outputs: one prompt of 16001 tokens, 64/8
 // heads of 128, 2.45 ms (1710 TFLOP/s, 0.90 of a measured cuBLAS product; 2.67 ms
-// = 0.82 of it where the power limit is reached); 6000 tokens, 32/8 heads, 0.188 ms
+// = 0.82 of it where the power limit is reached); 6000 tokens, 32/8 heads, 0.19 ms
 // (heads of 64 0.160, fp32 outputs 0.344); 2043 tokens 31 us; 24 prompts of 33 to
-// 4001 tokens 322 to 325 us (1190 TFLOP/s; 339 in a stream of calls). A step of two tiles takes about 2500 cycles of
-// the 2080 that its 32 products need; a block's first and last steps, whose code and
-// data are cold, 2 to 4 thousand more. 97 tokens: 6 us, of which 2.4 are start and
-// first loads.
+// 4001 tokens 322 to 325 us (1190 TFLOP/s; 339 in a stream of calls). A step of two
+// tiles takes about 2500 cycles of the 2080 that its 32 products need; a block's first
+// and last steps, whose code and data are cold, 2 to 4 thousand more. 97 tokens: 6 us,
+// of which 2.4 are start and first loads.
 // Prefixes: 64 tokens, 64/8 heads behind 100001 positions 163 us (1290 TFLOP/s with
-// the caches' parts and the merge; 176 in a stream of calls), 24 sequences of 5 tokens behind 8190, fp32, 50 us.
+// the caches' parts and the merge; 176 in a stream of calls), 24 sequences of 5 tokens
+// behind 8190, fp32, 50 us.
 //
 // Masked tiles. A key that some row of the CTA does not see may hold anything;
 // its score is replaced before use, and its value must not be multiplied by
