@@ -45,10 +45,10 @@
 //
 // Bound by the tensor cores from about 1000 rows on, where S, P and O pass through
 // tensor memory in time. GB300, causal, bf16 outputs: one prompt of 16001 tokens, 64/8
-// heads of 128, 2.45 ms (1710 TFLOP/s, 0.90 of a measured cuBLAS product; 2.67 ms
-// = 0.82 of it where the power limit is reached); 6000 tokens, 32/8 heads, 0.19 ms
+// heads of 128, 2.45 ms (1710 TFLOP/s, 0.90 of a measured cuBLAS product; 2.7 ms
+// = 0.81 of it where the power limit is reached); 6000 tokens, 32/8 heads, 0.19 ms
 // (heads of 64 0.160, fp32 outputs 0.344); 2043 tokens 31 us; 24 prompts of 33 to
-// 4001 tokens 322 to 325 us (1190 TFLOP/s; 339 in a stream of calls). A step of two
+// 4001 tokens 322 to 325 us (1190 TFLOP/s; 339 to 344 in a stream of calls). A step of two
 // tiles takes about 2500 cycles of the 2080 that its 32 products need; a block's first
 // and last steps, whose code and data are cold, 2 to 4 thousand more. 97 tokens: 6 us,
 // of which 2.4 are start and first loads.
